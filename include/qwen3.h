@@ -340,6 +340,26 @@ QWEN3_API size_t qwen3_greedy_workspace(int B);
 QWEN3_API int qwen3_op_greedy(const float* d_logits, int64_t ld, int B, int V, int stop_id, int32_t* d_done,
                               int32_t* d_next, int32_t* d_work, void* stream);
 
+/* Log probabilities of given tokens, with the entropy of each row's distribution and its largest
+ * alternatives (scoring a prompt from the all-rows logits of a prefill, or a sampled token from a decode
+ * step's). For row m of logits x = d_logits[m * ld ..] (V values, fp32 or bf16 by logits_type):
+ *   d_logprob[m]  = x[d_tokens[m]] - log sum_i e^x_i
+ *   d_entropy[m]  = -sum_i p_i log p_i in nats, p = softmax(x); a logit of -inf adds nothing
+ *   d_top_ids[m][j], d_top_logprobs[m][j], j < top_k: the top_k largest logits, largest first, the lowest
+ *                   index first on ties (a NaN counts as the largest, as torch.argmax)
+ * Sums are held in fp32 relative to the row's maximum. A row that holds NaN or +inf, or only -inf, has no
+ * distribution: its d_logprob, d_entropy and d_top_logprobs are NaN, its d_top_ids are still ordered.
+ * d_logprob and d_tokens go together; d_logprob, d_entropy, d_top_ids and d_top_logprobs may each be NULL.
+ * A token outside [0, V) gets NaN and sets bit 1 in *d_err (device int, may be NULL). 0 <= top_k <= 32 and
+ * top_k <= V; ld >= V, any alignment of the rows that the element type has. M = 0 does nothing. The call
+ * needs no workspace, and its result does not depend on timing. */
+#define QWEN3_LOGITS_F32 0
+#define QWEN3_LOGITS_BF16 1
+#define QWEN3_LOGPROB_MAX_TOP 32
+QWEN3_API int qwen3_op_token_logprobs(const void* d_logits, int logits_type, int64_t ld, int M, int V,
+                                      const int32_t* d_tokens, int top_k, float* d_logprob, float* d_entropy,
+                                      int32_t* d_top_ids, float* d_top_logprobs, int* d_err, void* stream);
+
 /* Allocation-free variant of qwen3_op_attention_decode, for callers that cannot call cudaMalloc:
  * code whose device memory belongs to another allocator (for example a framework's caching pool),
  * code that must not trigger the device-wide synchronisation an allocation can cause, and code that

@@ -105,6 +105,7 @@ def lib() -> ctypes.CDLL:
     L.qwen3_prefill_padded.argtypes = [_vp, _vp, _i32p, i, i, _vp, i, _vp]
     L.qwen3_share_prefix.argtypes = [_vp, i, _vp]
     L.qwen3_generate.argtypes = [_vp, _vp, _i32p, i, i, i, i, _vp, _i32p, _vp]
+    L.qwen3_op_token_logprobs.argtypes = [_vp, i, ctypes.c_int64, i, i, _vp, i, _vp, _vp, _vp, _vp, _vp, _vp]
     _lib = L
     return L
 
@@ -359,3 +360,87 @@ def op_greedy(logits, next_ids, stop_id=-1, done=None, work="auto", stream=None)
         work = _greedy_work[key]
     check(lib().qwen3_op_greedy(_p(logits), logits.stride(0), B, V, stop_id, _p(done), _p(next_ids), _p(work),
                                 _stream(stream)))
+
+
+# The operators below check their tensors: a wrong type, shape, layout or device raises ValueError before anything
+# is launched (sizes that the library itself refuses raise Qwen3Error). A decode step calls them in a launch-bound
+# loop, so the checks are plain comparisons and the messages are built only when one fails.
+
+def _want(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+
+
+def _dense(name, t, dtype, shape, device: int):
+    """t is a contiguous tensor of this type and shape on CUDA device `device` (-1: the host)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return
+    got = (f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}" if isinstance(t, torch.Tensor)
+           else type(t).__name__)
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on CUDA device {device}, not {got}")
+
+
+def _launch(fn, args, device: int, stream):
+    """Call an entry point with `device` as the current CUDA device, on its current stream unless one is given."""
+    _want(device >= 0, "the tensors must be on a CUDA device")
+    if stream is None and torch.cuda.current_device() == device:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        _want(stream is None or stream.device.index == device, "the stream belongs to another device")
+        with torch.cuda.device(device):
+            rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if rc:
+        check(rc)
+
+
+LOGPROB_MAX_TOP = 32
+
+
+def op_token_logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=None, top_logprobs=None, err=None,
+                      stream=None):
+    """Log probabilities of `tokens` [M] int32 under logits [M, V] (fp32 or bf16, unit stride along V) into logprob [M],
+    each row's entropy (nats) into entropy [M], and its largest alternatives, largest first, into top_ids [M, k] int32
+    and top_logprobs [M, k]; outputs are fp32, and those left out are not computed. err: device int (bit 1: a token id
+    outside the vocabulary)."""
+    _want(isinstance(logits, torch.Tensor) and logits.dim() == 2, "logits must be a tensor [M, V]")
+    f32 = logits.dtype is _F32
+    _want(f32 or logits.dtype is _BF16, "logits must be fp32 or bf16")
+    M, V = logits.shape
+    dev = logits.get_device()
+    ld, unit = logits.stride()
+    _want(V >= 1 and (V == 1 or unit == 1), "logits must be dense along the vocabulary")
+    if M <= 1:
+        ld = V
+    _want(ld >= V, "rows of the logits overlap")
+    _want((tokens is None) == (logprob is None), "tokens and logprob go together")
+    k = 0
+    if top_ids is not None or top_logprobs is not None:
+        t = top_logprobs if top_ids is None else top_ids
+        _want(isinstance(t, torch.Tensor) and t.dim() == 2, "top_ids and top_logprobs must be tensors [M, k]")
+        k = t.shape[1]
+        _want(k <= V and k <= LOGPROB_MAX_TOP, "at most 32 alternatives, and no more than the vocabulary")
+    p_tok = p_lp = p_ent = p_ids = p_tops = p_err = None
+    if tokens is not None:
+        _dense("tokens", tokens, _I32, (M,), dev)
+        _dense("logprob", logprob, _F32, (M,), dev)
+        p_tok, p_lp = tokens.data_ptr(), logprob.data_ptr()
+    if entropy is not None:
+        _dense("entropy", entropy, _F32, (M,), dev)
+        p_ent = entropy.data_ptr()
+    if top_ids is not None:
+        _dense("top_ids", top_ids, _I32, (M, k), dev)
+        p_ids = top_ids.data_ptr()
+    if top_logprobs is not None:
+        _dense("top_logprobs", top_logprobs, _F32, (M, k), dev)
+        p_tops = top_logprobs.data_ptr()
+    if err is not None:
+        _dense("err", err, _I32, (1,), dev)
+        p_err = err.data_ptr()
+    if M == 0:
+        return
+    _launch(lib().qwen3_op_token_logprobs,
+            (logits.data_ptr(), 0 if f32 else 1, ld, M, V, p_tok, k, p_lp, p_ent, p_ids, p_tops, p_err), dev, stream)

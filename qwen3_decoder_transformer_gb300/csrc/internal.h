@@ -29,6 +29,25 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The same with thread-block clusters of `cluster` CTAs along x (gridDim.x a multiple of it).
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, unsigned cluster, size_t smem,
+                                      cudaStream_t st, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // Device error-flag bits (one int per context, read by qwen3_get_error).
 enum : int { ERR_TOKEN = 1, ERR_TIMEOUT = 2 };
 
@@ -202,6 +221,13 @@ int attn_decode_kernel_count();
 // the current device (looked up on first use per device).
 size_t attn_decode_noalloc_max_bytes();
 cudaError_t attn_decode_noalloc_scratch(float** ptr);
+
+// ---------------------------------------------------------------- token log probabilities (logprobs.cu)
+constexpr int kLogprobMaxTop = 32;
+// One row of logits per cluster; see token_logprobs_kernel. bf16 != 0: the logits are bf16, else fp32.
+cudaError_t token_logprobs_launch(const void* logits, int bf16, long long ld, int M, int V, const int32_t* tokens,
+                                  int top_k, float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs,
+                                  int* err, cudaStream_t st);
 
 // One-time per-process kernel attribute setup (dynamic shared memory limits); idempotent, and must
 // run outside stream capture. Called by every entry point that launches these kernels.

@@ -761,6 +761,20 @@ int qwen3_op_greedy(const float* logits, int64_t ld, int B, int V, int stop_id, 
                : QWEN3_E_CUDA;
 }
 
+int qwen3_op_token_logprobs(const void* logits, int logits_type, int64_t ld, int M, int V, const int32_t* tokens,
+                            int top_k, float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs, int* err,
+                            void* stream) {
+    if (!logits || (logits_type != QWEN3_LOGITS_F32 && logits_type != QWEN3_LOGITS_BF16)) return QWEN3_E_ARG;
+    if (M < 0 || M > (1 << 27) || V < 1 || ld < V || top_k < 0 || top_k > QWEN3_LOGPROB_MAX_TOP || top_k > V)
+        return QWEN3_E_ARG;
+    if (!tokens != !logprob || !is_aligned(logits, logits_type == QWEN3_LOGITS_F32 ? 4 : 2)) return QWEN3_E_ARG;
+    return token_logprobs_launch(logits, logits_type == QWEN3_LOGITS_BF16, ld, M, V, tokens,
+                                 top_ids || top_logprobs ? top_k : 0, logprob, entropy, top_ids, top_logprobs, err,
+                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QWEN3_OK
+               : QWEN3_E_CUDA;
+}
+
 int qwen3_prefill_host(qwen3_ctx* c, const int32_t* h_ids, int B, int T, float* h_logits, int flags, void* stream) {
     if (!c || !h_ids || !h_logits) return QWEN3_E_ARG;
     TRY(check_call(c, B, T));
