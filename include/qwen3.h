@@ -340,6 +340,54 @@ QWEN3_API size_t qwen3_greedy_workspace(int B);
 QWEN3_API int qwen3_op_greedy(const float* d_logits, int64_t ld, int B, int V, int stop_id, int32_t* d_done,
                               int32_t* d_next, int32_t* d_work, void* stream);
 
+/* Decode attention for a batch that shares a long prefix, whose keys and values are read and multiplied once
+ * for the whole batch: for each sequence b and query head h, out = softmax(q k^T * dh^-0.5) V in one softmax
+ * over the prefix_len prefix keys and the sequence's own visible keys, kv head h / (Hq/Hkv). Prefix
+ * d_k_prefix / d_v_prefix [Hkv, prefix_cap, dh] (its first prefix_len rows); own caches [B, Hkv, cap, dh],
+ * sequence b's query at slot d_len0[b * len_stride] (len_stride 0: one length for all; 1: one per sequence),
+ * its keys in slots 0 .. that one. A negative length means no own keys (a length beyond cap - 1 counts as
+ * cap - 1); with no prefix either the row's output is zeros. d_seq_meta (may be NULL) is the layout of
+ * qwen3_op_attention_decode: own slots below psh are skipped (they are the prefix), padding slots
+ * [ps, ps + pad_b) are hidden. After qwen3_share_prefix the call is: the prefix is sequence 0's cache,
+ * prefix_len = psh, prefix_cap = cap. Hidden slots are never read.
+ * q [B, Hq, dh], out [B, Hq*dh] bf16; Hq / Hkv at most 8, dh 64 or 128, B at most 65535; q and caches
+ * 16-byte aligned. d_work is scratch of qwen3_attention_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len)
+ * bytes (0 when prefix_len is 0, then d_work may be NULL), 16-byte aligned; its contents on entry do not matter.
+ * Calls that share a d_work must not overlap on the GPU. Scores and sums are fp32, probabilities are rounded to
+ * bf16 for the weighted sum. d_err (may be NULL) receives bit 2 if a bounded wait gave up. */
+QWEN3_API size_t qwen3_attention_decode_shared_workspace(int B, int Hq, int Hkv, int dh, int prefix_len);
+QWEN3_API int qwen3_op_attention_decode_shared(const void* d_q, const void* d_k_prefix, const void* d_v_prefix,
+                                               int prefix_cap, int prefix_len, const void* d_k_cache,
+                                               const void* d_v_cache, int B, int Hq, int Hkv, int dh, int cap,
+                                               const int* d_len0, int len_stride, const int* d_seq_meta, void* d_work,
+                                               void* d_out, int* d_err, void* stream);
+
+/* Attention with a sliding window and attention sinks: the token in slot i sees slots j <= i with
+ * i - j < window or j < sinks (the first `sinks` tokens stay visible after the window has left them).
+ * Sequence b's first new token is in slot d_len0[b * len_stride] (len_stride 0: one length for all; 1: one per
+ * sequence); its K and V are in the caches [B, Hkv, cap, dh] already, the new tokens' included.
+ *   rolling 0: slot s is stored in cache row s; prefill len0 + T <= cap, decode len0 < cap (a longer length
+ *     counts as the longest that fits).
+ *   rolling 1: the first qwen3_attention_sink_rows(sinks) rows (sinks rounded up to 128) hold the slots of
+ *     those numbers for good, every other slot s is stored at sink_rows + (s - sink_rows) mod (cap - sink_rows),
+ *     so the cache holds sink_rows + ring rows however long the sequence grows. cap - sink_rows must be a
+ *     multiple of 128 and at least window + T - 1 (E_ARG), so that no new token replaces a key still seen.
+ * Prefill: q [B, Hq, T, dh], out [B*T, Hq*dh] bf16 (token-major); a negative length counts as 0. Value rows
+ * that some token of the call sees must be finite (they take part in that tile's products with weight 0 for the
+ * rows that do not see them); rows that none sees may hold anything.
+ * Decode: the form for one token per sequence, q [B, Hq, dh], out [B, Hq*dh], Hq / Hkv at most 8, B at most
+ * 65535; hidden rows are never read; a sequence with a negative length gets zeros. Neither needs a workspace.
+ * window >= 1, sinks >= 0, dh 64 or 128, 16-byte aligned tensors. d_err (may be NULL) as for
+ * qwen3_op_attention_prefill. */
+QWEN3_API int qwen3_attention_sink_rows(int sinks);
+QWEN3_API int qwen3_op_attention_prefill_sinks(const void* d_q, const void* d_k_cache, const void* d_v_cache, int B,
+                                               int T, int Hq, int Hkv, int dh, int cap, const int* d_len0, int len_stride,
+                                               int window, int sinks, int rolling, void* d_out, int* d_err,
+                                               void* stream);
+QWEN3_API int qwen3_op_attention_decode_sinks(const void* d_q, const void* d_k_cache, const void* d_v_cache, int B, int Hq,
+                                              int Hkv, int dh, int cap, const int* d_len0, int len_stride, int window,
+                                              int sinks, int rolling, void* d_out, void* stream);
+
 /* Log probabilities of given tokens, with the entropy of each row's distribution and its largest
  * alternatives (scoring a prompt from the all-rows logits of a prefill, or a sampled token from a decode
  * step's). For row m of logits x = d_logits[m * ld ..] (V values, fp32 or bf16 by logits_type):

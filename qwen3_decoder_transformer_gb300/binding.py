@@ -106,6 +106,13 @@ def lib() -> ctypes.CDLL:
     L.qwen3_share_prefix.argtypes = [_vp, i, _vp]
     L.qwen3_generate.argtypes = [_vp, _vp, _i32p, i, i, i, i, _vp, _i32p, _vp]
     L.qwen3_op_token_logprobs.argtypes = [_vp, i, ctypes.c_int64, i, i, _vp, i, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.qwen3_attention_decode_shared_workspace.restype = sz
+    L.qwen3_attention_decode_shared_workspace.argtypes = [i, i, i, i, i]
+    L.qwen3_op_attention_decode_shared.argtypes = [_vp, _vp, _vp, i, i, _vp, _vp, i, i, i, i, i, _vp, i, _vp, _vp, _vp,
+                                                   _vp, _vp]
+    L.qwen3_attention_sink_rows.argtypes = [i]
+    L.qwen3_op_attention_prefill_sinks.argtypes = [_vp, _vp, _vp, i, i, i, i, i, i, _vp, i, i, i, i, _vp, _vp, _vp]
+    L.qwen3_op_attention_decode_sinks.argtypes = [_vp, _vp, _vp, i, i, i, i, i, _vp, i, i, i, i, _vp, _vp]
     _lib = L
     return L
 
@@ -444,3 +451,113 @@ def op_token_logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=N
         return
     _launch(lib().qwen3_op_token_logprobs,
             (logits.data_ptr(), 0 if f32 else 1, ld, M, V, p_tok, k, p_lp, p_ent, p_ids, p_tops, p_err), dev, stream)
+
+
+def _caches(k_cache, v_cache, B, Hq, dh, device):
+    """Check a pair of caches [B, Hkv, cap, dh] of a call with Hq query heads; returns (Hkv, cap)."""
+    _want(isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4, "k_cache must be a tensor [B, Hkv, cap, dh]")
+    _, Hkv, cap, _ = shape = k_cache.shape
+    _want(shape[0] == B and shape[3] == dh, "the caches do not match the queries' batch and head_dim")
+    _want(Hkv >= 1 and cap >= 1 and Hq % Hkv == 0, "query heads must be a multiple of kv heads, with at least one slot")
+    _dense("k_cache", k_cache, _BF16, shape, device)
+    _dense("v_cache", v_cache, _BF16, shape, device)
+    return Hkv, cap
+
+
+def _lengths(len0, B, device) -> int:
+    """Check len0 [1] (one length for all) or [B]; returns the library's len_stride."""
+    _want(isinstance(len0, torch.Tensor) and len0.dim() == 1, "len0 must be a tensor [1] or [B]")
+    n = len0.shape[0]
+    _want(n == 1 or n == B, "len0 must hold one length, or one per sequence")
+    _dense("len0", len0, _I32, (n,), device)
+    return 0 if n == 1 else 1
+
+
+def attention_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len) -> int:
+    return lib().qwen3_attention_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len)
+
+
+def op_attention_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, len0, work, out, prefix_len=None, seq_meta=None,
+                               err=None, stream=None):
+    """Decode attention of q [B, Hq, dh] over a prefix shared by the batch (k_prefix, v_prefix [Hkv, P, dh], the first
+    prefix_len rows of it; None: no prefix) and each sequence's own cache [B, Hkv, cap, dh], slots 0..len0, into out
+    [B, Hq*dh]. work: attention_decode_shared_workspace bytes of scratch of any type (None without a prefix)."""
+    _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [B, Hq, dh]")
+    B, Hq, dh = q.shape
+    dev = q.get_device()
+    _dense("q", q, _BF16, (B, Hq, dh), dev)
+    Hkv, cap = _caches(k_cache, v_cache, B, Hq, dh, dev)
+    stride = _lengths(len0, B, dev)
+    _dense("out", out, _BF16, (B, Hq * dh), dev)
+    p_k = p_v = p_work = p_meta = p_err = None
+    rows = n = 0
+    if k_prefix is not None:
+        _want(isinstance(k_prefix, torch.Tensor) and k_prefix.dim() == 3, "k_prefix must be a tensor [Hkv, P, dh]")
+        rows = k_prefix.shape[1]
+        n = rows if prefix_len is None else prefix_len
+        _want(0 <= n <= rows, "prefix_len is not within the prefix")
+        _dense("k_prefix", k_prefix, _BF16, (Hkv, rows, dh), dev)
+        _dense("v_prefix", v_prefix, _BF16, (Hkv, rows, dh), dev)
+        p_k, p_v = k_prefix.data_ptr(), v_prefix.data_ptr()
+    else:
+        _want(v_prefix is None and not prefix_len, "v_prefix and prefix_len go with k_prefix")
+    if B == 0:
+        return
+    fn = lib()
+    if n > 0:
+        need = fn.qwen3_attention_decode_shared_workspace(B, Hq, Hkv, dh, n)
+        _want(isinstance(work, torch.Tensor) and work.get_device() == dev and work.is_contiguous()
+              and work.numel() * work.element_size() >= need, "work must be contiguous scratch of the size that "
+              "attention_decode_shared_workspace gives, on the same device")
+        p_work = work.data_ptr()
+    if seq_meta is not None:
+        _dense("seq_meta", seq_meta, _I32, (2 + B,), dev)
+        p_meta = seq_meta.data_ptr()
+    if err is not None:
+        _dense("err", err, _I32, (1,), dev)
+        p_err = err.data_ptr()
+    _launch(fn.qwen3_op_attention_decode_shared,
+            (q.data_ptr(), p_k, p_v, rows, n, k_cache.data_ptr(), v_cache.data_ptr(), B, Hq, Hkv, dh, cap,
+             len0.data_ptr(), stride, p_meta, p_work, out.data_ptr(), p_err), dev, stream)
+
+
+def attention_sink_rows(sinks) -> int:
+    """Cache rows in front of the ring of a rolling buffer with this many sink tokens."""
+    return lib().qwen3_attention_sink_rows(sinks)
+
+
+def op_attention_prefill_sinks(q, k_cache, v_cache, len0, out, window, sinks, rolling=False, err=None, stream=None):
+    """Attention of the new tokens q [B, Hq, T, dh] in slots len0 .. len0+T-1 of the caches [B, Hkv, cap, dh] with a
+    sliding window and sink tokens, into out [B*T, Hq*dh]; len0 [1] or [B]."""
+    _want(isinstance(q, torch.Tensor) and q.dim() == 4, "q must be a tensor [B, Hq, T, dh]")
+    B, Hq, T, dh = q.shape
+    dev = q.get_device()
+    _dense("q", q, _BF16, (B, Hq, T, dh), dev)
+    Hkv, cap = _caches(k_cache, v_cache, B, Hq, dh, dev)
+    stride = _lengths(len0, B, dev)
+    _dense("out", out, _BF16, (B * T, Hq * dh), dev)
+    p_err = None
+    if err is not None:
+        _dense("err", err, _I32, (1,), dev)
+        p_err = err.data_ptr()
+    if B == 0 or T == 0:
+        return
+    _launch(lib().qwen3_op_attention_prefill_sinks,
+            (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, T, Hq, Hkv, dh, cap, len0.data_ptr(), stride,
+             window, sinks, 1 if rolling else 0, out.data_ptr(), p_err), dev, stream)
+
+
+def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rolling=False, stream=None):
+    """The single-token form of op_attention_prefill_sinks: q [B, Hq, dh], out [B, Hq*dh]."""
+    _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [B, Hq, dh]")
+    B, Hq, dh = q.shape
+    dev = q.get_device()
+    _dense("q", q, _BF16, (B, Hq, dh), dev)
+    Hkv, cap = _caches(k_cache, v_cache, B, Hq, dh, dev)
+    stride = _lengths(len0, B, dev)
+    _dense("out", out, _BF16, (B, Hq * dh), dev)
+    if B == 0:
+        return
+    _launch(lib().qwen3_op_attention_decode_sinks,
+            (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, Hq, Hkv, dh, cap, len0.data_ptr(), stride, window,
+             sinks, 1 if rolling else 0, out.data_ptr()), dev, stream)

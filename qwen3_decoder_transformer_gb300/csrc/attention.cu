@@ -499,12 +499,18 @@ struct PsLayout {
     static constexpr int SMEM = XCH_OFF + (ALT ? 6 * TC_BM * 4 : 0) + 1024;
 };
 
-template <int DH, bool SPEC, bool ALT>
+// SINKS: a sliding window whose first `sinks` slots stay visible, each sequence at its own start
+// (len0p[b * len_stride]). A query tile then walks the tiles of the sinks and those of its window, which the
+// skip between tiles ja and jb (padding otherwise) expresses, and two visible intervals per row (before and
+// behind the padding otherwise) hold the sinks and the window. Rolling buffers keep sink_rows rows in front
+// of the ring. Padding layouts do not combine with it.
+template <int DH, bool SPEC, bool ALT, bool SINKS>
 __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
     attn_prefill_persistent_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                                    const __grid_constant__ CUtensorMap tmV, int T, int Hq, int Hkv, int B,
                                    const int* __restrict__ len0p, const int* __restrict__ meta, int window, int ring,
-                                   __nv_bfloat16* __restrict__ out, int* err) {
+                                   __nv_bfloat16* __restrict__ out, int* err, int sinks, int sink_rows, int len_stride,
+                                   int len_max) {
     using Ly = PsLayout<DH, ALT>;
     constexpr int NCH = Ly::NCH;
     constexpr uint32_t IDESC_S = idesc_bf16(TC_BM, TC_BN);
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
     bool ok = true;
     pdl_wait();  // Q and the cache come from the previous kernel
     pdl_trigger();
-    const int len0 = *len0p;
+    const int len0_all = SINKS ? 0 : *len0p;
     int ps_meta = 0, psh = 0;
     if (meta) {
         ps_meta = meta[0];
@@ -582,7 +588,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
 
     // The parameters of this CTA's round-th item (n_tiles = 0 when it has none left).
     struct Item {
-        int b, h, q0, q_end, n_valid, j_lo, ja, jb, n_tiles, ps, pe;
+        int b, h, q0, q_end, n_valid, j_lo, ja, jb, n_tiles, ps, pe, len0;
     };
     auto item_of = [&](int round) -> Item {
         Item it{};
@@ -593,15 +599,30 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
         it.h = rem % Hq;
         it.q0 = qt * TC_BM;
         it.q_end = min(T, it.q0 + TC_BM);
+        it.len0 = SINKS ? min(max(0, len0p[(size_t)it.b * len_stride]), len_max) : len0_all;
+        const int len0 = it.len0;
         it.ps = ps_meta;
         it.pe = meta ? ps_meta + meta[kSeqMetaHead + it.b] : 0;
         it.n_valid = len0 + it.q_end;
         const int n_end = (it.n_valid + TC_BN - 1) / TC_BN;
+        if constexpr (SINKS) {
+            it.j_lo = 0;
+            it.jb = max(0, len0 + it.q0 - window + 1) / TC_BN;  // first tile of the window
+            it.ja = min((sinks + TC_BN - 1) / TC_BN, it.jb);    // tiles of the sinks before it
+            it.n_tiles = n_end - (it.jb - it.ja);
+            return it;
+        }
         it.j_lo = window > 0 ? max(0, len0 + it.q0 - window + 1) / TC_BN : 0;
         it.ja = max(it.j_lo, (it.ps + TC_BN - 1) / TC_BN);
         it.jb = max(it.ja, min(it.pe / TC_BN, (len0 + it.q0) / TC_BN));
         it.n_tiles = n_end - it.j_lo - (it.jb - it.ja);
         return it;
+    };
+    // cache row of slot tile j: a rolling buffer wraps, behind its sink rows
+    auto tile_row = [&](int j) -> int {
+        const int s = j * TC_BN;
+        if constexpr (SINKS) return ring > 0 && s >= sink_rows ? sink_rows + (s - sink_rows) % ring : s;
+        return ring ? s % ring : s;
     };
     auto tile_j = [](const Item& it, int i) { return it.j_lo + i < it.ja ? it.j_lo + i : it.j_lo + i + (it.jb - it.ja); };
 
@@ -626,7 +647,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     for (int i = 0; i < it.n_tiles; ++i, ++g) {
                         const int s = g % PS_KST, j = tile_j(it, i);
                         const uint32_t free_ph = ((g / PS_KST) & 1) ^ 1;
-                        const int y = ring ? (j * TC_BN) % ring : j * TC_BN;
+                        const int y = tile_row(j);
                         const int z = (j * TC_BN < psh ? 0 : it.b) * Hkv + jkv;
                         if (!mbar_wait_suspend(&k_empty[s], free_ph, abort_flag)) { ok = false; break; }
                         mbar_expect_tx(&k_full[s], Ly::KV_BYTES);
@@ -648,7 +669,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     for (int i = 0; i < it.n_tiles; ++i, ++g) {
                         const int s = g & 1, j = tile_j(it, i);
                         const uint32_t free_ph = ((g >> 1) & 1) ^ 1;
-                        const int y = ring ? (j * TC_BN) % ring : j * TC_BN;
+                        const int y = tile_row(j);
                         const int z = (j * TC_BN < psh ? 0 : it.b) * Hkv + jkv;
                         if (!mbar_wait_suspend(&v_empty[s], free_ph, abort_flag)) { ok = false; break; }
                         mbar_expect_tx(&v_full[s], Ly::KV_BYTES);
@@ -707,6 +728,20 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     const int j = tile_j(it, i);
                     if (!__all_sync(0xffffffffu, mbar_wait_suspend(&v_full[s], (gi >> 1) & 1, abort_flag))) { ok = false; break; }
                     uint8_t* sv = smem + Ly::V_OFF + s * Ly::KV_BYTES;
+                    if constexpr (SINKS) {
+                        // value rows between the sinks and the first row's window, which no row sees: a
+                        // hidden row may hold anything, and 0 * NaN must not reach O
+                        const int z0 = max(0, sinks - j * TC_BN);
+                        const int z1 = min(TC_BN, it.len0 + it.q0 - window + 1 - j * TC_BN);
+                        if (z0 < z1) {
+                            for (int e = lane; e < (z1 - z0) * 8 * NCH; e += 32) {
+                                const int cc = e / ((z1 - z0) * 8), rem = e % ((z1 - z0) * 8);
+                                reinterpret_cast<uint4*>(sv + cc * TC_BN * 128 + (z0 + rem / 8) * 128)[rem % 8] =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                        }
+                    }
                     const int r0 = it.n_valid - j * TC_BN;  // first stale key row of this tile
                     if (r0 < TC_BN) {
                         for (int e = lane; e < (TC_BN - r0) * 8 * NCH; e += 32) {
@@ -764,7 +799,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             const Item it = item_of(round);
             const int nt = it.n_tiles;
             if (nt == 0) break;
-            const int t = it.q0 + row, pos = len0 + t;
+            const int t = it.q0 + row, pos = it.len0 + t;
             volatile float* m_row = m_sh + (round & 1) * TC_BM + row;
             float m_l = -INFINITY, l = 0.f;  // this warpgroup's share of the row sum, at scale m_l
             for (int i = ((g & 1) == wg) ? 0 : 1; i < nt; i += 2) {
@@ -779,15 +814,17 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     tmem_ld_32x32b_x32(tm_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
                 tmem_ld_wait();
                 const int k0 = j * TC_BN;
-                const bool diag = k0 + TC_BN - 1 > len0 + it.q0;
+                const bool diag = k0 + TC_BN - 1 > it.len0 + it.q0;
                 const bool pads = k0 < it.pe && k0 + TC_BN > it.ps;
-                const bool old = window > 0 && k0 < len0 + it.q_end - window;
+                const bool old = window > 0 && k0 < it.len0 + it.q_end - window && (!SINKS || k0 + TC_BN > sinks);
                 if (pads || old) {
                     // visible: (i <= lim, not padding, inside the window) or the query itself; branch-free
                     const int lim = pos - k0;
                     const int lo = window > 0 ? lim - window + 1 : -TC_BN;
-                    const int a1 = max(lo, 0), n1 = max(0, min(lim, it.ps - k0 - 1) - a1 + 1);
-                    const int a2 = max(lo, it.pe - k0), n2 = max(0, lim - a2 + 1);
+                    // SINKS: the sinks and the window take the places of the intervals around the padding
+                    const int a1 = SINKS ? 0 : max(lo, 0);
+                    const int n1 = SINKS ? max(0, min(lim + 1, sinks - k0)) : max(0, min(lim, it.ps - k0 - 1) - a1 + 1);
+                    const int a2 = SINKS ? max(lo, 0) : max(lo, it.pe - k0), n2 = max(0, lim - a2 + 1);
 #pragma unroll
                     for (int e = 0; e < TC_BN; ++e) {
                         const bool vis =
@@ -941,7 +978,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             const Item it = item_of(round);
             const int nt = it.n_tiles;
             if (nt == 0) break;
-            const int t = it.q0 + row, pos = len0 + t;
+            const int t = it.q0 + row, pos = it.len0 + t;
             float m_used = -INFINITY, l = 0.f;
             for (int i = 0; i < nt; ++i) {
                 const int gi = g + i, r = gi % NR;
@@ -955,15 +992,17 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     tmem_ld_32x32b_x32(tm_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
                 tmem_ld_wait();
                 const int k0 = j * TC_BN;
-                const bool diag = k0 + TC_BN - 1 > len0 + it.q0;
+                const bool diag = k0 + TC_BN - 1 > it.len0 + it.q0;
                 const bool pads = k0 < it.pe && k0 + TC_BN > it.ps;
-                const bool old = window > 0 && k0 < len0 + it.q_end - window;
+                const bool old = window > 0 && k0 < it.len0 + it.q_end - window && (!SINKS || k0 + TC_BN > sinks);
                 if (pads || old) {
                     // visible: (i <= lim, not padding, inside the window) or the query itself; branch-free
                     const int lim = pos - k0;
                     const int lo = window > 0 ? lim - window + 1 : -TC_BN;
-                    const int a1 = max(lo, 0), n1 = max(0, min(lim, it.ps - k0 - 1) - a1 + 1);
-                    const int a2 = max(lo, it.pe - k0), n2 = max(0, lim - a2 + 1);
+                    // SINKS: the sinks and the window take the places of the intervals around the padding
+                    const int a1 = SINKS ? 0 : max(lo, 0);
+                    const int n1 = SINKS ? max(0, min(lim + 1, sinks - k0)) : max(0, min(lim, it.ps - k0 - 1) - a1 + 1);
+                    const int a2 = SINKS ? max(lo, 0) : max(lo, it.pe - k0), n2 = max(0, lim - a2 + 1);
 #pragma unroll
                     for (int e = 0; e < TC_BN; ++e) {
                         const bool vis =
@@ -1546,16 +1585,36 @@ constexpr int kAltMinKeys = 8192;
 
 // setmaxnreg.inc waits until the registers it asks for are free, so the ALT form runs only when the
 // compiled kernel was given at least the registers per thread its split hands out (checked once).
-template <int DH>
+template <int DH, bool SINKS>
 bool alt_registers_cover_split() {
     static const bool ok = [] {
         cudaFuncAttributes fa{};
-        if (cudaFuncGetAttributes(&fa, attn_prefill_persistent_kernel<DH, true, true>) != cudaSuccess) return false;
+        if (cudaFuncGetAttributes(&fa, attn_prefill_persistent_kernel<DH, true, true, SINKS>) != cudaSuccess) return false;
         const long long have = (long long)ps_threads<true>() * fa.numRegs;
         const long long need = 128LL * PS_REG_PRODUCER + 256LL * PS_REG_SOFTMAX;
         return have >= need;
     }();
     return ok;
+}
+
+// The persistent kernel in the form that suits the key range kv_hint.
+template <int DH, bool SINKS>
+cudaError_t persistent_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int B, int T, int Hq,
+                              int Hkv, const int* len0, SeqMap sm, __nv_bfloat16* out, int* err, int kv_hint, int sinks,
+                              int sink_rows, int len_stride, int len_max, cudaStream_t st) {
+    const long long items = (long long)((T + TC_BM - 1) / TC_BM) * Hq * B;
+    const unsigned grid = (unsigned)std::min<long long>(items, device_sm_count());
+    if (kv_hint >= kAltMinKeys && alt_registers_cover_split<DH, SINKS>())
+        return launch_pdl(attn_prefill_persistent_kernel<DH, true, true, SINKS>, dim3(grid), dim3(ps_threads<true>()),
+                          PsLayout<DH, true>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out,
+                          err, sinks, sink_rows, len_stride, len_max);
+    if (kv_hint >= kSpecMinKeys)
+        return launch_pdl(attn_prefill_persistent_kernel<DH, true, false, SINKS>, dim3(grid), dim3(ps_threads<false>()),
+                          PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out,
+                          err, sinks, sink_rows, len_stride, len_max);
+    return launch_pdl(attn_prefill_persistent_kernel<DH, false, false, SINKS>, dim3(grid), dim3(ps_threads<false>()),
+                      PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out,
+                      err, sinks, sink_rows, len_stride, len_max);
 }
 
 template <int DH>
@@ -1580,16 +1639,23 @@ cudaError_t prefill_launch_dh(const __nv_bfloat16* q, const __nv_bfloat16* kc, c
         return prefill_launch_nh<DH, 2>(tq, tk, tv, B, T, Hq, Hkv, len0, sm, out, err, split, max_chunks, ws, st);
     if (split > 0)
         return prefill_launch_nh<DH, 1>(tq, tk, tv, B, T, Hq, Hkv, len0, sm, out, err, split, max_chunks, ws, st);
-    const long long items = (long long)((T + TC_BM - 1) / TC_BM) * Hq * B;
-    const unsigned grid = (unsigned)std::min<long long>(items, device_sm_count());
-    if (kv_hint >= kAltMinKeys && alt_registers_cover_split<DH>())
-        return launch_pdl(attn_prefill_persistent_kernel<DH, true, true>, dim3(grid), dim3(ps_threads<true>()),
-                          PsLayout<DH, true>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err);
-    if (kv_hint >= kSpecMinKeys)
-        return launch_pdl(attn_prefill_persistent_kernel<DH, true, false>, dim3(grid), dim3(ps_threads<false>()),
-                          PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err);
-    return launch_pdl(attn_prefill_persistent_kernel<DH, false, false>, dim3(grid), dim3(ps_threads<false>()),
-                      PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err);
+    return persistent_launch<DH, false>(tq, tk, tv, B, T, Hq, Hkv, len0, sm, out, err, kv_hint, 0, 0, 0, 0, st);
+}
+
+template <int DH>
+cudaError_t prefill_sinks_launch_dh(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B, int T,
+                                    int Hq, int Hkv, int cap, const int* len0, int len_stride, SinkMap sm,
+                                    __nv_bfloat16* out, int* err, cudaStream_t st) {
+    CUtensorMap tq, tk, tv;
+    if (!encode_tmap_bf16_3d(&tq, q, DH, T, (uint64_t)B * Hq) || !encode_tmap_bf16_3d(&tk, kc, DH, cap, (uint64_t)B * Hkv) ||
+        !encode_tmap_bf16_3d(&tv, vc, DH, cap, (uint64_t)B * Hkv))
+        return cudaErrorInvalidValue;
+    // largest start: the call's tokens end inside a full cache; a rolling buffer only bounds the slot arithmetic
+    const int len_max = sm.ring > 0 ? 1 << 30 : std::max(0, cap - T);
+    // keys of one query tile: the sinks, the window and the tile's own slots
+    const int keys = (int)std::min<long long>((long long)sm.window + sm.sinks + TC_BM, cap);
+    return persistent_launch<DH, true>(tq, tk, tv, B, T, Hq, Hkv, len0, SeqMap{nullptr, sm.window, sm.ring}, out, err,
+                                       keys, sm.sinks, sm.sink_rows, len_stride, len_max, st);
 }
 
 }  // namespace
@@ -1610,6 +1676,16 @@ cudaError_t attn_prefill_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc,
     if (dh == 64)
         return prefill_launch_dh<64>(q, kc, vc, B, T, Hq, Hkv, cap, len0, sm, out, err, split, max_chunks, ws, heads,
                                      kv_hint, st);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t attn_prefill_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B,
+                                      int T, int Hq, int Hkv, int dh, int cap, const int* len0, int len_stride,
+                                      SinkMap sm, __nv_bfloat16* out, int* err, cudaStream_t st) {
+    if (B <= 0 || T <= 0) return cudaSuccess;
+    if (dh == 128)
+        return prefill_sinks_launch_dh<128>(q, kc, vc, B, T, Hq, Hkv, cap, len0, len_stride, sm, out, err, st);
+    if (dh == 64) return prefill_sinks_launch_dh<64>(q, kc, vc, B, T, Hq, Hkv, cap, len0, len_stride, sm, out, err, st);
     return cudaErrorInvalidValue;
 }
 
@@ -1683,16 +1759,25 @@ cudaError_t decode_prepare_dh() {
 cudaError_t attention_prepare() {
     const void* fns[] = {(const void*)attn_prefill_tc_kernel<128, 1>, (const void*)attn_prefill_tc_kernel<128, 2>,
                          (const void*)attn_prefill_tc_kernel<64, 1>,  (const void*)attn_prefill_tc_kernel<64, 2>,
-                         (const void*)attn_prefill_persistent_kernel<128, false, false>,
-                         (const void*)attn_prefill_persistent_kernel<64, false, false>,
-                         (const void*)attn_prefill_persistent_kernel<128, true, false>,
-                         (const void*)attn_prefill_persistent_kernel<64, true, false>,
-                         (const void*)attn_prefill_persistent_kernel<128, true, true>,
-                         (const void*)attn_prefill_persistent_kernel<64, true, true>};
+                         (const void*)attn_prefill_persistent_kernel<128, false, false, false>,
+                         (const void*)attn_prefill_persistent_kernel<64, false, false, false>,
+                         (const void*)attn_prefill_persistent_kernel<128, true, false, false>,
+                         (const void*)attn_prefill_persistent_kernel<64, true, false, false>,
+                         (const void*)attn_prefill_persistent_kernel<128, true, true, false>,
+                         (const void*)attn_prefill_persistent_kernel<64, true, true, false>,
+                         (const void*)attn_prefill_persistent_kernel<128, false, false, true>,
+                         (const void*)attn_prefill_persistent_kernel<64, false, false, true>,
+                         (const void*)attn_prefill_persistent_kernel<128, true, false, true>,
+                         (const void*)attn_prefill_persistent_kernel<64, true, false, true>,
+                         (const void*)attn_prefill_persistent_kernel<128, true, true, true>,
+                         (const void*)attn_prefill_persistent_kernel<64, true, true, true>};
     const int smem[] = {TcLayout<128, 1>::SMEM, TcLayout<128, 2>::SMEM, TcLayout<64, 1>::SMEM, TcLayout<64, 2>::SMEM,
                         PsLayout<128, false>::SMEM, PsLayout<64, false>::SMEM, PsLayout<128, false>::SMEM,
+                        PsLayout<64, false>::SMEM, PsLayout<128, true>::SMEM,  PsLayout<64, true>::SMEM,
+                        PsLayout<128, false>::SMEM, PsLayout<64, false>::SMEM, PsLayout<128, false>::SMEM,
                         PsLayout<64, false>::SMEM, PsLayout<128, true>::SMEM,  PsLayout<64, true>::SMEM};
-    for (int i = 0; i < 10; ++i) {
+    static_assert(sizeof(fns) / sizeof(fns[0]) == sizeof(smem) / sizeof(smem[0]), "one size per kernel");
+    for (size_t i = 0; i < sizeof(fns) / sizeof(fns[0]); ++i) {
         cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, smem[i]);
         if (e != cudaSuccess) return e;
     }

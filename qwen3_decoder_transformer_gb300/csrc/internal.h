@@ -133,6 +133,12 @@ struct GemmMaps {
     CUtensorMap a, b, c, r, v;
 };
 bool encode_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2);
+// Rows [heads][rows of row_cap][dh] in boxes of 64 x 128 x 1; rows past `rows` read as zero.
+bool encode_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t dh, uint64_t rows, uint64_t row_cap,
+                           uint64_t heads);
+// Query rows [seqs][heads][group][dh] in boxes of 64 x group x 1 x box_seqs: one head's groups of box_seqs sequences.
+bool encode_tmap_bf16_groups(CUtensorMap* map, const void* base, uint64_t dh, uint64_t group, uint64_t heads,
+                             uint64_t seqs, uint32_t box_seqs);
 cudaError_t gemm_launch(const GemmMaps& maps, const GemmArgs& args, cudaStream_t st);
 
 // ---------------------------------------------------------------- skinny GEMM (gemm.cu)
@@ -222,6 +228,29 @@ int attn_decode_kernel_count();
 size_t attn_decode_noalloc_max_bytes();
 cudaError_t attn_decode_noalloc_scratch(float** ptr);
 
+// Sliding window with sinks: slot i sees slots j <= i with i - j < window or j < sinks. ring > 0 is a rolling
+// buffer of sink_rows + ring cache rows: slot s < sink_rows is stored at s, the others at
+// sink_rows + (s - sink_rows) mod ring (both multiples of 128, so a 128-slot tile stays contiguous).
+struct SinkMap {
+    int window, sinks, sink_rows, ring;
+};
+// Sequence b starts at slot len0[b * len_stride] (0 = one length for all).
+cudaError_t attn_prefill_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B,
+                                      int T, int Hq, int Hkv, int dh, int cap, const int* len0, int len_stride,
+                                      SinkMap sm, __nv_bfloat16* out, int* err, cudaStream_t st);
+
+// ---------------------------------------------------------------- attention over key ranges (attention_ranges.cu)
+cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B, int Hq,
+                                     int Hkv, int dh, int cap, const int* len0, int len_stride, SinkMap sm,
+                                     __nv_bfloat16* out, cudaStream_t st);
+// Decode attention of B sequences over a shared prefix (kp, vp: [Hkv][prefix_cap][dh], P rows of it) and their own
+// slots; meta as SeqMap::meta (own slots below psh are skipped). work: attn_decode_shared_workspace() bytes.
+size_t attn_decode_shared_workspace(int B, int Hq, int Hkv, int dh, int prefix_len);
+cudaError_t attn_decode_shared_launch(const __nv_bfloat16* q, const __nv_bfloat16* kp, const __nv_bfloat16* vp,
+                                      int prefix_cap, int P, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B,
+                                      int Hq, int Hkv, int dh, int cap, const int* len0, int len_stride, const int* meta,
+                                      float* work, __nv_bfloat16* out, int* err, cudaStream_t st);
+
 // ---------------------------------------------------------------- token log probabilities (logprobs.cu)
 constexpr int kLogprobMaxTop = 32;
 // One row of logits per cluster; see token_logprobs_kernel. bf16 != 0: the logits are bf16, else fp32.
@@ -233,6 +262,7 @@ cudaError_t token_logprobs_launch(const void* logits, int bf16, long long ld, in
 // run outside stream capture. Called by every entry point that launches these kernels.
 cudaError_t gemm_prepare();
 cudaError_t attention_prepare();
+cudaError_t attention_ranges_prepare();
 cudaError_t prepare_kernels();
 
 }  // namespace q3

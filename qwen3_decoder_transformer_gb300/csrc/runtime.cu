@@ -75,6 +75,7 @@ cudaError_t prepare_kernels() {
     if (done[dev]) return cudaSuccess;
     cudaError_t e = gemm_prepare();
     if (e == cudaSuccess) e = attention_prepare();
+    if (e == cudaSuccess) e = attention_ranges_prepare();
     if (e == cudaSuccess) done[dev] = true;
     return e;
 }
@@ -454,6 +455,19 @@ int ensure_generation_buffers(qwen3_ctx* c) {
         return QWEN3_E_CUDA;
     }
     return QWEN3_OK;
+}
+
+// Window and sinks of a call of T tokens on a cache of cap rows; false when they do not fit.
+bool sink_map(int window, int sinks, int rolling, int cap, int T, SinkMap* sm) {
+    if (window < 1 || sinks < 0 || (rolling != 0 && rolling != 1)) return false;
+    // slots past the cache do not exist, so a longer window or more sinks than 2^29 say nothing new
+    *sm = SinkMap{std::min(window, 1 << 29), std::min(sinks, 1 << 29), 0, 0};
+    if (!rolling) return true;
+    if (window > (1 << 29) || sinks > (1 << 29)) return false;
+    sm->sink_rows = (sinks + 127) / 128 * 128;
+    sm->ring = cap - sm->sink_rows;
+    // the ring holds the window of the call's first token and every token of the call
+    return sm->ring >= 128 && sm->ring % 128 == 0 && sm->ring >= (long long)window + T - 1;
 }
 
 }  // namespace
@@ -1053,6 +1067,69 @@ int qwen3_op_attention_decode(const void* q, const void* kc, const void* vc, int
     return attn_decode_launch(static_cast<const bf16*>(q), static_cast<const bf16*>(kc), static_cast<const bf16*>(vc), B,
                               Hq, Hkv, dh, cap, len0, SeqMap{seq_meta, window, ring}, static_cast<float*>(work),
                               static_cast<bf16*>(out), err, 0, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QWEN3_OK
+               : QWEN3_E_CUDA;
+}
+
+size_t qwen3_attention_decode_shared_workspace(int B, int Hq, int Hkv, int dh, int prefix_len) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 8 || (dh != 64 && dh != 128) || prefix_len < 0) return 0;
+    return attn_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len);
+}
+
+int qwen3_op_attention_decode_shared(const void* q, const void* kp, const void* vp, int prefix_cap, int prefix_len,
+                                     const void* kc, const void* vc, int B, int Hq, int Hkv, int dh, int cap,
+                                     const int* len0, int len_stride, const int* seq_meta, void* work, void* out, int* err,
+                                     void* stream) {
+    if (!q || !kc || !vc || !len0 || !out || B < 0 || B > 65535 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv ||
+        Hq / Hkv > 8 || (dh != 64 && dh != 128) || cap < 1 || (len_stride != 0 && len_stride != 1))
+        return QWEN3_E_ARG;
+    if (prefix_len < 0 || prefix_len > prefix_cap || (prefix_len > 0 && (!kp || !vp || !work))) return QWEN3_E_ARG;
+    const void* ptrs[] = {q, kc, vc, prefix_len > 0 ? kp : nullptr, prefix_len > 0 ? vp : nullptr, work};
+    for (const void* p : ptrs)
+        if (!is_aligned(p, 16)) return QWEN3_E_ARG;
+    if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
+    return attn_decode_shared_launch(static_cast<const bf16*>(q), static_cast<const bf16*>(kp),
+                                     static_cast<const bf16*>(vp), prefix_cap, prefix_len, static_cast<const bf16*>(kc),
+                                     static_cast<const bf16*>(vc), B, Hq, Hkv, dh, cap, len0, len_stride, seq_meta,
+                                     static_cast<float*>(work), static_cast<bf16*>(out), err,
+                                     static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QWEN3_OK
+               : QWEN3_E_CUDA;
+}
+
+int qwen3_attention_sink_rows(int sinks) { return sinks < 0 || sinks > (1 << 30) ? 0 : (sinks + 127) / 128 * 128; }
+
+int qwen3_op_attention_prefill_sinks(const void* q, const void* kc, const void* vc, int B, int T, int Hq, int Hkv, int dh,
+                                     int cap, const int* len0, int len_stride, int window, int sinks, int rolling,
+                                     void* out, int* err, void* stream) {
+    if (!q || !kc || !vc || !len0 || !out || B < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv ||
+        (dh != 64 && dh != 128) || cap < 1 || (len_stride != 0 && len_stride != 1))
+        return QWEN3_E_ARG;
+    if (((long long)T + 127) / 128 * Hq * B > 0x7fffffff) return QWEN3_E_ARG;
+    SinkMap sm;
+    if (!sink_map(window, sinks, rolling, cap, T, &sm)) return QWEN3_E_ARG;
+    if (!is_aligned(q, 16) || !is_aligned(kc, 16) || !is_aligned(vc, 16) || !is_aligned(out, 16)) return QWEN3_E_ARG;
+    if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
+    return attn_prefill_sinks_launch(static_cast<const bf16*>(q), static_cast<const bf16*>(kc),
+                                     static_cast<const bf16*>(vc), B, T, Hq, Hkv, dh, cap, len0, len_stride, sm,
+                                     static_cast<bf16*>(out), err, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QWEN3_OK
+               : QWEN3_E_CUDA;
+}
+
+int qwen3_op_attention_decode_sinks(const void* q, const void* kc, const void* vc, int B, int Hq, int Hkv, int dh, int cap,
+                                    const int* len0, int len_stride, int window, int sinks, int rolling, void* out,
+                                    void* stream) {
+    if (!q || !kc || !vc || !len0 || !out || B < 0 || B > 65535 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv ||
+        Hq / Hkv > 8 || (dh != 64 && dh != 128) || cap < 1 || (len_stride != 0 && len_stride != 1))
+        return QWEN3_E_ARG;
+    SinkMap sm;
+    if (!sink_map(window, sinks, rolling, cap, 1, &sm)) return QWEN3_E_ARG;
+    if (!is_aligned(q, 16) || !is_aligned(kc, 16) || !is_aligned(vc, 16)) return QWEN3_E_ARG;
+    if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
+    return attn_decode_sinks_launch(static_cast<const bf16*>(q), static_cast<const bf16*>(kc),
+                                    static_cast<const bf16*>(vc), B, Hq, Hkv, dh, cap, len0, len_stride, sm,
+                                    static_cast<bf16*>(out), static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? QWEN3_OK
                : QWEN3_E_CUDA;
 }
