@@ -112,7 +112,7 @@ def lib() -> ctypes.CDLL:
                                                    _vp, _vp]
     L.qwen3_attention_sink_rows.argtypes = [i]
     L.qwen3_op_attention_prefill_sinks.argtypes = [_vp, _vp, _vp, i, i, i, i, i, i, _vp, i, i, i, i, _vp, _vp, _vp]
-    L.qwen3_op_attention_decode_sinks.argtypes = [_vp, _vp, _vp, i, i, i, i, i, _vp, i, i, i, i, _vp, _vp]
+    L.qwen3_op_attention_decode_sinks.argtypes = [_vp, _vp, _vp, i, i, i, i, i, _vp, i, i, i, i, _vp, _vp, _vp]
     _lib = L
     return L
 
@@ -547,7 +547,7 @@ def op_attention_prefill_sinks(q, k_cache, v_cache, len0, out, window, sinks, ro
              window, sinks, 1 if rolling else 0, out.data_ptr(), p_err), dev, stream)
 
 
-def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rolling=False, stream=None):
+def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rolling=False, err=None, stream=None):
     """The single-token form of op_attention_prefill_sinks: q [B, Hq, dh], out [B, Hq*dh]."""
     _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [B, Hq, dh]")
     B, Hq, dh = q.shape
@@ -556,8 +556,12 @@ def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rol
     Hkv, cap = _caches(k_cache, v_cache, B, Hq, dh, dev)
     stride = _lengths(len0, B, dev)
     _dense("out", out, _BF16, (B, Hq * dh), dev)
+    p_err = None
+    if err is not None:
+        _dense("err", err, _I32, (1,), dev)
+        p_err = err.data_ptr()
     if B == 0:
         return
     _launch(lib().qwen3_op_attention_decode_sinks,
             (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, Hq, Hkv, dh, cap, len0.data_ptr(), stride, window,
-             sinks, 1 if rolling else 0, out.data_ptr()), dev, stream)
+             sinks, 1 if rolling else 0, out.data_ptr(), p_err), dev, stream)

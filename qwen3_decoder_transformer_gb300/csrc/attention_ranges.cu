@@ -1,10 +1,12 @@
 // Decode attention over key ranges: a sliding window with sink tokens, and a batch that shares a prefix.
 //
 // attn_ranges_kernel serves one query per (sequence, query head) over the visible keys of its sequence; a
-// cluster of CTAs shares the keys of one (sequence, kv head). attn_prefix_kernel computes the part of a
-// shared prefix for the query rows of the whole batch at once and leaves one partial result per query row
-// and key chunk, which attn_ranges_kernel joins to the sequence's own keys.
+// cluster of CTAs shares the keys of one (sequence, kv head). The prefix form of the persistent prefill kernel
+// computes the part of a shared prefix for the query rows of the whole batch at once and leaves one partial
+// result per query row and key chunk, which attn_ranges_kernel joins to the sequence's own keys.
 #include <algorithm>
+
+#include <cstdlib>
 
 #include "common.cuh"
 #include "internal.h"
@@ -13,24 +15,34 @@ namespace q3 {
 namespace {
 
 // ------------------------------------------------------------------------------------- own keys
-// O = sum_i p_i v_i / sum_i p_i, p_i = 2^(q k_i log2(e) / sqrt(dh) - m) over the visible keys i, which are
-// numbered 0 .. total-1 across two slot ranges [a0, a0 + na) and [b0, b0 + nb): sinks and window, or the own
-// slots before and behind a padding block. Only visible rows are ever read (the numbers past the end repeat
-// the last key with weight 0), so nothing stored in a hidden row can reach the result.
+// O = sum_i p_i v_i / sum_i p_i, p_i = 2^(q k_i log2(e) / sqrt(dh) - m) over the visible keys i: up to three
+// runs of cache rows (sinks, window, the wrapped part of a rolling buffer; or the own slots before and
+// behind a padding block), taken in units of 16 keys.
 //
-// A warp takes 16 keys at a time straight from global memory into the fragments of warp-level mma
-// (m16n8k16, bf16 in, fp32 accumulate), heads of the kv group as the 8 columns:
-//   S^T (keys x heads) = K q^T: the lane of key row g loads 16-byte pieces 4c + t of its row; the inner
-//   index of a product may be permuted freely, and q is loaded with the same permutation;
-//   P^T moves from accumulator to operand layout by a register transpose (movmatrix);
-//   O^T (head_dim x heads) += V^T P^T: the lane pairs the 16-bit halves of its four key rows.
-// No shared memory, barrier or tensor map stands between HBM and the products, and warps run
-// independently with a running maximum each (lazily rescaled, as in the prefill kernels). 16 warps an SM hold
-// two 4 KB loads each in flight, about twice what HBM latency x bandwidth needs.
-constexpr int RG_WARPS = 8, RG_THREADS = 32 * RG_WARPS, RG_KEYS = 16, RG_MAX_CLUSTER = 8, RG_MAX_G = 8;
+// Every warp works through its own units alone, with a running maximum (lazily rescaled, as in the prefill
+// kernels): its lane 0 keeps a ring of RG_BYTES full with the K and V boxes of the coming units (TMA, 128-byte
+// swizzle), so 24 KB a warp and 192 KB an SM are on their way or in use, four times what HBM latency x
+// bandwidth needs, and no barrier joins the warps before the end. The products are warp-level mma (m16n8k16,
+// bf16 in, fp32 accumulate; the contraction is far below a tcgen05 tile) with the heads of the kv group as
+// the 8 columns: S^T (keys x heads) = K q^T, P^T from accumulator to operand layout by a register transpose
+// (movmatrix), O^T (head_dim x heads) += V^T P^T.
+// Scores of rows behind a run are masked, and their value rows are zeroed in shared memory, so nothing
+// stored in a hidden row can reach the result.
+constexpr int RG_KEYS = 16, RG_MAX_CLUSTER = 16, RG_MAX_G = 8, RG_WARPS = 4, RG_THREADS = 32 * RG_WARPS;
+constexpr int RG_BYTES = 24576;  // ring of one warp
+template <int DH>
+struct RgLayout {
+    static constexpr int NCH = DH / 64;               // 64-column boxes of a row
+    static constexpr int BOX = RG_KEYS * 128;         // bytes of a box
+    static constexpr int HALF = NCH * BOX;            // K (or V) of a unit
+    static constexpr int ST = RG_BYTES / (2 * HALF);  // units in the ring: 3 (dh 128) or 6 (dh 64)
+    static constexpr int SMEM = RG_WARPS * RG_BYTES + 1024;
+};
+// two CTAs an SM; the warps' results take the first 16 KB of the rings once all of them are done
+static_assert(2 * (RG_WARPS * RG_BYTES + 1024 + 8192) <= 227 * 1024, "shared memory");
 
 struct RangeArgs {
-    const __nv_bfloat16 *q, *k, *v;
+    const __nv_bfloat16* q;
     __nv_bfloat16* out;
     const int* len0;
     int len_stride;
@@ -38,42 +50,80 @@ struct RangeArgs {
     // window and sinks; ring > 0: rows [0, sink_rows) keep the first slots, the others wrap over ring rows
     int window, sinks, sink_rows, ring;
     const int* meta;    // own slots of a shared prefix: SeqMap::meta, or null
-    const float* recs;  // [B * Hq][nrec][DH + 4] partial results to join (output floats, maximum, sum)
+    const float* recs;  // [B * Hq][nrec][DH + 4] partial results to join (output sums, maximum, sum)
     int nrec;
     int C;  // CTAs per (sequence, kv head)
+    int* err;
 };
 
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
-    uint4 r;
-    asm volatile("ld.global.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
-__device__ __forceinline__ void mma_keys(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_keys(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+// 16-byte piece `piece` (8 columns) of row `row` in boxes of 16 rows x 128 bytes written with the 128-byte swizzle
+__device__ __forceinline__ uint32_t rg_addr(uint32_t base, int row, int piece) {
+    return base + (uint32_t)((piece >> 3) * RG_KEYS * 128 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+}
 
 template <int DH, bool SINKS>
-__global__ void __launch_bounds__(RG_THREADS, 2) attn_ranges_kernel(const RangeArgs a) {
-    constexpr int KC = DH / 32;  // 16-byte pieces of a key row per lane
-    constexpr int VC = DH / 64;  // 16-byte pieces of a value row per lane
-    __shared__ float so[RG_WARPS][RG_MAX_G][DH];
-    __shared__ float sm[RG_WARPS][RG_MAX_G], sl[RG_WARPS][RG_MAX_G], sf[RG_WARPS][RG_MAX_G];
-    __shared__ float cm[RG_MAX_G], cl[RG_MAX_G];
+__global__ void __launch_bounds__(RG_THREADS, 2)
+    attn_ranges_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const RangeArgs a) {
+    using Ly = RgLayout<DH>;
+    constexpr int NW = RG_WARPS, THREADS = RG_THREADS, ST = Ly::ST;
+    constexpr int MAX_PARTS = RG_MAX_CLUSTER + kPrefixMaxChunks;
+    extern __shared__ uint8_t rg_raw[];
+    const uint32_t raw_addr = smem_u32(rg_raw);
+    uint8_t* rings = rg_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    auto so = reinterpret_cast<float(*)[RG_MAX_G][DH]>(rings);  // the warps' output sums, once the rings are done
+    __shared__ uint64_t bars[RG_WARPS][2 * ST];                 // [K of each stage, V of each stage]
+    __shared__ float sm[NW][RG_MAX_G], sl[NW][RG_MAX_G];
+    __shared__ float cm[RG_MAX_G], cl[RG_MAX_G];                   // this CTA's maximum and sum
+    __shared__ float pm[RG_MAX_G][MAX_PARTS], pl[RG_MAX_G][MAX_PARTS];  // of every part: CTAs, then prefix records
+    __shared__ float inv[RG_MAX_G];
+    __shared__ int abort_sh;
+    volatile int* abort_flag = &abort_sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gq = lane >> 2, tq = lane & 3;  // fragment coordinates
     const int rank = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
+    uint64_t* k_full = bars[warp];
+    uint64_t* v_full = bars[warp] + ST;
+    if (threadIdx.x == 0) abort_sh = 0;
+    if (lane == 0) {
+        for (int i = 0; i < 2 * ST; ++i) mbar_init(&bars[warp][i], 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    __syncthreads();
     // Without partial results to join this is an ordinary dependent launch. With them, the prefix kernel
     // before it has itself waited for everything earlier before it let this kernel start, and only the
     // join below has to wait for the prefix kernel.
@@ -81,14 +131,39 @@ __global__ void __launch_bounds__(RG_THREADS, 2) attn_ranges_kernel(const RangeA
         pdl_wait();
         pdl_trigger();
     }
+    // q^T fragments: column gq = query head gq of the group (zero past G)
+    uint32_t qf[DH / 16][2];
+    {
+        const uint32_t* qrow = reinterpret_cast<const uint32_t*>(a.q + ((size_t)b * a.Hq + (size_t)j * a.G + gq) * DH);
+#pragma unroll
+        for (int ks = 0; ks < DH / 16; ++ks) {
+            qf[ks][0] = gq < a.G ? __ldcg(qrow + ks * 8 + tq) : 0u;
+            qf[ks][1] = gq < a.G ? __ldcg(qrow + ks * 8 + 4 + tq) : 0u;
+        }
+    }
     int n = __ldcg(a.len0 + (size_t)b * a.len_stride);
     n = n < 0 ? 0 : min(n, 1 << 30) + 1;
     if (!SINKS || a.ring == 0) n = min(n, a.cap);
-    int a0 = 0, na, b0, nb;
+    // the runs of visible rows
+    int row[3] = {0, 0, 0}, cnt[3] = {0, 0, 0};
     if constexpr (SINKS) {
-        b0 = max(0, n - a.window);
-        nb = n - b0;
-        na = min(a.sinks, b0);
+        const int lo = max(0, n - a.window);
+        cnt[0] = min(a.sinks, lo);
+        if (a.ring == 0) {
+            row[1] = lo;
+            cnt[1] = n - lo;
+        } else if (lo < a.sink_rows) {  // the ring's first turn
+            row[1] = lo;
+            cnt[1] = min(n, a.sink_rows) - lo;
+            row[2] = a.sink_rows;
+            cnt[2] = max(0, n - a.sink_rows);
+        } else {
+            const int at = (lo - a.sink_rows) % a.ring;
+            row[1] = a.sink_rows + at;
+            cnt[1] = min(n - lo, a.ring - at);
+            row[2] = a.sink_rows;
+            cnt[2] = n - lo - cnt[1];
+        }
     } else {
         int ps = 0, pe = 0, psh = 0;
         if (a.meta) {
@@ -96,124 +171,121 @@ __global__ void __launch_bounds__(RG_THREADS, 2) attn_ranges_kernel(const RangeA
             psh = __ldcg(a.meta + 1);
             pe = ps + __ldcg(a.meta + kSeqMetaHead + b);
         }
-        a0 = min(max(psh, 0), n);
-        const int a1 = min(max(ps, a0), n);
-        na = a1 - a0;
-        b0 = min(max(pe, a1), n);
-        nb = n - b0;
+        row[0] = min(max(psh, 0), n);
+        const int end = min(max(ps, row[0]), n);
+        cnt[0] = end - row[0];
+        row[1] = min(max(pe, end), n);
+        cnt[1] = n - row[1];
     }
-    const int total = na + nb;
-    // rolling buffer: whole turns before the first slot of the second range
-    int turns = 0;
-    if (SINKS && a.ring > 0) turns = (max(b0, a.sink_rows) - a.sink_rows) / a.ring * a.ring;
-    auto row_of = [&](int i) -> int {  // cache row of visible key i
-        if (i < na) return a0 + i;
-        int s = b0 + (i - na);
-        if (SINKS && a.ring > 0 && s >= a.sink_rows) {
-            s -= turns;
-            if (s >= a.sink_rows + a.ring) s -= a.ring;
-        }
-        return s;
+    const int n0 = (cnt[0] + RG_KEYS - 1) / RG_KEYS, n1 = n0 + (cnt[1] + RG_KEYS - 1) / RG_KEYS;
+    const int units = n1 + (cnt[2] + RG_KEYS - 1) / RG_KEYS;
+    // first cache row of unit u, and how many rows of it are visible
+    auto unit = [&](int u, int& valid) -> int {
+        const int first = u < n0 ? 0 : u < n1 ? n0 : n1;
+        const int r = u < n0 ? row[0] : u < n1 ? row[1] : row[2], c = u < n0 ? cnt[0] : u < n1 ? cnt[1] : cnt[2];
+        valid = min(RG_KEYS, c - (u - first) * RG_KEYS);
+        return r + (u - first) * RG_KEYS;
     };
-    const int units = (total + RG_KEYS - 1) / RG_KEYS;
     const int u0 = (int)((long long)units * rank / a.C), u1 = (int)((long long)units * (rank + 1) / a.C);
+    const int mine = u1 - u0 > warp ? (u1 - u0 - warp + NW - 1) / NW : 0;  // units u0 + warp + NW i
 
-    const __nv_bfloat16* kb = a.k + ((size_t)b * a.Hkv + j) * a.cap * DH;
-    const __nv_bfloat16* vb = a.v + ((size_t)b * a.Hkv + j) * a.cap * DH;
-    // q^T fragments: column gq = query head gq of the group (zero past G)
-    uint4 qf[KC];
-    {
-        const __nv_bfloat16* qrow = a.q + ((size_t)b * a.Hq + (size_t)j * a.G + gq) * DH;
+    uint8_t* ring_p = rings + warp * RG_BYTES;
+    const uint32_t ring_a = smem_u32(ring_p);
+    const int z = b * a.Hkv + j;
+    auto load = [&](int i) {  // lane 0
+        int valid;
+        const int y = unit(u0 + warp + NW * i, valid), st = i % ST;
+        uint8_t* dst = ring_p + st * 2 * Ly::HALF;
+        mbar_expect_tx(&k_full[st], Ly::HALF);
 #pragma unroll
-        for (int c = 0; c < KC; ++c)
-            qf[c] = gq < a.G ? __ldcg(reinterpret_cast<const uint4*>(qrow) + c * 4 + tq) : make_uint4(0, 0, 0, 0);
-    }
-    uint4 kr[2][KC], vr[4][VC];
-    // lane i < 16 works out the row of the unit's key i, the others take it from there
-    auto unit_row = [&](int u) { return row_of(min(u * RG_KEYS + (lane & 15), total - 1)); };
-    auto load_k = [&](int my_row) {
+        for (int c = 0; c < Ly::NCH; ++c) tma_load_3d(dst + c * Ly::BOX, &tmK, &k_full[st], c * 64, y, z);
+        mbar_expect_tx(&v_full[st], Ly::HALF);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = __shfl_sync(0xffffffffu, my_row, gq + 8 * r);
-            const uint4* p = reinterpret_cast<const uint4*>(kb + (size_t)row * DH) + tq;
-#pragma unroll
-            for (int c = 0; c < KC; ++c) kr[r][c] = ld_stream16(p + c * 4);
-        }
+        for (int c = 0; c < Ly::NCH; ++c)
+            tma_load_3d(dst + Ly::HALF + c * Ly::BOX, &tmV, &v_full[st], c * 64, y, z);
     };
-    auto load_v = [&](int my_row) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = __shfl_sync(0xffffffffu, my_row, 2 * tq + (r & 1) + 8 * (r >> 1));
-            const uint4* p = reinterpret_cast<const uint4*>(vb + (size_t)row * DH) + gq;
-#pragma unroll
-            for (int c = 0; c < VC; ++c) vr[r][c] = ld_stream16(p + c * 8);
-        }
-    };
+    if (lane == 0)
+        for (int i = 0; i < min(ST, mine); ++i) load(i);
+
     const float sl2 = kLog2e / sqrtf((float)DH);
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2 tq and 2 tq + 1
-    float o[DH / 16][4];  // tile (c, w): rows gq and gq + 8 are dims c*64 + 8 gq + 2 w and the next one
+    float o[DH / 16][4];                                       // tile t: rows are dims 16 t + gq and 16 t + gq + 8
 #pragma unroll
     for (int t = 0; t < DH / 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-
-    int u = u0 + warp;
-    if (u < u1) {
-        int my_row = unit_row(u);
-        load_k(my_row);
-        load_v(my_row);
-        for (; u < u1; u += RG_WARPS) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+    bool ok = true;
+    int i = 0;
+    for (; i < mine; ++i) {
+        const int st = i % ST, ph = (i / ST) & 1;
+        int valid;
+        unit(u0 + warp + NW * i, valid);
+        const uint32_t ka = ring_a + st * 2 * Ly::HALF, va = ka + Ly::HALF;
+        if (!__all_sync(0xffffffffu, mbar_wait_suspend(&k_full[st], ph, abort_flag))) { ok = false; break; }
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                mma_keys(d, kr[0][c].x, kr[1][c].x, kr[0][c].y, kr[1][c].y, qf[c].x, qf[c].y);
-                mma_keys(d, kr[0][c].z, kr[1][c].z, kr[0][c].w, kr[1][c].w, qf[c].z, qf[c].w);
+        for (int ks = 0; ks < DH / 16; ++ks) {
+            uint32_t f[4];
+            ldsm4(rg_addr(ka, krow, 2 * ks + (lane >> 4)), f);
+            mma_keys(d, f, qf[ks][0], qf[ks][1]);
+        }
+        const bool in0 = gq < valid, in1 = gq + 8 < valid;
+        const float v0 = in0 ? d[0] * sl2 : -INFINITY, v1 = in0 ? d[1] * sl2 : -INFINITY;
+        const float v2 = in1 ? d[2] * sl2 : -INFINITY, v3 = in1 ? d[3] * sl2 : -INFINITY;
+        float x0 = fmaxf(v0, v2), x1 = fmaxf(v1, v3);
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) {
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, s));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, s));
+        }
+        // O and the sums move to a larger maximum only when it grew by more than 8 (P <= 2^8)
+        const bool g0 = x0 > m0 + 8.f, g1 = x1 > m1 + 8.f;
+        if (__any_sync(0xffffffffu, g0 | g1)) {
+            const float f0 = g0 ? ex2_approx(m0 - x0) : 1.f, f1 = g1 ? ex2_approx(m1 - x1) : 1.f;
+            m0 = g0 ? x0 : m0;
+            m1 = g1 ? x1 : m1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int t = 0; t < DH / 16; ++t) {
+                o[t][0] *= f0;
+                o[t][1] *= f1;
+                o[t][2] *= f0;
+                o[t][3] *= f1;
             }
-            const bool more = u + RG_WARPS < u1;
-            if (more) {
-                my_row = unit_row(u + RG_WARPS);
-                load_k(my_row);
+        }
+        const float s0 = m0 == -INFINITY ? 0.f : m0, s1 = m1 == -INFINITY ? 0.f : m1;
+        const float p0 = ex2_approx(v0 - s0), p1 = ex2_approx(v1 - s1);
+        const float p2 = ex2_approx(v2 - s0), p3 = ex2_approx(v3 - s1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        // P to bf16 for the product, as in the other attention kernels; the sums keep fp32
+        const uint32_t b_lo = transpose8x8(pack_bf16(p0, p1)), b_hi = transpose8x8(pack_bf16(p2, p3));
+        if (!__all_sync(0xffffffffu, mbar_wait_suspend(&v_full[st], ph, abort_flag))) { ok = false; break; }
+        if (valid < RG_KEYS) {  // value rows behind the run may hold anything: 0 * NaN must not reach O
+            for (int e = lane; e < (RG_KEYS - valid) * (DH / 8); e += 32) {
+                const int r = valid + e / (DH / 8), piece = e % (DH / 8);
+                *reinterpret_cast<uint4*>(ring_p + (rg_addr(va, r, piece) - ring_a)) = make_uint4(0, 0, 0, 0);
             }
-            const int i0 = u * RG_KEYS + gq;
-            const bool in0 = i0 < total, in1 = i0 + 8 < total;
-            const float v0 = in0 ? d[0] * sl2 : -INFINITY, v1 = in0 ? d[1] * sl2 : -INFINITY;
-            const float v2 = in1 ? d[2] * sl2 : -INFINITY, v3 = in1 ? d[3] * sl2 : -INFINITY;
-            float x0 = fmaxf(v0, v2), x1 = fmaxf(v1, v3);
+            fence_proxy_async_smem();  // the ring's next copy comes after these stores
+            __syncwarp();
+        }
+        const int vrow = (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
-            for (int s = 4; s < 32; s <<= 1) {
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, s));
-                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, s));
-            }
-            // O and the sums move to a larger maximum only when it grew by more than 8 (P <= 2^8)
-            const bool g0 = x0 > m0 + 8.f, g1 = x1 > m1 + 8.f;
-            if (__any_sync(0xffffffffu, g0 | g1)) {
-                const float f0 = g0 ? ex2_approx(m0 - x0) : 1.f, f1 = g1 ? ex2_approx(m1 - x1) : 1.f;
-                m0 = g0 ? x0 : m0;
-                m1 = g1 ? x1 : m1;
-                l0 *= f0;
-                l1 *= f1;
-#pragma unroll
-                for (int t = 0; t < DH / 16; ++t) {
-                    o[t][0] *= f0;
-                    o[t][1] *= f1;
-                    o[t][2] *= f0;
-                    o[t][3] *= f1;
-                }
-            }
-            const float n0 = m0 == -INFINITY ? 0.f : m0, n1 = m1 == -INFINITY ? 0.f : m1;
-            const float p0 = ex2_approx(v0 - n0), p1 = ex2_approx(v1 - n1);
-            const float p2 = ex2_approx(v2 - n0), p3 = ex2_approx(v3 - n1);
-            l0 += p0 + p2;
-            l1 += p1 + p3;
-            // P to bf16 for the product, as in the other attention kernels; the sums keep fp32
-            const uint32_t b_lo = transpose8x8(pack_bf16(p0, p1)), b_hi = transpose8x8(pack_bf16(p2, p3));
-#pragma unroll
-            for (int c = 0; c < VC; ++c)
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t e0 = word(vr[0][c], w), e1 = word(vr[1][c], w), e2 = word(vr[2][c], w), e3 = word(vr[3][c], w);
-                    mma_keys(o[c * 4 + w], __byte_perm(e0, e1, 0x5410), __byte_perm(e0, e1, 0x7632),
-                             __byte_perm(e2, e3, 0x5410), __byte_perm(e2, e3, 0x7632), b_lo, b_hi);
-                }
-            if (more) load_v(my_row);
+        for (int t = 0; t < DH / 16; ++t) {
+            uint32_t f[4];
+            ldsm4_trans(rg_addr(va, vrow, 2 * t + ((lane >> 3) & 1)), f);
+            mma_keys(o[t], f, b_lo, b_hi);
+        }
+        __syncwarp();  // every lane has read the stage
+        if (lane == 0 && i + ST < mine) load(i + ST);
+    }
+    if (!ok) {  // give up: wait, bounded, for the copies still on their way
+        *abort_flag = 1;
+        if (a.err && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
+        int never = 0;
+        for (int r = i; r < min(i + ST, mine); ++r) {
+            mbar_wait_suspend(&k_full[r % ST], (r / ST) & 1, &never);
+            mbar_wait_suspend(&v_full[r % ST], (r / ST) & 1, &never);
         }
     }
 #pragma unroll
@@ -221,12 +293,15 @@ __global__ void __launch_bounds__(RG_THREADS, 2) attn_ranges_kernel(const RangeA
         l0 += __shfl_xor_sync(0xffffffffu, l0, s);
         l1 += __shfl_xor_sync(0xffffffffu, l1, s);
     }
-    // join the warps
+    __syncthreads();  // the rings are done: their first bytes take the warps' results
+    // the warps' partial results
 #pragma unroll
     for (int t = 0; t < DH / 16; ++t) {
-        const int dim = (t >> 2) * 64 + gq * 8 + (t & 3) * 2;
-        *reinterpret_cast<float2*>(&so[warp][2 * tq][dim]) = make_float2(o[t][0], o[t][2]);
-        *reinterpret_cast<float2*>(&so[warp][2 * tq + 1][dim]) = make_float2(o[t][1], o[t][3]);
+        const int dim = t * 16 + gq;
+        so[warp][2 * tq][dim] = o[t][0];
+        so[warp][2 * tq + 1][dim] = o[t][1];
+        so[warp][2 * tq][dim + 8] = o[t][2];
+        so[warp][2 * tq + 1][dim + 8] = o[t][3];
     }
     if (gq == 0) {
         sm[warp][2 * tq] = m0;
@@ -235,394 +310,146 @@ __global__ void __launch_bounds__(RG_THREADS, 2) attn_ranges_kernel(const RangeA
         sl[warp][2 * tq + 1] = l1;
     }
     __syncthreads();
-    if (threadIdx.x < RG_MAX_G) {
-        const int h = threadIdx.x;
-        float M = sm[0][h], Lh = 0.f;
+    // four dims of one head per thread and step
+    const int quads = a.G * (DH / 4);
+    const bool alone = a.C == 1 && a.nrec == 0;
+    auto store = [&](int h, int dd, float4 v, float scale) {
+        const size_t row = (size_t)b * a.Hq + (size_t)j * a.G + h;
+        *reinterpret_cast<uint2*>(a.out + row * DH + dd) =
+            make_uint2(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale));
+    };
+    for (int e = threadIdx.x; e < quads; e += THREADS) {  // join the warps
+        const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
+        float M = sm[0][h], L = 0.f;
 #pragma unroll
-        for (int w = 1; w < RG_WARPS; ++w) M = fmaxf(M, sm[w][h]);
+        for (int w = 1; w < NW; ++w) M = fmaxf(M, sm[w][h]);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < RG_WARPS; ++w) {
+        for (int w = 0; w < NW; ++w) {
             const float f = sm[w][h] == -INFINITY ? 0.f : ex2_approx(sm[w][h] - M);
-            sf[w][h] = f;
-            Lh = fmaf(sl[w][h], f, Lh);
+            const float4 x = *reinterpret_cast<const float4*>(&so[w][h][dd]);
+            L = fmaf(sl[w][h], f, L);
+            v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
         }
-        cm[h] = M;
-        cl[h] = Lh;
+        if (alone) {
+            store(h, dd, v, L == 0.f ? 0.f : 1.f / L);  // no visible key: zeros
+        } else {
+            *reinterpret_cast<float4*>(&so[0][h][dd]) = v;
+            if (dd == 0) {
+                cm[h] = M;
+                cl[h] = L;
+            }
+        }
     }
-    __syncthreads();
-    const int elems = a.G * DH;
+    if (alone) return;
+    // join the cluster's CTAs and the prefix records; each CTA finishes a share of the output
     if (a.C > 1) {
-        for (int e = threadIdx.x; e < elems; e += RG_THREADS) {
-            const int h = e / DH, dd = e % DH;
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < RG_WARPS; ++w) v = fmaf(so[w][h][dd], sf[w][h], v);
-            so[0][h][dd] = v;
-        }
         cluster_sync();
+    } else {
+        __syncthreads();
     }
     if (a.nrec > 0) {
         pdl_wait();  // the prefix kernel's partial results
         pdl_trigger();
     }
-    // join the cluster's CTAs and the prefix records; each CTA finishes a share of the output
-    for (int e = threadIdx.x + RG_THREADS * rank; e < elems; e += RG_THREADS * a.C) {
-        const int h = e / DH, dd = e % DH;
-        const size_t row = (size_t)b * a.Hq + (size_t)j * a.G + h;
-        const float* rec = a.recs + row * a.nrec * (DH + 4);
-        float M = a.C > 1 ? -INFINITY : cm[h];
-        if (a.C > 1)
-            for (int c = 0; c < a.C; ++c) M = fmaxf(M, ld_cluster_f32(cluster_addr(&cm[h], c)));
-        for (int r = 0; r < a.nrec; ++r) M = fmaxf(M, __ldcg(rec + (size_t)r * (DH + 4) + DH));
-        float num = 0.f, den = 0.f;
-        if (a.C > 1) {
-            for (int c = 0; c < a.C; ++c) {
-                const float mc = ld_cluster_f32(cluster_addr(&cm[h], c));
-                const float f = mc == -INFINITY ? 0.f : ex2_approx(mc - M);
-                den = fmaf(ld_cluster_f32(cluster_addr(&cl[h], c)), f, den);
-                num = fmaf(ld_cluster_f32(cluster_addr(&so[0][h][dd], c)), f, num);
+    const int parts = a.C + a.nrec;
+    const float* rec0 = a.recs + ((size_t)b * a.Hq + (size_t)j * a.G) * a.nrec * (DH + 4);
+    for (int e = threadIdx.x; e < parts * RG_MAX_G; e += THREADS) {
+        const int p = e / RG_MAX_G, h = e % RG_MAX_G;
+        if (h < a.G) {
+            if (p < a.C) {
+                pm[h][p] = ld_cluster_f32(cluster_addr(&cm[h], p));
+                pl[h][p] = ld_cluster_f32(cluster_addr(&cl[h], p));
+            } else {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(
+                    rec0 + ((size_t)h * a.nrec + p - a.C) * (DH + 4) + DH));
+                pm[h][p] = ml.x;
+                pl[h][p] = ml.y;
             }
-        } else {
-            const float f = cm[h] == -INFINITY ? 0.f : ex2_approx(cm[h] - M);
-            float v = 0.f;
+        }
+    }
+    __syncthreads();
+    for (int h = warp; h < a.G; h += NW) {  // the parts' weights, into pm
+        float M = -INFINITY, L = 0.f;
+        for (int p = lane; p < parts; p += 32) M = fmaxf(M, pm[h][p]);
 #pragma unroll
-            for (int w = 0; w < RG_WARPS; ++w) v = fmaf(so[w][h][dd], sf[w][h], v);
-            den = cl[h] * f;
-            num = v * f;
+        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+        for (int p = lane; p < parts; p += 32) {
+            const float f = pm[h][p] == -INFINITY ? 0.f : ex2_approx(pm[h][p] - M);
+            L = fmaf(pl[h][p], f, L);
+            pm[h][p] = f;
         }
-        for (int r = 0; r < a.nrec; ++r) {
-            const float* rc = rec + (size_t)r * (DH + 4);
-            const float mc = __ldcg(rc + DH);
-            const float f = mc == -INFINITY ? 0.f : ex2_approx(mc - M);
-            den = fmaf(__ldcg(rc + DH + 1), f, den);
-            num = fmaf(__ldcg(rc + dd), f, num);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+        if (lane == 0) inv[h] = L == 0.f ? 0.f : 1.f / L;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x + THREADS * rank; e < quads; e += THREADS * a.C) {
+        const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4& x, float f) {
+            v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
+        };
+        if (a.C == 1) {
+            add(*reinterpret_cast<const float4*>(&so[0][h][dd]), pm[h][0]);
+        } else {
+#pragma unroll 4
+            for (int p = 0; p < a.C; ++p) add(ld_cluster_f32x4(cluster_addr(&so[0][h][dd], p)), pm[h][p]);
         }
-        a.out[row * DH + dd] = __float2bfloat16_rn(den == 0.f ? 0.f : num / den);  // no visible key: zeros
+        const float* rec = rec0 + (size_t)h * a.nrec * (DH + 4) + dd;
+#pragma unroll 8
+        for (int r = 0; r < a.nrec; ++r)
+            add(__ldcg(reinterpret_cast<const float4*>(rec + (size_t)r * (DH + 4))), pm[h][a.C + r]);
+        store(h, dd, v, inv[h]);
     }
     if (a.C > 1) cluster_sync();  // every CTA's partial stays in shared memory until the others have read it
 }
 
-// CTAs per (sequence, kv head): enough to give two CTAs to every SM, while each warp keeps a 16-key unit.
+// CTAs per (sequence, kv head): as many as two CTAs on every SM take, while each warp keeps a 16-key unit.
 int ranges_cluster(int B, int Hkv, int max_keys) {
     int c = 1;
     while (c < RG_MAX_CLUSTER && (long long)B * Hkv * c * 2 <= 2 * device_sm_count() &&
            max_keys >= 2 * c * RG_WARPS * RG_KEYS)
         c *= 2;
+    if (getenv("Q3_C")) c = atoi(getenv("Q3_C"));
     return c;
 }
 
-template <bool SINKS>
-cudaError_t ranges_launch(const RangeArgs& a0, int B, int dh, int max_keys, cudaStream_t st) {
-    RangeArgs a = a0;
+template <int DH, bool SINKS>
+cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfloat16* v, int B, int max_keys,
+                             cudaStream_t st) {
+    CUtensorMap tk, tv;
+    const uint64_t heads = (uint64_t)B * a.Hkv;
+    if (!encode_tmap_bf16_rows(&tk, k, DH, a.cap, a.cap, heads, RG_KEYS) ||
+        !encode_tmap_bf16_rows(&tv, v, DH, a.cap, a.cap, heads, RG_KEYS))
+        return cudaErrorInvalidValue;
     a.C = ranges_cluster(B, a.Hkv, max_keys);
-    const dim3 grid(a.C, a.Hkv, B), block(RG_THREADS);
-    if (dh == 128) return launch_pdl_cluster(attn_ranges_kernel<128, SINKS>, grid, block, a.C, 0, st, a);
-    if (dh == 64) return launch_pdl_cluster(attn_ranges_kernel<64, SINKS>, grid, block, a.C, 0, st, a);
+    return launch_pdl_cluster(attn_ranges_kernel<DH, SINKS>, dim3(a.C, a.Hkv, B), dim3(RG_THREADS), a.C,
+                              RgLayout<DH>::SMEM, st, tk, tv, a);
+}
+
+template <bool SINKS>
+cudaError_t ranges_launch(const RangeArgs& a, const __nv_bfloat16* k, const __nv_bfloat16* v, int B, int dh, int max_keys,
+                          cudaStream_t st) {
+    if (dh == 128) return ranges_launch_dh<128, SINKS>(a, k, v, B, max_keys, st);
+    if (dh == 64) return ranges_launch_dh<64, SINKS>(a, k, v, B, max_keys, st);
     return cudaErrorInvalidValue;
 }
 
-// ------------------------------------------------------------------------------------ shared prefix
-// Flash attention of all the batch's query rows of one kv head against a chunk of the prefix keys, on the
-// tensor cores (tcgen05, accumulators in tensor memory, operands by TMA). A tile of 128 rows holds the G
-// query heads of floor(128 / G) sequences; a CTA serves NT tiles from one read of each key and value tile.
-// K and V of the prefix are read once from HBM for up to 256 query rows, where the read (64 KB a 128-key tile,
-// 1.5 us at an SM's share of HBM) still covers the products (0.55 us a row tile at the measured tensor rate).
-// Roles as in the prefill kernel with a split key range: warp 0 TMA, warp 1 MMA, then four softmax warps
-// per row tile, thread <-> query row. With one row tile the scores run a tile ahead in a second region;
-// with two, one tile's scores are computed while the other's softmax runs.
-constexpr int PX_BM = 128, PX_BN = 128;
-template <int DH, int NT>
-struct PxLayout {
-    static constexpr int NCH = DH / 64;
-    static constexpr int ST = NT == 1 ? 3 : 2;  // stages of the key ring and of the value ring
-    static constexpr int Q_BYTES = PX_BM * DH * 2;
-    static constexpr int KV_BYTES = PX_BN * DH * 2;
-    static constexpr int K_OFF = NT * Q_BYTES;
-    static constexpr int V_OFF = K_OFF + ST * KV_BYTES;
-    static constexpr int BAR_OFF = V_OFF + ST * KV_BYTES;
-    static constexpr int SMEM = BAR_OFF + 256 + 1024;
-    static constexpr int THREADS = 64 + 128 * NT;
-};
-static_assert(PxLayout<128, 1>::SMEM <= 227 * 1024 && PxLayout<128, 2>::SMEM <= 227 * 1024, "shared memory");
-
-template <int DH, int NT>
-__global__ void __launch_bounds__(PxLayout<DH, NT>::THREADS, 1)
-    attn_prefix_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, int B, int Hq, int G, int P, int row_blocks, int chunks,
-                       float* __restrict__ recs, int* err) {
-    using Ly = PxLayout<DH, NT>;
-    constexpr int NCH = Ly::NCH, ST = Ly::ST;
-    constexpr uint32_t IDESC_S = idesc_bf16(PX_BM, PX_BN);
-    constexpr uint32_t IDESC_O = idesc_bf16(PX_BM, DH, true);
-    constexpr uint32_t TM_O = 2 * PX_BN;  // O of row tile x at TM_O + 128 x
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw_addr = smem_u32(smem_raw);
-    uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::BAR_OFF);
-    uint64_t* q_full = bars;
-    uint64_t* k_full = bars + 1;   // [ST]
-    uint64_t* v_full = bars + 4;   // [ST]
-    uint64_t* k_empty = bars + 7;  // [ST]
-    uint64_t* v_empty = bars + 10; // [ST]
-    uint64_t* s_full = bars + 13;  // [2] per score region
-    uint64_t* p_full = bars + 15;  // [2] per score region
-    uint64_t* o_done = bars + 17;  // [NT]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 20);
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rb = blockIdx.x % row_blocks, chunk = blockIdx.x / row_blocks % chunks;
-    const int j = blockIdx.x / (row_blocks * chunks);
-    const int spt = PX_BM / G;  // sequences per row tile
-    const int tiles = (P + PX_BN - 1) / PX_BN;
-    const int t0 = (int)((long long)tiles * chunk / chunks), nt = (int)((long long)tiles * (chunk + 1) / chunks) - t0;
-    // the last row block may hold fewer row tiles
-    const int live = min(NT, (B - rb * NT * spt + spt - 1) / spt);
-
-    if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
-        for (int i = 0; i < ST; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&v_full[i], 1);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
-        }
-        for (int x = 0; x < NT; ++x) mbar_init(&o_done[x], 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-        tma_prefetch_desc(&tmQ);
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-    }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    bool ok = true;
-    pdl_wait();
-    pdl_trigger();
-    // score region of row tile x at the CTA's key tile i, and how many earlier key tiles used it
-    auto region = [](int x, int i) { return NT == 2 ? x : (i & 1); };
-    auto uses = [](int i) { return NT == 2 ? i : (i >> 1); };
-
-    if (warp == 0) {
-        if (lane == 0) {
-            mbar_expect_tx(q_full, live * NCH * spt * G * 128);
-            for (int x = 0; x < live; ++x)
-                for (int c = 0; c < NCH; ++c)
-                    tma_load_4d(smem + x * Ly::Q_BYTES + c * PX_BM * 128, &tmQ, q_full, c * 64, 0, j, (rb * NT + x) * spt);
-            for (int i = 0; i < nt; ++i) {
-                const int s = i % ST, y = (t0 + i) * PX_BN;
-                const uint32_t free_ph = ((i / ST) & 1) ^ 1;
-                if (!mbar_wait_suspend(&k_empty[s], free_ph, abort_flag)) { ok = false; break; }
-                mbar_expect_tx(&k_full[s], Ly::KV_BYTES);
-                for (int c = 0; c < NCH; ++c)
-                    tma_load_3d(smem + Ly::K_OFF + s * Ly::KV_BYTES + c * PX_BN * 128, &tmK, &k_full[s], c * 64, y, j);
-                if (!mbar_wait_suspend(&v_empty[s], free_ph, abort_flag)) { ok = false; break; }
-                mbar_expect_tx(&v_full[s], Ly::KV_BYTES);
-                for (int c = 0; c < NCH; ++c)
-                    tma_load_3d(smem + Ly::V_OFF + s * Ly::KV_BYTES + c * PX_BN * 128, &tmV, &v_full[s], c * 64, y, j);
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            auto issue_s = [&](int x, int i) -> bool {
-                const int s = i % ST, r = region(x, i);
-                if (!mbar_wait_suspend(&k_full[s], (i / ST) & 1, abort_flag)) return false;
-                tc_fence_after();
-                const uint32_t sq = smem_u32(smem + x * Ly::Q_BYTES);
-                const uint32_t sk = smem_u32(smem + Ly::K_OFF + s * Ly::KV_BYTES);
-#pragma unroll
-                for (int kk = 0; kk < DH / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * PX_BM * 128 + (kk & 3) * 32;
-                    umma_bf16_ss(tmem + r * PX_BN, sdesc_kmajor_sw128(sq + off), sdesc_kmajor_sw128(sk + off), IDESC_S,
-                                 kk > 0);
-                }
-                umma_commit(&s_full[r]);
-                if (x == live - 1) umma_commit(&k_empty[s]);
-                return true;
-            };
-            ok = mbar_wait_suspend(q_full, 0, abort_flag);
-            for (int x = 0; ok && x < live; ++x) ok = issue_s(x, 0);
-            if (NT == 1 && ok && nt > 1) ok = issue_s(0, 1);
-            for (int i = 0; ok && i < nt; ++i) {
-                const int s = i % ST;
-                if (!mbar_wait_suspend(&v_full[s], (i / ST) & 1, abort_flag)) { ok = false; break; }
-                const uint32_t sv = smem_u32(smem + Ly::V_OFF + s * Ly::KV_BYTES);
-                for (int x = 0; ok && x < live; ++x) {
-                    const int r = region(x, i);
-                    if (!mbar_wait_suspend(&p_full[r], uses(i) & 1, abort_flag)) { ok = false; break; }
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < PX_BN / 16; ++kk) {
-                        const uint64_t bd = sdesc_mnmajor_sw128(sv + kk * 16 * 128, PX_BN * 128);
-                        umma_bf16_ts(tmem + TM_O + x * 128, tmem + r * PX_BN + kk * 8, bd, IDESC_O, (i | kk) != 0);
-                    }
-                    umma_commit(&o_done[x]);
-                    if (x == live - 1) umma_commit(&v_empty[s]);
-                    const int nxt = NT == 2 ? i + 1 : i + 2;  // the next key tile whose scores go to this region
-                    if (nxt < nt) ok = issue_s(x, nxt);
-                }
-            }
-        }
-    } else if ((warp - 2) / 4 < live) {
-        const int x = (warp - 2) >> 2;
-        const int quarter = warp & 3, row = quarter * 32 + lane;
-        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tm_o = tmem + lane_off + TM_O + x * 128;
-        const float sl2 = kLog2e / sqrtf((float)DH);
-        float m_used = -INFINITY, l = 0.f;
-        int pv_seen = 0;
-        auto confirm_pv = [&](int upto) -> bool {
-            while (pv_seen < upto) {
-                if (!mbar_wait_suspend(&o_done[x], pv_seen & 1, abort_flag)) return false;
-                ++pv_seen;
-            }
-            return true;
-        };
-        for (int i = 0; i < nt; ++i) {
-            const int r = region(x, i);
-            const uint32_t tm_s = tmem + lane_off + r * PX_BN;
-            if (!__all_sync(0xffffffffu, mbar_wait_suspend(&s_full[r], uses(i) & 1, abort_flag))) { ok = false; break; }
-            tc_fence_after();
-            uint32_t sr[PX_BN];
-#pragma unroll
-            for (int c = 0; c < PX_BN / 32; ++c)
-                tmem_ld_32x32b_x32(tm_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-            tmem_ld_wait();
-            const int left = P - (t0 + i) * PX_BN;  // keys of this tile
-            if (left < PX_BN) {
-#pragma unroll
-                for (int e = 0; e < PX_BN; ++e) sr[e] = e < left ? sr[e] : __float_as_uint(-INFINITY);
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < PX_BN; e += 2) mx = fmax3(mx, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
-            mx *= sl2;
-            // lazy rescale, decided per row but executed by the whole warp (tcgen05.ld/st are warp-wide)
-            const bool grow = mx > m_used + 8.0f;
-            const float alpha = grow ? ex2_approx(m_used - mx) : 1.0f;
-            if (i > 0 && __any_sync(0xffffffffu, grow)) {
-                const bool w = confirm_pv(i);
-                if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < DH / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(tm_o + c * 32, o);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                    tmem_st_32x32b_x32(tm_o + c * 32, o);
-                }
-                tmem_st_wait();
-            }
-            if (grow) {
-                l *= alpha;
-                m_used = mx;
-            }
-            const float nm = m_used == -INFINITY ? 0.f : -m_used;
-            const float2 sl2x2 = make_float2(sl2, sl2), nmx2 = make_float2(nm, nm);
-            float2 rs2 = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float2 z = fma2(make_float2(__uint_as_float(sr[half * 64 + 2 * e]),
-                                                      __uint_as_float(sr[half * 64 + 2 * e + 1])),
-                                          sl2x2, nmx2);
-                    const float2 pp = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-                    rs2 = add2(rs2, pp);
-                    pk[e] = pack_bf16(pp.x, pp.y);
-                }
-                tmem_st_32x32b_x32(tm_s + half * 32, pk);
-            }
-            tmem_st_wait();
-            l += rs2.x + rs2.y;
-            // see the previous P V complete before releasing this P: o_done then stays within one phase
-            if (i > 0) {
-                const bool w = confirm_pv(i);
-                if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
-            }
-            tc_fence_before();
-            mbar_arrive(&p_full[r]);
-        }
-        if (ok) ok = confirm_pv(nt);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-            tc_fence_after();
-            const int s = (rb * NT + x) * spt + row / G;  // sequence of this row
-            const bool mine = row < spt * G && s < B;
-            float* rec = recs + (((size_t)s * Hq + (size_t)j * G + row % G) * chunks + chunk) * (DH + 4);
-#pragma unroll 1
-            for (int c = 0; c < DH / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(tm_o + c * 32, o);
-                tmem_ld_wait();
-                if (mine) {
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        reinterpret_cast<uint4*>(rec + c * 32)[v] =
-                            make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-                }
-            }
-            if (mine) *reinterpret_cast<float4*>(rec + DH) = make_float4(m_used, l, 0.f, 0.f);
-        }
-    }
-    if (!ok) {
-        *abort_flag = 1;
-        if (err) atomicOr(err, ERR_TIMEOUT);
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    }
-}
-
-struct PrefixPlan {
-    int nt, row_blocks, chunks;
-};
-// Two row tiles a CTA once one does not hold the batch; then as many key chunks as fill the SMs in one wave.
-PrefixPlan prefix_plan(int B, int Hkv, int G, int P) {
-    const int spt = PX_BM / G, row_tiles = (B + spt - 1) / spt, tiles = (P + PX_BN - 1) / PX_BN;
-    PrefixPlan p;
-    p.nt = row_tiles > 1 ? 2 : 1;
-    p.row_blocks = (row_tiles + p.nt - 1) / p.nt;
-    const long long ctas = (long long)Hkv * p.row_blocks;
-    p.chunks = (int)std::max<long long>(1, std::min<long long>(tiles, device_sm_count() / ctas));
-    return p;
-}
-
-template <int DH, int NT>
-cudaError_t prefix_launch(const PrefixPlan& p, const __nv_bfloat16* q, const __nv_bfloat16* kp, const __nv_bfloat16* vp, int B,
-                          int Hq, int Hkv, int prefix_cap, int P, float* recs, int* err, cudaStream_t st) {
-    using Ly = PxLayout<DH, NT>;
-    const int G = Hq / Hkv, spt = PX_BM / G;
-    CUtensorMap tq, tk, tv;
-    if (!encode_tmap_bf16_groups(&tq, q, DH, G, Hkv, B, spt) || !encode_tmap_bf16_rows(&tk, kp, DH, P, prefix_cap, Hkv) ||
-        !encode_tmap_bf16_rows(&tv, vp, DH, P, prefix_cap, Hkv))
-        return cudaErrorInvalidValue;
-    return launch_pdl(attn_prefix_kernel<DH, NT>, dim3((unsigned)p.row_blocks * p.chunks * Hkv), dim3(Ly::THREADS),
-                      Ly::SMEM, st, tq, tk, tv, B, Hq, G, P, p.row_blocks, p.chunks, recs, err);
+// Clusters of sixteen CTAs are beyond the portable size.
+template <int DH, bool SINKS>
+cudaError_t ranges_prepare() {
+    cudaError_t e = cudaFuncSetAttribute(attn_ranges_kernel<DH, SINKS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(attn_ranges_kernel<DH, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                RgLayout<DH>::SMEM);
 }
 
 }  // namespace
 
 size_t attn_decode_shared_workspace(int B, int Hq, int Hkv, int dh, int prefix_len) {
     if (prefix_len <= 0) return 0;
-    return (size_t)B * Hq * prefix_plan(B, Hkv, Hq / Hkv, prefix_len).chunks * (dh + 4) * sizeof(float);
+    return (size_t)B * Hq * attn_prefix_chunks(B, Hq, Hkv, prefix_len) * (dh + 4) * sizeof(float);
 }
 
 cudaError_t attn_decode_shared_launch(const __nv_bfloat16* q, const __nv_bfloat16* kp, const __nv_bfloat16* vp,
@@ -632,8 +459,6 @@ cudaError_t attn_decode_shared_launch(const __nv_bfloat16* q, const __nv_bfloat1
     if (B <= 0) return cudaSuccess;
     RangeArgs a{};
     a.q = q;
-    a.k = kc;
-    a.v = vc;
     a.out = out;
     a.len0 = len0;
     a.len_stride = len_stride;
@@ -643,29 +468,21 @@ cudaError_t attn_decode_shared_launch(const __nv_bfloat16* q, const __nv_bfloat1
     a.cap = cap;
     a.meta = meta;
     if (P > 0) {
-        const PrefixPlan p = prefix_plan(B, Hkv, a.G, P);
         a.recs = work;
-        a.nrec = p.chunks;
-        cudaError_t e;
-        if (dh == 128)
-            e = p.nt == 2 ? prefix_launch<128, 2>(p, q, kp, vp, B, Hq, Hkv, prefix_cap, P, work, err, st)
-                          : prefix_launch<128, 1>(p, q, kp, vp, B, Hq, Hkv, prefix_cap, P, work, err, st);
-        else
-            e = p.nt == 2 ? prefix_launch<64, 2>(p, q, kp, vp, B, Hq, Hkv, prefix_cap, P, work, err, st)
-                          : prefix_launch<64, 1>(p, q, kp, vp, B, Hq, Hkv, prefix_cap, P, work, err, st);
+        a.nrec = attn_prefix_chunks(B, Hq, Hkv, P);
+        const cudaError_t e = attn_prefix_launch(q, kp, vp, B, Hq, Hkv, dh, prefix_cap, P, work, err, st);
         if (e != cudaSuccess) return e;
     }
-    return ranges_launch<false>(a, B, dh, cap, st);
+    a.err = err;
+    return ranges_launch<false>(a, kc, vc, B, dh, cap, st);
 }
 
 cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B, int Hq,
                                      int Hkv, int dh, int cap, const int* len0, int len_stride, SinkMap sm,
-                                     __nv_bfloat16* out, cudaStream_t st) {
+                                     __nv_bfloat16* out, int* err, cudaStream_t st) {
     if (B <= 0) return cudaSuccess;
     RangeArgs a{};
     a.q = q;
-    a.k = kc;
-    a.v = vc;
     a.out = out;
     a.len0 = len0;
     a.len_stride = len_stride;
@@ -677,15 +494,15 @@ cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16
     a.sinks = sm.sinks;
     a.sink_rows = sm.sink_rows;
     a.ring = sm.ring;
-    return ranges_launch<true>(a, B, dh, (int)std::min<long long>((long long)sm.window + sm.sinks, cap), st);
+    a.err = err;
+    return ranges_launch<true>(a, kc, vc, B, dh, (int)std::min<long long>((long long)sm.window + sm.sinks, cap), st);
 }
 
 cudaError_t attention_ranges_prepare() {
-    const void* fns[] = {(const void*)attn_prefix_kernel<128, 1>, (const void*)attn_prefix_kernel<128, 2>,
-                         (const void*)attn_prefix_kernel<64, 1>, (const void*)attn_prefix_kernel<64, 2>};
-    const int smem[] = {PxLayout<128, 1>::SMEM, PxLayout<128, 2>::SMEM, PxLayout<64, 1>::SMEM, PxLayout<64, 2>::SMEM};
-    for (int i = 0; i < 4; ++i) {
-        cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, smem[i]);
+    cudaError_t (*const prepare[])() = {ranges_prepare<128, false>, ranges_prepare<128, true>, ranges_prepare<64, false>,
+                                        ranges_prepare<64, true>};
+    for (auto f : prepare) {
+        cudaError_t e = f();
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -133,9 +133,9 @@ struct GemmMaps {
     CUtensorMap a, b, c, r, v;
 };
 bool encode_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2);
-// Rows [heads][rows of row_cap][dh] in boxes of 64 x 128 x 1; rows past `rows` read as zero.
+// Rows [heads][rows of row_cap][dh] in boxes of 64 x box_rows x 1; rows past `rows` read as zero.
 bool encode_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t dh, uint64_t rows, uint64_t row_cap,
-                           uint64_t heads);
+                           uint64_t heads, uint32_t box_rows);
 // Query rows [seqs][heads][group][dh] in boxes of 64 x group x 1 x box_seqs: one head's groups of box_seqs sequences.
 bool encode_tmap_bf16_groups(CUtensorMap* map, const void* base, uint64_t dh, uint64_t group, uint64_t heads,
                              uint64_t seqs, uint32_t box_seqs);
@@ -239,10 +239,17 @@ cudaError_t attn_prefill_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat1
                                       int T, int Hq, int Hkv, int dh, int cap, const int* len0, int len_stride,
                                       SinkMap sm, __nv_bfloat16* out, int* err, cudaStream_t st);
 
+// Query rows q [B, Hq, dh] against P rows of a prefix [Hkv][prefix_cap][dh]: per query row and chunk a record of dh
+// output sums, the maximum (log2 units) and the sum, [B * Hq][attn_prefix_chunks()][dh + 4] floats.
+constexpr int kPrefixMaxChunks = 64;
+int attn_prefix_chunks(int B, int Hq, int Hkv, int P);
+cudaError_t attn_prefix_launch(const __nv_bfloat16* q, const __nv_bfloat16* kp, const __nv_bfloat16* vp, int B, int Hq,
+                               int Hkv, int dh, int prefix_cap, int P, float* recs, int* err, cudaStream_t st);
+
 // ---------------------------------------------------------------- attention over key ranges (attention_ranges.cu)
 cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B, int Hq,
                                      int Hkv, int dh, int cap, const int* len0, int len_stride, SinkMap sm,
-                                     __nv_bfloat16* out, cudaStream_t st);
+                                     __nv_bfloat16* out, int* err, cudaStream_t st);
 // Decode attention of B sequences over a shared prefix (kp, vp: [Hkv][prefix_cap][dh], P rows of it) and their own
 // slots; meta as SeqMap::meta (own slots below psh are skipped). work: attn_decode_shared_workspace() bytes.
 size_t attn_decode_shared_workspace(int B, int Hq, int Hkv, int dh, int prefix_len);

@@ -1084,7 +1084,7 @@ int qwen3_op_attention_decode_shared(const void* q, const void* kp, const void* 
         Hq / Hkv > 8 || (dh != 64 && dh != 128) || cap < 1 || (len_stride != 0 && len_stride != 1))
         return QWEN3_E_ARG;
     if (prefix_len < 0 || prefix_len > prefix_cap || (prefix_len > 0 && (!kp || !vp || !work))) return QWEN3_E_ARG;
-    const void* ptrs[] = {q, kc, vc, prefix_len > 0 ? kp : nullptr, prefix_len > 0 ? vp : nullptr, work};
+    const void* ptrs[] = {q, kc, vc, out, prefix_len > 0 ? kp : nullptr, prefix_len > 0 ? vp : nullptr, work};
     for (const void* p : ptrs)
         if (!is_aligned(p, 16)) return QWEN3_E_ARG;
     if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
@@ -1119,17 +1119,17 @@ int qwen3_op_attention_prefill_sinks(const void* q, const void* kc, const void* 
 
 int qwen3_op_attention_decode_sinks(const void* q, const void* kc, const void* vc, int B, int Hq, int Hkv, int dh, int cap,
                                     const int* len0, int len_stride, int window, int sinks, int rolling, void* out,
-                                    void* stream) {
+                                    int* err, void* stream) {
     if (!q || !kc || !vc || !len0 || !out || B < 0 || B > 65535 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv ||
         Hq / Hkv > 8 || (dh != 64 && dh != 128) || cap < 1 || (len_stride != 0 && len_stride != 1))
         return QWEN3_E_ARG;
     SinkMap sm;
     if (!sink_map(window, sinks, rolling, cap, 1, &sm)) return QWEN3_E_ARG;
-    if (!is_aligned(q, 16) || !is_aligned(kc, 16) || !is_aligned(vc, 16)) return QWEN3_E_ARG;
+    if (!is_aligned(q, 16) || !is_aligned(kc, 16) || !is_aligned(vc, 16) || !is_aligned(out, 16)) return QWEN3_E_ARG;
     if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
     return attn_decode_sinks_launch(static_cast<const bf16*>(q), static_cast<const bf16*>(kc),
                                     static_cast<const bf16*>(vc), B, Hq, Hkv, dh, cap, len0, len_stride, sm,
-                                    static_cast<bf16*>(out), static_cast<cudaStream_t>(stream)) == cudaSuccess
+                                    static_cast<bf16*>(out), err, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? QWEN3_OK
                : QWEN3_E_CUDA;
 }

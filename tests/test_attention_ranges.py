@@ -232,13 +232,13 @@ def _sinks_case(bd, Bn, T, Hq, Hkv, dh, starts, window, sinks, rolling, cap=None
         x.masked_fill_(~seen[:, None, :, None], float("nan"))
     out = torch.full((Bn * T + 1, Hq * dh), 7.0, dtype=torch.bfloat16, device="cuda")
     lens = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    err = _err()
     if decode:
-        bd.op_attention_decode_sinks(q[:, :, 0].contiguous(), k, v, lens, out[:Bn], window, sinks, rolling=rolling)
+        bd.op_attention_decode_sinks(q[:, :, 0].contiguous(), k, v, lens, out[:Bn], window, sinks, rolling=rolling, err=err)
     else:
-        err = _err()
         bd.op_attention_prefill_sinks(q, k, v, lens, out[:Bn * T], window, sinks, rolling=rolling, err=err)
-        assert int(err.item()) == 0
     torch.cuda.synchronize()
+    assert int(err.item()) == 0
     assert torch.all(out[Bn * T] == 7.0)
     got = out[:Bn * T].reshape(Bn, T, Hq, dh)
     assert torch.isfinite(got).all()
@@ -432,7 +432,7 @@ def test_library_refuses(bd):
               out=p):
         if decode:
             return L.qwen3_op_attention_decode_sinks(q, kc, vc, B, Hq, Hkv, dh, cap, len0, st, window, sinks, roll, out,
-                                                     None)
+                                                     None, None)
         return L.qwen3_op_attention_prefill_sinks(q, kc, vc, B, T, Hq, Hkv, dh, cap, len0, st, window, sinks, roll, out,
                                                   None, None)
     for kw in (dict(q=None), dict(kc=None), dict(vc=None), dict(len0=None), dict(out=None), dict(B=-1), dict(Hq=9),
