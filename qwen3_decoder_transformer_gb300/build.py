@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libqwen3_gb300.so")
-SOURCES = ["gemm.cu", "kernels.cu", "attention.cu", "attention_ranges.cu", "logprobs.cu", "runtime.cu"]
+SOURCES = ["gemm.cu", "kernels.cu", "attention.cu", "attention_tiles.cu", "attention_ranges.cu", "logprobs.cu", "runtime.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + os.path.join(ROOT, "include")]

@@ -499,32 +499,14 @@ struct PsLayout {
     static constexpr int SMEM = XCH_OFF + (ALT ? 6 * TC_BM * 4 : 0) + 1024;
 };
 
-// MODE chooses what the items and the masks are:
-// PS_CAUSAL: causal attention with a padding layout, shared prefix tiles, a window or a ring, as above.
-// PS_SINKS: a sliding window whose first `sinks` slots stay visible, each sequence at its own start
-// (len0p[b * len_stride]). A query tile walks the tiles of the sinks and those of its window, which the
-// skip between tiles ja and jb (padding otherwise) expresses. Rolling buffers keep sink_rows rows in front
-// of the ring.
-// PS_PREFIX: the query rows of a batch against a prefix that all its sequences share (T = its keys). A row tile
-// holds the G query heads of floor(128 / G) sequences for one kv head, an item is a chunk of the prefix for one
-// row tile, and the item leaves (output sums, maximum, sum) in recs instead of an output row. The row
-// tiles of one (kv head, chunk) are neighbours in the item order, so they run at the same time and share
-// the chunk's keys and values in L2.
-constexpr int PS_CAUSAL = 0, PS_SINKS = 1, PS_PREFIX = 2;
-struct PsExtra {
-    int sinks, sink_rows, len_stride, len_max;  // PS_SINKS
-    int row_tiles, chunks;                      // PS_PREFIX
-    float* recs;                                // PS_PREFIX: [B * Hq][chunks][DH + 4]
-};
-template <int DH, bool SPEC, bool ALT, int MODE>
+template <int DH, bool SPEC, bool ALT>
 __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
     attn_prefill_persistent_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                                    const __grid_constant__ CUtensorMap tmV, int T, int Hq, int Hkv, int B,
                                    const int* __restrict__ len0p, const int* __restrict__ meta, int window, int ring,
-                                   __nv_bfloat16* __restrict__ out, int* err, const PsExtra ex) {
+                                   __nv_bfloat16* __restrict__ out, int* err) {
     using Ly = PsLayout<DH, ALT>;
     constexpr int NCH = Ly::NCH;
-    constexpr bool SINKS = MODE == PS_SINKS, PREFIX = MODE == PS_PREFIX;
     constexpr uint32_t IDESC_S = idesc_bf16(TC_BM, TC_BN);
     constexpr uint32_t IDESC_O = idesc_bf16(TC_BM, DH, true);
     constexpr int NR = 3;                  // score regions in tensor memory
@@ -551,8 +533,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_qt = (T + TC_BM - 1) / TC_BM;
     const int per_qt = B * Hq;
-    const int group = Hq / Hkv, tile_seqs = TC_BM / group;  // PS_PREFIX: sequences of a row tile
-    const int n_items = PREFIX ? ex.row_tiles * Hkv * ex.chunks : n_qt * per_qt;
+    const int n_items = n_qt * per_qt;
     const int G = (int)gridDim.x, c = (int)blockIdx.x;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -592,7 +573,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
     bool ok = true;
     pdl_wait();  // Q and the cache come from the previous kernel
     pdl_trigger();
-    const int len0_all = SINKS || PREFIX ? 0 : *len0p;
+    const int len0 = *len0p;
     int ps_meta = 0, psh = 0;
     if (meta) {
         ps_meta = meta[0];
@@ -601,70 +582,28 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
 
     // The parameters of this CTA's round-th item (n_tiles = 0 when it has none left).
     struct Item {
-        int b, h, q0, q_end, n_valid, j_lo, ja, jb, n_tiles, ps, pe, len0, chunk;
+        int b, h, q0, q_end, n_valid, j_lo, ja, jb, n_tiles, ps, pe;
     };
     auto item_of = [&](int round) -> Item {
         Item it{};
         const int k = round * G + ((round & 1) ? G - 1 - c : c);
         if (k >= n_items) return it;
-        if constexpr (PREFIX) {
-            it.b = k % ex.row_tiles;  // row tile
-            it.h = k / ex.row_tiles % Hkv;
-            it.chunk = k / (ex.row_tiles * Hkv);
-            const long long tiles = (T + TC_BN - 1) / TC_BN;
-            it.j_lo = (int)(tiles * it.chunk / ex.chunks);
-            it.n_tiles = (int)(tiles * (it.chunk + 1) / ex.chunks) - it.j_lo;
-            return it;
-        }
         const int qt = n_qt - 1 - k / per_qt, rem = k % per_qt;
         it.b = rem / Hq;
         it.h = rem % Hq;
         it.q0 = qt * TC_BM;
         it.q_end = min(T, it.q0 + TC_BM);
-        it.len0 = SINKS ? min(max(0, len0p[(size_t)it.b * ex.len_stride]), ex.len_max) : len0_all;
-        const int len0 = it.len0;
         it.ps = ps_meta;
         it.pe = meta ? ps_meta + meta[kSeqMetaHead + it.b] : 0;
         it.n_valid = len0 + it.q_end;
         const int n_end = (it.n_valid + TC_BN - 1) / TC_BN;
-        if constexpr (SINKS) {
-            it.j_lo = 0;
-            it.jb = max(0, len0 + it.q0 - window + 1) / TC_BN;  // first tile of the window
-            it.ja = min((ex.sinks + TC_BN - 1) / TC_BN, it.jb);    // tiles of the sinks before it
-            it.n_tiles = n_end - (it.jb - it.ja);
-            return it;
-        }
         it.j_lo = window > 0 ? max(0, len0 + it.q0 - window + 1) / TC_BN : 0;
         it.ja = max(it.j_lo, (it.ps + TC_BN - 1) / TC_BN);
         it.jb = max(it.ja, min(it.pe / TC_BN, (len0 + it.q0) / TC_BN));
         it.n_tiles = n_end - it.j_lo - (it.jb - it.ja);
         return it;
     };
-    // cache row of slot tile j: a rolling buffer wraps, behind its sink rows
-    auto tile_row = [&](int j) -> int {
-        const int s = j * TC_BN;
-        if constexpr (SINKS) return ring > 0 && s >= ex.sink_rows ? ex.sink_rows + (s - ex.sink_rows) % ring : s;
-        if constexpr (PREFIX) return s;
-        return ring ? s % ring : s;
-    };
     auto tile_j = [](const Item& it, int i) { return it.j_lo + i < it.ja ? it.j_lo + i : it.j_lo + i + (it.jb - it.ja); };
-
-    // PS_PREFIX: whether row `row` of the item's tile is a query row, and its record
-    struct PrefixRow {
-        bool live;
-        float* rec;
-    };
-    auto prefix_row = [&](const Item& it, int row) -> PrefixRow {
-        if constexpr (!PREFIX) return PrefixRow{false, nullptr};
-        const int s = it.b * tile_seqs + row / group;  // sequence
-        const size_t r = (size_t)s * Hq + (size_t)it.h * group + row % group;
-        return PrefixRow{row < tile_seqs * group && s < B, ex.recs + (r * ex.chunks + it.chunk) * (DH + 4)};
-    };
-    auto store_rec32 = [](float* dst, const uint32_t (&o)[32]) {
-#pragma unroll
-        for (int v = 0; v < 8; ++v)
-            reinterpret_cast<uint4*>(dst)[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-    };
 
     constexpr int W_VTMA = ALT ? 2 : 6, W_PV = ALT ? 3 : 7;
     const bool producer = ALT ? warp < 4 : (warp < 2 || warp >= 6);
@@ -679,24 +618,16 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                 for (int round = 0; ok; ++round) {
                     const Item it = item_of(round);
                     if (it.n_tiles == 0) break;
-                    const int jkv = PREFIX ? it.h : it.h / (Hq / Hkv);
+                    const int jkv = it.h / (Hq / Hkv);
                     if (!mbar_wait_suspend(q_empty, (round & 1) ^ 1, abort_flag)) { ok = false; break; }
-                    if constexpr (PREFIX) {  // the rows behind the last whole group keep whatever they held
-                        mbar_expect_tx(q_full, NCH * tile_seqs * group * 128);
-                        for (int cc = 0; cc < NCH; ++cc)
-                            tma_load_4d(smem + Ly::Q_OFF + cc * TC_BM * 128, &tmQ, q_full, cc * 64, 0, it.h,
-                                        it.b * tile_seqs);
-                    } else {
-                        mbar_expect_tx(q_full, Ly::Q_BYTES);
-                        for (int cc = 0; cc < NCH; ++cc)
-                            tma_load_3d(smem + Ly::Q_OFF + cc * TC_BM * 128, &tmQ, q_full, cc * 64, it.q0,
-                                        it.b * Hq + it.h);
-                    }
+                    mbar_expect_tx(q_full, Ly::Q_BYTES);
+                    for (int cc = 0; cc < NCH; ++cc)
+                        tma_load_3d(smem + Ly::Q_OFF + cc * TC_BM * 128, &tmQ, q_full, cc * 64, it.q0, it.b * Hq + it.h);
                     for (int i = 0; i < it.n_tiles; ++i, ++g) {
                         const int s = g % PS_KST, j = tile_j(it, i);
                         const uint32_t free_ph = ((g / PS_KST) & 1) ^ 1;
-                        const int y = tile_row(j);
-                        const int z = PREFIX ? jkv : (j * TC_BN < psh ? 0 : it.b) * Hkv + jkv;
+                        const int y = ring ? (j * TC_BN) % ring : j * TC_BN;
+                        const int z = (j * TC_BN < psh ? 0 : it.b) * Hkv + jkv;
                         if (!mbar_wait_suspend(&k_empty[s], free_ph, abort_flag)) { ok = false; break; }
                         mbar_expect_tx(&k_full[s], Ly::KV_BYTES);
                         for (int cc = 0; cc < NCH; ++cc)
@@ -713,12 +644,12 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                 for (int round = 0; ok; ++round) {
                     const Item it = item_of(round);
                     if (it.n_tiles == 0) break;
-                    const int jkv = PREFIX ? it.h : it.h / (Hq / Hkv);
+                    const int jkv = it.h / (Hq / Hkv);
                     for (int i = 0; i < it.n_tiles; ++i, ++g) {
                         const int s = g & 1, j = tile_j(it, i);
                         const uint32_t free_ph = ((g >> 1) & 1) ^ 1;
-                        const int y = tile_row(j);
-                        const int z = PREFIX ? jkv : (j * TC_BN < psh ? 0 : it.b) * Hkv + jkv;
+                        const int y = ring ? (j * TC_BN) % ring : j * TC_BN;
+                        const int z = (j * TC_BN < psh ? 0 : it.b) * Hkv + jkv;
                         if (!mbar_wait_suspend(&v_empty[s], free_ph, abort_flag)) { ok = false; break; }
                         mbar_expect_tx(&v_full[s], Ly::KV_BYTES);
                         for (int cc = 0; cc < NCH; ++cc)
@@ -776,30 +707,14 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     const int j = tile_j(it, i);
                     if (!__all_sync(0xffffffffu, mbar_wait_suspend(&v_full[s], (gi >> 1) & 1, abort_flag))) { ok = false; break; }
                     uint8_t* sv = smem + Ly::V_OFF + s * Ly::KV_BYTES;
-                    if constexpr (SINKS) {
-                        // value rows between the sinks and the first row's window, which no row sees: a
-                        // hidden row may hold anything, and 0 * NaN must not reach O
-                        const int z0 = max(0, ex.sinks - j * TC_BN);
-                        const int z1 = min(TC_BN, it.len0 + it.q0 - window + 1 - j * TC_BN);
-                        if (z0 < z1) {
-                            for (int e = lane; e < (z1 - z0) * 8 * NCH; e += 32) {
-                                const int cc = e / ((z1 - z0) * 8), rem = e % ((z1 - z0) * 8);
-                                reinterpret_cast<uint4*>(sv + cc * TC_BN * 128 + (z0 + rem / 8) * 128)[rem % 8] =
-                                    make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
+                    const int r0 = it.n_valid - j * TC_BN;  // first stale key row of this tile
+                    if (r0 < TC_BN) {
+                        for (int e = lane; e < (TC_BN - r0) * 8 * NCH; e += 32) {
+                            const int cc = e / ((TC_BN - r0) * 8), rem = e % ((TC_BN - r0) * 8);
+                            reinterpret_cast<uint4*>(sv + cc * TC_BN * 128 + (r0 + rem / 8) * 128)[rem % 8] =
+                                make_uint4(0, 0, 0, 0);
                         }
-                    }
-                    if constexpr (!PREFIX) {  // (TMA reads zeros behind a prefix)
-                        const int r0 = it.n_valid - j * TC_BN;  // first stale key row of this tile
-                        if (r0 < TC_BN) {
-                            for (int e = lane; e < (TC_BN - r0) * 8 * NCH; e += 32) {
-                                const int cc = e / ((TC_BN - r0) * 8), rem = e % ((TC_BN - r0) * 8);
-                                reinterpret_cast<uint4*>(sv + cc * TC_BN * 128 + (r0 + rem / 8) * 128)[rem % 8] =
-                                    make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                        }
+                        fence_proxy_async_smem();
                     }
                     __syncwarp();
                     if (lane == 0) {
@@ -849,7 +764,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             const Item it = item_of(round);
             const int nt = it.n_tiles;
             if (nt == 0) break;
-            const int t = it.q0 + row, pos = it.len0 + t;
+            const int t = it.q0 + row, pos = len0 + t;
             volatile float* m_row = m_sh + (round & 1) * TC_BM + row;
             float m_l = -INFINITY, l = 0.f;  // this warpgroup's share of the row sum, at scale m_l
             for (int i = ((g & 1) == wg) ? 0 : 1; i < nt; i += 2) {
@@ -864,52 +779,25 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     tmem_ld_32x32b_x32(tm_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
                 tmem_ld_wait();
                 const int k0 = j * TC_BN;
-                if constexpr (PREFIX) {
-                    const int left = T - k0;  // keys of this tile
-                    if (left < TC_BN) {
+                const bool diag = k0 + TC_BN - 1 > len0 + it.q0;
+                const bool pads = k0 < it.pe && k0 + TC_BN > it.ps;
+                const bool old = window > 0 && k0 < len0 + it.q_end - window;
+                if (pads || old) {
+                    // visible: (i <= lim, not padding, inside the window) or the query itself; branch-free
+                    const int lim = pos - k0;
+                    const int lo = window > 0 ? lim - window + 1 : -TC_BN;
+                    const int a1 = max(lo, 0), n1 = max(0, min(lim, it.ps - k0 - 1) - a1 + 1);
+                    const int a2 = max(lo, it.pe - k0), n2 = max(0, lim - a2 + 1);
 #pragma unroll
-                        for (int e = 0; e < TC_BN; ++e) sr[e] = e < left ? sr[e] : __float_as_uint(-INFINITY);
+                    for (int e = 0; e < TC_BN; ++e) {
+                        const bool vis =
+                            ((unsigned)(e - a1) < (unsigned)n1) | ((unsigned)(e - a2) < (unsigned)n2) | (e == lim);
+                        sr[e] = vis ? sr[e] : __float_as_uint(-INFINITY);
                     }
-                } else {
-                    const bool diag = k0 + TC_BN - 1 > it.len0 + it.q0;
-                    const bool pads = !SINKS && k0 < it.pe && k0 + TC_BN > it.ps;
-                    bool old = window > 0 && k0 < it.len0 + it.q_end - window;
-                    if constexpr (SINKS) {
-                        if (k0 + TC_BN <= it.len0 + it.q0 - window + 1) {  // below every row's window: sinks only
-                            old = false;
-                            const int left = ex.sinks - k0;
-                            if (left < TC_BN) {
+                } else if (diag) {
+                    const int lim = pos - k0;
 #pragma unroll
-                                for (int e = 0; e < TC_BN; ++e) sr[e] = e < left ? sr[e] : __float_as_uint(-INFINITY);
-                            }
-                        } else if (old && k0 >= ex.sinks && !diag) {  // only the window's lower edge
-                            old = false;
-                            const int lo = pos - k0 - window + 1;
-#pragma unroll
-                            for (int e = 0; e < TC_BN; ++e) sr[e] = e >= lo ? sr[e] : __float_as_uint(-INFINITY);
-                        }
-                        old = old && k0 + TC_BN > ex.sinks;
-                    }
-                    if (pads || old) {
-                        // visible: (i <= lim, not padding, inside the window) or the query itself; branch-free.
-                        // SINKS: the sinks and the window take the places of the intervals around the padding.
-                        const int lim = pos - k0;
-                        const int lo = window > 0 ? lim - window + 1 : -TC_BN;
-                        const int a1 = SINKS ? 0 : max(lo, 0);
-                        const int n1 = SINKS ? max(0, min(lim + 1, ex.sinks - k0))
-                                             : max(0, min(lim, it.ps - k0 - 1) - a1 + 1);
-                        const int a2 = SINKS ? max(lo, 0) : max(lo, it.pe - k0), n2 = max(0, lim - a2 + 1);
-#pragma unroll
-                        for (int e = 0; e < TC_BN; ++e) {
-                            const bool vis =
-                                ((unsigned)(e - a1) < (unsigned)n1) | ((unsigned)(e - a2) < (unsigned)n2) | (e == lim);
-                            sr[e] = vis ? sr[e] : __float_as_uint(-INFINITY);
-                        }
-                    } else if (diag) {
-                        const int lim = pos - k0;
-#pragma unroll
-                        for (int e = 0; e < TC_BN; ++e) sr[e] = e <= lim ? sr[e] : __float_as_uint(-INFINITY);
-                    }
+                    for (int e = 0; e < TC_BN; ++e) sr[e] = e <= lim ? sr[e] : __float_as_uint(-INFINITY);
                 }
                 // P = 2^(s * sl2 - m) as packed bf16 into the first 64 columns of this tile's region (a row
                 // with no visible key yet keeps m = -inf and gets P = 0); rs2 = their row sum
@@ -1016,17 +904,14 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             if (!ok) break;
             // O / l to the output, this warpgroup's half of the columns, then hand the accumulator back
             tc_fence_after();
-            const float l_all = l_row[0] + l_row[TC_BM], inv = 1.f / l_all;
+            const float inv = 1.f / (l_row[0] + l_row[TC_BM]);
             __nv_bfloat16* orow = out + (((size_t)it.b * T + t) * Hq + it.h) * DH + wg * (DH / 2);
-            const PrefixRow pr = prefix_row(it, row);
 #pragma unroll 1
             for (int cc = 0; cc < DH / 64; ++cc) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(tm_o + wg * (DH / 2) + cc * 32, o);
                 tmem_ld_wait();
-                if constexpr (PREFIX) {
-                    if (pr.live) store_rec32(pr.rec + wg * (DH / 2) + cc * 32, o);
-                } else if (t < T) {
+                if (t < T) {
                     uint32_t wv[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -1037,7 +922,6 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                             make_uint4(wv[4 * v], wv[4 * v + 1], wv[4 * v + 2], wv[4 * v + 3]);
                 }
             }
-            if (PREFIX && wg == 0 && pr.live) *reinterpret_cast<float4*>(pr.rec + DH) = make_float4(m_fin, l_all, 0.f, 0.f);
             tc_fence_before();
             mbar_arrive(o_free);
             g += nt;
@@ -1057,7 +941,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             const Item it = item_of(round);
             const int nt = it.n_tiles;
             if (nt == 0) break;
-            const int t = it.q0 + row, pos = it.len0 + t;
+            const int t = it.q0 + row, pos = len0 + t;
             float m_used = -INFINITY, l = 0.f;
             for (int i = 0; i < nt; ++i) {
                 const int gi = g + i, r = gi % NR;
@@ -1071,52 +955,25 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     tmem_ld_32x32b_x32(tm_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
                 tmem_ld_wait();
                 const int k0 = j * TC_BN;
-                if constexpr (PREFIX) {
-                    const int left = T - k0;  // keys of this tile
-                    if (left < TC_BN) {
+                const bool diag = k0 + TC_BN - 1 > len0 + it.q0;
+                const bool pads = k0 < it.pe && k0 + TC_BN > it.ps;
+                const bool old = window > 0 && k0 < len0 + it.q_end - window;
+                if (pads || old) {
+                    // visible: (i <= lim, not padding, inside the window) or the query itself; branch-free
+                    const int lim = pos - k0;
+                    const int lo = window > 0 ? lim - window + 1 : -TC_BN;
+                    const int a1 = max(lo, 0), n1 = max(0, min(lim, it.ps - k0 - 1) - a1 + 1);
+                    const int a2 = max(lo, it.pe - k0), n2 = max(0, lim - a2 + 1);
 #pragma unroll
-                        for (int e = 0; e < TC_BN; ++e) sr[e] = e < left ? sr[e] : __float_as_uint(-INFINITY);
+                    for (int e = 0; e < TC_BN; ++e) {
+                        const bool vis =
+                            ((unsigned)(e - a1) < (unsigned)n1) | ((unsigned)(e - a2) < (unsigned)n2) | (e == lim);
+                        sr[e] = vis ? sr[e] : __float_as_uint(-INFINITY);
                     }
-                } else {
-                    const bool diag = k0 + TC_BN - 1 > it.len0 + it.q0;
-                    const bool pads = !SINKS && k0 < it.pe && k0 + TC_BN > it.ps;
-                    bool old = window > 0 && k0 < it.len0 + it.q_end - window;
-                    if constexpr (SINKS) {
-                        if (k0 + TC_BN <= it.len0 + it.q0 - window + 1) {  // below every row's window: sinks only
-                            old = false;
-                            const int left = ex.sinks - k0;
-                            if (left < TC_BN) {
+                } else if (diag) {
+                    const int lim = pos - k0;
 #pragma unroll
-                                for (int e = 0; e < TC_BN; ++e) sr[e] = e < left ? sr[e] : __float_as_uint(-INFINITY);
-                            }
-                        } else if (old && k0 >= ex.sinks && !diag) {  // only the window's lower edge
-                            old = false;
-                            const int lo = pos - k0 - window + 1;
-#pragma unroll
-                            for (int e = 0; e < TC_BN; ++e) sr[e] = e >= lo ? sr[e] : __float_as_uint(-INFINITY);
-                        }
-                        old = old && k0 + TC_BN > ex.sinks;
-                    }
-                    if (pads || old) {
-                        // visible: (i <= lim, not padding, inside the window) or the query itself; branch-free.
-                        // SINKS: the sinks and the window take the places of the intervals around the padding.
-                        const int lim = pos - k0;
-                        const int lo = window > 0 ? lim - window + 1 : -TC_BN;
-                        const int a1 = SINKS ? 0 : max(lo, 0);
-                        const int n1 = SINKS ? max(0, min(lim + 1, ex.sinks - k0))
-                                             : max(0, min(lim, it.ps - k0 - 1) - a1 + 1);
-                        const int a2 = SINKS ? max(lo, 0) : max(lo, it.pe - k0), n2 = max(0, lim - a2 + 1);
-#pragma unroll
-                        for (int e = 0; e < TC_BN; ++e) {
-                            const bool vis =
-                                ((unsigned)(e - a1) < (unsigned)n1) | ((unsigned)(e - a2) < (unsigned)n2) | (e == lim);
-                            sr[e] = vis ? sr[e] : __float_as_uint(-INFINITY);
-                        }
-                    } else if (diag) {
-                        const int lim = pos - k0;
-#pragma unroll
-                        for (int e = 0; e < TC_BN; ++e) sr[e] = e <= lim ? sr[e] : __float_as_uint(-INFINITY);
-                    }
+                    for (int e = 0; e < TC_BN; ++e) sr[e] = e <= lim ? sr[e] : __float_as_uint(-INFINITY);
                 }
                 // P = 2^(s * sl2 - m) as packed bf16 into the first 64 columns of this tile's region (a row
                 // with no visible key yet keeps m = -inf and gets P = 0); rs2 = their row sum
@@ -1206,15 +1063,12 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             tc_fence_after();
             __nv_bfloat16* orow = out + (((size_t)it.b * T + t) * Hq + it.h) * DH;
             const float inv = 1.f / l;
-            const PrefixRow pr = prefix_row(it, row);
 #pragma unroll 1
             for (int cc = 0; cc < DH / 32; ++cc) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(tm_o + cc * 32, o);
                 tmem_ld_wait();
-                if constexpr (PREFIX) {
-                    if (pr.live) store_rec32(pr.rec + cc * 32, o);
-                } else if (t < T) {
+                if (t < T) {
                     uint32_t wv[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -1225,7 +1079,6 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                             make_uint4(wv[4 * v], wv[4 * v + 1], wv[4 * v + 2], wv[4 * v + 3]);
                 }
             }
-            if (PREFIX && pr.live) *reinterpret_cast<float4*>(pr.rec + DH) = make_float4(m_used, l, 0.f, 0.f);
             tc_fence_before();
             mbar_arrive(o_free);
             g += nt;
@@ -1691,47 +1544,18 @@ constexpr int kSpecMinKeys = 4096;
 // Key range from which the persistent kernel alternates tiles between two softmax warpgroups (ALT).
 constexpr int kAltMinKeys = 8192;
 
-// The same thresholds where every item has about the same number of keys.
-constexpr int kSpecItemKeys = 2048, kAltItemKeys = 4096;
-inline int item_keys(int v, const char* name) { const char* e = getenv(name); return e ? atoi(e) : v; }
-
 // setmaxnreg.inc waits until the registers it asks for are free, so the ALT form runs only when the
 // compiled kernel was given at least the registers per thread its split hands out (checked once).
-template <int DH, int MODE>
+template <int DH>
 bool alt_registers_cover_split() {
     static const bool ok = [] {
         cudaFuncAttributes fa{};
-        if (cudaFuncGetAttributes(&fa, attn_prefill_persistent_kernel<DH, true, true, MODE>) != cudaSuccess) return false;
+        if (cudaFuncGetAttributes(&fa, attn_prefill_persistent_kernel<DH, true, true>) != cudaSuccess) return false;
         const long long have = (long long)ps_threads<true>() * fa.numRegs;
         const long long need = 128LL * PS_REG_PRODUCER + 256LL * PS_REG_SOFTMAX;
         return have >= need;
     }();
     return ok;
-}
-
-// Row tiles of a batch's query rows for one kv head.
-int prefix_row_tiles(int B, int G) {
-    const int seqs = TC_BM / G;
-    return (B + seqs - 1) / seqs;
-}
-
-// The persistent kernel over `items` work items.
-template <int DH, int MODE>
-cudaError_t persistent_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, long long items, int B,
-                              int T, int Hq, int Hkv, const int* len0, SeqMap sm, __nv_bfloat16* out, int* err,
-                              bool alt, bool spec, const PsExtra& ex, cudaStream_t st) {
-    const unsigned grid = (unsigned)std::min<long long>(items, device_sm_count());
-    if (alt && alt_registers_cover_split<DH, MODE>())
-        return launch_pdl(attn_prefill_persistent_kernel<DH, true, true, MODE>, dim3(grid), dim3(ps_threads<true>()),
-                          PsLayout<DH, true>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out,
-                          err, ex);
-    if (spec)
-        return launch_pdl(attn_prefill_persistent_kernel<DH, true, false, MODE>, dim3(grid), dim3(ps_threads<false>()),
-                          PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out,
-                          err, ex);
-    return launch_pdl(attn_prefill_persistent_kernel<DH, false, false, MODE>, dim3(grid), dim3(ps_threads<false>()),
-                      PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out,
-                      err, ex);
 }
 
 template <int DH>
@@ -1757,47 +1581,15 @@ cudaError_t prefill_launch_dh(const __nv_bfloat16* q, const __nv_bfloat16* kc, c
     if (split > 0)
         return prefill_launch_nh<DH, 1>(tq, tk, tv, B, T, Hq, Hkv, len0, sm, out, err, split, max_chunks, ws, st);
     const long long items = (long long)((T + TC_BM - 1) / TC_BM) * Hq * B;
-    return persistent_launch<DH, PS_CAUSAL>(tq, tk, tv, items, B, T, Hq, Hkv, len0, sm, out, err, kv_hint >= kAltMinKeys,
-                                            kv_hint >= kSpecMinKeys, PsExtra{}, st);
-}
-
-template <int DH>
-cudaError_t prefill_sinks_launch_dh(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B, int T,
-                                    int Hq, int Hkv, int cap, const int* len0, int len_stride, SinkMap sm,
-                                    __nv_bfloat16* out, int* err, cudaStream_t st) {
-    CUtensorMap tq, tk, tv;
-    if (!encode_tmap_bf16_3d(&tq, q, DH, T, (uint64_t)B * Hq) || !encode_tmap_bf16_3d(&tk, kc, DH, cap, (uint64_t)B * Hkv) ||
-        !encode_tmap_bf16_3d(&tv, vc, DH, cap, (uint64_t)B * Hkv))
-        return cudaErrorInvalidValue;
-    PsExtra ex{};
-    ex.sinks = sm.sinks;
-    ex.sink_rows = sm.sink_rows;
-    ex.len_stride = len_stride;
-    // largest start: the call's tokens end inside a full cache; a rolling buffer only bounds the slot arithmetic
-    ex.len_max = sm.ring > 0 ? 1 << 30 : std::max(0, cap - T);
-    const long long items = (long long)((T + TC_BM - 1) / TC_BM) * Hq * B;
-    // keys of one query tile: the sinks, the window and the tile's own slots
-    const long long keys = std::min<long long>((long long)sm.window + sm.sinks + TC_BM, cap);
-    return persistent_launch<DH, PS_SINKS>(tq, tk, tv, items, B, T, Hq, Hkv, len0, SeqMap{nullptr, sm.window, sm.ring},
-                                           out, err, keys >= item_keys(kAltItemKeys, "Q3_ALT"), keys >= item_keys(kSpecItemKeys, "Q3_SPEC"), ex, st);
-}
-
-template <int DH>
-cudaError_t prefix_launch_dh(const __nv_bfloat16* q, const __nv_bfloat16* kp, const __nv_bfloat16* vp, int B, int Hq, int Hkv,
-                             int prefix_cap, int P, float* recs, int* err, cudaStream_t st) {
-    const int G = Hq / Hkv;
-    CUtensorMap tq, tk, tv;
-    if (!encode_tmap_bf16_groups(&tq, q, DH, G, Hkv, B, TC_BM / G) ||
-        !encode_tmap_bf16_rows(&tk, kp, DH, P, prefix_cap, Hkv, TC_BN) ||
-        !encode_tmap_bf16_rows(&tv, vp, DH, P, prefix_cap, Hkv, TC_BN))
-        return cudaErrorInvalidValue;
-    PsExtra ex{};
-    ex.row_tiles = prefix_row_tiles(B, G);
-    ex.chunks = attn_prefix_chunks(B, Hq, Hkv, P);
-    ex.recs = recs;
-    const int keys = ((P + TC_BN - 1) / TC_BN + ex.chunks - 1) / ex.chunks * TC_BN;
-    return persistent_launch<DH, PS_PREFIX>(tq, tk, tv, (long long)ex.row_tiles * Hkv * ex.chunks, B, P, Hq, Hkv, nullptr,
-                                            SeqMap{}, nullptr, err, keys >= item_keys(kAltItemKeys, "Q3_ALT"), keys >= item_keys(kSpecItemKeys, "Q3_SPEC"), ex, st);
+    const unsigned grid = (unsigned)std::min<long long>(items, device_sm_count());
+    if (kv_hint >= kAltMinKeys && alt_registers_cover_split<DH>())
+        return launch_pdl(attn_prefill_persistent_kernel<DH, true, true>, dim3(grid), dim3(ps_threads<true>()),
+                          PsLayout<DH, true>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err);
+    if (kv_hint >= kSpecMinKeys)
+        return launch_pdl(attn_prefill_persistent_kernel<DH, true, false>, dim3(grid), dim3(ps_threads<false>()),
+                          PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err);
+    return launch_pdl(attn_prefill_persistent_kernel<DH, false, false>, dim3(grid), dim3(ps_threads<false>()),
+                      PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err);
 }
 
 }  // namespace
@@ -1818,42 +1610,6 @@ cudaError_t attn_prefill_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc,
     if (dh == 64)
         return prefill_launch_dh<64>(q, kc, vc, B, T, Hq, Hkv, cap, len0, sm, out, err, split, max_chunks, ws, heads,
                                      kv_hint, st);
-    return cudaErrorInvalidValue;
-}
-
-cudaError_t attn_prefill_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B,
-                                      int T, int Hq, int Hkv, int dh, int cap, const int* len0, int len_stride,
-                                      SinkMap sm, __nv_bfloat16* out, int* err, cudaStream_t st) {
-    if (B <= 0 || T <= 0) return cudaSuccess;
-    if (dh == 128)
-        return prefill_sinks_launch_dh<128>(q, kc, vc, B, T, Hq, Hkv, cap, len0, len_stride, sm, out, err, st);
-    if (dh == 64) return prefill_sinks_launch_dh<64>(q, kc, vc, B, T, Hq, Hkv, cap, len0, len_stride, sm, out, err, st);
-    return cudaErrorInvalidValue;
-}
-
-// Chunks of the prefix: as few as give the busiest SM the least work, counting two key tiles' time for an
-// item's start and end, over one to four rounds of items.
-int attn_prefix_chunks(int B, int Hq, int Hkv, int P) {
-    const long long tiles = (P + TC_BN - 1) / TC_BN, rows = (long long)prefix_row_tiles(B, Hq / Hkv) * Hkv;
-    const int sms = device_sm_count();
-    long long best = -1;
-    int chunks = 1;
-    for (int rounds = 1; rounds <= 4; ++rounds) {
-        const long long c = std::max<long long>(1, std::min<long long>(std::min<long long>(tiles, kPrefixMaxChunks),
-                                                                      (long long)rounds * sms / rows));
-        const long long cost = (rows * c + sms - 1) / sms * ((tiles + c - 1) / c + 2);
-        if (best < 0 || cost < best) {
-            best = cost;
-            chunks = (int)c;
-        }
-    }
-    return chunks;
-}
-
-cudaError_t attn_prefix_launch(const __nv_bfloat16* q, const __nv_bfloat16* kp, const __nv_bfloat16* vp, int B, int Hq,
-                               int Hkv, int dh, int prefix_cap, int P, float* recs, int* err, cudaStream_t st) {
-    if (dh == 128) return prefix_launch_dh<128>(q, kp, vp, B, Hq, Hkv, prefix_cap, P, recs, err, st);
-    if (dh == 64) return prefix_launch_dh<64>(q, kp, vp, B, Hq, Hkv, prefix_cap, P, recs, err, st);
     return cudaErrorInvalidValue;
 }
 
@@ -1924,32 +1680,20 @@ cudaError_t decode_prepare_dh() {
     return e;
 }
 
-template <int DH, int MODE>
-cudaError_t persistent_prepare() {
-    const void* fns[] = {(const void*)attn_prefill_persistent_kernel<DH, false, false, MODE>,
-                         (const void*)attn_prefill_persistent_kernel<DH, true, false, MODE>,
-                         (const void*)attn_prefill_persistent_kernel<DH, true, true, MODE>};
-    const int smem[] = {PsLayout<DH, false>::SMEM, PsLayout<DH, false>::SMEM, PsLayout<DH, true>::SMEM};
-    for (int i = 0; i < 3; ++i) {
-        cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, smem[i]);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
-}
-
 cudaError_t attention_prepare() {
     const void* fns[] = {(const void*)attn_prefill_tc_kernel<128, 1>, (const void*)attn_prefill_tc_kernel<128, 2>,
-                         (const void*)attn_prefill_tc_kernel<64, 1>,  (const void*)attn_prefill_tc_kernel<64, 2>};
-    const int smem[] = {TcLayout<128, 1>::SMEM, TcLayout<128, 2>::SMEM, TcLayout<64, 1>::SMEM, TcLayout<64, 2>::SMEM};
-    for (int i = 0; i < 4; ++i) {
+                         (const void*)attn_prefill_tc_kernel<64, 1>,  (const void*)attn_prefill_tc_kernel<64, 2>,
+                         (const void*)attn_prefill_persistent_kernel<128, false, false>,
+                         (const void*)attn_prefill_persistent_kernel<64, false, false>,
+                         (const void*)attn_prefill_persistent_kernel<128, true, false>,
+                         (const void*)attn_prefill_persistent_kernel<64, true, false>,
+                         (const void*)attn_prefill_persistent_kernel<128, true, true>,
+                         (const void*)attn_prefill_persistent_kernel<64, true, true>};
+    const int smem[] = {TcLayout<128, 1>::SMEM, TcLayout<128, 2>::SMEM, TcLayout<64, 1>::SMEM, TcLayout<64, 2>::SMEM,
+                        PsLayout<128, false>::SMEM, PsLayout<64, false>::SMEM, PsLayout<128, false>::SMEM,
+                        PsLayout<64, false>::SMEM, PsLayout<128, true>::SMEM,  PsLayout<64, true>::SMEM};
+    for (int i = 0; i < 10; ++i) {
         cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, smem[i]);
-        if (e != cudaSuccess) return e;
-    }
-    cudaError_t (*const persistent[])() = {persistent_prepare<128, PS_CAUSAL>, persistent_prepare<64, PS_CAUSAL>,
-                                           persistent_prepare<128, PS_SINKS>,  persistent_prepare<64, PS_SINKS>,
-                                           persistent_prepare<128, PS_PREFIX>, persistent_prepare<64, PS_PREFIX>};
-    for (auto prepare : persistent) {
-        cudaError_t e = prepare();
         if (e != cudaSuccess) return e;
     }
     cudaError_t e = decode_prepare_dh<128>();

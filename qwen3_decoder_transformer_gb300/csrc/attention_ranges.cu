@@ -20,26 +20,30 @@ namespace {
 // behind a padding block), taken in units of 16 keys.
 //
 // Every warp works through its own units alone, with a running maximum (lazily rescaled, as in the prefill
-// kernels): its lane 0 keeps a ring of RG_BYTES full with the K and V boxes of the coming units (TMA, 128-byte
-// swizzle), so 24 KB a warp and 192 KB an SM are on their way or in use, four times what HBM latency x
-// bandwidth needs, and no barrier joins the warps before the end. The products are warp-level mma (m16n8k16,
+// kernels): its lane 0 keeps a ring full with the K and V boxes of the coming units (TMA, 128-byte
+// swizzle), so up to 192 KB an SM are on their way or in use, four times what HBM latency x bandwidth
+// needs, and no barrier joins the warps before the end. The products are warp-level mma (m16n8k16,
 // bf16 in, fp32 accumulate; the contraction is far below a tcgen05 tile) with the heads of the kv group as
 // the 8 columns: S^T (keys x heads) = K q^T, P^T from accumulator to operand layout by a register transpose
 // (movmatrix), O^T (head_dim x heads) += V^T P^T.
 // Scores of rows behind a run are masked, and their value rows are zeroed in shared memory, so nothing
 // stored in a hidden row can reach the result.
 constexpr int RG_KEYS = 16, RG_MAX_CLUSTER = 16, RG_MAX_G = 8, RG_WARPS = 4, RG_THREADS = 32 * RG_WARPS;
-constexpr int RG_BYTES = 24576;  // ring of one warp
-template <int DH>
+constexpr int RG_MAX_PARTS = RG_MAX_CLUSTER + kPrefixMaxChunks;
+template <int DH, int RING>
 struct RgLayout {
     static constexpr int NCH = DH / 64;               // 64-column boxes of a row
     static constexpr int BOX = RG_KEYS * 128;         // bytes of a box
     static constexpr int HALF = NCH * BOX;            // K (or V) of a unit
-    static constexpr int ST = RG_BYTES / (2 * HALF);  // units in the ring: 3 (dh 128) or 6 (dh 64)
+    static constexpr int RG_BYTES = RING * 8192;      // ring of one warp
+    static constexpr int ST = RG_BYTES / (2 * HALF);  // units in it: RING (dh 128) or 2 RING (dh 64)
     static constexpr int SMEM = RG_WARPS * RG_BYTES + 1024;
+    static constexpr int CTAS = RING == 3 ? 2 : RING == 2 ? 3 : 4;  // an SM
+    // the warps' results take the first bytes of the rings once all of them are done
+    static constexpr int PITCH = DH + 4;
+    static_assert(RG_WARPS * RG_MAX_G * PITCH * 4 <= RG_WARPS * RG_BYTES, "results fit the rings");
+    static_assert(CTAS * (SMEM + 8192) <= 227 * 1024, "shared memory");
 };
-// two CTAs an SM; the warps' results take the first 16 KB of the rings once all of them are done
-static_assert(2 * (RG_WARPS * RG_BYTES + 1024 + 8192) <= 227 * 1024, "shared memory");
 
 struct RangeArgs {
     const __nv_bfloat16* q;
@@ -50,8 +54,9 @@ struct RangeArgs {
     // window and sinks; ring > 0: rows [0, sink_rows) keep the first slots, the others wrap over ring rows
     int window, sinks, sink_rows, ring;
     const int* meta;    // own slots of a shared prefix: SeqMap::meta, or null
-    const float* recs;  // [B * Hq][nrec][DH + 4] partial results to join (output sums, maximum, sum)
-    int nrec;
+    const float* recs;  // records of the prefix to join (attn_prefix_launch)
+    int nrec, row_tiles;
+    float* own;  // [B][Hkv][G][DH + 4]: where the own keys' (output sums, maximum, sum) go, to be joined by a launch of its own; or null
     int C;  // CTAs per (sequence, kv head)
     int* err;
 };
@@ -92,20 +97,96 @@ __device__ __forceinline__ uint32_t rg_addr(uint32_t base, int row, int piece) {
     return base + (uint32_t)((piece >> 3) * RG_KEYS * 128 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
-template <int DH, bool SINKS>
-__global__ void __launch_bounds__(RG_THREADS, 2)
+// Four output dims dd.. of head h of the group, times scale.
+template <int DH>
+__device__ __forceinline__ void store_quad(const RangeArgs& a, int b, int j, int h, int dd, const float4& v, float scale) {
+    const size_t row = (size_t)b * a.Hq + (size_t)j * a.G + h;
+    *reinterpret_cast<uint2*>(a.out + row * DH + dd) =
+        make_uint2(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale));
+}
+
+// Join `n_own` parts of the own keys (statistics own_stat(p, h) = (maximum, sum), output sums own_quad(p, h, dd)) and
+// the prefix records by log-sum-exp: O = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i. The CTA finishes the quads
+// of four dims whose number has its rank modulo a.C (in steps of its threads).
+template <int DH, typename Stat, typename Quad>
+__device__ __forceinline__ void join_parts(const RangeArgs& a, int b, int j, int n_own, int rank,
+                                           float (&pm)[RG_MAX_G][RG_MAX_PARTS], float (&pl)[RG_MAX_G][RG_MAX_PARTS],
+                                           float (&inv)[RG_MAX_G], Stat own_stat, Quad own_quad) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int quads = a.G * (DH / 4), parts = n_own + a.nrec;
+    // this sequence's rows in its row tile, and the distance between the records of two chunks
+    const int seqs = kPrefixRows / a.G, row0 = b % seqs * a.G;
+    const float* rec0 = a.recs + ((size_t)j * a.row_tiles + b / seqs) * prefix_rec_floats(DH);
+    const size_t rec_step = (size_t)a.Hkv * a.row_tiles * prefix_rec_floats(DH);
+    auto rec_quad = [&](int r, int h, int dd) {
+        return __ldcg(reinterpret_cast<const float4*>(rec0 + r * rec_step + ((size_t)(dd / 4) * kPrefixRows + row0 + h) * 4));
+    };
+    // the output sums of the first records are on their way while the weights are worked out
+    constexpr int PRE = 8;
+    float4 pre[PRE];
+    const int e0 = threadIdx.x + RG_THREADS * rank;
+#pragma unroll
+    for (int r = 0; r < PRE; ++r)
+        if (r < a.nrec && e0 < quads) pre[r] = rec_quad(r, e0 % a.G, e0 / a.G * 4);
+    for (int e = threadIdx.x; e < parts * RG_MAX_G; e += RG_THREADS) {
+        const int p = e / RG_MAX_G, h = e % RG_MAX_G;
+        if (h < a.G) {
+            const float2 ml = p < n_own ? own_stat(p, h)
+                                        : __ldcg(reinterpret_cast<const float2*>(rec0 + (p - n_own) * rec_step +
+                                                                                 (size_t)DH * kPrefixRows + (row0 + h) * 2));
+            pm[h][p] = ml.x;
+            pl[h][p] = ml.y;
+        }
+    }
+    __syncthreads();
+    for (int h = warp; h < a.G; h += RG_WARPS) {  // the parts' weights, into pm
+        float M = -INFINITY, L = 0.f;
+        for (int p = lane; p < parts; p += 32) M = fmaxf(M, pm[h][p]);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+        for (int p = lane; p < parts; p += 32) {
+            const float f = pm[h][p] == -INFINITY ? 0.f : ex2_approx(pm[h][p] - M);
+            L = fmaf(pl[h][p], f, L);
+            pm[h][p] = f;
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+        if (lane == 0) inv[h] = L == 0.f ? 0.f : 1.f / L;
+    }
+    __syncthreads();
+    for (int e = e0; e < quads; e += RG_THREADS * a.C) {
+        const int h = e % a.G, dd = e / a.G * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](const float4& x, float f) {
+            v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
+        };
+#pragma unroll 4
+        for (int p = 0; p < n_own; ++p) add(own_quad(p, h, dd), pm[h][p]);
+        int r = 0;
+        if (e == e0) {
+#pragma unroll
+            for (; r < PRE; ++r)
+                if (r < a.nrec) add(pre[r], pm[h][n_own + r]);
+        }
+#pragma unroll 4
+        for (; r < a.nrec; ++r) add(rec_quad(r, h, dd), pm[h][n_own + r]);
+        store_quad<DH>(a, b, j, h, dd, v, inv[h]);
+    }
+}
+
+template <int DH, bool SINKS, int RING>
+__global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
     attn_ranges_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const RangeArgs a) {
-    using Ly = RgLayout<DH>;
-    constexpr int NW = RG_WARPS, THREADS = RG_THREADS, ST = Ly::ST;
-    constexpr int MAX_PARTS = RG_MAX_CLUSTER + kPrefixMaxChunks;
+    using Ly = RgLayout<DH, RING>;
+    constexpr int NW = RG_WARPS, THREADS = RG_THREADS, ST = Ly::ST, RG_BYTES = Ly::RG_BYTES;
     extern __shared__ uint8_t rg_raw[];
     const uint32_t raw_addr = smem_u32(rg_raw);
     uint8_t* rings = rg_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    auto so = reinterpret_cast<float(*)[RG_MAX_G][DH]>(rings);  // the warps' output sums, once the rings are done
+    auto so = reinterpret_cast<float(*)[RG_MAX_G][Ly::PITCH]>(rings);  // the warps' output sums, once the rings are done
     __shared__ uint64_t bars[RG_WARPS][2 * ST];                 // [K of each stage, V of each stage]
     __shared__ float sm[NW][RG_MAX_G], sl[NW][RG_MAX_G];
     __shared__ float cm[RG_MAX_G], cl[RG_MAX_G];                   // this CTA's maximum and sum
-    __shared__ float pm[RG_MAX_G][MAX_PARTS], pl[RG_MAX_G][MAX_PARTS];  // of every part: CTAs, then prefix records
+    __shared__ float pm[RG_MAX_G][RG_MAX_PARTS], pl[RG_MAX_G][RG_MAX_PARTS];  // of every part: CTAs, then prefix records
     __shared__ float inv[RG_MAX_G];
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
@@ -220,14 +301,16 @@ __global__ void __launch_bounds__(RG_THREADS, 2)
         unit(u0 + warp + NW * i, valid);
         const uint32_t ka = ring_a + st * 2 * Ly::HALF, va = ka + Ly::HALF;
         if (!__all_sync(0xffffffffu, mbar_wait_suspend(&k_full[st], ph, abort_flag))) { ok = false; break; }
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        float d[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of products
         const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
         for (int ks = 0; ks < DH / 16; ++ks) {
             uint32_t f[4];
             ldsm4(rg_addr(ka, krow, 2 * ks + (lane >> 4)), f);
-            mma_keys(d, f, qf[ks][0], qf[ks][1]);
+            mma_keys(ks & 1 ? d2 : d, f, qf[ks][0], qf[ks][1]);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] += d2[e];
         const bool in0 = gq < valid, in1 = gq + 8 < valid;
         const float v0 = in0 ? d[0] * sl2 : -INFINITY, v1 = in0 ? d[1] * sl2 : -INFINITY;
         const float v2 = in1 ? d[2] * sl2 : -INFINITY, v3 = in1 ? d[3] * sl2 : -INFINITY;
@@ -310,16 +393,12 @@ __global__ void __launch_bounds__(RG_THREADS, 2)
         sl[warp][2 * tq + 1] = l1;
     }
     __syncthreads();
-    // four dims of one head per thread and step
+    // four dims of one head per thread and step, the group's heads fastest
     const int quads = a.G * (DH / 4);
     const bool alone = a.C == 1 && a.nrec == 0;
-    auto store = [&](int h, int dd, float4 v, float scale) {
-        const size_t row = (size_t)b * a.Hq + (size_t)j * a.G + h;
-        *reinterpret_cast<uint2*>(a.out + row * DH + dd) =
-            make_uint2(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale));
-    };
+    float* own = a.own ? a.own + ((size_t)b * a.Hkv + j) * a.G * (DH + 4) : nullptr;
     for (int e = threadIdx.x; e < quads; e += THREADS) {  // join the warps
-        const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
+        const int h = e % a.G, dd = e / a.G * 4;
         float M = sm[0][h], L = 0.f;
 #pragma unroll
         for (int w = 1; w < NW; ++w) M = fmaxf(M, sm[w][h]);
@@ -331,8 +410,11 @@ __global__ void __launch_bounds__(RG_THREADS, 2)
             L = fmaf(sl[w][h], f, L);
             v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
         }
-        if (alone) {
-            store(h, dd, v, L == 0.f ? 0.f : 1.f / L);  // no visible key: zeros
+        if (own) {
+            *reinterpret_cast<float4*>(own + h * (DH + 4) + dd) = v;
+            if (dd == 0) *reinterpret_cast<float2*>(own + h * (DH + 4) + DH) = make_float2(M, L);
+        } else if (alone) {
+            store_quad<DH>(a, b, j, h, dd, v, L == 0.f ? 0.f : 1.f / L);  // no visible key: zeros
         } else {
             *reinterpret_cast<float4*>(&so[0][h][dd]) = v;
             if (dd == 0) {
@@ -340,6 +422,12 @@ __global__ void __launch_bounds__(RG_THREADS, 2)
                 cl[h] = L;
             }
         }
+    }
+    if (own) {
+        // The join is a launch of its own, which waits for this one only: this one must not end before the
+        // prefix kernel has.
+        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) pdl_wait();
+        return;
     }
     if (alone) return;
     // join the cluster's CTAs and the prefix records; each CTA finishes a share of the output
@@ -349,60 +437,33 @@ __global__ void __launch_bounds__(RG_THREADS, 2)
         __syncthreads();
     }
     if (a.nrec > 0) {
-        pdl_wait();  // the prefix kernel's partial results
+        pdl_wait();  // the prefix kernel's records
         pdl_trigger();
     }
-    const int parts = a.C + a.nrec;
-    const float* rec0 = a.recs + ((size_t)b * a.Hq + (size_t)j * a.G) * a.nrec * (DH + 4);
-    for (int e = threadIdx.x; e < parts * RG_MAX_G; e += THREADS) {
-        const int p = e / RG_MAX_G, h = e % RG_MAX_G;
-        if (h < a.G) {
-            if (p < a.C) {
-                pm[h][p] = ld_cluster_f32(cluster_addr(&cm[h], p));
-                pl[h][p] = ld_cluster_f32(cluster_addr(&cl[h], p));
-            } else {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(
-                    rec0 + ((size_t)h * a.nrec + p - a.C) * (DH + 4) + DH));
-                pm[h][p] = ml.x;
-                pl[h][p] = ml.y;
-            }
-        }
-    }
-    __syncthreads();
-    for (int h = warp; h < a.G; h += NW) {  // the parts' weights, into pm
-        float M = -INFINITY, L = 0.f;
-        for (int p = lane; p < parts; p += 32) M = fmaxf(M, pm[h][p]);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-        for (int p = lane; p < parts; p += 32) {
-            const float f = pm[h][p] == -INFINITY ? 0.f : ex2_approx(pm[h][p] - M);
-            L = fmaf(pl[h][p], f, L);
-            pm[h][p] = f;
-        }
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
-        if (lane == 0) inv[h] = L == 0.f ? 0.f : 1.f / L;
-    }
-    __syncthreads();
-    for (int e = threadIdx.x + THREADS * rank; e < quads; e += THREADS * a.C) {
-        const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](const float4& x, float f) {
-            v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
-        };
-        if (a.C == 1) {
-            add(*reinterpret_cast<const float4*>(&so[0][h][dd]), pm[h][0]);
-        } else {
-#pragma unroll 4
-            for (int p = 0; p < a.C; ++p) add(ld_cluster_f32x4(cluster_addr(&so[0][h][dd], p)), pm[h][p]);
-        }
-        const float* rec = rec0 + (size_t)h * a.nrec * (DH + 4) + dd;
-#pragma unroll 8
-        for (int r = 0; r < a.nrec; ++r)
-            add(__ldcg(reinterpret_cast<const float4*>(rec + (size_t)r * (DH + 4))), pm[h][a.C + r]);
-        store(h, dd, v, inv[h]);
-    }
+    join_parts<DH>(
+        a, b, j, a.C, rank, pm, pl, inv,
+        [&](int p, int h) {
+            return a.C == 1 ? make_float2(cm[h], cl[h])
+                            : make_float2(ld_cluster_f32(cluster_addr(&cm[h], p)), ld_cluster_f32(cluster_addr(&cl[h], p)));
+        },
+        [&](int p, int h, int dd) {
+            return a.C == 1 ? *reinterpret_cast<const float4*>(&so[0][h][dd]) : ld_cluster_f32x4(cluster_addr(&so[0][h][dd], p));
+        });
     if (a.C > 1) cluster_sync();  // every CTA's partial stays in shared memory until the others have read it
+}
+
+// The own keys' results (attn_ranges_kernel with a.own) and the prefix records of one (sequence, kv head).
+template <int DH>
+__global__ void __launch_bounds__(RG_THREADS) attn_join_kernel(const RangeArgs a) {
+    __shared__ float pm[RG_MAX_G][RG_MAX_PARTS], pl[RG_MAX_G][RG_MAX_PARTS], inv[RG_MAX_G];
+    const int j = blockIdx.x, b = blockIdx.y;
+    const float* own = a.own + ((size_t)b * a.Hkv + j) * a.G * (DH + 4);
+    pdl_trigger();
+    pdl_wait();
+    join_parts<DH>(
+        a, b, j, 1, 0, pm, pl, inv,
+        [&](int, int h) { return __ldcg(reinterpret_cast<const float2*>(own + h * (DH + 4) + DH)); },
+        [&](int, int h, int dd) { return __ldcg(reinterpret_cast<const float4*>(own + h * (DH + 4) + dd)); });
 }
 
 // CTAs per (sequence, kv head): as many as two CTAs on every SM take, while each warp keeps a 16-key unit.
@@ -415,41 +476,100 @@ int ranges_cluster(int B, int Hkv, int max_keys) {
     return c;
 }
 
+template <int DH, bool SINKS, int RING>
+cudaError_t ranges_launch_ring(const CUtensorMap& tk, const CUtensorMap& tv, const RangeArgs& a, int B, cudaStream_t st) {
+    return launch_pdl_cluster(attn_ranges_kernel<DH, SINKS, RING>, dim3(a.C, a.Hkv, B), dim3(RG_THREADS), a.C,
+                              RgLayout<DH, RING>::SMEM, st, tk, tv, a);
+}
+
 template <int DH, bool SINKS>
 cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfloat16* v, int B, int max_keys,
-                             cudaStream_t st) {
+                             int free_sms, cudaStream_t st) {
     CUtensorMap tk, tv;
     const uint64_t heads = (uint64_t)B * a.Hkv;
     if (!encode_tmap_bf16_rows(&tk, k, DH, a.cap, a.cap, heads, RG_KEYS) ||
         !encode_tmap_bf16_rows(&tv, v, DH, a.cap, a.cap, heads, RG_KEYS))
         return cudaErrorInvalidValue;
     a.C = ranges_cluster(B, a.Hkv, max_keys);
-    return launch_pdl_cluster(attn_ranges_kernel<DH, SINKS>, dim3(a.C, a.Hkv, B), dim3(RG_THREADS), a.C,
-                              RgLayout<DH>::SMEM, st, tk, tv, a);
+    // Own keys beside a prefix are few, and four small CTAs an SM start and end them fastest; a window's or a
+    // long cache's keys are streamed by two CTAs with three units a warp on their way (measured, cold cache: 64
+    // sequences x 4100 keys 176 us against 186).
+    int ring = a.nrec > 0 || max_keys <= a.C * RG_WARPS * RG_KEYS * 8 ? 1 : 3;
+    if (getenv("Q3_RING")) ring = atoi(getenv("Q3_RING"));
+    // Own CTAs that cannot all run beside the prefix kernel would keep the others out while they wait for its
+    // records: their results then go through memory to a launch that joins them.
+    if (a.nrec == 0 || a.C > 1 || (long long)B * a.Hkv <= (long long)free_sms * RgLayout<DH, 1>::CTAS) a.own = nullptr;
+    if (ring == 3 && !a.own) return ranges_launch_ring<DH, SINKS, 3>(tk, tv, a, B, st);
+    const cudaError_t e = ring == 2 ? ranges_launch_ring<DH, SINKS, 2>(tk, tv, a, B, st) : ranges_launch_ring<DH, SINKS, 1>(tk, tv, a, B, st);
+    if (e != cudaSuccess || !a.own) return e;
+    return launch_pdl(attn_join_kernel<DH>, dim3(a.Hkv, B), dim3(RG_THREADS), 0, st, a);
 }
 
 template <bool SINKS>
 cudaError_t ranges_launch(const RangeArgs& a, const __nv_bfloat16* k, const __nv_bfloat16* v, int B, int dh, int max_keys,
-                          cudaStream_t st) {
-    if (dh == 128) return ranges_launch_dh<128, SINKS>(a, k, v, B, max_keys, st);
-    if (dh == 64) return ranges_launch_dh<64, SINKS>(a, k, v, B, max_keys, st);
+                          int free_sms, cudaStream_t st) {
+    if (dh == 128) return ranges_launch_dh<128, SINKS>(a, k, v, B, max_keys, free_sms, st);
+    if (dh == 64) return ranges_launch_dh<64, SINKS>(a, k, v, B, max_keys, free_sms, st);
     return cudaErrorInvalidValue;
 }
 
 // Clusters of sixteen CTAs are beyond the portable size.
-template <int DH, bool SINKS>
+template <int DH, bool SINKS, int RING>
 cudaError_t ranges_prepare() {
-    cudaError_t e = cudaFuncSetAttribute(attn_ranges_kernel<DH, SINKS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const void* f = (const void*)attn_ranges_kernel<DH, SINKS, RING>;
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && getenv("Q3_CARVE")) e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(attn_ranges_kernel<DH, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                RgLayout<DH>::SMEM);
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, RgLayout<DH, RING>::SMEM);
 }
 
 }  // namespace
 
+namespace {
+
+// Key chunks of the prefix. The prefix kernel runs one CTA an SM, the own keys' CTAs run on the SMs it leaves, so
+// fewer chunks than SMs can pay: the estimate (us, on the measured rates) is the prefix kernel's time or, if it is
+// longer, the time to read everything, plus what is left of the own keys when the prefix kernel ends.
+// An item of the prefix kernel takes 0.8 us a key tile (its softmax warps), more when its SM's share of HBM is the
+// limit (the row tiles of a chunk share its keys), and 4.5 us for its start and end; an SM reads own keys at up to
+// 100 GB/s; half of the own cache is taken to be filled.
+constexpr int kPrefixMaxRounds = 2;
+int prefix_max_chunks(int B, int Hq, int Hkv, int P) {
+    const long long tiles = (P + 127) / 128, items = (long long)prefix_row_tiles(B, Hq / Hkv) * Hkv;
+    return (int)std::max<long long>(
+        1, std::min<long long>(std::min<long long>(tiles, kPrefixMaxChunks), kPrefixMaxRounds * device_sm_count() / items));
+}
+int prefix_chunks(int B, int Hq, int Hkv, int dh, int P, int cap) {
+    const int row_tiles = prefix_row_tiles(B, Hq / Hkv), sms = device_sm_count();
+    const long long tiles = (P + 127) / 128, items = (long long)row_tiles * Hkv;
+    constexpr double hbm = 6.8e6, sm_rate = 0.1e6;  // bytes per us
+    const double own = (double)B * Hkv * (cap / 2.0) * dh * 4, tile = 128.0 * dh * 4;
+    int best = 1;
+    double best_t = 0;
+    for (int c = 1; c <= prefix_max_chunks(B, Hq, Hkv, P); ++c) {
+        const long long n = items * c, rounds = (n + sms - 1) / sms;
+        const double running = (double)std::min<long long>(n, sms);
+        const double per_tile = std::max(0.8, running / row_tiles * tile / hbm);
+        const double t_prefix = rounds * (((tiles + c - 1) / c) * per_tile + 4.5);
+        const double rate = n < sms ? std::min(hbm, (sms - n) * sm_rate) : 0;
+        const double t = std::max(t_prefix + std::max(0.0, own - rate * t_prefix) / hbm, (own + Hkv * tiles * tile) / hbm) +
+                         0.05 * c;
+        if (c == 1 || t < best_t) {
+            best_t = t;
+            best = c;
+        }
+    }
+    if (getenv("Q3_CH")) best = std::min<int>(prefix_max_chunks(B, Hq, Hkv, P), atoi(getenv("Q3_CH")));
+    return best;
+}
+
+}  // namespace
+
+// The prefix records, then the own keys' results.
 size_t attn_decode_shared_workspace(int B, int Hq, int Hkv, int dh, int prefix_len) {
     if (prefix_len <= 0) return 0;
-    return (size_t)B * Hq * attn_prefix_chunks(B, Hq, Hkv, prefix_len) * (dh + 4) * sizeof(float);
+    const size_t recs = prefix_rec_floats(dh) * prefix_row_tiles(B, Hq / Hkv) * Hkv * prefix_max_chunks(B, Hq, Hkv, prefix_len);
+    return (recs + (size_t)B * Hq * (dh + 4)) * sizeof(float);
 }
 
 cudaError_t attn_decode_shared_launch(const __nv_bfloat16* q, const __nv_bfloat16* kp, const __nv_bfloat16* vp,
@@ -467,14 +587,18 @@ cudaError_t attn_decode_shared_launch(const __nv_bfloat16* q, const __nv_bfloat1
     a.G = Hq / Hkv;
     a.cap = cap;
     a.meta = meta;
+    int free_sms = 0;
     if (P > 0) {
+        a.nrec = prefix_chunks(B, Hq, Hkv, dh, P, cap);
+        a.row_tiles = prefix_row_tiles(B, a.G);
         a.recs = work;
-        a.nrec = attn_prefix_chunks(B, Hq, Hkv, P);
-        const cudaError_t e = attn_prefix_launch(q, kp, vp, B, Hq, Hkv, dh, prefix_cap, P, work, err, st);
+        a.own = work + prefix_rec_floats(dh) * a.row_tiles * Hkv * a.nrec;
+        free_sms = (int)std::max<long long>(0, device_sm_count() - (long long)a.row_tiles * Hkv * a.nrec);
+        const cudaError_t e = attn_prefix_launch(q, kp, vp, B, Hq, Hkv, dh, prefix_cap, P, a.nrec, work, err, st);
         if (e != cudaSuccess) return e;
     }
     a.err = err;
-    return ranges_launch<false>(a, kc, vc, B, dh, cap, st);
+    return ranges_launch<false>(a, kc, vc, B, dh, cap, free_sms, st);
 }
 
 cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B, int Hq,
@@ -495,12 +619,15 @@ cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16
     a.sink_rows = sm.sink_rows;
     a.ring = sm.ring;
     a.err = err;
-    return ranges_launch<true>(a, kc, vc, B, dh, (int)std::min<long long>((long long)sm.window + sm.sinks, cap), st);
+    return ranges_launch<true>(a, kc, vc, B, dh, (int)std::min<long long>((long long)sm.window + sm.sinks, cap), 0, st);
 }
 
 cudaError_t attention_ranges_prepare() {
-    cudaError_t (*const prepare[])() = {ranges_prepare<128, false>, ranges_prepare<128, true>, ranges_prepare<64, false>,
-                                        ranges_prepare<64, true>};
+    cudaError_t (*const prepare[])() = {
+        ranges_prepare<128, false, 1>, ranges_prepare<128, false, 3>, ranges_prepare<128, true, 1>,
+        ranges_prepare<128, true, 3>,  ranges_prepare<64, false, 1>,  ranges_prepare<64, false, 3>,
+        ranges_prepare<64, true, 1>,   ranges_prepare<64, true, 3>,
+        ranges_prepare<128, false, 2>, ranges_prepare<64, false, 2>, ranges_prepare<128, true, 2>, ranges_prepare<64, true, 2>};
     for (auto f : prepare) {
         cudaError_t e = f();
         if (e != cudaSuccess) return e;

@@ -317,6 +317,13 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The lowest n bits set (none for n <= 0, all from 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    uint32_t m;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(m) : "r"(max(n, 0)));
+    return m;
+}
+
 // Paired fp32 arithmetic (Blackwell f32x2 instructions: two lanes per instruction) and a
 // three-input maximum.
 __device__ __forceinline__ unsigned long long f2_bits(float2 v) { return *reinterpret_cast<unsigned long long*>(&v); }

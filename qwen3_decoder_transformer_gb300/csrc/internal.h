@@ -228,6 +228,7 @@ int attn_decode_kernel_count();
 size_t attn_decode_noalloc_max_bytes();
 cudaError_t attn_decode_noalloc_scratch(float** ptr);
 
+// ---------------------------------------------------------------- attention over chosen key tiles (attention_tiles.cu)
 // Sliding window with sinks: slot i sees slots j <= i with i - j < window or j < sinks. ring > 0 is a rolling
 // buffer of sink_rows + ring cache rows: slot s < sink_rows is stored at s, the others at
 // sink_rows + (s - sink_rows) mod ring (both multiples of 128, so a 128-slot tile stays contiguous).
@@ -239,12 +240,16 @@ cudaError_t attn_prefill_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat1
                                       int T, int Hq, int Hkv, int dh, int cap, const int* len0, int len_stride,
                                       SinkMap sm, __nv_bfloat16* out, int* err, cudaStream_t st);
 
-// Query rows q [B, Hq, dh] against P rows of a prefix [Hkv][prefix_cap][dh]: per query row and chunk a record of dh
-// output sums, the maximum (log2 units) and the sum, [B * Hq][attn_prefix_chunks()][dh + 4] floats.
+// Query rows q [B, Hq, dh] against P rows of a prefix [Hkv][prefix_cap][dh]. A row tile holds the G = Hq / Hkv query heads
+// of floor(128 / G) sequences for one kv head (row = sequence in the tile * G + head in the group); for each key chunk,
+// kv head and row tile the kernel leaves a record in recs, [chunks][kv head][row tile]: dh/4 groups of four output sums for
+// each of the 128 rows, [dh/4][128][4], then [128][2] maxima (log2 units) and sums.
+constexpr int kPrefixRows = 128;
+__host__ __device__ constexpr size_t prefix_rec_floats(int dh) { return (size_t)kPrefixRows * (dh + 2); }
+inline int prefix_row_tiles(int B, int G) { return (B + kPrefixRows / G - 1) / (kPrefixRows / G); }
 constexpr int kPrefixMaxChunks = 64;
-int attn_prefix_chunks(int B, int Hq, int Hkv, int P);
 cudaError_t attn_prefix_launch(const __nv_bfloat16* q, const __nv_bfloat16* kp, const __nv_bfloat16* vp, int B, int Hq,
-                               int Hkv, int dh, int prefix_cap, int P, float* recs, int* err, cudaStream_t st);
+                               int Hkv, int dh, int prefix_cap, int P, int chunks, float* recs, int* err, cudaStream_t st);
 
 // ---------------------------------------------------------------- attention over key ranges (attention_ranges.cu)
 cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B, int Hq,
@@ -269,6 +274,7 @@ cudaError_t token_logprobs_launch(const void* logits, int bf16, long long ld, in
 // run outside stream capture. Called by every entry point that launches these kernels.
 cudaError_t gemm_prepare();
 cudaError_t attention_prepare();
+cudaError_t attention_tiles_prepare();
 cudaError_t attention_ranges_prepare();
 cudaError_t prepare_kernels();
 

@@ -75,6 +75,7 @@ cudaError_t prepare_kernels() {
     if (done[dev]) return cudaSuccess;
     cudaError_t e = gemm_prepare();
     if (e == cudaSuccess) e = attention_prepare();
+    if (e == cudaSuccess) e = attention_tiles_prepare();
     if (e == cudaSuccess) e = attention_ranges_prepare();
     if (e == cudaSuccess) done[dev] = true;
     return e;
