@@ -6,8 +6,6 @@
 // result per query row and key chunk, which attn_ranges_kernel joins to the sequence's own keys.
 #include <algorithm>
 
-#include <cstdlib>
-
 #include "common.cuh"
 #include "internal.h"
 
@@ -38,7 +36,7 @@ struct RgLayout {
     static constexpr int RG_BYTES = RING * 8192;      // ring of one warp
     static constexpr int ST = RG_BYTES / (2 * HALF);  // units in it: RING (dh 128) or 2 RING (dh 64)
     static constexpr int SMEM = RG_WARPS * RG_BYTES + 1024;
-    static constexpr int CTAS = RING == 3 ? 2 : RING == 2 ? 3 : 4;  // an SM
+    static constexpr int CTAS = RING == 3 ? 2 : 4;  // an SM
     // the warps' results take the first bytes of the rings once all of them are done
     static constexpr int PITCH = DH + 4;
     static_assert(RG_WARPS * RG_MAX_G * PITCH * 4 <= RG_WARPS * RG_BYTES, "results fit the rings");
@@ -466,13 +464,17 @@ __global__ void __launch_bounds__(RG_THREADS) attn_join_kernel(const RangeArgs a
         [&](int, int h, int dd) { return __ldcg(reinterpret_cast<const float4*>(own + h * (DH + 4) + dd)); });
 }
 
+// Whether an own CTA for every (sequence, kv head) can run on the SMs that the prefix kernel leaves.
+bool fits_beside_prefix(int B, int Hkv, int dh, int free_sms) {
+    return (long long)B * Hkv <= (long long)free_sms * (dh == 128 ? RgLayout<128, 1>::CTAS : RgLayout<64, 1>::CTAS);
+}
+
 // CTAs per (sequence, kv head): as many as two CTAs on every SM take, while each warp keeps a 16-key unit.
 int ranges_cluster(int B, int Hkv, int max_keys) {
     int c = 1;
     while (c < RG_MAX_CLUSTER && (long long)B * Hkv * c * 2 <= 2 * device_sm_count() &&
            max_keys >= 2 * c * RG_WARPS * RG_KEYS)
         c *= 2;
-    if (getenv("Q3_C")) c = atoi(getenv("Q3_C"));
     return c;
 }
 
@@ -494,13 +496,12 @@ cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfl
     // Own keys beside a prefix are few, and four small CTAs an SM start and end them fastest; a window's or a
     // long cache's keys are streamed by two CTAs with three units a warp on their way (measured, cold cache: 64
     // sequences x 4100 keys 176 us against 186).
-    int ring = a.nrec > 0 || max_keys <= a.C * RG_WARPS * RG_KEYS * 8 ? 1 : 3;
-    if (getenv("Q3_RING")) ring = atoi(getenv("Q3_RING"));
+    const int ring = a.nrec > 0 || max_keys <= a.C * RG_WARPS * RG_KEYS * 8 ? 1 : 3;
     // Own CTAs that cannot all run beside the prefix kernel would keep the others out while they wait for its
     // records: their results then go through memory to a launch that joins them.
-    if (a.nrec == 0 || a.C > 1 || (long long)B * a.Hkv <= (long long)free_sms * RgLayout<DH, 1>::CTAS) a.own = nullptr;
-    if (ring == 3 && !a.own) return ranges_launch_ring<DH, SINKS, 3>(tk, tv, a, B, st);
-    const cudaError_t e = ring == 2 ? ranges_launch_ring<DH, SINKS, 2>(tk, tv, a, B, st) : ranges_launch_ring<DH, SINKS, 1>(tk, tv, a, B, st);
+    if (a.nrec == 0 || a.C > 1 || fits_beside_prefix(B, a.Hkv, DH, free_sms)) a.own = nullptr;
+    if (ring == 3) return ranges_launch_ring<DH, SINKS, 3>(tk, tv, a, B, st);
+    const cudaError_t e = ranges_launch_ring<DH, SINKS, 1>(tk, tv, a, B, st);
     if (e != cudaSuccess || !a.own) return e;
     return launch_pdl(attn_join_kernel<DH>, dim3(a.Hkv, B), dim3(RG_THREADS), 0, st, a);
 }
@@ -518,7 +519,6 @@ template <int DH, bool SINKS, int RING>
 cudaError_t ranges_prepare() {
     const void* f = (const void*)attn_ranges_kernel<DH, SINKS, RING>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && getenv("Q3_CARVE")) e = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, RgLayout<DH, RING>::SMEM);
 }
@@ -530,9 +530,9 @@ namespace {
 // Key chunks of the prefix. The prefix kernel runs one CTA an SM, the own keys' CTAs run on the SMs it leaves, so
 // fewer chunks than SMs can pay: the estimate (us, on the measured rates) is the prefix kernel's time or, if it is
 // longer, the time to read everything, plus what is left of the own keys when the prefix kernel ends.
-// An item of the prefix kernel takes 0.8 us a key tile (its softmax warps), more when its SM's share of HBM is the
-// limit (the row tiles of a chunk share its keys), and 4.5 us for its start and end; an SM reads own keys at up to
-// 100 GB/s; half of the own cache is taken to be filled.
+// An item of the prefix kernel takes 0.9 us a key tile (its softmax warps), more when its SM's share of HBM is the
+// limit (the row tiles of a chunk share its keys), and 4.5 us for its start and end; an SM's own CTAs read 55 GB/s;
+// a join launch takes 2.5 us; half of the own cache is taken to be filled.
 constexpr int kPrefixMaxRounds = 2;
 int prefix_max_chunks(int B, int Hq, int Hkv, int P) {
     const long long tiles = (P + 127) / 128, items = (long long)prefix_row_tiles(B, Hq / Hkv) * Hkv;
@@ -542,24 +542,24 @@ int prefix_max_chunks(int B, int Hq, int Hkv, int P) {
 int prefix_chunks(int B, int Hq, int Hkv, int dh, int P, int cap) {
     const int row_tiles = prefix_row_tiles(B, Hq / Hkv), sms = device_sm_count();
     const long long tiles = (P + 127) / 128, items = (long long)row_tiles * Hkv;
-    constexpr double hbm = 6.8e6, sm_rate = 0.1e6;  // bytes per us
+    constexpr double hbm = 6.8e6, sm_rate = 0.055e6;  // bytes per us
     const double own = (double)B * Hkv * (cap / 2.0) * dh * 4, tile = 128.0 * dh * 4;
     int best = 1;
     double best_t = 0;
     for (int c = 1; c <= prefix_max_chunks(B, Hq, Hkv, P); ++c) {
         const long long n = items * c, rounds = (n + sms - 1) / sms;
         const double running = (double)std::min<long long>(n, sms);
-        const double per_tile = std::max(0.8, running / row_tiles * tile / hbm);
+        const double per_tile = std::max(0.9, running / row_tiles * tile / hbm);
         const double t_prefix = rounds * (((tiles + c - 1) / c) * per_tile + 4.5);
         const double rate = n < sms ? std::min(hbm, (sms - n) * sm_rate) : 0;
+        const bool join = !fits_beside_prefix(B, Hkv, dh, (int)std::max<long long>(0, sms - n));
         const double t = std::max(t_prefix + std::max(0.0, own - rate * t_prefix) / hbm, (own + Hkv * tiles * tile) / hbm) +
-                         0.05 * c;
+                         0.05 * c + (join ? 2.5 : 0);
         if (c == 1 || t < best_t) {
             best_t = t;
             best = c;
         }
     }
-    if (getenv("Q3_CH")) best = std::min<int>(prefix_max_chunks(B, Hq, Hkv, P), atoi(getenv("Q3_CH")));
     return best;
 }
 
@@ -626,8 +626,7 @@ cudaError_t attention_ranges_prepare() {
     cudaError_t (*const prepare[])() = {
         ranges_prepare<128, false, 1>, ranges_prepare<128, false, 3>, ranges_prepare<128, true, 1>,
         ranges_prepare<128, true, 3>,  ranges_prepare<64, false, 1>,  ranges_prepare<64, false, 3>,
-        ranges_prepare<64, true, 1>,   ranges_prepare<64, true, 3>,
-        ranges_prepare<128, false, 2>, ranges_prepare<64, false, 2>, ranges_prepare<128, true, 2>, ranges_prepare<64, true, 2>};
+        ranges_prepare<64, true, 1>,   ranges_prepare<64, true, 3>};
     for (auto f : prepare) {
         cudaError_t e = f();
         if (e != cudaSuccess) return e;

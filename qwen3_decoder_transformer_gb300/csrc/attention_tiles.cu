@@ -20,17 +20,17 @@ namespace {
 // floor(128 / G) sequences; the item leaves a record (output sums, maximum, sum of each row) instead of an output.
 // The row tiles of one (kv head, chunk) are neighbours in the item order and share the chunk's keys in L2.
 //
-// Warps: 0 Q and keys (TMA), 1 score MMAs, 2 values (TMA), 3 P V MMAs, 4-11 softmax. Tensor memory: three score
-// regions of 128 columns and the output accumulator, so the scores run two tiles ahead of P V; P (bf16) takes the
-// first 64 columns of its score region.
-// Softmax: warps 4-7 take columns 0-63 of every tile, warps 8-11 columns 64-127, thread <-> (row, half). The two
-// threads of a row exchange their maxima through shared memory once a tile (an mbarrier of the two warps of a
-// row quarter) and so keep the same scale; O is rescaled only when the maximum grew by more than 2^8. With one
-// thread a row, the pass over a tile took about 1,600 cycles of mostly dependent work on one warp per sub-partition
-// against 1,024 of MMA work; two warps per sub-partition overlap their loads, maxima and exponentials
-// (TIMES).
+// Warps: 0 Q and keys (TMA), 1 score MMAs, 2 values (TMA), 3 P V MMAs, 4-7 softmax (thread <-> query row). Tensor
+// memory: three score regions of 128 columns and the output accumulator, so the scores run two tiles ahead of P V;
+// P (bf16) takes the first 64 columns of its score region. O is rescaled only when a row's maximum grew by more
+// than 2^8.
+// What bounds it: a softmax thread's chain over a tile (scores from tensor memory, maximum, exponentials, P back),
+// about 1,600 cycles against 1,024 of MMA work. Measured on timing copies of this kernel (8192 tokens, 32 heads,
+// window 4096): without the copies of K and V the time stays, with half of the MMAs it falls by 4%, without the
+// exponentials by 13%. Two threads a row that exchange their maxima: 310 us against 293; the same with the next
+// tile's scores loaded ahead: 409; two warpgroups on alternate tiles (as the causal prefill's ALT form): 305.
 constexpr int TL_SINKS = 0, TL_PREFIX = 1;
-constexpr int TL_BM = 128, TL_BN = 128, TL_THREADS = 384, TL_NR = 3, TL_KST = 3, TL_VST = 3;
+constexpr int TL_BM = 128, TL_BN = 128, TL_THREADS = 256, TL_NR = 3, TL_KST = 3, TL_VST = 3;
 
 template <int DH>
 struct TlLayout {
@@ -40,8 +40,7 @@ struct TlLayout {
     static constexpr int K_OFF = Q_BYTES;
     static constexpr int V_OFF = K_OFF + TL_KST * KV_BYTES;
     static constexpr int BAR_OFF = V_OFF + TL_VST * KV_BYTES;
-    static constexpr int XCH_OFF = BAR_OFF + 512;  // [2 slots][2 halves][128 rows] floats
-    static constexpr int SMEM = XCH_OFF + 2 * 2 * TL_BM * 4;
+    static constexpr int SMEM = BAR_OFF + 256 + 1024;
 };
 static_assert(TlLayout<128>::SMEM <= 227 * 1024, "shared memory");
 
@@ -67,7 +66,9 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
     constexpr uint32_t IDESC_S = idesc_bf16(TL_BM, TL_BN);
     constexpr uint32_t IDESC_O = idesc_bf16(TL_BM, DH, true);
     constexpr uint32_t TM_O = NR * TL_BN;
-    extern __shared__ __align__(1024) uint8_t smem[];  // TMA and the operand descriptors want 1024-byte tiles
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::BAR_OFF);
     uint64_t* q_full = bars;
     uint64_t* q_empty = bars + 1;
@@ -76,14 +77,12 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
     uint64_t* v_full = bars + 8;    // [VST]
     uint64_t* v_empty = bars + 11;  // [VST]
     uint64_t* s_full = bars + 14;   // [NR] scores of the region are complete
-    uint64_t* p_full = bars + 17;   // [NR] P of the region is written
+    uint64_t* p_full = bars + 17;   // [NR] P of the region is written (one arrival a warp, as for o_free)
     uint64_t* r_free = bars + 20;   // [NR] P V of the region's tile is done
     uint64_t* o_free = bars + 23;   // the item's output has been read out
     uint64_t* v_clean = bars + 24;  // [VST] hidden value rows of the stage's tile are zeroed (one phase per such tile)
-    uint64_t* x_met = bars + 27;    // [4 row quarters] both halves' warps have published a value for the other
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 31);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 32);
-    volatile float* xch = reinterpret_cast<volatile float*>(smem + Ly::XCH_OFF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 27);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 28);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -100,11 +99,10 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
         }
         for (int i = 0; i < NR; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 256);
+            mbar_init(&p_full[i], 4);
             mbar_init(&r_free[i], 1);
         }
-        mbar_init(o_free, 256);
-        for (int i = 0; i < 4; ++i) mbar_init(&x_met[i], 2);
+        mbar_init(o_free, 4);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmQ);
@@ -119,7 +117,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    bool ok = (smem_u32(smem) & 1023u) == 0;
+    bool ok = true;
     pdl_wait();  // Q and the cache come from earlier kernels
     pdl_trigger();
 
@@ -331,24 +329,11 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
             }
         }
     } else {
-        // ---------------- softmax: columns half * 64 .. of every tile, thread <-> row (TMEM lane)
-        const int half = (warp >> 2) - 1, quarter = warp & 3, row = quarter * 32 + lane;
+        // ---------------- softmax: thread <-> query row (TMEM lane)
+        const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tm_o = tmem + lane_off + TM_O + half * (DH / 2);
+        const uint32_t tm_o = tmem + lane_off + TM_O;
         const float sl2 = kLog2e / sqrtf((float)DH);
-        int n_xch = 0;
-        // v becomes the other half's v for this row. Two slots in turn: a slot is written again only behind the next
-        // exchange's meeting, which the reader reaches after it has read.
-        auto exchange = [&](float& v) -> bool {
-            volatile float* slot = xch + (n_xch & 1) * 2 * TL_BM;
-            slot[half * TL_BM + row] = v;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&x_met[quarter]);
-            if (!__all_sync(0xffffffffu, mbar_wait_suspend(&x_met[quarter], n_xch & 1, abort_flag))) return false;
-            ++n_xch;
-            v = slot[(half ^ 1) * TL_BM + row];
-            return true;
-        };
         // P V of global tile k (and so every earlier one) is done. The region's next completion would be P V of
         // tile k + NR, which needs a P this thread has not released yet: the parity cannot alias.
         auto pv_done = [&](int k) -> bool {
@@ -364,31 +349,28 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
         Pending pend{Item{}, 0.f, 0.f, -1};
         auto finish = [&](const Pending& p) -> bool {
             if (!pv_done(p.last)) return false;
-            float l = p.l;
-            if (!exchange(l)) return false;
-            l += p.l;
             tc_fence_after();
             if constexpr (PREFIX) {
                 // a warp stores 512 contiguous bytes at a time; every row of the tile has its place in the record
                 float* rec = a.recs + ((size_t)(p.it.chunk * Hkv + p.it.h) * a.row_tiles + p.it.b) * prefix_rec_floats(DH);
 #pragma unroll 1
-                for (int c = 0; c < DH / 64; ++c) {
+                for (int c = 0; c < DH / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(tm_o + c * 32, o);
                     tmem_ld_wait();
-                    float* dst = rec + ((size_t)(half * (DH / 8) + c * 8) * TL_BM + row) * 4;
+                    float* dst = rec + ((size_t)c * 8 * TL_BM + row) * 4;
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
                         *reinterpret_cast<uint4*>(dst + (size_t)v * TL_BM * 4) =
                             make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                 }
-                if (half == 0) *reinterpret_cast<float2*>(rec + (size_t)DH * TL_BM + row * 2) = make_float2(p.m, l);
+                *reinterpret_cast<float2*>(rec + (size_t)DH * TL_BM + row * 2) = make_float2(p.m, p.l);
             } else {
-                const float inv = 1.f / l;
+                const float inv = 1.f / p.l;
                 const int t0 = p.it.q0 + quarter * 32 + (lane & ~3);
-                __nv_bfloat16* dst = a.out + (((size_t)p.it.b * T + t0) * Hq + p.it.h) * DH + half * (DH / 2) + (lane & 3) * 8;
+                __nv_bfloat16* dst = a.out + (((size_t)p.it.b * T + t0) * Hq + p.it.h) * DH + (lane & 3) * 8;
 #pragma unroll 1
-                for (int c = 0; c < DH / 64; ++c) {
+                for (int c = 0; c < DH / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(tm_o + c * 32, o);
                     tmem_ld_wait();
@@ -422,7 +404,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                 }
             }
             tc_fence_before();
-            mbar_arrive(o_free);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
             return true;
         };
         int g = 0;
@@ -431,50 +414,48 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
             const int nt = it.n_tiles;
             if (nt <= 0) break;
             const int pos = it.len0 + it.q0 + row;
-            float m = -INFINITY, l = 0.f;  // the row's scale (log2 units), this half's sum
+            float m = -INFINITY, l = 0.f;  // the row's scale (log2 units) and sum
             for (int i = 0; i < nt; ++i) {
                 const int gi = g + i, r = gi % NR, k0 = tile_of(it, i) * TL_BN;
                 const uint32_t tm_s = tmem + lane_off + r * TL_BN;
                 if (!__all_sync(0xffffffffu, mbar_wait_suspend(&s_full[r], (gi / NR) & 1, abort_flag))) { ok = false; break; }
                 tc_fence_after();
-                uint32_t sr[64];
+                uint32_t sr[TL_BN];
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    tmem_ld_32x32b_x32(tm_s + half * 64 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+                for (int c = 0; c < TL_BN / 32; ++c)
+                    tmem_ld_32x32b_x32(tm_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
                 tmem_ld_wait();
-                // Hidden keys, only in the tiles at the ends of the sinks, of the window and of the item: the
-                // visible columns of the row as a bit mask, one test and one select per score.
-                if (PREFIX ? i + 1 == nt : (i <= it.ja + 1 && i + 1 >= it.ja) || i + 2 >= nt) {
-                    const int lim = PREFIX ? T - k0 - 1 : pos - k0;            // last visible column
-                    const int lo = PREFIX ? 0 : lim - a.window + 1;            // first column of the window
-                    const int sk = PREFIX ? 0 : a.sinks - k0;                  // columns below it are sinks
+                // Hidden keys, only in the tiles at the ends of the sinks, of the window and of the item: the visible
+                // columns of the row as a bit mask, one test and one select per score (range tests per score made
+                // such a tile take two to four times an ordinary one's time).
+                if (PREFIX ? k0 + TL_BN > T
+                           : ((i <= it.ja + 1 && i + 1 >= it.ja) || i + 2 >= nt) &&
+                                 (k0 + TL_BN - 1 > it.len0 + it.q0 ||
+                                  (k0 < it.len0 + it.q_end - a.window && k0 + TL_BN > a.sinks))) {
+                    const int lim = PREFIX ? T - k0 - 1 : pos - k0;  // last visible column
+                    const int lo = PREFIX ? 0 : lim - a.window + 1;  // first column of the window
+                    const int sk = PREFIX ? 0 : a.sinks - k0;        // columns below it are sinks
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int at = half * 64 + c * 32;
-                        const uint32_t vis = low_bits(lim + 1 - at) & (~low_bits(lo - at) | low_bits(sk - at));
+                    for (int c = 0; c < TL_BN / 32; ++c) {
+                        const uint32_t vis = low_bits(lim + 1 - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             sr[c * 32 + e] = vis & (1u << e) ? sr[c * 32 + e] : __float_as_uint(-INFINITY);
                     }
                 }
-                float mx = -INFINITY, mx1 = -INFINITY;
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // independent chains: 3% of a long window's time
 #pragma unroll
-                for (int e = 0; e < 64; e += 4) {
-                    mx = fmax3(mx, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
-                    mx1 = fmax3(mx1, __uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3]));
-                }
-                mx = fmaxf(mx, mx1);
-                // Both halves have read their scores once they have met; P may overwrite them.
-                float other = mx;
-                if (!exchange(other)) { ok = false; break; }
-                mx = fmaxf(mx, other) * sl2;
-                const bool grow = mx > m + 8.0f;  // the same for both threads of a row
+                for (int e = 0; e < TL_BN; e += 2)
+                    mx4[e / 2 % 4] = fmax3(mx4[e / 2 % 4], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+                // lazy rescale, decided per row but executed by the whole warp (tcgen05.ld/st are warp-wide)
+                const bool grow = mx > m + 8.0f;
                 const float alpha = grow ? ex2_approx(m - mx) : 1.0f;
                 if (i > 0 && __any_sync(0xffffffffu, grow)) {
                     if (!pv_done(gi - 1)) { ok = false; break; }  // O must hold every earlier tile's P V before it is scaled
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < DH / 64; ++c) {
+                    for (int c = 0; c < DH / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(tm_o + c * 32, o);
                         tmem_ld_wait();
@@ -492,19 +473,25 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                 const float nm = m == -INFINITY ? 0.f : -m;
                 const float2 sl2x2 = make_float2(sl2, sl2), nmx2 = make_float2(nm, nm);
                 float2 rs2 = make_float2(0.f, 0.f);
-                uint32_t pk[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float2 x = fma2(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sl2x2, nmx2);
-                    const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                    rs2 = add2(rs2, pp);
-                    pk[e] = pack_bf16(pp.x, pp.y);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 x = fma2(make_float2(__uint_as_float(sr[half * 64 + 2 * e]),
+                                                          __uint_as_float(sr[half * 64 + 2 * e + 1])),
+                                              sl2x2, nmx2);
+                        const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        rs2 = add2(rs2, pp);
+                        pk[e] = pack_bf16(pp.x, pp.y);
+                    }
+                    tmem_st_32x32b_x32(tm_s + half * 32, pk);
                 }
-                tmem_st_32x32b_x32(tm_s + half * 32, pk);
                 tmem_st_wait();
                 l += rs2.x + rs2.y;
                 tc_fence_before();
-                mbar_arrive(&p_full[r]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[r]);
                 if (i == 0 && pend.last >= 0) {
                     ok = finish(pend);
                     if (!ok) break;

@@ -276,6 +276,7 @@ cudaError_t gemm_prepare();
 cudaError_t attention_prepare();
 cudaError_t attention_tiles_prepare();
 cudaError_t attention_ranges_prepare();
+cudaError_t token_logprobs_prepare();
 cudaError_t prepare_kernels();
 
 }  // namespace q3

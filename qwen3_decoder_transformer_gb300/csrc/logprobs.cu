@@ -1,6 +1,7 @@
 // Log probabilities of given tokens, the entropy of each row's distribution and its largest alternatives,
 // in one pass over the logits.
 #include <algorithm>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "internal.h"
@@ -17,18 +18,20 @@ namespace {
 // Alternatives are ordered by a 64-bit key, the value's order-preserving bits above the complemented
 // index: unique keys, so ties go to the lowest index, and NaN is the largest value. A threshold keeps the
 // selection out of the main loop: the k-th largest of 64 group maxima over the first elements read (spread
-// over the slice, so that sorted rows do not defeat it) is a lower bound of the slice's k-th largest, and
-// only elements above it enter the candidate list. The list is then cut by the same rule and ranked by
-// counting. A slice whose list overflows, or that holds NaN or +inf, is rescanned once per alternative.
+// over the slice, both ends included, so that sorted rows do not defeat it) is a lower bound of the slice's k-th
+// largest, and only elements above it enter the candidate list; the bound is raised from the list twice on
+// the way. The list is then cut by the same rule and ranked by counting. A slice whose list overflows, or
+// that holds NaN or +inf, is rescanned once per alternative.
 //
 // A cluster of C CTAs shares a row (C = 1 when the rows alone fill the SMs) and CTA 0 joins the parts
 // through distributed shared memory: no workspace, one launch.
+// What bounds it: many rows, HBM (TIMES); few rows, the chain of a CTA (first loads, threshold, list, join).
 constexpr int LP_THREADS = 512;
 constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_GROUPS = 64;           // groups of 8 threads whose maxima give the threshold
 constexpr int LP_CAP = 2080;            // candidates of one CTA: a slice of fewer than 2048 + 14 elements fits whole
 constexpr int LP_CUT = 256, LP_RANK = 128;
-constexpr int LP_MAX_CLUSTER = 8;
+constexpr int LP_MAX_CLUSTER = 16;  // beyond the portable size
 static_assert(LP_THREADS == 8 * LP_GROUPS, "eight threads per group");
 
 using u64 = unsigned long long;
@@ -37,12 +40,15 @@ template <typename T>
 struct LpLoad;
 template <>
 struct LpLoad<float> {
-    static constexpr int EPV = 4, U = 4;  // elements per 16-byte vector, vectors per thread and step
+    static constexpr int EPV = 4;  // elements of a 16-byte vector
     static __device__ __forceinline__ void unpack(const uint4& r, float* x) {
         x[0] = __uint_as_float(r.x);
         x[1] = __uint_as_float(r.y);
         x[2] = __uint_as_float(r.z);
         x[3] = __uint_as_float(r.w);
+    }
+    static __device__ __forceinline__ float largest(const uint4& r) {
+        return fmax3(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), __uint_as_float(r.z), __uint_as_float(r.w));
     }
     static __device__ __forceinline__ float one(const float* p) { return *p; }
     static __device__ __forceinline__ uint4 fill() {
@@ -52,7 +58,7 @@ struct LpLoad<float> {
 };
 template <>
 struct LpLoad<__nv_bfloat16> {
-    static constexpr int EPV = 8, U = 2;
+    static constexpr int EPV = 8;
     static __device__ __forceinline__ void unpack(const uint4& r, float* x) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -60,6 +66,10 @@ struct LpLoad<__nv_bfloat16> {
             x[2 * i] = bf16_lo(w[i]);
             x[2 * i + 1] = bf16_hi(w[i]);
         }
+    }
+    static __device__ __forceinline__ float largest(const uint4& r) {
+        const uint32_t m = as_u32(__hmax2(__hmax2(as_bf2(r.x), as_bf2(r.y)), __hmax2(as_bf2(r.z), as_bf2(r.w))));
+        return fmaxf(bf16_lo(m), bf16_hi(m));
     }
     static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return bf16f(*p); }
     static __device__ __forceinline__ uint4 fill() {
@@ -96,7 +106,7 @@ struct LpShared {
     u64 cand[LP_CAP];
     u64 cut[LP_CUT];
     u64 groups[LP_GROUPS];
-    u64 top[kLogprobMaxTop];
+    u64 top[kLogprobMaxTop], joined[kLogprobMaxTop];
     u64 warp_best[LP_WARPS];
     u64 tau;
     LpStat warp_stat[LP_WARPS];
@@ -104,36 +114,80 @@ struct LpShared {
     int n_cand, n_cut;
 };
 
-// The k-th largest of the 64 group maxima of the threads' keys (0 = no element).
+// The k-th largest of the 64 group maxima of the threads' keys (0 = no element). Eight threads count the rank of
+// each group's key.
 __device__ __forceinline__ u64 lp_threshold(u64 rep, int k, LpShared& sh) {
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
         const u64 other = __shfl_xor_sync(0xffffffffu, rep, o);
         rep = other > rep ? other : rep;
     }
-    if ((threadIdx.x & 7) == 0) sh.groups[threadIdx.x >> 3] = rep;
+    const int grp = threadIdx.x >> 3, part = threadIdx.x & 7;
+    if (part == 0) sh.groups[grp] = rep;
     __syncthreads();
-    if (threadIdx.x < LP_GROUPS) {
-        const u64 mine = sh.groups[threadIdx.x];
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < LP_GROUPS; ++j) {
-            const u64 o = sh.groups[j];
-            rank += (o > mine) | ((o == mine) & (j < (int)threadIdx.x));
-        }
-        if (rank == k - 1) sh.tau = mine;
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < LP_GROUPS / 8; ++i) {
+        const int j = i * 8 + part;
+        const u64 o = sh.groups[j];
+        rank += (o > rep) | ((o == rep) & (j < grp));
     }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (part == 0 && rank == k - 1) sh.tau = rep;
     __syncthreads();
     return sh.tau;
 }
 
+// out[r] = the r-th largest of list[0 .. n), r < k; the list's keys are distinct, 0 stands for no element. P threads
+// share the count of one key.
+template <int P>
+__device__ __forceinline__ void lp_rank(const u64* list, int n, int k, u64* out) {
+    for (int i0 = 0; i0 < n; i0 += LP_THREADS / P) {
+        const int i = i0 + threadIdx.x / P, part = threadIdx.x % P;
+        const u64 mine = i < n ? list[i] : 0;
+        int r = 0;
+#pragma unroll 4
+        for (int j = part; j < n; j += P) r += list[j] > mine;
+#pragma unroll
+        for (int o = 1; o < P; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+        if (part == 0 && mine && r < k) out[r] = mine;
+    }
+}
+
+// The k largest of list[0 .. n) into out, sorted; false when the cut list overflows. n is the same in every thread;
+// sh.n_cut is 0 on entry.
+__device__ __forceinline__ bool lp_select(const u64* list, int n, int k, LpShared& sh, u64* out) {
+    if (n > LP_RANK) {  // cut the list first
+        u64 rep = 0;
+        for (int i = threadIdx.x; i < n; i += LP_THREADS) rep = list[i] > rep ? list[i] : rep;
+        const u64 cut = lp_threshold(rep, k, sh);
+        for (int i = threadIdx.x; i < n; i += LP_THREADS)
+            if (list[i] >= cut && list[i]) {
+                const int at = atomicAdd(&sh.n_cut, 1);
+                if (at < LP_CUT) sh.cut[at] = list[i];
+            }
+        __syncthreads();
+        list = sh.cut;
+        n = sh.n_cut;
+        if (n > LP_CUT) return false;
+    }
+    if (n <= LP_THREADS / 8)
+        lp_rank<8>(list, n, k, out);
+    else if (n <= LP_THREADS / 4)
+        lp_rank<4>(list, n, k, out);
+    else
+        lp_rank<2>(list, n, k, out);
+    return true;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(LP_THREADS)
+__global__ void __launch_bounds__(LP_THREADS, 2)
     token_logprobs_kernel(const T* __restrict__ logits, long long ld, int V, const int32_t* __restrict__ tokens, int k,
                           float* __restrict__ logprob, float* __restrict__ entropy, int32_t* __restrict__ top_ids,
                           float* __restrict__ top_logprobs, int C, int* err) {
     using L = LpLoad<T>;
-    constexpr int EPV = L::EPV, U = L::U;
+    constexpr int EPV = L::EPV, U = 4;  // U vectors a thread and step
     __shared__ LpShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row_i = blockIdx.x / C, rank = C > 1 ? (int)cluster_rank() : 0;
@@ -156,17 +210,15 @@ __global__ void __launch_bounds__(LP_THREADS)
     }
     if (tid < kLogprobMaxTop) sh.top[tid] = 0;
 
-    const int chunks = (n + LP_THREADS - 1) / LP_THREADS;
-    // chunk read at position p: the first U positions are spread from the first chunk to the last
-    auto chunk_at = [&](int p) -> int {
-        if (chunks <= U) return p;
-        if (p < U) return (int)((long long)p * (chunks - 1) / (U - 1));
-        int c = p - U;
-#pragma unroll
-        for (int i = 0; i < U; ++i) c += c >= (int)((long long)i * (chunks - 1) / (U - 1));
-        return c;
+    // U streams: stream u < U - 1 runs forward from vector u * span, the last one backward from the slice's end, so that
+    // the first step's elements are spread over the slice and include both ends
+    const int steps = max(1, (n + U * LP_THREADS - 1) / (U * LP_THREADS)), span = steps * LP_THREADS;
+    auto vector_at = [&](int step, int u) -> int {  // this thread's vector of stream u, or -1
+        const int off = step * LP_THREADS + tid;
+        if (u < U - 1) return u * span + off < n ? u * span + off : -1;
+        return n - 1 - off >= (U - 1) * span ? n - 1 - off : -1;
     };
-    LpStat st{kLowest, 0.f, 0.f};
+    float m = kLowest;
     u64 tau = 0;
     float tau_v = -INFINITY;
     auto push = [&](float v, int idx) {
@@ -176,65 +228,103 @@ __global__ void __launch_bounds__(LP_THREADS)
             if (at < LP_CAP) sh.cand[at] = key;
         }
     };
-    auto accumulate = [&](const float* x, int cnt, float mx) {
-        if (mx > st.m) {
-            const float d = fmaxf(st.m - mx, -1e30f), f = ex2_approx(d * kLog2e);
-            st.t = (st.t + st.s * d) * f;
-            st.s *= f;
-            st.m = mx;
-        }
-#pragma unroll
-        for (int i = 0; i < EPV * U; ++i) {
-            if (i >= cnt) break;
-            const float d = x[i] - st.m;
-            const float e = ex2_approx(d * kLog2e);
-            st.s += e;
-            st.t = fmaf(e, fmaxf(d, -200.f), st.t);
+    float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);  // two running sums a thread (paired fp32 arithmetic)
+    auto raise = [&](float mx) {  // move the sums to a larger maximum
+        if (mx > m) {
+            const float d = fmaxf(m - mx, -1e30f), f = ex2_approx(d * kLog2e);
+            const float2 d2 = make_float2(d, d), f2 = make_float2(f, f);
+            t2 = mul2(fma2(s2, d2, t2), f2);
+            s2 = mul2(s2, f2);
+            m = mx;
         }
     };
-    for (int p = 0; p < chunks || p == 0; p += U) {
-        uint4 raw[U];
-        int at[U];  // vector of the slice, or -1
+    auto add_pair = [&](float a, float b) {
+        const float2 d = add2(make_float2(a, b), make_float2(-m, -m));
+        const float2 y = mul2(d, make_float2(kLog2e, kLog2e));
+        const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+        s2 = add2(s2, e);
+        t2 = fma2(e, make_float2(fmaxf(d.x, -200.f), fmaxf(d.y, -200.f)), t2);
+    };
+    // the loads of one step ahead are in flight while a step is worked on
+    uint4 nxt[U];
+    auto load = [&](int step) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = p + u < chunks ? chunk_at(p + u) * LP_THREADS + tid : n;
-            at[u] = i < n ? i : -1;
-            raw[u] = i < n ? __ldcs(vec + i) : L::fill();
+            const int v = vector_at(step, u);
+            nxt[u] = v >= 0 ? __ldcs(vec + v) : L::fill();
         }
-        float x[EPV * U];
+    };
+    load(0);
+    for (int step = 0; step < steps; ++step) {
+        uint4 raw[U];
+        float vmax[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) L::unpack(raw[u], x + u * EPV);
-        float mx = x[0];
+        for (int u = 0; u < U; ++u) raw[u] = nxt[u];
+        if (step + 1 < steps) load(step + 1);
 #pragma unroll
-        for (int i = 1; i < EPV * U; ++i) mx = fmaxf(mx, x[i]);
+        for (int u = 0; u < U; ++u) vmax[u] = L::largest(raw[u]);
+        const float mx = fmax3(fmaxf(vmax[0], vmax[1]), vmax[2], vmax[3]);
         if (k > 0) {
-            if (p == 0) {  // threshold from the first elements read
+            if (step == 0) {  // threshold from the first elements read
                 u64 rep = 0;
 #pragma unroll
-                for (int i = 0; i < EPV * U; ++i)
-                    if (at[i / EPV] >= 0 && x[i] == mx) {
-                        const u64 key = lp_key(x[i], base + at[i / EPV] * EPV + i % EPV);
-                        rep = key > rep ? key : rep;
+                for (int u = 0; u < U; ++u)
+                    if (vmax[u] == mx) {
+                        const int v = vector_at(0, u);
+                        float x[EPV];
+                        L::unpack(raw[u], x);
+#pragma unroll
+                        for (int e = 0; e < EPV; ++e)
+                            if (v >= 0 && x[e] == mx) {
+                                const u64 key = lp_key(x[e], base + v * EPV + e);
+                                rep = key > rep ? key : rep;
+                            }
                     }
                 __syncthreads();  // the list's counters are set
                 tau = lp_threshold(rep, k, sh);
                 tau_v = tau == 0 ? -INFINITY : lp_value(tau);
+            } else if ((step == 3 || step == 8) && steps > 2 * step) {  // raise it from the list so far
+                __syncthreads();
+                const int nc = min(sh.n_cand, LP_CAP);
+                u64 rep = 0;
+                for (int i = tid; i < nc; i += LP_THREADS) rep = sh.cand[i] > rep ? sh.cand[i] : rep;
+                const u64 t = lp_threshold(rep, k, sh);
+                if (t > tau) {
+                    tau = t;
+                    tau_v = lp_value(tau);
+                }
             }
             if (mx >= tau_v) {
 #pragma unroll
-                for (int i = 0; i < EPV * U; ++i)
-                    if (x[i] >= tau_v && at[i / EPV] >= 0) push(x[i], base + at[i / EPV] * EPV + i % EPV);
+                for (int u = 0; u < U; ++u)
+                    if (vmax[u] >= tau_v) {
+                        const int v = vector_at(step, u);
+                        float x[EPV];
+                        L::unpack(raw[u], x);
+#pragma unroll
+                        for (int e = 0; e < EPV; ++e)
+                            if (v >= 0 && x[e] >= tau_v) push(x[e], base + v * EPV + e);
+                    }
             }
         }
-        accumulate(x, EPV * U, mx);
+        raise(mx);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float x[EPV];
+            L::unpack(raw[u], x);
+#pragma unroll
+            for (int e = 0; e < EPV; e += 2) add_pair(x[e], x[e + 1]);
+        }
     }
     if (one >= 0) {
         const float v = L::one(row + one);
-        accumulate(&v, 1, v);
+        raise(v);
+        add_pair(v, -INFINITY);
         if (k > 0 && v >= tau_v) push(v, one);
     }
 
     // join the threads' statistics
+    LpStat st{m, s2.x + s2.y, t2.x + t2.y};
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const LpStat b{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
@@ -259,30 +349,7 @@ __global__ void __launch_bounds__(LP_THREADS)
     if (k > 0) {
         const int nc = sh.n_cand;
         bool rescan = nc > LP_CAP || sh.stat.s != sh.stat.s;
-        if (!rescan) {
-            const u64* list = sh.cand;
-            int nl = nc;
-            if (nc > LP_RANK) {
-                u64 rep = 0;
-                for (int i = tid; i < nc; i += LP_THREADS) rep = sh.cand[i] > rep ? sh.cand[i] : rep;
-                const u64 cut = lp_threshold(rep, k, sh);
-                for (int i = tid; i < nc; i += LP_THREADS)
-                    if (sh.cand[i] >= cut) {
-                        const int at = atomicAdd(&sh.n_cut, 1);
-                        if (at < LP_CUT) sh.cut[at] = sh.cand[i];
-                    }
-                __syncthreads();
-                list = sh.cut;
-                nl = sh.n_cut;
-                rescan = nl > LP_CUT;
-            }
-            if (!rescan && tid < nl) {
-                const u64 mine = list[tid];
-                int r = 0;
-                for (int j = 0; j < nl; ++j) r += list[j] > mine;
-                if (r < k) sh.top[r] = mine;
-            }
-        }
+        if (!rescan) rescan = !lp_select(sh.cand, nc, k, sh, sh.top);
         if (rescan) {  // one scan of the slice per alternative: the largest key below the previous one
             u64 prev = ~0ull;
             for (int r = 0; r < k; ++r) {
@@ -321,30 +388,33 @@ __global__ void __launch_bounds__(LP_THREADS)
         cluster_sync();
         if (rank == 0) {
             if (k > 0) {
-                if (tid < C * kLogprobMaxTop)
-                    sh.cand[tid] = ld_cluster_u64(cluster_addr(&sh.top[tid % kLogprobMaxTop], tid / kLogprobMaxTop));
+                const int nk = C * k;
+                for (int i = tid; i < nk; i += LP_THREADS) sh.cand[i] = ld_cluster_u64(cluster_addr(&sh.top[i % k], i / k));
+                if (tid == 0) sh.n_cut = 0;
                 __syncthreads();
-                if (tid < C * kLogprobMaxTop) {
-                    const u64 mine = sh.cand[tid];
-                    int r = 0;
-                    for (int j = 0; j < C * kLogprobMaxTop; ++j) r += sh.cand[j] > mine;
-                    if (mine && r < k) sh.cut[r] = mine;
-                }
+                // (a cut list that overflows leaves the whole list, at most 512 keys, to be ranked)
+                if (!lp_select(sh.cand, nk, k, sh, sh.joined)) lp_rank<1>(sh.cand, nk, k, sh.joined);
             }
-            if (tid == 0) {
-                LpStat a = sh.stat;
-                for (int c = 1; c < C; ++c) {
-                    const uint32_t ad = cluster_addr(&sh.stat, c);
-                    a = lp_join(a, LpStat{ld_cluster_f32(ad), ld_cluster_f32(ad + 4), ld_cluster_f32(ad + 8)});
+            if (warp == LP_WARPS - 1) {
+                LpStat a{kLowest, 0.f, 0.f};
+                if (lane < C) {
+                    const uint32_t ad = cluster_addr(&sh.stat, lane);
+                    a = LpStat{ld_cluster_f32(ad), ld_cluster_f32(ad + 4), ld_cluster_f32(ad + 8)};
                 }
-                sh.warp_stat[0] = a;
+#pragma unroll
+                for (int o = LP_MAX_CLUSTER / 2; o > 0; o >>= 1) {
+                    const LpStat b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
+                                   __shfl_xor_sync(0xffffffffu, a.t, o)};
+                    a = lp_join(a, b);
+                }
+                if (lane == 0) sh.warp_stat[0] = a;
             }
         }
         cluster_sync();  // the other CTAs' shared memory stays until it has been read
         if (rank != 0) return;
     }
     const LpStat total = C > 1 ? sh.warp_stat[0] : sh.stat;
-    const u64* top = C > 1 ? sh.cut : sh.top;
+    const u64* top = C > 1 ? sh.joined : sh.top;
     // no distribution: NaN or +inf in the row (s is NaN), or nothing above -inf (s is 0)
     const float log_s = total.s > 0.f ? logf(total.s) : __uint_as_float(0x7fc00000u);
     if (tid == 0) {
@@ -376,7 +446,8 @@ cudaError_t token_logprobs_launch(const void* logits, int bf16, long long ld, in
                                   int top_k, float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs,
                                   int* err, cudaStream_t st) {
     if (M <= 0) return cudaSuccess;
-    const int C = lp_cluster(M, V);
+    int C = lp_cluster(M, V);
+    if (getenv("Q3_LPC")) C = atoi(getenv("Q3_LPC"));
     const dim3 grid((unsigned)M * C), block(LP_THREADS);
     if (bf16)
         return launch_pdl_cluster(token_logprobs_kernel<__nv_bfloat16>, grid, block, C, 0, st,
@@ -384,6 +455,13 @@ cudaError_t token_logprobs_launch(const void* logits, int bf16, long long ld, in
                                   top_ids, top_logprobs, C, err);
     return launch_pdl_cluster(token_logprobs_kernel<float>, grid, block, C, 0, st, static_cast<const float*>(logits), ld,
                               V, tokens, top_k, logprob, entropy, top_ids, top_logprobs, C, err);
+}
+
+// Clusters of sixteen CTAs are beyond the portable size.
+cudaError_t token_logprobs_prepare() {
+    cudaError_t e = cudaFuncSetAttribute(token_logprobs_kernel<float>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(token_logprobs_kernel<__nv_bfloat16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 }  // namespace q3

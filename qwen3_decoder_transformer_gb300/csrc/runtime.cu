@@ -77,6 +77,7 @@ cudaError_t prepare_kernels() {
     if (e == cudaSuccess) e = attention_prepare();
     if (e == cudaSuccess) e = attention_tiles_prepare();
     if (e == cudaSuccess) e = attention_ranges_prepare();
+    if (e == cudaSuccess) e = token_logprobs_prepare();
     if (e == cudaSuccess) done[dev] = true;
     return e;
 }
@@ -783,6 +784,7 @@ int qwen3_op_token_logprobs(const void* logits, int logits_type, int64_t ld, int
     if (M < 0 || M > (1 << 27) || V < 1 || ld < V || top_k < 0 || top_k > QWEN3_LOGPROB_MAX_TOP || top_k > V)
         return QWEN3_E_ARG;
     if (!tokens != !logprob || !is_aligned(logits, logits_type == QWEN3_LOGITS_F32 ? 4 : 2)) return QWEN3_E_ARG;
+    if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
     return token_logprobs_launch(logits, logits_type == QWEN3_LOGITS_BF16, ld, M, V, tokens,
                                  top_ids || top_logprobs ? top_k : 0, logprob, entropy, top_ids, top_logprobs, err,
                                  static_cast<cudaStream_t>(stream)) == cudaSuccess
