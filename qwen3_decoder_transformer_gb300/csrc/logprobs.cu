@@ -1,7 +1,6 @@
 // Log probabilities of given tokens, the entropy of each row's distribution and its largest alternatives,
 // in one pass over the logits.
 #include <algorithm>
-#include <cstdlib>
 
 #include "common.cuh"
 #include "internal.h"
@@ -23,16 +22,16 @@ namespace {
 // the way. The list is then cut by the same rule and ranked by counting. A slice whose list overflows, or
 // that holds NaN or +inf, is rescanned once per alternative.
 //
-// A cluster of C CTAs shares a row (C = 1 when the rows alone fill the SMs) and CTA 0 joins the parts
+// A cluster of C CTAs shares a row (C = 1 when there are rows enough) and CTA 0 joins the parts
 // through distributed shared memory: no workspace, one launch.
-// What bounds it: many rows, HBM (TIMES); few rows, the chain of a CTA (first loads, threshold, list, join).
-constexpr int LP_THREADS = 512;
-constexpr int LP_WARPS = LP_THREADS / 32;
-constexpr int LP_GROUPS = 64;           // groups of 8 threads whose maxima give the threshold
+// What bounds it. Many rows: HBM, 2048 x 151,936 fp32 with one alternative 197 us, 6.31 TB/s (93% of the measured copy);
+// bf16 has twice the elements a byte and is bound by their arithmetic, 124 us (5.0 TB/s), and with 32 alternatives by
+// the selection, 179. Few rows: the chain of a CTA, 8.0 us for one row of 151,936 with 20 alternatives (4.3 without:
+// launch, first loads, join), 12.7 for 64 rows with five (8.8 without).
+constexpr int LP_GROUPS = 64;           // groups of threads whose maxima give the threshold
 constexpr int LP_CAP = 2080;            // candidates of one CTA: a slice of fewer than 2048 + 14 elements fits whole
 constexpr int LP_CUT = 256, LP_RANK = 128;
 constexpr int LP_MAX_CLUSTER = 16;  // beyond the portable size
-static_assert(LP_THREADS == 8 * LP_GROUPS, "eight threads per group");
 
 using u64 = unsigned long long;
 
@@ -107,33 +106,35 @@ struct LpShared {
     u64 cut[LP_CUT];
     u64 groups[LP_GROUPS];
     u64 top[kLogprobMaxTop], joined[kLogprobMaxTop];
-    u64 warp_best[LP_WARPS];
+    u64 warp_best[16];
     u64 tau;
-    LpStat warp_stat[LP_WARPS];
+    LpStat warp_stat[16];
     LpStat stat;
     int n_cand, n_cut;
 };
 
-// The k-th largest of the 64 group maxima of the threads' keys (0 = no element). Eight threads count the rank of
-// each group's key.
+// The k-th largest of the 64 group maxima of the threads' keys (0 = no element). A group's threads share the count of
+// its key's rank.
+template <int THREADS>
 __device__ __forceinline__ u64 lp_threshold(u64 rep, int k, LpShared& sh) {
+    constexpr int P = THREADS / LP_GROUPS;  // threads of a group
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
+    for (int o = 1; o < P; o <<= 1) {
         const u64 other = __shfl_xor_sync(0xffffffffu, rep, o);
         rep = other > rep ? other : rep;
     }
-    const int grp = threadIdx.x >> 3, part = threadIdx.x & 7;
+    const int grp = threadIdx.x / P, part = threadIdx.x % P;
     if (part == 0) sh.groups[grp] = rep;
     __syncthreads();
     int rank = 0;
 #pragma unroll
-    for (int i = 0; i < LP_GROUPS / 8; ++i) {
-        const int j = i * 8 + part;
+    for (int i = 0; i < LP_GROUPS / P; ++i) {
+        const int j = i * P + part;
         const u64 o = sh.groups[j];
         rank += (o > rep) | ((o == rep) & (j < grp));
     }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    for (int o = 1; o < P; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
     if (part == 0 && rank == k - 1) sh.tau = rep;
     __syncthreads();
     return sh.tau;
@@ -141,7 +142,7 @@ __device__ __forceinline__ u64 lp_threshold(u64 rep, int k, LpShared& sh) {
 
 // out[r] = the r-th largest of list[0 .. n), r < k; the list's keys are distinct, 0 stands for no element. P threads
 // share the count of one key.
-template <int P>
+template <int P, int LP_THREADS>
 __device__ __forceinline__ void lp_rank(const u64* list, int n, int k, u64* out) {
     for (int i0 = 0; i0 < n; i0 += LP_THREADS / P) {
         const int i = i0 + threadIdx.x / P, part = threadIdx.x % P;
@@ -157,11 +158,12 @@ __device__ __forceinline__ void lp_rank(const u64* list, int n, int k, u64* out)
 
 // The k largest of list[0 .. n) into out, sorted; false when the cut list overflows. n is the same in every thread;
 // sh.n_cut is 0 on entry.
+template <int LP_THREADS>
 __device__ __forceinline__ bool lp_select(const u64* list, int n, int k, LpShared& sh, u64* out) {
     if (n > LP_RANK) {  // cut the list first
         u64 rep = 0;
         for (int i = threadIdx.x; i < n; i += LP_THREADS) rep = list[i] > rep ? list[i] : rep;
-        const u64 cut = lp_threshold(rep, k, sh);
+        const u64 cut = lp_threshold<LP_THREADS>(rep, k, sh);
         for (int i = threadIdx.x; i < n; i += LP_THREADS)
             if (list[i] >= cut && list[i]) {
                 const int at = atomicAdd(&sh.n_cut, 1);
@@ -173,20 +175,21 @@ __device__ __forceinline__ bool lp_select(const u64* list, int n, int k, LpShare
         if (n > LP_CUT) return false;
     }
     if (n <= LP_THREADS / 8)
-        lp_rank<8>(list, n, k, out);
+        lp_rank<8, LP_THREADS>(list, n, k, out);
     else if (n <= LP_THREADS / 4)
-        lp_rank<4>(list, n, k, out);
+        lp_rank<4, LP_THREADS>(list, n, k, out);
     else
-        lp_rank<2>(list, n, k, out);
+        lp_rank<2, LP_THREADS>(list, n, k, out);
     return true;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(LP_THREADS, 2)
+template <typename T, int LP_THREADS>
+__global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
     token_logprobs_kernel(const T* __restrict__ logits, long long ld, int V, const int32_t* __restrict__ tokens, int k,
                           float* __restrict__ logprob, float* __restrict__ entropy, int32_t* __restrict__ top_ids,
                           float* __restrict__ top_logprobs, int C, int* err) {
     using L = LpLoad<T>;
+    constexpr int LP_WARPS = LP_THREADS / 32;
     constexpr int EPV = L::EPV, U = 4;  // U vectors a thread and step
     __shared__ LpShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -217,6 +220,10 @@ __global__ void __launch_bounds__(LP_THREADS, 2)
         const int off = step * LP_THREADS + tid;
         if (u < U - 1) return u * span + off < n ? u * span + off : -1;
         return n - 1 - off >= (U - 1) * span ? n - 1 - off : -1;
+    };
+    auto index_of = [&](int step, int bit) -> int {  // index in the row of element bit % EPV of vector bit / EPV, or -1
+        const int v = vector_at(step, bit / EPV);
+        return v >= 0 ? base + v * EPV + bit % EPV : -1;
     };
     float m = kLowest;
     u64 tau = 0;
@@ -264,47 +271,49 @@ __global__ void __launch_bounds__(LP_THREADS, 2)
 #pragma unroll
         for (int u = 0; u < U; ++u) vmax[u] = L::largest(raw[u]);
         const float mx = fmax3(fmaxf(vmax[0], vmax[1]), vmax[2], vmax[3]);
+        // bit u * EPV + e: element e of vector u passes the test
+        auto which = [&](auto test) -> uint32_t {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[EPV];
+                L::unpack(raw[u], x);
+#pragma unroll
+                for (int e = 0; e < EPV; ++e)
+                    if (test(x[e])) bits |= 1u << (u * EPV + e);
+            }
+            return bits;
+        };
         if (k > 0) {
             if (step == 0) {  // threshold from the first elements read
-                u64 rep = 0;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (vmax[u] == mx) {
-                        const int v = vector_at(0, u);
-                        float x[EPV];
-                        L::unpack(raw[u], x);
-#pragma unroll
-                        for (int e = 0; e < EPV; ++e)
-                            if (v >= 0 && x[e] == mx) {
-                                const u64 key = lp_key(x[e], base + v * EPV + e);
-                                rep = key > rep ? key : rep;
-                            }
-                    }
+                const uint32_t at = which([&](float v) { return v == mx; });  // the lowest bit is the lowest index
+                const int idx = at ? index_of(step, __ffs(at) - 1) : -1;
+                const u64 rep = idx >= 0 ? lp_key(mx, idx) : 0;
                 __syncthreads();  // the list's counters are set
-                tau = lp_threshold(rep, k, sh);
+                tau = lp_threshold<LP_THREADS>(rep, k, sh);
                 tau_v = tau == 0 ? -INFINITY : lp_value(tau);
             } else if ((step == 3 || step == 8) && steps > 2 * step) {  // raise it from the list so far
                 __syncthreads();
                 const int nc = min(sh.n_cand, LP_CAP);
                 u64 rep = 0;
                 for (int i = tid; i < nc; i += LP_THREADS) rep = sh.cand[i] > rep ? sh.cand[i] : rep;
-                const u64 t = lp_threshold(rep, k, sh);
+                const u64 t = lp_threshold<LP_THREADS>(rep, k, sh);
                 if (t > tau) {
                     tau = t;
                     tau_v = lp_value(tau);
                 }
             }
-            if (mx >= tau_v) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (vmax[u] >= tau_v) {
-                        const int v = vector_at(step, u);
-                        float x[EPV];
-                        L::unpack(raw[u], x);
-#pragma unroll
-                        for (int e = 0; e < EPV; ++e)
-                            if (v >= 0 && x[e] >= tau_v) push(x[e], base + v * EPV + e);
+            if (mx >= tau_v) {  // a few elements of the row come here: read again unless it is the thread's largest
+                uint32_t hit = which([&](float v) { return v >= tau_v; });
+                if (__popc(hit) == 1) {
+                    const int idx = index_of(step, __ffs(hit) - 1);
+                    if (idx >= 0) push(mx, idx);
+                } else {
+                    for (; hit; hit &= hit - 1) {
+                        const int idx = index_of(step, __ffs(hit) - 1);
+                        if (idx >= 0) push(L::one(row + idx), idx);
                     }
+                }
             }
         }
         raise(mx);
@@ -349,7 +358,7 @@ __global__ void __launch_bounds__(LP_THREADS, 2)
     if (k > 0) {
         const int nc = sh.n_cand;
         bool rescan = nc > LP_CAP || sh.stat.s != sh.stat.s;
-        if (!rescan) rescan = !lp_select(sh.cand, nc, k, sh, sh.top);
+        if (!rescan) rescan = !lp_select<LP_THREADS>(sh.cand, nc, k, sh, sh.top);
         if (rescan) {  // one scan of the slice per alternative: the largest key below the previous one
             u64 prev = ~0ull;
             for (int r = 0; r < k; ++r) {
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(LP_THREADS, 2)
                 if (tid == 0) sh.n_cut = 0;
                 __syncthreads();
                 // (a cut list that overflows leaves the whole list, at most 512 keys, to be ranked)
-                if (!lp_select(sh.cand, nk, k, sh, sh.joined)) lp_rank<1>(sh.cand, nk, k, sh.joined);
+                if (!lp_select<LP_THREADS>(sh.cand, nk, k, sh, sh.joined)) lp_rank<1, LP_THREADS>(sh.cand, nk, k, sh.joined);
             }
             if (warp == LP_WARPS - 1) {
                 LpStat a{kLowest, 0.f, 0.f};
@@ -433,10 +442,13 @@ __global__ void __launch_bounds__(LP_THREADS, 2)
     }
 }
 
-// CTAs per row: as many as two CTAs on every SM take, while a slice keeps at least 4096 elements.
+// CTAs per row: as many as two on every SM take, while a slice keeps at least 4096 elements; clusters of eight and
+// sixteen only while they are few, since they wait for room in one part of the GPU (151,936 fp32 logits, five
+// alternatives: 16 rows by 4 CTAs 9.1 us, by 8 9.6, by 16 13.6; 4 rows 8.5, 7.9 and 7.2).
 int lp_cluster(int M, int V) {
     int c = 1;
-    while (c < LP_MAX_CLUSTER && (long long)M * c * 2 <= 2 * device_sm_count() && V / (2 * c) >= 4096) c *= 2;
+    while (c < LP_MAX_CLUSTER && (long long)M * c * 2 <= (c * 2 >= 8 ? 64 : 2 * device_sm_count()) && V / (2 * c) >= 4096)
+        c *= 2;
     return c;
 }
 
@@ -446,22 +458,35 @@ cudaError_t token_logprobs_launch(const void* logits, int bf16, long long ld, in
                                   int top_k, float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs,
                                   int* err, cudaStream_t st) {
     if (M <= 0) return cudaSuccess;
-    int C = lp_cluster(M, V);
-    if (getenv("Q3_LPC")) C = atoi(getenv("Q3_LPC"));
-    const dim3 grid((unsigned)M * C), block(LP_THREADS);
-    if (bf16)
-        return launch_pdl_cluster(token_logprobs_kernel<__nv_bfloat16>, grid, block, C, 0, st,
-                                  static_cast<const __nv_bfloat16*>(logits), ld, V, tokens, top_k, logprob, entropy,
-                                  top_ids, top_logprobs, C, err);
-    return launch_pdl_cluster(token_logprobs_kernel<float>, grid, block, C, 0, st, static_cast<const float*>(logits), ld,
-                              V, tokens, top_k, logprob, entropy, top_ids, top_logprobs, C, err);
+    // Many rows: CTAs of 256 threads, four an SM, so that one row's selection runs beside the others' loads (2048
+    // rows of 151,936 bf16 logits, one alternative 124 us against 137 with 512 threads, 32 alternatives 179
+    // against 212; fp32 198 and 197). Few rows: 512 threads, for a row's shorter chain (333 rows of 32,003 16.4 against
+    // 20.9, one row 8.0 against 9.2).
+    const int threads = M >= 8 * device_sm_count() ? 256 : 512;
+    const int C = lp_cluster(M, V);
+    const dim3 grid((unsigned)M * C), block(threads);
+    auto launch = [&](auto kernel, auto x) {
+        return launch_pdl_cluster(kernel, grid, block, C, 0, st, x, ld, V, tokens, top_k, logprob, entropy, top_ids,
+                                  top_logprobs, C, err);
+    };
+    if (bf16) {
+        const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(logits);
+        return threads == 512 ? launch(token_logprobs_kernel<__nv_bfloat16, 512>, x) : launch(token_logprobs_kernel<__nv_bfloat16, 256>, x);
+    }
+    const float* x = static_cast<const float*>(logits);
+    return threads == 512 ? launch(token_logprobs_kernel<float, 512>, x) : launch(token_logprobs_kernel<float, 256>, x);
 }
 
 // Clusters of sixteen CTAs are beyond the portable size.
 cudaError_t token_logprobs_prepare() {
-    cudaError_t e = cudaFuncSetAttribute(token_logprobs_kernel<float>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(token_logprobs_kernel<__nv_bfloat16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const void* fns[] = {(const void*)token_logprobs_kernel<float, 512>, (const void*)token_logprobs_kernel<float, 256>,
+                         (const void*)token_logprobs_kernel<__nv_bfloat16, 512>,
+                         (const void*)token_logprobs_kernel<__nv_bfloat16, 256>};
+    for (const void* f : fns) {
+        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace q3
