@@ -353,7 +353,8 @@ QWEN3_API int qwen3_op_greedy(const float* d_logits, int64_t ld, int B, int V, i
  * anything.
  * q [B, Hq, dh], out [B, Hq*dh] bf16; Hq / Hkv at most 8, dh 64 or 128, B at most 65535; q and caches
  * 16-byte aligned. d_work is scratch of qwen3_attention_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len)
- * bytes (0 when prefix_len is 0, then d_work may be NULL), 16-byte aligned; its contents on entry do not matter.
+ * bytes (0 when prefix_len is 0, then d_work may be NULL), 16-byte aligned; work_bytes is its size, and a smaller
+ * one is refused (E_ARG); its contents on entry do not matter.
  * Calls that share a d_work must not overlap on the GPU. Scores and sums are fp32, probabilities are rounded to
  * bf16 for the weighted sum. d_err (may be NULL) receives bit 2 if a bounded wait gave up. */
 QWEN3_API size_t qwen3_attention_decode_shared_workspace(int B, int Hq, int Hkv, int dh, int prefix_len);
@@ -361,7 +362,7 @@ QWEN3_API int qwen3_op_attention_decode_shared(const void* d_q, const void* d_k_
                                                int prefix_cap, int prefix_len, const void* d_k_cache,
                                                const void* d_v_cache, int B, int Hq, int Hkv, int dh, int cap,
                                                const int* d_len0, int len_stride, const int* d_seq_meta, void* d_work,
-                                               void* d_out, int* d_err, void* stream);
+                                               size_t work_bytes, void* d_out, int* d_err, void* stream);
 
 /* Attention with a sliding window and attention sinks: the token in slot i sees slots j <= i with
  * i - j < window or j < sinks (the first `sinks` tokens stay visible after the window has left them).

@@ -108,8 +108,8 @@ def lib() -> ctypes.CDLL:
     L.qwen3_op_token_logprobs.argtypes = [_vp, i, ctypes.c_int64, i, i, _vp, i, _vp, _vp, _vp, _vp, _vp, _vp]
     L.qwen3_attention_decode_shared_workspace.restype = sz
     L.qwen3_attention_decode_shared_workspace.argtypes = [i, i, i, i, i]
-    L.qwen3_op_attention_decode_shared.argtypes = [_vp, _vp, _vp, i, i, _vp, _vp, i, i, i, i, i, _vp, i, _vp, _vp, _vp,
-                                                   _vp, _vp]
+    L.qwen3_op_attention_decode_shared.argtypes = [_vp, _vp, _vp, i, i, _vp, _vp, i, i, i, i, i, _vp, i, _vp, _vp, sz,
+                                                   _vp, _vp, _vp]
     L.qwen3_attention_sink_rows.argtypes = [i]
     L.qwen3_op_attention_prefill_sinks.argtypes = [_vp, _vp, _vp, i, i, i, i, i, i, _vp, i, i, i, i, _vp, _vp, _vp]
     L.qwen3_op_attention_decode_sinks.argtypes = [_vp, _vp, _vp, i, i, i, i, i, _vp, i, i, i, i, _vp, _vp, _vp]
@@ -503,22 +503,20 @@ def op_attention_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, len0, wo
         _want(v_prefix is None and not prefix_len, "v_prefix and prefix_len go with k_prefix")
     if B == 0:
         return
-    fn = lib()
-    if n > 0:
-        need = fn.qwen3_attention_decode_shared_workspace(B, Hq, Hkv, dh, n)
-        _want(isinstance(work, torch.Tensor) and work.get_device() == dev and work.is_contiguous()
-              and work.numel() * work.element_size() >= need, "work must be contiguous scratch of the size that "
-              "attention_decode_shared_workspace gives, on the same device")
-        p_work = work.data_ptr()
+    size = 0
+    if n > 0:  # the library refuses scratch that is too small
+        _want(isinstance(work, torch.Tensor) and work.get_device() == dev and work.is_contiguous(),
+              "work must be contiguous scratch on the same device, of attention_decode_shared_workspace bytes")
+        p_work, size = work.data_ptr(), work.numel() * work.element_size()
     if seq_meta is not None:
         _dense("seq_meta", seq_meta, _I32, (2 + B,), dev)
         p_meta = seq_meta.data_ptr()
     if err is not None:
         _dense("err", err, _I32, (1,), dev)
         p_err = err.data_ptr()
-    _launch(fn.qwen3_op_attention_decode_shared,
+    _launch(lib().qwen3_op_attention_decode_shared,
             (q.data_ptr(), p_k, p_v, rows, n, k_cache.data_ptr(), v_cache.data_ptr(), B, Hq, Hkv, dh, cap,
-             len0.data_ptr(), stride, p_meta, p_work, out.data_ptr(), p_err), dev, stream)
+             len0.data_ptr(), stride, p_meta, p_work, size, out.data_ptr(), p_err), dev, stream)
 
 
 def attention_sink_rows(sinks) -> int:

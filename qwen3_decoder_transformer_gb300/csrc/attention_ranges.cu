@@ -271,27 +271,26 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
     uint8_t* ring_p = rings + warp * RG_BYTES;
     const uint32_t ring_a = smem_u32(ring_p);
     const int z = b * a.Hkv + j;
-    auto load = [&](int i) {  // lane 0
+    auto load = [&](int i, const CUtensorMap* map, uint64_t* full, int off) {  // lane 0: K or V of unit i
         int valid;
         const int y = unit(u0 + warp + NW * i, valid), st = i % ST;
-        uint8_t* dst = ring_p + st * 2 * Ly::HALF;
-        mbar_expect_tx(&k_full[st], Ly::HALF);
+        uint8_t* dst = ring_p + st * 2 * Ly::HALF + off;
+        mbar_expect_tx(&full[st], Ly::HALF);
 #pragma unroll
-        for (int c = 0; c < Ly::NCH; ++c) tma_load_3d(dst + c * Ly::BOX, &tmK, &k_full[st], c * 64, y, z);
-        mbar_expect_tx(&v_full[st], Ly::HALF);
-#pragma unroll
-        for (int c = 0; c < Ly::NCH; ++c)
-            tma_load_3d(dst + Ly::HALF + c * Ly::BOX, &tmV, &v_full[st], c * 64, y, z);
+        for (int c = 0; c < Ly::NCH; ++c) tma_load_3d(dst + c * Ly::BOX, map, &full[st], c * 64, y, z);
     };
     if (lane == 0)
-        for (int i = 0; i < min(ST, mine); ++i) load(i);
+        for (int i = 0; i < min(ST, mine); ++i) {
+            load(i, &tmK, k_full, 0);
+            load(i, &tmV, v_full, Ly::HALF);
+        }
 
     const float sl2 = kLog2e / sqrtf((float)DH);
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2 tq and 2 tq + 1
     float o[DH / 16][4];                                       // tile t: rows are dims 16 t + gq and 16 t + gq + 8
 #pragma unroll
     for (int t = 0; t < DH / 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    bool ok = true;
+    bool ok = true, k_ahead = false;  // k_ahead: the keys of unit i + ST are on their way
     int i = 0;
     for (; i < mine; ++i) {
         const int st = i % ST, ph = (i / ST) & 1;
@@ -309,6 +308,9 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[e] += d2[e];
+        __syncwarp();  // every lane has read the unit's keys: the next ones may come
+        k_ahead = i + ST < mine;
+        if (lane == 0 && k_ahead) load(i + ST, &tmK, k_full, 0);
         const bool in0 = gq < valid, in1 = gq + 8 < valid;
         const float v0 = in0 ? d[0] * sl2 : -INFINITY, v1 = in0 ? d[1] * sl2 : -INFINITY;
         const float v2 = in1 ? d[2] * sl2 : -INFINITY, v3 = in1 ? d[3] * sl2 : -INFINITY;
@@ -357,17 +359,17 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
             ldsm4_trans(rg_addr(va, vrow, 2 * t + ((lane >> 3) & 1)), f);
             mma_keys(o[t], f, b_lo, b_hi);
         }
-        __syncwarp();  // every lane has read the stage
-        if (lane == 0 && i + ST < mine) load(i + ST);
+        __syncwarp();
+        if (lane == 0 && k_ahead) load(i + ST, &tmV, v_full, Ly::HALF);
+        k_ahead = false;
     }
     if (!ok) {  // give up: wait, bounded, for the copies still on their way
         *abort_flag = 1;
         if (a.err && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
         int never = 0;
-        for (int r = i; r < min(i + ST, mine); ++r) {
-            mbar_wait_suspend(&k_full[r % ST], (r / ST) & 1, &never);
-            mbar_wait_suspend(&v_full[r % ST], (r / ST) & 1, &never);
-        }
+        for (int r = i; r < min(i + ST, mine); ++r) mbar_wait_suspend(&v_full[r % ST], (r / ST) & 1, &never);
+        for (int r = i; r < min(i + ST + 1, mine); ++r)
+            if (r < i + ST || k_ahead) mbar_wait_suspend(&k_full[r % ST], (r / ST) & 1, &never);
     }
 #pragma unroll
     for (int s = 4; s < 32; s <<= 1) {
@@ -544,9 +546,10 @@ int prefix_chunks(int B, int Hq, int Hkv, int dh, int P, int cap) {
     const long long tiles = (P + 127) / 128, items = (long long)row_tiles * Hkv;
     constexpr double hbm = 6.8e6, sm_rate = 0.055e6;  // bytes per us
     const double own = (double)B * Hkv * (cap / 2.0) * dh * 4, tile = 128.0 * dh * 4;
+    const int max_chunks = prefix_max_chunks(B, Hq, Hkv, P);
     int best = 1;
     double best_t = 0;
-    for (int c = 1; c <= prefix_max_chunks(B, Hq, Hkv, P); ++c) {
+    for (int c = 1; c <= max_chunks; ++c) {
         const long long n = items * c, rounds = (n + sms - 1) / sms;
         const double running = (double)std::min<long long>(n, sms);
         const double per_tile = std::max(0.9, running / row_tiles * tile / hbm);

@@ -1081,8 +1081,8 @@ size_t qwen3_attention_decode_shared_workspace(int B, int Hq, int Hkv, int dh, i
 
 int qwen3_op_attention_decode_shared(const void* q, const void* kp, const void* vp, int prefix_cap, int prefix_len,
                                      const void* kc, const void* vc, int B, int Hq, int Hkv, int dh, int cap,
-                                     const int* len0, int len_stride, const int* seq_meta, void* work, void* out, int* err,
-                                     void* stream) {
+                                     const int* len0, int len_stride, const int* seq_meta, void* work, size_t work_bytes,
+                                     void* out, int* err, void* stream) {
     if (!q || !kc || !vc || !len0 || !out || B < 0 || B > 65535 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv ||
         Hq / Hkv > 8 || (dh != 64 && dh != 128) || cap < 1 || (len_stride != 0 && len_stride != 1))
         return QWEN3_E_ARG;
@@ -1090,6 +1090,7 @@ int qwen3_op_attention_decode_shared(const void* q, const void* kp, const void* 
     const void* ptrs[] = {q, kc, vc, out, prefix_len > 0 ? kp : nullptr, prefix_len > 0 ? vp : nullptr, work};
     for (const void* p : ptrs)
         if (!is_aligned(p, 16)) return QWEN3_E_ARG;
+    if (B > 0 && work_bytes < attn_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len)) return QWEN3_E_ARG;
     if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
     return attn_decode_shared_launch(static_cast<const bf16*>(q), static_cast<const bf16*>(kp),
                                      static_cast<const bf16*>(vp), prefix_cap, prefix_len, static_cast<const bf16*>(kc),

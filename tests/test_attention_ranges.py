@@ -423,12 +423,14 @@ def test_library_refuses(bd):
     L = bd.lib()
     p, odd = ctypes.c_void_p(64), ctypes.c_void_p(72)  # never dereferenced
 
-    def shared(q=p, kp=p, vp=p, pc=100, P=100, kc=p, vc=p, B=2, Hq=8, Hkv=4, dh=64, cap=10, len0=p, st=0, work=p, out=p):
-        return L.qwen3_op_attention_decode_shared(q, kp, vp, pc, P, kc, vc, B, Hq, Hkv, dh, cap, len0, st, None, work, out,
-                                                  None, None)
+    def shared(q=p, kp=p, vp=p, pc=100, P=100, kc=p, vc=p, B=2, Hq=8, Hkv=4, dh=64, cap=10, len0=p, st=0, work=p, out=p,
+               size=1 << 30):
+        return L.qwen3_op_attention_decode_shared(q, kp, vp, pc, P, kc, vc, B, Hq, Hkv, dh, cap, len0, st, None, work, size,
+                                                  out, None, None)
     for kw in (dict(q=None), dict(kc=None), dict(vc=None), dict(len0=None), dict(out=None), dict(kp=None), dict(vp=None),
                dict(work=None), dict(P=101), dict(P=-1), dict(B=-1), dict(B=65536), dict(Hq=9), dict(Hq=36), dict(dh=96),
-               dict(cap=0), dict(st=2), dict(q=odd), dict(kp=odd), dict(vc=odd), dict(work=odd), dict(Hkv=0)):
+               dict(cap=0), dict(st=2), dict(q=odd), dict(kp=odd), dict(vc=odd), dict(work=odd), dict(Hkv=0),
+               dict(size=bd.attention_decode_shared_workspace(2, 8, 4, 64, 100) - 1)):
         assert shared(**kw) == 5, kw
     ws = bd.attention_decode_shared_workspace
     assert ws(2, 8, 4, 64, 0) == 0 and ws(0, 8, 4, 64, 10) == 0 and ws(2, 36, 4, 64, 10) == 0
