@@ -30,7 +30,7 @@ namespace {
 // launch, first loads, join), 12.7 for 64 rows with five (8.8 without).
 constexpr int LP_GROUPS = 64;           // groups of threads whose maxima give the threshold
 constexpr int LP_CAP = 2080;            // candidates of one CTA: a slice of fewer than 2048 + 14 elements fits whole
-constexpr int LP_CUT = 256, LP_RANK = 128;
+constexpr int LP_CUT = 256, LP_RANK = 128, kFill = 64;
 constexpr int LP_MAX_CLUSTER = 16;  // beyond the portable size
 
 using u64 = unsigned long long;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
     };
     float m = kLowest;
     u64 tau = 0;
-    float tau_v = -INFINITY;
+    float tau_v = kLowest;  // -inf stays out of the list: a row may hold little else
     auto push = [&](float v, int idx) {
         const u64 key = lp_key(v, idx);
         if (key >= tau) {
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
                 const u64 rep = idx >= 0 ? lp_key(mx, idx) : 0;
                 __syncthreads();  // the list's counters are set
                 tau = lp_threshold<LP_THREADS>(rep, k, sh);
-                tau_v = tau == 0 ? -INFINITY : lp_value(tau);
+                tau_v = tau == 0 ? kLowest : fmaxf(lp_value(tau), kLowest);
             } else if ((step == 3 || step == 8) && steps > 2 * step) {  // raise it from the list so far
                 __syncthreads();
                 const int nc = min(sh.n_cand, LP_CAP);
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
                 const u64 t = lp_threshold<LP_THREADS>(rep, k, sh);
                 if (t > tau) {
                     tau = t;
-                    tau_v = lp_value(tau);
+                    tau_v = fmaxf(lp_value(tau), kLowest);
                 }
             }
             if (mx >= tau_v) {  // a few elements of the row come here: read again unless it is the thread's largest
@@ -356,8 +356,20 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
 
     // this CTA's k largest, sorted, into sh.top (0 where the slice has fewer elements)
     if (k > 0) {
-        const int nc = sh.n_cand;
-        bool rescan = nc > LP_CAP || sh.stat.s != sh.stat.s;
+        const bool no_sum = sh.stat.s != sh.stat.s;
+        // fewer than k elements above -inf (a mask): the lowest indices of the others fill the list
+        const int first = rank == 0 ? 0 : base, end = rank == C - 1 ? V : base + n * EPV;
+        int nc = sh.n_cand;
+        for (int at = first; !no_sum && nc < k && at < end; at += kFill) {
+            __syncthreads();  // every thread has read the count
+            if (tid < kFill && at + tid < end && L::one(row + at + tid) == -INFINITY) {
+                const int slot = atomicAdd(&sh.n_cand, 1);
+                if (slot < LP_CAP) sh.cand[slot] = lp_key(-INFINITY, at + tid);
+            }
+            __syncthreads();
+            nc = sh.n_cand;
+        }
+        bool rescan = nc > LP_CAP || no_sum;
         if (!rescan) rescan = !lp_select<LP_THREADS>(sh.cand, nc, k, sh, sh.top);
         if (rescan) {  // one scan of the slice per alternative: the largest key below the previous one
             u64 prev = ~0ull;

@@ -1111,7 +1111,7 @@ int qwen3_op_attention_prefill_sinks(const void* q, const void* kc, const void* 
         return QWEN3_E_ARG;
     if (((long long)T + 127) / 128 * Hq * B > 0x7fffffff) return QWEN3_E_ARG;
     SinkMap sm;
-    if (!sink_map(window, sinks, rolling, cap, T, &sm)) return QWEN3_E_ARG;
+    if (T > cap || !sink_map(window, sinks, rolling, cap, T, &sm)) return QWEN3_E_ARG;
     if (!is_aligned(q, 16) || !is_aligned(kc, 16) || !is_aligned(vc, 16) || !is_aligned(out, 16)) return QWEN3_E_ARG;
     if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
     return attn_prefill_sinks_launch(static_cast<const bf16*>(q), static_cast<const bf16*>(kc),

@@ -451,6 +451,7 @@ def test_library_refuses(bd):
         for decode in (True, False):
             assert sinks(decode, **kw) == 5, (decode, kw)
     assert sinks(False, window=382, T=4) == 5  # ring of 384 < window + T - 1
+    assert sinks(False, T=513, roll=0) == 5
     assert sinks(False, T=-1) == 5 and sinks(False, T=2 ** 30, B=64, roll=0) == 5
     assert sinks(True, Hq=36) == 5 and sinks(True, B=65536) == 5
     assert bd.attention_sink_rows(0) == 0 and bd.attention_sink_rows(1) == 128 and bd.attention_sink_rows(129) == 256

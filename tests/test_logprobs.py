@@ -135,6 +135,25 @@ def test_rows_without_a_distribution(bd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,V", [(2, 40), (1, 30011), (70, 30011), (400, 5003)])
+def test_masked_rows(bd, dtype, M, V):
+    """Rows in which a mask leaves fewer tokens than alternatives are asked for (none, one, a few, scattered or at the ends):
+    the alternatives go on with the masked tokens in index order."""
+    k = 20
+    g = torch.Generator().manual_seed(V + M)
+    full = torch.full((M, V), float("-inf"))
+    for r in range(M):
+        n = [1, 2, 7, 19, 20, 21, 3][r % 7]
+        at = torch.randperm(V, generator=g)[:n] if r % 3 else torch.arange(V - n, V)
+        full[r, at] = torch.randn(n, generator=g) * 5
+    full = full.to(dtype)
+    tokens = full.float().argmax(1).int()
+    got = _run(bd, full.cuda(), tokens.cuda(), k)
+    _check(got, _ref(full.float(), tokens, k), V)
+
+
+@pytest.mark.gpu
 def test_bad_tokens_flagged(bd):
     x = torch.randn(4, 1000, generator=torch.Generator().manual_seed(4))
     tokens = torch.tensor([0, -1, 1000, 999], dtype=torch.int32)
