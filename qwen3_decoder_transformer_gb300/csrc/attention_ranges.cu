@@ -1,9 +1,10 @@
 // Decode attention over key ranges: a sliding window with sink tokens, and a batch that shares a prefix.
 //
 // attn_ranges_kernel serves one query per (sequence, query head) over the visible keys of its sequence; a
-// cluster of CTAs shares the keys of one (sequence, kv head). The prefix form of the persistent prefill kernel
-// computes the part of a shared prefix for the query rows of the whole batch at once and leaves one partial
-// result per query row and key chunk, which attn_ranges_kernel joins to the sequence's own keys.
+// cluster of CTAs shares the keys of one (sequence, kv head). For a shared prefix, attn_prefix_launch
+// (attention_tiles.cu) computes its part for the query rows of the whole batch at once and leaves one record per row
+// tile and key chunk; attn_ranges_kernel works on the sequences' own keys beside it and joins the records, or
+// attn_join_kernel does.
 #include <algorithm>
 
 #include "common.cuh"
@@ -26,6 +27,11 @@ namespace {
 // (movmatrix), O^T (head_dim x heads) += V^T P^T.
 // Scores of rows behind a run are masked, and their value rows are zeroed in shared memory, so nothing
 // stored in a hidden row can reach the result.
+// What bounds it. Many sequences: HBM, 64 sequences x 4,100 keys of 8 kv heads, dh 128 (1.08 GB) 151 us from call to call
+// (part of the keys still in L2), 158 us with a cold L2 under ncu, 6.8 TB/s (100% of the measured copy rate). Fragments loaded
+// straight from global memory, without rings, took 219 us for any split: too little on its way per warp. One
+// sequence: the chain of launch, length, first boxes and joins, 9.6 us for 4,100 keys by clusters of 16 CTAs
+// (14.5 by 4).
 constexpr int RG_KEYS = 16, RG_MAX_CLUSTER = 16, RG_MAX_G = 8, RG_WARPS = 4, RG_THREADS = 32 * RG_WARPS;
 constexpr int RG_MAX_PARTS = RG_MAX_CLUSTER + kPrefixMaxChunks;
 template <int DH, int RING>
@@ -525,27 +531,24 @@ cudaError_t ranges_prepare() {
     return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, RgLayout<DH, RING>::SMEM);
 }
 
-}  // namespace
-
-namespace {
-
 // Key chunks of the prefix. The prefix kernel runs one CTA an SM, the own keys' CTAs run on the SMs it leaves, so
 // fewer chunks than SMs can pay: the estimate (us, on the measured rates) is the prefix kernel's time or, if it is
 // longer, the time to read everything, plus what is left of the own keys when the prefix kernel ends.
 // An item of the prefix kernel takes 0.9 us a key tile (its softmax warps), more when its SM's share of HBM is the
 // limit (the row tiles of a chunk share its keys), and 4.5 us for its start and end; an SM's own CTAs read 55 GB/s;
-// a join launch takes 2.5 us; half of the own cache is taken to be filled.
+// a join launch takes 2.5 us; half of the own cache is taken to be filled. (Measured, 64 sequences: 32768 keys, 8B
+// heads, 512 own keys on average, 6 chunks 50 us, 9 chunks 57; 4096 keys, 0.6B heads, 256 own keys, 3 chunks 15.5, 19 chunks 22.)
 constexpr int kPrefixMaxRounds = 2;
 int prefix_max_chunks(int B, int Hq, int Hkv, int P) {
-    const long long tiles = (P + 127) / 128, items = (long long)prefix_row_tiles(B, Hq / Hkv) * Hkv;
+    const long long tiles = (P + 127ll) / 128, items = (long long)prefix_row_tiles(B, Hq / Hkv) * Hkv;
     return (int)std::max<long long>(
         1, std::min<long long>(std::min<long long>(tiles, kPrefixMaxChunks), kPrefixMaxRounds * device_sm_count() / items));
 }
-int prefix_chunks(int B, int Hq, int Hkv, int dh, int P, int cap) {
+int prefix_chunks(int B, int Hq, int Hkv, int dh, int P, int own_cap) {
     const int row_tiles = prefix_row_tiles(B, Hq / Hkv), sms = device_sm_count();
-    const long long tiles = (P + 127) / 128, items = (long long)row_tiles * Hkv;
+    const long long tiles = (P + 127ll) / 128, items = (long long)row_tiles * Hkv;
     constexpr double hbm = 6.8e6, sm_rate = 0.055e6;  // bytes per us
-    const double own = (double)B * Hkv * (cap / 2.0) * dh * 4, tile = 128.0 * dh * 4;
+    const double own = (double)B * Hkv * (own_cap / 2.0) * dh * 4, tile = 128.0 * dh * 4;
     const int max_chunks = prefix_max_chunks(B, Hq, Hkv, P);
     int best = 1;
     double best_t = 0;
@@ -592,7 +595,8 @@ cudaError_t attn_decode_shared_launch(const __nv_bfloat16* q, const __nv_bfloat1
     a.meta = meta;
     int free_sms = 0;
     if (P > 0) {
-        a.nrec = prefix_chunks(B, Hq, Hkv, dh, P, cap);
+        // with a layout the first slots of the own caches are the prefix
+        a.nrec = prefix_chunks(B, Hq, Hkv, dh, P, meta ? std::max(0, cap - P) : cap);
         a.row_tiles = prefix_row_tiles(B, a.G);
         a.recs = work;
         a.own = work + prefix_rec_floats(dh) * a.row_tiles * Hkv * a.nrec;

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
             it.b = k % a.row_tiles;  // row tile
             it.h = k / a.row_tiles % Hkv;
             it.chunk = k / (a.row_tiles * Hkv);
-            const long long tiles = (T + TL_BN - 1) / TL_BN;
+            const long long tiles = ((long long)T + TL_BN - 1) / TL_BN;
             it.skip = (int)(tiles * it.chunk / a.chunks);
             it.n_tiles = (int)(tiles * (it.chunk + 1) / a.chunks) - it.skip;
         } else {
