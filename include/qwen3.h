@@ -349,10 +349,9 @@ QWEN3_API int qwen3_op_greedy(const float* d_logits, int64_t ld, int B, int V, i
  * cap - 1); with no prefix either the row's output is zeros. d_seq_meta (may be NULL) is the layout of
  * qwen3_op_attention_decode: own slots below psh are skipped (they are the prefix), padding slots
  * [ps, ps + pad_b) are hidden. After qwen3_share_prefix the call is: the prefix is sequence 0's cache,
- * prefix_len = psh, prefix_cap = cap. Hidden slots may hold
- * anything.
- * q [B, Hq, dh], out [B, Hq*dh] bf16; Hq / Hkv at most 8, dh 64 or 128, B at most 65535; q and caches
- * 16-byte aligned. d_work is scratch of qwen3_attention_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len)
+ * prefix_len = psh, prefix_cap = cap. Hidden slots may hold anything.
+ * q [B, Hq, dh], out [B, Hq*dh] bf16; Hq / Hkv at most 8, dh 64 or 128, B at most 65535, cap and prefix_len at most
+ * 2^30; q and caches 16-byte aligned. d_work is scratch of qwen3_attention_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len)
  * bytes (0 when prefix_len is 0, then d_work may be NULL), 16-byte aligned; work_bytes is its size, and a smaller
  * one is refused (E_ARG); its contents on entry do not matter.
  * Calls that share a d_work must not overlap on the GPU. Scores and sums are fp32, probabilities are rounded to
@@ -379,7 +378,8 @@ QWEN3_API int qwen3_op_attention_decode_shared(const void* d_q, const void* d_k_
  * rows that do not see them); rows that none sees may hold anything.
  * Decode: the form for one token per sequence, q [B, Hq, dh], out [B, Hq*dh], Hq / Hkv at most 8, B at most
  * 65535; hidden rows may hold anything; a sequence with a negative length gets zeros. Neither needs a workspace.
- * window >= 1, sinks >= 0, dh 64 or 128, 16-byte aligned tensors. d_err (may be NULL) as for
+ * window >= 1, sinks >= 0, dh 64 or 128, cap at most 2^30 and lengths too (a longer one counts as 2^30), 16-byte
+ * aligned tensors. d_err (may be NULL) as for
  * qwen3_op_attention_prefill. */
 QWEN3_API int qwen3_attention_sink_rows(int sinks);
 QWEN3_API int qwen3_op_attention_prefill_sinks(const void* d_q, const void* d_k_cache, const void* d_v_cache, int B,

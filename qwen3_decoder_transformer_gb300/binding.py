@@ -420,6 +420,7 @@ def op_token_logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=N
     dev = logits.get_device()
     ld, unit = logits.stride()
     _want(V >= 1 and (V == 1 or unit == 1), "logits must be dense along the vocabulary")
+    _want(M <= 1 << 27 and V < 1 << 31, "at most 2^27 rows of fewer than 2^31 logits")
     if M <= 1:
         ld = V
     _want(ld >= V, "rows of the logits overlap")
@@ -519,9 +520,15 @@ def op_attention_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, len0, wo
              len0.data_ptr(), stride, p_meta, p_work, size, out.data_ptr(), p_err), dev, stream)
 
 
+def _int32(v) -> int:
+    """v, or the nearest 32-bit integer, for the library to refuse or to take as no limit (a plain conversion would
+    drop its upper bits)."""
+    return v if -1 << 31 <= v < 1 << 31 else (1 << 31) - 1 if v > 0 else -1 << 31
+
+
 def attention_sink_rows(sinks) -> int:
     """Cache rows in front of the ring of a rolling buffer with this many sink tokens."""
-    return lib().qwen3_attention_sink_rows(sinks)
+    return lib().qwen3_attention_sink_rows(_int32(sinks))
 
 
 def op_attention_prefill_sinks(q, k_cache, v_cache, len0, out, window, sinks, rolling=False, err=None, stream=None):
@@ -542,7 +549,7 @@ def op_attention_prefill_sinks(q, k_cache, v_cache, len0, out, window, sinks, ro
         return
     _launch(lib().qwen3_op_attention_prefill_sinks,
             (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, T, Hq, Hkv, dh, cap, len0.data_ptr(), stride,
-             window, sinks, 1 if rolling else 0, out.data_ptr(), p_err), dev, stream)
+             _int32(window), _int32(sinks), 1 if rolling else 0, out.data_ptr(), p_err), dev, stream)
 
 
 def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rolling=False, err=None, stream=None):
@@ -561,5 +568,5 @@ def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rol
     if B == 0:
         return
     _launch(lib().qwen3_op_attention_decode_sinks,
-            (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, Hq, Hkv, dh, cap, len0.data_ptr(), stride, window,
-             sinks, 1 if rolling else 0, out.data_ptr(), p_err), dev, stream)
+            (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, Hq, Hkv, dh, cap, len0.data_ptr(), stride,
+             _int32(window), _int32(sinks), 1 if rolling else 0, out.data_ptr(), p_err), dev, stream)

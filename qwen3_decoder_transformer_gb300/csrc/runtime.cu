@@ -459,13 +459,16 @@ int ensure_generation_buffers(qwen3_ctx* c) {
     return QWEN3_OK;
 }
 
+// Longest cache of the operators over key ranges: slot numbers and sums of two of them stay within 31 bits.
+constexpr int kMaxSlots = 1 << 30;
+
 // Window and sinks of a call of T tokens on a cache of cap rows; false when they do not fit.
 bool sink_map(int window, int sinks, int rolling, int cap, int T, SinkMap* sm) {
     if (window < 1 || sinks < 0 || (rolling != 0 && rolling != 1)) return false;
-    // slots past the cache do not exist, so a longer window or more sinks than 2^29 say nothing new
-    *sm = SinkMap{std::min(window, 1 << 29), std::min(sinks, 1 << 29), 0, 0};
+    // slots past the cache do not exist, so a longer window or more sinks than it has say nothing new
+    *sm = SinkMap{std::min(window, cap), std::min(sinks, cap), 0, 0};
     if (!rolling) return true;
-    if (window > (1 << 29) || sinks > (1 << 29)) return false;
+    if (window > cap || sinks > cap) return false;
     sm->sink_rows = (sinks + 127) / 128 * 128;
     sm->ring = cap - sm->sink_rows;
     // the ring holds the window of the call's first token and every token of the call
@@ -1087,6 +1090,7 @@ int qwen3_op_attention_decode_shared(const void* q, const void* kp, const void* 
         Hq / Hkv > 8 || (dh != 64 && dh != 128) || cap < 1 || (len_stride != 0 && len_stride != 1))
         return QWEN3_E_ARG;
     if (prefix_len < 0 || prefix_len > prefix_cap || (prefix_len > 0 && (!kp || !vp || !work))) return QWEN3_E_ARG;
+    if (cap > kMaxSlots || prefix_len > kMaxSlots) return QWEN3_E_ARG;
     const void* ptrs[] = {q, kc, vc, out, prefix_len > 0 ? kp : nullptr, prefix_len > 0 ? vp : nullptr, work};
     for (const void* p : ptrs)
         if (!is_aligned(p, 16)) return QWEN3_E_ARG;
@@ -1111,7 +1115,7 @@ int qwen3_op_attention_prefill_sinks(const void* q, const void* kc, const void* 
         return QWEN3_E_ARG;
     if (((long long)T + 127) / 128 * Hq * B > 0x7fffffff) return QWEN3_E_ARG;
     SinkMap sm;
-    if (T > cap || !sink_map(window, sinks, rolling, cap, T, &sm)) return QWEN3_E_ARG;
+    if (T > cap || cap > kMaxSlots || !sink_map(window, sinks, rolling, cap, T, &sm)) return QWEN3_E_ARG;
     if (!is_aligned(q, 16) || !is_aligned(kc, 16) || !is_aligned(vc, 16) || !is_aligned(out, 16)) return QWEN3_E_ARG;
     if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
     return attn_prefill_sinks_launch(static_cast<const bf16*>(q), static_cast<const bf16*>(kc),
@@ -1128,7 +1132,7 @@ int qwen3_op_attention_decode_sinks(const void* q, const void* kc, const void* v
         Hq / Hkv > 8 || (dh != 64 && dh != 128) || cap < 1 || (len_stride != 0 && len_stride != 1))
         return QWEN3_E_ARG;
     SinkMap sm;
-    if (!sink_map(window, sinks, rolling, cap, 1, &sm)) return QWEN3_E_ARG;
+    if (cap > kMaxSlots || !sink_map(window, sinks, rolling, cap, 1, &sm)) return QWEN3_E_ARG;
     if (!is_aligned(q, 16) || !is_aligned(kc, 16) || !is_aligned(vc, 16) || !is_aligned(out, 16)) return QWEN3_E_ARG;
     if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
     return attn_decode_sinks_launch(static_cast<const bf16*>(q), static_cast<const bf16*>(kc),

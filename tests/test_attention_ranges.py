@@ -311,6 +311,35 @@ def test_sinks_prefill_without_sinks_is_the_windowed_prefill(bd):
 
 
 @gpu
+def test_sinks_windows_past_32_bits(bd):
+    """A window or a number of sinks that no 32-bit integer holds is a limit that hides nothing, not its lower bits."""
+    g = _gen(15)
+    Bn, Hq, Hkv, dh, T, cap = 1, 4, 2, 64, 140, 500
+    q, k, v = _normal(g, Bn, Hq, T, dh), _normal(g, Bn, Hkv, cap, dh), _normal(g, Bn, Hkv, cap, dh)
+    len0 = torch.tensor([cap - T], dtype=torch.int32, device="cuda")
+    outs = []
+    for window, sinks in ((cap, 0), (2 ** 33 + 3, 0), (2 ** 31, 0), (3, 2 ** 40)):
+        o = torch.empty(Bn * T, Hq * dh, dtype=torch.bfloat16, device="cuda")
+        d = torch.empty(Bn, Hq * dh, dtype=torch.bfloat16, device="cuda")
+        bd.op_attention_prefill_sinks(q, k, v, len0, o, window, sinks)
+        bd.op_attention_decode_sinks(q[:, :, 0].contiguous(), k, v, len0, d, window, sinks)
+        outs.append((o, d))
+    torch.cuda.synchronize()
+    G = Hq // Hkv
+    for h in range(Hkv):
+        for t in (0, T - 1):
+            n = cap - T + t + 1
+            ref, spread = _attend(q[0, h * G:(h + 1) * G, t], k[0, h, :n], v[0, h, :n])
+            for o, d in outs:
+                _close(o.reshape(T, Hq, dh)[t, h * G:(h + 1) * G], ref, spread)
+                if t == 0:
+                    _close(d.reshape(Hq, dh)[h * G:(h + 1) * G], ref, spread)
+    for window, sinks in ((5 - 2 ** 32, 0), (5, 3 - 2 ** 32)):
+        with pytest.raises(bd.Qwen3Error):
+            bd.op_attention_prefill_sinks(q, k, v, len0, o, window, sinks)
+
+
+@gpu
 def test_sinks_captured_and_repeatable(bd):
     g = _gen(12)
     Bn, Hq, Hkv, dh, window, sinks = 2, 32, 8, 128, 1000, 4
@@ -450,6 +479,9 @@ def test_library_refuses(bd):
                dict(window=2 ** 30, cap=2 ** 30)):
         for decode in (True, False):
             assert sinks(decode, **kw) == 5, (decode, kw)
+    for decode in (True, False):  # slot numbers past 2^30
+        assert sinks(decode, roll=0, cap=2 ** 30 + 1) == 5 and sinks(decode, cap=2 ** 30 + 128) == 5
+    assert shared(cap=2 ** 30 + 1) == 5 and shared(P=2 ** 30 + 1, pc=2 ** 30 + 1) == 5
     assert sinks(False, window=382, T=4) == 5  # ring of 384 < window + T - 1
     assert sinks(False, T=513, roll=0) == 5
     assert sinks(False, T=-1) == 5 and sinks(False, T=2 ** 30, B=64, roll=0) == 5

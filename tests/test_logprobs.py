@@ -261,6 +261,8 @@ def test_binding_refuses(bd):
            dict(top_ids=ids, top_logprobs=torch.zeros(2, 4)), dict(logprob=torch.zeros(4)[::2]),
            dict(logits=x.expand(2, 10)[:1].expand(2, 10)), dict(err=torch.zeros(2, dtype=torch.int32)),
            {}]  # the last: host tensors
+    with pytest.raises(ValueError, match="2\\^27"):  # sizes past the library's integers
+        bd.op_token_logprobs(torch.empty((1 << 32) + 1, 1, device="meta"), entropy=lp)
     for change in bad:
         kw = dict(logits=x, tokens=t, logprob=lp)
         kw.update(change)
