@@ -154,6 +154,29 @@ def test_masked_rows(bd, dtype, M, V):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 30, 1300])
+@pytest.mark.parametrize("kind", ["lowest", "zero", "levels"])
+def test_ties_at_the_threshold(bd, dtype, M, kind):
+    """Most of a row has one value, by a mask of the type's lowest value or otherwise, and it is the last alternatives'
+    value too: its tokens follow in index order, from wherever in the row they start."""
+    V, k = 20011, 20
+    g = torch.Generator().manual_seed(M)
+    low = {"lowest": torch.finfo(dtype).min, "zero": -0.0, "levels": -2.0}[kind]
+    full = torch.full((M, V), low, dtype=dtype)
+    for r in range(M):
+        n = [0, 1, 5, 19, 20, 21][r % 6]
+        at = torch.randperm(V, generator=g)[:n] if r % 2 else torch.arange(V - n, V)
+        full[r, at] = (torch.randn(n, generator=g).abs() + 1).to(dtype)
+        if kind == "levels":  # the ties start late, behind lower values
+            full[r, :[0, 9000, 19950][r % 3]] = -3.0
+        if kind == "zero":  # both zeros are one value
+            full[r, ::7] = full[r, ::7].clamp(min=0.0) + 0.0
+    tokens = full.float().argmax(1).int()
+    _check(_run(bd, full.cuda(), tokens.cuda(), k), _ref(full.float(), tokens, k), V)
+
+
+@pytest.mark.gpu
 def test_bad_tokens_flagged(bd):
     x = torch.randn(4, 1000, generator=torch.Generator().manual_seed(4))
     tokens = torch.tensor([0, -1, 1000, 999], dtype=torch.int32)
