@@ -371,21 +371,21 @@ def op_greedy(logits, next_ids, stop_id=-1, done=None, work="auto", stream=None)
 
 # The operators below check their tensors: a wrong type, shape, layout or device raises ValueError before anything
 # is launched (sizes that the library itself refuses raise Qwen3Error). A decode step calls them in a launch-bound
-# loop, so the checks are plain comparisons and the messages are built only when one fails.
+# loop, so a call's tensors are compared in one expression, and what is wrong is worked out only when that fails.
+
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+
 
 def _want(ok, what: str):
     if not ok:
         raise ValueError(what)
 
 
-_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
-
-
-def _dense(name, t, dtype, shape, device: int):
-    """t is a contiguous tensor of this type and shape on CUDA device `device` (-1: the host)."""
+def _dense(name, t, dtype, shape, device: int) -> int:
+    """Address of t, which must be a contiguous tensor of this type and shape on CUDA device `device` (-1: the host)."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device
             and t.is_contiguous()):
-        return
+        return t.data_ptr()
     got = (f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}" if isinstance(t, torch.Tensor)
            else type(t).__name__)
     raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on CUDA device {device}, not {got}")
@@ -393,8 +393,9 @@ def _dense(name, t, dtype, shape, device: int):
 
 def _launch(fn, args, device: int, stream):
     """Call an entry point with `device` as the current CUDA device, on its current stream unless one is given."""
-    _want(device >= 0, "the tensors must be on a CUDA device")
-    if stream is None and torch.cuda.current_device() == device:
+    if device < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if stream is None and torch._C._cuda_getDevice() == device:
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         _want(stream is None or stream.device.index == device, "the stream belongs to another device")
@@ -413,65 +414,80 @@ def op_token_logprobs(logits, tokens=None, logprob=None, entropy=None, top_ids=N
     each row's entropy (nats) into entropy [M], and its largest alternatives, largest first, into top_ids [M, k] int32
     and top_logprobs [M, k]; outputs are fp32, and those left out are not computed. err: device int (bit 1: a token id
     outside the vocabulary)."""
-    _want(isinstance(logits, torch.Tensor) and logits.dim() == 2, "logits must be a tensor [M, V]")
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a tensor [M, V]")
     f32 = logits.dtype is _F32
-    _want(f32 or logits.dtype is _BF16, "logits must be fp32 or bf16")
+    if not f32 and logits.dtype is not _BF16:
+        raise ValueError("logits must be fp32 or bf16")
     M, V = logits.shape
     dev = logits.get_device()
     ld, unit = logits.stride()
-    _want(V >= 1 and (V == 1 or unit == 1), "logits must be dense along the vocabulary")
-    _want(M <= 1 << 27 and V < 1 << 31, "at most 2^27 rows of fewer than 2^31 logits")
+    if V < 1 or (V > 1 and unit != 1):
+        raise ValueError("logits must be dense along the vocabulary")
+    if M > 1 << 27 or V >= 1 << 31:
+        raise ValueError("at most 2^27 rows of fewer than 2^31 logits")
     if M <= 1:
         ld = V
-    _want(ld >= V, "rows of the logits overlap")
-    _want((tokens is None) == (logprob is None), "tokens and logprob go together")
+    if ld < V:
+        raise ValueError("rows of the logits overlap")
+    if (tokens is None) != (logprob is None):
+        raise ValueError("tokens and logprob go together")
     k = 0
     if top_ids is not None or top_logprobs is not None:
         t = top_logprobs if top_ids is None else top_ids
-        _want(isinstance(t, torch.Tensor) and t.dim() == 2, "top_ids and top_logprobs must be tensors [M, k]")
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError("top_ids and top_logprobs must be tensors [M, k]")
         k = t.shape[1]
-        _want(k <= V and k <= LOGPROB_MAX_TOP, "at most 32 alternatives, and no more than the vocabulary")
+        if k > V or k > LOGPROB_MAX_TOP:
+            raise ValueError("at most 32 alternatives, and no more than the vocabulary")
+    row, top = (M,), (M, k)
     p_tok = p_lp = p_ent = p_ids = p_tops = p_err = None
     if tokens is not None:
-        _dense("tokens", tokens, _I32, (M,), dev)
-        _dense("logprob", logprob, _F32, (M,), dev)
-        p_tok, p_lp = tokens.data_ptr(), logprob.data_ptr()
+        p_tok = _dense("tokens", tokens, _I32, row, dev)
+        p_lp = _dense("logprob", logprob, _F32, row, dev)
     if entropy is not None:
-        _dense("entropy", entropy, _F32, (M,), dev)
-        p_ent = entropy.data_ptr()
+        p_ent = _dense("entropy", entropy, _F32, row, dev)
     if top_ids is not None:
-        _dense("top_ids", top_ids, _I32, (M, k), dev)
-        p_ids = top_ids.data_ptr()
+        p_ids = _dense("top_ids", top_ids, _I32, top, dev)
     if top_logprobs is not None:
-        _dense("top_logprobs", top_logprobs, _F32, (M, k), dev)
-        p_tops = top_logprobs.data_ptr()
+        p_tops = _dense("top_logprobs", top_logprobs, _F32, top, dev)
     if err is not None:
-        _dense("err", err, _I32, (1,), dev)
-        p_err = err.data_ptr()
+        p_err = _dense("err", err, _I32, (1,), dev)
     if M == 0:
         return
     _launch(lib().qwen3_op_token_logprobs,
             (logits.data_ptr(), 0 if f32 else 1, ld, M, V, p_tok, k, p_lp, p_ent, p_ids, p_tops, p_err), dev, stream)
 
 
-def _caches(k_cache, v_cache, B, Hq, dh, device):
-    """Check a pair of caches [B, Hkv, cap, dh] of a call with Hq query heads; returns (Hkv, cap)."""
+def _attention_tensors(q, what, k_cache, v_cache, len0, out, out_shape, dev):
+    """Check the tensors of an attention call: q (its shape as `what` says), caches [B, Hkv, cap, dh], len0 [1] (one
+    length for all) or [B], out of out_shape. Returns Hkv, cap and the library's len_stride."""
+    try:
+        shape = k_cache.shape
+        n, = len0.shape
+        B, Hkv, cap, dh = shape
+        if (q.dtype is _BF16 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16 and out.dtype is _BF16
+                and len0.dtype is _I32 and v_cache.shape == shape and out.shape == out_shape
+                and B == q.shape[0] and dh == q.shape[-1] and (n == 1 or n == B) and Hkv >= 1 and cap >= 1
+                and q.shape[1] % Hkv == 0 and k_cache.get_device() == dev and v_cache.get_device() == dev
+                and out.get_device() == dev and len0.get_device() == dev and q.is_contiguous()
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and out.is_contiguous() and len0.is_contiguous()):
+            return Hkv, cap, 0 if n == 1 else 1
+    except (AttributeError, ValueError):  # not tensors, or not of these numbers of dimensions
+        pass
+    _dense(f"q {what}", q, _BF16, q.shape, dev)
     _want(isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4, "k_cache must be a tensor [B, Hkv, cap, dh]")
-    _, Hkv, cap, _ = shape = k_cache.shape
-    _want(shape[0] == B and shape[3] == dh, "the caches do not match the queries' batch and head_dim")
-    _want(Hkv >= 1 and cap >= 1 and Hq % Hkv == 0, "query heads must be a multiple of kv heads, with at least one slot")
-    _dense("k_cache", k_cache, _BF16, shape, device)
-    _dense("v_cache", v_cache, _BF16, shape, device)
-    return Hkv, cap
-
-
-def _lengths(len0, B, device) -> int:
-    """Check len0 [1] (one length for all) or [B]; returns the library's len_stride."""
-    _want(isinstance(len0, torch.Tensor) and len0.dim() == 1, "len0 must be a tensor [1] or [B]")
-    n = len0.shape[0]
-    _want(n == 1 or n == B, "len0 must hold one length, or one per sequence")
-    _dense("len0", len0, _I32, (n,), device)
-    return 0 if n == 1 else 1
+    shape = k_cache.shape
+    _want(shape[0] == q.shape[0] and shape[3] == q.shape[-1], "the caches do not match the queries' batch and head_dim")
+    _want(shape[1] >= 1 and shape[2] >= 1 and q.shape[1] % shape[1] == 0,
+          "query heads must be a multiple of kv heads, with at least one slot")
+    _dense("k_cache", k_cache, _BF16, shape, dev)
+    _dense("v_cache", v_cache, _BF16, shape, dev)
+    _want(isinstance(len0, torch.Tensor) and len0.dim() == 1 and len0.shape[0] in (1, q.shape[0]),
+          "len0 must be a tensor [1] (one length for all) or [B]")
+    _dense("len0", len0, _I32, len0.shape, dev)
+    _dense("out", out, _BF16, out_shape, dev)
+    raise ValueError("the tensors do not fit the call")
 
 
 def attention_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len) -> int:
@@ -483,38 +499,37 @@ def op_attention_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, len0, wo
     """Decode attention of q [B, Hq, dh] over a prefix shared by the batch (k_prefix, v_prefix [Hkv, P, dh], the first
     prefix_len rows of it; None: no prefix) and each sequence's own cache [B, Hkv, cap, dh], slots 0..len0, into out
     [B, Hq*dh]. work: attention_decode_shared_workspace bytes of scratch of any type (None without a prefix)."""
-    _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [B, Hq, dh]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [B, Hq, dh]")
     B, Hq, dh = q.shape
     dev = q.get_device()
-    _dense("q", q, _BF16, (B, Hq, dh), dev)
-    Hkv, cap = _caches(k_cache, v_cache, B, Hq, dh, dev)
-    stride = _lengths(len0, B, dev)
-    _dense("out", out, _BF16, (B, Hq * dh), dev)
+    Hkv, cap, stride = _attention_tensors(q, "[B, Hq, dh]", k_cache, v_cache, len0, out, (B, Hq * dh), dev)
     p_k = p_v = p_work = p_meta = p_err = None
     rows = n = 0
     if k_prefix is not None:
-        _want(isinstance(k_prefix, torch.Tensor) and k_prefix.dim() == 3, "k_prefix must be a tensor [Hkv, P, dh]")
+        if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 3:
+            raise ValueError("k_prefix must be a tensor [Hkv, P, dh]")
         rows = k_prefix.shape[1]
         n = rows if prefix_len is None else prefix_len
-        _want(0 <= n <= rows, "prefix_len is not within the prefix")
-        _dense("k_prefix", k_prefix, _BF16, (Hkv, rows, dh), dev)
-        _dense("v_prefix", v_prefix, _BF16, (Hkv, rows, dh), dev)
-        p_k, p_v = k_prefix.data_ptr(), v_prefix.data_ptr()
+        if not 0 <= n <= rows:
+            raise ValueError("prefix_len is not within the prefix")
+        shape = (Hkv, rows, dh)
+        p_k = _dense("k_prefix", k_prefix, _BF16, shape, dev)
+        p_v = _dense("v_prefix", v_prefix, _BF16, shape, dev)
     else:
         _want(v_prefix is None and not prefix_len, "v_prefix and prefix_len go with k_prefix")
     if B == 0:
         return
     size = 0
     if n > 0:  # the library refuses scratch that is too small
-        _want(isinstance(work, torch.Tensor) and work.get_device() == dev and work.is_contiguous(),
-              "work must be contiguous scratch on the same device, of attention_decode_shared_workspace bytes")
-        p_work, size = work.data_ptr(), work.numel() * work.element_size()
+        if not isinstance(work, torch.Tensor) or work.get_device() != dev or not work.is_contiguous():
+            raise ValueError("work must be contiguous scratch on the same device, of attention_decode_shared_workspace "
+                             "bytes")
+        p_work, size = work.data_ptr(), work.nbytes
     if seq_meta is not None:
-        _dense("seq_meta", seq_meta, _I32, (2 + B,), dev)
-        p_meta = seq_meta.data_ptr()
+        p_meta = _dense("seq_meta", seq_meta, _I32, (2 + B,), dev)
     if err is not None:
-        _dense("err", err, _I32, (1,), dev)
-        p_err = err.data_ptr()
+        p_err = _dense("err", err, _I32, (1,), dev)
     _launch(lib().qwen3_op_attention_decode_shared,
             (q.data_ptr(), p_k, p_v, rows, n, k_cache.data_ptr(), v_cache.data_ptr(), B, Hq, Hkv, dh, cap,
              len0.data_ptr(), stride, p_meta, p_work, size, out.data_ptr(), p_err), dev, stream)
@@ -534,17 +549,12 @@ def attention_sink_rows(sinks) -> int:
 def op_attention_prefill_sinks(q, k_cache, v_cache, len0, out, window, sinks, rolling=False, err=None, stream=None):
     """Attention of the new tokens q [B, Hq, T, dh] in slots len0 .. len0+T-1 of the caches [B, Hkv, cap, dh] with a
     sliding window and sink tokens, into out [B*T, Hq*dh]; len0 [1] or [B]."""
-    _want(isinstance(q, torch.Tensor) and q.dim() == 4, "q must be a tensor [B, Hq, T, dh]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a tensor [B, Hq, T, dh]")
     B, Hq, T, dh = q.shape
     dev = q.get_device()
-    _dense("q", q, _BF16, (B, Hq, T, dh), dev)
-    Hkv, cap = _caches(k_cache, v_cache, B, Hq, dh, dev)
-    stride = _lengths(len0, B, dev)
-    _dense("out", out, _BF16, (B * T, Hq * dh), dev)
-    p_err = None
-    if err is not None:
-        _dense("err", err, _I32, (1,), dev)
-        p_err = err.data_ptr()
+    Hkv, cap, stride = _attention_tensors(q, "[B, Hq, T, dh]", k_cache, v_cache, len0, out, (B * T, Hq * dh), dev)
+    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
     if B == 0 or T == 0:
         return
     _launch(lib().qwen3_op_attention_prefill_sinks,
@@ -554,17 +564,12 @@ def op_attention_prefill_sinks(q, k_cache, v_cache, len0, out, window, sinks, ro
 
 def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rolling=False, err=None, stream=None):
     """The single-token form of op_attention_prefill_sinks: q [B, Hq, dh], out [B, Hq*dh]."""
-    _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [B, Hq, dh]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [B, Hq, dh]")
     B, Hq, dh = q.shape
     dev = q.get_device()
-    _dense("q", q, _BF16, (B, Hq, dh), dev)
-    Hkv, cap = _caches(k_cache, v_cache, B, Hq, dh, dev)
-    stride = _lengths(len0, B, dev)
-    _dense("out", out, _BF16, (B, Hq * dh), dev)
-    p_err = None
-    if err is not None:
-        _dense("err", err, _I32, (1,), dev)
-        p_err = err.data_ptr()
+    Hkv, cap, stride = _attention_tensors(q, "[B, Hq, dh]", k_cache, v_cache, len0, out, (B, Hq * dh), dev)
+    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
     if B == 0:
         return
     _launch(lib().qwen3_op_attention_decode_sinks,
