@@ -4,7 +4,7 @@
 // cluster of CTAs shares the keys of one (sequence, kv head). For a shared prefix, attn_prefix_launch
 // (attention_tiles.cu) computes its part for the query rows of the whole batch at once and leaves one record per row
 // tile and key chunk; attn_ranges_kernel works on the sequences' own keys beside it and joins the records, or
-// attn_join_kernel does.
+// attn_join_kernel does. A prefix of few keys for few sequences is another run of keys of attn_ranges_kernel.
 #include <algorithm>
 
 #include "common.cuh"
@@ -16,7 +16,7 @@ namespace {
 // ------------------------------------------------------------------------------------- own keys
 // O = sum_i p_i v_i / sum_i p_i, p_i = 2^(q k_i log2(e) / sqrt(dh) - m) over the visible keys i: up to three
 // runs of cache rows (sinks, window, the wrapped part of a rolling buffer; or the own slots before and
-// behind a padding block), taken in units of 16 keys.
+// behind a padding block, and a short prefix), taken in units of 16 keys.
 //
 // Every warp works through its own units alone, with a running maximum (lazily rescaled, as in the prefill
 // kernels): its lane 0 keeps a ring full with the K and V boxes of the coming units (TMA, 128-byte
@@ -58,6 +58,7 @@ struct RangeArgs {
     // window and sinks; ring > 0: rows [0, sink_rows) keep the first slots, the others wrap over ring rows
     int window, sinks, sink_rows, ring;
     const int* meta;    // own slots of a shared prefix: SeqMap::meta, or null
+    int P;              // rows of the prefix that each sequence reads for itself, as a third run (0: none, or by records)
     const float* recs;  // records of the prefix to join (attn_prefix_launch)
     int nrec, row_tiles;
     float* own;  // [B][Hkv][G][DH + 4]: where the own keys' (output sums, maximum, sum) go, to be joined by a launch of its own; or null
@@ -180,7 +181,8 @@ __device__ __forceinline__ void join_parts(const RangeArgs& a, int b, int j, int
 
 template <int DH, bool SINKS, int RING>
 __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
-    attn_ranges_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const RangeArgs a) {
+    attn_ranges_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CUtensorMap tmPK, const __grid_constant__ CUtensorMap tmPV, const RangeArgs a) {
     using Ly = RgLayout<DH, RING>;
     constexpr int NW = RG_WARPS, THREADS = RG_THREADS, ST = Ly::ST, RG_BYTES = Ly::RG_BYTES;
     extern __shared__ uint8_t rg_raw[];
@@ -261,6 +263,7 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
         cnt[0] = end - row[0];
         row[1] = min(max(pe, end), n);
         cnt[1] = n - row[1];
+        cnt[2] = a.P;
     }
     const int n0 = (cnt[0] + RG_KEYS - 1) / RG_KEYS, n1 = n0 + (cnt[1] + RG_KEYS - 1) / RG_KEYS;
     const int units = n1 + (cnt[2] + RG_KEYS - 1) / RG_KEYS;
@@ -276,19 +279,22 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
 
     uint8_t* ring_p = rings + warp * RG_BYTES;
     const uint32_t ring_a = smem_u32(ring_p);
-    const int z = b * a.Hkv + j;
-    auto load = [&](int i, const CUtensorMap* map, uint64_t* full, int off) {  // lane 0: K or V of unit i
+    auto load = [&](int i, const CUtensorMap* map, const CUtensorMap* pmap, uint64_t* full, int off) {
         int valid;
-        const int y = unit(u0 + warp + NW * i, valid), st = i % ST;
+        const int u = u0 + warp + NW * i, y = unit(u, valid), st = i % ST;
+        const bool prefix = !SINKS && u >= n1;
+        const int z = prefix ? j : b * a.Hkv + j;
         uint8_t* dst = ring_p + st * 2 * Ly::HALF + off;
         mbar_expect_tx(&full[st], Ly::HALF);
 #pragma unroll
-        for (int c = 0; c < Ly::NCH; ++c) tma_load_3d(dst + c * Ly::BOX, map, &full[st], c * 64, y, z);
+        for (int c = 0; c < Ly::NCH; ++c) tma_load_3d(dst + c * Ly::BOX, prefix ? pmap : map, &full[st], c * 64, y, z);
     };
+    auto load_k = [&](int i) { load(i, &tmK, &tmPK, k_full, 0); };  // lane 0: K or V of unit i
+    auto load_v = [&](int i) { load(i, &tmV, &tmPV, v_full, Ly::HALF); };
     if (lane == 0)
         for (int i = 0; i < min(ST, mine); ++i) {
-            load(i, &tmK, k_full, 0);
-            load(i, &tmV, v_full, Ly::HALF);
+            load_k(i);
+            load_v(i);
         }
 
     const float sl2 = kLog2e / sqrtf((float)DH);
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
         for (int e = 0; e < 4; ++e) d[e] += d2[e];
         __syncwarp();  // every lane has read the unit's keys: the next ones may come
         k_ahead = i + ST < mine;
-        if (lane == 0 && k_ahead) load(i + ST, &tmK, k_full, 0);
+        if (lane == 0 && k_ahead) load_k(i + ST);
         const bool in0 = gq < valid, in1 = gq + 8 < valid;
         const float v0 = in0 ? d[0] * sl2 : -INFINITY, v1 = in0 ? d[1] * sl2 : -INFINITY;
         const float v2 = in1 ? d[2] * sl2 : -INFINITY, v3 = in1 ? d[3] * sl2 : -INFINITY;
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
             mma_keys(o[t], f, b_lo, b_hi);
         }
         __syncwarp();
-        if (lane == 0 && k_ahead) load(i + ST, &tmV, v_full, Ly::HALF);
+        if (lane == 0 && k_ahead) load_v(i + ST);
         k_ahead = false;
     }
     if (!ok) {  // give up: wait, bounded, for the copies still on their way
@@ -486,20 +492,32 @@ int ranges_cluster(int B, int Hkv, int max_keys) {
     return c;
 }
 
+struct Prefix {
+    const __nv_bfloat16 *k, *v;
+    int cap;
+};
+
 template <int DH, bool SINKS, int RING>
-cudaError_t ranges_launch_ring(const CUtensorMap& tk, const CUtensorMap& tv, const RangeArgs& a, int B, cudaStream_t st) {
+cudaError_t ranges_launch_ring(const CUtensorMap (&maps)[4], const RangeArgs& a, int B, cudaStream_t st) {
     return launch_pdl_cluster(attn_ranges_kernel<DH, SINKS, RING>, dim3(a.C, a.Hkv, B), dim3(RG_THREADS), a.C,
-                              RgLayout<DH, RING>::SMEM, st, tk, tv, a);
+                              RgLayout<DH, RING>::SMEM, st, maps[0], maps[1], maps[2], maps[3], a);
 }
 
 template <int DH, bool SINKS>
-cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfloat16* v, int B, int max_keys,
-                             int free_sms, cudaStream_t st) {
-    CUtensorMap tk, tv;
+cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfloat16* v, const Prefix& p, int B,
+                             int max_keys, int free_sms, cudaStream_t st) {
+    CUtensorMap maps[4];  // K and V of the caches and of the prefix
     const uint64_t heads = (uint64_t)B * a.Hkv;
-    if (!encode_tmap_bf16_rows(&tk, k, DH, a.cap, a.cap, heads, RG_KEYS) ||
-        !encode_tmap_bf16_rows(&tv, v, DH, a.cap, a.cap, heads, RG_KEYS))
+    if (!encode_tmap_bf16_rows(&maps[0], k, DH, a.cap, a.cap, heads, RG_KEYS) ||
+        !encode_tmap_bf16_rows(&maps[1], v, DH, a.cap, a.cap, heads, RG_KEYS))
         return cudaErrorInvalidValue;
+    if (a.P == 0) {
+        maps[2] = maps[0];
+        maps[3] = maps[1];
+    } else if (!encode_tmap_bf16_rows(&maps[2], p.k, DH, a.P, p.cap, a.Hkv, RG_KEYS) ||
+               !encode_tmap_bf16_rows(&maps[3], p.v, DH, a.P, p.cap, a.Hkv, RG_KEYS)) {
+        return cudaErrorInvalidValue;
+    }
     a.C = ranges_cluster(B, a.Hkv, max_keys);
     // Own keys beside a prefix are few, and four small CTAs an SM start and end them fastest; a window's or a
     // long cache's keys are streamed by two CTAs with three units a warp on their way (measured, cold cache: 64
@@ -508,17 +526,17 @@ cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfl
     // Own CTAs that cannot all run beside the prefix kernel would keep the others out while they wait for its
     // records: their results then go through memory to a launch that joins them.
     if (a.nrec == 0 || a.C > 1 || fits_beside_prefix(B, a.Hkv, DH, free_sms)) a.own = nullptr;
-    if (ring == 3) return ranges_launch_ring<DH, SINKS, 3>(tk, tv, a, B, st);
-    const cudaError_t e = ranges_launch_ring<DH, SINKS, 1>(tk, tv, a, B, st);
+    if (ring == 3) return ranges_launch_ring<DH, SINKS, 3>(maps, a, B, st);
+    const cudaError_t e = ranges_launch_ring<DH, SINKS, 1>(maps, a, B, st);
     if (e != cudaSuccess || !a.own) return e;
     return launch_pdl(attn_join_kernel<DH>, dim3(a.Hkv, B), dim3(RG_THREADS), 0, st, a);
 }
 
 template <bool SINKS>
-cudaError_t ranges_launch(const RangeArgs& a, const __nv_bfloat16* k, const __nv_bfloat16* v, int B, int dh, int max_keys,
-                          int free_sms, cudaStream_t st) {
-    if (dh == 128) return ranges_launch_dh<128, SINKS>(a, k, v, B, max_keys, free_sms, st);
-    if (dh == 64) return ranges_launch_dh<64, SINKS>(a, k, v, B, max_keys, free_sms, st);
+cudaError_t ranges_launch(const RangeArgs& a, const __nv_bfloat16* k, const __nv_bfloat16* v, const Prefix& p, int B, int dh,
+                          int max_keys, int free_sms, cudaStream_t st) {
+    if (dh == 128) return ranges_launch_dh<128, SINKS>(a, k, v, p, B, max_keys, free_sms, st);
+    if (dh == 64) return ranges_launch_dh<64, SINKS>(a, k, v, p, B, max_keys, free_sms, st);
     return cudaErrorInvalidValue;
 }
 
@@ -534,10 +552,12 @@ cudaError_t ranges_prepare() {
 // Key chunks of the prefix. The prefix kernel runs one CTA an SM, the own keys' CTAs run on the SMs it leaves, so
 // fewer chunks than SMs can pay: the estimate (us, on the measured rates) is the prefix kernel's time or, if it is
 // longer, the time to read everything, plus what is left of the own keys when the prefix kernel ends.
-// An item of the prefix kernel takes 0.9 us a key tile (its softmax warps), more when its SM's share of HBM is the
-// limit (the row tiles of a chunk share its keys), and 4.5 us for its start and end; an SM's own CTAs read 55 GB/s;
-// a join launch takes 2.5 us; half of the own cache is taken to be filled. (Measured, 64 sequences: 32768 keys, 8B
-// heads, 512 own keys on average, 6 chunks 50 us, 9 chunks 57; 4096 keys, 0.6B heads, 256 own keys, 3 chunks 15.5, 19 chunks 22.)
+// An item of the prefix kernel takes 0.9 us a key tile (its softmax warps), more when all of them together would read
+// more than 5 TB/s (the row tiles of a chunk share its keys), and 4.5 us for its start and end; an SM's own CTAs read
+// 55 GB/s; a join launch takes 2.5 us, records past the eighth 0.5 us each (they are not read ahead); half of the own
+// cache is taken to be filled. Measured (us, dh 128, 8 kv heads): 64 sequences, 32768 keys, 32 heads, 512 own keys on average,
+// 6 chunks 50, 9 chunks 57; 4096 keys, 16 heads, 256 own keys, 3 chunks 15.5, 19 chunks 27; 16 sequences, 8192 keys, 32 heads,
+// 8 chunks 14.4, 13 chunks 16.7; 8 sequences, 32768 keys, 9 chunks 31.9, 16 chunks 33.4, 5 chunks 45.9.
 constexpr int kPrefixMaxRounds = 2;
 int prefix_max_chunks(int B, int Hq, int Hkv, int P) {
     const long long tiles = (P + 127ll) / 128, items = (long long)prefix_row_tiles(B, Hq / Hkv) * Hkv;
@@ -547,7 +567,7 @@ int prefix_max_chunks(int B, int Hq, int Hkv, int P) {
 int prefix_chunks(int B, int Hq, int Hkv, int dh, int P, int own_cap) {
     const int row_tiles = prefix_row_tiles(B, Hq / Hkv), sms = device_sm_count();
     const long long tiles = (P + 127ll) / 128, items = (long long)row_tiles * Hkv;
-    constexpr double hbm = 6.8e6, sm_rate = 0.055e6;  // bytes per us
+    constexpr double hbm = 6.8e6, prefix_hbm = 5.0e6, sm_rate = 0.055e6;  // bytes per us
     const double own = (double)B * Hkv * (own_cap / 2.0) * dh * 4, tile = 128.0 * dh * 4;
     const int max_chunks = prefix_max_chunks(B, Hq, Hkv, P);
     int best = 1;
@@ -555,18 +575,28 @@ int prefix_chunks(int B, int Hq, int Hkv, int dh, int P, int own_cap) {
     for (int c = 1; c <= max_chunks; ++c) {
         const long long n = items * c, rounds = (n + sms - 1) / sms;
         const double running = (double)std::min<long long>(n, sms);
-        const double per_tile = std::max(0.9, running / row_tiles * tile / hbm);
+        const double per_tile = std::max(0.9, running / row_tiles * tile / prefix_hbm);
         const double t_prefix = rounds * (((tiles + c - 1) / c) * per_tile + 4.5);
         const double rate = n < sms ? std::min(hbm, (sms - n) * sm_rate) : 0;
         const bool join = !fits_beside_prefix(B, Hkv, dh, (int)std::max<long long>(0, sms - n));
         const double t = std::max(t_prefix + std::max(0.0, own - rate * t_prefix) / hbm, (own + Hkv * tiles * tile) / hbm) +
-                         0.05 * c + (join ? 2.5 : 0);
+                         0.05 * c + 0.5 * std::max(0, c - 8) + (join ? 2.5 : 0);
         if (c == 1 || t < best_t) {
             best_t = t;
             best = c;
         }
     }
     return best;
+}
+
+// Whether every sequence reads the prefix (if there is one) for itself, in one launch: little to read again (from L2, about 10 TB/s) costs
+// less than the prefix kernel and its records. Measured (us, here against with records; 16 query heads, 8 kv heads, dh 128,
+// own caches of 64 slots): 1 sequence, 600 keys 5.9 / 8.1, 4096 8.6 / 11.5; 2 at 4096 9.5 / 11.4; 16 at 600 8.9 / 8.2; 4 at 4096
+// 11.5 / 11.2. Where the own keys already fill the GPU the second reading is not hidden: 64 sequences, 128 keys, 512 own
+// slots 16.4 / 13.2, 64 own slots 5.9 / 7.8. And the host has one launch to make: 8.9 us a call against 11.3.
+bool prefix_read_by_each(int B, int Hkv, int P, int own_cap) {
+    const long long pairs = (long long)B * Hkv;
+    return P == 0 || (pairs * P <= 1 << 16 && pairs * (P + own_cap / 2ll) <= 1 << 17);
 }
 
 }  // namespace
@@ -594,9 +624,11 @@ cudaError_t attn_decode_shared_launch(const __nv_bfloat16* q, const __nv_bfloat1
     a.cap = cap;
     a.meta = meta;
     int free_sms = 0;
-    if (P > 0) {
-        // with a layout the first slots of the own caches are the prefix
-        a.nrec = prefix_chunks(B, Hq, Hkv, dh, P, meta ? std::max(0, cap - P) : cap);
+    const int own_cap = meta ? std::max(0, cap - P) : cap;  // with a layout the first slots are the prefix
+    if (prefix_read_by_each(B, Hkv, P, own_cap)) {
+        a.P = P;
+    } else {
+        a.nrec = prefix_chunks(B, Hq, Hkv, dh, P, own_cap);
         a.row_tiles = prefix_row_tiles(B, a.G);
         a.recs = work;
         a.own = work + prefix_rec_floats(dh) * a.row_tiles * Hkv * a.nrec;
@@ -605,7 +637,8 @@ cudaError_t attn_decode_shared_launch(const __nv_bfloat16* q, const __nv_bfloat1
         if (e != cudaSuccess) return e;
     }
     a.err = err;
-    return ranges_launch<false>(a, kc, vc, B, dh, cap, free_sms, st);
+    return ranges_launch<false>(a, kc, vc, Prefix{kp, vp, prefix_cap}, B, dh, (int)std::min(cap + (long long)a.P, 1ll << 30),
+                                free_sms, st);
 }
 
 cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc, const __nv_bfloat16* vc, int B, int Hq,
@@ -626,7 +659,8 @@ cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16
     a.sink_rows = sm.sink_rows;
     a.ring = sm.ring;
     a.err = err;
-    return ranges_launch<true>(a, kc, vc, B, dh, (int)std::min<long long>((long long)sm.window + sm.sinks, cap), 0, st);
+    return ranges_launch<true>(a, kc, vc, Prefix{}, B, dh, (int)std::min<long long>((long long)sm.window + sm.sinks, cap), 0,
+                               st);
 }
 
 cudaError_t attention_ranges_prepare() {

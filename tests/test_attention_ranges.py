@@ -151,6 +151,32 @@ def test_shared_padding(bd, ps, psh, pads):
 
 
 @gpu
+@pytest.mark.parametrize("Bn,Hq,Hkv,dh,P", [(600, 8, 8, 64, 15), (520, 16, 8, 128, 1 + 15), (70, 3, 1, 128, 1000), (150, 6, 1, 64, 500),
+                                            (41, 10, 2, 128, 900), (33, 14, 2, 128, 1100), (9, 16, 2, 64, 4000),
+                                            (1, 1, 1, 128, 70000), (1, 8, 1, 64, 66001), (2, 16, 8, 128, 4097),
+                                            (2, 16, 8, 128, 4096), (64, 16, 8, 128, 128), (65, 16, 8, 128, 128)])
+def test_shared_read_once_or_by_each(bd, Bn, Hq, Hkv, dh, P):
+    """Sizes at and past the border between a prefix read once for the batch and one that each sequence reads for itself
+    (65,536 keys over all kv heads), groups of 1 to 8 heads."""
+    _shared_case(bd, Bn, Hq, Hkv, dh, P, 40, [(b * 11) % 41 - 1 for b in range(Bn)], seed=Hq + Bn, prefix_cap=P + 5)
+
+
+@gpu
+def test_shared_many_own_keys_without_a_prefix(bd):
+    lens = [(b * 53) % 700 for b in range(64)]
+    _shared_case(bd, 64, 16, 8, 128, 0, 700, lens)
+    _shared_case(bd, 64, 16, 8, 128, 0, 700, lens, prefix_cap=9, seed=1)
+
+
+@gpu
+@pytest.mark.parametrize("Bn,Hq,Hkv", [(3, 8, 2), (40, 8, 8)])
+def test_shared_short_prefix_and_padding(bd, Bn, Hq, Hkv):
+    """A layout with padding beside a prefix of every form."""
+    for P in (1, 100, 700):
+        _shared_case(bd, Bn, Hq, Hkv, 128, P, 200, [180], meta=[130, 128] + [(7 * b) % 45 for b in range(Bn)], seed=P)
+
+
+@gpu
 def test_shared_large_scores(bd):
     """Scores of a few hundred: the running maxima of chunks, warps and CTAs differ widely."""
     _shared_case(bd, 9, 16, 8, 128, 3000, 300, [(b * 97) % 300 for b in range(9)], seed=5, scale=60.0)
