@@ -30,10 +30,10 @@ namespace {
 // What bounds it. Many sequences: HBM, 64 sequences x 4,100 keys of 8 kv heads, dh 128 (1.08 GB) 151 us from call to call
 // (part of the keys still in L2), 158 us with a cold L2 under ncu, 6.8 TB/s (100% of the measured copy rate). Fragments loaded
 // straight from global memory, without rings, took 219 us for any split: too little on its way per warp. One
-// sequence: the chain of launch, length, first boxes and joins, 9.6 us for 4,100 keys by clusters of 16 CTAs
-// (14.5 by 4).
+// sequence: the chain of launch, length, first boxes and the join, 8.4 us for 4,100 keys by clusters of 16 CTAs
+// (13.7 by 4).
 constexpr int RG_KEYS = 16, RG_MAX_CLUSTER = 16, RG_MAX_G = 8, RG_WARPS = 4, RG_THREADS = 32 * RG_WARPS;
-constexpr int RG_MAX_PARTS = RG_MAX_CLUSTER + kPrefixMaxChunks;
+constexpr int RG_MAX_PARTS = 1 + kPrefixMaxChunks;
 template <int DH, int RING>
 struct RgLayout {
     static constexpr int NCH = DH / 64;               // 64-column boxes of a row
@@ -110,35 +110,50 @@ __device__ __forceinline__ void store_quad(const RangeArgs& a, int b, int j, int
         make_uint2(pack_bf16(v.x * scale, v.y * scale), pack_bf16(v.z * scale, v.w * scale));
 }
 
-// Join `n_own` parts of the own keys (statistics own_stat(p, h) = (maximum, sum), output sums own_quad(p, h, dd)) and
-// the prefix records by log-sum-exp: O = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i. The CTA finishes the quads
-// of four dims whose number has its rank modulo a.C (in steps of its threads).
+// The prefix records of one (sequence, kv head): this sequence's rows in its row tile.
+template <int DH>
+struct Records {
+    const float* rec;
+    size_t step;  // between two key chunks
+    int row;
+    __device__ __forceinline__ Records(const RangeArgs& a, int b, int j) {
+        const int seqs = kPrefixRows / a.G;
+        row = b % seqs * a.G;
+        rec = a.recs + ((size_t)j * a.row_tiles + b / seqs) * prefix_rec_floats(DH);
+        step = (size_t)a.Hkv * a.row_tiles * prefix_rec_floats(DH);
+    }
+    __device__ __forceinline__ float4 quad(int r, int h, int dd) const {
+        return __ldcg(reinterpret_cast<const float4*>(rec + r * step + ((size_t)(dd / 4) * kPrefixRows + row + h) * 4));
+    }
+    __device__ __forceinline__ float2 stat(int r, int h) const {  // maximum, sum
+        return __ldcg(reinterpret_cast<const float2*>(rec + r * step + (size_t)DH * kPrefixRows + (row + h) * 2));
+    }
+};
+
+__device__ __forceinline__ void add_scaled(float4& v, const float4& x, float f) {
+    v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
+}
+
+// Join the own keys' result (own_stat(h) = (maximum, sum), output sums own_quad(h, dd)) and the prefix records by
+// log-sum-exp: O = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 template <int DH, typename Stat, typename Quad>
-__device__ __forceinline__ void join_parts(const RangeArgs& a, int b, int j, int n_own, int rank,
-                                           float (&pm)[RG_MAX_G][RG_MAX_PARTS], float (&pl)[RG_MAX_G][RG_MAX_PARTS],
-                                           float (&inv)[RG_MAX_G], Stat own_stat, Quad own_quad) {
+__device__ __forceinline__ void join_records(const RangeArgs& a, int b, int j, float (&pm)[RG_MAX_G][RG_MAX_PARTS],
+                                             float (&pl)[RG_MAX_G][RG_MAX_PARTS], float (&inv)[RG_MAX_G], Stat own_stat,
+                                             Quad own_quad) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int quads = a.G * (DH / 4), parts = n_own + a.nrec;
-    // this sequence's rows in its row tile, and the distance between the records of two chunks
-    const int seqs = kPrefixRows / a.G, row0 = b % seqs * a.G;
-    const float* rec0 = a.recs + ((size_t)j * a.row_tiles + b / seqs) * prefix_rec_floats(DH);
-    const size_t rec_step = (size_t)a.Hkv * a.row_tiles * prefix_rec_floats(DH);
-    auto rec_quad = [&](int r, int h, int dd) {
-        return __ldcg(reinterpret_cast<const float4*>(rec0 + r * rec_step + ((size_t)(dd / 4) * kPrefixRows + row0 + h) * 4));
-    };
+    const int quads = a.G * (DH / 4), parts = 1 + a.nrec;
+    const Records<DH> rec(a, b, j);
     // the output sums of the first records are on their way while the weights are worked out
     constexpr int PRE = 8;
     float4 pre[PRE];
-    const int e0 = threadIdx.x + RG_THREADS * rank;
+    const int e0 = threadIdx.x;
 #pragma unroll
     for (int r = 0; r < PRE; ++r)
-        if (r < a.nrec && e0 < quads) pre[r] = rec_quad(r, e0 % a.G, e0 / a.G * 4);
+        if (r < a.nrec && e0 < quads) pre[r] = rec.quad(r, e0 % a.G, e0 / a.G * 4);
     for (int e = threadIdx.x; e < parts * RG_MAX_G; e += RG_THREADS) {
         const int p = e / RG_MAX_G, h = e % RG_MAX_G;
         if (h < a.G) {
-            const float2 ml = p < n_own ? own_stat(p, h)
-                                        : __ldcg(reinterpret_cast<const float2*>(rec0 + (p - n_own) * rec_step +
-                                                                                 (size_t)DH * kPrefixRows + (row0 + h) * 2));
+            const float2 ml = p == 0 ? own_stat(h) : rec.stat(p - 1, h);
             pm[h][p] = ml.x;
             pl[h][p] = ml.y;
         }
@@ -159,23 +174,75 @@ __device__ __forceinline__ void join_parts(const RangeArgs& a, int b, int j, int
         if (lane == 0) inv[h] = L == 0.f ? 0.f : 1.f / L;
     }
     __syncthreads();
-    for (int e = e0; e < quads; e += RG_THREADS * a.C) {
+    for (int e = e0; e < quads; e += RG_THREADS) {
         const int h = e % a.G, dd = e / a.G * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](const float4& x, float f) {
-            v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
-        };
-#pragma unroll 4
-        for (int p = 0; p < n_own; ++p) add(own_quad(p, h, dd), pm[h][p]);
+        add_scaled(v, own_quad(h, dd), pm[h][0]);
         int r = 0;
         if (e == e0) {
 #pragma unroll
             for (; r < PRE; ++r)
-                if (r < a.nrec) add(pre[r], pm[h][n_own + r]);
+                if (r < a.nrec) add_scaled(v, pre[r], pm[h][1 + r]);
         }
 #pragma unroll 4
-        for (; r < a.nrec; ++r) add(rec_quad(r, h, dd), pm[h][n_own + r]);
+        for (; r < a.nrec; ++r) add_scaled(v, rec.quad(r, h, dd), pm[h][1 + r]);
         store_quad<DH>(a, b, j, h, dd, v, inv[h]);
+    }
+}
+
+// The same over the a.C CTAs of a cluster, each of which finishes its share of the output: C neighbouring threads take one
+// quad of four dims, each one CTA's part (statistics cm, cl and sums so of that CTA's shared memory, all read at once)
+// and every C-th record, and add up by shuffles. (One thread a quad that read the parts in turn took 9.7 us for 4,100
+// keys of one sequence by clusters of 16, this 8.5.)
+template <int DH>
+__device__ __forceinline__ void join_cluster(const RangeArgs& a, int b, int j, int rank, const float* cm, const float* cl,
+                                             const float* so, int pitch) {
+    const int C = a.C, p = threadIdx.x % C, nq = a.G * (DH / 4) / C;  // C, a power of two up to 16, divides DH / 4
+    const Records<DH> rec(a, b, j);
+    for (int q0 = 0; q0 < nq; q0 += RG_THREADS / C) {
+        const int q = q0 + threadIdx.x / C, e = rank * nq + min(q, nq - 1), h = e % a.G, dd = e / a.G * 4;
+        const float m = ld_cluster_f32(cluster_addr(cm + h, p)), l = ld_cluster_f32(cluster_addr(cl + h, p));
+        const float4 x = ld_cluster_f32x4(cluster_addr(so + h * pitch + dd, p));
+        constexpr int PRE = 4;
+        float2 rml[PRE];
+        float4 rx[PRE];
+#pragma unroll
+        for (int k = 0; k < PRE; ++k)
+            if (p + k * C < a.nrec) {
+                rml[k] = rec.stat(p + k * C, h);
+                rx[k] = rec.quad(p + k * C, h, dd);
+            }
+        float M = m;
+#pragma unroll
+        for (int k = 0; k < PRE; ++k)
+            if (p + k * C < a.nrec) M = fmaxf(M, rml[k].x);
+#pragma unroll 4
+        for (int r = p + PRE * C; r < a.nrec; r += C) M = fmaxf(M, rec.stat(r, h).x);
+        for (int o = C / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float pm, float pl, const float4& px) {
+            const float f = pm == -INFINITY ? 0.f : ex2_approx(pm - M);
+            L = fmaf(pl, f, L);
+            add_scaled(v, px, f);
+        };
+        add(m, l, x);
+#pragma unroll
+        for (int k = 0; k < PRE; ++k)
+            if (p + k * C < a.nrec) add(rml[k].x, rml[k].y, rx[k]);
+#pragma unroll 4
+        for (int r = p + PRE * C; r < a.nrec; r += C) {
+            const float2 ml = rec.stat(r, h);
+            add(ml.x, ml.y, rec.quad(r, h, dd));
+        }
+        for (int o = C / 2; o > 0; o >>= 1) {
+            L += __shfl_xor_sync(0xffffffffu, L, o);
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+            v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+        }
+        if (p == 0 && q < nq) store_quad<DH>(a, b, j, h, dd, v, L == 0.f ? 0.f : 1.f / L);
     }
 }
 
@@ -192,7 +259,7 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
     __shared__ uint64_t bars[RG_WARPS][2 * ST];                 // [K of each stage, V of each stage]
     __shared__ float sm[NW][RG_MAX_G], sl[NW][RG_MAX_G];
     __shared__ float cm[RG_MAX_G], cl[RG_MAX_G];                   // this CTA's maximum and sum
-    __shared__ float pm[RG_MAX_G][RG_MAX_PARTS], pl[RG_MAX_G][RG_MAX_PARTS];  // of every part: CTAs, then prefix records
+    __shared__ float pm[RG_MAX_G][RG_MAX_PARTS], pl[RG_MAX_G][RG_MAX_PARTS];  // of the own keys, then of the prefix records
     __shared__ float inv[RG_MAX_G];
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
@@ -442,26 +509,21 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
         return;
     }
     if (alone) return;
-    // join the cluster's CTAs and the prefix records; each CTA finishes a share of the output
-    if (a.C > 1) {
-        cluster_sync();
-    } else {
-        __syncthreads();
-    }
+    // join the cluster's CTAs and the prefix records
     if (a.nrec > 0) {
         pdl_wait();  // the prefix kernel's records
         pdl_trigger();
     }
-    join_parts<DH>(
-        a, b, j, a.C, rank, pm, pl, inv,
-        [&](int p, int h) {
-            return a.C == 1 ? make_float2(cm[h], cl[h])
-                            : make_float2(ld_cluster_f32(cluster_addr(&cm[h], p)), ld_cluster_f32(cluster_addr(&cl[h], p)));
-        },
-        [&](int p, int h, int dd) {
-            return a.C == 1 ? *reinterpret_cast<const float4*>(&so[0][h][dd]) : ld_cluster_f32x4(cluster_addr(&so[0][h][dd], p));
-        });
-    if (a.C > 1) cluster_sync();  // every CTA's partial stays in shared memory until the others have read it
+    if (a.C > 1) {
+        cluster_sync();
+        join_cluster<DH>(a, b, j, rank, cm, cl, &so[0][0][0], Ly::PITCH);
+        cluster_sync();  // every CTA's partial stays in shared memory until the others have read it
+    } else {
+        __syncthreads();
+        join_records<DH>(
+            a, b, j, pm, pl, inv, [&](int h) { return make_float2(cm[h], cl[h]); },
+            [&](int h, int dd) { return *reinterpret_cast<const float4*>(&so[0][h][dd]); });
+    }
 }
 
 // The own keys' results (attn_ranges_kernel with a.own) and the prefix records of one (sequence, kv head).
@@ -472,10 +534,9 @@ __global__ void __launch_bounds__(RG_THREADS) attn_join_kernel(const RangeArgs a
     const float* own = a.own + ((size_t)b * a.Hkv + j) * a.G * (DH + 4);
     pdl_trigger();
     pdl_wait();
-    join_parts<DH>(
-        a, b, j, 1, 0, pm, pl, inv,
-        [&](int, int h) { return __ldcg(reinterpret_cast<const float2*>(own + h * (DH + 4) + DH)); },
-        [&](int, int h, int dd) { return __ldcg(reinterpret_cast<const float4*>(own + h * (DH + 4) + dd)); });
+    join_records<DH>(
+        a, b, j, pm, pl, inv, [&](int h) { return __ldcg(reinterpret_cast<const float2*>(own + h * (DH + 4) + DH)); },
+        [&](int h, int dd) { return __ldcg(reinterpret_cast<const float4*>(own + h * (DH + 4) + dd)); });
 }
 
 // Whether an own CTA for every (sequence, kv head) can run on the SMs that the prefix kernel leaves.
@@ -483,12 +544,24 @@ bool fits_beside_prefix(int B, int Hkv, int dh, int free_sms) {
     return (long long)B * Hkv <= (long long)free_sms * (dh == 128 ? RgLayout<128, 1>::CTAS : RgLayout<64, 1>::CTAS);
 }
 
-// CTAs per (sequence, kv head): as many as two CTAs on every SM take, while each warp keeps a 16-key unit.
-int ranges_cluster(int B, int Hkv, int max_keys) {
+// CTAs per (sequence, kv head). Clusters of up to four CTAs while all CTAs fit the GPU (four an SM), of eight while they
+// are two an SM at most and of sixteen while they are one, since larger clusters wait for room in one part of the GPU; each
+// warp keeps a 16-key unit, two once there is a CTA for every SM and in clusters of sixteen, eight past two CTAs an SM.
+// Measured (us, caches from HBM, 8 kv heads, dh 128): 1 sequence of 4096 keys by 8 CTAs 11.2, by 16 9.3; 4 by 8 15.7, by 16 20.5;
+// 8 of 1024 keys by 4 10.4, by 8 11.3; 16 of 4096 by 2 44.8, by 4 42.7; 32 of 4096 by 1 82.4, by 2 80.2; 1 of 1024 by 8 5.5, by 16
+// 6.1; 32 of 256 by 1 9.1, by 2 10.7. Beside a prefix kernel: two CTAs an SM at most, since they cannot all start
+// before its CTAs end.
+int ranges_cluster(int B, int Hkv, int max_keys, bool beside) {
+    const long long sms = device_sm_count();
     int c = 1;
-    while (c < RG_MAX_CLUSTER && (long long)B * Hkv * c * 2 <= 2 * device_sm_count() &&
-           max_keys >= 2 * c * RG_WARPS * RG_KEYS)
-        c *= 2;
+    while (c < RG_MAX_CLUSTER) {
+        const int d = 2 * c;
+        const long long ctas = (long long)B * Hkv * d;
+        if (ctas > (beside || d == 8 ? 2 * sms : d < 8 ? 4 * sms : sms)) break;
+        const int units = beside ? 1 : ctas > 2 * sms ? 8 : d == 16 || ctas > sms ? 2 : 1;
+        if (max_keys < d * RG_WARPS * RG_KEYS * units) break;
+        c = d;
+    }
     return c;
 }
 
@@ -518,11 +591,11 @@ cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfl
                !encode_tmap_bf16_rows(&maps[3], p.v, DH, a.P, p.cap, a.Hkv, RG_KEYS)) {
         return cudaErrorInvalidValue;
     }
-    a.C = ranges_cluster(B, a.Hkv, max_keys);
-    // Own keys beside a prefix are few, and four small CTAs an SM start and end them fastest; a window's or a
-    // long cache's keys are streamed by two CTAs with three units a warp on their way (measured, cold cache: 64
-    // sequences x 4100 keys 176 us against 186).
-    const int ring = a.nrec > 0 || max_keys <= a.C * RG_WARPS * RG_KEYS * 8 ? 1 : 3;
+    a.C = ranges_cluster(B, a.Hkv, max_keys, a.nrec > 0);
+    // Four small CTAs an SM start and end fastest and stream as well as larger ones; only a CTA with a long cache of its own
+    // gains from three units a warp on their way, two CTAs an SM (64 sequences x 4100 keys, a cold L2, 176 us against 186; x 1024
+    // keys 43.8 against 41.9).
+    const int ring = a.nrec == 0 && a.C == 1 && max_keys >= 2048 ? 3 : 1;
     // Own CTAs that cannot all run beside the prefix kernel would keep the others out while they wait for its
     // records: their results then go through memory to a launch that joins them.
     if (a.nrec == 0 || a.C > 1 || fits_beside_prefix(B, a.Hkv, DH, free_sms)) a.own = nullptr;

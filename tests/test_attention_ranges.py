@@ -162,6 +162,16 @@ def test_shared_read_once_or_by_each(bd, Bn, Hq, Hkv, dh, P):
 
 
 @gpu
+@pytest.mark.parametrize("Bn,Hq,Hkv,dh,P,cap", [(2, 10, 2, 128, 20000, 3000), (1, 7, 1, 64, 70000, 5000), (37, 4, 4, 64, 30000, 140),
+                                                (19, 12, 4, 128, 9000, 300), (3, 8, 1, 128, 30000, 900), (9, 9, 3, 64, 6000, 600)])
+def test_shared_own_keys_of_several_ctas(bd, Bn, Hq, Hkv, dh, P, cap):
+    """Own keys split over a cluster beside a long prefix: the cluster's parts and the records of many chunks in one join."""
+    _shared_case(bd, Bn, Hq, Hkv, dh, P, cap, [(b * 131 + cap - 2) % cap for b in range(Bn)], seed=Bn)
+    _shared_case(bd, Bn, Hq, Hkv, dh, P, cap, [cap - 1], seed=Bn + 1,
+                 meta=[cap // 3, 0] + [(17 * b + 5) % (cap // 2) for b in range(Bn)])
+
+
+@gpu
 def test_shared_many_own_keys_without_a_prefix(bd):
     lens = [(b * 53) % 700 for b in range(64)]
     _shared_case(bd, 64, 16, 8, 128, 0, 700, lens)
@@ -289,6 +299,15 @@ def test_sinks_decode(bd, Bn, Hq, Hkv, dh, window, sinks, rolling):
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (8, 8), (10, 2), (12, 2), (14, 2), (8, 1)])
 def test_sinks_decode_head_groups(bd, Hq, Hkv):
     _sinks_case(bd, 5, 1, Hq, Hkv, 64, [900, 10, 300, 299, 301], 300, 5, False, decode=True, seed=Hq)
+
+
+@gpu
+@pytest.mark.parametrize("Bn,window,dh", [(1, 2500, 64), (1, 1100, 128), (3, 2500, 128), (20, 5000, 64), (130, 2500, 64)])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (5, 1), (6, 1), (7, 1), (8, 1), (8, 4)])
+def test_sinks_decode_clusters(bd, Bn, window, dh, Hq, Hkv):
+    """Sequences split over two to sixteen CTAs, by any group of heads, down to one key each."""
+    _sinks_case(bd, Bn, 1, Hq, Hkv, dh, [(b * 611 + window + 40) % (window + 300) for b in range(Bn)], window, 7, False,
+                decode=True, seed=Hq)
 
 
 @gpu
