@@ -340,8 +340,8 @@ QWEN3_API size_t qwen3_greedy_workspace(int B);
 QWEN3_API int qwen3_op_greedy(const float* d_logits, int64_t ld, int B, int V, int stop_id, int32_t* d_done,
                               int32_t* d_next, int32_t* d_work, void* stream);
 
-/* Decode attention for a batch that shares a long prefix, whose keys and values are read and multiplied once
- * for the whole batch: for each sequence b and query head h, out = softmax(q k^T * dh^-0.5) V in one softmax
+/* Decode attention for a batch that shares a prefix, whose keys and values are read and multiplied once for the
+ * whole batch (a prefix of few keys by each sequence, where that is faster): for each sequence b and query head h, out = softmax(q k^T * dh^-0.5) V in one softmax
  * over the prefix_len prefix keys and the sequence's own visible keys, kv head h / (Hq/Hkv). Prefix
  * d_k_prefix / d_v_prefix [Hkv, prefix_cap, dh] (its first prefix_len rows); own caches [B, Hkv, cap, dh],
  * sequence b's query at slot d_len0[b * len_stride] (len_stride 0: one length for all; 1: one per sequence),
