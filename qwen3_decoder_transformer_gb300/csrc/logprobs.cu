@@ -94,15 +94,24 @@ struct LpStat {
     float m, s, t;
 };
 constexpr float kLowest = -3.402823466e38f;
-__device__ __forceinline__ LpStat lp_join(const LpStat& a, const LpStat& b) {
-    const float m = fmaxf(a.m, b.m);
-    const float da = fmaxf(a.m - m, -1e30f), db = fmaxf(b.m - m, -1e30f);
-    const float fa = ex2_approx(da * kLog2e), fb = ex2_approx(db * kLog2e);
-    return {m, a.s * fa + b.s * fb, (a.t + a.s * da) * fa + (b.t + b.s * db) * fb};
+// Join the threads of a warp: the maximum first, then everyone's sums at its scale.
+__device__ __forceinline__ LpStat lp_warp_join(const LpStat& a) {
+    const int bits = __float_as_int(a.m), top = __reduce_max_sync(0xffffffffu, bits ^ ((bits >> 31) & 0x7fffffff));
+    const float m = __int_as_float(top ^ ((top >> 31) & 0x7fffffff));
+    const float d = fmaxf(a.m - m, -1e30f), f = ex2_approx(d * kLog2e);
+    float s = a.s * f, t = (a.t + a.s * d) * f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    return {m, s, t};
 }
 
 struct LpShared {
     u64 cand[LP_CAP];
+    u64 gather[LP_MAX_CLUSTER * kLogprobMaxTop];  // CTA 0: the cluster's largest, and statistics
+    LpStat gather_stat[LP_MAX_CLUSTER];
     u64 cut[LP_CUT];
     u64 groups[LP_GROUPS];
     u64 top[kLogprobMaxTop], joined[kLogprobMaxTop];
@@ -194,6 +203,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
     __shared__ LpShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row_i = blockIdx.x / C, rank = C > 1 ? (int)cluster_rank() : 0;
+    if (C > 1) cluster_arrive();  // every CTA has started, by the time the parts are sent to CTA 0
     pdl_wait();
     pdl_trigger();
     const T* row = logits + (size_t)row_i * ld;
@@ -271,7 +281,11 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
             nxt[u] = v >= 0 ? __ldcs(vec + v) : L::fill();
         }
     };
+    // the given token and its logit, two loads in turn, are on their way with the first vectors
+    const bool scores = logprob && rank == 0 && tid == 0;
+    const int tok = scores ? tokens[row_i] : -1;
     load(0);
+    const float tok_logit = tok >= 0 && tok < V ? L::one(row + tok) : 0.f;
     for (int step = 0; step < steps; ++step) {
         uint4 raw[U];
         float vmax[U];
@@ -296,8 +310,9 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
         };
         if (k > 0) {
             if (step == 0) {  // threshold from the first elements read
-                const uint32_t at = which([&](float v) { return v == mx; });  // the lowest bit is the lowest index
-                const int idx = at ? index_of(step, __ffs(at) - 1) : -1;
+                // the thread's largest, at the last index of the first vector that holds it: its own key is no smaller
+                const int at = vmax[0] == mx ? 0 : vmax[1] == mx ? 1 : vmax[2] == mx ? 2 : 3;
+                const int idx = mx == mx ? index_of(step, at * EPV + EPV - 1) : -1;
                 const u64 rep = idx >= 0 ? lp_key(mx, idx) : 0;
                 __syncthreads();  // the list's counters are set
                 set_tau(lp_threshold<LP_THREADS>(rep, k, sh));
@@ -339,23 +354,11 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
     }
 
     // join the threads' statistics
-    LpStat st{m, s2.x + s2.y, t2.x + t2.y};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const LpStat b{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-                       __shfl_xor_sync(0xffffffffu, st.t, o)};
-        st = lp_join(st, b);
-    }
+    LpStat st = lp_warp_join({m, s2.x + s2.y, t2.x + t2.y});
     if (lane == 0) sh.warp_stat[warp] = st;
     __syncthreads();
     if (warp == 0) {
-        st = lane < LP_WARPS ? sh.warp_stat[lane] : LpStat{kLowest, 0.f, 0.f};
-#pragma unroll
-        for (int o = LP_WARPS / 2; o > 0; o >>= 1) {
-            const LpStat b{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-                           __shfl_xor_sync(0xffffffffu, st.t, o)};
-            st = lp_join(st, b);
-        }
+        st = lp_warp_join(lane < LP_WARPS ? sh.warp_stat[lane] : LpStat{kLowest, 0.f, 0.f});
         if (lane == 0) sh.stat = st;
     }
     __syncthreads();
@@ -411,44 +414,35 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
         __syncthreads();
     }
 
-    if (C > 1) {  // CTA 0 joins the cluster's parts
-        cluster_sync();
-        if (rank == 0) {
-            if (k > 0) {
-                const int nk = C * k;
-                for (int i = tid; i < nk; i += LP_THREADS) sh.cand[i] = ld_cluster_u64(cluster_addr(&sh.top[i % k], i / k));
-                if (tid == 0) sh.n_cut = 0;
-                __syncthreads();
-                // (a cut list that overflows leaves the whole list, at most 512 keys, to be ranked)
-                if (!lp_select<LP_THREADS>(sh.cand, nk, k, sh, sh.joined)) lp_rank<1, LP_THREADS>(sh.cand, nk, k, sh.joined);
-            }
-            if (warp == LP_WARPS - 1) {
-                LpStat a{kLowest, 0.f, 0.f};
-                if (lane < C) {
-                    const uint32_t ad = cluster_addr(&sh.stat, lane);
-                    a = LpStat{ld_cluster_f32(ad), ld_cluster_f32(ad + 4), ld_cluster_f32(ad + 8)};
-                }
-#pragma unroll
-                for (int o = LP_MAX_CLUSTER / 2; o > 0; o >>= 1) {
-                    const LpStat b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                                   __shfl_xor_sync(0xffffffffu, a.t, o)};
-                    a = lp_join(a, b);
-                }
-                if (lane == 0) sh.warp_stat[0] = a;
-            }
+    if (C > 1) {  // every CTA sends its part to CTA 0, which joins them
+        cluster_wait();
+        if (tid < k) st_cluster_u64(cluster_addr(&sh.gather[rank * k + tid], 0), sh.top[tid]);
+        if (tid == LP_THREADS - 1) {
+            const uint32_t to = cluster_addr(&sh.gather_stat[rank], 0);
+            st_cluster_f32(to, sh.stat.m);
+            st_cluster_f32(to + 4, sh.stat.s);
+            st_cluster_f32(to + 8, sh.stat.t);
         }
-        cluster_sync();  // the other CTAs' shared memory stays until it has been read
+        if (tid == 0) sh.n_cut = 0;
+        cluster_sync();
         if (rank != 0) return;
+        if (warp == LP_WARPS - 1) {
+            st = lp_warp_join(lane < C ? sh.gather_stat[lane] : LpStat{kLowest, 0.f, 0.f});
+            if (lane == 0) sh.stat = st;
+        }
+        // (a cut list that overflows leaves the whole list, at most 512 keys, to be ranked)
+        if (k > 0 && !lp_select<LP_THREADS>(sh.gather, C * k, k, sh, sh.joined))
+            lp_rank<1, LP_THREADS>(sh.gather, C * k, k, sh.joined);
+        __syncthreads();
     }
-    const LpStat total = C > 1 ? sh.warp_stat[0] : sh.stat;
+    const LpStat total = sh.stat;
     const u64* top = C > 1 ? sh.joined : sh.top;
     // no distribution: NaN or +inf in the row (s is NaN), or nothing above -inf (s is 0)
     const float log_s = total.s > 0.f ? logf(total.s) : __uint_as_float(0x7fc00000u);
     if (tid == 0) {
         if (logprob) {
-            const int tok = tokens[row_i];
             const bool in = tok >= 0 && tok < V;
-            logprob[row_i] = in ? (L::one(row + tok) - total.m) - log_s : __uint_as_float(0x7fc00000u);
+            logprob[row_i] = in ? (tok_logit - total.m) - log_s : __uint_as_float(0x7fc00000u);
             if (!in && err) atomicOr(err, ERR_TOKEN);
         }
         if (entropy) entropy[row_i] = log_s - total.t / total.s;
