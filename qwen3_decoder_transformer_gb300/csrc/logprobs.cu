@@ -24,10 +24,11 @@ namespace {
 //
 // A cluster of C CTAs shares a row (C = 1 when there are rows enough) and CTA 0 joins the parts
 // through distributed shared memory: no workspace, one launch.
-// What bounds it. Many rows: HBM, 2048 x 151,936 fp32 with one alternative 197 us, 6.31 TB/s (93% of the measured copy);
-// bf16 has twice the elements a byte and is bound by their arithmetic, 124 us (5.0 TB/s), and with 32 alternatives by
-// the selection, 179. Few rows: the chain of a CTA, 8.0 us for one row of 151,936 with 20 alternatives (4.3 without:
-// launch, first loads, join), 12.7 for 64 rows with five (8.8 without).
+// What bounds it. Many rows: HBM, 2048 x 151,936 fp32 with one alternative 195 us, 6.38 TB/s (94% of the measured copy);
+// bf16 has twice the elements a byte and is bound by their arithmetic, 121 us (5.1 TB/s), and with 32 alternatives by
+// the selection, 176. Few rows: the chain of a CTA, 7.1 us for one row of 151,936 with 20 alternatives (3.4 without:
+// launch, first loads, join), 11.6 for 64 rows with five (7.7 without): at eight warps a scheduler each instruction that
+// every thread adds costs eight issue slots, and a threshold, a select and a join are some hundred instructions each.
 constexpr int LP_GROUPS = 64;           // groups of threads whose maxima give the threshold
 constexpr int LP_CAP = 2080;            // candidates of one CTA: a slice of fewer than 2048 + 14 elements fits whole
 constexpr int LP_CUT = 256, LP_RANK = 128, kFill = 64;
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
 
 // CTAs per row: as many as two on every SM take, while a slice keeps at least 4096 elements; clusters of eight and
 // sixteen only while they are few, since they wait for room in one part of the GPU (151,936 fp32 logits, five
-// alternatives: 16 rows by 4 CTAs 9.1 us, by 8 9.6, by 16 13.6; 4 rows 8.5, 7.9 and 7.2).
+// alternatives: 16 rows by 4 CTAs 8.2 us, by 8 8.6, by 16 11.4; 4 rows 7.6, 6.6 and 6.1).
 int lp_cluster(int M, int V) {
     int c = 1;
     while (c < LP_MAX_CLUSTER && (long long)M * c * 2 <= (c * 2 >= 8 ? 64 : 2 * device_sm_count()) && V / (2 * c) >= 4096)
@@ -471,9 +472,9 @@ cudaError_t token_logprobs_launch(const void* logits, int bf16, long long ld, in
                                   int* err, cudaStream_t st) {
     if (M <= 0) return cudaSuccess;
     // Many rows: CTAs of 256 threads, four an SM, so that one row's selection runs beside the others' loads (2048
-    // rows of 151,936 bf16 logits, one alternative 124 us against 137 with 512 threads, 32 alternatives 179
-    // against 212; fp32 198 and 197). Few rows: 512 threads, for a row's shorter chain (333 rows of 32,003 16.4 against
-    // 20.9, one row 8.0 against 9.2).
+    // rows of 151,936 bf16 logits, one alternative 121 us against 133 with 512 threads, 32 alternatives 176
+    // against 204; fp32 200 either way). Few rows: 512 threads, for a row's shorter chain (333 bf16 rows of 32,003, 32
+    // alternatives 15.2 against 20.0, one row 7.1 against 8.6).
     const int threads = M >= 8 * device_sm_count() ? 256 : 512;
     const int C = lp_cluster(M, V);
     const dim3 grid((unsigned)M * C), block(threads);
