@@ -30,8 +30,8 @@ namespace {
 // What bounds it. Many sequences: HBM, 64 sequences x 4,100 keys of 8 kv heads, dh 128 (1.08 GB) 151 us from call to call
 // (part of the keys still in L2), 158 us with a cold L2 under ncu, 6.8 TB/s (100% of the measured copy rate). Fragments loaded
 // straight from global memory, without rings, took 219 us for any split: too little on its way per warp. One
-// sequence: the chain of launch, length, first boxes and the join, 8.4 us for 4,100 keys by clusters of 16 CTAs
-// (13.7 by 4).
+// sequence: the chain of launch, length, first boxes and the join, 6.9 us for 4,100 keys by clusters of 16 CTAs
+// (13 by 4).
 constexpr int RG_KEYS = 16, RG_MAX_CLUSTER = 16, RG_MAX_G = 8, RG_WARPS = 4, RG_THREADS = 32 * RG_WARPS;
 constexpr int RG_MAX_PARTS = 1 + kPrefixMaxChunks;
 template <int DH, int RING>
@@ -62,7 +62,8 @@ struct RangeArgs {
     const float* recs;  // records of the prefix to join (attn_prefix_launch)
     int nrec, row_tiles;
     float* own;  // [B][Hkv][G][DH + 4]: where the own keys' (output sums, maximum, sum) go, to be joined by a launch of its own; or null
-    int C;  // CTAs per (sequence, kv head)
+    int C, log_c;    // CTAs per (sequence, kv head), a power of two
+    unsigned inv_g;  // 2^16 / G + 1: e / G = e * inv_g >> 16 for e < 2^8
     int* err;
 };
 
@@ -88,14 +89,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
 }
 // 16-byte piece `piece` (8 columns) of row `row` in boxes of 16 rows x 128 bytes written with the 128-byte swizzle
 __device__ __forceinline__ uint32_t rg_addr(uint32_t base, int row, int piece) {
@@ -134,12 +127,31 @@ __device__ __forceinline__ void add_scaled(float4& v, const float4& x, float f) 
     v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
 }
 
+// Head and first dim of quad e of the group's output (four dims of one head, the heads fastest).
+__device__ __forceinline__ void quad_of(const RangeArgs& a, int e, int& h, int& dd) {
+    const int d = (int)((unsigned)e * a.inv_g >> 16);
+    h = e - d * a.G;
+    dd = d * 4;
+}
+
+constexpr int RG_MAX_QUADS = RG_MAX_G * 32;
+union JoinShared {
+    struct {  // the own keys' part, then the prefix records
+        float pm[RG_MAX_G][RG_MAX_PARTS], pl[RG_MAX_G][RG_MAX_PARTS], inv[RG_MAX_G];
+    } records;
+    struct {  // this CTA's share of the output, [its quads][CTAs of the cluster]
+        float4 sums[RG_MAX_QUADS];
+        float2 stat[RG_MAX_QUADS];
+    } cluster;
+};
+
 // Join the own keys' result (own_stat(h) = (maximum, sum), output sums own_quad(h, dd)) and the prefix records by
 // log-sum-exp: O = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 template <int DH, typename Stat, typename Quad>
-__device__ __forceinline__ void join_records(const RangeArgs& a, int b, int j, float (&pm)[RG_MAX_G][RG_MAX_PARTS],
-                                             float (&pl)[RG_MAX_G][RG_MAX_PARTS], float (&inv)[RG_MAX_G], Stat own_stat,
-                                             Quad own_quad) {
+__device__ __forceinline__ void join_records(const RangeArgs& a, int b, int j, JoinShared& js, Stat own_stat, Quad own_quad) {
+    auto& pm = js.records.pm;
+    auto& pl = js.records.pl;
+    auto& inv = js.records.inv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int quads = a.G * (DH / 4), parts = 1 + a.nrec;
     const Records<DH> rec(a, b, j);
@@ -147,9 +159,11 @@ __device__ __forceinline__ void join_records(const RangeArgs& a, int b, int j, f
     constexpr int PRE = 8;
     float4 pre[PRE];
     const int e0 = threadIdx.x;
+    int h0, d0;
+    quad_of(a, e0, h0, d0);
 #pragma unroll
     for (int r = 0; r < PRE; ++r)
-        if (r < a.nrec && e0 < quads) pre[r] = rec.quad(r, e0 % a.G, e0 / a.G * 4);
+        if (r < a.nrec && e0 < quads) pre[r] = rec.quad(r, h0, d0);
     for (int e = threadIdx.x; e < parts * RG_MAX_G; e += RG_THREADS) {
         const int p = e / RG_MAX_G, h = e % RG_MAX_G;
         if (h < a.G) {
@@ -175,7 +189,8 @@ __device__ __forceinline__ void join_records(const RangeArgs& a, int b, int j, f
     }
     __syncthreads();
     for (int e = e0; e < quads; e += RG_THREADS) {
-        const int h = e % a.G, dd = e / a.G * 4;
+        int h, dd;
+        quad_of(a, e, h, dd);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         add_scaled(v, own_quad(h, dd), pm[h][0]);
         int r = 0;
@@ -190,19 +205,21 @@ __device__ __forceinline__ void join_records(const RangeArgs& a, int b, int j, f
     }
 }
 
-// The same over the a.C CTAs of a cluster, each of which finishes its share of the output: C neighbouring threads take one
-// quad of four dims, each one CTA's part (statistics cm, cl and sums so of that CTA's shared memory, all read at once)
-// and every C-th record, and add up by shuffles. (One thread a quad that read the parts in turn took 9.7 us for 4,100
-// keys of one sequence by clusters of 16, this 8.5.)
+// The same over the a.C CTAs of a cluster, which have sent every CTA their parts of its share of the output (quad e is CTA
+// e mod C's): C neighbouring threads take one quad, each one CTA's part and every C-th record, and add up by shuffles.
+// (4,100 keys of one sequence by clusters of 16: one thread a quad reading the other CTAs' parts in turn 9.7 us, C threads
+// reading them at once 8.4; sent, with one copy a unit and no divisions, 6.9.)
 template <int DH>
-__device__ __forceinline__ void join_cluster(const RangeArgs& a, int b, int j, int rank, const float* cm, const float* cl,
-                                             const float* so, int pitch) {
-    const int C = a.C, p = threadIdx.x % C, nq = a.G * (DH / 4) / C;  // C, a power of two up to 16, divides DH / 4
+__device__ __forceinline__ void join_cluster(const RangeArgs& a, int b, int j, int rank, const JoinShared& js) {
+    const int C = a.C, quads = a.G * (DH / 4), p = threadIdx.x & (C - 1);  // C, up to 16, divides quads
     const Records<DH> rec(a, b, j);
-    for (int q0 = 0; q0 < nq; q0 += RG_THREADS / C) {
-        const int q = q0 + threadIdx.x / C, e = rank * nq + min(q, nq - 1), h = e % a.G, dd = e / a.G * 4;
-        const float m = ld_cluster_f32(cluster_addr(cm + h, p)), l = ld_cluster_f32(cluster_addr(cl + h, p));
-        const float4 x = ld_cluster_f32x4(cluster_addr(so + h * pitch + dd, p));
+    for (int t0 = 0; t0 < quads; t0 += RG_THREADS) {
+        const bool on = t0 + threadIdx.x < quads;
+        const int t = on ? t0 + threadIdx.x : p;
+        int h, dd;
+        quad_of(a, (t & ~(C - 1)) + rank, h, dd);
+        const float m = js.cluster.stat[t].x, l = js.cluster.stat[t].y;
+        const float4 x = js.cluster.sums[t];
         constexpr int PRE = 4;
         float2 rml[PRE];
         float4 rx[PRE];
@@ -242,7 +259,7 @@ __device__ __forceinline__ void join_cluster(const RangeArgs& a, int b, int j, i
             v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
             v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
         }
-        if (p == 0 && q < nq) store_quad<DH>(a, b, j, h, dd, v, L == 0.f ? 0.f : 1.f / L);
+        if (p == 0 && on) store_quad<DH>(a, b, j, h, dd, v, L == 0.f ? 0.f : 1.f / L);
     }
 }
 
@@ -259,8 +276,7 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
     __shared__ uint64_t bars[RG_WARPS][2 * ST];                 // [K of each stage, V of each stage]
     __shared__ float sm[NW][RG_MAX_G], sl[NW][RG_MAX_G];
     __shared__ float cm[RG_MAX_G], cl[RG_MAX_G];                   // this CTA's maximum and sum
-    __shared__ float pm[RG_MAX_G][RG_MAX_PARTS], pl[RG_MAX_G][RG_MAX_PARTS];  // of the own keys, then of the prefix records
-    __shared__ float inv[RG_MAX_G];
+    __shared__ JoinShared js;
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -268,6 +284,7 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
     const int rank = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
     uint64_t* k_full = bars[warp];
     uint64_t* v_full = bars[warp] + ST;
+    if (a.C > 1) cluster_arrive();  // every CTA has started, by the time parts are sent
     if (threadIdx.x == 0) abort_sh = 0;
     if (lane == 0) {
         for (int i = 0; i < 2 * ST; ++i) mbar_init(&bars[warp][i], 1);
@@ -341,7 +358,7 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
         valid = min(RG_KEYS, c - (u - first) * RG_KEYS);
         return r + (u - first) * RG_KEYS;
     };
-    const int u0 = (int)((long long)units * rank / a.C), u1 = (int)((long long)units * (rank + 1) / a.C);
+    const int u0 = (int)((unsigned)units * (unsigned)rank >> a.log_c), u1 = (int)((unsigned)units * (rank + 1u) >> a.log_c);
     const int mine = u1 - u0 > warp ? (u1 - u0 - warp + NW - 1) / NW : 0;  // units u0 + warp + NW i
 
     uint8_t* ring_p = rings + warp * RG_BYTES;
@@ -353,8 +370,7 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
         const int z = prefix ? j : b * a.Hkv + j;
         uint8_t* dst = ring_p + st * 2 * Ly::HALF + off;
         mbar_expect_tx(&full[st], Ly::HALF);
-#pragma unroll
-        for (int c = 0; c < Ly::NCH; ++c) tma_load_3d(dst + c * Ly::BOX, prefix ? pmap : map, &full[st], c * 64, y, z);
+        tma_load_4d(dst, prefix ? pmap : map, &full[st], 0, y, 0, z);
     };
     auto load_k = [&](int i) { load(i, &tmK, &tmPK, k_full, 0); };  // lane 0: K or V of unit i
     auto load_v = [&](int i) { load(i, &tmV, &tmPV, v_full, Ly::HALF); };
@@ -476,8 +492,10 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
     const int quads = a.G * (DH / 4);
     const bool alone = a.C == 1 && a.nrec == 0;
     float* own = a.own ? a.own + ((size_t)b * a.Hkv + j) * a.G * (DH + 4) : nullptr;
+    if (a.C > 1) cluster_wait();
     for (int e = threadIdx.x; e < quads; e += THREADS) {  // join the warps
-        const int h = e % a.G, dd = e / a.G * 4;
+        int h, dd;
+        quad_of(a, e, h, dd);
         float M = sm[0][h], L = 0.f;
 #pragma unroll
         for (int w = 1; w < NW; ++w) M = fmaxf(M, sm[w][h]);
@@ -494,6 +512,10 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
             if (dd == 0) *reinterpret_cast<float2*>(own + h * (DH + 4) + DH) = make_float2(M, L);
         } else if (alone) {
             store_quad<DH>(a, b, j, h, dd, v, L == 0.f ? 0.f : 1.f / L);  // no visible key: zeros
+        } else if (a.C > 1) {
+            const int owner = e & (a.C - 1), slot = e - owner + rank;
+            st_cluster_f32x4(cluster_addr(&js.cluster.sums[slot], owner), v);
+            st_cluster_f32x2(cluster_addr(&js.cluster.stat[slot], owner), make_float2(M, L));
         } else {
             *reinterpret_cast<float4*>(&so[0][h][dd]) = v;
             if (dd == 0) {
@@ -516,12 +538,11 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
     }
     if (a.C > 1) {
         cluster_sync();
-        join_cluster<DH>(a, b, j, rank, cm, cl, &so[0][0][0], Ly::PITCH);
-        cluster_sync();  // every CTA's partial stays in shared memory until the others have read it
+        join_cluster<DH>(a, b, j, rank, js);
     } else {
         __syncthreads();
         join_records<DH>(
-            a, b, j, pm, pl, inv, [&](int h) { return make_float2(cm[h], cl[h]); },
+            a, b, j, js, [&](int h) { return make_float2(cm[h], cl[h]); },
             [&](int h, int dd) { return *reinterpret_cast<const float4*>(&so[0][h][dd]); });
     }
 }
@@ -529,13 +550,13 @@ __global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
 // The own keys' results (attn_ranges_kernel with a.own) and the prefix records of one (sequence, kv head).
 template <int DH>
 __global__ void __launch_bounds__(RG_THREADS) attn_join_kernel(const RangeArgs a) {
-    __shared__ float pm[RG_MAX_G][RG_MAX_PARTS], pl[RG_MAX_G][RG_MAX_PARTS], inv[RG_MAX_G];
+    __shared__ JoinShared js;
     const int j = blockIdx.x, b = blockIdx.y;
     const float* own = a.own + ((size_t)b * a.Hkv + j) * a.G * (DH + 4);
     pdl_trigger();
     pdl_wait();
     join_records<DH>(
-        a, b, j, pm, pl, inv, [&](int h) { return __ldcg(reinterpret_cast<const float2*>(own + h * (DH + 4) + DH)); },
+        a, b, j, js, [&](int h) { return __ldcg(reinterpret_cast<const float2*>(own + h * (DH + 4) + DH)); },
         [&](int h, int dd) { return __ldcg(reinterpret_cast<const float4*>(own + h * (DH + 4) + dd)); });
 }
 
@@ -581,17 +602,19 @@ cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfl
                              int max_keys, int free_sms, cudaStream_t st) {
     CUtensorMap maps[4];  // K and V of the caches and of the prefix
     const uint64_t heads = (uint64_t)B * a.Hkv;
-    if (!encode_tmap_bf16_rows(&maps[0], k, DH, a.cap, a.cap, heads, RG_KEYS) ||
-        !encode_tmap_bf16_rows(&maps[1], v, DH, a.cap, a.cap, heads, RG_KEYS))
+    if (!encode_tmap_bf16_units(&maps[0], k, DH, a.cap, a.cap, heads, RG_KEYS) ||
+        !encode_tmap_bf16_units(&maps[1], v, DH, a.cap, a.cap, heads, RG_KEYS))
         return cudaErrorInvalidValue;
     if (a.P == 0) {
         maps[2] = maps[0];
         maps[3] = maps[1];
-    } else if (!encode_tmap_bf16_rows(&maps[2], p.k, DH, a.P, p.cap, a.Hkv, RG_KEYS) ||
-               !encode_tmap_bf16_rows(&maps[3], p.v, DH, a.P, p.cap, a.Hkv, RG_KEYS)) {
+    } else if (!encode_tmap_bf16_units(&maps[2], p.k, DH, a.P, p.cap, a.Hkv, RG_KEYS) ||
+               !encode_tmap_bf16_units(&maps[3], p.v, DH, a.P, p.cap, a.Hkv, RG_KEYS)) {
         return cudaErrorInvalidValue;
     }
     a.C = ranges_cluster(B, a.Hkv, max_keys, a.nrec > 0);
+    while (1 << a.log_c < a.C) ++a.log_c;
+    a.inv_g = 65536u / a.G + 1;
     // Four small CTAs an SM start and end fastest and stream as well as larger ones; only a CTA with a long cache of its own
     // gains from three units a warp on their way, two CTAs an SM (64 sequences x 4100 keys, a cold L2, 176 us against 186; x 1024
     // keys 43.8 against 41.9).
