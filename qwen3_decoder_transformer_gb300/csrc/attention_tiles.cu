@@ -201,15 +201,13 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                         tma_load_4d(smem + cc * TL_BM * 128, &tmQ, q_full, cc * 64, 0, it.h, it.b * tile_seqs);
                 } else {
                     mbar_expect_tx(q_full, Ly::Q_BYTES);
-                    for (int cc = 0; cc < NCH; ++cc)
-                        tma_load_3d(smem + cc * TL_BM * 128, &tmQ, q_full, cc * 64, it.q0, it.b * Hq + it.h);
+                    tma_load_4d(smem, &tmQ, q_full, 0, it.q0, 0, it.b * Hq + it.h);
                 }
                 for (int i = 0; i < it.n_tiles; ++i, ++g) {
                     const int s = g % KST, y = tile_row(tile_of(it, i)), z = PREFIX ? jkv : it.b * Hkv + jkv;
                     if (!mbar_wait_suspend(&k_empty[s], ((g / KST) & 1) ^ 1, abort_flag)) { ok = false; break; }
                     mbar_expect_tx(&k_full[s], Ly::KV_BYTES);
-                    for (int cc = 0; cc < NCH; ++cc)
-                        tma_load_3d(smem + Ly::K_OFF + s * Ly::KV_BYTES + cc * TL_BN * 128, &tmK, &k_full[s], cc * 64, y, z);
+                    tma_load_4d(smem + Ly::K_OFF + s * Ly::KV_BYTES, &tmK, &k_full[s], 0, y, 0, z);
                 }
             }
         }
@@ -277,8 +275,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                 if (lane == 0) {
                     const int y = tile_row(j);
                     mbar_expect_tx(&v_full[s], Ly::KV_BYTES);
-                    for (int cc = 0; cc < NCH; ++cc)
-                        tma_load_3d(smem + Ly::V_OFF + s * Ly::KV_BYTES + cc * TL_BN * 128, &tmV, &v_full[s], cc * 64, y, z);
+                    tma_load_4d(smem + Ly::V_OFF + s * Ly::KV_BYTES, &tmV, &v_full[s], 0, y, 0, z);
                 }
                 __syncwarp();
                 if (pend && !clean()) { ok = false; break; }
@@ -532,8 +529,9 @@ cudaError_t prefill_sinks_launch_dh(const __nv_bfloat16* q, const __nv_bfloat16*
                                     int Hq, int Hkv, int cap, const int* len0, int len_stride, SinkMap sm,
                                     __nv_bfloat16* out, int* err, cudaStream_t st) {
     CUtensorMap tq, tk, tv;
-    if (!encode_tmap_bf16_3d(&tq, q, DH, T, (uint64_t)B * Hq) || !encode_tmap_bf16_3d(&tk, kc, DH, cap, (uint64_t)B * Hkv) ||
-        !encode_tmap_bf16_3d(&tv, vc, DH, cap, (uint64_t)B * Hkv))
+    if (!encode_tmap_bf16_units(&tq, q, DH, T, T, (uint64_t)B * Hq, TL_BM) ||
+        !encode_tmap_bf16_units(&tk, kc, DH, cap, cap, (uint64_t)B * Hkv, TL_BN) ||
+        !encode_tmap_bf16_units(&tv, vc, DH, cap, cap, (uint64_t)B * Hkv, TL_BN))
         return cudaErrorInvalidValue;
     TileArgs a{};
     a.T = T;
@@ -559,8 +557,8 @@ cudaError_t prefix_launch_dh(const __nv_bfloat16* q, const __nv_bfloat16* kp, co
     const int G = Hq / Hkv;
     CUtensorMap tq, tk, tv;
     if (!encode_tmap_bf16_groups(&tq, q, DH, G, Hkv, B, TL_BM / G) ||
-        !encode_tmap_bf16_rows(&tk, kp, DH, P, prefix_cap, Hkv, TL_BN) ||
-        !encode_tmap_bf16_rows(&tv, vp, DH, P, prefix_cap, Hkv, TL_BN))
+        !encode_tmap_bf16_units(&tk, kp, DH, P, prefix_cap, Hkv, TL_BN) ||
+        !encode_tmap_bf16_units(&tv, vp, DH, P, prefix_cap, Hkv, TL_BN))
         return cudaErrorInvalidValue;
     TileArgs a{};
     a.T = P;

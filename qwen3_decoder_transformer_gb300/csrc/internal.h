@@ -133,10 +133,8 @@ struct GemmMaps {
     CUtensorMap a, b, c, r, v;
 };
 bool encode_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2);
-// Rows [heads][rows of row_cap][dh] in boxes of 64 x box_rows x 1; rows past `rows` read as zero.
-bool encode_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t dh, uint64_t rows, uint64_t row_cap,
-                           uint64_t heads, uint32_t box_rows);
-// The same rows in boxes of box_rows whole rows, stored as dh / 64 halves of 64 columns: coordinates (0, row, 0, head).
+// Rows [heads][rows of row_cap][dh] in boxes of box_rows whole rows, stored as dh / 64 parts of 64 columns; coordinates
+// (0, row, 0, head), rows past `rows` read as zero.
 bool encode_tmap_bf16_units(CUtensorMap* map, const void* base, uint64_t dh, uint64_t rows, uint64_t row_cap,
                             uint64_t heads, uint32_t box_rows);
 // Query rows [seqs][heads][group][dh] in boxes of 64 x group x 1 x box_seqs: one head's groups of box_seqs sequences.
