@@ -139,17 +139,18 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
         const int k = round * G + ((round & 1) ? G - 1 - cta : cta);
         if (k >= n_items) return it;
         if constexpr (PREFIX) {
-            it.b = k % a.row_tiles;  // row tile
-            it.h = k / a.row_tiles % Hkv;
-            it.chunk = k / (a.row_tiles * Hkv);
-            const long long tiles = ((long long)T + TL_BN - 1) / TL_BN;
-            it.skip = (int)(tiles * it.chunk / a.chunks);
-            it.n_tiles = (int)(tiles * (it.chunk + 1) / a.chunks) - it.skip;
+            const unsigned strip = (unsigned)k / (unsigned)a.row_tiles;  // (kv head, chunk)
+            it.b = k - (int)strip * a.row_tiles;                         // row tile
+            it.chunk = (int)(strip / (unsigned)Hkv);
+            it.h = (int)strip - it.chunk * Hkv;
+            const unsigned tiles = ((unsigned)T + TL_BN - 1) / TL_BN;  // at most 2^23, by at most 64 chunks
+            it.skip = (int)(tiles * it.chunk / (unsigned)a.chunks);
+            it.n_tiles = (int)(tiles * (it.chunk + 1) / (unsigned)a.chunks) - it.skip;
         } else {
-            const int rem = k % per_qt;
-            it.q0 = (n_qt - 1 - k / per_qt) * TL_BM;  // the longest key ranges first
-            it.b = rem / Hq;
-            it.h = rem % Hq;
+            const int from_end = (int)((unsigned)k / (unsigned)per_qt), rem = k - from_end * per_qt;
+            it.q0 = (n_qt - 1 - from_end) * TL_BM;  // the longest key ranges first
+            it.b = (int)((unsigned)rem / (unsigned)Hq);
+            it.h = rem - it.b * Hq;
             it.q_end = min(T, it.q0 + TL_BM);
             it.len0 = min(max(0, a.len0[(size_t)it.b * a.len_stride]), a.len_max);
             const int jw = max(0, it.len0 + it.q0 - a.window + 1) / TL_BN;  // first tile of the window
