@@ -60,7 +60,7 @@ struct RangeArgs {
     const int* meta;    // own slots of a shared prefix: SeqMap::meta, or null
     int P;              // rows of the prefix that each sequence reads for itself, as a third run (0: none, or by records)
     const float* recs;  // records of the prefix to join (attn_prefix_launch)
-    int nrec, row_tiles;
+    int nrec, row_tiles, tile_seqs;  // sequences of a row tile
     float* own;  // [B][Hkv][G][DH + 4]: where the own keys' (output sums, maximum, sum) go, to be joined by a launch of its own; or null
     int C, log_c;    // CTAs per (sequence, kv head), a power of two
     unsigned inv_g;  // 2^16 / G + 1: e / G = e * inv_g >> 16 for e < 2^8
@@ -110,9 +110,9 @@ struct Records {
     size_t step;  // between two key chunks
     int row;
     __device__ __forceinline__ Records(const RangeArgs& a, int b, int j) {
-        const int seqs = kPrefixRows / a.G;
-        row = b % seqs * a.G;
-        rec = a.recs + ((size_t)j * a.row_tiles + b / seqs) * prefix_rec_floats(DH);
+        const int tile = (int)((unsigned)b / (unsigned)a.tile_seqs);
+        row = (b - tile * a.tile_seqs) * a.G;
+        rec = a.recs + ((size_t)j * a.row_tiles + tile) * prefix_rec_floats(DH);
         step = (size_t)a.Hkv * a.row_tiles * prefix_rec_floats(DH);
     }
     __device__ __forceinline__ float4 quad(int r, int h, int dd) const {
@@ -212,7 +212,7 @@ __device__ __forceinline__ void join_records(const RangeArgs& a, int b, int j, J
 template <int DH>
 __device__ __forceinline__ void join_cluster(const RangeArgs& a, int b, int j, int rank, const JoinShared& js) {
     const int C = a.C, quads = a.G * (DH / 4), p = threadIdx.x & (C - 1);  // C, up to 16, divides quads
-    const Records<DH> rec(a, b, j);
+    const Records<DH> rec(a, b, j);  // (not read without records)
     for (int t0 = 0; t0 < quads; t0 += RG_THREADS) {
         const bool on = t0 + threadIdx.x < quads;
         const int t = on ? t0 + threadIdx.x : p;
@@ -615,6 +615,7 @@ cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfl
     a.C = ranges_cluster(B, a.Hkv, max_keys, a.nrec > 0);
     while (1 << a.log_c < a.C) ++a.log_c;
     a.inv_g = 65536u / a.G + 1;
+    a.tile_seqs = kPrefixRows / a.G;
     // Four small CTAs an SM start and end fastest and stream as well as larger ones; only a CTA with a long cache of its own
     // gains from three units a warp on their way, two CTAs an SM (64 sequences x 4100 keys, a cold L2, 176 us against 186; x 1024
     // keys 43.8 against 41.9).

@@ -197,13 +197,13 @@ template <typename T, int LP_THREADS>
 __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
     token_logprobs_kernel(const T* __restrict__ logits, long long ld, int V, const int32_t* __restrict__ tokens, int k,
                           float* __restrict__ logprob, float* __restrict__ entropy, int32_t* __restrict__ top_ids,
-                          float* __restrict__ top_logprobs, int C, int* err) {
+                          float* __restrict__ top_logprobs, int log_c, int* err) {
     using L = LpLoad<T>;
     constexpr int LP_WARPS = LP_THREADS / 32;
     constexpr int EPV = L::EPV, U = 4;  // U vectors a thread and step
     __shared__ LpShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row_i = blockIdx.x / C, rank = C > 1 ? (int)cluster_rank() : 0;
+    const int C = 1 << log_c, row_i = blockIdx.x >> log_c, rank = C > 1 ? (int)cluster_rank() : 0;
     if (C > 1) cluster_arrive();  // every CTA has started, by the time the parts are sent to CTA 0
     pdl_wait();
     pdl_trigger();
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
     // (CTA C - 1) taken one by one
     const int head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T)));
     const int nv = (V - head) / EPV;
-    const int v0 = (int)((long long)nv * rank / C), n = (int)((long long)nv * (rank + 1) / C) - v0;
+    const int v0 = (int)((long long)nv * rank >> log_c), n = (int)((long long)nv * (rank + 1) >> log_c) - v0;
     const uint4* vec = reinterpret_cast<const uint4*>(row + head) + v0;
     const int base = head + v0 * EPV;  // index of the slice's first vector element
     int one = -1;                      // this thread's single element, if any
@@ -477,10 +477,12 @@ cudaError_t token_logprobs_launch(const void* logits, int bf16, long long ld, in
     // alternatives 15.2 against 20.0, one row 7.1 against 8.6).
     const int threads = M >= 8 * device_sm_count() ? 256 : 512;
     const int C = lp_cluster(M, V);
+    int log_c = 0;
+    while (1 << log_c < C) ++log_c;
     const dim3 grid((unsigned)M * C), block(threads);
     auto launch = [&](auto kernel, auto x) {
         return launch_pdl_cluster(kernel, grid, block, C, 0, st, x, ld, V, tokens, top_k, logprob, entropy, top_ids,
-                                  top_logprobs, C, err);
+                                  top_logprobs, log_c, err);
     };
     if (bf16) {
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(logits);
