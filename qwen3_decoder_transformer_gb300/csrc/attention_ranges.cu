@@ -20,8 +20,10 @@ namespace {
 //
 // Every warp works through its own units alone, with a running maximum (lazily rescaled, as in the prefill
 // kernels): its lane 0 keeps a ring full with the K and V boxes of the coming units (TMA, 128-byte
-// swizzle), so up to 192 KB an SM are on their way or in use, four times what HBM latency x bandwidth
-// needs, and no barrier joins the warps before the end. The products are warp-level mma (m16n8k16,
+// swizzle; a stage's keys are asked for again right after its scores, its values after P V), so up to 128 KB an SM are on
+// their way or in use, and no barrier joins the warps before the end. Three units a warp with two CTAs an SM instead of one
+// unit with four stream no faster (64 sequences x 4,100 keys 152.5 us against 153.4) and start slower (one sequence 7.5
+// against 6.8). The products are warp-level mma (m16n8k16,
 // bf16 in, fp32 accumulate; the contraction is far below a tcgen05 tile) with the heads of the kv group as
 // the 8 columns: S^T (keys x heads) = K q^T, P^T from accumulator to operand layout by a register transpose
 // (movmatrix), O^T (head_dim x heads) += V^T P^T.
@@ -34,19 +36,19 @@ namespace {
 // (13 by 4).
 constexpr int RG_KEYS = 16, RG_MAX_CLUSTER = 16, RG_MAX_G = 8, RG_WARPS = 4, RG_THREADS = 32 * RG_WARPS;
 constexpr int RG_MAX_PARTS = 1 + kPrefixMaxChunks;
-template <int DH, int RING>
+constexpr int RG_CTAS = 4;  // an SM
+template <int DH>
 struct RgLayout {
     static constexpr int NCH = DH / 64;               // 64-column boxes of a row
     static constexpr int BOX = RG_KEYS * 128;         // bytes of a box
     static constexpr int HALF = NCH * BOX;            // K (or V) of a unit
-    static constexpr int RG_BYTES = RING * 8192;      // ring of one warp
-    static constexpr int ST = RG_BYTES / (2 * HALF);  // units in it: RING (dh 128) or 2 RING (dh 64)
+    static constexpr int RG_BYTES = 8192;             // ring of one warp
+    static constexpr int ST = RG_BYTES / (2 * HALF);  // units in it: 1 (dh 128) or 2 (dh 64)
     static constexpr int SMEM = RG_WARPS * RG_BYTES + 1024;
-    static constexpr int CTAS = RING == 3 ? 2 : 4;  // an SM
     // the warps' results take the first bytes of the rings once all of them are done
     static constexpr int PITCH = DH + 4;
     static_assert(RG_WARPS * RG_MAX_G * PITCH * 4 <= RG_WARPS * RG_BYTES, "results fit the rings");
-    static_assert(CTAS * (SMEM + 8192) <= 227 * 1024, "shared memory");
+    static_assert(RG_CTAS * (SMEM + 8192) <= 227 * 1024, "shared memory");
 };
 
 struct RangeArgs {
@@ -263,11 +265,11 @@ __device__ __forceinline__ void join_cluster(const RangeArgs& a, int b, int j, i
     }
 }
 
-template <int DH, bool SINKS, int RING>
-__global__ void __launch_bounds__(RG_THREADS, RgLayout<DH, RING>::CTAS)
+template <int DH, bool SINKS>
+__global__ void __launch_bounds__(RG_THREADS, RG_CTAS)
     attn_ranges_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ CUtensorMap tmPK, const __grid_constant__ CUtensorMap tmPV, const RangeArgs a) {
-    using Ly = RgLayout<DH, RING>;
+    using Ly = RgLayout<DH>;
     constexpr int NW = RG_WARPS, THREADS = RG_THREADS, ST = Ly::ST, RG_BYTES = Ly::RG_BYTES;
     extern __shared__ uint8_t rg_raw[];
     const uint32_t raw_addr = smem_u32(rg_raw);
@@ -561,16 +563,16 @@ __global__ void __launch_bounds__(RG_THREADS) attn_join_kernel(const RangeArgs a
 }
 
 // Whether an own CTA for every (sequence, kv head) can run on the SMs that the prefix kernel leaves.
-bool fits_beside_prefix(int B, int Hkv, int dh, int free_sms) {
-    return (long long)B * Hkv <= (long long)free_sms * (dh == 128 ? RgLayout<128, 1>::CTAS : RgLayout<64, 1>::CTAS);
+bool fits_beside_prefix(int B, int Hkv, int free_sms) {
+    return (long long)B * Hkv <= (long long)free_sms * RG_CTAS;
 }
 
 // CTAs per (sequence, kv head). Clusters of up to four CTAs while all CTAs fit the GPU (four an SM), of eight while they
 // are two an SM at most and of sixteen while they are one, since larger clusters wait for room in one part of the GPU; each
 // warp keeps a 16-key unit, two once there is a CTA for every SM and in clusters of sixteen, eight past two CTAs an SM.
-// Measured (us, caches from HBM, 8 kv heads, dh 128): 1 sequence of 4096 keys by 8 CTAs 11.2, by 16 9.3; 4 by 8 15.7, by 16 20.5;
-// 8 of 1024 keys by 4 10.4, by 8 11.3; 16 of 4096 by 2 44.8, by 4 42.7; 32 of 4096 by 1 82.4, by 2 80.2; 1 of 1024 by 8 5.5, by 16
-// 6.1; 32 of 256 by 1 9.1, by 2 10.7. Beside a prefix kernel: two CTAs an SM at most, since they cannot all start
+// Measured (us, caches from HBM, 8 kv heads, dh 128): 1 sequence of 4096 keys by 8 CTAs 10.7, by 16 8.3; 4 by 8 15.0, by 16 17.5;
+// 8 of 1024 keys by 4 9.7, by 8 10.1; 16 of 4096 by 2 44.1, by 4 42.4; 32 of 4096 by 1 82.2, by 2 79.9; 1 of 1024 by 8 4.7, by 16
+// 4.9; 32 of 256 by 1 8.9, by 2 10.0. Beside a prefix kernel: two CTAs an SM at most, since they cannot all start
 // before its CTAs end.
 int ranges_cluster(int B, int Hkv, int max_keys, bool beside) {
     const long long sms = device_sm_count();
@@ -591,12 +593,6 @@ struct Prefix {
     int cap;
 };
 
-template <int DH, bool SINKS, int RING>
-cudaError_t ranges_launch_ring(const CUtensorMap (&maps)[4], const RangeArgs& a, int B, cudaStream_t st) {
-    return launch_pdl_cluster(attn_ranges_kernel<DH, SINKS, RING>, dim3(a.C, a.Hkv, B), dim3(RG_THREADS), a.C,
-                              RgLayout<DH, RING>::SMEM, st, maps[0], maps[1], maps[2], maps[3], a);
-}
-
 template <int DH, bool SINKS>
 cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfloat16* v, const Prefix& p, int B,
                              int max_keys, int free_sms, cudaStream_t st) {
@@ -616,15 +612,11 @@ cudaError_t ranges_launch_dh(RangeArgs a, const __nv_bfloat16* k, const __nv_bfl
     while (1 << a.log_c < a.C) ++a.log_c;
     a.inv_g = 65536u / a.G + 1;
     a.tile_seqs = kPrefixRows / a.G;
-    // Four small CTAs an SM start and end fastest and stream as well as larger ones; only a CTA with a long cache of its own
-    // gains from three units a warp on their way, two CTAs an SM (64 sequences x 4100 keys, a cold L2, 176 us against 186; x 1024
-    // keys 43.8 against 41.9).
-    const int ring = a.nrec == 0 && a.C == 1 && max_keys >= 2048 ? 3 : 1;
     // Own CTAs that cannot all run beside the prefix kernel would keep the others out while they wait for its
     // records: their results then go through memory to a launch that joins them.
-    if (a.nrec == 0 || a.C > 1 || fits_beside_prefix(B, a.Hkv, DH, free_sms)) a.own = nullptr;
-    if (ring == 3) return ranges_launch_ring<DH, SINKS, 3>(maps, a, B, st);
-    const cudaError_t e = ranges_launch_ring<DH, SINKS, 1>(maps, a, B, st);
+    if (a.nrec == 0 || a.C > 1 || fits_beside_prefix(B, a.Hkv, free_sms)) a.own = nullptr;
+    const cudaError_t e = launch_pdl_cluster(attn_ranges_kernel<DH, SINKS>, dim3(a.C, a.Hkv, B), dim3(RG_THREADS), a.C,
+                                             RgLayout<DH>::SMEM, st, maps[0], maps[1], maps[2], maps[3], a);
     if (e != cudaSuccess || !a.own) return e;
     return launch_pdl(attn_join_kernel<DH>, dim3(a.Hkv, B), dim3(RG_THREADS), 0, st, a);
 }
@@ -638,12 +630,12 @@ cudaError_t ranges_launch(const RangeArgs& a, const __nv_bfloat16* k, const __nv
 }
 
 // Clusters of sixteen CTAs are beyond the portable size.
-template <int DH, bool SINKS, int RING>
+template <int DH, bool SINKS>
 cudaError_t ranges_prepare() {
-    const void* f = (const void*)attn_ranges_kernel<DH, SINKS, RING>;
+    const void* f = (const void*)attn_ranges_kernel<DH, SINKS>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, RgLayout<DH, RING>::SMEM);
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, RgLayout<DH>::SMEM);
 }
 
 // Key chunks of the prefix. The prefix kernel runs one CTA an SM, the own keys' CTAs run on the SMs it leaves, so
@@ -653,8 +645,8 @@ cudaError_t ranges_prepare() {
 // more than 5 TB/s (the row tiles of a chunk share its keys), and 4.5 us for its start and end; an SM's own CTAs read
 // 55 GB/s; a join launch takes 2.5 us, records past the eighth 0.5 us each (they are not read ahead); half of the own
 // cache is taken to be filled. Measured (us, dh 128, 8 kv heads): 64 sequences, 32768 keys, 32 heads, 512 own keys on average,
-// 6 chunks 50, 9 chunks 57; 4096 keys, 16 heads, 256 own keys, 3 chunks 15.5, 19 chunks 27; 16 sequences, 8192 keys, 32 heads,
-// 8 chunks 14.4, 13 chunks 16.7; 8 sequences, 32768 keys, 9 chunks 31.9, 16 chunks 33.4, 5 chunks 45.9.
+// 6 chunks 47, 9 chunks 53; 4096 keys, 16 heads, 256 own keys, 3 chunks 14.5, 19 chunks 23.6; 16 sequences, 8192 keys, 32 heads,
+// 8 chunks 12.9, 13 chunks 15.7; 8 sequences, 32768 keys, 9 chunks 30.3, 16 chunks 31.5, 5 chunks 44.
 constexpr int kPrefixMaxRounds = 2;
 int prefix_max_chunks(int B, int Hq, int Hkv, int P) {
     const long long tiles = (P + 127ll) / 128, items = (long long)prefix_row_tiles(B, Hq / Hkv) * Hkv;
@@ -675,7 +667,7 @@ int prefix_chunks(int B, int Hq, int Hkv, int dh, int P, int own_cap) {
         const double per_tile = std::max(0.9, running / row_tiles * tile / prefix_hbm);
         const double t_prefix = rounds * (((tiles + c - 1) / c) * per_tile + 4.5);
         const double rate = n < sms ? std::min(hbm, (sms - n) * sm_rate) : 0;
-        const bool join = !fits_beside_prefix(B, Hkv, dh, (int)std::max<long long>(0, sms - n));
+        const bool join = !fits_beside_prefix(B, Hkv, (int)std::max<long long>(0, sms - n));
         const double t = std::max(t_prefix + std::max(0.0, own - rate * t_prefix) / hbm, (own + Hkv * tiles * tile) / hbm) +
                          0.05 * c + 0.5 * std::max(0, c - 8) + (join ? 2.5 : 0);
         if (c == 1 || t < best_t) {
@@ -688,9 +680,9 @@ int prefix_chunks(int B, int Hq, int Hkv, int dh, int P, int own_cap) {
 
 // Whether every sequence reads the prefix (if there is one) for itself, in one launch: little to read again (from L2, about 10 TB/s) costs
 // less than the prefix kernel and its records. Measured (us, here against with records; 16 query heads, 8 kv heads, dh 128,
-// own caches of 64 slots): 1 sequence, 600 keys 5.9 / 8.1, 4096 8.6 / 11.5; 2 at 4096 9.5 / 11.4; 16 at 600 8.9 / 8.2; 4 at 4096
-// 11.5 / 11.2. Where the own keys already fill the GPU the second reading is not hidden: 64 sequences, 128 keys, 512 own
-// slots 16.4 / 13.2, 64 own slots 5.9 / 7.8. And the host has one launch to make: 8.9 us a call against 11.3.
+// own caches of 64 slots): 1 sequence, 600 keys 4.3 / 7.3, 4096 6.7 / 9.9; 2 at 4096 8.5 / 10.0; 16 at 600 7.0 / 7.4; 8 at 2048
+// 8.8 / 8.3. Where the own keys already fill the GPU the second reading is not hidden: 64 sequences, 128 keys, 512 own
+// slots 10.8 / 10.5, 64 own slots 5.8 / 7.3. And the host has one launch to make: 9.4 us a call against 12.
 bool prefix_read_by_each(int B, int Hkv, int P, int own_cap) {
     const long long pairs = (long long)B * Hkv;
     return P == 0 || (pairs * P <= 1 << 16 && pairs * (P + own_cap / 2ll) <= 1 << 17);
@@ -762,9 +754,7 @@ cudaError_t attn_decode_sinks_launch(const __nv_bfloat16* q, const __nv_bfloat16
 
 cudaError_t attention_ranges_prepare() {
     cudaError_t (*const prepare[])() = {
-        ranges_prepare<128, false, 1>, ranges_prepare<128, false, 3>, ranges_prepare<128, true, 1>,
-        ranges_prepare<128, true, 3>,  ranges_prepare<64, false, 1>,  ranges_prepare<64, false, 3>,
-        ranges_prepare<64, true, 1>,   ranges_prepare<64, true, 3>};
+        ranges_prepare<128, false>, ranges_prepare<128, true>, ranges_prepare<64, false>, ranges_prepare<64, true>};
     for (auto f : prepare) {
         cudaError_t e = f();
         if (e != cudaSuccess) return e;
