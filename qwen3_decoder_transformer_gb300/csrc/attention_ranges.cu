@@ -29,8 +29,8 @@ namespace {
 // (movmatrix), O^T (head_dim x heads) += V^T P^T.
 // Scores of rows behind a run are masked, and their value rows are zeroed in shared memory, so nothing
 // stored in a hidden row can reach the result.
-// What bounds it. Many sequences: HBM, 64 sequences x 4,100 keys of 8 kv heads, dh 128 (1.08 GB) 151 us from call to call
-// (part of the keys still in L2), 158 us with a cold L2 under ncu, 6.8 TB/s (100% of the measured copy rate). Fragments loaded
+// What bounds it. Many sequences: HBM, 64 sequences x 4,100 keys of 8 kv heads, dh 128 (1.08 GB) 149-152 us from call to call
+// (part of the keys still in L2), 155 us with a cold L2 under ncu, 6.9 TB/s (102% of the measured copy rate). Fragments loaded
 // straight from global memory, without rings, took 219 us for any split: too little on its way per warp. One
 // sequence: the chain of launch, length, first boxes and the join, 6.9 us for 4,100 keys by clusters of 16 CTAs
 // (13 by 4).

@@ -32,7 +32,8 @@ namespace {
 // with two accumulators and two score regions 322; a tile's exponentials at the scale of the tiles before it, its
 // maximum beside them, 341; two warpgroups on alternate tiles (the causal prefill's ALT form) 305, but slower
 // from 1024 keys down.
-// 16384 tokens, window 4096, 128 sinks: 712 us, 1.39 PFLOP/s of counted pairs (72% of the measured tensor rate).
+// 16384 tokens, window 4096, 128 sinks: 697-711 us, 1.4 PFLOP/s of visible pairs (73% of the measured tensor rate; the power
+// limit lowers the clock after some 0.2 s of it). Looking for the next tile's scores in the middle of a tile: no gain.
 constexpr int TL_SINKS = 0, TL_PREFIX = 1;
 constexpr int TL_BM = 128, TL_BN = 128, TL_THREADS = 256, TL_NR = 3, TL_KST = 3, TL_VST = 3;
 
