@@ -416,6 +416,34 @@ def test_sinks_captured_and_repeatable(bd):
 
 
 @gpu
+def test_sinks_decode_on_two_streams(bd):
+    """Calls that take clusters of sixteen and of four CTAs, and a prefill, on two streams at once: each as alone."""
+    g = _gen(16)
+    calls = []
+    for Bn, Hq, Hkv, dh, cap, T in ((1, 32, 8, 128, 5000, 1), (10, 16, 8, 64, 3000, 1), (1, 16, 8, 128, 2000, 300)):
+        k, v = _normal(g, Bn, Hkv, cap, dh), _normal(g, Bn, Hkv, cap, dh)
+        lens = torch.randint(cap // 2, cap - T, (Bn,), device="cuda", dtype=torch.int32)
+        out = torch.zeros(2, Bn * T, Hq * dh, dtype=torch.bfloat16, device="cuda")
+        q = _normal(g, Bn, Hq, T, dh) if T > 1 else _normal(g, Bn, Hq, dh)
+        op = bd.op_attention_prefill_sinks if T > 1 else bd.op_attention_decode_sinks
+        calls.append((op, q, k, v, lens, out, min(cap, 4096)))
+    want = []
+    for op, q, k, v, lens, out, window in calls:
+        op(q, k, v, lens, out[0], window, 4)
+        torch.cuda.synchronize()
+        want.append(out[0].clone())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i in range(30):
+        for n, s in enumerate(streams):
+            op, q, k, v, lens, out, window = calls[(i + n) % 3]
+            op(q, k, v, lens, out[n], window, 4, stream=s)
+    torch.cuda.synchronize()
+    for w, c in zip(want, calls):
+        assert torch.equal(c[5][0], w) and torch.equal(c[5][1], w)
+
+
+@gpu
 def test_streaming_loop(bd):
     """The operators as a streaming server uses them: chunks of a prompt, then tokens, appended to a rolling buffer with
     sinks; every result equals attention in float64 over the whole history, and the prefill form agrees on one token."""

@@ -234,6 +234,33 @@ def test_captured_on_another_stream_and_repeatable(bd):
 
 
 @pytest.mark.gpu
+def test_two_streams(bd):
+    """Calls of one row (a cluster of sixteen CTAs), of 30 and of 700 rows on two streams at once: each as alone."""
+    g = torch.Generator().manual_seed(7)
+    calls = []
+    for M, V in ((1, 151936), (30, 50001), (700, 4099)):
+        x = (torch.randn(M, V, generator=g) * 3).cuda()
+        tok = torch.randint(0, V, (M,), generator=g, dtype=torch.int32).cuda()
+        outs = [(torch.zeros(M, device="cuda"), torch.zeros(M, device="cuda"),
+                 torch.zeros(M, 9, dtype=torch.int32, device="cuda"), torch.zeros(M, 9, device="cuda")) for _ in range(2)]
+        calls.append((x, tok, outs))
+    want = []
+    for x, tok, outs in calls:
+        bd.op_token_logprobs(x, tok, *outs[0])
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs[0]])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i in range(30):
+        for n, s in enumerate(streams):
+            x, tok, outs = calls[(i + n) % 3]
+            bd.op_token_logprobs(x, tok, *outs[n], stream=s)
+    torch.cuda.synchronize()
+    for w, (_, _, outs) in zip(want, calls):
+        assert all(torch.equal(a, b) for o in outs for a, b in zip(o, w))
+
+
+@pytest.mark.gpu
 def test_with_greedy_on_model_logits(bd):
     """On the logits of a prefill (all rows): the first alternative is the greedy token, and the log probability of the
     given tokens sums to the sequence's score."""
