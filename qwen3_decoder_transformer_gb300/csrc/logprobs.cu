@@ -382,12 +382,12 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
         bool rescan = nc > LP_CAP || no_sum;
         if (!rescan) rescan = !lp_select<LP_THREADS>(sh.cand, nc, k, sh, sh.top);
         if (rescan) {  // one scan of the slice per alternative: the largest key below the previous one
-            u64 prev = ~0ull;
+            u64 prev = 0;
             for (int r = 0; r < k; ++r) {
                 u64 best = 0;
                 auto take = [&](float v, int idx) {
-                    const u64 key = lp_key(v, idx);
-                    if (key < prev && key > best) best = key;
+                    const u64 key = lp_key(v, idx);  // (a NaN at index 0 has the largest key there is)
+                    if ((r == 0 || key < prev) && key > best) best = key;
                 };
                 for (int i = tid; i < n; i += LP_THREADS) {
                     float x[EPV];

@@ -177,6 +177,41 @@ def test_ties_at_the_threshold(bd, dtype, M, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,V,k", [(1, 1, 1), (3, 4, 4), (5, 33, 32), (1, 30011, 20), (40, 30011, 32), (200, 9001, 5),
+                                   (1300, 2050, 4)])
+def test_nan_at_the_first_tokens(bd, dtype, M, V, k):
+    """Token 0 is an alternative like any other when its logit is NaN: alone, with others, and in rows of NaN only (a
+    diverged model's), down to as many alternatives as tokens. NaN first, ties to the lowest index, no id outside [0, V)."""
+    g = torch.Generator().manual_seed(V + M)
+    full = (torch.randn(M, V, generator=g) * 3).to(dtype)
+    for r in range(M):
+        kind = (r + (M == 1)) % 5
+        if kind == 0:
+            full[r, 0] = float("nan")
+        elif kind == 1:
+            full[r, :] = float("nan")
+        elif kind == 2:
+            full[r, torch.tensor([0, V // 2, V - 1])] = float("nan")
+        elif kind == 3:
+            full[r, 0], full[r, V - 1] = float("inf"), float("nan")
+    tokens = torch.zeros(M, dtype=torch.int32)
+    lp, ent, ids, tops, err = _run(bd, full.cuda(), tokens.cuda(), k)
+    x = full.float().numpy()
+    order = np.argsort(-np.where(np.isnan(x), np.inf, x), axis=1, kind="stable")
+    nan_first = np.argsort(~np.take_along_axis(np.isnan(x), order, 1), axis=1, kind="stable")
+    want = torch.from_numpy(np.take_along_axis(order, nan_first, 1)[:, :k].copy()).int()
+    assert err == 0
+    assert int(ids.min()) >= 0 and int(ids.max()) < V
+    assert torch.equal(ids, want)
+    none = ~torch.isfinite(full.float()).all(1)
+    assert torch.isnan(lp[none]).all() and torch.isnan(ent[none]).all() and torch.isnan(tops[none]).all()
+    if (~none).any():
+        rest = ~none
+        _check((lp[rest], ent[rest], ids[rest], tops[rest], err), _ref(full[rest].float(), tokens[rest], k), V)
+
+
+@pytest.mark.gpu
 def test_bad_tokens_flagged(bd):
     x = torch.randn(4, 1000, generator=torch.Generator().manual_seed(4))
     tokens = torch.tensor([0, -1, 1000, 999], dtype=torch.int32)
