@@ -355,7 +355,9 @@ QWEN3_API int qwen3_op_greedy(const float* d_logits, int64_t ld, int B, int V, i
  * bytes (0 when prefix_len is 0, then d_work may be NULL), 16-byte aligned; work_bytes is its size, and a smaller
  * one is refused (E_ARG); its contents on entry do not matter.
  * Calls that share a d_work must not overlap on the GPU. Scores and sums are fp32, probabilities are rounded to
- * bf16 for the weighted sum. d_err (may be NULL) receives bit 2 if a bounded wait gave up. */
+ * bf16 for the weighted sum. The sums before the division take weights of up to 2^8 times the largest one's, so the
+ * visible keys times the largest |v| must stay below 2^119. d_err (may be NULL) receives bit 2 if a bounded wait
+ * gave up. */
 QWEN3_API size_t qwen3_attention_decode_shared_workspace(int B, int Hq, int Hkv, int dh, int prefix_len);
 QWEN3_API int qwen3_op_attention_decode_shared(const void* d_q, const void* d_k_prefix, const void* d_v_prefix,
                                                int prefix_cap, int prefix_len, const void* d_k_cache,
@@ -379,7 +381,7 @@ QWEN3_API int qwen3_op_attention_decode_shared(const void* d_q, const void* d_k_
  * Decode: the form for one token per sequence, q [B, Hq, dh], out [B, Hq*dh], Hq / Hkv at most 8, B at most
  * 65535; hidden rows may hold anything; a sequence with a negative length gets zeros. Neither needs a workspace.
  * window >= 1, sinks >= 0, dh 64 or 128, cap at most 2^30 and lengths too (a longer one counts as 2^30), 16-byte
- * aligned tensors. d_err (may be NULL) as for
+ * aligned tensors; values of the size that qwen3_op_attention_decode_shared takes. d_err (may be NULL) as for
  * qwen3_op_attention_prefill. */
 QWEN3_API int qwen3_attention_sink_rows(int sinks);
 QWEN3_API int qwen3_op_attention_prefill_sinks(const void* d_q, const void* d_k_cache, const void* d_v_cache, int B,
