@@ -1,5 +1,6 @@
 """Attention with a sliding window and sinks, and over a shared prefix, at the limits of their arguments: scores whose
-maximum rises from tile to tile, large values, and lengths past the cache.
+maximum rises from tile to tile, large values, lengths past the cache, and own slots at the border of the rule for who reads a
+prefix.
 
 Tolerance as in test_attention_ranges: half a step of bf16 for each probability and for the result, and e for scores of up
 to X in log2 units, 10 fp32 roundings of them: e = 0.7 * 10 * 2^-24 X. Scaling the sums to a larger maximum adds a few
@@ -10,7 +11,7 @@ import math
 import pytest
 import torch
 
-from tests.test_attention_ranges import _attend, _close, _err, _gen, _normal, _row, bd  # noqa: F401
+from tests.test_attention_ranges import _attend, _close, _err, _gen, _normal, _row, _shared_case, bd  # noqa: F401
 
 gpu = pytest.mark.gpu
 
@@ -172,3 +173,15 @@ def test_sinks_lengths_past_the_limits(bd, dh):
             got = _call(bd, q, k, v, given, window, sinks, True, decode)
             assert torch.equal(got, _call(bd, q, k, v, counts, window, sinks, True, decode))
             _check_rows(got, q, k, v, counts, window, sinks, sink_rows, ring, sorted({0, T - 1}), 10.0)
+
+
+@gpu
+@pytest.mark.parametrize("Bn,Hq,Hkv,P,cap", [(64, 16, 8, 128, 256), (64, 16, 8, 128, 258), (64, 16, 8, 128, 512),
+                                             (2, 8, 8, 4096, 8192), (2, 8, 8, 4096, 8194), (16, 8, 4, 600, 2896),
+                                             (16, 8, 4, 600, 2898)])
+def test_shared_own_slots_at_the_border(bd, Bn, Hq, Hkv, P, cap):
+    """A prefix is read by each sequence only while the pairs of sequence and kv head times P are at most 2^16 and, counted
+    with half of the own slots, at most 2^17: sizes on both sides of the second border, with and without a layout."""
+    _shared_case(bd, Bn, Hq, Hkv, 64, P, cap, [(b * 37 + cap - 3) % cap for b in range(Bn)], seed=cap)
+    if cap <= 512:
+        _shared_case(bd, Bn, Hq, Hkv, 128, P, cap + P, [cap - 1], seed=cap, meta=[130, 128] + [(7 * b) % 45 for b in range(Bn)])
