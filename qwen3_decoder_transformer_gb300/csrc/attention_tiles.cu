@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "rings.h"
 
 namespace q3 {
 namespace {
@@ -188,10 +189,17 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
         return s;
     };
 
+    // A role ends when what it has asked for is done, also after a wait of the CTA gave up: no copy or product of this CTA may
+    // land in shared or tensor memory that the next one has taken over. These last waits are bounded, all of a role's by
+    // one limit, and look at no abort flag. (In an ordinary run they end before the softmax warps' last tile does.)
+    int never = 0;
+    bool arrives = true;
+    auto last_wait = [&](uint64_t* bar, int parity) { arrives = arrives && mbar_wait_suspend(bar, parity, &never); };
+
     if (warp == 0) {
         // ---------------- Q and key tiles
         if (lane == 0) {
-            int g = 0;
+            int g = 0, q_copies = 0;
             for (int round = 0; ok; ++round) {
                 const Item it = item_of(round);
                 if (it.n_tiles <= 0) break;
@@ -205,6 +213,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                     mbar_expect_tx(q_full, Ly::Q_BYTES);
                     tma_load_4d(smem, &tmQ, q_full, 0, it.q0, 0, it.b * Hq + it.h);
                 }
+                ++q_copies;
                 for (int i = 0; i < it.n_tiles; ++i, ++g) {
                     const int s = g % KST, y = tile_row(tile_of(it, i)), z = PREFIX ? jkv : it.b * Hkv + jkv;
                     if (!mbar_wait_suspend(&k_empty[s], ((g / KST) & 1) ^ 1, abort_flag)) { ok = false; break; }
@@ -212,6 +221,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                     tma_load_4d(smem + Ly::K_OFF + s * Ly::KV_BYTES, &tmK, &k_full[s], 0, y, 0, z);
                 }
             }
+            drain_ring(g, KST, [&](int s, int parity) { last_wait(&k_full[s], parity); });
+            drain_ring(q_copies, 1, [&](int, int parity) { last_wait(q_full, parity); });
         }
     } else if (warp == 1) {
         // ---------------- S of tile g into region g % NR, once P V of tile g - NR has finished with it
@@ -240,6 +251,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                     if (i == nt - 1) umma_commit(q_empty);  // the item's last score releases Q
                 }
             }
+            if (g > 0) last_wait(&s_full[(g - 1) % NR], ((g - 1) / NR) & 1);  // (completes behind every earlier tile's)
         }
     } else if (warp == 2) {
         // ---------------- value tiles; and zeros in the rows that no row of the item sees, which may hold anything
@@ -280,7 +292,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                     tma_load_4d(smem + Ly::V_OFF + s * Ly::KV_BYTES, &tmV, &v_full[s], 0, y, 0, z);
                 }
                 __syncwarp();
-                if (pend && !clean()) { ok = false; break; }
+                if (pend && !clean()) { ok = false; ++g; break; }  // (g: tiles asked for)
                 if (edge(it, i)) {
                     pend = true;
                     pend_s = s;
@@ -290,6 +302,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
             }
         }
         if (ok && pend) ok = clean();
+        if (lane == 0) drain_ring(g, VST, [&](int s, int parity) { last_wait(&v_full[s], parity); });
+        __syncwarp();
     } else if (warp == 3) {
         // ---------------- O += P V of tile g: P from region g % NR (A operand in tensor memory), V from stage g % VST
         if (lane == 0) {
@@ -330,6 +344,7 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                     umma_commit(&r_free[r]);
                 }
             }
+            if (g > 0) last_wait(&r_free[(g - 1) % NR], ((g - 1) / NR) & 1);
         }
     } else {
         // ---------------- softmax: thread <-> query row (TMEM lane)
