@@ -341,8 +341,9 @@ QWEN3_API int qwen3_op_greedy(const float* d_logits, int64_t ld, int B, int V, i
                               int32_t* d_next, int32_t* d_work, void* stream);
 
 /* Decode attention for a batch that shares a prefix, whose keys and values are read and multiplied once for the
- * whole batch (a prefix of few keys by each sequence, where that is faster): for each sequence b and query head h, out = softmax(q k^T * dh^-0.5) V in one softmax
- * over the prefix_len prefix keys and the sequence's own visible keys, kv head h / (Hq/Hkv). Prefix
+ * whole batch (a prefix of few keys by each sequence, where that is faster): for each sequence b and query head h,
+ * out = softmax(q k^T * dh^-0.5) V in one softmax over the prefix_len prefix keys and the sequence's own visible
+ * keys, kv head h / (Hq/Hkv). Prefix
  * d_k_prefix / d_v_prefix [Hkv, prefix_cap, dh] (its first prefix_len rows); own caches [B, Hkv, cap, dh],
  * sequence b's query at slot d_len0[b * len_stride] (len_stride 0: one length for all; 1: one per sequence),
  * its keys in slots 0 .. that one. A negative length means no own keys (a length beyond cap - 1 counts as
@@ -351,9 +352,10 @@ QWEN3_API int qwen3_op_greedy(const float* d_logits, int64_t ld, int B, int V, i
  * [ps, ps + pad_b) are hidden. After qwen3_share_prefix the call is: the prefix is sequence 0's cache,
  * prefix_len = psh, prefix_cap = cap. Hidden slots may hold anything.
  * q [B, Hq, dh], out [B, Hq*dh] bf16; Hq / Hkv at most 8, dh 64 or 128, B at most 65535, cap and prefix_len at most
- * 2^30; q and caches 16-byte aligned. d_work is scratch of qwen3_attention_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len)
- * bytes (0 when prefix_len is 0, then d_work may be NULL), 16-byte aligned; work_bytes is its size, and a smaller
- * one is refused (E_ARG); its contents on entry do not matter.
+ * 2^30; q and caches 16-byte aligned. d_work is scratch of
+ * qwen3_attention_decode_shared_workspace(B, Hq, Hkv, dh, prefix_len) bytes (0 when prefix_len is 0, then d_work may
+ * be NULL), 16-byte aligned; work_bytes is its size, and a smaller one is refused (E_ARG); its contents on entry do
+ * not matter.
  * Calls that share a d_work must not overlap on the GPU. Scores and sums are fp32, probabilities are rounded to
  * bf16 for the weighted sum. The sums before the division take weights of up to 2^8 times the largest one's, so the
  * visible keys times the largest |v| must stay below 2^119. d_err (may be NULL) receives bit 2 if a bounded wait
@@ -368,7 +370,9 @@ QWEN3_API int qwen3_op_attention_decode_shared(const void* d_q, const void* d_k_
 /* Attention with a sliding window and attention sinks: the token in slot i sees slots j <= i with
  * i - j < window or j < sinks (the first `sinks` tokens stay visible after the window has left them).
  * Sequence b's first new token is in slot d_len0[b * len_stride] (len_stride 0: one length for all; 1: one per
- * sequence); its K and V are in the caches [B, Hkv, cap, dh] already, the new tokens' included.
+ * sequence); its K and V are in the caches [B, Hkv, cap, dh] already, the new tokens' included. The caller puts them
+ * there: qwen3_op_qknorm_rope_append writes slot s to row s with one length for all sequences, which is rolling 0
+ * with len_stride 0; no operator here writes the rows of a rolling buffer or of sequences at lengths of their own.
  *   rolling 0: slot s is stored in cache row s; prefill len0 + T <= cap, decode len0 < cap (a longer length
  *     counts as the longest that fits).
  *   rolling 1: the first qwen3_attention_sink_rows(sinks) rows (sinks rounded up to 128) hold the slots of

@@ -27,14 +27,17 @@ namespace {
 // than 2^8.
 // What bounds it: a softmax thread's chain over a tile (scores from tensor memory, maximum, exponentials, P back),
 // about 1,600 cycles against 1,024 of MMA work (tensor pipe 63% active under ncu). 8192 tokens, 32 heads, dh 128, window
-// 4096 and 4 sinks: 307 us; timing copies of the kernel without the copies of K and V 298, with half of the MMAs 284,
+// 4096 and 4 sinks: 284 us, 300 with inputs that are not in L2 (dh 64, 8 query and 8 kv heads, 16384 tokens, 128 sinks: 163).
+// The comparisons that follow were made when it took 307 (where the roles' code lies in the kernel moves its time by some per
+// cent either way): timing copies of the kernel without the copies of K and V 298, with half of the MMAs 284,
 // without the exponentials 258. Other forms of the softmax, on the same case: two threads a row that exchange their
 // maxima 310-322; the same with the next tile's scores loaded ahead 409; the two 64-key halves as streams of their own
 // with two accumulators and two score regions 322; a tile's exponentials at the scale of the tiles before it, its
 // maximum beside them, 341; two warpgroups on alternate tiles (the causal prefill's ALT form) 305, but slower
 // from 1024 keys down.
-// 16384 tokens, window 4096, 128 sinks: 697-711 us, 1.4 PFLOP/s of visible pairs (73% of the measured tensor rate; the power
+// 16384 tokens, window 4096, 128 sinks: 640-680 us, 1.5 PFLOP/s of visible pairs (76-80% of the measured tensor rate; the power
 // limit lowers the clock after some 0.2 s of it). Looking for the next tile's scores in the middle of a tile: no gain.
+// Few new tokens: an item's tiles run in turn on one CTA, so 1 to 256 tokens over a window of 4096 take 29-30 us.
 constexpr int TL_SINKS = 0, TL_PREFIX = 1;
 constexpr int TL_BM = 128, TL_BN = 128, TL_THREADS = 256, TL_NR = 3, TL_KST = 3, TL_VST = 3;
 
@@ -487,7 +490,8 @@ __global__ void __launch_bounds__(TL_THREADS, 1)
                     l *= alpha;
                     m = mx;
                 }
-                // P = 2^(s * sl2 - m) as packed bf16 (a row with no visible key yet keeps m = -inf and gets P = 0)
+                // P = 2^(s * sl2 - m) as packed bf16, the type that the tensor cores take beside V's (off by 2^-8 of itself at
+                // most; the sum keeps fp32). A row with no visible key yet keeps m = -inf and gets P = 0.
                 const float nm = m == -INFINITY ? 0.f : -m;
                 const float2 sl2x2 = make_float2(sl2, sl2), nmx2 = make_float2(nm, nm);
                 float2 rs2 = make_float2(0.f, 0.f);

@@ -317,7 +317,10 @@ __global__ void __launch_bounds__(LP_THREADS, 1024 / LP_THREADS)
                 const u64 rep = idx >= 0 ? lp_key(mx, idx) : 0;
                 __syncthreads();  // the list's counters are set
                 set_tau(lp_threshold<LP_THREADS>(rep, k, sh));
-            } else if ((step == 3 || step == 8) && steps > 2 * step) {  // raise it from the list so far
+            } else if ((step == 3 || step == 8) && steps > 2 * step) {
+                // raise it from the list so far, while the list is far from full and most of the slice is still to come (2048
+                // fp32 rows of 151,936, 32 alternatives: never 1,964 us, since lists overflow; at step 3 alone 239; at 3 and 8
+                // 216; at 2 and 5 219; at 4 and 16 211. 64 rows, five: 10.9, 11.1, 11.3, 12.3, 11.1)
                 __syncthreads();
                 const int nc = min(sh.n_cand, LP_CAP);
                 u64 rep = 0;
@@ -475,6 +478,9 @@ cudaError_t token_logprobs_launch(const void* logits, int bf16, long long ld, in
     // rows of 151,936 bf16 logits, one alternative 121 us against 133 with 512 threads, 32 alternatives 176
     // against 204; fp32 200 either way). Few rows: 512 threads, for a row's shorter chain (333 bf16 rows of 32,003, 32
     // alternatives 15.2 against 20.0, one row 7.1 against 8.6).
+    // Rows of 151,936 about the border, 256 against 512 threads, one and 32 alternatives: bf16 304 rows 22.5 / 20.7 and 35.7 / 33.2,
+    // 608 39.2 / 41.2 and 57.4 / 63.4, 1216 72.5 / 78.1 and 106 / 121; fp32 304 35.0 / 32.7 and 42.2 / 38.2, 900 94.3 / 90.2
+    // and 110 / 104, 1216 115 / 120 and 128 / 138, 1500 148 / 147 and 160 / 169: past 1216 no case loses more than 1%.
     const int threads = M >= 8 * device_sm_count() ? 256 : 512;
     const int C = lp_cluster(M, V);
     int log_c = 0;
