@@ -1113,7 +1113,8 @@ int qwen3_op_attention_prefill_sinks(const void* q, const void* kc, const void* 
     if (!q || !kc || !vc || !len0 || !out || B < 0 || T < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv ||
         (dh != 64 && dh != 128) || cap < 1 || (len_stride != 0 && len_stride != 1))
         return QWEN3_E_ARG;
-    if (((long long)T + 127) / 128 * Hq * B > 0x7fffffff) return QWEN3_E_ARG;
+    // the kernel counts items in an int, up to two rounds of CTAs past the last one
+    if (((long long)T + 127) / 128 * Hq * B > 0x7fff0000) return QWEN3_E_ARG;
     SinkMap sm;
     if (T > cap || cap > kMaxSlots || !sink_map(window, sinks, rolling, cap, T, &sm)) return QWEN3_E_ARG;
     if (!is_aligned(q, 16) || !is_aligned(kc, 16) || !is_aligned(vc, 16) || !is_aligned(out, 16)) return QWEN3_E_ARG;

@@ -185,3 +185,14 @@ def test_shared_own_slots_at_the_border(bd, Bn, Hq, Hkv, P, cap):
     _shared_case(bd, Bn, Hq, Hkv, 64, P, cap, [(b * 37 + cap - 3) % cap for b in range(Bn)], seed=cap)
     if cap <= 512:
         _shared_case(bd, Bn, Hq, Hkv, 128, P, cap + P, [cap - 1], seed=cap, meta=[130, 128] + [(7 * b) % 45 for b in range(Bn)])
+
+
+# ------------------------------------------------------------------------------------------------ refusals (CPU)
+
+def test_prefill_refuses_items_past_the_kernels_counters(bd):  # noqa: F811
+    """Query tiles x heads x sequences are counted in 32 bits, a round of CTAs past the last one included."""
+    import ctypes
+    p = ctypes.c_void_p(64)  # never dereferenced: the call is refused on the host
+    L = bd.lib()
+    for Hq, Bn in ((2 ** 16 - 1, 2 ** 15), (2 ** 31 - 1, 1), (1, 2 ** 31 - 1), (2 ** 31 - 300, 1)):
+        assert L.qwen3_op_attention_prefill_sinks(p, p, p, Bn, 1, Hq, Hq, 64, 512, p, 0, 100, 4, 0, p, None, None) == 5
