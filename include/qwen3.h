@@ -396,6 +396,80 @@ QWEN3_API int qwen3_op_attention_decode_sinks(const void* d_q, const void* d_k_c
                                               int Hkv, int dh, int cap, const int* d_len0, int len_stride, int window,
                                               int sinks, int rolling, void* d_out, int* d_err, void* stream);
 
+/* ---- A paged KV cache held in 4 bits, and packed batches of sequences of different lengths.
+ *
+ * Pages: d_k_pages and d_v_pages [n_pages, Hkv, qwen3_paged4_page_bytes(page_size, dh)] bytes hold page_size tokens (16, 32,
+ * 64, 128 or 256) of each kv head. A page of one head holds the tokens' codes [page_size, dh / 2] (two a byte, the lower
+ * nibble first), then [page_size, dh / 64] pairs of bf16 (scale, minimum), one for each 64 dims of a token:
+ * value = minimum + scale * code. d_page_table [sequences, max_pages] int32: entry i of a sequence is the page of its slots
+ * i * page_size ..; entries that a call does not need are not read. 4.5 bits a value: 144 bytes a token and kv head at
+ * dh 128, K and V together. dh is 64 or 128.
+ * Packed batch: N rows, of which [cu[s], cu[s + 1]) belong to sequence s, s < S (d_cu [S + 1] int32, ascending); rows from
+ * cu[S] on belong to none and their outputs are left as they were. Row cu[s] + i takes slot d_start[s] + i of its
+ * sequence, which is also its position. A decode step is the batch of one row a sequence.
+ * A page id outside [0, n_pages), a slot that is negative or that the table does not reach, a position outside the rotation
+ * table and bounds that are not ascending set bit 4 in *d_err (device int, may be NULL). */
+QWEN3_API size_t qwen3_paged4_page_bytes(int page_size, int dh);
+
+/* Append to the paged cache: RMSNorm of each query and key head over head_dim (d_q_gamma / d_k_gamma [dh] bf16; NULL: no norm),
+ * rotate-half RoPE at the row's position, then q to d_q_out [N, Hq, dh] and (unless NULL) the keys to d_k_out [N, Hkv, dh],
+ * both bf16, and keys and values in 4 bits to their slots. d_qkv: bf16 rows of (Hq + 2 Hkv) dh (q, k and v heads), ld
+ * elements apart (a multiple of 8); d_cos_sin [n_pos, dh] as qwen3_op_rope_table writes it.
+ * Unlike qwen3_op_qknorm_rope_append, which rounds where the pages' bf16 model does, everything is fp32 and rounded
+ * once at the end. For each 64 dims: minimum = the least value rounded down to bf16, scale = (largest - minimum) / 15 rounded up
+ * to bf16, code = the nearest of 0..15 (even on ties), all from the unrounded fp32 values: a cached value is off by half a
+ * scale at most. 64 dims that hold a NaN or an infinity become NaN.
+ * A row without a page (bit 4) still gets its outputs; one without a position gets none. Two rows must not share a
+ * slot, nor any written page hold two sequences' slots. d_k_out may not overlap d_qkv. All tensors 16-byte aligned. */
+QWEN3_API int qwen3_op_append_paged4(const void* d_qkv, int64_t ld, int N, const int* d_cu, const int* d_start, int S, int Hq,
+                                     int Hkv, int dh, const void* d_q_gamma, const void* d_k_gamma, float eps,
+                                     const void* d_cos_sin, int n_pos, void* d_q_out, void* d_k_out, void* d_k_pages,
+                                     void* d_v_pages, int n_pages, int page_size, const int* d_page_table, int max_pages,
+                                     int* d_err, void* stream);
+
+/* Read slots of the paged cache: row cu[s] + i of d_k_out and d_v_out [N, Hkv, dh] bf16 becomes slot d_start[s] + i of sequence s,
+ * each value rounded once (to go on from a cached history with qwen3_op_attention_prefill_packed, or to look at it). A row
+ * whose slot has no page is left as it was (bit 4). */
+QWEN3_API int qwen3_op_read_paged4(const void* d_k_pages, const void* d_v_pages, int n_pages, int page_size,
+                                   const int* d_page_table, int max_pages, const int* d_cu, const int* d_start, int S, int N,
+                                   int Hkv, int dh, void* d_k_out, void* d_v_out, int* d_err, void* stream);
+
+/* Decode attention over the paged cache, one query per (sequence, query head): out = softmax(q k^T * dh^-0.5) V over the slots
+ * 0 .. d_len0[b] of sequence b (the query's own slot, appended before), each sequence at its own length, kv head
+ * h / (Hq/Hkv). A negative length gives zeros, one past the page table's reach counts as the last slot. q [B, Hq, dh], out
+ * [B, Hq*dh] bf16; Hq / Hkv at most 8, B at most 65535; the table's reach at most 2^30 slots, and B times its 32-slot units
+ * below 2^31. Slots behind a length may hold anything. d_work: qwen3_attention_decode_paged4_workspace() bytes (of the current
+ * device; work_bytes is its size, a smaller one is refused), 16-byte aligned, any contents on entry; calls that share one must
+ * not overlap on the GPU. Scores, sums and softmax statistics are fp32; the cached codes are used as they are, and
+ * probabilities times scales are rounded to bf16 for the product with the codes. |q| up to 2^90, and values as for
+ * qwen3_op_attention_decode_shared. A page id out of range (bit 4) makes the sequence's output invalid; bit 2 as for the other
+ * attention operators. The result does not depend on timing. */
+QWEN3_API size_t qwen3_attention_decode_paged4_workspace(int B, int Hq, int Hkv, int dh);
+QWEN3_API int qwen3_op_attention_decode_paged4(const void* d_q, const void* d_k_pages, const void* d_v_pages, int n_pages,
+                                               int page_size, const int* d_page_table, int max_pages, const int* d_len0, int B,
+                                               int Hq, int Hkv, int dh, void* d_work, size_t work_bytes, void* d_out, int* d_err,
+                                               void* stream);
+
+/* Causal attention over packed sequences of different lengths. Sequence s has the query rows [cu_q[s], cu_q[s + 1]) of d_q
+ * [Nq, Hq, dh] and the key rows [cu_k[s], cu_k[s + 1]) of d_k, d_v [Nk, Hkv, dh]; with lq of the one and lk of the other, query
+ * i sees keys j <= i + lk - lq (whole prompts: d_cu_k = d_cu_q; a continued prompt has its history's keys in front). A query
+ * that sees no key gets zeros. out [Nq, Hq*dh] bf16. Rows may be ldq, ldk, ldv elements apart (multiples of 8), so that
+ * values can be read from packed qkv rows in place; tensors are 16-byte aligned.
+ * The plan is the work list of a batch, made once for all layers: qwen3_op_attention_packed_plan writes
+ * qwen3_attention_packed_plan_bytes(Nq, S) bytes (16-byte aligned) on the stream; a sequence whose bounds descend or
+ * leave Nq and Nk, or whose query rows begin before an earlier bound, is left out (bit 4), its output rows untouched. The attention call takes a plan made for its Nq and Nk
+ * (plan_bytes as for the plan); calls may share one. `longest`, the keys of the longest sequence, only picks between
+ * equivalent forms of the kernel: any value gives a right result.
+ * Scores, sums and softmax statistics are fp32, probabilities are rounded to bf16 for the product with V. Value rows that some
+ * query of a 128-row tile sees must be finite; nothing stored in another sequence's rows, or behind the tile's last visible
+ * key, reaches a result. Nq, Nk and S at most 2^30, and plan entries times Hq below 2^31 - 2^16. */
+QWEN3_API size_t qwen3_attention_packed_plan_bytes(int Nq, int S);
+QWEN3_API int qwen3_op_attention_packed_plan(const int* d_cu_q, const int* d_cu_k, int S, int Nq, int Nk, void* d_plan,
+                                             size_t plan_bytes, int* d_err, void* stream);
+QWEN3_API int qwen3_op_attention_prefill_packed(const void* d_q, int64_t ldq, const void* d_k, int64_t ldk, const void* d_v,
+                                                int64_t ldv, int Nq, int Nk, int Hq, int Hkv, int dh, const void* d_plan,
+                                                size_t plan_bytes, int longest, void* d_out, int* d_err, void* stream);
+
 /* Log probabilities of given tokens, with the entropy of each row's distribution and its largest
  * alternatives (scoring a prompt from the all-rows logits of a prefill, or a sampled token from a decode
  * step's). For row m of logits x = d_logits[m * ld ..] (V values, fp32 or bf16 by logits_type):

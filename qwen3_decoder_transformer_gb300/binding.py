@@ -113,6 +113,19 @@ def lib() -> ctypes.CDLL:
     L.qwen3_attention_sink_rows.argtypes = [i]
     L.qwen3_op_attention_prefill_sinks.argtypes = [_vp, _vp, _vp, i, i, i, i, i, i, _vp, i, i, i, i, _vp, _vp, _vp]
     L.qwen3_op_attention_decode_sinks.argtypes = [_vp, _vp, _vp, i, i, i, i, i, _vp, i, i, i, i, _vp, _vp, _vp]
+    i64 = ctypes.c_int64
+    L.qwen3_paged4_page_bytes.restype = sz
+    L.qwen3_paged4_page_bytes.argtypes = [i, i]
+    L.qwen3_op_append_paged4.argtypes = [_vp, i64, i, _vp, _vp, i, i, i, i, _vp, _vp, ctypes.c_float, _vp, i, _vp, _vp, _vp,
+                                         _vp, i, i, _vp, i, _vp, _vp]
+    L.qwen3_op_read_paged4.argtypes = [_vp, _vp, i, i, _vp, i, _vp, _vp, i, i, i, i, _vp, _vp, _vp, _vp]
+    L.qwen3_attention_decode_paged4_workspace.restype = sz
+    L.qwen3_attention_decode_paged4_workspace.argtypes = [i, i, i, i]
+    L.qwen3_op_attention_decode_paged4.argtypes = [_vp, _vp, _vp, i, i, _vp, i, _vp, i, i, i, i, _vp, sz, _vp, _vp, _vp]
+    L.qwen3_attention_packed_plan_bytes.restype = sz
+    L.qwen3_attention_packed_plan_bytes.argtypes = [i, i]
+    L.qwen3_op_attention_packed_plan.argtypes = [_vp, _vp, i, i, i, _vp, sz, _vp, _vp]
+    L.qwen3_op_attention_prefill_packed.argtypes = [_vp, i64, _vp, i64, _vp, i64, i, i, i, i, i, _vp, sz, i, _vp, _vp, _vp]
     _lib = L
     return L
 
@@ -575,3 +588,166 @@ def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rol
     _launch(lib().qwen3_op_attention_decode_sinks,
             (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), B, Hq, Hkv, dh, cap, len0.data_ptr(), stride,
              _int32(window), _int32(sinks), 1 if rolling else 0, out.data_ptr(), p_err), dev, stream)
+
+
+# ------------------------------------------------------------------ the paged 4-bit cache and packed batches
+
+_U8 = torch.uint8
+PAGE_SIZES = (16, 32, 64, 128, 256)
+
+
+def paged4_page_bytes(page_size, dh) -> int:
+    """Bytes of a page of page_size tokens of one kv head (0: not a page size or head_dim of the cache)."""
+    return lib().qwen3_paged4_page_bytes(_int32(page_size), _int32(dh))
+
+
+def _pages(k_pages, v_pages, page_table, dh, dev):
+    """Check a paged cache (k_pages, v_pages [n_pages, Hkv, page bytes] uint8, page_table [sequences, max_pages] int32).
+    Returns n_pages, Hkv, the page size and max_pages."""
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _want(isinstance(t, torch.Tensor) and t.dim() == 3, f"{name} must be a tensor [n_pages, Hkv, page bytes]")
+    _want(dh in (64, 128), "head_dim must be 64 or 128")
+    n, Hkv, size = k_pages.shape
+    page = size // (dh // 2 + dh // 16)
+    _want(page in PAGE_SIZES and size == page * (dh // 2 + dh // 16),
+          "a page must hold 16, 32, 64, 128 or 256 tokens of paged4_page_bytes")
+    _dense("k_pages", k_pages, _U8, (n, Hkv, size), dev)
+    _dense("v_pages", v_pages, _U8, (n, Hkv, size), dev)
+    _want(isinstance(page_table, torch.Tensor) and page_table.dim() == 2, "page_table must be a tensor [sequences, max_pages]")
+    _dense("page_table", page_table, _I32, page_table.shape, dev)
+    _want(n >= 1 and Hkv >= 1 and page_table.shape[1] >= 1, "the cache needs a page, a kv head and a page a sequence")
+    return n, Hkv, page, page_table.shape[1]
+
+
+def _bounds(cu, start, sequences, dev):
+    """Check cu [S + 1] and start [S] against the page table's sequences; returns S."""
+    _dense("cu", cu, _I32, (sequences + 1,), dev)
+    _dense("start", start, _I32, (sequences,), dev)
+    return sequences
+
+
+def op_append_paged4(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out=None, q_gamma=None, k_gamma=None,
+                     eps=1e-6, err=None, stream=None):
+    """Head norms (with gammas), rotation and append to the paged 4-bit cache of the rows qkv [N, (Hq + 2 Hkv) dh] (unit
+    stride along a row): rows cu[s] .. cu[s+1]-1 take the slots start[s] .. of sequence s. Writes q_out [N, Hq, dh], k_out
+    [N, Hkv, dh] (None: not wanted) and the pages; rows from cu[-1] on are left as they were. err: device int (bit 4: a
+    page id or a position out of range)."""
+    _want(isinstance(qkv, torch.Tensor) and qkv.dim() == 2, "qkv must be a tensor [N, (Hq + 2 Hkv) dh]")
+    _want(isinstance(q_out, torch.Tensor) and q_out.dim() == 3, "q_out must be a tensor [N, Hq, dh]")
+    N, Hq, dh = q_out.shape
+    dev = qkv.get_device()
+    n_pages, Hkv, page, max_pages = _pages(k_pages, v_pages, page_table, dh, dev)
+    _want(Hq >= 1 and Hq % Hkv == 0, "query heads must be a multiple of kv heads")
+    width = (Hq + 2 * Hkv) * dh
+    _want(qkv.dtype is _BF16 and qkv.shape == (N, width) and qkv.stride(1) == 1,
+          f"qkv must be bf16 rows {(N, width)}, dense along a row")
+    ld = qkv.stride(0) if N > 1 else width
+    S = _bounds(cu, start, page_table.shape[0], dev)
+    _dense("q_out", q_out, _BF16, (N, Hq, dh), dev)
+    _want(isinstance(cos_sin, torch.Tensor) and cos_sin.dim() == 2, "cos_sin must be a tensor [positions, dh]")
+    _dense("cos_sin", cos_sin, _BF16, (cos_sin.shape[0], dh), dev)
+    p_k = None if k_out is None else _dense("k_out", k_out, _BF16, (N, Hkv, dh), dev)
+    p_qg = None if q_gamma is None else _dense("q_gamma", q_gamma, _BF16, (dh,), dev)
+    p_kg = None if k_gamma is None else _dense("k_gamma", k_gamma, _BF16, (dh,), dev)
+    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
+    if N == 0 or S == 0:
+        return
+    _launch(lib().qwen3_op_append_paged4,
+            (qkv.data_ptr(), ld, N, cu.data_ptr(), start.data_ptr(), S, Hq, Hkv, dh, p_qg, p_kg, eps, cos_sin.data_ptr(),
+             cos_sin.shape[0], q_out.data_ptr(), p_k, k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page,
+             page_table.data_ptr(), max_pages, p_err), dev, stream)
+
+
+def op_read_paged4(k_pages, v_pages, page_table, cu, start, k_out, v_out, err=None, stream=None):
+    """Slots start[s] .. of sequence s of the paged 4-bit cache into the rows cu[s] .. cu[s+1]-1 of k_out and v_out
+    [N, Hkv, dh] bf16."""
+    _want(isinstance(k_out, torch.Tensor) and k_out.dim() == 3, "k_out must be a tensor [N, Hkv, dh]")
+    N, Hkv, dh = k_out.shape
+    dev = k_out.get_device()
+    n_pages, heads, page, max_pages = _pages(k_pages, v_pages, page_table, dh, dev)
+    S = _bounds(cu, start, page_table.shape[0], dev)
+    _dense("k_out", k_out, _BF16, (N, heads, dh), dev)
+    _dense("v_out", v_out, _BF16, (N, heads, dh), dev)
+    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
+    if N == 0 or S == 0:
+        return
+    _launch(lib().qwen3_op_read_paged4,
+            (k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, cu.data_ptr(),
+             start.data_ptr(), S, N, Hkv, dh, k_out.data_ptr(), v_out.data_ptr(), p_err), dev, stream)
+
+
+def attention_decode_paged4_workspace(B, Hq, Hkv, dh) -> int:
+    return lib().qwen3_attention_decode_paged4_workspace(B, Hq, Hkv, dh)
+
+
+def op_attention_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out, err=None, stream=None):
+    """Decode attention of q [B, Hq, dh] over the slots 0..len0[b] of each sequence of the paged 4-bit cache, into out
+    [B, Hq*dh]. work: attention_decode_paged4_workspace bytes of scratch of any type."""
+    _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [B, Hq, dh]")
+    B, Hq, dh = q.shape
+    dev = q.get_device()
+    n_pages, Hkv, page, max_pages = _pages(k_pages, v_pages, page_table, dh, dev)
+    _want(Hq >= 1 and Hq % Hkv == 0 and Hq // Hkv <= 8, "query heads must be 1 to 8 times the kv heads")
+    _want(page_table.shape[0] == B, "page_table must have a row for each sequence")
+    p_q = _dense("q", q, _BF16, (B, Hq, dh), dev)
+    p_len = _dense("len0", len0, _I32, (B,), dev)
+    p_out = _dense("out", out, _BF16, (B, Hq * dh), dev)
+    _want(isinstance(work, torch.Tensor) and work.get_device() == dev and work.is_contiguous(),
+          "work must be contiguous scratch on the same device, of attention_decode_paged4_workspace bytes")
+    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
+    if B == 0:
+        return
+    _launch(lib().qwen3_op_attention_decode_paged4,
+            (p_q, k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, p_len, B, Hq, Hkv,
+             dh, work.data_ptr(), work.nbytes, p_out, p_err), dev, stream)
+
+
+def attention_packed_plan_bytes(Nq, S) -> int:
+    """Bytes of the work list of a packed batch of Nq query rows in S sequences."""
+    return lib().qwen3_attention_packed_plan_bytes(_int32(Nq), _int32(S))
+
+
+def op_attention_packed_plan(cu_q, cu_k, Nq, Nk, plan, err=None, stream=None):
+    """Write the work list of a packed batch (query rows cu_q [S + 1], key rows cu_k [S + 1]) into plan, contiguous scratch of
+    attention_packed_plan_bytes; made once for all layers. err: device int (bit 4: bounds out of order or range)."""
+    _want(isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 and cu_q.shape[0] >= 1, "cu_q must be a tensor [S + 1]")
+    dev = cu_q.get_device()
+    n = cu_q.shape[0]
+    _dense("cu_q", cu_q, _I32, (n,), dev)
+    _dense("cu_k", cu_k, _I32, (n,), dev)
+    _want(isinstance(plan, torch.Tensor) and plan.get_device() == dev and plan.is_contiguous(),
+          "plan must be contiguous scratch on the same device, of attention_packed_plan_bytes")
+    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
+    _launch(lib().qwen3_op_attention_packed_plan,
+            (cu_q.data_ptr(), cu_k.data_ptr(), n - 1, _int32(Nq), _int32(Nk), plan.data_ptr(), plan.nbytes, p_err), dev, stream)
+
+
+def _packed_rows(name, t, dh, dev):
+    """Check t [rows, heads, dh] bf16, its heads and dims dense; returns the elements from row to row."""
+    ok = (isinstance(t, torch.Tensor) and t.dim() == 3 and t.dtype is _BF16 and t.get_device() == dev and t.shape[2] == dh
+          and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == dh))
+    _want(ok, f"{name} must be a bf16 tensor [rows, heads, dh], dense along heads and dims")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dh
+
+
+def op_attention_prefill_packed(q, k, v, plan, longest, out, err=None, stream=None):
+    """Causal attention over packed sequences: q [Nq, Hq, dh], k and v [Nk, Hkv, dh] (rows may be further apart, as views of
+    packed qkv rows are), plan as op_attention_packed_plan wrote it for these Nq and Nk, longest = keys of the longest sequence
+    (any value is right, it picks the kernel's form); out [Nq, Hq*dh]."""
+    _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [Nq, Hq, dh]")
+    Nq, Hq, dh = q.shape
+    dev = q.get_device()
+    ldq = _packed_rows("q", q, dh, dev)
+    ldk, ldv = _packed_rows("k", k, dh, dev), _packed_rows("v", v, dh, dev)
+    Nk, Hkv = k.shape[0], k.shape[1]
+    _want(v.shape[:2] == (Nk, Hkv) and Hkv >= 1 and Hq >= 1 and Hq % Hkv == 0,
+          "k and v must have the same rows and heads, and query heads must be a multiple of them")
+    p_out = _dense("out", out, _BF16, (Nq, Hq * dh), dev)
+    _want(isinstance(plan, torch.Tensor) and plan.get_device() == dev and plan.is_contiguous(),
+          "plan must be the contiguous work list that op_attention_packed_plan wrote, on the same device")
+    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
+    if Nq == 0:
+        return
+    _launch(lib().qwen3_op_attention_prefill_packed,
+            (q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, Nq, Nk, Hq, Hkv, dh, plan.data_ptr(), plan.nbytes,
+             _int32(longest), p_out, p_err), dev, stream)

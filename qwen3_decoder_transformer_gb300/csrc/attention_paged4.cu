@@ -1,0 +1,720 @@
+// Decode attention over the paged KV cache held in 4 bits (layout: paged4.cuh).
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "paged4.cuh"
+#include "rings.h"
+
+namespace q3 {
+namespace {
+
+// One query per (sequence b, query head) over the slots 0 .. len0[b] of its sequence, each sequence at its own length:
+//   x_i = q . k_i log2(e) / sqrt(dh),  p_i = 2^(x_i - m),  O = sum_i p_i v_i / sum_i p_i.
+// K and V stay in 4 bits up to the tensor cores. With k_id = min_ig + scale_ig code_id (g: the group of 64 dims),
+//   q . k_i = sum_g scale_ig (sum_{d in g} q_d code_id) + min_ig (sum_{d in g} q_d)
+//   sum_i p_i v_id = sum_i (p_i scale_ig) code_id + sum_i p_i min_ig
+// so a code is only turned into a 16-bit operand, and scales are applied to scores and probabilities.
+//   Codes of K become fp16 by a mask alone: a nibble in the lowest bits of an fp16 word is the subnormal code * 2^-24 (the
+//   next nibble code * 2^-20, its query value divided by 16), exact on the tensor cores. q is scaled by a power of two
+//   for each head so that its fp16 form is exact (its largest value lies in [2^10, 2^11)).
+//   Codes of V become bf16 by a mask and an or: 0x4300 | code = 128 + code. P * scale is rounded to bf16, the type that the
+//   tensor cores take beside it (off by 2^-9 of itself); its sum over the keys comes out of the same products
+//   (a row of ones), and 128 times it is taken off at the end, so the offset leaves no rounding of its own.
+//
+// Work: the units of 32 keys of all (sequence, kv head) pairs in one list, cut into as many equal runs as there are warps.
+// A warp works through its run alone: its lanes 0 and 1 keep a ring of units full with untiled bulk copies, and warp-level
+// mma (m16n8k16; far below a tcgen05 tile) takes 16 keys by the heads of the group: S^T = K q^T, then O^T += V^T P^T with
+// P^T moved from accumulator to operand layout by movmatrix. The running maximum is rescaled only when it grew by 2^8.
+// A (sequence, kv head) within one run is written out at once. Of one that is cut, each warp leaves a piece (sums,
+// maximum, sum of weights); pieces of one CTA are joined in shared memory, the others in the workspace by
+// attn_paged4_join_kernel, in the order of their keys: the result does not depend on timing.
+constexpr int P4_KEYS = 32, P4_WARPS = 8, P4_THREADS = 32 * P4_WARPS, P4_CTAS = 2, P4_MAX_G = 8;
+constexpr int P4_STRIPS = P4_THREADS;  // strips of sequences whose units are counted at the start
+template <int DH>
+struct P4Layout {
+    static constexpr int NG = DH / kP4Group;
+    static constexpr int UNIT = P4_KEYS * p4_token_bytes(DH);  // bytes of K (or V) of a unit
+    static constexpr int ST = 24 / (DH / 16);                  // units in a ring: 3 (dh 128), 6 (dh 64)
+    static constexpr int RING = ST * 2 * UNIT;
+    static constexpr int PITCH = DH + 4;  // floats of a head's piece: sums, maximum, sum of weights
+    static constexpr int SMEM = P4_WARPS * RING;
+    static_assert(P4_MAX_G * PITCH * 4 <= RING, "a piece fits a ring");
+    static_assert(P4_CTAS * (SMEM + 4096) <= 227 * 1024, "shared memory");
+};
+
+// What a warp leaves of a piece that ends before its sequence does: the record of its run's first piece is slot 0, that of the
+// piece at the end of its run slot 1. first[w]: slots that hold one (bit 0, bit 1). For the warp whose run holds the
+// beginning, but not the end, of a (sequence, kv head): seg[w] is its number, last[w] the warp that holds the end, and
+// last_slot[w] its slot; otherwise seg[w] is -1.
+struct P4Desc {
+    int has, seg, last, last_slot;
+};
+
+struct P4Args {
+    const __nv_bfloat16* q;
+    __nv_bfloat16* out;
+    Paged4 cache;
+    const int* len0;
+    int B, Hq, Hkv, G, cap;  // cap: slots that the page table reaches
+    P4Desc* desc;            // [warps]
+    float* recs;             // [warps][2][G][PITCH]
+    int* err;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+// ((w >> 4 i) & 0x000f000f) | 0x43004300: codes i of both halves as bf16 values 128 + code
+__device__ __forceinline__ uint32_t code_bf16(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
+
+// Keys that sequence b's query sees.
+__device__ __forceinline__ int p4_keys(const P4Args& a, int b) {
+    const int n = __ldg(a.len0 + b);
+    return n < 0 ? 0 : n >= a.cap ? a.cap : n + 1;
+}
+__device__ __forceinline__ int p4_units(int keys) { return (keys + P4_KEYS - 1) / P4_KEYS; }
+
+// A place in the list of units: unit u of n of (sequence b, kv head h).
+struct P4Cursor {
+    int b, h, u, n, keys;
+};
+__device__ __forceinline__ void p4_step(const P4Args& a, P4Cursor& c) {
+    if (++c.u < c.n) return;
+    c.u = 0;
+    if (++c.h < a.Hkv) return;
+    c.h = 0;
+    do {  // (sequences without keys have no units)
+        ++c.b;
+        c.keys = c.b < a.B ? p4_keys(a, c.b) : 1;
+    } while (c.keys == 0);
+    c.n = p4_units(c.keys);
+}
+
+template <int DH>
+__global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
+    attn_paged4_kernel(const P4Args a) {
+    using Ly = P4Layout<DH>;
+    constexpr int NG = Ly::NG, ST = Ly::ST, UNIT = Ly::UNIT, PITCH = Ly::PITCH;
+    extern __shared__ __align__(128) uint8_t p4_rings[];
+    __shared__ uint64_t bars[P4_WARPS][2 * ST];  // [K of each stage, V of each stage]
+    __shared__ int strip_end[P4_STRIPS];         // units of one kv head up to the strip's end
+    __shared__ int warp_sum[P4_WARPS];
+    __shared__ int seg_sh[P4_WARPS], whole_sh[P4_WARPS];
+    __shared__ int abort_sh;
+    volatile int* abort_flag = &abort_sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;  // fragment coordinates
+    uint64_t* k_full = bars[warp];
+    uint64_t* v_full = bars[warp] + ST;
+    if (threadIdx.x == 0) abort_sh = 0;
+    if (lane == 0) {
+        for (int i = 0; i < 2 * ST; ++i) mbar_init(&bars[warp][i], 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    // ---------------- this warp's run of units [x0, x0 + mine)
+    const int per = (a.B + P4_STRIPS - 1) / P4_STRIPS;
+    {
+        int sum = 0;
+        const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
+        for (int b = b0; b < b1; ++b) sum += p4_units(p4_keys(a, b));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+        strip_end[threadIdx.x] = sum;
+        __syncthreads();
+    }
+    const long long units = (long long)strip_end[P4_STRIPS - 1] * a.Hkv;
+    const int gw = blockIdx.x * P4_WARPS + warp;
+    // a unit a warp at least: no run between two others is empty
+    const long long all = (long long)gridDim.x * P4_WARPS, warps = min(all, units);
+    auto run_begin = [&](long long w) { return warps ? units * w / warps : 0; };
+    const long long x0 = gw < warps ? run_begin(gw) : units, x1 = gw < warps ? run_begin(gw + 1) : units;
+    const int mine = (int)(x1 - x0);
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // sequences without keys
+        if (p4_keys(a, b) == 0)
+            for (int e = threadIdx.x; e < a.Hq * DH / 8; e += P4_THREADS)
+                reinterpret_cast<uint4*>(a.out + (size_t)b * a.Hq * DH)[e] = make_uint4(0, 0, 0, 0);
+
+    P4Cursor use{0, 0, 0, 1, 1};
+    long long seg_begin = x0;  // of the list, where the current (sequence, kv head) begins
+    if (mine > 0) {
+        // the strip, then the sequence, that holds unit x0: sequence b's units are [Hkv P_b, Hkv P_(b+1))
+        int lo = 0, hi = P4_STRIPS - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if ((long long)strip_end[mid] * a.Hkv > x0) hi = mid;
+            else lo = mid + 1;
+        }
+        long long p = lo > 0 ? strip_end[lo - 1] : 0;
+        use.b = lo * per;
+        while (true) {
+            use.keys = p4_keys(a, use.b);
+            use.n = p4_units(use.keys);
+            if ((p + use.n) * a.Hkv > x0) break;
+            p += use.n;
+            ++use.b;
+        }
+        const long long in = x0 - p * a.Hkv;
+        use.h = (int)(in / use.n);
+        use.u = (int)(in - (long long)use.h * use.n);
+        seg_begin = x0 - use.u;
+    }
+
+    // ---------------- the ring: copies of the unit at `ask`
+    P4Cursor ask = use;
+    const int page_log = a.cache.page_log, page = 1 << page_log;
+    const size_t page_bytes = p4_page_bytes(page, DH);
+    const bool small = page < P4_KEYS;  // a unit is two pages of 16 tokens
+    const uint32_t ring_a = smem_u32(p4_rings + warp * Ly::RING);
+    // tile i (16 keys) of a unit: codes at i * tile_step, scales and minima at side_off + i * side_step
+    const int tile_step = small ? 16 * p4_token_bytes(DH) : 16 * DH / 2;
+    const int side_off = small ? 16 * DH / 2 : P4_KEYS * DH / 2, side_step = small ? tile_step : 16 * NG * 4;
+    int tab = 0, tab_b = -1, tab_at = 0;  // this lane's entry of the page table, tab_at + lane of sequence tab_b
+    long long src = 0;                    // lanes 0 and 1: offset of their copy in the pages
+    uint32_t src_bytes = 0, unit_bytes = 0;
+    bool bad_page = false;
+    auto locate = [&]() {  // where the unit at `ask` lies
+        const int first = small ? ask.u * 2 : ask.u * P4_KEYS >> page_log, at = first & ~31;
+        if (tab_b != ask.b || tab_at != at) {
+            tab_b = ask.b;
+            tab_at = at;
+            tab = at + lane < a.cache.max_pages ? __ldg(a.cache.table + (size_t)ask.b * a.cache.max_pages + at + lane) : 0;
+        }
+        int id = __shfl_sync(0xffffffffu, tab, (first & 31) + (small ? (lane & 1) : 0));
+        const int blocks = small && ask.keys - ask.u * P4_KEYS > 16 ? 2 : 1;
+        const bool mine_bad = (unsigned)id >= (unsigned)a.cache.n_pages && (lane & 1) < blocks;
+        bad_page = bad_page || mine_bad;
+        if ((unsigned)id >= (unsigned)a.cache.n_pages) id = 0;  // (flagged; the output is invalid)
+        src = ((long long)id * a.Hkv + ask.h) * (long long)page_bytes;
+        if (small) {
+            src_bytes = lane < blocks ? 16 * p4_token_bytes(DH) : 0;
+            unit_bytes = blocks * 16 * p4_token_bytes(DH);
+        } else {
+            const int row = (ask.u * P4_KEYS) & (page - 1);
+            src += lane == 0 ? row * (DH / 2) : page * (DH / 2) + row * NG * 4;
+            src_bytes = lane == 0 ? P4_KEYS * DH / 2 : lane == 1 ? P4_KEYS * NG * 4 : 0;
+            unit_bytes = UNIT;
+        }
+    };
+    auto load = [&](const uint8_t* pages, uint64_t* full, int st, int off) {
+        if (lane == 0) mbar_expect_tx(&full[st], unit_bytes);
+        __syncwarp();
+        if (lane < 2 && src_bytes)
+            bulk_load(ring_a + st * 2 * UNIT + off + (lane == 0 ? 0 : small ? 16 * p4_token_bytes(DH) : P4_KEYS * DH / 2),
+                      pages + src, src_bytes, &full[st]);
+    };
+    __syncwarp();  // the barriers are set
+    for (int i = 0; i < min(ST, mine); ++i) {
+        locate();
+        load(a.cache.k, k_full, i, 0);
+        load(a.cache.v, v_full, i, UNIT);
+        p4_step(a, ask);
+    }
+
+    // ---------------- products
+    const float sl2 = kLog2e / sqrtf((float)DH);
+    uint32_t qf[NG][4][2];      // q^T fragments: column g = query head g of the group (zero past G)
+    float qs[NG][2], qscale[2]; // heads 2t and 2t + 1: sums of the fp16 values of a group of dims; what they are scaled by
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[NG][4][4], r[NG][4], z[NG][2];
+    auto reset = [&]() {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            m[e] = -INFINITY;
+            l[e] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < NG; ++c) {
+            z[c][0] = z[c][1] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                r[c][e] = 0.f;
+                o[c][0][e] = o[c][1][e] = o[c][2][e] = o[c][3][e] = 0.f;
+            }
+        }
+    };
+    auto load_q = [&]() {
+        float x[NG][16];
+        float big = 0.f;
+        const __nv_bfloat16* row = a.q + ((size_t)use.b * a.Hq + (size_t)use.h * a.G + g) * DH + 16 * t;
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (g < a.G) v = __ldg(reinterpret_cast<const uint4*>(row + c * kP4Group) + e);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[c][e * 8 + 2 * i] = bf16_lo(w[i]);
+                    x[c][e * 8 + 2 * i + 1] = bf16_hi(w[i]);
+                }
+            }
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(x[c][i]));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^-e: the head's largest value comes to [2^10, 2^11)
+        const int e = min(max((int)(__float_as_uint(big) >> 23) - 137, -100), 100);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        float sums[NG];
+#pragma unroll
+        for (int c = 0; c < NG; ++c) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[c][i] *= down;
+                s += x[c][i];
+            }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            sums[c] = s * 5.9604644775390625e-8f;  // 2^-24, the unit of the products of codes
+            auto pair = [](float lo, float hi) {
+                const __half2 v = __floats2half2_rn(lo, hi);
+                return *reinterpret_cast<const uint32_t*>(&v);
+            };
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // word k / 2, nibbles 2 (k % 2) and that + 4; then the ones after them
+                const int d = (k >> 1) * 8 + (k & 1) * 2;
+                qf[c][k][0] = pair(x[c][d], x[c][d + 4]);
+                qf[c][k][1] = pair(x[c][d + 1] * 0.0625f, x[c][d + 5] * 0.0625f);
+            }
+        }
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23) * 16777216.f * sl2;
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+            const int from = (2 * t + e2) * 4;
+            qscale[e2] = __shfl_sync(0xffffffffu, up, from);
+#pragma unroll
+            for (int c = 0; c < NG; ++c) qs[c][e2] = __shfl_sync(0xffffffffu, sums[c], from);
+        }
+    };
+    // the sums of this warp's piece at scale m: dims c * 64 + 8 g + (0..7) of head 2t + e
+    auto piece = [&](int c, int e, float (&v)[8]) {
+        const float add = z[c][e] - 128.f * r[c][e];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = o[c][i][e] + add;
+            v[4 + i] = o[c][i][2 + e] + add;
+        }
+    };
+    auto total = [&]() {  // l and z over the keys that other lanes took
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], s);
+#pragma unroll
+                for (int c = 0; c < NG; ++c) z[c][e] += __shfl_xor_sync(0xffffffffu, z[c][e], s);
+            }
+        }
+    };
+    auto leave = [&](float* rec) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = 2 * t + e;
+            if (h >= a.G) continue;
+#pragma unroll
+            for (int c = 0; c < NG; ++c) {
+                float v[8];
+                piece(c, e, v);
+                float4* dst = reinterpret_cast<float4*>(rec + h * PITCH + c * kP4Group + 8 * g);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+            if (g == 0) *reinterpret_cast<float2*>(rec + h * PITCH + DH) = make_float2(m[e], l[e]);
+        }
+    };
+    auto write_out = [&]() {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = 2 * t + e;
+            if (h >= a.G) continue;
+            const float inv = 1.f / l[e];
+#pragma unroll
+            for (int c = 0; c < NG; ++c) {
+                float v[8];
+                piece(c, e, v);
+                *reinterpret_cast<uint4*>(a.out + ((size_t)use.b * a.Hq + (size_t)use.h * a.G + h) * DH + c * kP4Group + 8 * g) =
+                    make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                               pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+            }
+        }
+    };
+    float* my_recs = a.recs + (size_t)gw * 2 * a.G * PITCH;
+    int has = 0;
+    const int swap = (g & 4) | (g & 1) << 1 | (g >> 1 & 1);  // row g of a tile is key swap (and row g + 8 key swap + 8):
+    const int vkey = (2 * t & 4) | (t & 1);                  // the keys of rows 2t, which one load of V takes, are 0, 1, 4, 5
+    bool ok = true, ahead = false;
+    reset();
+    int i = 0;
+    for (; i < mine; ++i) {
+        if (i == 0 || use.u == 0) load_q();
+        const int st = i % ST, ph = (i / ST) & 1;
+        const uint32_t ka = ring_a + st * 2 * UNIT, va = ka + UNIT;
+        if (!__all_sync(0xffffffffu, mbar_wait_suspend(&k_full[st], ph, abort_flag))) { ok = false; break; }
+        const int valid = use.keys - use.u * P4_KEYS;  // keys of the unit, 32 or more: all
+        const int tiles = valid > 16 ? 2 : 1;
+        float x[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k < tiles) {
+                const uint32_t codes = ka + k * tile_step + swap * (DH / 2) + 8 * t, side = ka + side_off + k * side_step + swap * (NG * 4);
+                float acc[NG][4];
+                uint32_t sd[2][NG];
+                if constexpr (NG == 2) {
+                    const uint2 s0 = lds64(side), s1 = lds64(side + 8 * NG * 4);
+                    sd[0][0] = s0.x;
+                    sd[0][1] = s0.y;
+                    sd[1][0] = s1.x;
+                    sd[1][1] = s1.y;
+                } else {
+                    sd[0][0] = lds32(side);
+                    sd[1][0] = lds32(side + 8 * NG * 4);
+                }
+#pragma unroll
+                for (int c = 0; c < NG; ++c) {
+                    const uint2 w0 = lds64(codes + c * 32), w1 = lds64(codes + 8 * (DH / 2) + c * 32);
+                    acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+                    const uint32_t a0[2] = {w0.x, w0.y}, a1[2] = {w1.x, w1.y};
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const uint32_t y0 = a0[w] >> 8, y1 = a1[w] >> 8;
+                        mma_f16(acc[c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u, a1[w] & 0x00f000f0u,
+                                qf[c][2 * w][0], qf[c][2 * w][1]);
+                        mma_f16(acc[c], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
+                                qf[c][2 * w + 1][0], qf[c][2 * w + 1][1]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int c = 0; c < NG; ++c)
+                        s = fmaf(bf16_lo(sd[e >> 1][c]), acc[c][e], fmaf(bf16_hi(sd[e >> 1][c]), qs[c][e & 1], s));
+                    x[k][e] = s * qscale[e & 1];
+                }
+                if (valid < P4_KEYS) {
+                    if (k * 16 + swap >= valid) x[k][0] = x[k][1] = -INFINITY;
+                    if (k * 16 + swap + 8 >= valid) x[k][2] = x[k][3] = -INFINITY;
+                }
+            } else {
+                x[k][0] = x[k][1] = x[k][2] = x[k][3] = -INFINITY;
+            }
+        }
+        __syncwarp();  // every lane has read the unit's keys: the next ones may come
+        ahead = i + ST < mine;
+        if (ahead) {
+            locate();
+            load(a.cache.k, k_full, st, 0);
+        }
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e]));
+        // O and the sums move to a larger maximum only when it grew by more than 8 (P <= 2^8)
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], s));
+                const bool grow = mx[e] > m[e] + 8.f;
+                const float f = grow ? ex2_approx(m[e] - mx[e]) : 1.f;
+                m[e] = grow ? mx[e] : m[e];
+                l[e] *= f;
+#pragma unroll
+                for (int c = 0; c < NG; ++c) {
+                    z[c][e] *= f;
+                    r[c][e] *= f;
+                    r[c][2 + e] *= f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[c][k][e] *= f;
+                        o[c][k][2 + e] *= f;
+                    }
+                }
+            }
+        }
+        const float nm[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[k][e] = ex2_approx(x[k][e] + nm[e & 1]);
+                l[e & 1] += x[k][e];
+            }
+        if (!__all_sync(0xffffffffu, mbar_wait_suspend(&v_full[st], ph, abort_flag))) { ok = false; break; }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k < tiles) {
+                const uint32_t side = va + side_off + k * side_step + swap * (NG * 4);
+                uint32_t sd[2][NG];
+                if constexpr (NG == 2) {
+                    const uint2 s0 = lds64(side), s1 = lds64(side + 8 * NG * 4);
+                    sd[0][0] = s0.x;
+                    sd[0][1] = s0.y;
+                    sd[1][0] = s1.x;
+                    sd[1][1] = s1.y;
+                } else {
+                    sd[0][0] = lds32(side);
+                    sd[1][0] = lds32(side + 8 * NG * 4);
+                }
+                if (valid < P4_KEYS) {  // what stands behind the last key may be anything: 0 * NaN must not reach O
+#pragma unroll
+                    for (int c = 0; c < NG; ++c) {
+                        if (k * 16 + swap >= valid) sd[0][c] = 0;
+                        if (k * 16 + swap + 8 >= valid) sd[1][c] = 0;
+                    }
+                }
+                const uint32_t codes = va + k * tile_step + vkey * (DH / 2) + 4 * g;
+#pragma unroll
+                for (int c = 0; c < NG; ++c) {
+                    const float s0 = bf16_lo(sd[0][c]), s1 = bf16_lo(sd[1][c]);
+                    const float z0 = bf16_hi(sd[0][c]), z1 = bf16_hi(sd[1][c]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) z[c][e] = fmaf(x[k][e], z0, fmaf(x[k][2 + e], z1, z[c][e]));
+                    const uint32_t b0 = transpose8x8(pack_bf16(x[k][0] * s0, x[k][1] * s0));
+                    const uint32_t b1 = transpose8x8(pack_bf16(x[k][2] * s1, x[k][3] * s1));
+                    // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further
+                    const uint32_t wa = lds32(codes + c * 32), wb = lds32(codes + c * 32 + 2 * (DH / 2));
+                    const uint32_t wc = lds32(codes + c * 32 + 8 * (DH / 2)), wd = lds32(codes + c * 32 + 10 * (DH / 2));
+                    const uint32_t lo0 = __byte_perm(wa, wb, 0x5410), hi0 = __byte_perm(wa, wb, 0x7632);
+                    const uint32_t lo1 = __byte_perm(wc, wd, 0x5410), hi1 = __byte_perm(wc, wd, 0x7632);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mma_bf16(o[c][q], code_bf16(lo0, q), code_bf16(hi0, q), code_bf16(lo1, q), code_bf16(hi1, q), b0, b1);
+                    mma_bf16(r[c], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, b0, b1);
+                }
+            }
+        }
+        __syncwarp();
+        if (ahead) {
+            load(a.cache.v, v_full, st, UNIT);
+            p4_step(a, ask);
+        }
+        ahead = false;
+        const bool seg_done = use.u + 1 == use.n;
+        if (seg_done && i + 1 < mine) {  // the sequence ends within the run
+            total();
+            if (seg_begin >= x0) {
+                write_out();
+            } else {
+                leave(my_recs);
+                has |= 1;
+            }
+            reset();
+            seg_begin = x0 + i + 1;
+        }
+        if (i + 1 < mine) p4_step(a, use);
+    }
+    if (__any_sync(0xffffffffu, bad_page) && lane == 0 && a.err) atomicOr(a.err, ERR_INDEX);
+    if (!ok) {  // give up: wait, bounded, for the copies still on their way
+        *abort_flag = 1;
+        if (a.err && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
+        int never = 0;
+        for (int k = i; k < min(i + ST, mine); ++k) mbar_wait_suspend(&v_full[k % ST], (k / ST) & 1, &never);
+        for (int k = i; k < min(i + ST + 1, mine); ++k)
+            if (k < i + ST || ahead) mbar_wait_suspend(&k_full[k % ST], (k / ST) & 1, &never);
+    }
+
+    // ---------------- the piece at the end of the run
+    const bool ends = mine > 0 && use.u + 1 == use.n;          // the sequence ends with the run
+    const bool open = mine > 0 && !(seg_begin >= x0 && ends);  // a part of it lies in another run
+    total();
+    if (mine > 0 && !open && ok) write_out();
+    const int seg = use.b * a.Hkv + use.h;
+    float* my_smem = reinterpret_cast<float*>(p4_rings + warp * Ly::RING);
+    if (open) leave(my_smem);  // (the ring is done)
+    if (lane == 0) {
+        seg_sh[warp] = open ? seg : -1;
+        whole_sh[warp] = (open && seg_begin >= x0 ? 1 : 0) | (open && ends ? 2 : 0);  // begins, ends in this run
+    }
+    __syncthreads();
+    const int G = a.G, quads = G * (DH / 4);
+    for (int w0 = 0; w0 < P4_WARPS;) {
+        const int s = seg_sh[w0];
+        int w1 = w0 + 1;
+        while (w1 < P4_WARPS && s >= 0 && seg_sh[w1] == s) ++w1;
+        if (s >= 0) {
+            const bool whole = (whole_sh[w0] & 1) && (whole_sh[w1 - 1] & 2);
+            for (int e = threadIdx.x; e < quads; e += P4_THREADS) {
+                const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
+                const float* rec = reinterpret_cast<const float*>(p4_rings) + h * PITCH;
+                constexpr int STEP = Ly::RING / 4;
+                float M = -INFINITY, L = 0.f;
+                for (int w = w0; w < w1; ++w) M = fmaxf(M, rec[w * STEP + DH]);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = w0; w < w1; ++w) {
+                    const float mw = rec[w * STEP + DH];
+                    // (a piece whose scores are all NaN keeps m = -inf, and its sums are NaN)
+                    const float f = mw == -INFINITY ? 1.f : ex2_approx(mw - M);
+                    const float4 y = *reinterpret_cast<const float4*>(rec + w * STEP + dd);
+                    L = fmaf(rec[w * STEP + DH + 1], f, L);
+                    v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
+                }
+                if (whole) {
+                    const float inv = 1.f / L;
+                    const size_t row = (size_t)(s / a.Hkv) * a.Hq + (size_t)(s % a.Hkv) * G + h;
+                    *reinterpret_cast<uint2*>(a.out + row * DH + dd) =
+                        make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+                } else {
+                    float* dst = a.recs + ((size_t)(blockIdx.x * P4_WARPS + w0) * 2 + 1) * G * PITCH + h * PITCH;
+                    *reinterpret_cast<float4*>(dst + dd) = v;
+                    if (dd == 0) *reinterpret_cast<float2*>(dst + DH) = make_float2(M, L);
+                }
+            }
+            if (warp == w0 && !whole) has |= 2;
+        }
+        w0 = w1;
+    }
+    if (lane == 0) {
+        P4Desc d{has, -1, 0, 0};
+        if (open && seg_begin >= x0 && !ends) {
+            const long long end = seg_begin + use.n;  // of the segment
+            d.last = (int)((end * warps - 1) / units);
+            d.last_slot = run_begin(d.last + 1) == end ? 1 : 0;
+            // within the CTA it is written out already
+            if (d.last / P4_WARPS != (int)blockIdx.x) d.seg = seg;
+            else if (d.last_slot == 0) d.seg = seg;
+        }
+        a.desc[gw] = d;
+    }
+}
+
+// Join the pieces of the (sequence, kv head) that begins in warp blockIdx.x's run: quads of dims by ways of pieces.
+constexpr int P4_JOIN_THREADS = 256;
+template <int DH>
+__global__ void __launch_bounds__(P4_JOIN_THREADS)
+    attn_paged4_join_kernel(const P4Args a) {
+    constexpr int PITCH = P4Layout<DH>::PITCH;
+    __shared__ float4 part[P4_JOIN_THREADS];
+    __shared__ float2 stat[P4_JOIN_THREADS];
+    pdl_wait();
+    pdl_trigger();
+    const P4Desc d = a.desc[blockIdx.x];
+    if (d.seg < 0) return;
+    const int first = blockIdx.x, G = a.G, quads = G * (DH / 4);
+    const int ways = max(1, P4_JOIN_THREADS / quads);
+    const int e = threadIdx.x % quads, way = threadIdx.x / quads;
+    const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
+    float M = -INFINITY, L = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float m, float l, const float4& y) {
+        if (m > M) {
+            const float f = M == -INFINITY ? 1.f : ex2_approx(M - m);
+            L *= f;
+            v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            M = m;
+        }
+        const float f = m == -INFINITY ? 1.f : ex2_approx(m - M);
+        L = fmaf(l, f, L);
+        v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
+    };
+    if (way < ways)
+        for (int w = first + way; w <= d.last; w += ways) {
+            const int slot = w == d.last ? d.last_slot : 1;
+            if (!(a.desc[w].has >> slot & 1)) continue;
+            const float* rec = a.recs + ((size_t)w * 2 + slot) * G * PITCH + h * PITCH;
+            const float2 ml = *reinterpret_cast<const float2*>(rec + DH);
+            add(ml.x, ml.y, *reinterpret_cast<const float4*>(rec + dd));
+        }
+    part[threadIdx.x] = v;
+    stat[threadIdx.x] = make_float2(M, L);
+    __syncthreads();
+    if (way > 0) return;
+    for (int k = 1; k < ways; ++k) add(stat[k * quads + e].x, stat[k * quads + e].y, part[k * quads + e]);
+    const float inv = 1.f / L;
+    const size_t row = (size_t)(d.seg / a.Hkv) * a.Hq + (size_t)(d.seg % a.Hkv) * G + h;
+    *reinterpret_cast<uint2*>(a.out + row * DH + dd) =
+        make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+}
+
+int p4_ctas() { return device_sm_count() * P4_CTAS; }
+
+template <int DH>
+cudaError_t paged4_launch_dh(P4Args a, cudaStream_t st) {
+    const int ctas = p4_ctas();
+    cudaError_t e = launch_pdl(attn_paged4_kernel<DH>, dim3(ctas), dim3(P4_THREADS), P4Layout<DH>::SMEM, st, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attn_paged4_join_kernel<DH>, dim3(ctas * P4_WARPS), dim3(P4_JOIN_THREADS), 0, st, a);
+}
+
+size_t desc_bytes(int warps) { return ((size_t)warps * sizeof(P4Desc) + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t attn_decode_paged4_workspace(int G, int dh) {
+    const int warps = p4_ctas() * P4_WARPS;
+    return desc_bytes(warps) + (size_t)warps * 2 * G * (dh + 4) * sizeof(float);
+}
+
+cudaError_t attn_decode_paged4_launch(const __nv_bfloat16* q, const void* k_pages, const void* v_pages, int n_pages, int page,
+                                      const int* table, int max_pages, const int* len0, int B, int Hq, int Hkv, int dh,
+                                      void* work, __nv_bfloat16* out, int* err, cudaStream_t st) {
+    P4Args a{};
+    a.q = q;
+    a.out = out;
+    int log = 0;
+    while (1 << log < page) ++log;
+    a.cache = Paged4{static_cast<const uint8_t*>(k_pages), static_cast<const uint8_t*>(v_pages), table, n_pages, max_pages, log};
+    a.len0 = len0;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.cap = (int)std::min<long long>((long long)max_pages * page, 1 << 30);
+    a.desc = static_cast<P4Desc*>(work);
+    a.recs = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + desc_bytes(p4_ctas() * P4_WARPS));
+    a.err = err;
+    return dh == 128 ? paged4_launch_dh<128>(a, st) : paged4_launch_dh<64>(a, st);
+}
+
+cudaError_t attention_paged4_prepare() {
+    cudaError_t e = cudaFuncSetAttribute(attn_paged4_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, P4Layout<128>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attn_paged4_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, P4Layout<64>::SMEM);
+    return e;
+}
+
+}  // namespace q3

@@ -49,7 +49,7 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
 }
 
 // Device error-flag bits (one int per context, read by qwen3_get_error).
-enum : int { ERR_TOKEN = 1, ERR_TIMEOUT = 2 };
+enum : int { ERR_TOKEN = 1, ERR_TIMEOUT = 2, ERR_INDEX = 4 };
 
 enum Epilogue : int { EPI_BF16 = 0, EPI_SWIGLU = 1, EPI_RESIDUAL = 2, EPI_F32 = 3, EPI_QKV_ROPE = 4, EPI_RESIDUAL_NORM = 5 };
 
@@ -137,6 +137,10 @@ bool encode_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64
 // (0, row, 0, head), rows past `rows` read as zero.
 bool encode_tmap_bf16_units(CUtensorMap* map, const void* base, uint64_t dh, uint64_t rows, uint64_t row_cap,
                             uint64_t heads, uint32_t box_rows);
+// Rows [rows] of `blocks` 64-column blocks, row_bytes apart, in boxes of box_rows rows by box_blocks blocks; coordinates
+// (0, row, block), rows past `rows` read as zero.
+bool encode_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t blocks, uint64_t rows, uint64_t row_bytes,
+                           uint32_t box_rows, uint32_t box_blocks);
 // Query rows [seqs][heads][group][dh] in boxes of 64 x group x 1 x box_seqs: one head's groups of box_seqs sequences.
 bool encode_tmap_bf16_groups(CUtensorMap* map, const void* base, uint64_t dh, uint64_t group, uint64_t heads,
                              uint64_t seqs, uint32_t box_seqs);
@@ -229,6 +233,41 @@ int attn_decode_kernel_count();
 size_t attn_decode_noalloc_max_bytes();
 cudaError_t attn_decode_noalloc_scratch(float** ptr);
 
+// Packed sequences: the work list of attn_packed_plan_launch, and a call that walks it (the persistent prefill kernel).
+struct PackedTiles {
+    const int4* items;  // (first query row, rows, first key row of the sequence, key position of the first query row)
+    const int* count;
+    int capacity, max_keys;
+};
+struct PackedCall {
+    const __nv_bfloat16 *q, *k, *v;
+    long long ldq, ldk, ldv;  // elements from row to row
+    int Nq, Nk, Hq, Hkv;
+    const void* plan;
+    int capacity, longest;  // longest: keys of the longest sequence; it only picks between equivalent forms
+    __nv_bfloat16* out;
+    int* err;
+};
+size_t attn_packed_plan_bytes(int Nq, int S);
+int attn_packed_capacity(size_t bytes);  // items that a plan of this size holds
+cudaError_t attn_packed_plan_launch(const int* cu_q, const int* cu_k, int S, int Nq, int Nk, void* plan, int capacity, int* err,
+                                    cudaStream_t st);
+cudaError_t attn_packed_launch(const PackedCall& c, int dh, cudaStream_t st);
+
+// ---------------------------------------------------------------- the paged 4-bit cache (paged4.cu, attention_paged4.cu)
+cudaError_t append_paged4_launch(const __nv_bfloat16* qkv, long long ld, int N, const int* cu, const int* start, int S, int Hq,
+                                 int Hkv, int dh, const __nv_bfloat16* q_gamma, const __nv_bfloat16* k_gamma, float eps,
+                                 const __nv_bfloat16* cos_sin, int n_pos, __nv_bfloat16* q_out, __nv_bfloat16* k_out,
+                                 void* k_pages, void* v_pages, int n_pages, int page, const int* table, int max_pages,
+                                 int* err, cudaStream_t st);
+cudaError_t read_paged4_launch(const void* k_pages, const void* v_pages, int n_pages, int page, const int* table, int max_pages,
+                               const int* cu, const int* start, int S, int N, int Hkv, int dh, __nv_bfloat16* k_out,
+                               __nv_bfloat16* v_out, int* err, cudaStream_t st);
+size_t attn_decode_paged4_workspace(int G, int dh);
+cudaError_t attn_decode_paged4_launch(const __nv_bfloat16* q, const void* k_pages, const void* v_pages, int n_pages, int page,
+                                      const int* table, int max_pages, const int* len0, int B, int Hq, int Hkv, int dh,
+                                      void* work, __nv_bfloat16* out, int* err, cudaStream_t st);
+
 // ---------------------------------------------------------------- attention over chosen key tiles (attention_tiles.cu)
 // Sliding window with sinks: slot i sees slots j <= i with i - j < window or j < sinks. ring > 0 is a rolling
 // buffer of sink_rows + ring cache rows: slot s < sink_rows is stored at s, the others at
@@ -277,6 +316,7 @@ cudaError_t gemm_prepare();
 cudaError_t attention_prepare();
 cudaError_t attention_tiles_prepare();
 cudaError_t attention_ranges_prepare();
+cudaError_t attention_paged4_prepare();
 cudaError_t token_logprobs_prepare();
 cudaError_t prepare_kernels();
 

@@ -77,6 +77,7 @@ cudaError_t prepare_kernels() {
     if (e == cudaSuccess) e = attention_prepare();
     if (e == cudaSuccess) e = attention_tiles_prepare();
     if (e == cudaSuccess) e = attention_ranges_prepare();
+    if (e == cudaSuccess) e = attention_paged4_prepare();
     if (e == cudaSuccess) e = token_logprobs_prepare();
     if (e == cudaSuccess) done[dev] = true;
     return e;
@@ -1141,6 +1142,124 @@ int qwen3_op_attention_decode_sinks(const void* q, const void* kc, const void* v
                                     static_cast<bf16*>(out), err, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? QWEN3_OK
                : QWEN3_E_CUDA;
+}
+
+// ------------------------------------------------------------------ the paged 4-bit cache and packed sequences
+namespace {
+bool page_ok(int page, int dh) {
+    return page >= 16 && page <= 256 && (page & (page - 1)) == 0 && (dh == 64 || dh == 128);
+}
+bool pages_ok(const void* kp, const void* vp, int n_pages, int page, int dh, const int* table, int max_pages) {
+    return kp && vp && table && n_pages >= 1 && max_pages >= 1 && page_ok(page, dh) && is_aligned(kp, 16) && is_aligned(vp, 16);
+}
+constexpr int kMaxRows = 1 << 30;  // rows of a packed batch
+}  // namespace
+
+size_t qwen3_paged4_page_bytes(int page_size, int dh) {
+    return page_ok(page_size, dh) ? (size_t)page_size * (dh / 2 + dh / 64 * 4) : 0;
+}
+
+int qwen3_op_append_paged4(const void* qkv, int64_t ld, int N, const int* cu, const int* start, int S, int Hq, int Hkv, int dh,
+                           const void* q_gamma, const void* k_gamma, float eps, const void* cos_sin, int n_pos, void* q_out,
+                           void* k_out, void* k_pages, void* v_pages, int n_pages, int page_size, const int* table,
+                           int max_pages, int* err, void* stream) {
+    if (N < 0 || N > kMaxRows || S < 0 || S > kMaxRows || Hq < 1 || Hkv < 1 || Hq > 65535 || Hkv > 65535 || Hq % Hkv ||
+        !pages_ok(k_pages, v_pages, n_pages, page_size, dh, table, max_pages))
+        return QWEN3_E_ARG;
+    if (!qkv || !cu || !start || !cos_sin || !q_out || n_pos < 1 || ld < (int64_t)(Hq + 2 * Hkv) * dh || ld % 8)
+        return QWEN3_E_ARG;
+    const void* ptrs[] = {qkv, q_gamma, k_gamma, cos_sin, q_out, k_out};
+    for (const void* p : ptrs)
+        if (!is_aligned(p, 16)) return QWEN3_E_ARG;
+    if (N == 0 || S == 0) return QWEN3_OK;
+    if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
+    return append_paged4_launch(static_cast<const bf16*>(qkv), ld, N, cu, start, S, Hq, Hkv, dh,
+                                static_cast<const bf16*>(q_gamma), static_cast<const bf16*>(k_gamma), eps,
+                                static_cast<const bf16*>(cos_sin), n_pos, static_cast<bf16*>(q_out),
+                                static_cast<bf16*>(k_out), k_pages, v_pages, n_pages, page_size, table, max_pages, err,
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QWEN3_OK
+               : QWEN3_E_CUDA;
+}
+
+int qwen3_op_read_paged4(const void* k_pages, const void* v_pages, int n_pages, int page_size, const int* table, int max_pages,
+                         const int* cu, const int* start, int S, int N, int Hkv, int dh, void* k_out, void* v_out, int* err,
+                         void* stream) {
+    if (N < 0 || N > kMaxRows || S < 0 || S > kMaxRows || Hkv < 1 || Hkv > 65535 ||
+        !pages_ok(k_pages, v_pages, n_pages, page_size, dh, table, max_pages))
+        return QWEN3_E_ARG;
+    if (!cu || !start || !k_out || !v_out || !is_aligned(k_out, 16) || !is_aligned(v_out, 16)) return QWEN3_E_ARG;
+    if (N == 0 || S == 0) return QWEN3_OK;
+    if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
+    return read_paged4_launch(k_pages, v_pages, n_pages, page_size, table, max_pages, cu, start, S, N, Hkv, dh,
+                              static_cast<bf16*>(k_out), static_cast<bf16*>(v_out), err,
+                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QWEN3_OK
+               : QWEN3_E_CUDA;
+}
+
+size_t qwen3_attention_decode_paged4_workspace(int B, int Hq, int Hkv, int dh) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 8 || (dh != 64 && dh != 128)) return 0;
+    return attn_decode_paged4_workspace(Hq / Hkv, dh);
+}
+
+int qwen3_op_attention_decode_paged4(const void* q, const void* k_pages, const void* v_pages, int n_pages, int page_size,
+                                     const int* table, int max_pages, const int* len0, int B, int Hq, int Hkv, int dh,
+                                     void* work, size_t work_bytes, void* out, int* err, void* stream) {
+    if (B < 0 || B > 65535 || Hq < 1 || Hkv < 1 || Hkv > 65535 || Hq % Hkv || Hq / Hkv > 8 ||
+        !pages_ok(k_pages, v_pages, n_pages, page_size, dh, table, max_pages))
+        return QWEN3_E_ARG;
+    if (!q || !len0 || !work || !out || !is_aligned(q, 16) || !is_aligned(out, 16) || !is_aligned(work, 16)) return QWEN3_E_ARG;
+    // the kernel counts the (sequence, kv head) pairs, and the units of 32 keys of one kv head, in an int
+    const long long slots = std::min<long long>((long long)max_pages * page_size, kMaxSlots);
+    if ((long long)B * Hkv > 0x7fffffff || B * ((slots + 31) / 32) > 0x7fffffff) return QWEN3_E_ARG;
+    if (B == 0) return QWEN3_OK;
+    if (work_bytes < attn_decode_paged4_workspace(Hq / Hkv, dh)) return QWEN3_E_ARG;
+    if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
+    return attn_decode_paged4_launch(static_cast<const bf16*>(q), k_pages, v_pages, n_pages, page_size, table, max_pages, len0,
+                                     B, Hq, Hkv, dh, work, static_cast<bf16*>(out), err,
+                                     static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QWEN3_OK
+               : QWEN3_E_CUDA;
+}
+
+size_t qwen3_attention_packed_plan_bytes(int Nq, int S) {
+    return Nq < 0 || Nq > kMaxRows || S < 0 || S > kMaxRows ? 0 : attn_packed_plan_bytes(Nq, S);
+}
+
+int qwen3_op_attention_packed_plan(const int* cu_q, const int* cu_k, int S, int Nq, int Nk, void* plan, size_t plan_bytes,
+                                   int* err, void* stream) {
+    if (!cu_q || !cu_k || !plan || S < 0 || S > kMaxRows || Nq < 0 || Nq > kMaxRows || Nk < 0 || Nk > kMaxRows ||
+        !is_aligned(plan, 16) || plan_bytes < attn_packed_plan_bytes(Nq, S))
+        return QWEN3_E_ARG;
+    if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
+    return attn_packed_plan_launch(cu_q, cu_k, S, Nq, Nk, plan, attn_packed_capacity(attn_packed_plan_bytes(Nq, S)), err,
+                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QWEN3_OK
+               : QWEN3_E_CUDA;
+}
+
+int qwen3_op_attention_prefill_packed(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                      int Nq, int Nk, int Hq, int Hkv, int dh, const void* plan, size_t plan_bytes,
+                                      int longest, void* out, int* err, void* stream) {
+    if (!q || !plan || !out || Nq < 0 || Nq > kMaxRows || Nk < 0 || Nk > kMaxRows || (Nk > 0 && (!k || !v)) || Hq < 1 ||
+        Hkv < 1 || Hq > 65535 || Hq % Hkv || (dh != 64 && dh != 128))
+        return QWEN3_E_ARG;
+    const int64_t lds[] = {ldq, ldk, ldv};
+    const void* ptrs[] = {q, k, v, plan, out};
+    for (const void* p : ptrs)
+        if (!is_aligned(p, 16)) return QWEN3_E_ARG;
+    for (int i = 0; i < 3; ++i)  // (a row stride of a tensor map: a multiple of 16 bytes below 2^40)
+        if (lds[i] < (int64_t)(i == 0 ? Hq : Hkv) * dh || lds[i] % 8 || lds[i] >= (int64_t)1 << 38) return QWEN3_E_ARG;
+    if (plan_bytes < attn_packed_plan_bytes(Nq, 0)) return QWEN3_E_ARG;
+    // the kernel counts items in an int, up to two rounds of CTAs past the last one
+    const long long capacity = attn_packed_capacity(plan_bytes);
+    if (capacity * Hq > 0x7fff0000) return QWEN3_E_ARG;
+    if (Nq == 0 || capacity == 0) return QWEN3_OK;
+    if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
+    const PackedCall c{static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v), ldq, ldk, ldv, Nq,
+                       Nk, Hq, Hkv, plan, (int)capacity, longest, static_cast<bf16*>(out), err};
+    return attn_packed_launch(c, dh, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QWEN3_OK : QWEN3_E_CUDA;
 }
 
 int qwen3_op_attention_decode_noalloc(const void* q, const void* kc, const void* vc, int B, int Hq, int Hkv, int dh,

@@ -1,0 +1,616 @@
+"""The paged 4-bit cache: append (qwen3_op_append_paged4), read (qwen3_op_read_paged4) and decode attention
+(qwen3_op_attention_decode_paged4) against float64.
+
+Tolerances. A bf16 result is off by half a step, 2^-8 of its value at most.
+  Rotated heads: fp32 products and sums of a few terms of the size |a| + |b| of the rotated pair, after a norm whose sum of
+  up to 128 squares is off by at most 128 * 2^-24 of itself (half of that in its root): 2^-16 (|a| + |b|) covers both.
+  Cached values: a code stands for a value within half a scale of it; the fp32 key that is quantised is off as above.
+  Decode: the reference takes the cache's own bytes, so K and V are exact. Probability times scale is rounded to bf16
+  (2^-8 of itself) before it multiplies codes 0..15; those products carry an offset of 128 that is taken off again, in fp32
+  sums of at most one step for 16 keys, each off by 2^-23 of a sum of up to 143 times the weights. Scores are fp32 sums of
+  a few exact products, off by 2^-20 of their terms, and so is the exponential: 2^-18 (1 + the largest score term) of every weight.
+"""
+import numpy as np
+import pytest
+import torch
+
+from qwen3_decoder_transformer_gb300 import build as B
+
+HEADS = [(8, 4, 64), (16, 8, 128), (4, 4, 128), (12, 4, 64), (12, 4, 128), (32, 8, 128), (16, 2, 64), (8, 1, 128)]
+PAGES = [16, 32, 64, 128, 256]
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def bd():
+    B.build()
+    from qwen3_decoder_transformer_gb300 import binding
+    binding.lib()
+    return binding
+
+
+# ------------------------------------------------------------------------------------------------ the cache in numpy
+
+def _unpack(pages, page, dh):
+    """pages [P, Hkv, bytes] uint8 (host) -> codes [P, Hkv, page, dh], scale and minimum [P, Hkv, page, dh / 64] (float64)."""
+    raw = pages.numpy()
+    P, H, _ = raw.shape
+    c = raw[:, :, :page * dh // 2].reshape(P, H, page, dh // 2)
+    codes = np.stack([c & 15, c >> 4], axis=-1).reshape(P, H, page, dh)
+    side = np.ascontiguousarray(raw[:, :, page * dh // 2:]).view(np.uint16).reshape(P, H, page, dh // 64, 2)
+    side = (side.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    return codes, side[..., 0], side[..., 1]
+
+
+def _values(pages, page, dh):
+    codes, scale, low = _unpack(pages, page, dh)
+    with np.errstate(invalid="ignore", over="ignore"):
+        return np.repeat(low, 64, axis=-1) + np.repeat(scale, 64, axis=-1) * codes
+
+
+def _rows(values, table, page, slots, b):
+    """values [P, Hkv, page, dh] -> the slots of sequence b, [n, Hkv, dh]."""
+    return values[table[b, slots // page], :, slots % page]
+
+
+class Cache:
+    """A page pool on the GPU with every byte 255 (codes 15, scales and minima NaN), and shuffled page tables."""
+
+    def __init__(self, Hkv, dh, page, lens, seed, spare=2):
+        rng = np.random.default_rng(seed)
+        counts = [-(-n // page) for n in lens]
+        self.page, self.dh, self.Hkv = page, dh, Hkv
+        n_pages = sum(counts) + spare
+        order = rng.permutation(n_pages)
+        # entries that no call needs are far out of range
+        self.table = np.full((len(lens), max(1, max(counts, default=1)) + 1), 2 ** 30, dtype=np.int32)
+        at = 0
+        for b, n in enumerate(counts):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        size = page * (dh // 2 + dh // 16)
+        self.k = torch.full((n_pages, Hkv, size), 255, dtype=torch.uint8, device="cuda")
+        self.v = torch.full((n_pages, Hkv, size), 255, dtype=torch.uint8, device="cuda")
+        self.dtable = torch.from_numpy(self.table).cuda()
+
+    def fill(self, lens, seed, spread=1.0):
+        """Random codes with scales and minima of either sign's size in the slots below lens."""
+        gen = torch.Generator().manual_seed(seed)
+        page, dh = self.page, self.dh
+        for pages in (self.k, self.v):
+            host = pages.cpu()
+            P, H, _ = host.shape
+            codes = torch.randint(0, 256, (P, H, page, dh // 2), generator=gen, dtype=torch.uint8)
+            scale = (torch.rand(P, H, page, dh // 64, generator=gen) + 0.1) * 0.3 * spread
+            low = -7.5 * scale * (1 + 0.3 * torch.randn(P, H, page, dh // 64, generator=gen))
+            side = torch.stack([scale, low], dim=-1).to(torch.bfloat16).view(torch.uint8).reshape(P, H, page, -1)
+            hv = host[:, :, :page * dh // 2].view(P, H, page, dh // 2)
+            sv = host[:, :, page * dh // 2:].view(P, H, page, dh // 16)
+            for b, n in enumerate(lens):
+                s = np.arange(max(n, 0))
+                at, off = torch.from_numpy(self.table[b, s // page]).long(), torch.from_numpy(s % page)
+                hv[at, :, off] = codes[at, :, off]
+                sv[at, :, off] = side[at, :, off]
+            pages.copy_(host)
+        return self
+
+
+def _cu(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def _table(dh, n):
+    """[n, dh] bf16 cos and sin on the host."""
+    w = 1e6 ** (-np.arange(0, dh, 2) / dh)
+    a = np.arange(n)[:, None] * w
+    return torch.from_numpy(np.concatenate([np.cos(a), np.sin(a)], axis=1)).to(torch.bfloat16)
+
+
+def _rotated(x, gamma, cs):
+    """x [n, H, dh] float64, cs [n, dh]: norm, rotation; and the size of the terms."""
+    if gamma is not None:
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + EPS) * gamma
+    h = x.shape[-1] // 2
+    a, b, c, s = x[..., :h], x[..., h:], cs[:, None, :h], cs[:, None, h:]
+    size = np.abs(a) + np.abs(b)
+    return np.concatenate([a * c - b * s, b * c + a * s], -1), np.concatenate([size, size], -1)
+
+
+def _append(bd, heads, page, lens, start, pad=0, norm=True, seed=0, scale=1.0, ld_extra=0, qkv=None, n_pos=None, cache=None,
+            stream=None):
+    Hq, Hkv, dh = heads
+    n = sum(lens)
+    ends = [a + k for a, k in zip(start, lens)]
+    c = cache or Cache(Hkv, dh, page, ends, seed)
+    gen = torch.Generator().manual_seed(seed)
+    width = (Hq + 2 * Hkv) * dh
+    if qkv is None:
+        qkv = (torch.randn(n + pad, width + ld_extra, generator=gen) * scale).to(torch.bfloat16)
+    g = [(1 + 0.1 * torch.randn(dh, generator=gen)).to(torch.bfloat16) if norm else None for _ in range(2)]
+    cs = _table(dh, n_pos or max(1, max(ends, default=1)))
+    dq = qkv.cuda()[:, :width]
+    q_out = torch.full((n + pad, Hq, dh), 7.0, dtype=torch.bfloat16, device="cuda")
+    k_out = torch.full((n + pad, Hkv, dh), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu, st = _cu(lens), torch.tensor(start, dtype=torch.int32, device="cuda")
+    args = dict(q_gamma=None if g[0] is None else g[0].cuda(), k_gamma=None if g[1] is None else g[1].cuda(), eps=EPS, err=err)
+    bd.op_append_paged4(dq, cu, st, cs.cuda(), c.k, c.v, c.dtable, q_out, k_out=k_out, stream=stream, **args)
+    torch.cuda.synchronize()
+    return dict(cache=c, qkv=qkv[:, :width], g=g, cs=cs, q=q_out.cpu(), k=k_out.cpu(), err=int(err.item()), cu=cu, start=st)
+
+
+def _positions(lens, start):
+    return np.concatenate([np.arange(a, a + n) for a, n in zip(start, lens)]).astype(int) if lens else np.zeros(0, int)
+
+
+def _check_append(r, heads, lens, start):
+    Hq, Hkv, dh = heads
+    n = sum(lens)
+    pos = _positions(lens, start)
+    x = r["qkv"][:n].double().numpy().reshape(n, Hq + 2 * Hkv, dh)
+    cs = r["cs"].double().numpy()[pos]
+    g = [None if t is None else t.double().numpy() for t in r["g"]]
+    c = r["cache"]
+    for got, part, gamma in ((r["q"], x[:, :Hq], g[0]), (r["k"], x[:, Hq:Hq + Hkv], g[1])):
+        ref, size = _rotated(part, gamma, cs)
+        y = got[:n].double().numpy()
+        assert np.all(np.abs(y - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * size)
+        assert torch.all(got[n:] == 7.0)  # behind the last sequence
+    seq = np.repeat(np.arange(len(lens)), lens)
+    for pages, is_k in ((c.k, True), (c.v, False)):
+        codes, scale, low = _unpack(pages.cpu(), c.page, dh)
+        at, off = c.table[seq, pos // c.page], pos % c.page
+        codes, scale, low = codes[at, :, off], scale[at, :, off], low[at, :, off]
+        if is_k:
+            ref, size = _rotated(x[:, Hq:Hq + Hkv], g[1], cs)
+        else:
+            ref = x[:, Hq + Hkv:]
+            size = np.zeros_like(ref)
+        gr = ref.reshape(n, Hkv, dh // 64, 64)
+        slack = 2.0 ** -16 * size.reshape(gr.shape).max(-1)
+        mn, mx = gr.min(-1), gr.max(-1)
+        # rounded down (up) to bf16: below (above) by less than a step, 2^-7 of the value
+        assert np.all(low <= mn + slack) and np.all(low >= mn - 2.0 ** -7 * np.abs(mn) - slack)
+        want = (mx - low) / 15
+        assert np.all(scale >= want * (1 - 2.0 ** -20) - slack) and np.all(scale <= want * (1 + 2.0 ** -7) + slack)
+        val = low[..., None] + scale[..., None] * codes.reshape(gr.shape)
+        assert np.all(np.abs(val - gr) <= scale[..., None] * (0.5 + 2.0 ** -18) + slack[..., None])
+        if not is_k:  # bf16 inputs: exactly the definition
+            q = np.where(scale[..., None] > 0, (gr - low[..., None]) / np.where(scale > 0, scale, 1)[..., None], 0)
+            assert np.array_equal(codes.reshape(gr.shape), np.clip(np.rint(q), 0, 15))
+    # every other byte of the pages is as it was
+    for pages in (c.k, c.v):
+        host = pages.cpu().numpy().copy()
+        P, H, _ = host.shape
+        cv = host[:, :, :c.page * dh // 2].reshape(P, H, c.page, dh // 2)
+        sv = host[:, :, c.page * dh // 2:].reshape(P, H, c.page, dh // 16)
+        at, off = c.table[seq, pos // c.page], pos % c.page
+        cv[at, :, off] = 255
+        sv[at, :, off] = 255
+        assert np.all(cv == 255) and np.all(sv == 255)
+
+
+# ---------------------------------------------------------------------------------------------------- append and read
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", PAGES)
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+def test_append(bd, heads, page):
+    lens, start = [1, 0, 40, 3, 0, 17, 300], [0, 5, 33, 15, 0, 255, 1]
+    r = _append(bd, heads, page, lens, start, pad=3, norm=page != 32, seed=page + heads[0], scale=1.0 if page < 64 else 5.0)
+    assert r["err"] == 0
+    _check_append(r, heads, lens, start)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seqs", [1, 2, 31, 32, 33, 64, 1023, 1025, 1100])
+def test_append_decode_batches(bd, seqs):
+    """One row a sequence, over the sizes at which the search for a row's sequence takes another step."""
+    heads, start = (4, 2, 64), [(i * 37) % 50 for i in range(seqs)]
+    r = _append(bd, heads, 16, [1] * seqs, start, pad=2, seed=seqs)
+    assert r["err"] == 0
+    _check_append(r, heads, [1] * seqs, start)
+
+
+@pytest.mark.gpu
+def test_append_rows_further_apart_and_no_keys_out(bd):
+    heads, lens, start = (8, 4, 64), [9, 2], [3, 30]
+    r = _append(bd, heads, 16, lens, start, ld_extra=24, seed=3)
+    _check_append(r, heads, lens, start)
+    c = Cache(4, 64, 16, [12, 32], 3)
+    q = torch.zeros(11, 8, 64, dtype=torch.bfloat16, device="cuda")
+    bd.op_append_paged4(r["qkv"].contiguous().cuda(), r["cu"], r["start"], r["cs"].cuda(), c.k, c.v, c.dtable, q,
+                        q_gamma=r["g"][0].cuda(), k_gamma=r["g"][1].cuda(), eps=EPS)
+    assert torch.equal(q.cpu(), r["q"]) and torch.equal(c.k.cpu(), r["cache"].k.cpu())
+
+
+@pytest.mark.gpu
+def test_append_values_at_the_edges(bd):
+    """Groups of one value, of both signs, of zeros, of very large and of subnormal values; NaN and infinities."""
+    heads, dh = (2, 2, 64), 64
+    width = 6 * dh
+    x = torch.randn(9, width, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    v = x.view(9, 6, dh)
+    v[0, 4] = 3.0
+    v[1, 4] = 0.0
+    v[2, 4] = -2.5
+    v[3, 4, :32] = 1e-40
+    v[3, 4, 32:] = -3e-39
+    v[4, 4] *= 1e37
+    v[5, 4, 7] = float("nan")
+    v[6, 4, 8] = float("inf")
+    v[7, 4, 9] = float("-inf")
+    v[8, 4, 0], v[8, 4, 1] = 3e38, -3e38  # their difference is past fp32
+    r = _append(bd, heads, 16, [9], [0], norm=False, qkv=x)
+    codes, scale, low = _unpack(r["cache"].v.cpu(), 16, dh)
+    at = r["cache"].table[0, 0]
+    codes, scale, low = codes[at, 0, :9], scale[at, 0, :9, 0], low[at, 0, :9, 0]
+    assert np.all(np.isnan(scale[5:])) and np.all(np.isnan(low[5:]))
+    ref = v[:5, 4].double().numpy()
+    val = low[:5, None] + scale[:5, None] * codes[:5]
+    assert np.all(np.abs(val - ref) <= scale[:5, None] * (0.5 + 2.0 ** -18))
+    assert np.array_equal(val[:3], ref[:3])
+    # the other head of the same rows is untouched by it
+    c2, s2, l2 = _unpack(r["cache"].v.cpu(), 16, dh)
+    assert np.all(np.isfinite(s2[at, 1, :9])) and np.all(np.isfinite(l2[at, 1, :9]))
+
+
+@pytest.mark.gpu
+def test_append_flags_what_it_cannot_place(bd):
+    heads, lens = (8, 4, 64), [4, 4, 4, 4]
+    ref = _append(bd, heads, 16, lens, [14, 3, 5, 9], seed=5, n_pos=64)
+    assert ref["err"] == 0
+
+    def again(start, table=None, n_pos=64, cu=None):
+        c = Cache(4, 64, 16, [18, 7, 9, 13], 5)
+        if table is not None:
+            c.dtable = torch.from_numpy(table(c.table.copy())).cuda()
+        q = torch.full((16, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        k = torch.full((16, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        bd.op_append_paged4(ref["qkv"].contiguous().cuda(), ref["cu"] if cu is None else cu,
+                            torch.tensor(start, dtype=torch.int32, device="cuda"), ref["cs"].cuda()[:n_pos].contiguous(), c.k,
+                            c.v, c.dtable, q, k_out=k, q_gamma=ref["g"][0].cuda(), k_gamma=ref["g"][1].cuda(), eps=EPS, err=err)
+        return q.cpu(), c, int(err.item())
+
+    def bad(t):
+        t[0, 1] = -1          # slots 16, 17 of sequence 0
+        t[2, 0] = 1 << 20
+        return t
+
+    q, c, err = again([14, 3, 5, 9], bad)
+    assert err == 4 and torch.equal(q, ref["q"])  # the rows without a page still get their outputs
+    got, want = _values(c.k.cpu(), 16, 64), _values(ref["cache"].k.cpu(), 16, 64)
+    for b, s in ((0, [14, 15]), (1, [3, 4, 5, 6]), (3, [9, 10, 11, 12])):
+        assert np.array_equal(_rows(got, c.table, 16, np.array(s), b), _rows(want, c.table, 16, np.array(s), b))
+    assert np.all(np.isnan(_rows(got, c.table, 16, np.array([5, 6, 7, 8]), 2)))
+    # slots that are negative, past the rotation table, past the page table's reach
+    q, c, err = again([-2, 60, 5, 2 ** 31 - 2])
+    assert err == 4
+    assert torch.all(q[:2] == 7.0) and not torch.any(q[2:4] == 7.0)
+    assert torch.all(q[12:] == 7.0) and torch.equal(q[8:12], ref["q"][8:12])
+    q, c, err = again([14, 3, 5, 9], n_pos=8)
+    assert err == 4 and torch.all(q[0:4] == 7.0) and torch.equal(q[4:8], ref["q"][4:8]) and torch.all(q[11] == 7.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", PAGES)
+@pytest.mark.parametrize("heads", HEADS[:5], ids=str)
+def test_read(bd, heads, page):
+    _, Hkv, dh = heads
+    lens, start = [1, 0, 60, 5, 200], [0, 3, 20, 250, 31]
+    ends = [a + n for a, n in zip(start, lens)]
+    c = Cache(Hkv, dh, page, ends, page).fill(ends, page)
+    n = sum(lens)
+    k = torch.full((n + 2, Hkv, dh), 7.0, dtype=torch.bfloat16, device="cuda")
+    v, err = k.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    bd.op_read_paged4(c.k, c.v, c.dtable, _cu(lens), torch.tensor(start, dtype=torch.int32, device="cuda"), k, v, err=err)
+    assert int(err.item()) == 0
+    seq, pos = np.repeat(np.arange(len(lens)), lens), _positions(lens, start)
+    for got, pages in ((k, c.k), (v, c.v)):
+        val = _values(pages.cpu(), page, dh)[c.table[seq, pos // page], :, pos % page]
+        # the sum is rounded to fp32 (2^-24 of it), then to bf16
+        assert np.all(np.abs(got[:n].cpu().double().numpy() - val) <= 2.0 ** -8 * np.abs(val) * (1 + 2.0 ** -14))
+        assert torch.all(got[n:] == 7.0)
+
+
+@pytest.mark.gpu
+def test_read_leaves_what_it_cannot_find(bd):
+    c = Cache(2, 64, 16, [40, 40], 1).fill([40, 40], 1)
+    c.dtable[0, 1] = -5
+    k = torch.full((80, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    v, err = k.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    bd.op_read_paged4(c.k, c.v, c.dtable, _cu([40, 40]), torch.zeros(2, dtype=torch.int32, device="cuda"), k, v, err=err)
+    assert int(err.item()) == 4
+    assert torch.all(k[16:32] == 7.0) and torch.all(v[16:32] == 7.0)
+    assert not torch.any(k[:16].float() == 7.0) and torch.isfinite(k[32:].float()).all()
+
+
+# ---------------------------------------------------------------------------------------------------- decode attention
+
+def _decode(bd, q, c, len0, work=None, stream=None, out=None):
+    Bq, Hq, dh = q.shape
+    if out is None:
+        out = torch.full((Bq, Hq * dh), 7.0, dtype=torch.bfloat16, device="cuda")
+    if work is None:
+        work = torch.full((bd.attention_decode_paged4_workspace(Bq, Hq, c.Hkv, dh),), 255, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bd.op_attention_decode_paged4(q, c.k, c.v, c.dtable, len0, work, out, err=err, stream=stream)
+    torch.cuda.synchronize()
+    return out, int(err.item())
+
+
+def _ref_decode(q, c, lens, cap=None):
+    """Result and bound [B, Hq, dh] for q (host bf16)."""
+    Bq, Hq, dh = q.shape
+    codes_k, scale_k, low_k = _unpack(c.k.cpu(), c.page, dh)
+    codes_v, scale_v, low_v = _unpack(c.v.cpu(), c.page, dh)
+    ref, tol = np.zeros((Bq, Hq, dh)), np.zeros((Bq, Hq, dh))
+    g = Hq // c.Hkv
+    for b, n in enumerate(lens):
+        if n <= 0:
+            continue
+        s = np.arange(n)
+        pick = lambda a: a[c.table[b, s // c.page], :, s % c.page]  # noqa: E731
+        sk, lk = np.repeat(pick(scale_k), 64, -1), np.repeat(pick(low_k), 64, -1)
+        k = lk + sk * pick(codes_k)
+        sv, lv, cv = np.repeat(pick(scale_v), 64, -1), np.repeat(pick(low_v), 64, -1), pick(codes_v)
+        v = lv + sv * cv
+        for h in range(Hq):
+            j = h // g
+            qq = q[b, h].double().numpy()
+            x = k[:, j] @ qq / dh ** 0.5
+            size = ((np.abs(lk[:, j]) + sk[:, j] * pick(codes_k)[:, j]) @ np.abs(qq)).max() / dh ** 0.5
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            ref[b, h] = p @ v[:, j]
+            steps = 2 * -(-n // 32) + 16
+            tol[b, h] = (2.0 ** -8 * np.abs(ref[b, h]) + 2.0 ** -8 * (p @ (sv[:, j] * cv[:, j])) +
+                         steps * 2.0 ** -23 * 143 * (p @ sv[:, j]) +
+                         2.0 ** -18 * (1 + size) * (p @ (np.abs(lv[:, j]) + sv[:, j] * cv[:, j])))
+    return ref, tol
+
+
+def _check_decode(got, q, c, lens):
+    ref, tol = _ref_decode(q, c, lens)
+    y = got.cpu().double().numpy().reshape(ref.shape)
+    assert np.all(np.abs(y - ref) <= tol), float((np.abs(y - ref) / np.where(tol > 0, tol, 1)).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", PAGES)
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+def test_decode(bd, heads, page):
+    Hq, Hkv, dh = heads
+    lens = [1, 15, 16, 17, 0, 31, 32, 33, 100, 257, 700]
+    c = Cache(Hkv, dh, page, lens, page + dh).fill(lens, page)
+    q = torch.randn(len(lens), Hq, dh, generator=torch.Generator().manual_seed(page)).to(torch.bfloat16)
+    len0 = torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda")
+    out, err = _decode(bd, q.cuda(), c, len0)
+    assert err == 0
+    _check_decode(out, q, c, lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B_", [1, 2, 7, 255, 256, 257, 600])
+@pytest.mark.parametrize("heads", [(8, 4, 64), (16, 8, 128)], ids=str)
+def test_decode_batches(bd, heads, B_):
+    """Batches past the strips in which lengths are counted, with empty sequences among them."""
+    Hq, Hkv, dh = heads
+    lens = [(i * 131) % 97 for i in range(B_)]
+    lens[0] = 61
+    c = Cache(Hkv, dh, 16, lens, B_).fill(lens, B_)
+    q = torch.randn(B_, Hq, dh, generator=torch.Generator().manual_seed(B_)).to(torch.bfloat16)
+    len0 = torch.tensor([n - 1 if n else -1 - i for i, n in enumerate(lens)], dtype=torch.int32, device="cuda")
+    out, err = _decode(bd, q.cuda(), c, len0)
+    assert err == 0
+    _check_decode(out, q, c, lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,lens,page", [((8, 1, 128), [20011], 64), ((4, 4, 64), [30000, 1], 256),
+                                             ((32, 8, 128), [5000, 3000, 40], 16), ((16, 2, 64), [9999], 32)], ids=str)
+def test_decode_long(bd, heads, lens, page):
+    Hq, Hkv, dh = heads
+    c = Cache(Hkv, dh, page, lens, page).fill(lens, page)
+    q = torch.randn(len(lens), Hq, dh, generator=torch.Generator().manual_seed(page)).to(torch.bfloat16)
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    _check_decode(out, q, c, lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_scale,spread", [(30.0, 1.0), (1e-6, 1.0), (1.0, 1e4), (1e10, 1e-10), (1.0, 1e-3)])
+def test_decode_sizes_of_values(bd, q_scale, spread):
+    """Scores far apart, all alike, and values of other sizes."""
+    heads, lens = (12, 4, 128), [300, 64]
+    c = Cache(4, 128, 32, lens, 9).fill(lens, 9, spread)
+    q = (torch.randn(2, 12, 128, generator=torch.Generator().manual_seed(9)) * q_scale).to(torch.bfloat16)
+    q[0, 3] = 0
+    q[0, 4, 1:] = 0
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([299, 63], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    _check_decode(out, q, c, lens)
+
+
+@pytest.mark.gpu
+def test_decode_rising_scores(bd):
+    """Keys that grow along the sequence: the running maximum moves in every unit."""
+    lens = [4096]
+    c = Cache(2, 64, 64, lens, 4).fill(lens, 4)
+    host = c.k.cpu()
+    P, H, _ = host.shape
+    side = host[:, :, 64 * 32:].view(torch.bfloat16).view(P, H, 64, 2)
+    s = np.arange(4096)
+    at, off = torch.from_numpy(c.table[0, s // 64]).long(), torch.from_numpy(s % 64)
+    low = (torch.from_numpy(s).float() * 0.01).to(torch.bfloat16)
+    side[at, :, off, 1] = low[:, None].expand(-1, H)
+    c.k.copy_(host)
+    q = torch.full((1, 8, 64), 0.5).to(torch.bfloat16)
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([4095], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    _check_decode(out, q, c, lens)
+
+
+@pytest.mark.gpu
+def test_decode_length_past_the_table(bd):
+    """A length that the page table does not reach counts as its last slot; negative ones give zeros."""
+    c = Cache(4, 64, 16, [48, 48, 48], 2).fill([48] * 3, 2)
+    c.dtable = c.dtable[:, :3].contiguous()
+    q = torch.randn(3, 8, 64, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([2 ** 31 - 1, -2 ** 31, 48], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    _check_decode(out, q, c, [48, 0, 48])
+
+
+@pytest.mark.gpu
+def test_decode_bad_page_and_nan_stay_in_their_sequence(bd):
+    heads, lens = (8, 4, 64), [100, 70, 50]
+    c = Cache(4, 64, 16, lens, 6).fill(lens, 6)
+    q = torch.randn(3, 8, 64, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16)
+    len0 = torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda")
+    good, err = _decode(bd, q.cuda(), c, len0)
+    assert err == 0
+    keep = int(c.dtable[1, 2])
+    for bad in (-1, c.k.shape[0], 2 ** 31 - 1):
+        c.dtable[1, 2] = bad
+        out, err = _decode(bd, q.cuda(), c, len0)
+        assert err == 4
+        assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
+    c.dtable[1, 2] = keep
+    # a key (scale, minimum) of NaN in kv head 2 of sequence 0, slot 40
+    side = c.k[:, :, 16 * 32:].view(torch.bfloat16)
+    side[int(c.table[0, 2]), 2, 8 * 2:8 * 2 + 2] = float("nan")
+    out, err = _decode(bd, q.cuda(), c, len0)
+    assert err == 0
+    o = out.view(3, 8, 64)
+    assert torch.isnan(o[0, 4:6]).all()
+    g = good.view(3, 8, 64)
+    assert torch.equal(o[0, :4], g[0, :4]) and torch.equal(o[0, 6:], g[0, 6:]) and torch.equal(o[1:], g[1:])
+
+
+@pytest.mark.gpu
+def test_decode_repeats_streams_and_graph(bd):
+    """Bit-equal results from repeated calls with any workspace contents, on two streams at once, from a replayed graph; and the
+    graph follows lengths that change."""
+    lens = [3000, 1, 513, 90] * 3
+    c = Cache(8, 128, 16, lens, 8).fill(lens, 8)
+    q = torch.randn(12, 16, 128, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    len0 = torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda")
+    base, _ = _decode(bd, q, c, len0)
+    size = bd.attention_decode_paged4_workspace(12, 16, 8, 128)
+    for fill in (0, 255, 127):
+        out, _ = _decode(bd, q, c, len0, work=torch.full((size,), fill, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(out, base)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    works = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in streams]
+    outs = [torch.zeros_like(base) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, w, o in zip(streams, works, outs):
+            bd.op_attention_decode_paged4(q, c.k, c.v, c.dtable, len0, w, o, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, base) for o in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        bd.op_attention_decode_paged4(q, c.k, c.v, c.dtable, len0, works[0], outs[0])
+    outs[0].zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], base)
+    len0 -= 1
+    graph.replay()
+    torch.cuda.synchronize()
+    want, _ = _decode(bd, q, c, len0)
+    assert torch.equal(outs[0], want)
+
+
+# ------------------------------------------------------------------------------------------------------------ refusals
+
+def test_page_bytes(bd):
+    for page in PAGES:
+        assert bd.paged4_page_bytes(page, 128) == page * 72 and bd.paged4_page_bytes(page, 64) == page * 36
+    for page, dh in ((0, 128), (8, 128), (24, 128), (512, 128), (64, 96), (-16, 64), (2 ** 40, 128)):
+        assert bd.paged4_page_bytes(page, dh) == 0
+
+
+def test_library_refuses(bd):
+    """Argument checks on the host: nothing is launched (the addresses are never dereferenced)."""
+    L, p = bd.lib(), 4096
+
+    def append(**c):
+        a = dict(qkv=p, ld=1024, N=3, cu=p, start=p, S=1, Hq=8, Hkv=4, dh=64, qg=p, kg=p, cs=p, n_pos=10, q=p, k=p, kp=p, vp=p,
+                 n_pages=4, page=16, table=p, max_pages=2)
+        a.update(c)
+        return L.qwen3_op_append_paged4(a["qkv"], a["ld"], a["N"], a["cu"], a["start"], a["S"], a["Hq"], a["Hkv"], a["dh"], a["qg"],
+                                        a["kg"], 1e-6, a["cs"], a["n_pos"], a["q"], a["k"], a["kp"], a["vp"], a["n_pages"],
+                                        a["page"], a["table"], a["max_pages"], None, None)
+
+    for c in (dict(qkv=None), dict(ld=1023), dict(ld=1016), dict(ld=1028), dict(N=-1), dict(N=2 ** 30 + 1), dict(cu=None),
+              dict(start=None), dict(S=-1), dict(Hq=0), dict(Hq=7), dict(Hkv=0), dict(dh=96), dict(cs=None), dict(n_pos=0),
+              dict(q=None), dict(kp=None), dict(vp=None), dict(n_pages=0), dict(page=8), dict(page=48), dict(page=512),
+              dict(table=None), dict(max_pages=0), dict(qkv=p + 2), dict(q=p + 8), dict(k=p + 8), dict(kp=p + 8), dict(vp=p + 1),
+              dict(cs=p + 2), dict(qg=p + 2), dict(kg=p + 2), dict(Hq=65536 * 4)):
+        assert append(**c) == 5, c
+    assert append(N=0) == 0 and append(S=0) == 0
+
+    def read(**c):
+        a = dict(kp=p, vp=p, n_pages=4, page=16, table=p, max_pages=2, cu=p, start=p, S=1, N=3, Hkv=4, dh=64, k=p, v=p)
+        a.update(c)
+        return L.qwen3_op_read_paged4(*[a[n] for n in ("kp", "vp", "n_pages", "page", "table", "max_pages", "cu", "start", "S", "N",
+                                                       "Hkv", "dh", "k", "v")], None, None)
+
+    for c in (dict(kp=None), dict(vp=None), dict(kp=p + 8), dict(n_pages=0), dict(page=20), dict(table=None), dict(max_pages=0),
+              dict(cu=None), dict(start=None), dict(S=-1), dict(N=-1), dict(Hkv=0), dict(dh=32), dict(k=None), dict(v=None),
+              dict(k=p + 2), dict(v=p + 8)):
+        assert read(**c) == 5, c
+    assert read(N=0) == 0 and read(S=0) == 0
+
+    size = 1 << 30
+
+    def decode(**c):
+        a = dict(q=p, kp=p, vp=p, n_pages=4, page=16, table=p, max_pages=2, len0=p, B=2, Hq=8, Hkv=4, dh=64, work=p, bytes=size,
+                 out=p)
+        a.update(c)
+        return L.qwen3_op_attention_decode_paged4(*[a[n] for n in ("q", "kp", "vp", "n_pages", "page", "table", "max_pages", "len0",
+                                                                   "B", "Hq", "Hkv", "dh", "work", "bytes", "out")], None, None)
+
+    for c in (dict(q=None), dict(kp=None), dict(vp=None), dict(n_pages=0), dict(page=17), dict(table=None), dict(max_pages=0),
+              dict(len0=None), dict(B=-1), dict(B=65536), dict(Hq=9), dict(Hq=36), dict(Hkv=0), dict(dh=80), dict(work=None),
+              dict(out=None), dict(q=p + 8), dict(out=p + 2), dict(work=p + 4), dict(bytes=0), dict(bytes=1000),
+              dict(B=65535, max_pages=2 ** 26)):
+        assert decode(**c) == 5, c
+    assert decode(B=0) == 0
+    assert bd.attention_decode_paged4_workspace(0, 8, 4, 64) == 0
+    assert bd.attention_decode_paged4_workspace(1, 36, 4, 64) == 0
+
+
+def test_binding_refuses(bd):
+    bf, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    kp, vp = torch.zeros(5, 4, 16 * 36, dtype=u8), torch.zeros(5, 4, 16 * 36, dtype=u8)
+    table, cu, start = torch.zeros(2, 3, dtype=i32), torch.zeros(3, dtype=i32), torch.zeros(2, dtype=i32)
+    base = dict(qkv=torch.zeros(6, 1024, dtype=bf), cu=cu, start=start, cos_sin=torch.zeros(9, 64, dtype=bf), k_pages=kp,
+                v_pages=vp, page_table=table, q_out=torch.zeros(6, 8, 64, dtype=bf), k_out=torch.zeros(6, 4, 64, dtype=bf),
+                q_gamma=torch.zeros(64, dtype=bf), k_gamma=torch.zeros(64, dtype=bf))
+    pages = (dict(k_pages=kp[0]), dict(k_pages=kp.float()), dict(v_pages=vp[:4]), dict(k_pages=kp[:, :, :-1], v_pages=vp[:, :, :-1]),
+             dict(page_table=table[0]), dict(page_table=table.long()), dict(page_table=table[:, :0]), dict(v_pages=None))
+    for change in pages + (dict(qkv=base["qkv"].float()), dict(qkv=base["qkv"][:5]), dict(qkv=base["qkv"][:, :1000]),
+                           dict(qkv=torch.zeros(1024, 6, dtype=bf).t()), dict(cu=cu[:2]), dict(cu=cu.long()),
+                           dict(start=torch.zeros(3, dtype=i32)), dict(cos_sin=torch.zeros(9, 32, dtype=bf)),
+                           dict(q_out=base["q_out"].float()), dict(q_out=base["q_out"][:, :7]), dict(k_out=base["k_out"][:5]),
+                           dict(q_gamma=torch.zeros(32, dtype=bf)), dict(k_gamma=torch.zeros(64)), dict(err=torch.zeros(1)), {}):
+        with pytest.raises(ValueError):
+            bd.op_append_paged4(**{**base, **change})
+    base = dict(k_pages=kp, v_pages=vp, page_table=table, cu=cu, start=start, k_out=torch.zeros(6, 4, 64, dtype=bf),
+                v_out=torch.zeros(6, 4, 64, dtype=bf))
+    for change in pages + (dict(k_out=base["k_out"][:, :3]), dict(v_out=base["v_out"][:5]), dict(k_out=base["k_out"].float()),
+                           dict(cu=cu[:1]), {}):
+        with pytest.raises(ValueError):
+            bd.op_read_paged4(**{**base, **change})
+    base = dict(q=torch.zeros(2, 8, 64, dtype=bf), k_pages=kp, v_pages=vp, page_table=table, len0=start,
+                work=torch.zeros(10, dtype=u8), out=torch.zeros(2, 512, dtype=bf))
+    for change in pages + (dict(q=base["q"][0]), dict(q=base["q"].float()), dict(q=torch.zeros(2, 36, 64, dtype=bf)),
+                           dict(q=torch.zeros(3, 8, 64, dtype=bf)), dict(len0=cu), dict(len0=start.long()), dict(work=None),
+                           dict(out=base["out"][:1]), dict(out=base["out"].float()), {}):
+        with pytest.raises(ValueError):
+            bd.op_attention_decode_paged4(**{**base, **change})
