@@ -18,9 +18,11 @@ namespace {
 //   Codes of K become fp16 by a mask alone: a nibble in the lowest bits of an fp16 word is the subnormal code * 2^-24 (the
 //   next nibble code * 2^-20, its query value divided by 16), exact on the tensor cores. q is scaled by a power of two
 //   for each head so that its fp16 form is exact (its largest value lies in [2^10, 2^11)).
-//   Codes of V become bf16 by a mask and an or: 0x4300 | code = 128 + code. P * scale is rounded to bf16, the type that the
-//   tensor cores take beside it (off by 2^-9 of itself); its sum over the keys comes out of the same products
-//   (a row of ones), and 128 times it is taken off at the end, so the offset leaves no rounding of its own.
+//   Codes of V become fp16 in the same way (odd nibbles end up 16 times too large in output rows of their own). Their
+//   weights p * scale are rounded to fp16, off by 2^-11 of themselves at most: a power of two for each head keeps the largest
+//   weight of the run so far in [2^13, 2^15], so what falls below fp16's normal range is less than 2^-25 of that.
+//   (bf16 weights, with codes as 128 + code and the offset taken off again, left 0.5-1.2% of error on long sequences against
+//   0.2%: a rounding of 2^-8 multiplies codes of one sign, and the tensor cores cut their sums off.)
 //
 // Work: the units of 32 keys of all (sequence, kv head) pairs in one list, cut into as many equal runs as there are warps.
 // A warp works through its run alone: its lanes 0 and 1 keep a ring of units full with untiled bulk copies, and warp-level
@@ -43,12 +45,10 @@ struct P4Layout {
     static_assert(P4_CTAS * (SMEM + 4096) <= 227 * 1024, "shared memory");
 };
 
-// What a warp leaves of a piece that ends before its sequence does: the record of its run's first piece is slot 0, that of the
-// piece at the end of its run slot 1. first[w]: slots that hold one (bit 0, bit 1). For the warp whose run holds the
-// beginning, but not the end, of a (sequence, kv head): seg[w] is its number, last[w] the warp that holds the end, and
-// last_slot[w] its slot; otherwise seg[w] is -1.
+// A (sequence, kv head) that begins, but does not end, in a CTA's runs: its number (-1: none), the warp whose run holds its
+// beginning, the one whose run holds its end, and whether the end's record is that run's first piece (0) or the last (1).
 struct P4Desc {
-    int has, seg, last, last_slot;
+    int seg, first, last, last_slot;
 };
 
 struct P4Args {
@@ -57,8 +57,8 @@ struct P4Args {
     Paged4 cache;
     const int* len0;
     int B, Hq, Hkv, G, cap;  // cap: slots that the page table reaches
-    P4Desc* desc;            // [warps]
-    float* recs;             // [warps][2][G][PITCH]
+    P4Desc* desc;            // [CTAs]
+    float* recs;             // [warps][2][G][PITCH]: of the piece at the beginning, and of the piece at the end of a run
     int* err;
 };
 
@@ -70,13 +70,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -96,8 +89,10 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
-// ((w >> 4 i) & 0x000f000f) | 0x43004300: codes i of both halves as bf16 values 128 + code
-__device__ __forceinline__ uint32_t code_bf16(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 // Keys that sequence b's query sees.
 __device__ __forceinline__ int p4_keys(const P4Args& a, int b) {
@@ -256,7 +251,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     uint32_t qf[NG][4][2];      // q^T fragments: column g = query head g of the group (zero past G)
     float qs[NG][2], qscale[2]; // heads 2t and 2t + 1: sums of the fp16 values of a group of dims; what they are scaled by
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[NG][4][4], r[NG][4], z[NG][2];
+    float o[NG][4][4], z[NG][2];  // sums of codes (in units of 2^-24 / nu, odd rows of tiles 2^-20 / nu), and of minima
+    float nu[2] = {1.f, 1.f};      // heads 2t and 2t + 1: the power of two on the weights of V
     auto reset = [&]() {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -268,7 +264,6 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             z[c][0] = z[c][1] = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                r[c][e] = 0.f;
                 o[c][0][e] = o[c][1][e] = o[c][2][e] = o[c][3][e] = 0.f;
             }
         }
@@ -311,15 +306,11 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
             sums[c] = s * 5.9604644775390625e-8f;  // 2^-24, the unit of the products of codes
-            auto pair = [](float lo, float hi) {
-                const __half2 v = __floats2half2_rn(lo, hi);
-                return *reinterpret_cast<const uint32_t*>(&v);
-            };
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // word k / 2, nibbles 2 (k % 2) and that + 4; then the ones after them
                 const int d = (k >> 1) * 8 + (k & 1) * 2;
-                qf[c][k][0] = pair(x[c][d], x[c][d + 4]);
-                qf[c][k][1] = pair(x[c][d + 1] * 0.0625f, x[c][d + 5] * 0.0625f);
+                qf[c][k][0] = pack_f16(x[c][d], x[c][d + 4]);
+                qf[c][k][1] = pack_f16(x[c][d + 1] * 0.0625f, x[c][d + 5] * 0.0625f);
             }
         }
         const float up = __uint_as_float((uint32_t)(127 + e) << 23) * 16777216.f * sl2;
@@ -333,11 +324,12 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     };
     // the sums of this warp's piece at scale m: dims c * 64 + 8 g + (0..7) of head 2t + e
     auto piece = [&](int c, int e, float (&v)[8]) {
-        const float add = z[c][e] - 128.f * r[c][e];
+        const float unit = 16777216.f * (1.f / nu[e]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[i] = o[c][i][e] + add;
-            v[4 + i] = o[c][i][2 + e] + add;
+            const float u = i & 1 ? unit * 0.0625f : unit;
+            v[i] = fmaf(o[c][i][e], u, z[c][e]);
+            v[4 + i] = fmaf(o[c][i][2 + e], u, z[c][e]);
         }
     };
     auto total = [&]() {  // l and z over the keys that other lanes took
@@ -384,7 +376,6 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         }
     };
     float* my_recs = a.recs + (size_t)gw * 2 * a.G * PITCH;
-    int has = 0;
     const int swap = (g & 4) | (g & 1) << 1 | (g >> 1 & 1);  // row g of a tile is key swap (and row g + 8 key swap + 8):
     const int vkey = (2 * t & 4) | (t & 1);                  // the keys of rows 2t, which one load of V takes, are 0, 1, 4, 5
     bool ok = true, ahead = false;
@@ -454,7 +445,9 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
 #pragma unroll
         for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e]));
         // O and the sums move to a larger maximum only when it grew by more than 8 (P <= 2^8)
-        if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+        const bool moved = __any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f);
+        float shrink[2] = {1.f, 1.f};
+        if (moved) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -463,17 +456,9 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 const float f = grow ? ex2_approx(m[e] - mx[e]) : 1.f;
                 m[e] = grow ? mx[e] : m[e];
                 l[e] *= f;
+                shrink[e] = f;  // (O follows below)
 #pragma unroll
-                for (int c = 0; c < NG; ++c) {
-                    z[c][e] *= f;
-                    r[c][e] *= f;
-                    r[c][2 + e] *= f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        o[c][k][e] *= f;
-                        o[c][k][2 + e] *= f;
-                    }
-                }
+                for (int c = 0; c < NG; ++c) z[c][e] *= f;
             }
         }
         const float nm[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
@@ -485,6 +470,9 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 l[e & 1] += x[k][e];
             }
         if (!__all_sync(0xffffffffu, mbar_wait_suspend(&v_full[st], ph, abort_flag))) { ok = false; break; }
+        // weights of V by group of dims: p * scale, and the sums of p * minimum
+        float wt[2][NG][4];
+        float top[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (k < tiles) {
@@ -507,24 +495,61 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                         if (k * 16 + swap + 8 >= valid) sd[1][c] = 0;
                     }
                 }
+#pragma unroll
+                for (int c = 0; c < NG; ++c)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        z[c][e] = fmaf(x[k][e], bf16_hi(sd[0][c]), fmaf(x[k][2 + e], bf16_hi(sd[1][c]), z[c][e]));
+                        wt[k][c][e] = x[k][e] * bf16_lo(sd[0][c]);
+                        wt[k][c][2 + e] = x[k][2 + e] * bf16_lo(sd[1][c]);
+                        top[e] = fmax3(top[e], fabsf(wt[k][c][e]), fabsf(wt[k][c][2 + e]));
+                    }
+            } else {
+#pragma unroll
+                for (int c = 0; c < NG; ++c) wt[k][c][0] = wt[k][c][1] = wt[k][c][2] = wt[k][c][3] = 0.f;
+            }
+        }
+        if (moved || __any_sync(0xffffffffu, top[0] * nu[0] > 32768.f || top[1] * nu[1] > 32768.f)) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], s));
+                // the largest weight of the run so far: what was below 2^14 / nu has shrunk with the scores' maximum
+                const float big = fmaxf(top[e], shrink[e] * (16384.f / nu[e]));
+                const int at = min(max(13 + 127 - (int)(__float_as_uint(big) >> 23), -100), 100);  // big 2^at in [2^13, 2^14)
+                const float next = big > 0.f ? __uint_as_float((uint32_t)(127 + at) << 23) : nu[e], f = next / nu[e] * shrink[e];
+                nu[e] = next;
+#pragma unroll
+                for (int c = 0; c < NG; ++c)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[c][k][e] *= f;
+                        o[c][k][2 + e] *= f;
+                    }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k < tiles) {
                 const uint32_t codes = va + k * tile_step + vkey * (DH / 2) + 4 * g;
 #pragma unroll
                 for (int c = 0; c < NG; ++c) {
-                    const float s0 = bf16_lo(sd[0][c]), s1 = bf16_lo(sd[1][c]);
-                    const float z0 = bf16_hi(sd[0][c]), z1 = bf16_hi(sd[1][c]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) z[c][e] = fmaf(x[k][e], z0, fmaf(x[k][2 + e], z1, z[c][e]));
-                    const uint32_t b0 = transpose8x8(pack_bf16(x[k][0] * s0, x[k][1] * s0));
-                    const uint32_t b1 = transpose8x8(pack_bf16(x[k][2] * s1, x[k][3] * s1));
-                    // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further
+                    const uint32_t b0 = transpose8x8(pack_f16(wt[k][c][0] * nu[0], wt[k][c][1] * nu[1]));
+                    const uint32_t b1 = transpose8x8(pack_f16(wt[k][c][2] * nu[0], wt[k][c][3] * nu[1]));
+                    // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further: the first and the last four nibbles
                     const uint32_t wa = lds32(codes + c * 32), wb = lds32(codes + c * 32 + 2 * (DH / 2));
                     const uint32_t wc = lds32(codes + c * 32 + 8 * (DH / 2)), wd = lds32(codes + c * 32 + 10 * (DH / 2));
-                    const uint32_t lo0 = __byte_perm(wa, wb, 0x5410), hi0 = __byte_perm(wa, wb, 0x7632);
-                    const uint32_t lo1 = __byte_perm(wc, wd, 0x5410), hi1 = __byte_perm(wc, wd, 0x7632);
+                    uint32_t v[4] = {__byte_perm(wa, wb, 0x5410), __byte_perm(wa, wb, 0x7632), __byte_perm(wc, wd, 0x5410),
+                                     __byte_perm(wc, wd, 0x7632)};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mma_bf16(o[c][q], code_bf16(lo0, q), code_bf16(hi0, q), code_bf16(lo1, q), code_bf16(hi1, q), b0, b1);
-                    mma_bf16(r[c], 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, b0, b1);
+                    for (int q = 0; q < 4; ++q) {
+                        if (q == 2) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[j] >>= 8;
+                        }
+                        const uint32_t mask = q & 1 ? 0x00f000f0u : 0x000f000fu;
+                        mma_f16(o[c][q], v[0] & mask, v[1] & mask, v[2] & mask, v[3] & mask, b0, b1);
+                    }
                 }
             }
         }
@@ -541,7 +566,6 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 write_out();
             } else {
                 leave(my_recs);
-                has |= 1;
             }
             reset();
             seg_begin = x0 + i + 1;
@@ -571,59 +595,74 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         whole_sh[warp] = (open && seg_begin >= x0 ? 1 : 0) | (open && ends ? 2 : 0);  // begins, ends in this run
     }
     __syncthreads();
+    // Join the pieces at the ends of this CTA's runs: those of neighbouring warps that belong to one (sequence, kv head), and, where
+    // it ends as the first piece of the next warp's run, that warp's record. Quads of dims of the group that begins at warp w0:
     const int G = a.G, quads = G * (DH / 4);
-    for (int w0 = 0; w0 < P4_WARPS;) {
-        const int s = seg_sh[w0];
+    const int cta0 = blockIdx.x * P4_WARPS, here = (int)max(0LL, min((long long)P4_WARPS, warps - cta0));  // warps with a run
+    for (int e0 = threadIdx.x; e0 < P4_WARPS * quads; e0 += P4_THREADS) {
+        const int w0 = e0 / quads, e = e0 - w0 * quads, s = seg_sh[w0];
+        if (s < 0 || (w0 > 0 && seg_sh[w0 - 1] == s)) continue;
         int w1 = w0 + 1;
-        while (w1 < P4_WARPS && s >= 0 && seg_sh[w1] == s) ++w1;
-        if (s >= 0) {
-            const bool whole = (whole_sh[w0] & 1) && (whole_sh[w1 - 1] & 2);
-            for (int e = threadIdx.x; e < quads; e += P4_THREADS) {
-                const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
-                const float* rec = reinterpret_cast<const float*>(p4_rings) + h * PITCH;
-                constexpr int STEP = Ly::RING / 4;
-                float M = -INFINITY, L = 0.f;
-                for (int w = w0; w < w1; ++w) M = fmaxf(M, rec[w * STEP + DH]);
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int w = w0; w < w1; ++w) {
-                    const float mw = rec[w * STEP + DH];
-                    // (a piece whose scores are all NaN keeps m = -inf, and its sums are NaN)
-                    const float f = mw == -INFINITY ? 1.f : ex2_approx(mw - M);
-                    const float4 y = *reinterpret_cast<const float4*>(rec + w * STEP + dd);
-                    L = fmaf(rec[w * STEP + DH + 1], f, L);
-                    v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
-                }
-                if (whole) {
-                    const float inv = 1.f / L;
-                    const size_t row = (size_t)(s / a.Hkv) * a.Hq + (size_t)(s % a.Hkv) * G + h;
-                    *reinterpret_cast<uint2*>(a.out + row * DH + dd) =
-                        make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-                } else {
-                    float* dst = a.recs + ((size_t)(blockIdx.x * P4_WARPS + w0) * 2 + 1) * G * PITCH + h * PITCH;
-                    *reinterpret_cast<float4*>(dst + dd) = v;
-                    if (dd == 0) *reinterpret_cast<float2*>(dst + DH) = make_float2(M, L);
-                }
-            }
-            if (warp == w0 && !whole) has |= 2;
+        while (w1 < P4_WARPS && seg_sh[w1] == s) ++w1;
+        const bool tail = !(whole_sh[w1 - 1] & 2) && w1 < here;
+        const bool whole = (whole_sh[w0] & 1) && ((whole_sh[w1 - 1] & 2) || tail);
+        const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
+        const float* rec = reinterpret_cast<const float*>(p4_rings) + h * PITCH;
+        const float* far = a.recs + (size_t)(cta0 + w1) * 2 * G * PITCH + h * PITCH;
+        constexpr int STEP = Ly::RING / 4;
+        float M = -INFINITY, L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float m, float l, const float4& y) {
+            // (a piece whose scores are all NaN keeps m = -inf, and its sums are NaN)
+            const float f = m == -INFINITY ? 1.f : ex2_approx(m - M);
+            L = fmaf(l, f, L);
+            v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
+        };
+        float2 ml = make_float2(-INFINITY, 0.f);
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (tail && whole) {
+            ml = __ldcg(reinterpret_cast<const float2*>(far + DH));
+            y = __ldcg(reinterpret_cast<const float4*>(far + dd));
         }
-        w0 = w1;
+        for (int w = w0; w < w1; ++w) M = fmaxf(M, rec[w * STEP + DH]);
+        M = fmaxf(M, ml.x);
+        for (int w = w0; w < w1; ++w)
+            add(rec[w * STEP + DH], rec[w * STEP + DH + 1], *reinterpret_cast<const float4*>(rec + w * STEP + dd));
+        add(ml.x, ml.y, y);
+        if (whole) {
+            const float inv = 1.f / L;
+            const size_t row = (size_t)(s / a.Hkv) * a.Hq + (size_t)(s % a.Hkv) * G + h;
+            *reinterpret_cast<uint2*>(a.out + row * DH + dd) =
+                make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+        } else {
+            float* dst = a.recs + ((size_t)(cta0 + w0) * 2 + 1) * G * PITCH + h * PITCH;
+            *reinterpret_cast<float4*>(dst + dd) = v;
+            if (dd == 0) *reinterpret_cast<float2*>(dst + DH) = make_float2(M, L);
+        }
     }
-    if (lane == 0) {
-        P4Desc d{has, -1, 0, 0};
-        if (open && seg_begin >= x0 && !ends) {
-            const long long end = seg_begin + use.n;  // of the segment
-            d.last = (int)((end * warps - 1) / units);
-            d.last_slot = run_begin(d.last + 1) == end ? 1 : 0;
-            // within the CTA it is written out already
-            if (d.last / P4_WARPS != (int)blockIdx.x) d.seg = seg;
-            else if (d.last_slot == 0) d.seg = seg;
+    // the (sequence, kv head) that goes on behind this CTA, if it began here
+    if (warp == P4_WARPS - 1 && lane == 0) {
+        P4Desc d{-1, 0, 0, 0};
+        const int s = seg_sh[P4_WARPS - 1];
+        if (s >= 0 && !(whole_sh[P4_WARPS - 1] & 2)) {
+            int w0 = P4_WARPS - 1;
+            while (w0 > 0 && seg_sh[w0 - 1] == s) --w0;
+            if (whole_sh[w0] & 1) {
+                const long long end = seg_begin + use.n;  // (this warp is in it)
+                d.seg = s;
+                d.first = cta0 + w0;
+                d.last = (int)((end * warps - 1) / units);
+                d.last_slot = run_begin(d.last + 1) == end ? 1 : 0;
+            }
         }
-        a.desc[gw] = d;
+        a.desc[blockIdx.x] = d;
     }
 }
 
-// Join the pieces of the (sequence, kv head) that begins in warp blockIdx.x's run: quads of dims by ways of pieces.
-constexpr int P4_JOIN_THREADS = 256;
+// Join the records of the (sequence, kv head) that begins in CTA blockIdx.x's runs and ends in another's: the one at its
+// beginning, one of each CTA behind it (in that CTA's first warp's place) and the one at its end. A thread takes
+// a quad of dims and every ways-th record.
+constexpr int P4_JOIN_THREADS = 512;
 template <int DH>
 __global__ void __launch_bounds__(P4_JOIN_THREADS)
     attn_paged4_join_kernel(const P4Args a) {
@@ -634,10 +673,18 @@ __global__ void __launch_bounds__(P4_JOIN_THREADS)
     pdl_trigger();
     const P4Desc d = a.desc[blockIdx.x];
     if (d.seg < 0) return;
-    const int first = blockIdx.x, G = a.G, quads = G * (DH / 4);
-    const int ways = max(1, P4_JOIN_THREADS / quads);
+    const int G = a.G, quads = G * (DH / 4);  // at most 256
+    const int ways = P4_JOIN_THREADS / quads;
     const int e = threadIdx.x % quads, way = threadIdx.x / quads;
     const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
+    // CTAs behind the first whose first warp leaves a record in place 1; then, for last_slot 0, the end's own
+    const int c0 = d.first / P4_WARPS + 1, c1 = (d.last + d.last_slot - 1) / P4_WARPS;
+    const int middle = max(0, c1 - c0 + 1), n = 1 + middle + (d.last_slot == 0 ? 1 : 0);
+    auto record = [&](int i) -> const float* {
+        const int w = i == 0 ? d.first : i <= middle ? (c0 + i - 1) * P4_WARPS : d.last;
+        const int slot = i <= middle ? 1 : 0;
+        return a.recs + ((size_t)w * 2 + slot) * G * PITCH + h * PITCH;
+    };
     float M = -INFINITY, L = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float m, float l, const float4& y) {
@@ -651,19 +698,28 @@ __global__ void __launch_bounds__(P4_JOIN_THREADS)
         L = fmaf(l, f, L);
         v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
     };
-    if (way < ways)
-        for (int w = first + way; w <= d.last; w += ways) {
-            const int slot = w == d.last ? d.last_slot : 1;
-            if (!(a.desc[w].has >> slot & 1)) continue;
-            const float* rec = a.recs + ((size_t)w * 2 + slot) * G * PITCH + h * PITCH;
-            const float2 ml = *reinterpret_cast<const float2*>(rec + DH);
-            add(ml.x, ml.y, *reinterpret_cast<const float4*>(rec + dd));
+    if (way < ways) {
+        constexpr int U = 4;  // records on their way at once
+        for (int i0 = way; i0 < n; i0 += U * ways) {
+            float2 ml[U];
+            float4 y[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * ways < n) {
+                    const float* rec = record(i0 + u * ways);
+                    ml[u] = __ldcg(reinterpret_cast<const float2*>(rec + DH));
+                    y[u] = __ldcg(reinterpret_cast<const float4*>(rec + dd));
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * ways < n) add(ml[u].x, ml[u].y, y[u]);
         }
+    }
     part[threadIdx.x] = v;
     stat[threadIdx.x] = make_float2(M, L);
     __syncthreads();
     if (way > 0) return;
-    for (int k = 1; k < ways; ++k) add(stat[k * quads + e].x, stat[k * quads + e].y, part[k * quads + e]);
+    for (int k = 1; k < min(ways, n); ++k) add(stat[k * quads + e].x, stat[k * quads + e].y, part[k * quads + e]);
     const float inv = 1.f / L;
     const size_t row = (size_t)(d.seg / a.Hkv) * a.Hq + (size_t)(d.seg % a.Hkv) * G + h;
     *reinterpret_cast<uint2*>(a.out + row * DH + dd) =
@@ -677,16 +733,16 @@ cudaError_t paged4_launch_dh(P4Args a, cudaStream_t st) {
     const int ctas = p4_ctas();
     cudaError_t e = launch_pdl(attn_paged4_kernel<DH>, dim3(ctas), dim3(P4_THREADS), P4Layout<DH>::SMEM, st, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_paged4_join_kernel<DH>, dim3(ctas * P4_WARPS), dim3(P4_JOIN_THREADS), 0, st, a);
+    return launch_pdl(attn_paged4_join_kernel<DH>, dim3(ctas), dim3(P4_JOIN_THREADS), 0, st, a);
 }
 
-size_t desc_bytes(int warps) { return ((size_t)warps * sizeof(P4Desc) + 255) / 256 * 256; }
+size_t desc_bytes() { return ((size_t)p4_ctas() * sizeof(P4Desc) + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t attn_decode_paged4_workspace(int G, int dh) {
     const int warps = p4_ctas() * P4_WARPS;
-    return desc_bytes(warps) + (size_t)warps * 2 * G * (dh + 4) * sizeof(float);
+    return desc_bytes() + (size_t)warps * 2 * G * (dh + 4) * sizeof(float);
 }
 
 cudaError_t attn_decode_paged4_launch(const __nv_bfloat16* q, const void* k_pages, const void* v_pages, int n_pages, int page,
@@ -705,7 +761,7 @@ cudaError_t attn_decode_paged4_launch(const __nv_bfloat16* q, const void* k_page
     a.G = Hq / Hkv;
     a.cap = (int)std::min<long long>((long long)max_pages * page, 1 << 30);
     a.desc = static_cast<P4Desc*>(work);
-    a.recs = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + desc_bytes(p4_ctas() * P4_WARPS));
+    a.recs = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + desc_bytes());
     a.err = err;
     return dh == 128 ? paged4_launch_dh<128>(a, st) : paged4_launch_dh<64>(a, st);
 }
