@@ -15,10 +15,9 @@ namespace {
 //   q . k_i = sum_g scale_ig (sum_{d in g} q_d code_id) + min_ig (sum_{d in g} q_d)
 //   sum_i p_i v_id = sum_i (p_i scale_ig) code_id + sum_i p_i min_ig
 // so a code is only turned into a 16-bit operand, and scales are applied to scores and probabilities.
-//   Codes of K become fp16 by a mask alone: a nibble in the lowest bits of an fp16 word is the subnormal code * 2^-24 (the
-//   next nibble code * 2^-20, its query value divided by 16), exact on the tensor cores. q is scaled by a power of two
-//   for each head so that its fp16 form is exact (its largest value lies in [2^10, 2^11)).
-//   Codes of V become fp16 in the same way (odd nibbles end up 16 times too large in output rows of their own). Their
+//   Codes of K and V become fp16 by a mask alone: a nibble in the lowest bits of an fp16 word is the subnormal code * 2^-24, the
+//   next nibble code * 2^-20, exact on the tensor cores (K: its query value is divided by 16; V: output rows of its own).
+//   q is scaled by a power of two for each head so that its fp16 form is exact (its largest value lies in [2^10, 2^11)). V's
 //   weights p * scale are rounded to fp16, off by 2^-11 of themselves at most: a power of two for each head keeps the largest
 //   weight of the run so far in [2^13, 2^15], so what falls below fp16's normal range is less than 2^-25 of that.
 //   (bf16 weights, with codes as 128 + code and the offset taken off again, left 0.5-1.2% of error on long sequences against
@@ -31,14 +30,16 @@ namespace {
 // A (sequence, kv head) within one run is written out at once. Of one that is cut, each warp leaves a piece (sums,
 // maximum, sum of weights); pieces of one CTA are joined in shared memory, the others in the workspace by
 // attn_paged4_join_kernel, in the order of their keys: the result does not depend on timing.
-constexpr int P4_KEYS = 32, P4_WARPS = 8, P4_THREADS = 32 * P4_WARPS, P4_CTAS = 2, P4_MAX_G = 8;
+constexpr int P4_UNIT = 32, P4_TILES = P4_UNIT / 16;
+constexpr int P4_WARPS = 8, P4_THREADS = 32 * P4_WARPS, P4_CTAS = 2, P4_MAX_G = 8;
 constexpr int P4_STRIPS = P4_THREADS;  // strips of sequences whose units are counted at the start
 template <int DH>
 struct P4Layout {
     static constexpr int NG = DH / kP4Group;
-    static constexpr int UNIT = P4_KEYS * p4_token_bytes(DH);  // bytes of K (or V) of a unit
-    static constexpr int ST = 24 / (DH / 16);                  // units in a ring: 3 (dh 128), 6 (dh 64)
-    static constexpr int RING = ST * 2 * UNIT;
+    static constexpr int HALF = P4_UNIT * p4_token_bytes(DH);  // bytes of K (or V) of a unit
+    static constexpr int SLOT = 2 * HALF;
+    static constexpr int NS = 3 * 128 / DH;  // slots of a ring
+    static constexpr int RING = NS * SLOT;
     static constexpr int PITCH = DH + 4;  // floats of a head's piece: sums, maximum, sum of weights
     static constexpr int SMEM = P4_WARPS * RING;
     static_assert(P4_MAX_G * PITCH * 4 <= RING, "a piece fits a ring");
@@ -74,6 +75,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {  // d = a b
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %10, %10, %10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -89,6 +97,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -99,49 +110,49 @@ __device__ __forceinline__ int p4_keys(const P4Args& a, int b) {
     const int n = __ldg(a.len0 + b);
     return n < 0 ? 0 : n >= a.cap ? a.cap : n + 1;
 }
-__device__ __forceinline__ int p4_units(int keys) { return (keys + P4_KEYS - 1) / P4_KEYS; }
+__device__ __forceinline__ int p4_units(int keys) { return (keys + P4_UNIT - 1) / P4_UNIT; }
 
-// A place in the list of units: unit u of n of (sequence b, kv head h).
+// A place in the list of units: unit u of n of (sequence b, kv head h), `left` units before the end of the run.
 struct P4Cursor {
-    int b, h, u, n, keys;
+    int b, h, u, n, keys, left;
 };
 __device__ __forceinline__ void p4_step(const P4Args& a, P4Cursor& c) {
-    if (++c.u < c.n) return;
+    --c.left;
+    if (++c.u < c.n || c.left == 0) return;
     c.u = 0;
     if (++c.h < a.Hkv) return;
     c.h = 0;
-    do {  // (sequences without keys have no units)
-        ++c.b;
-        c.keys = c.b < a.B ? p4_keys(a, c.b) : 1;
+    do {  // (sequences without keys have no units; the run is within the list)
+        c.keys = p4_keys(a, ++c.b);
     } while (c.keys == 0);
     c.n = p4_units(c.keys);
 }
 
-template <int DH>
+// BT: 16-key tiles of a page that a unit takes (1: two pages of 16 tokens; 2: a page of 32 or a part of a larger one).
+template <int DH, int BT>
 __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     attn_paged4_kernel(const P4Args a) {
     using Ly = P4Layout<DH>;
-    constexpr int NG = Ly::NG, ST = Ly::ST, UNIT = Ly::UNIT, PITCH = Ly::PITCH;
+    constexpr int NG = Ly::NG, NS = Ly::NS, SLOT = Ly::SLOT, PITCH = Ly::PITCH;
     extern __shared__ __align__(128) uint8_t p4_rings[];
-    __shared__ uint64_t bars[P4_WARPS][2 * ST];  // [K of each stage, V of each stage]
-    __shared__ int strip_end[P4_STRIPS];         // units of one kv head up to the strip's end
+    __shared__ uint64_t bars[P4_WARPS][NS];
+    __shared__ int strip_end[P4_STRIPS];  // units of one kv head up to the strip's end
     __shared__ int warp_sum[P4_WARPS];
     __shared__ int seg_sh[P4_WARPS], whole_sh[P4_WARPS];
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;  // fragment coordinates
-    uint64_t* k_full = bars[warp];
-    uint64_t* v_full = bars[warp] + ST;
+    uint64_t* full = bars[warp];
     if (threadIdx.x == 0) abort_sh = 0;
     if (lane == 0) {
-        for (int i = 0; i < 2 * ST; ++i) mbar_init(&bars[warp][i], 1);
+        for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
         fence_mbar_init();
     }
     pdl_wait();
     pdl_trigger();
 
-    // ---------------- this warp's run of units [x0, x0 + mine)
+    // ---------------- this warp's run of units [x0, x1)
     const int per = (a.B + P4_STRIPS - 1) / P4_STRIPS;
     {
         int sum = 0;
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             for (int e = threadIdx.x; e < a.Hq * DH / 8; e += P4_THREADS)
                 reinterpret_cast<uint4*>(a.out + (size_t)b * a.Hq * DH)[e] = make_uint4(0, 0, 0, 0);
 
-    P4Cursor use{0, 0, 0, 1, 1};
+    P4Cursor use{0, 0, 0, 1, 1, mine};
     long long seg_begin = x0;  // of the list, where the current (sequence, kv head) begins
     if (mine > 0) {
         // the strip, then the sequence, that holds unit x0: sequence b's units are [Hkv P_b, Hkv P_(b+1))
@@ -195,77 +206,66 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         seg_begin = x0 - use.u;
     }
 
-    // ---------------- the ring: copies of the unit at `ask`
+    // ---------------- the ring: the run's unit i goes to slot i % NS, K in the first half of it, V in the second
+    constexpr int TILE = 16 * DH / 2, SIDE = 16 * NG * 4;  // codes, and scales and minima, of 16 keys
+    auto tile_at = [](int i) { return BT == 1 ? i * (TILE + SIDE) : i * TILE; };  // tile i in its half
+    auto side_at = [](int i) { return BT == 1 ? i * (TILE + SIDE) + TILE : P4_TILES * TILE + i * SIDE; };
     P4Cursor ask = use;
+    int issued = 0, used = 0;
     const int page_log = a.cache.page_log, page = 1 << page_log;
     const size_t page_bytes = p4_page_bytes(page, DH);
-    const bool small = page < P4_KEYS;  // a unit is two pages of 16 tokens
     const uint32_t ring_a = smem_u32(p4_rings + warp * Ly::RING);
-    // tile i (16 keys) of a unit: codes at i * tile_step, scales and minima at side_off + i * side_step
-    const int tile_step = small ? 16 * p4_token_bytes(DH) : 16 * DH / 2;
-    const int side_off = small ? 16 * DH / 2 : P4_KEYS * DH / 2, side_step = small ? tile_step : 16 * NG * 4;
     int tab = 0, tab_b = -1, tab_at = 0;  // this lane's entry of the page table, tab_at + lane of sequence tab_b
-    long long src = 0;                    // lanes 0 and 1: offset of their copy in the pages
-    uint32_t src_bytes = 0, unit_bytes = 0;
     bool bad_page = false;
-    auto locate = [&]() {  // where the unit at `ask` lies
-        const int first = small ? ask.u * 2 : ask.u * P4_KEYS >> page_log, at = first & ~31;
+    // Lanes 0 and 1 copy K, lanes 2 and 3 V: a page each (BT 1), or the codes and the scales and minima of a part of one.
+    const uint8_t* from = (lane & 2 ? a.cache.v : a.cache.k) + (BT == 2 && (lane & 1) ? page * (DH / 2) : 0);
+    const int row_bytes = BT == 1 ? 0 : lane & 1 ? NG * 4 : DH / 2;
+    const uint32_t to = ring_a + (lane & 2 ? Ly::HALF : 0) + (lane & 1 ? (BT == 1 ? TILE + SIDE : P4_TILES * TILE) : 0);
+    auto issue = [&](int slot) {  // the next unit, if the run has one
+        if (ask.left == 0) return;
+        const int first = ask.u * P4_UNIT >> page_log, at = first & ~31;
         if (tab_b != ask.b || tab_at != at) {
             tab_b = ask.b;
             tab_at = at;
             tab = at + lane < a.cache.max_pages ? __ldg(a.cache.table + (size_t)ask.b * a.cache.max_pages + at + lane) : 0;
         }
-        int id = __shfl_sync(0xffffffffu, tab, (first & 31) + (small ? (lane & 1) : 0));
-        const int blocks = small && ask.keys - ask.u * P4_KEYS > 16 ? 2 : 1;
-        const bool mine_bad = (unsigned)id >= (unsigned)a.cache.n_pages && (lane & 1) < blocks;
-        bad_page = bad_page || mine_bad;
-        if ((unsigned)id >= (unsigned)a.cache.n_pages) id = 0;  // (flagged; the output is invalid)
-        src = ((long long)id * a.Hkv + ask.h) * (long long)page_bytes;
-        if (small) {
-            src_bytes = lane < blocks ? 16 * p4_token_bytes(DH) : 0;
-            unit_bytes = blocks * 16 * p4_token_bytes(DH);
-        } else {
-            const int row = (ask.u * P4_KEYS) & (page - 1);
-            src += lane == 0 ? row * (DH / 2) : page * (DH / 2) + row * NG * 4;
-            src_bytes = lane == 0 ? P4_KEYS * DH / 2 : lane == 1 ? P4_KEYS * NG * 4 : 0;
-            unit_bytes = UNIT;
+        // (the second of two pages is fetched only if the sequence reaches it)
+        const int pages = BT == 1 && ask.keys - ask.u * P4_UNIT > 16 ? 2 : 1;
+        int id = __shfl_sync(0xffffffffu, tab, (first & 31) + (BT == 1 ? lane & 1 : 0));
+        const bool copies = lane < 4 && (BT == 2 || (lane & 1) < pages);
+        if ((unsigned)id >= (unsigned)a.cache.n_pages) {  // (flagged; the output is invalid)
+            bad_page = bad_page || copies;
+            id = 0;
         }
-    };
-    auto load = [&](const uint8_t* pages, uint64_t* full, int st, int off) {
-        if (lane == 0) mbar_expect_tx(&full[st], unit_bytes);
+        if (lane == 0) mbar_expect_tx(&full[slot], BT == 1 ? pages * 2 * (TILE + SIDE) : Ly::SLOT);
         __syncwarp();
-        if (lane < 2 && src_bytes)
-            bulk_load(ring_a + st * 2 * UNIT + off + (lane == 0 ? 0 : small ? 16 * p4_token_bytes(DH) : P4_KEYS * DH / 2),
-                      pages + src, src_bytes, &full[st]);
+        if (copies)
+            bulk_load(to + slot * Ly::SLOT,
+                      from + ((long long)id * a.Hkv + ask.h) * (long long)page_bytes + ((ask.u * P4_UNIT) & (page - 1)) * row_bytes,
+                      BT == 1 ? TILE + SIDE : lane & 1 ? P4_TILES * SIDE : P4_TILES * TILE, &full[slot]);
+        ++issued;
+        p4_step(a, ask);
     };
     __syncwarp();  // the barriers are set
-    for (int i = 0; i < min(ST, mine); ++i) {
-        locate();
-        load(a.cache.k, k_full, i, 0);
-        load(a.cache.v, v_full, i, UNIT);
-        p4_step(a, ask);
-    }
+#pragma unroll 1
+    for (int i = 0; i < NS; ++i) issue(i);
 
     // ---------------- products
     const float sl2 = kLog2e / sqrtf((float)DH);
-    uint32_t qf[NG][4][2];      // q^T fragments: column g = query head g of the group (zero past G)
-    float qs[NG][2], qscale[2]; // heads 2t and 2t + 1: sums of the fp16 values of a group of dims; what they are scaled by
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float o[NG][4][4], z[NG][2];  // sums of codes (in units of 2^-24 / nu, odd rows of tiles 2^-20 / nu), and of minima
-    float nu[2] = {1.f, 1.f};      // heads 2t and 2t + 1: the power of two on the weights of V
+    uint32_t qf[NG][2][2][2];  // q^T fragments [group][word][part][half]: column g = query head g of the group (zero past G)
+    float2 qs[NG], qscale;     // heads 2t and 2t + 1: sums of the scaled queries over a group of dims; what x is scaled by
+    float2 m = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
+    float o[NG][4][4];             // sums of codes, in units of 2^-24 / nu (tiles 1 and 3: 2^-20 / nu)
+    float2 z[NG];                  // sums of minima
+    float2 nu = make_float2(1.f, 1.f);  // the power of two on the weights of V
     auto reset = [&]() {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            m[e] = -INFINITY;
-            l[e] = 0.f;
-        }
+        m = make_float2(-INFINITY, -INFINITY);
+        l = make_float2(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
-            z[c][0] = z[c][1] = 0.f;
+            z[c] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                o[c][0][e] = o[c][1][e] = o[c][2][e] = o[c][3][e] = 0.f;
-            }
+            for (int e = 0; e < 4; ++e) o[c][0][e] = o[c][1][e] = o[c][2][e] = o[c][3][e] = 0.f;
         }
     };
     auto load_q = [&]() {
@@ -307,39 +307,41 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             s += __shfl_xor_sync(0xffffffffu, s, 2);
             sums[c] = s * 5.9604644775390625e-8f;  // 2^-24, the unit of the products of codes
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // word k / 2, nibbles 2 (k % 2) and that + 4; then the ones after them
-                const int d = (k >> 1) * 8 + (k & 1) * 2;
-                qf[c][k][0] = pack_f16(x[c][d], x[c][d + 4]);
-                qf[c][k][1] = pack_f16(x[c][d + 1] * 0.0625f, x[c][d + 5] * 0.0625f);
-            }
-        }
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23) * 16777216.f * sl2;
+            for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) {
-            const int from = (2 * t + e2) * 4;
-            qscale[e2] = __shfl_sync(0xffffffffu, up, from);
-#pragma unroll
-            for (int c = 0; c < NG; ++c) qs[c][e2] = __shfl_sync(0xffffffffu, sums[c], from);
+                for (int part = 0; part < 2; ++part) {  // nibbles 2 part and that + 4; the ones after them
+                    const int d = w * 8 + part * 2;
+                    qf[c][w][part][0] = pack_f16(x[c][d], x[c][d + 4]);
+                    qf[c][w][part][1] = pack_f16(x[c][d + 1] * 0.0625f, x[c][d + 5] * 0.0625f);
+                }
         }
+        // (a query of infinity has no finite form)
+        const float up = big < INFINITY ? __uint_as_float((uint32_t)(127 + e) << 23) * 16777216.f * sl2 : __uint_as_float(0x7fc00000u);
+        const int from = 2 * t * 4;
+        qscale = make_float2(__shfl_sync(0xffffffffu, up, from), __shfl_sync(0xffffffffu, up, from + 4));
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+            qs[c] = make_float2(__shfl_sync(0xffffffffu, sums[c], from), __shfl_sync(0xffffffffu, sums[c], from + 4));
     };
     // the sums of this warp's piece at scale m: dims c * 64 + 8 g + (0..7) of head 2t + e
     auto piece = [&](int c, int e, float (&v)[8]) {
-        const float unit = 16777216.f * (1.f / nu[e]);
+        const float unit = 16777216.f / (e ? nu.y : nu.x), add = e ? z[c].y : z[c].x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float u = i & 1 ? unit * 0.0625f : unit;
-            v[i] = fmaf(o[c][i][e], u, z[c][e]);
-            v[4 + i] = fmaf(o[c][i][2 + e], u, z[c][e]);
+            v[i] = fmaf(o[c][i][e], u, add);
+            v[4 + i] = fmaf(o[c][i][2 + e], u, add);
         }
     };
     auto total = [&]() {  // l and z over the keys that other lanes took
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) {
+            l.x += __shfl_xor_sync(0xffffffffu, l.x, s);
+            l.y += __shfl_xor_sync(0xffffffffu, l.y, s);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], s);
-#pragma unroll
-                for (int c = 0; c < NG; ++c) z[c][e] += __shfl_xor_sync(0xffffffffu, z[c][e], s);
+            for (int c = 0; c < NG; ++c) {
+                z[c].x += __shfl_xor_sync(0xffffffffu, z[c].x, s);
+                z[c].y += __shfl_xor_sync(0xffffffffu, z[c].y, s);
             }
         }
     };
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
-            if (g == 0) *reinterpret_cast<float2*>(rec + h * PITCH + DH) = make_float2(m[e], l[e]);
+            if (g == 0) *reinterpret_cast<float2*>(rec + h * PITCH + DH) = e ? make_float2(m.y, l.y) : make_float2(m.x, l.x);
         }
     };
     auto write_out = [&]() {
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         for (int e = 0; e < 2; ++e) {
             const int h = 2 * t + e;
             if (h >= a.G) continue;
-            const float inv = 1.f / l[e];
+            const float inv = 1.f / (e ? l.y : l.x);
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
                 float v[8];
@@ -375,215 +377,206 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             }
         }
     };
+    auto sides = [&](uint32_t at, uint32_t (&sd)[2][NG]) {  // scales and minima of this lane's two keys of a tile
+        if constexpr (NG == 2) {
+            const uint2 s0 = lds64(at), s1 = lds64(at + 8 * NG * 4);
+            sd[0][0] = s0.x;
+            sd[0][1] = s0.y;
+            sd[1][0] = s1.x;
+            sd[1][1] = s1.y;
+        } else {
+            sd[0][0] = lds32(at);
+            sd[1][0] = lds32(at + 8 * NG * 4);
+        }
+    };
     float* my_recs = a.recs + (size_t)gw * 2 * a.G * PITCH;
     const int swap = (g & 4) | (g & 1) << 1 | (g >> 1 & 1);  // row g of a tile is key swap (and row g + 8 key swap + 8):
     const int vkey = (2 * t & 4) | (t & 1);                  // the keys of rows 2t, which one load of V takes, are 0, 1, 4, 5
-    bool ok = true, ahead = false;
+    bool ok = true, fresh = true;
+    int slot = 0, phase = 0;
     reset();
-    int i = 0;
-    for (; i < mine; ++i) {
-        if (i == 0 || use.u == 0) load_q();
-        const int st = i % ST, ph = (i / ST) & 1;
-        const uint32_t ka = ring_a + st * 2 * UNIT, va = ka + UNIT;
-        if (!__all_sync(0xffffffffu, mbar_wait_suspend(&k_full[st], ph, abort_flag))) { ok = false; break; }
-        const int valid = use.keys - use.u * P4_KEYS;  // keys of the unit, 32 or more: all
-        const int tiles = valid > 16 ? 2 : 1;
-        float x[2][4];
+#pragma unroll 1
+    while (use.left > 0) {
+        if (fresh) load_q();
+        if (!__all_sync(0xffffffffu, mbar_wait_suspend(&full[slot], phase, abort_flag))) { ok = false; break; }
+        const uint32_t ka = ring_a + slot * Ly::SLOT, va = ka + Ly::HALF;
+        const int valid = use.keys - use.u * P4_UNIT;  // keys of the unit; 32 or more: all
+        if (valid < P4_UNIT) {
+            // what stands behind the last key may be anything: its scales and minima become 0 (0 * NaN must not reach O)
+            for (int e = lane; e < (P4_UNIT - valid) * NG; e += 32) {
+                const int key = valid + e / NG, tile = key >> 4;
+                sts32(va + side_at(0) + tile * (side_at(1) - side_at(0)) + (key & 15) * (NG * 4) + e % NG * 4, 0u);
+            }
+            fence_proxy_async_smem();  // (the slot's next copy comes after these stores)
+            __syncwarp();
+        }
+        float2 x[P4_TILES][2];  // [tile][row g, row g + 8]: heads 2t, 2t + 1
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (k < tiles) {
-                const uint32_t codes = ka + k * tile_step + swap * (DH / 2) + 8 * t, side = ka + side_off + k * side_step + swap * (NG * 4);
-                float acc[NG][4];
-                uint32_t sd[2][NG];
-                if constexpr (NG == 2) {
-                    const uint2 s0 = lds64(side), s1 = lds64(side + 8 * NG * 4);
-                    sd[0][0] = s0.x;
-                    sd[0][1] = s0.y;
-                    sd[1][0] = s1.x;
-                    sd[1][1] = s1.y;
-                } else {
-                    sd[0][0] = lds32(side);
-                    sd[1][0] = lds32(side + 8 * NG * 4);
+        for (int k = 0; k < P4_TILES; ++k) {
+            const uint32_t codes = ka + tile_at(k) + swap * (DH / 2) + 8 * t;
+            float acc[NG][4];
+            uint32_t sd[2][NG];
+            sides(ka + side_at(k) + swap * (NG * 4), sd);
+#pragma unroll
+            for (int c = 0; c < NG; ++c) {
+                const uint2 w0 = lds64(codes + c * 32), w1 = lds64(codes + 8 * (DH / 2) + c * 32);
+                const uint32_t a0[2] = {w0.x, w0.y}, a1[2] = {w1.x, w1.y};
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t y0 = a0[w] >> 8, y1 = a1[w] >> 8;
+                    if (w == 0)
+                        mma_f16_first(acc[c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
+                                      a1[w] & 0x00f000f0u, qf[c][w][0][0], qf[c][w][0][1]);
+                    else
+                        mma_f16(acc[c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u, a1[w] & 0x00f000f0u,
+                                qf[c][w][0][0], qf[c][w][0][1]);
+                    mma_f16(acc[c], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
+                            qf[c][w][1][0], qf[c][w][1][1]);
                 }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                 for (int c = 0; c < NG; ++c) {
-                    const uint2 w0 = lds64(codes + c * 32), w1 = lds64(codes + 8 * (DH / 2) + c * 32);
-                    acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
-                    const uint32_t a0[2] = {w0.x, w0.y}, a1[2] = {w1.x, w1.y};
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t y0 = a0[w] >> 8, y1 = a1[w] >> 8;
-                        mma_f16(acc[c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u, a1[w] & 0x00f000f0u,
-                                qf[c][2 * w][0], qf[c][2 * w][1]);
-                        mma_f16(acc[c], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
-                                qf[c][2 * w + 1][0], qf[c][2 * w + 1][1]);
-                    }
+                    const float sc = bf16_lo(sd[r][c]), lo = bf16_hi(sd[r][c]);
+                    s0 = fmaf(sc, acc[c][2 * r], c == 0 ? lo * qs[c].x : fmaf(lo, qs[c].x, s0));
+                    s1 = fmaf(sc, acc[c][2 * r + 1], c == 0 ? lo * qs[c].y : fmaf(lo, qs[c].y, s1));
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int c = 0; c < NG; ++c)
-                        s = fmaf(bf16_lo(sd[e >> 1][c]), acc[c][e], fmaf(bf16_hi(sd[e >> 1][c]), qs[c][e & 1], s));
-                    x[k][e] = s * qscale[e & 1];
-                }
-                if (valid < P4_KEYS) {
-                    if (k * 16 + swap >= valid) x[k][0] = x[k][1] = -INFINITY;
-                    if (k * 16 + swap + 8 >= valid) x[k][2] = x[k][3] = -INFINITY;
-                }
-            } else {
-                x[k][0] = x[k][1] = x[k][2] = x[k][3] = -INFINITY;
+                x[k][r] = make_float2(s0 * qscale.x, s1 * qscale.y);
             }
         }
-        __syncwarp();  // every lane has read the unit's keys: the next ones may come
-        ahead = i + ST < mine;
-        if (ahead) {
-            locate();
-            load(a.cache.k, k_full, st, 0);
-        }
-        float mx[2];
+        if (valid < P4_UNIT) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e]));
+            for (int k = 0; k < P4_TILES; ++k)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    if (k * 16 + swap + 8 * r >= valid) x[k][r] = make_float2(-INFINITY, -INFINITY);
+        }
+        float2 mx = make_float2(fmax3(fmaxf(x[0][0].x, x[0][1].x), x[1][0].x, x[1][1].x),
+                                fmax3(fmaxf(x[0][0].y, x[0][1].y), x[1][0].y, x[1][1].y));
         // O and the sums move to a larger maximum only when it grew by more than 8 (P <= 2^8)
-        const bool moved = __any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f);
-        float shrink[2] = {1.f, 1.f};
+        const bool moved = __any_sync(0xffffffffu, mx.x > m.x + 8.f || mx.y > m.y + 8.f);
+        float2 shrink = make_float2(1.f, 1.f);  // (O follows below)
         if (moved) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int s = 4; s < 32; s <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], s));
-                const bool grow = mx[e] > m[e] + 8.f;
-                const float f = grow ? ex2_approx(m[e] - mx[e]) : 1.f;
-                m[e] = grow ? mx[e] : m[e];
-                l[e] *= f;
-                shrink[e] = f;  // (O follows below)
-#pragma unroll
-                for (int c = 0; c < NG; ++c) z[c][e] *= f;
+            for (int s = 4; s < 32; s <<= 1) {
+                mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, s));
+                mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, s));
             }
+            if (mx.x > m.x + 8.f) {
+                shrink.x = ex2_approx(m.x - mx.x);
+                m.x = mx.x;
+            }
+            if (mx.y > m.y + 8.f) {
+                shrink.y = ex2_approx(m.y - mx.y);
+                m.y = mx.y;
+            }
+            l = mul2(l, shrink);
+#pragma unroll
+            for (int c = 0; c < NG; ++c) z[c] = mul2(z[c], shrink);
         }
-        const float nm[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[k][e] = ex2_approx(x[k][e] + nm[e & 1]);
-                l[e & 1] += x[k][e];
-            }
-        if (!__all_sync(0xffffffffu, mbar_wait_suspend(&v_full[st], ph, abort_flag))) { ok = false; break; }
+        const float2 nm = make_float2(m.x == -INFINITY ? 0.f : -m.x, m.y == -INFINITY ? 0.f : -m.y);
         // weights of V by group of dims: p * scale, and the sums of p * minimum
-        float wt[2][NG][4];
-        float top[2] = {0.f, 0.f};
+        float2 wt[P4_TILES][NG][2];
+        float2 top = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (k < tiles) {
-                const uint32_t side = va + side_off + k * side_step + swap * (NG * 4);
-                uint32_t sd[2][NG];
-                if constexpr (NG == 2) {
-                    const uint2 s0 = lds64(side), s1 = lds64(side + 8 * NG * 4);
-                    sd[0][0] = s0.x;
-                    sd[0][1] = s0.y;
-                    sd[1][0] = s1.x;
-                    sd[1][1] = s1.y;
-                } else {
-                    sd[0][0] = lds32(side);
-                    sd[1][0] = lds32(side + 8 * NG * 4);
-                }
-                if (valid < P4_KEYS) {  // what stands behind the last key may be anything: 0 * NaN must not reach O
+        for (int k = 0; k < P4_TILES; ++k) {
+            uint32_t sd[2][NG];
+            sides(va + side_at(k) + swap * (NG * 4), sd);
 #pragma unroll
-                    for (int c = 0; c < NG; ++c) {
-                        if (k * 16 + swap >= valid) sd[0][c] = 0;
-                        if (k * 16 + swap + 8 >= valid) sd[1][c] = 0;
-                    }
-                }
-#pragma unroll
-                for (int c = 0; c < NG; ++c)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        z[c][e] = fmaf(x[k][e], bf16_hi(sd[0][c]), fmaf(x[k][2 + e], bf16_hi(sd[1][c]), z[c][e]));
-                        wt[k][c][e] = x[k][e] * bf16_lo(sd[0][c]);
-                        wt[k][c][2 + e] = x[k][2 + e] * bf16_lo(sd[1][c]);
-                        top[e] = fmax3(top[e], fabsf(wt[k][c][e]), fabsf(wt[k][c][2 + e]));
-                    }
-            } else {
-#pragma unroll
-                for (int c = 0; c < NG; ++c) wt[k][c][0] = wt[k][c][1] = wt[k][c][2] = wt[k][c][3] = 0.f;
-            }
-        }
-        if (moved || __any_sync(0xffffffffu, top[0] * nu[0] > 32768.f || top[1] * nu[1] > 32768.f)) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int s = 4; s < 32; s <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], s));
-                // the largest weight of the run so far: what was below 2^14 / nu has shrunk with the scores' maximum
-                const float big = fmaxf(top[e], shrink[e] * (16384.f / nu[e]));
-                const int at = min(max(13 + 127 - (int)(__float_as_uint(big) >> 23), -100), 100);  // big 2^at in [2^13, 2^14)
-                const float next = big > 0.f ? __uint_as_float((uint32_t)(127 + at) << 23) : nu[e], f = next / nu[e] * shrink[e];
-                nu[e] = next;
-#pragma unroll
-                for (int c = 0; c < NG; ++c)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        o[c][k][e] *= f;
-                        o[c][k][2 + e] *= f;
-                    }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (k < tiles) {
-                const uint32_t codes = va + k * tile_step + vkey * (DH / 2) + 4 * g;
+            for (int r = 0; r < 2; ++r) {
+                const float2 p = make_float2(ex2_approx(x[k][r].x + nm.x), ex2_approx(x[k][r].y + nm.y));
+                l = add2(l, p);
 #pragma unroll
                 for (int c = 0; c < NG; ++c) {
-                    const uint32_t b0 = transpose8x8(pack_f16(wt[k][c][0] * nu[0], wt[k][c][1] * nu[1]));
-                    const uint32_t b1 = transpose8x8(pack_f16(wt[k][c][2] * nu[0], wt[k][c][3] * nu[1]));
-                    // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further: the first and the last four nibbles
-                    const uint32_t wa = lds32(codes + c * 32), wb = lds32(codes + c * 32 + 2 * (DH / 2));
-                    const uint32_t wc = lds32(codes + c * 32 + 8 * (DH / 2)), wd = lds32(codes + c * 32 + 10 * (DH / 2));
-                    uint32_t v[4] = {__byte_perm(wa, wb, 0x5410), __byte_perm(wa, wb, 0x7632), __byte_perm(wc, wd, 0x5410),
-                                     __byte_perm(wc, wd, 0x7632)};
+                    const float sc = bf16_lo(sd[r][c]), lo = bf16_hi(sd[r][c]);
+                    z[c] = make_float2(fmaf(p.x, lo, z[c].x), fmaf(p.y, lo, z[c].y));
+                    wt[k][c][r] = make_float2(p.x * sc, p.y * sc);
+                }
+            }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (q == 2) {
+            for (int c = 0; c < NG; ++c) {
+                top.x = fmax3(top.x, fabsf(wt[k][c][0].x), fabsf(wt[k][c][1].x));
+                top.y = fmax3(top.y, fabsf(wt[k][c][0].y), fabsf(wt[k][c][1].y));
+            }
+        }
+        if (moved || __any_sync(0xffffffffu, top.x * nu.x > 32768.f || top.y * nu.y > 32768.f)) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) v[j] >>= 8;
-                        }
-                        const uint32_t mask = q & 1 ? 0x00f000f0u : 0x000f000fu;
-                        mma_f16(o[c][q], v[0] & mask, v[1] & mask, v[2] & mask, v[3] & mask, b0, b1);
+            for (int s = 4; s < 32; s <<= 1) {
+                top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, s));
+                top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, s));
+            }
+            // the largest weight of the run so far: what was below 2^14 / nu has shrunk with the scores' maximum
+            auto next_nu = [](float top, float shrink, float nu) {
+                const float big = fmaxf(top, shrink * (16384.f / nu));
+                const int at = min(max(140 - (int)(__float_as_uint(big) >> 23), -100), 100);  // big 2^at in [2^13, 2^14)
+                return big > 0.f ? __uint_as_float((uint32_t)(127 + at) << 23) : nu;
+            };
+            const float2 next = make_float2(next_nu(top.x, shrink.x, nu.x), next_nu(top.y, shrink.y, nu.y));
+            const float2 f = make_float2(next.x / nu.x * shrink.x, next.y / nu.y * shrink.y);
+            nu = next;
+#pragma unroll
+            for (int c = 0; c < NG; ++c)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    o[c][q][0] *= f.x;
+                    o[c][q][1] *= f.y;
+                    o[c][q][2] *= f.x;
+                    o[c][q][3] *= f.y;
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < P4_TILES; ++k) {
+            const uint32_t codes = va + tile_at(k) + vkey * (DH / 2) + 4 * g;
+#pragma unroll
+            for (int c = 0; c < NG; ++c) {
+                const float2 w0 = mul2(wt[k][c][0], nu), w1 = mul2(wt[k][c][1], nu);
+                const uint32_t b0 = transpose8x8(pack_f16(w0.x, w0.y)), b1 = transpose8x8(pack_f16(w1.x, w1.y));
+                // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further: the first and the last four nibbles
+                const uint32_t wa = lds32(codes + c * 32), wb = lds32(codes + c * 32 + 2 * (DH / 2));
+                const uint32_t wc = lds32(codes + c * 32 + 8 * (DH / 2)), wd = lds32(codes + c * 32 + 10 * (DH / 2));
+                uint32_t v[4] = {__byte_perm(wa, wb, 0x5410), __byte_perm(wa, wb, 0x7632), __byte_perm(wc, wd, 0x5410),
+                                 __byte_perm(wc, wd, 0x7632)};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q == 2) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] >>= 8;
                     }
+                    const uint32_t mask = q & 1 ? 0x00f000f0u : 0x000f000fu;
+                    mma_f16(o[c][q], v[0] & mask, v[1] & mask, v[2] & mask, v[3] & mask, b0, b1);
                 }
             }
         }
-        __syncwarp();
-        if (ahead) {
-            load(a.cache.v, v_full, st, UNIT);
-            p4_step(a, ask);
+        __syncwarp();  // every lane has read the slot: the unit NS further may come
+        ++used;
+        issue(slot);
+        if (++slot == NS) {
+            slot = 0;
+            phase ^= 1;
         }
-        ahead = false;
-        const bool seg_done = use.u + 1 == use.n;
-        if (seg_done && i + 1 < mine) {  // the sequence ends within the run
+        fresh = use.u + 1 == use.n;
+        if (use.left == 1) break;  // (`use` stays at the run's last unit)
+        if (fresh) {               // the (sequence, kv head) ends within the run
             total();
-            if (seg_begin >= x0) {
-                write_out();
-            } else {
-                leave(my_recs);
-            }
+            if (seg_begin >= x0) write_out();
+            else leave(my_recs);
             reset();
-            seg_begin = x0 + i + 1;
+            seg_begin = x1 - use.left + 1;
         }
-        if (i + 1 < mine) p4_step(a, use);
+        p4_step(a, use);
     }
     if (__any_sync(0xffffffffu, bad_page) && lane == 0 && a.err) atomicOr(a.err, ERR_INDEX);
     if (!ok) {  // give up: wait, bounded, for the copies still on their way
         *abort_flag = 1;
         if (a.err && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
         int never = 0;
-        for (int k = i; k < min(i + ST, mine); ++k) mbar_wait_suspend(&v_full[k % ST], (k / ST) & 1, &never);
-        for (int k = i; k < min(i + ST + 1, mine); ++k)
-            if (k < i + ST || ahead) mbar_wait_suspend(&k_full[k % ST], (k / ST) & 1, &never);
+        for (int j = used; j < issued; ++j) mbar_wait_suspend(&full[j % NS], (j / NS) & 1, &never);
     }
 
     // ---------------- the piece at the end of the run
-    const bool ends = mine > 0 && use.u + 1 == use.n;          // the sequence ends with the run
+    const bool ends = mine > 0 && fresh;                       // the sequence ends with the run
     const bool open = mine > 0 && !(seg_begin >= x0 && ends);  // a part of it lies in another run
     total();
     if (mine > 0 && !open && ok) write_out();
@@ -728,12 +721,17 @@ __global__ void __launch_bounds__(P4_JOIN_THREADS)
 
 int p4_ctas() { return device_sm_count() * P4_CTAS; }
 
-template <int DH>
-cudaError_t paged4_launch_dh(P4Args a, cudaStream_t st) {
+template <int DH, int BT>
+cudaError_t paged4_launch_bt(const P4Args& a, cudaStream_t st) {
     const int ctas = p4_ctas();
-    cudaError_t e = launch_pdl(attn_paged4_kernel<DH>, dim3(ctas), dim3(P4_THREADS), P4Layout<DH>::SMEM, st, a);
+    cudaError_t e = launch_pdl(attn_paged4_kernel<DH, BT>, dim3(ctas), dim3(P4_THREADS), P4Layout<DH>::SMEM, st, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(attn_paged4_join_kernel<DH>, dim3(ctas), dim3(P4_JOIN_THREADS), 0, st, a);
+}
+template <int DH>
+cudaError_t paged4_launch_dh(const P4Args& a, int page, cudaStream_t st) {
+    if (page == 16) return paged4_launch_bt<DH, 1>(a, st);
+    return paged4_launch_bt<DH, 2>(a, st);
 }
 
 size_t desc_bytes() { return ((size_t)p4_ctas() * sizeof(P4Desc) + 255) / 256 * 256; }
@@ -763,14 +761,18 @@ cudaError_t attn_decode_paged4_launch(const __nv_bfloat16* q, const void* k_page
     a.desc = static_cast<P4Desc*>(work);
     a.recs = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + desc_bytes());
     a.err = err;
-    return dh == 128 ? paged4_launch_dh<128>(a, st) : paged4_launch_dh<64>(a, st);
+    return dh == 128 ? paged4_launch_dh<128>(a, page, st) : paged4_launch_dh<64>(a, page, st);
 }
 
 cudaError_t attention_paged4_prepare() {
-    cudaError_t e = cudaFuncSetAttribute(attn_paged4_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, P4Layout<128>::SMEM);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attn_paged4_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, P4Layout<64>::SMEM);
-    return e;
+    const void* fns[] = {(const void*)attn_paged4_kernel<128, 1>, (const void*)attn_paged4_kernel<128, 2>,
+                         (const void*)attn_paged4_kernel<64, 1>, (const void*)attn_paged4_kernel<64, 2>};
+    for (int i = 0; i < 4; ++i) {
+        cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             i < 2 ? P4Layout<128>::SMEM : P4Layout<64>::SMEM);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace q3
