@@ -68,37 +68,23 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
+// (not volatile: the compiler may order the products of a unit as it likes)
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {  // d = a b
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%10, %10, %10, %10};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
@@ -129,7 +115,10 @@ __device__ __forceinline__ void p4_step(const P4Args& a, P4Cursor& c) {
 }
 
 // BT: 16-key tiles of a page that a unit takes (1: two pages of 16 tokens; 2: a page of 32 or a part of a larger one).
-template <int DH, int BT>
+// PAIR, for groups of up to four query heads: the 8 columns hold the heads twice. Of the scores of a unit's two tiles, columns
+// 0-3 keep the first tile's and columns 4-7 the second's, so that no lane works on a column without a head, and O's
+// two halves are added at the end (64 sequences of up to 4096 keys, two heads a group: 56 us -> see below).
+template <int DH, int BT, bool PAIR>
 __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     attn_paged4_kernel(const P4Args a) {
     using Ly = P4Layout<DH>;
@@ -218,32 +207,41 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     int tab = 0, tab_b = -1, tab_at = 0;  // this lane's entry of the page table, tab_at + lane of sequence tab_b
     bool bad_page = false;
     // Lanes 0 and 1 copy K, lanes 2 and 3 V: a page each (BT 1), or the codes and the scales and minima of a part of one.
-    const uint8_t* from = (lane & 2 ? a.cache.v : a.cache.k) + (BT == 2 && (lane & 1) ? page * (DH / 2) : 0);
-    const int row_bytes = BT == 1 ? 0 : lane & 1 ? NG * 4 : DH / 2;
+    const uint8_t* pages = (lane & 2 ? a.cache.v : a.cache.k) + (BT == 2 && (lane & 1) ? page * (DH / 2) : 0);
+    const uint8_t* from = nullptr;
+    const int unit_bytes = P4_UNIT * (lane & 1 ? NG * 4 : DH / 2);  // BT 2: from unit to unit of a page
     const uint32_t to = ring_a + (lane & 2 ? Ly::HALF : 0) + (lane & 1 ? (BT == 1 ? TILE + SIDE : P4_TILES * TILE) : 0);
+    const int page_units = BT == 1 ? 1 : page / P4_UNIT;
+    bool ask_new = true;  // the unit is the first of the run or of a (sequence, kv head)
     auto issue = [&](int slot) {  // the next unit, if the run has one
         if (ask.left == 0) return;
-        const int first = ask.u * P4_UNIT >> page_log, at = first & ~31;
-        if (tab_b != ask.b || tab_at != at) {
-            tab_b = ask.b;
-            tab_at = at;
-            tab = at + lane < a.cache.max_pages ? __ldg(a.cache.table + (size_t)ask.b * a.cache.max_pages + at + lane) : 0;
-        }
         // (the second of two pages is fetched only if the sequence reaches it)
-        const int pages = BT == 1 && ask.keys - ask.u * P4_UNIT > 16 ? 2 : 1;
-        int id = __shfl_sync(0xffffffffu, tab, (first & 31) + (BT == 1 ? lane & 1 : 0));
-        const bool copies = lane < 4 && (BT == 2 || (lane & 1) < pages);
-        if ((unsigned)id >= (unsigned)a.cache.n_pages) {  // (flagged; the output is invalid)
-            bad_page = bad_page || copies;
-            id = 0;
+        const int blocks = BT == 1 && ask.keys - ask.u * P4_UNIT > 16 ? 2 : 1;
+        const bool copies = lane < 4 && (BT == 2 || (lane & 1) < blocks);
+        if (BT == 1 || ask_new || (ask.u & (page_units - 1)) == 0) {
+            const int first = ask.u * P4_UNIT >> page_log, at = first & ~31;
+            if (tab_b != ask.b || tab_at != at) {
+                tab_b = ask.b;
+                tab_at = at;
+                tab = at + lane < a.cache.max_pages ? __ldg(a.cache.table + (size_t)ask.b * a.cache.max_pages + at + lane) : 0;
+            }
+            int id = __shfl_sync(0xffffffffu, tab, (first & 31) + (BT == 1 ? lane & 1 : 0));
+            if ((unsigned)id >= (unsigned)a.cache.n_pages) {  // (flagged; the output is invalid)
+                bad_page = bad_page || copies;
+                id = 0;
+            }
+            from = pages + ((long long)id * a.Hkv + ask.h) * (long long)page_bytes;
+            if (BT == 2) from += (ask.u & (page_units - 1)) * unit_bytes;
+        } else {
+            from += unit_bytes;
         }
-        if (lane == 0) mbar_expect_tx(&full[slot], BT == 1 ? pages * 2 * (TILE + SIDE) : Ly::SLOT);
+        if (lane == 0) mbar_expect_tx(&full[slot], BT == 1 ? blocks * 2 * (TILE + SIDE) : Ly::SLOT);
         __syncwarp();
         if (copies)
-            bulk_load(to + slot * Ly::SLOT,
-                      from + ((long long)id * a.Hkv + ask.h) * (long long)page_bytes + ((ask.u * P4_UNIT) & (page - 1)) * row_bytes,
-                      BT == 1 ? TILE + SIDE : lane & 1 ? P4_TILES * SIDE : P4_TILES * TILE, &full[slot]);
+            bulk_load(to + slot * Ly::SLOT, from, BT == 1 ? TILE + SIDE : unit_bytes, &full[slot]);
         ++issued;
+        const int n = ask.n;
+        ask_new = ask.u + 1 == n;
         p4_step(a, ask);
     };
     __syncwarp();  // the barriers are set
@@ -258,6 +256,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     float o[NG][4][4];             // sums of codes, in units of 2^-24 / nu (tiles 1 and 3: 2^-20 / nu)
     float2 z[NG];                  // sums of minima
     float2 nu = make_float2(1.f, 1.f);  // the power of two on the weights of V
+    const int qh = PAIR ? g & 3 : g;         // head of this lane's column of q
+    const int ch = PAIR ? 2 * (t & 1) : 2 * t;  // head of this lane's first column of scores and outputs
     auto reset = [&]() {
         m = make_float2(-INFINITY, -INFINITY);
         l = make_float2(0.f, 0.f);
@@ -271,13 +271,13 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     auto load_q = [&]() {
         float x[NG][16];
         float big = 0.f;
-        const __nv_bfloat16* row = a.q + ((size_t)use.b * a.Hq + (size_t)use.h * a.G + g) * DH + 16 * t;
+        const __nv_bfloat16* row = a.q + ((size_t)use.b * a.Hq + (size_t)use.h * a.G + qh) * DH + 16 * t;
 #pragma unroll
         for (int c = 0; c < NG; ++c)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (g < a.G) v = __ldg(reinterpret_cast<const uint4*>(row + c * kP4Group) + e);
+                if (qh < a.G) v = __ldg(reinterpret_cast<const uint4*>(row + c * kP4Group) + e);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -317,13 +317,13 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         }
         // (a query of infinity has no finite form)
         const float up = big < INFINITY ? __uint_as_float((uint32_t)(127 + e) << 23) * 16777216.f * sl2 : __uint_as_float(0x7fc00000u);
-        const int from = 2 * t * 4;
-        qscale = make_float2(__shfl_sync(0xffffffffu, up, from), __shfl_sync(0xffffffffu, up, from + 4));
+        const int at = ch * 4;  // the lane that holds it as a row
+        qscale = make_float2(__shfl_sync(0xffffffffu, up, at), __shfl_sync(0xffffffffu, up, at + 4));
 #pragma unroll
         for (int c = 0; c < NG; ++c)
-            qs[c] = make_float2(__shfl_sync(0xffffffffu, sums[c], from), __shfl_sync(0xffffffffu, sums[c], from + 4));
+            qs[c] = make_float2(__shfl_sync(0xffffffffu, sums[c], at), __shfl_sync(0xffffffffu, sums[c], at + 4));
     };
-    // the sums of this warp's piece at scale m: dims c * 64 + 8 g + (0..7) of head 2t + e
+    // the sums of this warp's piece at scale m: dims c * 64 + 8 g + (0..7) of head ch + e
     auto piece = [&](int c, int e, float (&v)[8]) {
         const float unit = 16777216.f / (e ? nu.y : nu.x), add = e ? z[c].y : z[c].x;
 #pragma unroll
@@ -333,9 +333,9 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             v[4 + i] = fmaf(o[c][i][2 + e], u, add);
         }
     };
-    auto total = [&]() {  // l and z over the keys that other lanes took
+    auto total = [&]() {  // sums over the keys that other lanes took
 #pragma unroll
-        for (int s = 4; s < 32; s <<= 1) {
+        for (int s = PAIR ? 2 : 4; s < 32; s <<= 1) {
             l.x += __shfl_xor_sync(0xffffffffu, l.x, s);
             l.y += __shfl_xor_sync(0xffffffffu, l.y, s);
 #pragma unroll
@@ -344,31 +344,44 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 z[c].y += __shfl_xor_sync(0xffffffffu, z[c].y, s);
             }
         }
+        if constexpr (PAIR) {
+#pragma unroll
+            for (int c = 0; c < NG; ++c)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[c][q][e] += __shfl_xor_sync(0xffffffffu, o[c][q][e], 2);
+        }
     };
+    // (PAIR: lanes t and t + 2 hold the same sums; each stores one of the two groups of dims)
+    auto stores = [&](int c) { return !PAIR || c == t >> 1; };
     auto leave = [&](float* rec) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int h = 2 * t + e;
+            const int h = ch + e;
             if (h >= a.G) continue;
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
+                if (!stores(c)) continue;
                 float v[8];
                 piece(c, e, v);
                 float4* dst = reinterpret_cast<float4*>(rec + h * PITCH + c * kP4Group + 8 * g);
                 dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
-            if (g == 0) *reinterpret_cast<float2*>(rec + h * PITCH + DH) = e ? make_float2(m.y, l.y) : make_float2(m.x, l.x);
+            if (g == 0 && stores(0))
+                *reinterpret_cast<float2*>(rec + h * PITCH + DH) = e ? make_float2(m.y, l.y) : make_float2(m.x, l.x);
         }
     };
     auto write_out = [&]() {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int h = 2 * t + e;
+            const int h = ch + e;
             if (h >= a.G) continue;
             const float inv = 1.f / (e ? l.y : l.x);
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
+                if (!stores(c)) continue;
                 float v[8];
                 piece(c, e, v);
                 *reinterpret_cast<uint4*>(a.out + ((size_t)use.b * a.Hq + (size_t)use.h * a.G + h) * DH + c * kP4Group + 8 * g) =
@@ -377,21 +390,26 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             }
         }
     };
-    auto sides = [&](uint32_t at, uint32_t (&sd)[2][NG]) {  // scales and minima of this lane's two keys of a tile
+    auto sides = [](const uint8_t* at, uint32_t (&sd)[2][NG]) {  // scales and minima of this lane's two keys of a tile
         if constexpr (NG == 2) {
-            const uint2 s0 = lds64(at), s1 = lds64(at + 8 * NG * 4);
+            const uint2 s0 = *reinterpret_cast<const uint2*>(at), s1 = *reinterpret_cast<const uint2*>(at + 8 * NG * 4);
             sd[0][0] = s0.x;
             sd[0][1] = s0.y;
             sd[1][0] = s1.x;
             sd[1][1] = s1.y;
         } else {
-            sd[0][0] = lds32(at);
-            sd[1][0] = lds32(at + 8 * NG * 4);
+            sd[0][0] = *reinterpret_cast<const uint32_t*>(at);
+            sd[1][0] = *reinterpret_cast<const uint32_t*>(at + 8 * NG * 4);
         }
     };
+    // Scores and weights of a unit: sets of two rows by two columns. PAIR: one, of tile t >> 1 of the unit; otherwise a set a tile.
+    constexpr int SETS = PAIR ? 1 : P4_TILES;
     float* my_recs = a.recs + (size_t)gw * 2 * a.G * PITCH;
     const int swap = (g & 4) | (g & 1) << 1 | (g >> 1 & 1);  // row g of a tile is key swap (and row g + 8 key swap + 8):
     const int vkey = (2 * t & 4) | (t & 1);                  // the keys of rows 2t, which one load of V takes, are 0, 1, 4, 5
+    const int tile_l = PAIR ? t >> 1 : 0, key_l = tile_l * 16 + swap;
+    const int side_l = tile_l * (side_at(1) - side_at(0)) + swap * (NG * 4), kcode_l = swap * (DH / 2) + 8 * t;
+    const int vcode_l = vkey * (DH / 2) + 4 * g;
     bool ok = true, fresh = true;
     int slot = 0, phase = 0;
     reset();
@@ -399,68 +417,75 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     while (use.left > 0) {
         if (fresh) load_q();
         if (!__all_sync(0xffffffffu, mbar_wait_suspend(&full[slot], phase, abort_flag))) { ok = false; break; }
-        const uint32_t ka = ring_a + slot * Ly::SLOT, va = ka + Ly::HALF;
+        uint8_t* ka = p4_rings + warp * Ly::RING + slot * Ly::SLOT;
+        uint8_t* va = ka + Ly::HALF;
         const int valid = use.keys - use.u * P4_UNIT;  // keys of the unit; 32 or more: all
         if (valid < P4_UNIT) {
             // what stands behind the last key may be anything: its scales and minima become 0 (0 * NaN must not reach O)
             for (int e = lane; e < (P4_UNIT - valid) * NG; e += 32) {
                 const int key = valid + e / NG, tile = key >> 4;
-                sts32(va + side_at(0) + tile * (side_at(1) - side_at(0)) + (key & 15) * (NG * 4) + e % NG * 4, 0u);
+                *reinterpret_cast<uint32_t*>(va + side_at(0) + tile * (side_at(1) - side_at(0)) + (key & 15) * (NG * 4) + e % NG * 4) = 0u;
             }
             fence_proxy_async_smem();  // (the slot's next copy comes after these stores)
             __syncwarp();
         }
-        float2 x[P4_TILES][2];  // [tile][row g, row g + 8]: heads 2t, 2t + 1
+        float acc[P4_TILES][NG][4];
 #pragma unroll
         for (int k = 0; k < P4_TILES; ++k) {
-            const uint32_t codes = ka + tile_at(k) + swap * (DH / 2) + 8 * t;
-            float acc[NG][4];
-            uint32_t sd[2][NG];
-            sides(ka + side_at(k) + swap * (NG * 4), sd);
+            const uint8_t* codes = ka + tile_at(k) + kcode_l;
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
-                const uint2 w0 = lds64(codes + c * 32), w1 = lds64(codes + 8 * (DH / 2) + c * 32);
+                const uint2 w0 = *reinterpret_cast<const uint2*>(codes + c * 32);
+                const uint2 w1 = *reinterpret_cast<const uint2*>(codes + 8 * (DH / 2) + c * 32);
                 const uint32_t a0[2] = {w0.x, w0.y}, a1[2] = {w1.x, w1.y};
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     const uint32_t y0 = a0[w] >> 8, y1 = a1[w] >> 8;
                     if (w == 0)
-                        mma_f16_first(acc[c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
+                        mma_f16_first(acc[k][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
                                       a1[w] & 0x00f000f0u, qf[c][w][0][0], qf[c][w][0][1]);
                     else
-                        mma_f16(acc[c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u, a1[w] & 0x00f000f0u,
+                        mma_f16(acc[k][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u, a1[w] & 0x00f000f0u,
                                 qf[c][w][0][0], qf[c][w][0][1]);
-                    mma_f16(acc[c], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
+                    mma_f16(acc[k][c], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
                             qf[c][w][1][0], qf[c][w][1][1]);
                 }
             }
+        }
+        float2 x[SETS][2];  // [set][row g, row g + 8]: heads ch, ch + 1
+#pragma unroll
+        for (int k = 0; k < SETS; ++k) {
+            uint32_t sd[2][NG];
+            sides(ka + side_at(k) + side_l, sd);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                 for (int c = 0; c < NG; ++c) {
                     const float sc = bf16_lo(sd[r][c]), lo = bf16_hi(sd[r][c]);
-                    s0 = fmaf(sc, acc[c][2 * r], c == 0 ? lo * qs[c].x : fmaf(lo, qs[c].x, s0));
-                    s1 = fmaf(sc, acc[c][2 * r + 1], c == 0 ? lo * qs[c].y : fmaf(lo, qs[c].y, s1));
+                    const float a0 = PAIR && tile_l ? acc[1][c][2 * r] : acc[k][c][2 * r];
+                    const float a1 = PAIR && tile_l ? acc[1][c][2 * r + 1] : acc[k][c][2 * r + 1];
+                    s0 = fmaf(sc, a0, c == 0 ? lo * qs[c].x : fmaf(lo, qs[c].x, s0));
+                    s1 = fmaf(sc, a1, c == 0 ? lo * qs[c].y : fmaf(lo, qs[c].y, s1));
                 }
                 x[k][r] = make_float2(s0 * qscale.x, s1 * qscale.y);
             }
         }
         if (valid < P4_UNIT) {
 #pragma unroll
-            for (int k = 0; k < P4_TILES; ++k)
+            for (int k = 0; k < SETS; ++k)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    if (k * 16 + swap + 8 * r >= valid) x[k][r] = make_float2(-INFINITY, -INFINITY);
+                    if (k * 16 + key_l + 8 * r >= valid) x[k][r] = make_float2(-INFINITY, -INFINITY);
         }
-        float2 mx = make_float2(fmax3(fmaxf(x[0][0].x, x[0][1].x), x[1][0].x, x[1][1].x),
-                                fmax3(fmaxf(x[0][0].y, x[0][1].y), x[1][0].y, x[1][1].y));
+        float2 mx = make_float2(fmaxf(x[0][0].x, x[0][1].x), fmaxf(x[0][0].y, x[0][1].y));
+        if constexpr (!PAIR) mx = make_float2(fmax3(mx.x, x[SETS - 1][0].x, x[SETS - 1][1].x), fmax3(mx.y, x[SETS - 1][0].y, x[SETS - 1][1].y));
         // O and the sums move to a larger maximum only when it grew by more than 8 (P <= 2^8)
         const bool moved = __any_sync(0xffffffffu, mx.x > m.x + 8.f || mx.y > m.y + 8.f);
         float2 shrink = make_float2(1.f, 1.f);  // (O follows below)
         if (moved) {
 #pragma unroll
-            for (int s = 4; s < 32; s <<= 1) {
+            for (int s = PAIR ? 2 : 4; s < 32; s <<= 1) {
                 mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, s));
                 mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, s));
             }
@@ -478,12 +503,12 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         }
         const float2 nm = make_float2(m.x == -INFINITY ? 0.f : -m.x, m.y == -INFINITY ? 0.f : -m.y);
         // weights of V by group of dims: p * scale, and the sums of p * minimum
-        float2 wt[P4_TILES][NG][2];
+        float2 wt[SETS][NG][2];
         float2 top = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < P4_TILES; ++k) {
+        for (int k = 0; k < SETS; ++k) {
             uint32_t sd[2][NG];
-            sides(va + side_at(k) + swap * (NG * 4), sd);
+            sides(va + side_at(k) + side_l, sd);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const float2 p = make_float2(ex2_approx(x[k][r].x + nm.x), ex2_approx(x[k][r].y + nm.y));
@@ -503,7 +528,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         }
         if (moved || __any_sync(0xffffffffu, top.x * nu.x > 32768.f || top.y * nu.y > 32768.f)) {
 #pragma unroll
-            for (int s = 4; s < 32; s <<= 1) {
+            for (int s = PAIR ? 2 : 4; s < 32; s <<= 1) {
                 top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, s));
                 top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, s));
             }
@@ -526,17 +551,28 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                     o[c][q][3] *= f.y;
                 }
         }
+        uint32_t wb[SETS][NG][2];  // P^T fragments
+#pragma unroll
+        for (int k = 0; k < SETS; ++k)
+#pragma unroll
+            for (int c = 0; c < NG; ++c)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 w = mul2(wt[k][c][r], nu);
+                    wb[k][c][r] = transpose8x8(pack_f16(w.x, w.y));
+                }
 #pragma unroll
         for (int k = 0; k < P4_TILES; ++k) {
-            const uint32_t codes = va + tile_at(k) + vkey * (DH / 2) + 4 * g;
+            const uint8_t* codes = va + tile_at(k) + vcode_l;
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
-                const float2 w0 = mul2(wt[k][c][0], nu), w1 = mul2(wt[k][c][1], nu);
-                const uint32_t b0 = transpose8x8(pack_f16(w0.x, w0.y)), b1 = transpose8x8(pack_f16(w1.x, w1.y));
+                // PAIR: columns g < 4 take the first tile's weights, the others the second's
+                const uint32_t b0 = PAIR ? ((g >> 2) == k ? wb[0][c][0] : 0u) : wb[SETS == 1 ? 0 : k][c][0];
+                const uint32_t b1 = PAIR ? ((g >> 2) == k ? wb[0][c][1] : 0u) : wb[SETS == 1 ? 0 : k][c][1];
                 // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further: the first and the last four nibbles
-                const uint32_t wa = lds32(codes + c * 32), wb = lds32(codes + c * 32 + 2 * (DH / 2));
-                const uint32_t wc = lds32(codes + c * 32 + 8 * (DH / 2)), wd = lds32(codes + c * 32 + 10 * (DH / 2));
-                uint32_t v[4] = {__byte_perm(wa, wb, 0x5410), __byte_perm(wa, wb, 0x7632), __byte_perm(wc, wd, 0x5410),
+                auto word = [&](int key) { return *reinterpret_cast<const uint32_t*>(codes + c * 32 + key * (DH / 2)); };
+                const uint32_t wa = word(0), wb2 = word(2), wc = word(8), wd = word(10);
+                uint32_t v[4] = {__byte_perm(wa, wb2, 0x5410), __byte_perm(wa, wb2, 0x7632), __byte_perm(wc, wd, 0x5410),
                                  __byte_perm(wc, wd, 0x7632)};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -721,17 +757,17 @@ __global__ void __launch_bounds__(P4_JOIN_THREADS)
 
 int p4_ctas() { return device_sm_count() * P4_CTAS; }
 
-template <int DH, int BT>
-cudaError_t paged4_launch_bt(const P4Args& a, cudaStream_t st) {
+template <int DH, int BT, bool PAIR>
+cudaError_t paged4_launch_one(const P4Args& a, cudaStream_t st) {
     const int ctas = p4_ctas();
-    cudaError_t e = launch_pdl(attn_paged4_kernel<DH, BT>, dim3(ctas), dim3(P4_THREADS), P4Layout<DH>::SMEM, st, a);
+    cudaError_t e = launch_pdl(attn_paged4_kernel<DH, BT, PAIR>, dim3(ctas), dim3(P4_THREADS), P4Layout<DH>::SMEM, st, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(attn_paged4_join_kernel<DH>, dim3(ctas), dim3(P4_JOIN_THREADS), 0, st, a);
 }
 template <int DH>
 cudaError_t paged4_launch_dh(const P4Args& a, int page, cudaStream_t st) {
-    if (page == 16) return paged4_launch_bt<DH, 1>(a, st);
-    return paged4_launch_bt<DH, 2>(a, st);
+    if (a.G <= 4) return page == 16 ? paged4_launch_one<DH, 1, true>(a, st) : paged4_launch_one<DH, 2, true>(a, st);
+    return page == 16 ? paged4_launch_one<DH, 1, false>(a, st) : paged4_launch_one<DH, 2, false>(a, st);
 }
 
 size_t desc_bytes() { return ((size_t)p4_ctas() * sizeof(P4Desc) + 255) / 256 * 256; }
@@ -765,11 +801,13 @@ cudaError_t attn_decode_paged4_launch(const __nv_bfloat16* q, const void* k_page
 }
 
 cudaError_t attention_paged4_prepare() {
-    const void* fns[] = {(const void*)attn_paged4_kernel<128, 1>, (const void*)attn_paged4_kernel<128, 2>,
-                         (const void*)attn_paged4_kernel<64, 1>, (const void*)attn_paged4_kernel<64, 2>};
-    for (int i = 0; i < 4; ++i) {
+    const void* fns[] = {(const void*)attn_paged4_kernel<128, 1, false>, (const void*)attn_paged4_kernel<128, 2, false>,
+                         (const void*)attn_paged4_kernel<128, 1, true>,  (const void*)attn_paged4_kernel<128, 2, true>,
+                         (const void*)attn_paged4_kernel<64, 1, false>,  (const void*)attn_paged4_kernel<64, 2, false>,
+                         (const void*)attn_paged4_kernel<64, 1, true>,   (const void*)attn_paged4_kernel<64, 2, true>};
+    for (int i = 0; i < 8; ++i) {
         cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             i < 2 ? P4Layout<128>::SMEM : P4Layout<64>::SMEM);
+                                             i < 4 ? P4Layout<128>::SMEM : P4Layout<64>::SMEM);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
