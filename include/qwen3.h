@@ -437,8 +437,8 @@ QWEN3_API int qwen3_op_read_paged4(const void* d_k_pages, const void* d_v_pages,
 /* Decode attention over the paged cache, one query per (sequence, query head): out = softmax(q k^T * dh^-0.5) V over the slots
  * 0 .. d_len0[b] of sequence b (the query's own slot, appended before), each sequence at its own length, kv head
  * h / (Hq/Hkv). A negative length gives zeros, one past the page table's reach counts as the last slot. q [B, Hq, dh], out
- * [B, Hq*dh] bf16; Hq / Hkv at most 8, B at most 65535; the table's reach at most 2^30 slots, and B times its 32-slot units
- * below 2^31. Slots behind a length may hold anything. d_work: qwen3_attention_decode_paged4_workspace() bytes (of the current
+ * [B, Hq*dh] bf16; Hq / Hkv at most 8, B at most 65535; the table's reach at most 2^30 slots, and B * Hkv times its
+ * 32-slot units below 2^31. Slots behind a length may hold anything. d_work: qwen3_attention_decode_paged4_workspace() bytes (of the current
  * device; work_bytes is its size, a smaller one is refused), 16-byte aligned, any contents on entry; calls that share one must
  * not overlap on the GPU. Scores, sums and softmax statistics are fp32; the cached codes are used as they are, and
  * probabilities times scales are rounded to bf16 for the product with the codes. |q| up to 2^90, and values as for

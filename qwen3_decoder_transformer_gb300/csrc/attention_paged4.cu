@@ -32,7 +32,7 @@ namespace {
 // attn_paged4_join_kernel, in the order of their keys: the result does not depend on timing.
 constexpr int P4_UNIT = 32, P4_TILES = P4_UNIT / 16;
 constexpr int P4_WARPS = 8, P4_THREADS = 32 * P4_WARPS, P4_CTAS = 2, P4_MAX_G = 8;
-constexpr int P4_STRIPS = P4_THREADS;  // strips of sequences whose units are counted at the start
+constexpr int P4_STRIPS = 256;  // strips of sequences whose units are counted at the start
 template <int DH>
 struct P4Layout {
     static constexpr int NG = DH / kP4Group;
@@ -86,6 +86,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
+__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -125,7 +130,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     constexpr int NG = Ly::NG, NS = Ly::NS, SLOT = Ly::SLOT, PITCH = Ly::PITCH;
     extern __shared__ __align__(128) uint8_t p4_rings[];
     __shared__ uint64_t bars[P4_WARPS][NS];
-    __shared__ int strip_end[P4_STRIPS];  // units of one kv head up to the strip's end
+    __shared__ int strip_end[P4_STRIPS];   // units of one kv head up to the strip's end
+    __shared__ int strip_keys[P4_STRIPS];  // keys of the strip's (last) sequence
     __shared__ int warp_sum[P4_WARPS];
     __shared__ int seg_sh[P4_WARPS], whole_sh[P4_WARPS];
     __shared__ int abort_sh;
@@ -141,12 +147,18 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     pdl_wait();
     pdl_trigger();
 
-    // ---------------- this warp's run of units [x0, x1)
+    // ---------------- this warp's run of units [x0, x0 + mine)
     const int per = (a.B + P4_STRIPS - 1) / P4_STRIPS;
     {
-        int sum = 0;
-        const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
-        for (int b = b0; b < b1; ++b) sum += p4_units(p4_keys(a, b));
+        int sum = 0, keys = 0;
+        const int b0 = threadIdx.x * per, b1 = threadIdx.x < P4_STRIPS ? min(a.B, b0 + per) : 0;
+        for (int b = b0; b < b1; ++b) {
+            keys = p4_keys(a, b);
+            sum += p4_units(keys);
+            if (keys == 0 && b % gridDim.x == blockIdx.x)  // a sequence without keys
+                for (int e = 0; e < a.Hq * DH / 8; ++e)
+                    reinterpret_cast<uint4*>(a.out + (size_t)b * a.Hq * DH)[e] = make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, sum, o);
@@ -154,45 +166,47 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         }
         if (lane == 31) warp_sum[warp] = sum;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) sum += warp_sum[w];
-        strip_end[threadIdx.x] = sum;
+#pragma unroll
+        for (int w = 0; w < P4_WARPS; ++w) sum += w < warp ? warp_sum[w] : 0;
+        if (threadIdx.x < P4_STRIPS) {
+            strip_end[threadIdx.x] = sum;
+            strip_keys[threadIdx.x] = keys;
+        }
         __syncthreads();
     }
-    const long long units = (long long)strip_end[P4_STRIPS - 1] * a.Hkv;
+    static_assert(P4_THREADS >= P4_STRIPS, "a thread a strip");
+    const int units = strip_end[P4_STRIPS - 1] * a.Hkv;  // (fewer than 2^31: checked on the host)
     const int gw = blockIdx.x * P4_WARPS + warp;
-    // a unit a warp at least: no run between two others is empty
-    const long long all = (long long)gridDim.x * P4_WARPS, warps = min(all, units);
-    auto run_begin = [&](long long w) { return warps ? units * w / warps : 0; };
-    const long long x0 = gw < warps ? run_begin(gw) : units, x1 = gw < warps ? run_begin(gw + 1) : units;
-    const int mine = (int)(x1 - x0);
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)  // sequences without keys
-        if (p4_keys(a, b) == 0)
-            for (int e = threadIdx.x; e < a.Hq * DH / 8; e += P4_THREADS)
-                reinterpret_cast<uint4*>(a.out + (size_t)b * a.Hq * DH)[e] = make_uint4(0, 0, 0, 0);
+    // as many warps as there are places, but a unit a warp at least (no run between two others is empty); the first `more`
+    // runs are a unit longer
+    const int warps = min((int)gridDim.x * P4_WARPS, units), len = warps ? units / warps : 0, more = units - len * warps;
+    const int x0 = gw * len + min(gw, more), mine = gw < warps ? len + (gw < more ? 1 : 0) : 0;
 
     P4Cursor use{0, 0, 0, 1, 1, mine};
-    long long seg_begin = x0;  // of the list, where the current (sequence, kv head) begins
+    bool inside = true;  // the current (sequence, kv head) begins in this run
     if (mine > 0) {
         // the strip, then the sequence, that holds unit x0: sequence b's units are [Hkv P_b, Hkv P_(b+1))
+        const int y0 = x0 / a.Hkv;  // (P_b <= y0 < P_(b+1))
         int lo = 0, hi = P4_STRIPS - 1;
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
-            if ((long long)strip_end[mid] * a.Hkv > x0) hi = mid;
+            if (strip_end[mid] > y0) hi = mid;
             else lo = mid + 1;
         }
-        long long p = lo > 0 ? strip_end[lo - 1] : 0;
+        int p = lo > 0 ? strip_end[lo - 1] : 0;
         use.b = lo * per;
-        while (true) {
+        use.keys = strip_keys[lo];
+        while (per > 1) {
             use.keys = p4_keys(a, use.b);
-            use.n = p4_units(use.keys);
-            if ((p + use.n) * a.Hkv > x0) break;
-            p += use.n;
+            if (p + p4_units(use.keys) > y0) break;
+            p += p4_units(use.keys);
             ++use.b;
         }
-        const long long in = x0 - p * a.Hkv;
-        use.h = (int)(in / use.n);
-        use.u = (int)(in - (long long)use.h * use.n);
-        seg_begin = x0 - use.u;
+        use.n = p4_units(use.keys);
+        const int in = x0 - p * a.Hkv;
+        use.h = in / use.n;
+        use.u = in - use.h * use.n;
+        inside = use.u == 0;
     }
 
     // ---------------- the ring: the run's unit i goes to slot i % NS, K in the first half of it, V in the second
@@ -202,23 +216,21 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     P4Cursor ask = use;
     int issued = 0, used = 0;
     const int page_log = a.cache.page_log, page = 1 << page_log;
-    const size_t page_bytes = p4_page_bytes(page, DH);
     const uint32_t ring_a = smem_u32(p4_rings + warp * Ly::RING);
     int tab = 0, tab_b = -1, tab_at = 0;  // this lane's entry of the page table, tab_at + lane of sequence tab_b
     bool bad_page = false;
     // Lanes 0 and 1 copy K, lanes 2 and 3 V: a page each (BT 1), or the codes and the scales and minima of a part of one.
-    const uint8_t* pages = (lane & 2 ? a.cache.v : a.cache.k) + (BT == 2 && (lane & 1) ? page * (DH / 2) : 0);
     const uint8_t* from = nullptr;
     const int unit_bytes = P4_UNIT * (lane & 1 ? NG * 4 : DH / 2);  // BT 2: from unit to unit of a page
     const uint32_t to = ring_a + (lane & 2 ? Ly::HALF : 0) + (lane & 1 ? (BT == 1 ? TILE + SIDE : P4_TILES * TILE) : 0);
     const int page_units = BT == 1 ? 1 : page / P4_UNIT;
-    bool ask_new = true;  // the unit is the first of the run or of a (sequence, kv head)
+    int same_page = 0;  // BT 2: units of the sequence in the page behind this one
     auto issue = [&](int slot) {  // the next unit, if the run has one
         if (ask.left == 0) return;
         // (the second of two pages is fetched only if the sequence reaches it)
         const int blocks = BT == 1 && ask.keys - ask.u * P4_UNIT > 16 ? 2 : 1;
         const bool copies = lane < 4 && (BT == 2 || (lane & 1) < blocks);
-        if (BT == 1 || ask_new || (ask.u & (page_units - 1)) == 0) {
+        if (BT == 1 || --same_page < 0) {
             const int first = ask.u * P4_UNIT >> page_log, at = first & ~31;
             if (tab_b != ask.b || tab_at != at) {
                 tab_b = ask.b;
@@ -230,8 +242,13 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 bad_page = bad_page || copies;
                 id = 0;
             }
-            from = pages + ((long long)id * a.Hkv + ask.h) * (long long)page_bytes;
-            if (BT == 2) from += (ask.u & (page_units - 1)) * unit_bytes;
+            from = (lane & 2 ? a.cache.v : a.cache.k) + ((long long)id * a.Hkv + ask.h) * (long long)p4_page_bytes(page, DH) +
+                   (BT == 2 && (lane & 1) ? page * (DH / 2) : 0);
+            if (BT == 2) {
+                const int at_unit = ask.u & (page_units - 1);
+                from += at_unit * unit_bytes;
+                same_page = min(page_units - at_unit, ask.n - ask.u) - 1;
+            }
         } else {
             from += unit_bytes;
         }
@@ -240,14 +257,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         if (copies)
             bulk_load(to + slot * Ly::SLOT, from, BT == 1 ? TILE + SIDE : unit_bytes, &full[slot]);
         ++issued;
-        const int n = ask.n;
-        ask_new = ask.u + 1 == n;
         p4_step(a, ask);
     };
-    __syncwarp();  // the barriers are set
-#pragma unroll 1
-    for (int i = 0; i < NS; ++i) issue(i);
-
     // ---------------- products
     const float sl2 = kLog2e / sqrtf((float)DH);
     uint32_t qf[NG][2][2][2];  // q^T fragments [group][word][part][half]: column g = query head g of the group (zero past G)
@@ -268,16 +279,23 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             for (int e = 0; e < 4; ++e) o[c][0][e] = o[c][1][e] = o[c][2][e] = o[c][3][e] = 0.f;
         }
     };
-    auto load_q = [&]() {
-        float x[NG][16];
-        float big = 0.f;
+    uint4 qraw[NG][2];
+    auto fetch_q = [&]() {
         const __nv_bfloat16* row = a.q + ((size_t)use.b * a.Hq + (size_t)use.h * a.G + qh) * DH + 16 * t;
 #pragma unroll
         for (int c = 0; c < NG; ++c)
 #pragma unroll
+            for (int e = 0; e < 2; ++e)
+                qraw[c][e] = qh < a.G ? __ldg(reinterpret_cast<const uint4*>(row + c * kP4Group) + e) : make_uint4(0, 0, 0, 0);
+    };
+    auto set_q = [&]() {
+        float x[NG][16];
+        float big = 0.f;
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+#pragma unroll
             for (int e = 0; e < 2; ++e) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (qh < a.G) v = __ldg(reinterpret_cast<const uint4*>(row + c * kP4Group) + e);
+                const uint4 v = qraw[c][e];
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -404,22 +422,29 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     };
     // Scores and weights of a unit: sets of two rows by two columns. PAIR: one, of tile t >> 1 of the unit; otherwise a set a tile.
     constexpr int SETS = PAIR ? 1 : P4_TILES;
-    float* my_recs = a.recs + (size_t)gw * 2 * a.G * PITCH;
     const int swap = (g & 4) | (g & 1) << 1 | (g >> 1 & 1);  // row g of a tile is key swap (and row g + 8 key swap + 8):
     const int vkey = (2 * t & 4) | (t & 1);                  // the keys of rows 2t, which one load of V takes, are 0, 1, 4, 5
     const int tile_l = PAIR ? t >> 1 : 0, key_l = tile_l * 16 + swap;
     const int side_l = tile_l * (side_at(1) - side_at(0)) + swap * (NG * 4), kcode_l = swap * (DH / 2) + 8 * t;
+    const uint32_t col_l[2] = {g < 4 ? 0x3c003c00u : 0u, g < 4 ? 0u : 0x3c003c00u};  // PAIR: fp16 1 where its column takes tile 0, 1
     const int vcode_l = vkey * (DH / 2) + 4 * g;
     bool ok = true, fresh = true;
-    int slot = 0, phase = 0;
+    int slot = 0, phase = 0, run_left = mine;
+    int keys_left = use.keys - use.u * P4_UNIT;  // of the (sequence, kv head), from the unit at hand on
+    use.left = 1 << 30;                          // (counted by run_left)
     reset();
+    if (mine > 0) fetch_q();
+    __syncwarp();  // the barriers are set
 #pragma unroll 1
-    while (use.left > 0) {
-        if (fresh) load_q();
+    for (int i = 0; i < NS; ++i) issue(i);
+    float* const my_smem = reinterpret_cast<float*>(p4_rings + warp * Ly::RING);
+#pragma unroll 1
+    while (run_left > 0) {
+        if (fresh) set_q();
         if (!__all_sync(0xffffffffu, mbar_wait_suspend(&full[slot], phase, abort_flag))) { ok = false; break; }
         uint8_t* ka = p4_rings + warp * Ly::RING + slot * Ly::SLOT;
         uint8_t* va = ka + Ly::HALF;
-        const int valid = use.keys - use.u * P4_UNIT;  // keys of the unit; 32 or more: all
+        const int valid = keys_left;  // keys of the unit; 32 or more: all
         if (valid < P4_UNIT) {
             // what stands behind the last key may be anything: its scales and minima become 0 (0 * NaN must not reach O)
             for (int e = lane; e < (P4_UNIT - valid) * NG; e += 32) {
@@ -463,10 +488,10 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
 #pragma unroll
                 for (int c = 0; c < NG; ++c) {
                     const float sc = bf16_lo(sd[r][c]), lo = bf16_hi(sd[r][c]);
-                    const float a0 = PAIR && tile_l ? acc[1][c][2 * r] : acc[k][c][2 * r];
-                    const float a1 = PAIR && tile_l ? acc[1][c][2 * r + 1] : acc[k][c][2 * r + 1];
-                    s0 = fmaf(sc, a0, c == 0 ? lo * qs[c].x : fmaf(lo, qs[c].x, s0));
-                    s1 = fmaf(sc, a1, c == 0 ? lo * qs[c].y : fmaf(lo, qs[c].y, s1));
+                    s0 = c == 0 ? lo * qs[c].x : fmaf(lo, qs[c].x, s0);
+                    s1 = c == 0 ? lo * qs[c].y : fmaf(lo, qs[c].y, s1);
+                    s0 = fmaf(sc, PAIR && tile_l ? acc[1][c][2 * r] : acc[k][c][2 * r], s0);
+                    s1 = fmaf(sc, PAIR && tile_l ? acc[1][c][2 * r + 1] : acc[k][c][2 * r + 1], s1);
                 }
                 x[k][r] = make_float2(s0 * qscale.x, s1 * qscale.y);
             }
@@ -567,8 +592,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
                 // PAIR: columns g < 4 take the first tile's weights, the others the second's
-                const uint32_t b0 = PAIR ? ((g >> 2) == k ? wb[0][c][0] : 0u) : wb[SETS == 1 ? 0 : k][c][0];
-                const uint32_t b1 = PAIR ? ((g >> 2) == k ? wb[0][c][1] : 0u) : wb[SETS == 1 ? 0 : k][c][1];
+                const uint32_t b0 = PAIR ? mul_f16(wb[0][c][0], col_l[k]) : wb[SETS == 1 ? 0 : k][c][0];
+                const uint32_t b1 = PAIR ? mul_f16(wb[0][c][1], col_l[k]) : wb[SETS == 1 ? 0 : k][c][1];
                 // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further: the first and the last four nibbles
                 auto word = [&](int key) { return *reinterpret_cast<const uint32_t*>(codes + c * 32 + key * (DH / 2)); };
                 const uint32_t wa = word(0), wb2 = word(2), wc = word(8), wd = word(10);
@@ -592,16 +617,21 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             slot = 0;
             phase ^= 1;
         }
-        fresh = use.u + 1 == use.n;
-        if (use.left == 1) break;  // (`use` stays at the run's last unit)
-        if (fresh) {               // the (sequence, kv head) ends within the run
-            total();
-            if (seg_begin >= x0) write_out();
-            else leave(my_recs);
-            reset();
-            seg_begin = x1 - use.left + 1;
-        }
+        keys_left -= P4_UNIT;
+        fresh = keys_left <= 0;
+        if (--run_left > 0 && !fresh) continue;
+        // the (sequence, kv head) or the run ends: written out if all of it was in this run, left as a piece otherwise (that at the
+        // end of the run in the ring, which is done)
+        total();
+        if (inside && fresh) write_out();
+        else leave(run_left == 0 ? my_smem : a.recs + (size_t)gw * 2 * a.G * PITCH);
+        if (run_left == 0) break;
+        reset();
+        inside = true;
+        use.u = use.n - 1;
         p4_step(a, use);
+        keys_left = use.keys;
+        fetch_q();
     }
     if (__any_sync(0xffffffffu, bad_page) && lane == 0 && a.err) atomicOr(a.err, ERR_INDEX);
     if (!ok) {  // give up: wait, bounded, for the copies still on their way
@@ -611,23 +641,19 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         for (int j = used; j < issued; ++j) mbar_wait_suspend(&full[j % NS], (j / NS) & 1, &never);
     }
 
-    // ---------------- the piece at the end of the run
-    const bool ends = mine > 0 && fresh;                       // the sequence ends with the run
-    const bool open = mine > 0 && !(seg_begin >= x0 && ends);  // a part of it lies in another run
-    total();
-    if (mine > 0 && !open && ok) write_out();
+    // ---------------- the pieces at the ends of this CTA's runs
+    const bool ends = fresh;                             // the (sequence, kv head) ends with the run
+    const bool open = mine > 0 && !(inside && ends);     // a part of it lies in another run
     const int seg = use.b * a.Hkv + use.h;
-    float* my_smem = reinterpret_cast<float*>(p4_rings + warp * Ly::RING);
-    if (open) leave(my_smem);  // (the ring is done)
     if (lane == 0) {
         seg_sh[warp] = open ? seg : -1;
-        whole_sh[warp] = (open && seg_begin >= x0 ? 1 : 0) | (open && ends ? 2 : 0);  // begins, ends in this run
+        whole_sh[warp] = (open && inside ? 1 : 0) | (open && ends ? 2 : 0);  // begins, ends in this run
     }
     __syncthreads();
     // Join the pieces at the ends of this CTA's runs: those of neighbouring warps that belong to one (sequence, kv head), and, where
     // it ends as the first piece of the next warp's run, that warp's record. Quads of dims of the group that begins at warp w0:
     const int G = a.G, quads = G * (DH / 4);
-    const int cta0 = blockIdx.x * P4_WARPS, here = (int)max(0LL, min((long long)P4_WARPS, warps - cta0));  // warps with a run
+    const int cta0 = blockIdx.x * P4_WARPS, here = max(0, min(P4_WARPS, warps - cta0));  // warps with a run
     for (int e0 = threadIdx.x; e0 < P4_WARPS * quads; e0 += P4_THREADS) {
         const int w0 = e0 / quads, e = e0 - w0 * quads, s = seg_sh[w0];
         if (s < 0 || (w0 > 0 && seg_sh[w0 - 1] == s)) continue;
@@ -677,11 +703,12 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             int w0 = P4_WARPS - 1;
             while (w0 > 0 && seg_sh[w0 - 1] == s) --w0;
             if (whole_sh[w0] & 1) {
-                const long long end = seg_begin + use.n;  // (this warp is in it)
+                // the unit behind it, the warp whose run holds the one before, and whether that run goes on
+                const int end = x0 + mine + p4_units(max(keys_left, 0)), longer = more * (len + 1);
                 d.seg = s;
                 d.first = cta0 + w0;
-                d.last = (int)((end * warps - 1) / units);
-                d.last_slot = run_begin(d.last + 1) == end ? 1 : 0;
+                d.last = end <= longer ? (end - 1) / (len + 1) : more + (end - 1 - longer) / len;
+                d.last_slot = (d.last + 1) * len + min(d.last + 1, more) == end ? 1 : 0;
             }
         }
         a.desc[blockIdx.x] = d;
