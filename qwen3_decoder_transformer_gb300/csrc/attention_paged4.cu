@@ -30,15 +30,15 @@ namespace {
 // A (sequence, kv head) within one run is written out at once. Of one that is cut, each warp leaves a piece (sums,
 // maximum, sum of weights); pieces of one CTA are joined in shared memory, the others in the workspace by
 // attn_paged4_join_kernel, in the order of their keys: the result does not depend on timing.
-constexpr int P4_UNIT = 32, P4_TILES = P4_UNIT / 16;
-constexpr int P4_WARPS = 8, P4_THREADS = 32 * P4_WARPS, P4_CTAS = 2, P4_MAX_G = 8;
-constexpr int P4_STRIPS = 256;  // strips of sequences whose units are counted at the start
+constexpr int P4_STEP = 64, P4_TILES = P4_STEP / 16;  // keys that a warp takes at once
+constexpr int P4_WARPS = 6, P4_THREADS = 32 * P4_WARPS, P4_CTAS = 2, P4_MAX_G = 8;
+constexpr int P4_STRIPS = P4_THREADS;  // strips of sequences whose units are counted at the start
 template <int DH>
 struct P4Layout {
     static constexpr int NG = DH / kP4Group;
-    static constexpr int HALF = P4_UNIT * p4_token_bytes(DH);  // bytes of K (or V) of a unit
+    static constexpr int HALF = P4_STEP * p4_token_bytes(DH);  // bytes of K (or V) of a step
     static constexpr int SLOT = 2 * HALF;
-    static constexpr int NS = 3 * 128 / DH;  // slots of a ring
+    static constexpr int NS = 2 * 128 / DH;  // slots of a ring
     static constexpr int RING = NS * SLOT;
     static constexpr int PITCH = DH + 4;  // floats of a head's piece: sums, maximum, sum of weights
     static constexpr int SMEM = P4_WARPS * RING;
@@ -101,38 +101,39 @@ __device__ __forceinline__ int p4_keys(const P4Args& a, int b) {
     const int n = __ldg(a.len0 + b);
     return n < 0 ? 0 : n >= a.cap ? a.cap : n + 1;
 }
-__device__ __forceinline__ int p4_units(int keys) { return (keys + P4_UNIT - 1) / P4_UNIT; }
 
-// A place in the list of units: unit u of n of (sequence b, kv head h), `left` units before the end of the run.
+// A place in the list of units: unit u of n of (sequence b, kv head h).
 struct P4Cursor {
-    int b, h, u, n, keys, left;
+    int b, h, u, n, keys;
 };
-__device__ __forceinline__ void p4_step(const P4Args& a, P4Cursor& c) {
-    --c.left;
-    if (++c.u < c.n || c.left == 0) return;
+// To the next (sequence, kv head); there is one. ulog: log2 of a unit's keys.
+__device__ __forceinline__ void p4_next(const P4Args& a, P4Cursor& c, int ulog) {
     c.u = 0;
     if (++c.h < a.Hkv) return;
     c.h = 0;
-    do {  // (sequences without keys have no units; the run is within the list)
+    do {  // (sequences without keys have no units)
         c.keys = p4_keys(a, ++c.b);
     } while (c.keys == 0);
-    c.n = p4_units(c.keys);
+    c.n = (c.keys + (1 << ulog) - 1) >> ulog;
 }
 
-// BT: 16-key tiles of a page that a unit takes (1: two pages of 16 tokens; 2: a page of 32 or a part of a larger one).
-// PAIR, for groups of up to four query heads: the 8 columns hold the heads twice. Of the scores of a unit's two tiles, columns
-// 0-3 keep the first tile's and columns 4-7 the second's, so that no lane works on a column without a head, and O's
-// two halves are added at the end (64 sequences of up to 4096 keys, two heads a group: 56 us -> see below).
-template <int DH, int BT, bool PAIR>
+// BT: 16-key tiles of a page that a step takes (1, 2: pages of 16 and 32 tokens, fetched whole; 4: a part of a larger page).
+// HC: columns of a product that the heads of a group take (the least power of two that holds them, 2 at least). With fewer than 8
+// the columns hold the heads 8 / HC times, and of the scores of 8 / HC tiles each tile keeps its own columns: no lane
+// works on the softmax of a column without a head, and O's column sets are added at the end.
+template <int DH, int BT, int HC>
 __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     attn_paged4_kernel(const P4Args a) {
     using Ly = P4Layout<DH>;
-    constexpr int NG = Ly::NG, NS = Ly::NS, SLOT = Ly::SLOT, PITCH = Ly::PITCH;
+    constexpr int NG = Ly::NG, NS = Ly::NS, PITCH = Ly::PITCH;
+    constexpr int SHARE = 8 / HC;            // tiles whose scores share the columns
+    constexpr int SETS = P4_TILES / SHARE;   // sets of scores of a step: two rows by two columns a lane
+    constexpr int LANES = HC / 2;            // lanes t that hold the columns of one tile
     extern __shared__ __align__(128) uint8_t p4_rings[];
     __shared__ uint64_t bars[P4_WARPS][NS];
     __shared__ int strip_end[P4_STRIPS];   // units of one kv head up to the strip's end
     __shared__ int strip_keys[P4_STRIPS];  // keys of the strip's (last) sequence
-    __shared__ int warp_sum[P4_WARPS];
+    __shared__ int2 warp_sum[P4_WARPS];
     __shared__ int seg_sh[P4_WARPS], whole_sh[P4_WARPS];
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
@@ -147,42 +148,53 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     pdl_wait();
     pdl_trigger();
 
-    // ---------------- this warp's run of units [x0, x0 + mine)
-    const int per = (a.B + P4_STRIPS - 1) / P4_STRIPS;
+    // ---------------- this warp's run of units [x0, x0 + mine): units of 64 keys, or of 32 where there are few of them
+    const int per = (a.B + P4_STRIPS - 1) / P4_STRIPS, places = (int)gridDim.x * P4_WARPS;
+    int ulog;
     {
-        int sum = 0, keys = 0;
-        const int b0 = threadIdx.x * per, b1 = threadIdx.x < P4_STRIPS ? min(a.B, b0 + per) : 0;
+        int n32 = 0, n64 = 0, keys = 0;
+        const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
         for (int b = b0; b < b1; ++b) {
             keys = p4_keys(a, b);
-            sum += p4_units(keys);
+            n32 += (keys + 31) >> 5;
+            n64 += (keys + 63) >> 6;
             if (keys == 0 && b % gridDim.x == blockIdx.x)  // a sequence without keys
                 for (int e = 0; e < a.Hq * DH / 8; ++e)
                     reinterpret_cast<uint4*>(a.out + (size_t)b * a.Hq * DH)[e] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
+            const int v = __shfl_up_sync(0xffffffffu, n32, o), w = __shfl_up_sync(0xffffffffu, n64, o);
+            if (lane >= o) {
+                n32 += v;
+                n64 += w;
+            }
         }
-        if (lane == 31) warp_sum[warp] = sum;
+        if (lane == 31) warp_sum[warp] = make_int2(n32, n64);
         __syncthreads();
+        int all = 0;
 #pragma unroll
-        for (int w = 0; w < P4_WARPS; ++w) sum += w < warp ? warp_sum[w] : 0;
-        if (threadIdx.x < P4_STRIPS) {
-            strip_end[threadIdx.x] = sum;
-            strip_keys[threadIdx.x] = keys;
+        for (int w = 0; w < P4_WARPS; ++w) {
+            const int2 v = warp_sum[w];
+            all += v.x;
+            if (w < warp) {
+                n32 += v.x;
+                n64 += v.y;
+            }
         }
+        ulog = all <= 2 * places / a.Hkv ? 5 : 6;
+        strip_end[threadIdx.x] = ulog == 5 ? n32 : n64;
+        strip_keys[threadIdx.x] = keys;
         __syncthreads();
     }
-    static_assert(P4_THREADS >= P4_STRIPS, "a thread a strip");
     const int units = strip_end[P4_STRIPS - 1] * a.Hkv;  // (fewer than 2^31: checked on the host)
     const int gw = blockIdx.x * P4_WARPS + warp;
     // as many warps as there are places, but a unit a warp at least (no run between two others is empty); the first `more`
     // runs are a unit longer
-    const int warps = min((int)gridDim.x * P4_WARPS, units), len = warps ? units / warps : 0, more = units - len * warps;
+    const int warps = min(places, units), len = warps ? units / warps : 0, more = units - len * warps;
     const int x0 = gw * len + min(gw, more), mine = gw < warps ? len + (gw < more ? 1 : 0) : 0;
 
-    P4Cursor use{0, 0, 0, 1, 1, mine};
+    P4Cursor use{0, 0, 0, 1, 1};
     bool inside = true;  // the current (sequence, kv head) begins in this run
     if (mine > 0) {
         // the strip, then the sequence, that holds unit x0: sequence b's units are [Hkv P_b, Hkv P_(b+1))
@@ -196,13 +208,13 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         int p = lo > 0 ? strip_end[lo - 1] : 0;
         use.b = lo * per;
         use.keys = strip_keys[lo];
-        while (per > 1) {
-            use.keys = p4_keys(a, use.b);
-            if (p + p4_units(use.keys) > y0) break;
-            p += p4_units(use.keys);
+        while (true) {
+            if (per > 1) use.keys = p4_keys(a, use.b);
+            use.n = (use.keys + (1 << ulog) - 1) >> ulog;
+            if (per == 1 || p + use.n > y0) break;
+            p += use.n;
             ++use.b;
         }
-        use.n = p4_units(use.keys);
         const int in = x0 - p * a.Hkv;
         use.h = in / use.n;
         use.u = in - use.h * use.n;
@@ -211,75 +223,71 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
 
     // ---------------- the ring: the run's unit i goes to slot i % NS, K in the first half of it, V in the second
     constexpr int TILE = 16 * DH / 2, SIDE = 16 * NG * 4;  // codes, and scales and minima, of 16 keys
-    auto tile_at = [](int i) { return BT == 1 ? i * (TILE + SIDE) : i * TILE; };  // tile i in its half
-    auto side_at = [](int i) { return BT == 1 ? i * (TILE + SIDE) + TILE : P4_TILES * TILE + i * SIDE; };
+    auto tile_at = [](int i) { return i / BT * BT * (TILE + SIDE) + i % BT * TILE; };  // tile i in its half
+    auto side_at = [](int i) { return i / BT * BT * (TILE + SIDE) + BT * TILE + i % BT * SIDE; };
+    // Lanes that copy K, then as many for V: one for each page, or (BT 4) one for the codes and one for the scales and minima.
+    constexpr int COPY = BT == 4 ? 2 : P4_TILES / BT;
+    const int page_log = a.cache.page_log;
+    const uint32_t to = smem_u32(p4_rings + warp * Ly::RING) + (lane & COPY ? Ly::HALF : 0) +
+                        (lane & (COPY - 1)) * (BT == 4 ? P4_TILES * TILE : BT * (TILE + SIDE));
     P4Cursor ask = use;
-    int issued = 0, used = 0;
-    const int page_log = a.cache.page_log, page = 1 << page_log;
-    const uint32_t ring_a = smem_u32(p4_rings + warp * Ly::RING);
+    int ask_left = mine, issued = 0;
     int tab = 0, tab_b = -1, tab_at = 0;  // this lane's entry of the page table, tab_at + lane of sequence tab_b
-    bool bad_page = false;
-    // Lanes 0 and 1 copy K, lanes 2 and 3 V: a page each (BT 1), or the codes and the scales and minima of a part of one.
     const uint8_t* from = nullptr;
-    const int unit_bytes = P4_UNIT * (lane & 1 ? NG * 4 : DH / 2);  // BT 2: from unit to unit of a page
-    const uint32_t to = ring_a + (lane & 2 ? Ly::HALF : 0) + (lane & 1 ? (BT == 1 ? TILE + SIDE : P4_TILES * TILE) : 0);
-    const int page_units = BT == 1 ? 1 : page / P4_UNIT;
-    int same_page = 0;  // BT 2: units of the sequence in the page behind this one
+    int same_page = 0;  // BT 4: units of the sequence in the page behind this one
+    bool bad_page = false;
     auto issue = [&](int slot) {  // the next unit, if the run has one
-        if (ask.left == 0) return;
-        // (the second of two pages is fetched only if the sequence reaches it)
-        const int blocks = BT == 1 && ask.keys - ask.u * P4_UNIT > 16 ? 2 : 1;
-        const bool copies = lane < 4 && (BT == 2 || (lane & 1) < blocks);
-        if (BT == 1 || --same_page < 0) {
-            const int first = ask.u * P4_UNIT >> page_log, at = first & ~31;
+        if (ask_left == 0) return;
+        const int k0 = ask.u << ulog, tiles = (min(1 << ulog, ask.keys - k0) + 15) >> 4;
+        const bool side = BT == 4 && (lane & 1);
+        // (of several pages those that the sequence reaches)
+        const bool copies = lane < 2 * COPY && (BT == 4 || (lane & (COPY - 1)) * BT < tiles);
+        if (BT < 4 || --same_page < 0) {
+            const int first = k0 >> page_log, at = first & ~31;
             if (tab_b != ask.b || tab_at != at) {
                 tab_b = ask.b;
                 tab_at = at;
                 tab = at + lane < a.cache.max_pages ? __ldg(a.cache.table + (size_t)ask.b * a.cache.max_pages + at + lane) : 0;
             }
-            int id = __shfl_sync(0xffffffffu, tab, (first & 31) + (BT == 1 ? lane & 1 : 0));
+            int id = __shfl_sync(0xffffffffu, tab, (first & 31) + (BT < 4 ? lane & (COPY - 1) : 0));
             if ((unsigned)id >= (unsigned)a.cache.n_pages) {  // (flagged; the output is invalid)
                 bad_page = bad_page || copies;
                 id = 0;
             }
-            from = (lane & 2 ? a.cache.v : a.cache.k) + ((long long)id * a.Hkv + ask.h) * (long long)p4_page_bytes(page, DH) +
-                   (BT == 2 && (lane & 1) ? page * (DH / 2) : 0);
-            if (BT == 2) {
-                const int at_unit = ask.u & (page_units - 1);
-                from += at_unit * unit_bytes;
-                same_page = min(page_units - at_unit, ask.n - ask.u) - 1;
+            from = (lane & COPY ? a.cache.v : a.cache.k) +
+                   ((long long)id * a.Hkv + ask.h) * (long long)p4_page_bytes(1 << page_log, DH);
+            if constexpr (BT == 4) {
+                const int row = k0 & ((1 << page_log) - 1);
+                from += side ? (DH / 2 << page_log) + row * (NG * 4) : row * (DH / 2);
+                same_page = min((1 << page_log) - row, ask.keys - k0) - 1 >> ulog;
             }
         } else {
-            from += unit_bytes;
+            from += (side ? NG * 4 : DH / 2) << ulog;
         }
-        if (lane == 0) mbar_expect_tx(&full[slot], BT == 1 ? blocks * 2 * (TILE + SIDE) : Ly::SLOT);
+        const int pages = BT == 4 ? 0 : (tiles + BT - 1) / BT;
+        if (lane == 0) mbar_expect_tx(&full[slot], 2 * (TILE + SIDE) * (BT == 4 ? tiles : pages * BT));
         __syncwarp();
         if (copies)
-            bulk_load(to + slot * Ly::SLOT, from, BT == 1 ? TILE + SIDE : unit_bytes, &full[slot]);
+            bulk_load(to + slot * Ly::SLOT, from, BT == 4 ? tiles * (side ? SIDE : TILE) : BT * (TILE + SIDE), &full[slot]);
         ++issued;
-        p4_step(a, ask);
-    };
-    // ---------------- products
-    const float sl2 = kLog2e / sqrtf((float)DH);
-    uint32_t qf[NG][2][2][2];  // q^T fragments [group][word][part][half]: column g = query head g of the group (zero past G)
-    float2 qs[NG], qscale;     // heads 2t and 2t + 1: sums of the scaled queries over a group of dims; what x is scaled by
-    float2 m = make_float2(-INFINITY, -INFINITY), l = make_float2(0.f, 0.f);
-    float o[NG][4][4];             // sums of codes, in units of 2^-24 / nu (tiles 1 and 3: 2^-20 / nu)
-    float2 z[NG];                  // sums of minima
-    float2 nu = make_float2(1.f, 1.f);  // the power of two on the weights of V
-    const int qh = PAIR ? g & 3 : g;         // head of this lane's column of q
-    const int ch = PAIR ? 2 * (t & 1) : 2 * t;  // head of this lane's first column of scores and outputs
-    auto reset = [&]() {
-        m = make_float2(-INFINITY, -INFINITY);
-        l = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < NG; ++c) {
-            z[c] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[c][0][e] = o[c][1][e] = o[c][2][e] = o[c][3][e] = 0.f;
+        if (--ask_left > 0 && ++ask.u == ask.n) {
+            p4_next(a, ask, ulog);
+            same_page = 0;
         }
     };
+
+    // ---------------- products
+    const int qh = g & (HC - 1);              // head of this lane's column of q
+    const int ch = 2 * (t & (LANES - 1));     // head of this lane's first column of scores and outputs
+    const int part = t / LANES;               // which of the tiles that share the columns they belong to
     uint4 qraw[NG][2];
+    uint32_t qf[NG][2][2][2];  // q^T fragments [group][word][nibbles][half]; zero past G
+    float2 qs[NG], qscale;     // heads ch, ch + 1: sums of the scaled queries over a group of dims; what scores are scaled by
+    // Weights p = 2^(score * qscale + nm) and p * scale, which has to fit fp16: nm is chosen so that the largest p * scale of the
+    // run so far lies in [2^13, 2^15] (p itself below 2^75: a score past `high` is looked at first).
+    float2 nm, high, l;
+    float o[NG][4][4];  // sums of weight * code, in units of 2^-24 (tiles 1 and 3 of a group: 2^-20)
+    float2 z[NG];       // sums of weight * minimum
     auto fetch_q = [&]() {
         const __nv_bfloat16* row = a.q + ((size_t)use.b * a.Hq + (size_t)use.h * a.G + qh) * DH + 16 * t;
 #pragma unroll
@@ -288,15 +296,14 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             for (int e = 0; e < 2; ++e)
                 qraw[c][e] = qh < a.G ? __ldg(reinterpret_cast<const uint4*>(row + c * kP4Group) + e) : make_uint4(0, 0, 0, 0);
     };
-    auto set_q = [&]() {
+    auto begin = [&]() {  // a (sequence, kv head): its query, sums of nothing
         float x[NG][16];
         float big = 0.f;
 #pragma unroll
         for (int c = 0; c < NG; ++c)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const uint4 v = qraw[c][e];
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const uint32_t w[4] = {qraw[c][e].x, qraw[c][e].y, qraw[c][e].z, qraw[c][e].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     x[c][e * 8 + 2 * i] = bf16_lo(w[i]);
@@ -327,33 +334,41 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {  // nibbles 2 part and that + 4; the ones after them
-                    const int d = w * 8 + part * 2;
-                    qf[c][w][part][0] = pack_f16(x[c][d], x[c][d + 4]);
-                    qf[c][w][part][1] = pack_f16(x[c][d + 1] * 0.0625f, x[c][d + 5] * 0.0625f);
+                for (int k = 0; k < 2; ++k) {  // nibbles 2k and that + 4; the ones after them
+                    const int d = w * 8 + k * 2;
+                    qf[c][w][k][0] = pack_f16(x[c][d], x[c][d + 4]);
+                    qf[c][w][k][1] = pack_f16(x[c][d + 1] * 0.0625f, x[c][d + 5] * 0.0625f);
                 }
         }
         // (a query of infinity has no finite form)
-        const float up = big < INFINITY ? __uint_as_float((uint32_t)(127 + e) << 23) * 16777216.f * sl2 : __uint_as_float(0x7fc00000u);
-        const int at = ch * 4;  // the lane that holds it as a row
+        const float up = big < INFINITY ? __uint_as_float((uint32_t)(127 + e) << 23) * 16777216.f * (kLog2e / sqrtf((float)DH))
+                                        : __uint_as_float(0x7fc00000u);
+        const int at = ch * 4;  // the lane that holds the head as a row
         qscale = make_float2(__shfl_sync(0xffffffffu, up, at), __shfl_sync(0xffffffffu, up, at + 4));
 #pragma unroll
-        for (int c = 0; c < NG; ++c)
+        for (int c = 0; c < NG; ++c) {
             qs[c] = make_float2(__shfl_sync(0xffffffffu, sums[c], at), __shfl_sync(0xffffffffu, sums[c], at + 4));
+            z[c] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[c][0][i] = o[c][1][i] = o[c][2][i] = o[c][3][i] = 0.f;
+        }
+        l = make_float2(0.f, 0.f);
+        nm = make_float2(0.f, 0.f);
+        high = make_float2(-INFINITY, -INFINITY);  // the first score moves it
     };
-    // the sums of this warp's piece at scale m: dims c * 64 + 8 g + (0..7) of head ch + e
+    // the sums of this warp's piece: dims c * 64 + 8 g + (0..7) of head ch + e
     auto piece = [&](int c, int e, float (&v)[8]) {
-        const float unit = 16777216.f / (e ? nu.y : nu.x), add = e ? z[c].y : z[c].x;
+        const float add = e ? z[c].y : z[c].x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float u = i & 1 ? unit * 0.0625f : unit;
+            const float u = i & 1 ? 1048576.f : 16777216.f;
             v[i] = fmaf(o[c][i][e], u, add);
             v[4 + i] = fmaf(o[c][i][2 + e], u, add);
         }
     };
     auto total = [&]() {  // sums over the keys that other lanes took
 #pragma unroll
-        for (int s = PAIR ? 2 : 4; s < 32; s <<= 1) {
+        for (int s = LANES; s < 32; s <<= 1) {
             l.x += __shfl_xor_sync(0xffffffffu, l.x, s);
             l.y += __shfl_xor_sync(0xffffffffu, l.y, s);
 #pragma unroll
@@ -362,17 +377,17 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 z[c].y += __shfl_xor_sync(0xffffffffu, z[c].y, s);
             }
         }
-        if constexpr (PAIR) {
+#pragma unroll
+        for (int s = LANES; s < 4; s <<= 1)
 #pragma unroll
             for (int c = 0; c < NG; ++c)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[c][q][e] += __shfl_xor_sync(0xffffffffu, o[c][q][e], 2);
-        }
+                    for (int e = 0; e < 4; ++e) o[c][q][e] += __shfl_xor_sync(0xffffffffu, o[c][q][e], s);
     };
-    // (PAIR: lanes t and t + 2 hold the same sums; each stores one of the two groups of dims)
-    auto stores = [&](int c) { return !PAIR || c == t >> 1; };
+    // (lanes that hold the same columns' sums share the groups of dims to store)
+    auto stores = [&](int c) { return SHARE == 1 || c == part; };
     auto leave = [&](float* rec) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -388,7 +403,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
             if (g == 0 && stores(0))
-                *reinterpret_cast<float2*>(rec + h * PITCH + DH) = e ? make_float2(m.y, l.y) : make_float2(m.x, l.x);
+                *reinterpret_cast<float2*>(rec + h * PITCH + DH) = e ? make_float2(-nm.y, l.y) : make_float2(-nm.x, l.x);
         }
     };
     auto write_out = [&]() {
@@ -420,19 +435,16 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             sd[1][0] = *reinterpret_cast<const uint32_t*>(at + 8 * NG * 4);
         }
     };
-    // Scores and weights of a unit: sets of two rows by two columns. PAIR: one, of tile t >> 1 of the unit; otherwise a set a tile.
-    constexpr int SETS = PAIR ? 1 : P4_TILES;
     const int swap = (g & 4) | (g & 1) << 1 | (g >> 1 & 1);  // row g of a tile is key swap (and row g + 8 key swap + 8):
     const int vkey = (2 * t & 4) | (t & 1);                  // the keys of rows 2t, which one load of V takes, are 0, 1, 4, 5
-    const int tile_l = PAIR ? t >> 1 : 0, key_l = tile_l * 16 + swap;
-    const int side_l = tile_l * (side_at(1) - side_at(0)) + swap * (NG * 4), kcode_l = swap * (DH / 2) + 8 * t;
-    const uint32_t col_l[2] = {g < 4 ? 0x3c003c00u : 0u, g < 4 ? 0u : 0x3c003c00u};  // PAIR: fp16 1 where its column takes tile 0, 1
-    const int vcode_l = vkey * (DH / 2) + 4 * g;
+    const int side_l = swap * (NG * 4), kcode_l = swap * (DH / 2) + 8 * t, vcode_l = vkey * (DH / 2) + 4 * g;
+    int part_side = 0;  // where the lane's tile of a set has its scales and minima, from the set's first tile on
+#pragma unroll
+    for (int k = 1; k < SHARE; ++k)
+        if (part == k) part_side = side_at(k) - side_at(0);
     bool ok = true, fresh = true;
     int slot = 0, phase = 0, run_left = mine;
-    int keys_left = use.keys - use.u * P4_UNIT;  // of the (sequence, kv head), from the unit at hand on
-    use.left = 1 << 30;                          // (counted by run_left)
-    reset();
+    int keys_left = use.keys - (use.u << ulog);  // of the (sequence, kv head), from the unit at hand on
     if (mine > 0) fetch_q();
     __syncwarp();  // the barriers are set
 #pragma unroll 1
@@ -440,160 +452,171 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     float* const my_smem = reinterpret_cast<float*>(p4_rings + warp * Ly::RING);
 #pragma unroll 1
     while (run_left > 0) {
-        if (fresh) set_q();
+        if (fresh) begin();
         if (!__all_sync(0xffffffffu, mbar_wait_suspend(&full[slot], phase, abort_flag))) { ok = false; break; }
         uint8_t* ka = p4_rings + warp * Ly::RING + slot * Ly::SLOT;
         uint8_t* va = ka + Ly::HALF;
-        const int valid = keys_left;  // keys of the unit; 32 or more: all
-        if (valid < P4_UNIT) {
+        const int valid = min(keys_left, 1 << ulog);  // keys of the unit
+        if (valid < P4_STEP) {
             // what stands behind the last key may be anything: its scales and minima become 0 (0 * NaN must not reach O)
-            for (int e = lane; e < (P4_UNIT - valid) * NG; e += 32) {
+            for (int e = lane; e < (P4_STEP - valid) * NG; e += 32) {
                 const int key = valid + e / NG, tile = key >> 4;
-                *reinterpret_cast<uint32_t*>(va + side_at(0) + tile * (side_at(1) - side_at(0)) + (key & 15) * (NG * 4) + e % NG * 4) = 0u;
+                *reinterpret_cast<uint32_t*>(va + tile / BT * BT * (TILE + SIDE) + BT * TILE + tile % BT * SIDE +
+                                             (key & 15) * (NG * 4) + e % NG * 4) = 0u;
             }
             fence_proxy_async_smem();  // (the slot's next copy comes after these stores)
             __syncwarp();
         }
-        float acc[P4_TILES][NG][4];
-#pragma unroll
-        for (int k = 0; k < P4_TILES; ++k) {
-            const uint8_t* codes = ka + tile_at(k) + kcode_l;
-#pragma unroll
-            for (int c = 0; c < NG; ++c) {
-                const uint2 w0 = *reinterpret_cast<const uint2*>(codes + c * 32);
-                const uint2 w1 = *reinterpret_cast<const uint2*>(codes + 8 * (DH / 2) + c * 32);
-                const uint32_t a0[2] = {w0.x, w0.y}, a1[2] = {w1.x, w1.y};
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const uint32_t y0 = a0[w] >> 8, y1 = a1[w] >> 8;
-                    if (w == 0)
-                        mma_f16_first(acc[k][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
-                                      a1[w] & 0x00f000f0u, qf[c][w][0][0], qf[c][w][0][1]);
-                    else
-                        mma_f16(acc[k][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u, a1[w] & 0x00f000f0u,
-                                qf[c][w][0][0], qf[c][w][0][1]);
-                    mma_f16(acc[k][c], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
-                            qf[c][w][1][0], qf[c][w][1][1]);
-                }
-            }
-        }
-        float2 x[SETS][2];  // [set][row g, row g + 8]: heads ch, ch + 1
+        float2 x[SETS][2];  // scores [set][row g, row g + 8] of heads ch, ch + 1
 #pragma unroll
         for (int k = 0; k < SETS; ++k) {
+            float acc[SHARE][NG][4];
+#pragma unroll
+            for (int j = 0; j < SHARE; ++j) {
+                const uint8_t* codes = ka + tile_at(k * SHARE + j) + kcode_l;
+#pragma unroll
+                for (int c = 0; c < NG; ++c) {
+                    const uint2 w0 = *reinterpret_cast<const uint2*>(codes + c * 32);
+                    const uint2 w1 = *reinterpret_cast<const uint2*>(codes + 8 * (DH / 2) + c * 32);
+                    const uint32_t a0[2] = {w0.x, w0.y}, a1[2] = {w1.x, w1.y};
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const uint32_t y0 = a0[w] >> 8, y1 = a1[w] >> 8;
+                        if (w == 0)
+                            mma_f16_first(acc[j][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
+                                          a1[w] & 0x00f000f0u, qf[c][w][0][0], qf[c][w][0][1]);
+                        else
+                            mma_f16(acc[j][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
+                                    a1[w] & 0x00f000f0u, qf[c][w][0][0], qf[c][w][0][1]);
+                        mma_f16(acc[j][c], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
+                                qf[c][w][1][0], qf[c][w][1][1]);
+                    }
+                }
+            }
             uint32_t sd[2][NG];
-            sides(ka + side_at(k) + side_l, sd);
+            sides(ka + side_at(k * SHARE) + part_side + side_l, sd);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                 for (int c = 0; c < NG; ++c) {
                     const float sc = bf16_lo(sd[r][c]), lo = bf16_hi(sd[r][c]);
-                    s0 = c == 0 ? lo * qs[c].x : fmaf(lo, qs[c].x, s0);
-                    s1 = c == 0 ? lo * qs[c].y : fmaf(lo, qs[c].y, s1);
-                    s0 = fmaf(sc, PAIR && tile_l ? acc[1][c][2 * r] : acc[k][c][2 * r], s0);
-                    s1 = fmaf(sc, PAIR && tile_l ? acc[1][c][2 * r + 1] : acc[k][c][2 * r + 1], s1);
+                    float a0 = acc[0][c][2 * r], a1 = acc[0][c][2 * r + 1];
+#pragma unroll
+                    for (int j = 1; j < SHARE; ++j) {
+                        a0 = part == j ? acc[j][c][2 * r] : a0;
+                        a1 = part == j ? acc[j][c][2 * r + 1] : a1;
+                    }
+                    s0 = fmaf(sc, a0, c == 0 ? lo * qs[c].x : fmaf(lo, qs[c].x, s0));
+                    s1 = fmaf(sc, a1, c == 0 ? lo * qs[c].y : fmaf(lo, qs[c].y, s1));
                 }
-                x[k][r] = make_float2(s0 * qscale.x, s1 * qscale.y);
+                x[k][r] = make_float2(s0, s1);
             }
         }
-        if (valid < P4_UNIT) {
+        if (valid < P4_STEP) {
 #pragma unroll
             for (int k = 0; k < SETS; ++k)
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    if (k * 16 + key_l + 8 * r >= valid) x[k][r] = make_float2(-INFINITY, -INFINITY);
+                    if ((k * SHARE + part) * 16 + swap + 8 * r >= valid) x[k][r] = make_float2(-INFINITY, -INFINITY);
         }
-        float2 mx = make_float2(fmaxf(x[0][0].x, x[0][1].x), fmaxf(x[0][0].y, x[0][1].y));
-        if constexpr (!PAIR) mx = make_float2(fmax3(mx.x, x[SETS - 1][0].x, x[SETS - 1][1].x), fmax3(mx.y, x[SETS - 1][0].y, x[SETS - 1][1].y));
-        // O and the sums move to a larger maximum only when it grew by more than 8 (P <= 2^8)
-        const bool moved = __any_sync(0xffffffffu, mx.x > m.x + 8.f || mx.y > m.y + 8.f);
-        float2 shrink = make_float2(1.f, 1.f);  // (O follows below)
-        if (moved) {
+        // weights p, and p * scale by group of dims
+        float2 p[SETS][2], wt[SETS][NG][2];
+        uint32_t sd[SETS][2][NG];
 #pragma unroll
-            for (int s = PAIR ? 2 : 4; s < 32; s <<= 1) {
-                mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, s));
-                mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, s));
-            }
-            if (mx.x > m.x + 8.f) {
-                shrink.x = ex2_approx(m.x - mx.x);
-                m.x = mx.x;
-            }
-            if (mx.y > m.y + 8.f) {
-                shrink.y = ex2_approx(m.y - mx.y);
-                m.y = mx.y;
-            }
-            l = mul2(l, shrink);
-#pragma unroll
-            for (int c = 0; c < NG; ++c) z[c] = mul2(z[c], shrink);
-        }
-        const float2 nm = make_float2(m.x == -INFINITY ? 0.f : -m.x, m.y == -INFINITY ? 0.f : -m.y);
-        // weights of V by group of dims: p * scale, and the sums of p * minimum
-        float2 wt[SETS][NG][2];
-        float2 top = make_float2(0.f, 0.f);
+        for (int k = 0; k < SETS; ++k) sides(va + side_at(k * SHARE) + part_side + side_l, sd[k]);
+        float2 mx = x[0][0];
 #pragma unroll
         for (int k = 0; k < SETS; ++k) {
-            uint32_t sd[2][NG];
-            sides(va + side_at(k) + side_l, sd);
+            mx.x = fmax3(mx.x, x[k][0].x, x[k][1].x);
+            mx.y = fmax3(mx.y, x[k][0].y, x[k][1].y);
+        }
+        float2 was = nm;
+        struct {
+            bool x, y;
+        } up{};
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+            float2 top = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float2 p = make_float2(ex2_approx(x[k][r].x + nm.x), ex2_approx(x[k][r].y + nm.y));
-                l = add2(l, p);
+            for (int k = 0; k < SETS; ++k) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    p[k][r] = make_float2(ex2_approx(fmaf(x[k][r].x, qscale.x, nm.x)), ex2_approx(fmaf(x[k][r].y, qscale.y, nm.y)));
+#pragma unroll
+                    for (int c = 0; c < NG; ++c) {
+                        const float sc = bf16_lo(sd[k][r][c]);
+                        wt[k][c][r] = make_float2(p[k][r].x * sc, p[k][r].y * sc);
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < NG; ++c) {
-                    const float sc = bf16_lo(sd[r][c]), lo = bf16_hi(sd[r][c]);
-                    z[c] = make_float2(fmaf(p.x, lo, z[c].x), fmaf(p.y, lo, z[c].y));
-                    wt[k][c][r] = make_float2(p.x * sc, p.y * sc);
+                    top.x = fmax3(top.x, fabsf(wt[k][c][0].x), fabsf(wt[k][c][1].x));
+                    top.y = fmax3(top.y, fabsf(wt[k][c][0].y), fabsf(wt[k][c][1].y));
                 }
             }
+            if (pass == 2) break;
+            if (pass == 0) {
+                if (!__any_sync(0xffffffffu, mx.x > high.x || mx.y > high.y || top.x > 32768.f || top.y > 32768.f)) break;
 #pragma unroll
-            for (int c = 0; c < NG; ++c) {
-                top.x = fmax3(top.x, fabsf(wt[k][c][0].x), fabsf(wt[k][c][1].x));
-                top.y = fmax3(top.y, fabsf(wt[k][c][0].y), fabsf(wt[k][c][1].y));
-            }
-        }
-        if (moved || __any_sync(0xffffffffu, top.x * nu.x > 32768.f || top.y * nu.y > 32768.f)) {
-#pragma unroll
-            for (int s = PAIR ? 2 : 4; s < 32; s <<= 1) {
-                top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, s));
-                top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, s));
-            }
-            // the largest weight of the run so far: what was below 2^14 / nu has shrunk with the scores' maximum
-            auto next_nu = [](float top, float shrink, float nu) {
-                const float big = fmaxf(top, shrink * (16384.f / nu));
-                const int at = min(max(140 - (int)(__float_as_uint(big) >> 23), -100), 100);  // big 2^at in [2^13, 2^14)
-                return big > 0.f ? __uint_as_float((uint32_t)(127 + at) << 23) : nu;
-            };
-            const float2 next = make_float2(next_nu(top.x, shrink.x, nu.x), next_nu(top.y, shrink.y, nu.y));
-            const float2 f = make_float2(next.x / nu.x * shrink.x, next.y / nu.y * shrink.y);
-            nu = next;
-#pragma unroll
-            for (int c = 0; c < NG; ++c)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    o[c][q][0] *= f.x;
-                    o[c][q][1] *= f.y;
-                    o[c][q][2] *= f.x;
-                    o[c][q][3] *= f.y;
+                for (int s = LANES; s < 32; s <<= 1) {
+                    mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, s));
+                    mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, s));
                 }
+                // scores first: p is 1 for the largest
+                up = {mx.x > high.x, mx.y > high.y};
+                if (up.x) nm.x = -mx.x * qscale.x;
+                if (up.y) nm.y = -mx.y * qscale.y;
+            } else {
+                // then the weights of V: the largest one to [2^13, 2^14), p at most 2^60
+#pragma unroll
+                for (int s = LANES; s < 32; s <<= 1) {
+                    top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, s));
+                    top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, s));
+                }
+                auto suit = [](float top, bool up, float& nm) {
+                    if (up || top > 32768.f) nm += (float)min(140 - (int)(__float_as_uint(top) >> 23), up ? 60 : 0);
+                };
+                suit(top.x, up.x, nm.x);
+                suit(top.y, up.y, nm.y);
+                // (nothing is there before the first score)
+                const float2 f = make_float2(high.x == -INFINITY ? 0.f : ex2_approx(nm.x - was.x),
+                                             high.y == -INFINITY ? 0.f : ex2_approx(nm.y - was.y));
+                high = make_float2((75.f - nm.x) / qscale.x, (75.f - nm.y) / qscale.y);
+                l = mul2(l, f);
+#pragma unroll
+                for (int c = 0; c < NG; ++c) {
+                    z[c] = mul2(z[c], f);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        o[c][q][0] *= f.x;
+                        o[c][q][1] *= f.y;
+                        o[c][q][2] *= f.x;
+                        o[c][q][3] *= f.y;
+                    }
+                }
+            }
         }
         uint32_t wb[SETS][NG][2];  // P^T fragments
 #pragma unroll
         for (int k = 0; k < SETS; ++k)
 #pragma unroll
-            for (int c = 0; c < NG; ++c)
+            for (int r = 0; r < 2; ++r) {
+                l = add2(l, p[k][r]);
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float2 w = mul2(wt[k][c][r], nu);
-                    wb[k][c][r] = transpose8x8(pack_f16(w.x, w.y));
+                for (int c = 0; c < NG; ++c) {
+                    const float lo = bf16_hi(sd[k][r][c]);
+                    z[c] = make_float2(fmaf(p[k][r].x, lo, z[c].x), fmaf(p[k][r].y, lo, z[c].y));
+                    wb[k][c][r] = transpose8x8(pack_f16(wt[k][c][r].x, wt[k][c][r].y));
                 }
+            }
 #pragma unroll
         for (int k = 0; k < P4_TILES; ++k) {
             const uint8_t* codes = va + tile_at(k) + vcode_l;
+            const bool mine_k = SHARE == 1 || g / HC == k % SHARE;  // this lane's column of O takes the tile
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
-                // PAIR: columns g < 4 take the first tile's weights, the others the second's
-                const uint32_t b0 = PAIR ? mul_f16(wb[0][c][0], col_l[k]) : wb[SETS == 1 ? 0 : k][c][0];
-                const uint32_t b1 = PAIR ? mul_f16(wb[0][c][1], col_l[k]) : wb[SETS == 1 ? 0 : k][c][1];
+                const uint32_t b0 = mine_k ? wb[k / SHARE][c][0] : 0u, b1 = mine_k ? wb[k / SHARE][c][1] : 0u;
                 // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further: the first and the last four nibbles
                 auto word = [&](int key) { return *reinterpret_cast<const uint32_t*>(codes + c * 32 + key * (DH / 2)); };
                 const uint32_t wa = word(0), wb2 = word(2), wc = word(8), wd = word(10);
@@ -611,13 +634,12 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             }
         }
         __syncwarp();  // every lane has read the slot: the unit NS further may come
-        ++used;
         issue(slot);
         if (++slot == NS) {
             slot = 0;
             phase ^= 1;
         }
-        keys_left -= P4_UNIT;
+        keys_left -= 1 << ulog;
         fresh = keys_left <= 0;
         if (--run_left > 0 && !fresh) continue;
         // the (sequence, kv head) or the run ends: written out if all of it was in this run, left as a piece otherwise (that at the
@@ -626,10 +648,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         if (inside && fresh) write_out();
         else leave(run_left == 0 ? my_smem : a.recs + (size_t)gw * 2 * a.G * PITCH);
         if (run_left == 0) break;
-        reset();
         inside = true;
-        use.u = use.n - 1;
-        p4_step(a, use);
+        p4_next(a, use, ulog);
         keys_left = use.keys;
         fetch_q();
     }
@@ -638,12 +658,12 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         *abort_flag = 1;
         if (a.err && lane == 0) atomicOr(a.err, ERR_TIMEOUT);
         int never = 0;
-        for (int j = used; j < issued; ++j) mbar_wait_suspend(&full[j % NS], (j / NS) & 1, &never);
+        for (int j = mine - run_left; j < issued; ++j) mbar_wait_suspend(&full[j % NS], (j / NS) & 1, &never);
     }
 
     // ---------------- the pieces at the ends of this CTA's runs
-    const bool ends = fresh;                             // the (sequence, kv head) ends with the run
-    const bool open = mine > 0 && !(inside && ends);     // a part of it lies in another run
+    const bool ends = fresh;                          // the (sequence, kv head) ends with the run
+    const bool open = mine > 0 && !(inside && ends);  // a part of it lies in another run
     const int seg = use.b * a.Hkv + use.h;
     if (lane == 0) {
         seg_sh[warp] = open ? seg : -1;
@@ -668,8 +688,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         float M = -INFINITY, L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](float m, float l, const float4& y) {
-            // (a piece whose scores are all NaN keeps m = -inf, and its sums are NaN)
-            const float f = m == -INFINITY ? 1.f : ex2_approx(m - M);
+            const float f = ex2_approx(m - M);
             L = fmaf(l, f, L);
             v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
         };
@@ -680,7 +699,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             y = __ldcg(reinterpret_cast<const float4*>(far + dd));
         }
         for (int w = w0; w < w1; ++w) M = fmaxf(M, rec[w * STEP + DH]);
-        M = fmaxf(M, ml.x);
+        M = fmaxf(M, ml.x);  // (finite: a group has a piece)
         for (int w = w0; w < w1; ++w)
             add(rec[w * STEP + DH], rec[w * STEP + DH + 1], *reinterpret_cast<const float4*>(rec + w * STEP + dd));
         add(ml.x, ml.y, y);
@@ -704,7 +723,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             while (w0 > 0 && seg_sh[w0 - 1] == s) --w0;
             if (whole_sh[w0] & 1) {
                 // the unit behind it, the warp whose run holds the one before, and whether that run goes on
-                const int end = x0 + mine + p4_units(max(keys_left, 0)), longer = more * (len + 1);
+                const int end = x0 + mine + ((max(keys_left, 0) + (1 << ulog) - 1) >> ulog), longer = more * (len + 1);
                 d.seg = s;
                 d.first = cta0 + w0;
                 d.last = end <= longer ? (end - 1) / (len + 1) : more + (end - 1 - longer) / len;
@@ -745,12 +764,12 @@ __global__ void __launch_bounds__(P4_JOIN_THREADS)
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float m, float l, const float4& y) {
         if (m > M) {
-            const float f = M == -INFINITY ? 1.f : ex2_approx(M - m);
+            const float f = ex2_approx(M - m);
             L *= f;
             v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
             M = m;
         }
-        const float f = m == -INFINITY ? 1.f : ex2_approx(m - M);
+        const float f = m == -INFINITY ? 0.f : ex2_approx(m - M);  // (-inf: a way without a record)
         L = fmaf(l, f, L);
         v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
     };
@@ -784,17 +803,42 @@ __global__ void __launch_bounds__(P4_JOIN_THREADS)
 
 int p4_ctas() { return device_sm_count() * P4_CTAS; }
 
-template <int DH, int BT, bool PAIR>
+template <int DH, int BT, int HC>
 cudaError_t paged4_launch_one(const P4Args& a, cudaStream_t st) {
     const int ctas = p4_ctas();
-    cudaError_t e = launch_pdl(attn_paged4_kernel<DH, BT, PAIR>, dim3(ctas), dim3(P4_THREADS), P4Layout<DH>::SMEM, st, a);
+    cudaError_t e = launch_pdl(attn_paged4_kernel<DH, BT, HC>, dim3(ctas), dim3(P4_THREADS), P4Layout<DH>::SMEM, st, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(attn_paged4_join_kernel<DH>, dim3(ctas), dim3(P4_JOIN_THREADS), 0, st, a);
 }
+template <int DH, int BT>
+cudaError_t paged4_launch_bt(const P4Args& a, cudaStream_t st) {
+    if (a.G <= 2) return paged4_launch_one<DH, BT, 2>(a, st);
+    if (a.G <= 4) return paged4_launch_one<DH, BT, 4>(a, st);
+    return paged4_launch_one<DH, BT, 8>(a, st);
+}
 template <int DH>
 cudaError_t paged4_launch_dh(const P4Args& a, int page, cudaStream_t st) {
-    if (a.G <= 4) return page == 16 ? paged4_launch_one<DH, 1, true>(a, st) : paged4_launch_one<DH, 2, true>(a, st);
-    return page == 16 ? paged4_launch_one<DH, 1, false>(a, st) : paged4_launch_one<DH, 2, false>(a, st);
+    if (page == 16) return paged4_launch_bt<DH, 1>(a, st);
+    if (page == 32) return paged4_launch_bt<DH, 2>(a, st);
+    return paged4_launch_bt<DH, 4>(a, st);
+}
+
+template <int DH, int BT>
+cudaError_t paged4_prepare_bt() {
+    const void* fns[] = {(const void*)attn_paged4_kernel<DH, BT, 2>, (const void*)attn_paged4_kernel<DH, BT, 4>,
+                         (const void*)attn_paged4_kernel<DH, BT, 8>};
+    for (const void* f : fns) {
+        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, P4Layout<DH>::SMEM);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+template <int DH>
+cudaError_t paged4_prepare_dh() {
+    cudaError_t e = paged4_prepare_bt<DH, 1>();
+    if (e == cudaSuccess) e = paged4_prepare_bt<DH, 2>();
+    if (e == cudaSuccess) e = paged4_prepare_bt<DH, 4>();
+    return e;
 }
 
 size_t desc_bytes() { return ((size_t)p4_ctas() * sizeof(P4Desc) + 255) / 256 * 256; }
@@ -828,16 +872,8 @@ cudaError_t attn_decode_paged4_launch(const __nv_bfloat16* q, const void* k_page
 }
 
 cudaError_t attention_paged4_prepare() {
-    const void* fns[] = {(const void*)attn_paged4_kernel<128, 1, false>, (const void*)attn_paged4_kernel<128, 2, false>,
-                         (const void*)attn_paged4_kernel<128, 1, true>,  (const void*)attn_paged4_kernel<128, 2, true>,
-                         (const void*)attn_paged4_kernel<64, 1, false>,  (const void*)attn_paged4_kernel<64, 2, false>,
-                         (const void*)attn_paged4_kernel<64, 1, true>,   (const void*)attn_paged4_kernel<64, 2, true>};
-    for (int i = 0; i < 8; ++i) {
-        cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             i < 4 ? P4Layout<128>::SMEM : P4Layout<64>::SMEM);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    cudaError_t e = paged4_prepare_dh<128>();
+    return e == cudaSuccess ? paged4_prepare_dh<64>() : e;
 }
 
 }  // namespace q3
