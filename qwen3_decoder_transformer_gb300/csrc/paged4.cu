@@ -39,9 +39,7 @@ struct Place {
     long long page;  // page id * Hkv, or -1
     int row;         // within the page
 };
-__device__ __forceinline__ bool place_token(const Packed& p, const Paged4& c, int Hkv, int t, int lane, Place& pl) {
-    const int s = find_sequence(p, t, lane);
-    if (s < 0) return false;
+__device__ __forceinline__ void place_at(const Packed& p, const Paged4& c, int Hkv, int s, int t, Place& pl) {
     const long long slot = (long long)__ldg(p.start + s) + (t - __ldg(p.cu + s));
     pl.slot = slot < 0 || slot > 0x7fffffff ? -1 : (int)slot;
     pl.page = -1;
@@ -51,6 +49,11 @@ __device__ __forceinline__ bool place_token(const Packed& p, const Paged4& c, in
         if ((unsigned)id < (unsigned)c.n_pages) pl.page = (long long)id * Hkv;
     }
     pl.row = pl.slot & ((1 << c.page_log) - 1);
+}
+__device__ __forceinline__ bool place_token(const Packed& p, const Paged4& c, int Hkv, int t, int lane, Place& pl) {
+    const int s = find_sequence(p, t, lane);
+    if (s < 0) return false;
+    place_at(p, c, Hkv, s, t, pl);
     return true;
 }
 
@@ -66,46 +69,56 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// Quantise a group's values, of which this thread holds n: minimum rounded down to bf16 and scale = (max - minimum) / 15
-// rounded up, so that the codes 0..15 cover the group and a value is off by half a scale at most. The scale's pair is
-// returned; a group that holds NaN or infinity (or spans more than fp32 does) gets NaN for both.
-template <int N, int LANES>
-__device__ __forceinline__ uint32_t quantize(const float* x, uint32_t (&codes)[N / 8]) {
-    float mn = x[0], mx = x[0], bad = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        mn = fminf(mn, x[i]);
-        mx = fmaxf(mx, x[i]);
-        bad += x[i] * 0.f;  // 0, or NaN
-    }
-#pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        bad += __shfl_xor_sync(0xffffffffu, bad, o);
-    }
+__device__ __forceinline__ float min_nan(float a, float b) {  // (a NaN stays)
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The pair (scale, minimum) of a group with these extremes: minimum rounded down to bf16 and scale = (max - minimum) / 15 rounded
+// up, so that the codes 0..15 cover the group and a value is off by half a scale at most. A group that holds NaN or
+// infinity, or spans more than fp32 does, gets NaN.
+__device__ __forceinline__ uint32_t side_of(float mn, float mx) {
     const __nv_bfloat16 lo = __float2bfloat16_rd(mn);
-    const float low = __bfloat162float(lo);
-    const __nv_bfloat16 sc = __float2bfloat16_ru(__fdiv_rn(__fsub_rn(mx, low), 15.f));
-    const float scale = __bfloat162float(sc);
-    if (bad != 0.f || !(scale < INFINITY)) {
-#pragma unroll
-        for (int w = 0; w < N / 8; ++w) codes[w] = 0;
-        return 0x7fff7fffu;
-    }
-    const float div = scale > 0.f ? scale : 1.f;
-#pragma unroll
-    for (int w = 0; w < N / 8; ++w) {
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // a true quotient: ties (bf16 values between two codes) go to the even code as the definition says
-            const int q = __float2int_rn(__fdiv_rn(__fsub_rn(x[w * 8 + i], low), div));
-            c |= (uint32_t)min(max(q, 0), 15) << (4 * i);
-        }
-        codes[w] = c;
-    }
+    const __nv_bfloat16 sc = __float2bfloat16_ru(__fdiv_rn(__fsub_rn(mx, __bfloat162float(lo)), 15.f));
+    if (!(__bfloat162float(sc) < INFINITY)) return 0x7fff7fffu;
     return (uint32_t)__bfloat16_as_ushort(sc) | (uint32_t)__bfloat16_as_ushort(lo) << 16;
+}
+
+// The codes of eight values, the first one in the lowest nibble: the whole number nearest to q = (x - minimum) / scale, the even
+// one of a tie, without a division a value: q is bracketed by products with floats below and above 1 / scale, each rounded
+// to a whole number by one fused multiply-add. Where they agree that is the code; where they do not, q is a tie (of
+// bf16 values there are many) and the even one of the two is meant. (A quotient within 2^-20 of a tie counts as one.)
+__device__ __forceinline__ uint32_t codes_of(const float2 (&x)[4], uint32_t side) {
+    const float scale = bf16_lo(side), low = bf16_hi(side);
+    // scale 0 (all values alike), NaN, and scales whose reciprocal is no normal float: one by one
+    if (!(scale >= 2e-38f && scale < 4e37f)) {
+        uint32_t c = 0;
+        if (scale > 0.f)
+            for (int i = 0; i < 8; ++i) {
+                const float d = __fsub_rn(i & 1 ? x[i / 2].y : x[i / 2].x, low);
+                c |= (uint32_t)min(__float2int_rn(__fdiv_rn(d, scale)), 15) << (4 * i);
+            }
+        return c;
+    }
+    const uint32_t inv = __float_as_uint(rcp_approx(scale));  // off by one unit in the last place at most
+    const float below = __uint_as_float(inv - 2), above = __uint_as_float(inv + 2);
+    constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, in the lowest bits
+    const float2 whole = make_float2(kWhole, kWhole), b2 = make_float2(below, below), a2 = make_float2(above, above);
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+        const float2 d = add2(x[i], make_float2(-low, -low)), q0 = fma2(d, b2, whole), q1 = fma2(d, a2, whole);
+        const uint32_t y0 = __float_as_uint(q0.y), x0 = __float_as_uint(q0.x);
+        c = c * 16u + y0 + ((__float_as_uint(q1.y) - y0) & y0);  // (the difference is 0 or 1: the odd one of two goes up)
+        c = c * 16u + x0 + ((__float_as_uint(q1.x) - x0) & x0);
+    }
+    return c - 0x11111111u * 0x4b400000u;  // every code carries the bits of kWhole
 }
 
 struct AppendArgs {
@@ -123,89 +136,190 @@ struct AppendArgs {
     int* err;
 };
 
-// One token a CTA. A head takes DH / 16 lanes; each holds 8 dims of the first half and the 8 dims that they are rotated with.
-//   q, k: y = x * rsqrt(mean x^2 + eps) * gamma; rotated (a, b) -> (a cos - b sin, b cos + a sin), fp32, rounded once
+// A warp takes every `parts`-th piece of the heads of `per` consecutive tokens; a piece is 32 / LPH heads of LPH = DH / 16 lanes,
+// each with 8 dims of the first half and the 8 dims that they are rotated with. With r = (mean x^2 + eps)^-1/2,
+//   (a, b) -> (r (g_a cos a - g_b sin b), r (g_b cos b + g_a sin a)) in fp32, rounded once;
+// the products of gains and angles are made once a token and kind of head. The next piece's values, and the next token's
+// angles, are on their way meanwhile; a sequence is looked up once, then followed from token to token.
 template <int DH>
-__global__ void __launch_bounds__(512)
-    append_paged4_kernel(const AppendArgs a) {
-    constexpr int LPH = DH / 16;
-    const int lane = threadIdx.x & 31, t = blockIdx.x;
-    const int heads = a.Hq + 2 * a.Hkv, l = threadIdx.x % LPH;
+__global__ void __launch_bounds__(128)
+    append_paged4_kernel(const AppendArgs a, int per, int parts) {
+    constexpr int LPH = DH / 16, HPW = 32 / LPH;
+    const int lane = threadIdx.x & 31, l = lane % LPH;
+    const int w = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+    const int chunk = (int)((unsigned)w / (unsigned)parts), part = w - chunk * parts;
+    const int t0 = chunk * per, t1 = min(a.N, t0 + per);
+    const int heads = a.Hq + 2 * a.Hkv, pieces = (heads + HPW - 1) / HPW;
+    const int page_log = a.cache.page_log;
     pdl_wait();
     pdl_trigger();
-    Place pl;
-    if (!place_token(a.batch, a.cache, a.Hkv, t, lane, pl)) return;  // behind the last sequence: left as it was
-    if (pl.slot < 0 || pl.slot >= a.n_pos) {  // no position to rotate by
-        if (threadIdx.x == 0 && a.err) atomicOr(a.err, ERR_INDEX);
-        return;
-    }
-    if (pl.page < 0 && threadIdx.x == 0 && a.err) atomicOr(a.err, ERR_INDEX);
-    const __nv_bfloat16* cs = a.cos_sin + (size_t)pl.slot * DH + l * 8;
-    float c[8], s[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(cs)), c);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(cs + DH / 2)), s);
-    const int page = 1 << a.cache.page_log;
-    // (whole warps stay in the loop: the lanes of the last heads work on head 0 and store nothing)
-    for (int h0 = threadIdx.x / LPH - lane / LPH; h0 < heads; h0 += blockDim.x / LPH) {
-        const int h = h0 + lane / LPH;
-        const bool on = h < heads;
-        const int hh = on ? h : 0;
-        const __nv_bfloat16* x = a.qkv + (size_t)t * a.ld + (size_t)hh * DH + l * 8;
-        float y[16];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(x)), y);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(x + DH / 2)), y + 8);
-        const bool is_q = hh < a.Hq, is_v = hh >= a.Hq + a.Hkv;
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (!is_v) {
-            const __nv_bfloat16* gamma = is_q ? a.q_gamma : a.k_gamma;
-            if (gamma) {
-                const float r = rsqrtf(ss / DH + a.eps);
-                float g[16];
-                unpack8(__ldg(reinterpret_cast<const uint4*>(gamma + l * 8)), g);
-                unpack8(__ldg(reinterpret_cast<const uint4*>(gamma + DH / 2 + l * 8)), g + 8);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = y[i] * r * g[i];
+    if (t0 >= t1) return;
+    uint4 raw[2];
+    auto load = [&](int t, int piece) {
+        const __nv_bfloat16* x = a.qkv + (size_t)t * a.ld + (size_t)min(piece * HPW + lane / LPH, heads - 1) * DH + l * 8;
+        raw[0] = __ldg(reinterpret_cast<const uint4*>(x));
+        raw[1] = __ldg(reinterpret_cast<const uint4*>(x + DH / 2));
+    };
+    load(t0, part);
+    int seq = -1, seq_end = t0;  // the sequence at hand and the row behind it
+    Place pl{-1, -1, 0};
+    uint4 ang[2];  // the token's cos and sin
+    auto place = [&](int t) {  // where row t goes
+        if (t < seq_end && seq >= 0) {
+            ++pl.slot;  // (a slot below n_pos - 1, or the row before had none)
+            pl.row = pl.slot & ((1 << page_log) - 1);
+            if (pl.slot <= 0 || pl.row != 0) return;
+            pl.page = -1;
+            const int at = pl.slot >> page_log;
+            if (at < a.cache.max_pages) {
+                const int id = __ldg(a.cache.table + (size_t)seq * a.cache.max_pages + at);
+                if ((unsigned)id < (unsigned)a.cache.n_pages) pl.page = (long long)id * a.Hkv;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p = y[i], q = y[8 + i];
-                y[i] = p * c[i] - q * s[i];
-                y[8 + i] = q * c[i] + p * s[i];
-            }
-            __nv_bfloat16* dst = nullptr;
-            if (is_q)
-                dst = a.q_out + ((size_t)t * a.Hq + hh) * DH;
-            else if (a.k_out)
-                dst = a.k_out + ((size_t)t * a.Hkv + (hh - a.Hq)) * DH;
-            if (on && dst) {
-                *reinterpret_cast<uint4*>(dst + l * 8) = pack8(y);
-                *reinterpret_cast<uint4*>(dst + DH / 2 + l * 8) = pack8(y + 8);
-            }
+            return;
         }
-        if (__all_sync(0xffffffffu, is_q)) continue;
-        uint32_t w[2], side[2];
-        if constexpr (DH == 128) {
-            uint32_t w0[1], w1[1];
-            side[0] = quantize<8, LPH>(y, w0);
-            side[1] = quantize<8, LPH>(y + 8, w1);
-            w[0] = w0[0];
-            w[1] = w1[0];
-        } else {
-            side[0] = quantize<16, LPH>(y, w);
-            side[1] = 0;
+        seq = -1;
+        seq_end = t;
+        const int s = find_sequence(a.batch, t, lane);
+        if (s < 0) return;
+        place_at(a.batch, a.cache, a.Hkv, s, t, pl);
+        seq = s;
+        // (from a slot that is no position on, every row is looked up by itself)
+        seq_end = pl.slot >= 0 && pl.slot < (1 << 30) ? __ldg(a.batch.cu + s + 1) : t;
+    };
+    auto angles = [&]() {
+        if (seq >= 0 && pl.slot >= 0 && pl.slot < a.n_pos) {
+            const __nv_bfloat16* cs = a.cos_sin + (size_t)pl.slot * DH + l * 8;
+            ang[0] = __ldg(reinterpret_cast<const uint4*>(cs));
+            ang[1] = __ldg(reinterpret_cast<const uint4*>(cs + DH / 2));
         }
-        if (on && !is_q && pl.page >= 0) {
-            uint8_t* base = (is_v ? a.v_pages : a.k_pages) +
-                            (size_t)(pl.page + (hh - a.Hq - (is_v ? a.Hkv : 0))) * p4_page_bytes(page, DH);
-            uint32_t* codes = reinterpret_cast<uint32_t*>(base + (size_t)pl.row * (DH / 2));
-            codes[l] = w[0];
-            codes[DH / 16 + l] = w[1];
-            uint32_t* sd = reinterpret_cast<uint32_t*>(base + (size_t)page * (DH / 2)) + pl.row * (DH / kP4Group);
-            if (l < DH / kP4Group) sd[l] = l == 0 ? side[0] : side[1];
+    };
+    auto floats = [](const uint4& v, float2 (&x)[4]) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
+    };
+    auto bytes = [](const float2 (&x)[4]) {
+        return make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y), pack_bf16(x[2].x, x[2].y),
+                          pack_bf16(x[3].x, x[3].y));
+    };
+    place(t0);
+    angles();
+    for (int t = t0; t < t1; ++t) {
+        const Place at = pl;
+        const bool in = seq >= 0, rotates = in && at.slot >= 0 && at.slot < a.n_pos;
+        // behind the last sequence: left as it was; no position to rotate by, or no page: flagged
+        if (part == 0 && lane == 0 && a.err && in && (!rotates || at.page < 0)) atomicOr(a.err, ERR_INDEX);
+        float2 c[4], s[4];
+        floats(ang[0], c);
+        floats(ang[1], s);
+        if (t + 1 < t1) {
+            place(t + 1);
+            angles();
+        }
+        float2 ac[4], bs[4], bc[4], as[4];  // g_a cos, -g_b sin, g_b cos, g_a sin
+        int kind = -1;                      // of the head that they are for: 0 a query, 1 a key
+        for (int piece = part; piece < pieces; piece += parts) {
+            const int h = piece * HPW + lane / LPH;
+            const bool on = h < heads && rotates;
+            const int hh = min(h, heads - 1);
+            float2 x[4], y[4];
+            floats(raw[0], x);
+            floats(raw[1], y);
+            if (piece + parts < pieces) load(t, piece + parts);
+            else if (t + 1 < t1) load(t + 1, part);
+            if (!rotates) continue;
+            const int is = hh < a.Hq ? 0 : hh < a.Hq + a.Hkv ? 1 : 2;
+            if (__any_sync(0xffffffffu, is < 2)) {
+                const __nv_bfloat16* gamma = is == 0 ? a.q_gamma : is == 1 ? a.k_gamma : nullptr;
+                if (__any_sync(0xffffffffu, is != kind && is < 2)) {
+                    kind = is;
+                    float2 ga[4], gb[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ga[i] = gb[i] = make_float2(1.f, 1.f);
+                    if (gamma) {
+                        floats(__ldg(reinterpret_cast<const uint4*>(gamma + l * 8)), ga);
+                        floats(__ldg(reinterpret_cast<const uint4*>(gamma + DH / 2 + l * 8)), gb);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        ac[i] = mul2(ga[i], c[i]);
+                        as[i] = mul2(ga[i], s[i]);
+                        bc[i] = mul2(gb[i], c[i]);
+                        bs[i] = mul2(gb[i], make_float2(-s[i].x, -s[i].y));
+                    }
+                }
+                float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ss = fma2(y[i], y[i], fma2(x[i], x[i], ss));
+                float sum = ss.x + ss.y;
+#pragma unroll
+                for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const float r = gamma ? rsqrtf(sum / DH + a.eps) : 1.f;
+                if (is < 2) {
+                    const float2 r2 = make_float2(r, r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 p = x[i], q = y[i];
+                        x[i] = mul2(fma2(ac[i], p, mul2(bs[i], q)), r2);
+                        y[i] = mul2(fma2(bc[i], q, mul2(as[i], p)), r2);
+                    }
+                    __nv_bfloat16* dst = nullptr;
+                    if (is == 0)
+                        dst = a.q_out + ((size_t)t * a.Hq + hh) * DH;
+                    else if (a.k_out)
+                        dst = a.k_out + ((size_t)t * a.Hkv + (hh - a.Hq)) * DH;
+                    if (on && dst) {
+                        *reinterpret_cast<uint4*>(dst + l * 8) = bytes(x);
+                        *reinterpret_cast<uint4*>(dst + DH / 2 + l * 8) = bytes(y);
+                    }
+                }
+            }
+            if (__all_sync(0xffffffffu, is == 0)) continue;
+            // the extremes of the first and the second 64 dims (dh 64: of all)
+            auto low = [](const float2 (&v)[4]) {
+                return min_nan(min_nan(min_nan(v[0].x, v[0].y), min_nan(v[1].x, v[1].y)),
+                               min_nan(min_nan(v[2].x, v[2].y), min_nan(v[3].x, v[3].y)));
+            };
+            auto high = [](const float2 (&v)[4]) {
+                return max_nan(max_nan(max_nan(v[0].x, v[0].y), max_nan(v[1].x, v[1].y)),
+                               max_nan(max_nan(v[2].x, v[2].y), max_nan(v[3].x, v[3].y)));
+            };
+            float mn = low(x), mx = high(x), mn1 = low(y), mx1 = high(y);
+            uint32_t side0, side1;
+            if constexpr (DH == 128) {  // lanes 0-3 of a head go on with the first group, lanes 4-7 with the second
+                const bool second = l >= 4;
+                const float mn2 = __shfl_xor_sync(0xffffffffu, second ? mn : mn1, 4);
+                const float mx2 = __shfl_xor_sync(0xffffffffu, second ? mx : mx1, 4);
+                mn = min_nan(second ? mn1 : mn, mn2);
+                mx = max_nan(second ? mx1 : mx, mx2);
+            } else {
+                mn = min_nan(mn, mn1);
+                mx = max_nan(mx, mx1);
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            }
+            const uint32_t side = side_of(mn, mx);
+            if constexpr (DH == 128) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, side, 4);
+                side0 = l >= 4 ? other : side;
+                side1 = l >= 4 ? side : other;
+            } else {
+                side0 = side1 = side;
+            }
+            const uint32_t c0 = codes_of(x, side0), c1 = codes_of(y, side1);
+            if (on && is > 0 && at.page >= 0) {
+                uint8_t* base = (is == 2 ? a.v_pages : a.k_pages) +
+                                (size_t)(at.page + (hh - a.Hq - (is == 2 ? a.Hkv : 0))) * p4_page_bytes(1 << page_log, DH);
+                uint32_t* codes = reinterpret_cast<uint32_t*>(base + (size_t)at.row * (DH / 2));
+                codes[l] = c0;
+                codes[DH / 16 + l] = c1;
+                uint32_t* sd = reinterpret_cast<uint32_t*>(base + ((size_t)(DH / 2) << page_log)) + at.row * (DH / kP4Group);
+                if (l == 0) sd[0] = side0;
+                if (DH == 128 && l == 4) sd[1] = side1;
+            }
         }
     }
 }
@@ -266,9 +380,14 @@ cudaError_t append_paged4_launch(const __nv_bfloat16* qkv, long long ld, int N, 
     AppendArgs a{qkv, ld, {cu, start, S}, {nullptr, nullptr, table, n_pages, max_pages, log2_of(page)}, N, Hq, Hkv, q_gamma,
                  k_gamma, eps, cos_sin, n_pos, q_out, k_out, static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages),
                  err};
-    const int threads = std::min(512, ((Hq + 2 * Hkv) * (dh / 16) + 31) / 32 * 32);
-    return dh == 128 ? launch_pdl(append_paged4_kernel<128>, dim3(N), dim3(threads), 0, st, a)
-                     : launch_pdl(append_paged4_kernel<64>, dim3(N), dim3(threads), 0, st, a);
+    // A warp a piece of a token while that does not fill the GPU; then fewer pieces apart, and several tokens a warp.
+    const long long pieces = (Hq + 2 * Hkv + 512 / dh - 1) / (512 / dh), room = 16LL * device_sm_count();
+    const int parts = (int)std::min<long long>(pieces, std::max<long long>(1, room / N));
+    const int per = (int)std::min<long long>(8, std::max<long long>(1, N / room));
+    const long long warps = ((long long)N + per - 1) / per * parts;
+    const dim3 grid((unsigned)((warps + 3) / 4));
+    return dh == 128 ? launch_pdl(append_paged4_kernel<128>, grid, dim3(128), 0, st, a, per, parts)
+                     : launch_pdl(append_paged4_kernel<64>, grid, dim3(128), 0, st, a, per, parts);
 }
 
 cudaError_t read_paged4_launch(const void* k_pages, const void* v_pages, int n_pages, int page, const int* table, int max_pages,
