@@ -141,8 +141,9 @@ struct AppendArgs {
 //   (a, b) -> (r (g_a cos a - g_b sin b), r (g_b cos b + g_a sin a)) in fp32, rounded once;
 // the products of gains and angles are made once a token and kind of head. The next piece's values, and the next token's
 // angles, are on their way meanwhile; a sequence is looked up once, then followed from token to token.
+constexpr int AP_AHEAD = 2, AP_CTAS = 5;  // CTAs of four warps an SM
 template <int DH>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, AP_CTAS)
     append_paged4_kernel(const AppendArgs a, int per, int parts) {
     constexpr int LPH = DH / 16, HPW = 32 / LPH;
     const int lane = threadIdx.x & 31, l = lane % LPH;
@@ -150,17 +151,34 @@ __global__ void __launch_bounds__(128)
     const int chunk = (int)((unsigned)w / (unsigned)parts), part = w - chunk * parts;
     const int t0 = chunk * per, t1 = min(a.N, t0 + per);
     const int heads = a.Hq + 2 * a.Hkv, pieces = (heads + HPW - 1) / HPW;
-    const int page_log = a.cache.page_log;
+    const int page_log = a.cache.page_log, head_bytes = (int)p4_page_bytes(1 << page_log, DH);
+    __shared__ float gains[2][DH];  // of queries and keys
+    __shared__ float4 turn[4][2][8][LPH];  // [warp][queries, keys]: the products of gains and angles of the token, 32 floats a lane l
     pdl_wait();
     pdl_trigger();
+    for (int i = threadIdx.x; i < 2 * DH; i += blockDim.x) {
+        const __nv_bfloat16* gamma = i < DH ? a.q_gamma : a.k_gamma;
+        gains[0][i] = gamma ? bf16f(gamma[i % DH]) : 1.f;
+    }
+    __syncthreads();
     if (t0 >= t1) return;
-    uint4 raw[2];
-    auto load = [&](int t, int piece) {
-        const __nv_bfloat16* x = a.qkv + (size_t)t * a.ld + (size_t)min(piece * HPW + lane / LPH, heads - 1) * DH + l * 8;
-        raw[0] = __ldg(reinterpret_cast<const uint4*>(x));
-        raw[1] = __ldg(reinterpret_cast<const uint4*>(x + DH / 2));
+    const int hl = lane / LPH;  // this lane's head of a piece
+    uint4 raw[AP_AHEAD][2];  // of the pieces ahead
+    const __nv_bfloat16* load_row = a.qkv + (size_t)t0 * a.ld + l * 8;
+    int load_left = t1 - t0, load_piece = part;
+    auto load = [&](uint4 (&to)[2]) {  // the next piece of this warp, if there is one
+        if (load_left <= 0) return;
+        const __nv_bfloat16* x = load_row + min(load_piece * HPW + hl, heads - 1) * DH;
+        to[0] = __ldg(reinterpret_cast<const uint4*>(x));
+        to[1] = __ldg(reinterpret_cast<const uint4*>(x + DH / 2));
+        if ((load_piece += parts) >= pieces) {
+            load_piece = part;
+            load_row += a.ld;
+            --load_left;
+        }
     };
-    load(t0, part);
+#pragma unroll
+    for (int i = 0; i < AP_AHEAD; ++i) load(raw[i]);
     int seq = -1, seq_end = t0;  // the sequence at hand and the row behind it
     Place pl{-1, -1, 0};
     uint4 ang[2];  // the token's cos and sin
@@ -209,72 +227,71 @@ __global__ void __launch_bounds__(128)
         const bool in = seq >= 0, rotates = in && at.slot >= 0 && at.slot < a.n_pos;
         // behind the last sequence: left as it was; no position to rotate by, or no page: flagged
         if (part == 0 && lane == 0 && a.err && in && (!rotates || at.page < 0)) atomicOr(a.err, ERR_INDEX);
-        float2 c[4], s[4];
-        floats(ang[0], c);
-        floats(ang[1], s);
+        const uint4 now[2] = {ang[0], ang[1]};
         if (t + 1 < t1) {
             place(t + 1);
             angles();
         }
-        float2 ac[4], bs[4], bc[4], as[4];  // g_a cos, -g_b sin, g_b cos, g_a sin
-        int kind = -1;                      // of the head that they are for: 0 a query, 1 a key
+        __nv_bfloat16* const q_row = a.q_out + (size_t)t * a.Hq * DH + l * 8;
+        __nv_bfloat16* const k_row = a.k_out ? a.k_out + (size_t)t * a.Hkv * DH + l * 8 : nullptr;
+        uint8_t* const k_page = a.k_pages + at.page * head_bytes;
+        uint8_t* const v_page = a.v_pages + at.page * head_bytes;
+        float4(*const my_turn)[8][LPH] = turn[threadIdx.x >> 5];
+        if (rotates) {
+            __syncwarp();  // the row before is done with them
+            if (hl < 2) {  // the first head's lanes make the queries' products, the second's the keys'
+                float2 c[4], s[4];
+                floats(now[0], c);
+                floats(now[1], s);
+                const float2* g = reinterpret_cast<const float2*>(gains[hl] + l * 8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // g_a cos, -g_b sin; g_b cos, g_a sin
+                    const float2 ga = g[i], gb = g[DH / 4 + i];
+                    my_turn[hl][2 * i][l] = make_float4(ga.x * c[i].x, ga.y * c[i].y, -gb.x * s[i].x, -gb.y * s[i].y);
+                    my_turn[hl][2 * i + 1][l] = make_float4(gb.x * c[i].x, gb.y * c[i].y, ga.x * s[i].x, ga.y * s[i].y);
+                }
+            }
+            __syncwarp();
+        }
         for (int piece = part; piece < pieces; piece += parts) {
-            const int h = piece * HPW + lane / LPH;
-            const bool on = h < heads && rotates;
-            const int hh = min(h, heads - 1);
+            const int h = piece * HPW + hl, hh = min(h, heads - 1);
+            const bool on = h < heads;
             float2 x[4], y[4];
-            floats(raw[0], x);
-            floats(raw[1], y);
-            if (piece + parts < pieces) load(t, piece + parts);
-            else if (t + 1 < t1) load(t + 1, part);
+            floats(raw[0][0], x);
+            floats(raw[0][1], y);
+#pragma unroll
+            for (int i = 0; i + 1 < AP_AHEAD; ++i) {
+                raw[i][0] = raw[i + 1][0];
+                raw[i][1] = raw[i + 1][1];
+            }
+            load(raw[AP_AHEAD - 1]);
             if (!rotates) continue;
             const int is = hh < a.Hq ? 0 : hh < a.Hq + a.Hkv ? 1 : 2;
-            if (__any_sync(0xffffffffu, is < 2)) {
-                const __nv_bfloat16* gamma = is == 0 ? a.q_gamma : is == 1 ? a.k_gamma : nullptr;
-                if (__any_sync(0xffffffffu, is != kind && is < 2)) {
-                    kind = is;
-                    float2 ga[4], gb[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) ga[i] = gb[i] = make_float2(1.f, 1.f);
-                    if (gamma) {
-                        floats(__ldg(reinterpret_cast<const uint4*>(gamma + l * 8)), ga);
-                        floats(__ldg(reinterpret_cast<const uint4*>(gamma + DH / 2 + l * 8)), gb);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        ac[i] = mul2(ga[i], c[i]);
-                        as[i] = mul2(ga[i], s[i]);
-                        bc[i] = mul2(gb[i], c[i]);
-                        bs[i] = mul2(gb[i], make_float2(-s[i].x, -s[i].y));
-                    }
-                }
+            if (piece * HPW < a.Hq + a.Hkv) {  // (the same for the whole warp, as is what follows but for the heads' kinds)
                 float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) ss = fma2(y[i], y[i], fma2(x[i], x[i], ss));
                 float sum = ss.x + ss.y;
 #pragma unroll
                 for (int o = 1; o < LPH; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                const float r = gamma ? rsqrtf(sum / DH + a.eps) : 1.f;
+                const float r = (is == 0 ? a.q_gamma : a.k_gamma) ? rsqrtf(sum * (1.f / DH) + a.eps) : 1.f;
                 if (is < 2) {
                     const float2 r2 = make_float2(r, r);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        const float4 u = my_turn[is][2 * i][l], v = my_turn[is][2 * i + 1][l];
                         const float2 p = x[i], q = y[i];
-                        x[i] = mul2(fma2(ac[i], p, mul2(bs[i], q)), r2);
-                        y[i] = mul2(fma2(bc[i], q, mul2(as[i], p)), r2);
+                        x[i] = mul2(fma2(make_float2(u.x, u.y), p, mul2(make_float2(u.z, u.w), q)), r2);
+                        y[i] = mul2(fma2(make_float2(v.x, v.y), q, mul2(make_float2(v.z, v.w), p)), r2);
                     }
-                    __nv_bfloat16* dst = nullptr;
-                    if (is == 0)
-                        dst = a.q_out + ((size_t)t * a.Hq + hh) * DH;
-                    else if (a.k_out)
-                        dst = a.k_out + ((size_t)t * a.Hkv + (hh - a.Hq)) * DH;
+                    __nv_bfloat16* dst = is == 0 ? q_row + hh * DH : k_row ? k_row + (hh - a.Hq) * DH : nullptr;
                     if (on && dst) {
-                        *reinterpret_cast<uint4*>(dst + l * 8) = bytes(x);
-                        *reinterpret_cast<uint4*>(dst + DH / 2 + l * 8) = bytes(y);
+                        *reinterpret_cast<uint4*>(dst) = bytes(x);
+                        *reinterpret_cast<uint4*>(dst + DH / 2) = bytes(y);
                     }
                 }
             }
-            if (__all_sync(0xffffffffu, is == 0)) continue;
+            if ((piece + 1) * HPW <= a.Hq) continue;
             // the extremes of the first and the second 64 dims (dh 64: of all)
             auto low = [](const float2 (&v)[4]) {
                 return min_nan(min_nan(min_nan(v[0].x, v[0].y), min_nan(v[1].x, v[1].y)),
@@ -311,12 +328,11 @@ __global__ void __launch_bounds__(128)
             }
             const uint32_t c0 = codes_of(x, side0), c1 = codes_of(y, side1);
             if (on && is > 0 && at.page >= 0) {
-                uint8_t* base = (is == 2 ? a.v_pages : a.k_pages) +
-                                (size_t)(at.page + (hh - a.Hq - (is == 2 ? a.Hkv : 0))) * p4_page_bytes(1 << page_log, DH);
-                uint32_t* codes = reinterpret_cast<uint32_t*>(base + (size_t)at.row * (DH / 2));
+                uint8_t* base = is == 2 ? v_page + (hh - a.Hq - a.Hkv) * head_bytes : k_page + (hh - a.Hq) * head_bytes;
+                uint32_t* codes = reinterpret_cast<uint32_t*>(base + at.row * (DH / 2));
                 codes[l] = c0;
                 codes[DH / 16 + l] = c1;
-                uint32_t* sd = reinterpret_cast<uint32_t*>(base + ((size_t)(DH / 2) << page_log)) + at.row * (DH / kP4Group);
+                uint32_t* sd = reinterpret_cast<uint32_t*>(base + (DH / 2 << page_log)) + at.row * (DH / kP4Group);
                 if (l == 0) sd[0] = side0;
                 if (DH == 128 && l == 4) sd[1] = side1;
             }
@@ -381,9 +397,9 @@ cudaError_t append_paged4_launch(const __nv_bfloat16* qkv, long long ld, int N, 
                  k_gamma, eps, cos_sin, n_pos, q_out, k_out, static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages),
                  err};
     // A warp a piece of a token while that does not fill the GPU; then fewer pieces apart, and several tokens a warp.
-    const long long pieces = (Hq + 2 * Hkv + 512 / dh - 1) / (512 / dh), room = 16LL * device_sm_count();
+    const long long pieces = (Hq + 2 * Hkv + 512 / dh - 1) / (512 / dh), room = 4LL * AP_CTAS * device_sm_count();
     const int parts = (int)std::min<long long>(pieces, std::max<long long>(1, room / N));
-    const int per = (int)std::min<long long>(8, std::max<long long>(1, N / room));
+    const int per = (int)((N + room - 1) / room);
     const long long warps = ((long long)N + per - 1) / per * parts;
     const dim3 grid((unsigned)((warps + 3) / 4));
     return dh == 128 ? launch_pdl(append_paged4_kernel<128>, grid, dim3(128), 0, st, a, per, parts)
