@@ -499,15 +499,12 @@ struct PsLayout {
     static constexpr int SMEM = XCH_OFF + (ALT ? 6 * TC_BM * 4 : 0) + 1024;
 };
 
-// PACKED: sequences of different lengths packed along the rows of q and of k, v (tensor maps over [row][64-column block]).
-// An item is a (query tile, head) of the list that attn_packed_plan_kernel left, longest key ranges first; rows of another
-// sequence that its tiles reach into are masked (keys), zeroed (values) and not stored (queries).
-template <int DH, bool SPEC, bool ALT, bool PACKED>
+template <int DH, bool SPEC, bool ALT>
 __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
     attn_prefill_persistent_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                                    const __grid_constant__ CUtensorMap tmV, int T, int Hq, int Hkv, int B,
                                    const int* __restrict__ len0p, const int* __restrict__ meta, int window, int ring,
-                                   __nv_bfloat16* __restrict__ out, int* err, const PackedTiles pk) {
+                                   __nv_bfloat16* __restrict__ out, int* err) {
     using Ly = PsLayout<DH, ALT>;
     constexpr int NCH = Ly::NCH;
     constexpr uint32_t IDESC_S = idesc_bf16(TC_BM, TC_BN);
@@ -536,6 +533,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n_qt = (T + TC_BM - 1) / TC_BM;
     const int per_qt = B * Hq;
+    const int n_items = n_qt * per_qt;
     const int G = (int)gridDim.x, c = (int)blockIdx.x;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -575,8 +573,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
     bool ok = true;
     pdl_wait();  // Q and the cache come from the previous kernel
     pdl_trigger();
-    const int n_items = PACKED ? min(max(*pk.count, 0), pk.capacity) * Hq : n_qt * per_qt;
-    const int len0 = PACKED ? 0 : *len0p;
+    const int len0 = *len0p;
     int ps_meta = 0, psh = 0;
     if (meta) {
         ps_meta = meta[0];
@@ -586,24 +583,11 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
     // The parameters of this CTA's round-th item (n_tiles = 0 when it has none left).
     struct Item {
         int b, h, q0, q_end, n_valid, j_lo, ja, jb, n_tiles, ps, pe;
-        int pos0;  // PACKED: key position of query row q0 (b: the sequence's first key row)
     };
     auto item_of = [&](int round) -> Item {
         Item it{};
         const int k = round * G + ((round & 1) ? G - 1 - c : c);
         if (k >= n_items) return it;
-        if constexpr (PACKED) {
-            const int rank = (int)((unsigned)k / (unsigned)Hq);
-            const int4 v = __ldg(pk.items + rank);
-            it.h = k - rank * Hq;
-            it.q0 = v.x;
-            it.q_end = min(v.x + v.y, T);
-            it.b = v.z;
-            it.pos0 = v.w;
-            it.n_valid = min(max(v.w + v.y, 0), pk.max_keys);
-            it.n_tiles = max(1, (it.n_valid + TC_BN - 1) / TC_BN);  // without a key: one tile, all of it masked
-            return it;
-        }
         const int qt = n_qt - 1 - k / per_qt, rem = k % per_qt;
         it.b = rem / Hq;
         it.h = rem % Hq;
@@ -619,23 +603,8 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
         it.n_tiles = n_end - it.j_lo - (it.jb - it.ja);
         return it;
     };
-    auto first_pos = [&](const Item& it) { return PACKED ? it.pos0 : len0 + it.q0; };
-    // A role's items; a packed one comes from memory and is read one round ahead (not by the softmax warps of the ALT
-    // form, whose registers are full).
-    const bool reads_ahead = PACKED && (!ALT || warp < 4);
-    Item ahead{};
-    auto begin_items = [&]() {
-        if (reads_ahead) ahead = item_of(0);
-    };
-    auto next_item = [&](int round) -> Item {
-        if (!reads_ahead) return item_of(round);
-        const Item it = ahead;
-        ahead = item_of(round + 1);
-        return it;
-    };
     auto tile_j = [](const Item& it, int i) { return it.j_lo + i < it.ja ? it.j_lo + i : it.j_lo + i + (it.jb - it.ja); };
 
-    begin_items();
     constexpr int W_VTMA = ALT ? 2 : 6, W_PV = ALT ? 3 : 7;
     const bool producer = ALT ? warp < 4 : (warp < 2 || warp >= 6);
     // with ALT the register split dominates each role's code, so that ptxas allocates it under the
@@ -647,16 +616,13 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             if (lane == 0) {
                 int g = 0;
                 for (int round = 0; ok; ++round) {
-                    const Item it = next_item(round);
+                    const Item it = item_of(round);
                     if (it.n_tiles == 0) break;
                     const int jkv = it.h / (Hq / Hkv);
                     if (!mbar_wait_suspend(q_empty, (round & 1) ^ 1, abort_flag)) { ok = false; break; }
                     mbar_expect_tx(q_full, Ly::Q_BYTES);
-                    if constexpr (PACKED)
-                        tma_load_3d(smem + Ly::Q_OFF, &tmQ, q_full, 0, it.q0, it.h * NCH);
-                    else
-                        for (int cc = 0; cc < NCH; ++cc)
-                            tma_load_3d(smem + Ly::Q_OFF + cc * TC_BM * 128, &tmQ, q_full, cc * 64, it.q0, it.b * Hq + it.h);
+                    for (int cc = 0; cc < NCH; ++cc)
+                        tma_load_3d(smem + Ly::Q_OFF + cc * TC_BM * 128, &tmQ, q_full, cc * 64, it.q0, it.b * Hq + it.h);
                     for (int i = 0; i < it.n_tiles; ++i, ++g) {
                         const int s = g % PS_KST, j = tile_j(it, i);
                         const uint32_t free_ph = ((g / PS_KST) & 1) ^ 1;
@@ -664,11 +630,8 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                         const int z = (j * TC_BN < psh ? 0 : it.b) * Hkv + jkv;
                         if (!mbar_wait_suspend(&k_empty[s], free_ph, abort_flag)) { ok = false; break; }
                         mbar_expect_tx(&k_full[s], Ly::KV_BYTES);
-                        if constexpr (PACKED)
-                            tma_load_3d(smem + Ly::K_OFF + s * Ly::KV_BYTES, &tmK, &k_full[s], 0, it.b + j * TC_BN, jkv * NCH);
-                        else
-                            for (int cc = 0; cc < NCH; ++cc)
-                                tma_load_3d(smem + Ly::K_OFF + s * Ly::KV_BYTES + cc * TC_BN * 128, &tmK, &k_full[s], cc * 64, y, z);
+                        for (int cc = 0; cc < NCH; ++cc)
+                            tma_load_3d(smem + Ly::K_OFF + s * Ly::KV_BYTES + cc * TC_BN * 128, &tmK, &k_full[s], cc * 64, y, z);
                     }
                 }
             }
@@ -679,7 +642,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             if (lane == 0) {
                 int g = 0;
                 for (int round = 0; ok; ++round) {
-                    const Item it = next_item(round);
+                    const Item it = item_of(round);
                     if (it.n_tiles == 0) break;
                     const int jkv = it.h / (Hq / Hkv);
                     for (int i = 0; i < it.n_tiles; ++i, ++g) {
@@ -689,11 +652,8 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                         const int z = (j * TC_BN < psh ? 0 : it.b) * Hkv + jkv;
                         if (!mbar_wait_suspend(&v_empty[s], free_ph, abort_flag)) { ok = false; break; }
                         mbar_expect_tx(&v_full[s], Ly::KV_BYTES);
-                        if constexpr (PACKED)
-                            tma_load_3d(smem + Ly::V_OFF + s * Ly::KV_BYTES, &tmV, &v_full[s], 0, it.b + j * TC_BN, jkv * NCH);
-                        else
-                            for (int cc = 0; cc < NCH; ++cc)
-                                tma_load_3d(smem + Ly::V_OFF + s * Ly::KV_BYTES + cc * TC_BN * 128, &tmV, &v_full[s], cc * 64, y, z);
+                        for (int cc = 0; cc < NCH; ++cc)
+                            tma_load_3d(smem + Ly::V_OFF + s * Ly::KV_BYTES + cc * TC_BN * 128, &tmV, &v_full[s], cc * 64, y, z);
                     }
                 }
             }
@@ -705,7 +665,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             if (lane == 0) {
                 int g = 0;  // tiles of earlier items
                 for (int round = 0; ok; ++round) {
-                    const Item it = next_item(round);
+                    const Item it = item_of(round);
                     const int nt = it.n_tiles;
                     if (nt == 0) break;
                     if (!mbar_wait_suspend(q_full, round & 1, abort_flag)) { ok = false; break; }
@@ -739,7 +699,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             // tensor memory), V from value stage gi & 1
             int g = 0;
             for (int round = 0; ok; ++round) {
-                const Item it = next_item(round);
+                const Item it = item_of(round);
                 const int nt = it.n_tiles;
                 if (nt == 0) break;
                 for (int i = 0; ok && i < nt; ++i) {
@@ -804,7 +764,7 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             const Item it = item_of(round);
             const int nt = it.n_tiles;
             if (nt == 0) break;
-            const int t = it.q0 + row, pos = first_pos(it) + row;
+            const int t = it.q0 + row, pos = len0 + t;
             volatile float* m_row = m_sh + (round & 1) * TC_BM + row;
             float m_l = -INFINITY, l = 0.f;  // this warpgroup's share of the row sum, at scale m_l
             for (int i = ((g & 1) == wg) ? 0 : 1; i < nt; i += 2) {
@@ -819,9 +779,9 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     tmem_ld_32x32b_x32(tm_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
                 tmem_ld_wait();
                 const int k0 = j * TC_BN;
-                const bool diag = k0 + TC_BN - 1 > first_pos(it);
-                const bool pads = !PACKED && k0 < it.pe && k0 + TC_BN > it.ps;
-                const bool old = !PACKED && window > 0 && k0 < len0 + it.q_end - window;
+                const bool diag = k0 + TC_BN - 1 > len0 + it.q0;
+                const bool pads = k0 < it.pe && k0 + TC_BN > it.ps;
+                const bool old = window > 0 && k0 < len0 + it.q_end - window;
                 if (pads || old) {
                     // visible: (i <= lim, not padding, inside the window) or the query itself; branch-free
                     const int lim = pos - k0;
@@ -944,15 +904,14 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             if (!ok) break;
             // O / l to the output, this warpgroup's half of the columns, then hand the accumulator back
             tc_fence_after();
-            const float l_all = l_row[0] + l_row[TC_BM];
-            const float inv = PACKED && l_all == 0.f ? 0.f : 1.f / l_all;  // (a packed row without a key: zeros)
-            __nv_bfloat16* orow = out + ((PACKED ? (size_t)t : (size_t)it.b * T + t) * Hq + it.h) * DH + wg * (DH / 2);
+            const float inv = 1.f / (l_row[0] + l_row[TC_BM]);
+            __nv_bfloat16* orow = out + (((size_t)it.b * T + t) * Hq + it.h) * DH + wg * (DH / 2);
 #pragma unroll 1
             for (int cc = 0; cc < DH / 64; ++cc) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(tm_o + wg * (DH / 2) + cc * 32, o);
                 tmem_ld_wait();
-                if (t < (PACKED ? it.q_end : T)) {
+                if (t < T) {
                     uint32_t wv[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -979,10 +938,10 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
         auto pv_done = [&](int k) -> bool { return mbar_wait_suspend(&r_free[k % NR], (k / NR) & 1, abort_flag); };
         int g = 0;
         for (int round = 0; ok; ++round) {
-            const Item it = next_item(round);
+            const Item it = item_of(round);
             const int nt = it.n_tiles;
             if (nt == 0) break;
-            const int t = it.q0 + row, pos = first_pos(it) + row;
+            const int t = it.q0 + row, pos = len0 + t;
             float m_used = -INFINITY, l = 0.f;
             for (int i = 0; i < nt; ++i) {
                 const int gi = g + i, r = gi % NR;
@@ -996,9 +955,9 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
                     tmem_ld_32x32b_x32(tm_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
                 tmem_ld_wait();
                 const int k0 = j * TC_BN;
-                const bool diag = k0 + TC_BN - 1 > first_pos(it);
-                const bool pads = !PACKED && k0 < it.pe && k0 + TC_BN > it.ps;
-                const bool old = !PACKED && window > 0 && k0 < len0 + it.q_end - window;
+                const bool diag = k0 + TC_BN - 1 > len0 + it.q0;
+                const bool pads = k0 < it.pe && k0 + TC_BN > it.ps;
+                const bool old = window > 0 && k0 < len0 + it.q_end - window;
                 if (pads || old) {
                     // visible: (i <= lim, not padding, inside the window) or the query itself; branch-free
                     const int lim = pos - k0;
@@ -1102,14 +1061,14 @@ __global__ void __launch_bounds__(ps_threads<ALT>(), 1)
             if (!ok) break;
             // O / l to the output, then hand the accumulator back to the MMA warp
             tc_fence_after();
-            __nv_bfloat16* orow = out + ((PACKED ? (size_t)t : (size_t)it.b * T + t) * Hq + it.h) * DH;
-            const float inv = PACKED && l == 0.f ? 0.f : 1.f / l;
+            __nv_bfloat16* orow = out + (((size_t)it.b * T + t) * Hq + it.h) * DH;
+            const float inv = 1.f / l;
 #pragma unroll 1
             for (int cc = 0; cc < DH / 32; ++cc) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(tm_o + cc * 32, o);
                 tmem_ld_wait();
-                if (t < (PACKED ? it.q_end : T)) {
+                if (t < T) {
                     uint32_t wv[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
@@ -1587,11 +1546,11 @@ constexpr int kAltMinKeys = 8192;
 
 // setmaxnreg.inc waits until the registers it asks for are free, so the ALT form runs only when the
 // compiled kernel was given at least the registers per thread its split hands out (checked once).
-template <int DH, bool PACKED>
+template <int DH>
 bool alt_registers_cover_split() {
     static const bool ok = [] {
         cudaFuncAttributes fa{};
-        if (cudaFuncGetAttributes(&fa, attn_prefill_persistent_kernel<DH, true, true, PACKED>) != cudaSuccess) return false;
+        if (cudaFuncGetAttributes(&fa, attn_prefill_persistent_kernel<DH, true, true>) != cudaSuccess) return false;
         const long long have = (long long)ps_threads<true>() * fa.numRegs;
         const long long need = 128LL * PS_REG_PRODUCER + 256LL * PS_REG_SOFTMAX;
         return have >= need;
@@ -1623,119 +1582,14 @@ cudaError_t prefill_launch_dh(const __nv_bfloat16* q, const __nv_bfloat16* kc, c
         return prefill_launch_nh<DH, 1>(tq, tk, tv, B, T, Hq, Hkv, len0, sm, out, err, split, max_chunks, ws, st);
     const long long items = (long long)((T + TC_BM - 1) / TC_BM) * Hq * B;
     const unsigned grid = (unsigned)std::min<long long>(items, device_sm_count());
-    if (kv_hint >= kAltMinKeys && alt_registers_cover_split<DH, false>())
-        return launch_pdl(attn_prefill_persistent_kernel<DH, true, true, false>, dim3(grid), dim3(ps_threads<true>()),
-                          PsLayout<DH, true>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err, PackedTiles{});
+    if (kv_hint >= kAltMinKeys && alt_registers_cover_split<DH>())
+        return launch_pdl(attn_prefill_persistent_kernel<DH, true, true>, dim3(grid), dim3(ps_threads<true>()),
+                          PsLayout<DH, true>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err);
     if (kv_hint >= kSpecMinKeys)
-        return launch_pdl(attn_prefill_persistent_kernel<DH, true, false, false>, dim3(grid), dim3(ps_threads<false>()),
-                          PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err, PackedTiles{});
-    return launch_pdl(attn_prefill_persistent_kernel<DH, false, false, false>, dim3(grid), dim3(ps_threads<false>()),
-                      PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err, PackedTiles{});
-}
-
-// ------------------------------------------------------------------------------------- packed sequences
-// The work list of a packed batch: for every 128-row query tile (first query row, rows, the sequence's first key row, key
-// position of the first query row), the longest key ranges first (a counting sort by key tiles, those past kPlanBins - 1
-// together). One CTA, a warp a sequence. The order of equal tiles depends on timing; it decides which SM
-// computes a tile, not its result. 16 sequences of 300 tokens over 4,096 keys each: 6 us, once for all layers.
-constexpr int kPlanThreads = 1024, kPlanBins = 1024, kPlanHeader = 256;
-__global__ void __launch_bounds__(kPlanThreads)
-    attn_packed_plan_kernel(const int* __restrict__ cu_q, const int* __restrict__ cu_k, int S, int Nq, int Nk, int* count,
-                            int4* items, int capacity, int* err) {
-    __shared__ int bins[kPlanBins], warp_sum[kPlanThreads / 32];
-    __shared__ int4 seqs[kPlanThreads];  // first query row, queries (0: left out), first key row, keys in front of the queries
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_wait();
-    pdl_trigger();
-    for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) bins[i] = 0;
-    auto each = [&](auto take) {  // take(item, bin) for every tile
-        int end = 0;              // of the query rows of the sequences so far
-        for (int base = 0; base < S; base += kPlanThreads) {
-            const int s = base + threadIdx.x;
-            int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-            if (s < S) {
-                q0 = __ldg(cu_q + s);
-                q1 = __ldg(cu_q + s + 1);
-                k0 = __ldg(cu_k + s);
-                k1 = __ldg(cu_k + s + 1);
-            }
-            // the largest bound before this one: a sequence that begins before it would write rows of another
-            int top = q0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, top, o);
-                if (lane >= o) top = max(top, v);
-            }
-            __syncthreads();  // the previous round's sequences are done
-            if (lane == 31) warp_sum[warp] = top;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) top = max(top, warp_sum[w]);
-            top = max(top, end);
-            for (int w = 0; w < kPlanThreads / 32; ++w) end = max(end, warp_sum[w]);
-            const bool ok = q0 >= top && q1 >= q0 && q1 <= Nq && k0 >= 0 && k1 >= k0 && k1 <= Nk;
-            if (s < S && !ok && err) atomicOr(err, ERR_INDEX);
-            seqs[threadIdx.x] = make_int4(q0, ok ? q1 - q0 : 0, k0, ok ? k1 - k0 - (q1 - q0) : 0);
-            __syncthreads();
-            for (int i = warp; i < min(kPlanThreads, S - base); i += kPlanThreads / 32) {
-                const int4 v = seqs[i];
-                for (int t = lane; t * TC_BM < v.y; t += 32) {
-                    const int rows = min(TC_BM, v.y - t * TC_BM), pos = v.w + t * TC_BM;
-                    const int tiles = (max(pos + rows, 0) + TC_BN - 1) / TC_BN;
-                    take(make_int4(v.x + t * TC_BM, rows, v.z, pos), kPlanBins - 1 - min(tiles, kPlanBins - 1));
-                }
-            }
-        }
-    };
-    __syncthreads();
-    each([&](const int4&, int bin) { atomicAdd(&bins[bin], 1); });
-    __syncthreads();
-    static_assert(kPlanBins == kPlanThreads, "a thread a bin");
-    const int mine = bins[threadIdx.x];
-    int sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-    }
-    if (lane == 31) warp_sum[warp] = sum;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) sum += warp_sum[w];
-    bins[threadIdx.x] = sum - mine;
-    if (threadIdx.x == kPlanThreads - 1) *count = min(sum, capacity);  // (no more: the sequences do not overlap)
-    __syncthreads();
-    each([&](const int4& item, int bin) {
-        const int at = atomicAdd(&bins[bin], 1);
-        if (at < capacity) items[at] = item;
-    });
-}
-
-// [row][heads * dh / 64][64] with rows ld elements apart: boxes of 128 rows of one head.
-bool encode_tmap_packed(CUtensorMap* map, const void* base, int dh, int heads, long long rows, long long ld) {
-    return encode_tmap_bf16_rows(map, base, (uint64_t)heads * (dh / 64), (uint64_t)std::max(1LL, rows), (uint64_t)ld * 2,
-                                 TC_BM, (uint32_t)(dh / 64));
-}
-
-template <int DH>
-cudaError_t packed_launch_dh(const PackedCall& c, cudaStream_t st) {
-    CUtensorMap tq, tk, tv;
-    // without a key row there is nothing to read: any memory serves as the masked tile
-    const bool none = c.Nk == 0;
-    if (!encode_tmap_packed(&tq, c.q, DH, c.Hq, c.Nq, c.ldq) ||
-        !encode_tmap_packed(&tk, none ? c.q : c.k, DH, c.Hkv, none ? 1 : c.Nk, none ? c.ldq : c.ldk) ||
-        !encode_tmap_packed(&tv, none ? c.q : c.v, DH, c.Hkv, none ? 1 : c.Nk, none ? c.ldq : c.ldv))
-        return cudaErrorInvalidValue;
-    const PackedTiles pk{reinterpret_cast<const int4*>(static_cast<const char*>(c.plan) + kPlanHeader),
-                         static_cast<const int*>(c.plan), c.capacity, c.Nk};
-    const unsigned grid = (unsigned)std::min<long long>((long long)c.capacity * c.Hq, device_sm_count());
-    auto launch = [&](auto kernel, int threads, size_t smem) {
-        return launch_pdl(kernel, dim3(grid), dim3(threads), smem, st, tq, tk, tv, c.Nq, c.Hq, c.Hkv, 1, nullptr, nullptr, 0,
-                          0, c.out, c.err, pk);
-    };
-    if (c.longest >= kAltMinKeys && alt_registers_cover_split<DH, true>())
-        return launch(attn_prefill_persistent_kernel<DH, true, true, true>, ps_threads<true>(), PsLayout<DH, true>::SMEM);
-    if (c.longest >= kSpecMinKeys)
-        return launch(attn_prefill_persistent_kernel<DH, true, false, true>, ps_threads<false>(), PsLayout<DH, false>::SMEM);
-    return launch(attn_prefill_persistent_kernel<DH, false, false, true>, ps_threads<false>(), PsLayout<DH, false>::SMEM);
+        return launch_pdl(attn_prefill_persistent_kernel<DH, true, false>, dim3(grid), dim3(ps_threads<false>()),
+                          PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err);
+    return launch_pdl(attn_prefill_persistent_kernel<DH, false, false>, dim3(grid), dim3(ps_threads<false>()),
+                      PsLayout<DH, false>::SMEM, st, tq, tk, tv, T, Hq, Hkv, B, len0, sm.meta, sm.window, sm.ring, out, err);
 }
 
 }  // namespace
@@ -1756,23 +1610,6 @@ cudaError_t attn_prefill_launch(const __nv_bfloat16* q, const __nv_bfloat16* kc,
     if (dh == 64)
         return prefill_launch_dh<64>(q, kc, vc, B, T, Hq, Hkv, cap, len0, sm, out, err, split, max_chunks, ws, heads,
                                      kv_hint, st);
-    return cudaErrorInvalidValue;
-}
-
-size_t attn_packed_plan_bytes(int Nq, int S) {
-    return kPlanHeader + ((size_t)(Nq + TC_BM - 1) / TC_BM + (size_t)S) * sizeof(int4);
-}
-int attn_packed_capacity(size_t bytes) {
-    return bytes < kPlanHeader ? 0 : (int)std::min<size_t>((bytes - kPlanHeader) / sizeof(int4), 0x7fffffff);
-}
-cudaError_t attn_packed_plan_launch(const int* cu_q, const int* cu_k, int S, int Nq, int Nk, void* plan, int capacity, int* err,
-                                    cudaStream_t st) {
-    return launch_pdl(attn_packed_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, cu_q, cu_k, S, Nq, Nk,
-                      static_cast<int*>(plan), reinterpret_cast<int4*>(static_cast<char*>(plan) + kPlanHeader), capacity, err);
-}
-cudaError_t attn_packed_launch(const PackedCall& c, int dh, cudaStream_t st) {
-    if (dh == 128) return packed_launch_dh<128>(c, st);
-    if (dh == 64) return packed_launch_dh<64>(c, st);
     return cudaErrorInvalidValue;
 }
 
@@ -1846,24 +1683,16 @@ cudaError_t decode_prepare_dh() {
 cudaError_t attention_prepare() {
     const void* fns[] = {(const void*)attn_prefill_tc_kernel<128, 1>, (const void*)attn_prefill_tc_kernel<128, 2>,
                          (const void*)attn_prefill_tc_kernel<64, 1>,  (const void*)attn_prefill_tc_kernel<64, 2>,
-                         (const void*)attn_prefill_persistent_kernel<128, false, false, false>,
-                         (const void*)attn_prefill_persistent_kernel<64, false, false, false>,
-                         (const void*)attn_prefill_persistent_kernel<128, true, false, false>,
-                         (const void*)attn_prefill_persistent_kernel<64, true, false, false>,
-                         (const void*)attn_prefill_persistent_kernel<128, true, true, false>,
-                         (const void*)attn_prefill_persistent_kernel<64, true, true, false>,
-                         (const void*)attn_prefill_persistent_kernel<128, false, false, true>,
-                         (const void*)attn_prefill_persistent_kernel<64, false, false, true>,
-                         (const void*)attn_prefill_persistent_kernel<128, true, false, true>,
-                         (const void*)attn_prefill_persistent_kernel<64, true, false, true>,
-                         (const void*)attn_prefill_persistent_kernel<128, true, true, true>,
-                         (const void*)attn_prefill_persistent_kernel<64, true, true, true>};
+                         (const void*)attn_prefill_persistent_kernel<128, false, false>,
+                         (const void*)attn_prefill_persistent_kernel<64, false, false>,
+                         (const void*)attn_prefill_persistent_kernel<128, true, false>,
+                         (const void*)attn_prefill_persistent_kernel<64, true, false>,
+                         (const void*)attn_prefill_persistent_kernel<128, true, true>,
+                         (const void*)attn_prefill_persistent_kernel<64, true, true>};
     const int smem[] = {TcLayout<128, 1>::SMEM, TcLayout<128, 2>::SMEM, TcLayout<64, 1>::SMEM, TcLayout<64, 2>::SMEM,
                         PsLayout<128, false>::SMEM, PsLayout<64, false>::SMEM, PsLayout<128, false>::SMEM,
-                        PsLayout<64, false>::SMEM, PsLayout<128, true>::SMEM,  PsLayout<64, true>::SMEM,
-                        PsLayout<128, false>::SMEM, PsLayout<64, false>::SMEM, PsLayout<128, false>::SMEM,
                         PsLayout<64, false>::SMEM, PsLayout<128, true>::SMEM,  PsLayout<64, true>::SMEM};
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 10; ++i) {
         cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, smem[i]);
         if (e != cudaSuccess) return e;
     }

@@ -1,0 +1,566 @@
+// Causal attention over packed sequences of different lengths on the tensor cores (tcgen05, TMA): the work list of a batch, and
+// the kernel that walks it.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "rings.h"
+
+namespace q3 {
+namespace {
+
+constexpr int PK_BM = 128, PK_BN = 128;
+
+// ------------------------------------------------------------------------------------- packed sequences
+// The work list of a packed batch: for every 128-row query tile (first query row, rows, the sequence's first key row, key
+// position of the first query row), the longest key ranges first (a counting sort by key tiles, those past kPlanBins - 1
+// together). One CTA, a warp a sequence. The order of equal tiles depends on timing; it decides which SM
+// computes a tile, not its result. 16 sequences of 300 tokens over 4,096 keys each: 6 us, once for all layers.
+constexpr int kPlanThreads = 1024, kPlanBins = 1024, kPlanHeader = 256;
+__global__ void __launch_bounds__(kPlanThreads)
+    attn_packed_plan_kernel(const int* __restrict__ cu_q, const int* __restrict__ cu_k, int S, int Nq, int Nk, int* count,
+                            int4* items, int capacity, int* err) {
+    __shared__ int bins[kPlanBins], warp_sum[kPlanThreads / 32];
+    __shared__ int4 seqs[kPlanThreads];  // first query row, queries (0: left out), first key row, keys in front of the queries
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_trigger();
+    for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) bins[i] = 0;
+    auto each = [&](auto take) {  // take(item, bin) for every tile
+        int end = 0;              // of the query rows of the sequences so far
+        for (int base = 0; base < S; base += kPlanThreads) {
+            const int s = base + threadIdx.x;
+            int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+            if (s < S) {
+                q0 = __ldg(cu_q + s);
+                q1 = __ldg(cu_q + s + 1);
+                k0 = __ldg(cu_k + s);
+                k1 = __ldg(cu_k + s + 1);
+            }
+            // the largest bound before this one: a sequence that begins before it would write rows of another
+            int top = q0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, top, o);
+                if (lane >= o) top = max(top, v);
+            }
+            __syncthreads();  // the previous round's sequences are done
+            if (lane == 31) warp_sum[warp] = top;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) top = max(top, warp_sum[w]);
+            top = max(top, end);
+            for (int w = 0; w < kPlanThreads / 32; ++w) end = max(end, warp_sum[w]);
+            const bool ok = q0 >= top && q1 >= q0 && q1 <= Nq && k0 >= 0 && k1 >= k0 && k1 <= Nk;
+            if (s < S && !ok && err) atomicOr(err, ERR_INDEX);
+            seqs[threadIdx.x] = make_int4(q0, ok ? q1 - q0 : 0, k0, ok ? k1 - k0 - (q1 - q0) : 0);
+            __syncthreads();
+            for (int i = warp; i < min(kPlanThreads, S - base); i += kPlanThreads / 32) {
+                const int4 v = seqs[i];
+                for (int t = lane; t * PK_BM < v.y; t += 32) {
+                    const int rows = min(PK_BM, v.y - t * PK_BM), pos = v.w + t * PK_BM;
+                    const int tiles = (max(pos + rows, 0) + PK_BN - 1) / PK_BN;
+                    take(make_int4(v.x + t * PK_BM, rows, v.z, pos), kPlanBins - 1 - min(tiles, kPlanBins - 1));
+                }
+            }
+        }
+    };
+    __syncthreads();
+    each([&](const int4&, int bin) { atomicAdd(&bins[bin], 1); });
+    __syncthreads();
+    static_assert(kPlanBins == kPlanThreads, "a thread a bin");
+    const int mine = bins[threadIdx.x];
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+    bins[threadIdx.x] = sum - mine;
+    if (threadIdx.x == kPlanThreads - 1) *count = min(sum, capacity);  // (no more: the sequences do not overlap)
+    __syncthreads();
+    each([&](const int4& item, int bin) {
+        const int at = atomicAdd(&bins[bin], 1);
+        if (at < capacity) items[at] = item;
+    });
+}
+
+// ------------------------------------------------------------------------------------- the kernel
+// Flash attention with an online softmax over 128-key tiles. An item is a tile of 128 query rows, PG = the largest power of two
+// in the group's query heads by 128 / PG tokens (so short runs of queries fill a tile), with one kv head.
+// Persistent: CTA c of G takes items c, 2G-1-c, 2G+c, ... of the list, which has the longest key ranges first. Tiles are counted
+// across items, so rings, score regions and barrier phases simply continue.
+//
+// Warps: 0 Q and K (TMA), 1 score MMAs, 2 V (TMA), 3 P V MMAs, 4-7 softmax (thread <-> query row), 8-11 output. Tensor memory: two
+// score regions of 128 columns (P, bf16, takes the first half of its scores) and two output accumulators, items
+// taking turns: while warps 8-11 read one item's output out, the next item's products and softmax go on. With one accumulator that the
+// softmax warps read out themselves (and three score regions) short prompts stood still at every item's end: 64 prompts
+// of 512 tokens, 32 heads, 315 us.
+// O is rescaled only when a row's maximum grew by more than 2^8. Rows of another sequence that a tile reaches into are masked
+// (keys), zeroed (values) and not stored (queries).
+constexpr int PK_THREADS = 384, PK_NR = 2;
+constexpr uint32_t PK_REG_PRODUCER = 56, PK_REG_SOFTMAX = 240, PK_REG_OUTPUT = 104;
+static_assert(PK_REG_PRODUCER + PK_REG_SOFTMAX + PK_REG_OUTPUT <= 3 * 168, "register split exceeds the launch");
+template <int DH>
+struct PkLayout {
+    static constexpr int NCH = DH / 64;
+    static constexpr int TILE_BYTES = 128 * DH * 2;
+    static constexpr int QST = 2, KST = 3, VST = 2;
+    static constexpr int K_OFF = QST * TILE_BYTES, V_OFF = K_OFF + KST * TILE_BYTES;
+    static constexpr int INV_OFF = V_OFF + VST * TILE_BYTES;  // [item parity][row]: 1 / sum
+    static constexpr int BAR_OFF = INV_OFF + 2 * PK_BM * 4;
+    static constexpr int SMEM = BAR_OFF + 256 + 1024;
+};
+static_assert(PkLayout<128>::SMEM <= 227 * 1024, "shared memory");
+
+struct PackedArgs {
+    const int4* items;
+    const int* count;
+    int capacity, max_keys;
+    int Nq, Hq, Hkv, pg_log;
+    __nv_bfloat16* out;
+    int* err;
+};
+
+template <int DH>
+__global__ void __launch_bounds__(PK_THREADS, 1)
+    attn_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const PackedArgs a) {
+    using Ly = PkLayout<DH>;
+    constexpr int NCH = Ly::NCH, QST = Ly::QST, KST = Ly::KST, VST = Ly::VST, NR = PK_NR, TB = Ly::TILE_BYTES;
+    constexpr uint32_t IDESC_S = idesc_bf16(PK_BM, PK_BN);
+    constexpr uint32_t IDESC_O = idesc_bf16(PK_BM, DH, true);
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::BAR_OFF);
+    uint64_t* q_full = bars;              // [QST]
+    uint64_t* q_empty = q_full + QST;     // [QST]
+    uint64_t* k_full = q_empty + QST;     // [KST]
+    uint64_t* k_empty = k_full + KST;     // [KST]
+    uint64_t* v_full = k_empty + KST;     // [VST]
+    uint64_t* v_empty = v_full + VST;     // [VST]
+    uint64_t* s_full = v_empty + VST;     // [NR] scores of the region are complete
+    uint64_t* p_full = s_full + NR;       // [NR] P of the region is written (one arrival a warp, as for the next ones but o_full)
+    uint64_t* r_free = p_full + NR;       // [NR] P V of the region's tile is done
+    uint64_t* o_full = r_free + NR;       // [item parity] the item's last P V is done
+    uint64_t* l_full = o_full + 2;        // [item parity] the rows' sums are in shared memory
+    uint64_t* o_free = l_full + 2;        // [item parity] accumulator and sums have been read out
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_free + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(o_free + 3);
+    static_assert((2 * (QST + KST + VST) + 3 * NR + 6 + 2) * 8 <= 256, "barriers");
+    volatile float* inv_sh = reinterpret_cast<volatile float*>(smem + Ly::INV_OFF);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (uint64_t* b = bars; b < o_free + 2; ++b) {
+            const bool by_warps = (b >= p_full && b < r_free) || b >= l_full;
+            mbar_init(b, by_warps ? 4 : 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot, tmem_o = tmem + NR * PK_BN;  // accumulator of item n: tmem_o + (n & 1) * 128
+    bool ok = true;
+    pdl_wait();  // the plan, Q, K and V come from earlier kernels
+    pdl_trigger();
+
+    // A role's items, read one ahead of their use. n_tiles = 0: none left.
+    const int Hq = a.Hq, pg_log = a.pg_log, groups = Hq >> pg_log, tpt_log = 7 - pg_log;  // tokens of a tile
+    const int n_items = min(max(*a.count, 0), a.capacity) * Hq;
+    const int G = (int)gridDim.x, me = (int)blockIdx.x;
+    struct Item {
+        int q0, q_end, k0, pos0, hg, n_valid, n_tiles;  // hg: group of PG heads
+    };
+    int round = 0;
+    auto fetch = [&]() -> Item {
+        Item it{};
+        while (true) {
+            const int k = round * G + ((round & 1) ? G - 1 - me : me);
+            if (k >= n_items) return it;
+            ++round;
+            const int entry = (int)((unsigned)k / (unsigned)Hq), rem = k - entry * Hq;
+            const int sub = (int)((unsigned)rem / (unsigned)groups);
+            const int4 v = __ldg(a.items + entry);
+            const int first = sub << tpt_log, rows = min(v.y - first, 1 << tpt_log);
+            if (rows <= 0) continue;  // the entry has fewer tokens
+            it.hg = rem - sub * groups;
+            it.q0 = v.x + first;
+            it.q_end = min(it.q0 + rows, a.Nq);
+            it.k0 = v.z;
+            it.pos0 = v.w + first;
+            it.n_valid = min(max(it.pos0 + rows, 0), a.max_keys);
+            it.n_tiles = max(1, (it.n_valid + PK_BN - 1) / PK_BN);  // without a key: one tile, all of it masked
+            return it;
+        }
+    };
+    Item ahead = fetch();
+    auto next_item = [&]() -> Item {
+        const Item it = ahead;
+        ahead = fetch();
+        return it;
+    };
+
+    // A role ends when what it has asked for is done, also after a wait of the CTA gave up: no copy or product of this CTA may
+    // land in shared or tensor memory that the next one has taken over. These last waits are bounded and look at no flag.
+    int never = 0;
+    bool arrives = true;
+    auto last_wait = [&](uint64_t* bar, int parity) { arrives = arrives && mbar_wait_suspend(bar, parity, &never); };
+
+    if (warp < 4) {
+        setmaxnreg_dec<PK_REG_PRODUCER>();
+        if (warp == 0) {
+            // ---------------- Q and key tiles
+            if (lane == 0) {
+                int g = 0, n = 0;
+                for (; ok; ++n) {
+                    const Item it = next_item();
+                    if (it.n_tiles == 0) break;
+                    const int jkv = it.hg / (groups / a.Hkv), qs = n % QST;
+                    if (!mbar_wait_suspend(&q_empty[qs], ((n / QST) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                    mbar_expect_tx(&q_full[qs], TB);
+                    tma_load_5d(smem + qs * TB, &tmQ, &q_full[qs], 0, 0, it.q0, 0, it.hg);
+                    for (int i = 0; i < it.n_tiles; ++i, ++g) {
+                        const int s = g % KST;
+                        if (!mbar_wait_suspend(&k_empty[s], ((g / KST) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                        mbar_expect_tx(&k_full[s], TB);
+                        tma_load_3d(smem + Ly::K_OFF + s * TB, &tmK, &k_full[s], 0, it.k0 + i * PK_BN, jkv * NCH);
+                    }
+                    if (!ok) {
+                        ++n;  // (its Q was asked for)
+                        break;
+                    }
+                }
+                drain_ring(g, KST, [&](int s, int parity) { last_wait(&k_full[s], parity); });
+                drain_ring(n, QST, [&](int s, int parity) { last_wait(&q_full[s], parity); });
+            }
+        } else if (warp == 1) {
+            // ---------------- S of tile g into region g % NR, once P V of tile g - NR has finished with it
+            if (lane == 0) {
+                int g = 0;
+                for (int n = 0; ok; ++n) {
+                    const Item it = next_item();
+                    const int nt = it.n_tiles, qs = n % QST;
+                    if (nt == 0) break;
+                    if (!mbar_wait_suspend(&q_full[qs], (n / QST) & 1, abort_flag)) { ok = false; break; }
+                    for (int i = 0; i < nt; ++i, ++g) {
+                        const int s = g % KST, r = g % NR;
+                        if (!mbar_wait_suspend(&k_full[s], (g / KST) & 1, abort_flag)) { ok = false; break; }
+                        // the region's next completion would be P V of tile g itself: the parity cannot alias
+                        if (g >= NR && !mbar_wait_suspend(&r_free[r], ((g - NR) / NR) & 1, abort_flag)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t sq = smem_u32(smem + qs * TB), sk = smem_u32(smem + Ly::K_OFF + s * TB);
+#pragma unroll
+                        for (int kk = 0; kk < DH / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * PK_BM * 128 + (kk & 3) * 32;
+                            umma_bf16_ss(tmem + r * PK_BN, sdesc_kmajor_sw128(sq + off), sdesc_kmajor_sw128(sk + off), IDESC_S,
+                                         kk > 0);
+                        }
+                        umma_commit(&s_full[r]);
+                        umma_commit(&k_empty[s]);
+                        if (i == nt - 1) umma_commit(&q_empty[qs]);  // the item's last scores release Q
+                    }
+                }
+                if (g > 0) last_wait(&s_full[(g - 1) % NR], ((g - 1) / NR) & 1);  // (completes behind every earlier tile's)
+            }
+        } else if (warp == 2) {
+            // ---------------- value tiles
+            if (lane == 0) {
+                int g = 0;
+                while (ok) {
+                    const Item it = next_item();
+                    if (it.n_tiles == 0) break;
+                    const int jkv = it.hg / (groups / a.Hkv);
+                    for (int i = 0; i < it.n_tiles; ++i, ++g) {
+                        const int s = g % VST;
+                        if (!mbar_wait_suspend(&v_empty[s], ((g / VST) & 1) ^ 1, abort_flag)) { ok = false; break; }
+                        mbar_expect_tx(&v_full[s], TB);
+                        tma_load_3d(smem + Ly::V_OFF + s * TB, &tmV, &v_full[s], 0, it.k0 + i * PK_BN, jkv * NCH);
+                    }
+                }
+                drain_ring(g, VST, [&](int s, int parity) { last_wait(&v_full[s], parity); });
+            }
+        } else {
+            // ---------------- O += P V of tile g: P from region g % NR (A operand in tensor memory), V from stage g % VST
+            int g = 0, done = 0;
+            for (int n = 0; ok; ++n) {
+                const Item it = next_item();
+                const int nt = it.n_tiles;
+                if (nt == 0) break;
+                const uint32_t to = tmem_o + (n & 1) * 128;
+                for (int i = 0; ok && i < nt; ++i, ++g) {
+                    const int s = g % VST, r = g % NR;
+                    if (!__all_sync(0xffffffffu, mbar_wait_suspend(&v_full[s], (g / VST) & 1, abort_flag))) { ok = false; break; }
+                    uint8_t* sv_p = smem + Ly::V_OFF + s * TB;
+                    const int r0 = it.n_valid - i * PK_BN;  // value rows from here on are not seen by the item, and may hold anything
+                    const int steps = min(PK_BN / 16, (max(r0, 1) + 15) / 16);  // 16-row steps that hold a seen one
+                    if (r0 < PK_BN) {  // (0 * NaN must not reach O)
+                        for (int e = lane; e < (steps * 16 - r0) * 8 * NCH; e += 32) {
+                            const int row = r0 + e / (8 * NCH), p = e % (8 * NCH);
+                            reinterpret_cast<uint4*>(sv_p + (p >> 3) * PK_BN * 128 + row * 128)[p & 7] = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        bool w = i > 0 || mbar_wait_suspend(&o_free[n & 1], ((n >> 1) & 1) ^ 1, abort_flag);  // item n - 2's O is read out
+                        w = w && mbar_wait_suspend(&p_full[r], (g / NR) & 1, abort_flag);
+                        if (w) {
+                            tc_fence_after();
+                            const uint32_t sv = smem_u32(sv_p);
+                            if (steps < PK_BN / 16) {
+                                for (int kk = 0; kk < steps; ++kk)
+                                    umma_bf16_ts(to, tmem + r * PK_BN + kk * 8, sdesc_mnmajor_sw128(sv + kk * 16 * 128, PK_BN * 128),
+                                                 IDESC_O, (i | kk) != 0);
+                            } else {
+#pragma unroll
+                                for (int kk = 0; kk < PK_BN / 16; ++kk)
+                                    umma_bf16_ts(to, tmem + r * PK_BN + kk * 8, sdesc_mnmajor_sw128(sv + kk * 16 * 128, PK_BN * 128),
+                                                 IDESC_O, (i | kk) != 0);
+                            }
+                            umma_commit(&r_free[r]);
+                            umma_commit(&v_empty[s]);
+                            if (i == nt - 1) umma_commit(&o_full[n & 1]);
+                            ++done;
+                        }
+                        ok = w;
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                }
+            }
+            if (lane == 0 && done > 0) last_wait(&r_free[(done - 1) % NR], ((done - 1) / NR) & 1);
+            __syncwarp();
+        }
+    } else if (warp < 8) {
+        setmaxnreg_inc<PK_REG_SOFTMAX>();
+        // ---------------- softmax: thread <-> query row (TMEM lane)
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const float sl2 = kLog2e / sqrtf((float)DH);
+        int g = 0;
+        for (int n = 0; ok; ++n) {
+            const Item it = next_item();
+            const int nt = it.n_tiles;
+            if (nt == 0) break;
+            const int pos = it.pos0 + (row >> pg_log);
+            const uint32_t to = tmem_o + (n & 1) * 128 + lane_off;
+            float m = -INFINITY, l = 0.f;  // the row's scale (log2 units) and sum
+            for (int i = 0; i < nt; ++i, ++g) {
+                const int r = g % NR;
+                const uint32_t ts = tmem + r * PK_BN + lane_off;
+                if (!__all_sync(0xffffffffu, mbar_wait_suspend(&s_full[r], (g / NR) & 1, abort_flag))) { ok = false; break; }
+                tc_fence_after();
+                uint32_t sr[PK_BN];
+#pragma unroll
+                for (int c = 0; c < PK_BN / 32; ++c)
+                    tmem_ld_32x32b_x32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+                tmem_ld_wait();
+                if (i * PK_BN + PK_BN - 1 > it.pos0) {  // some row does not see all of the tile
+                    const int lim = pos - i * PK_BN;    // last visible column
+#pragma unroll
+                    for (int c = 0; c < PK_BN / 32; ++c) {
+                        const uint32_t vis = low_bits(lim + 1 - 32 * c);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            sr[c * 32 + e] = vis & (1u << e) ? sr[c * 32 + e] : __float_as_uint(-INFINITY);
+                    }
+                }
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // independent chains
+#pragma unroll
+                for (int e = 0; e < PK_BN; e += 2)
+                    mx4[e / 2 % 4] = fmax3(mx4[e / 2 % 4], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+                // lazy rescale, decided per row but executed by the whole warp (tcgen05.ld/st are warp-wide)
+                const bool grow = mx > m + 8.0f;
+                const float alpha = grow ? ex2_approx(m - mx) : 1.0f;
+                if (i > 0 && __any_sync(0xffffffffu, grow)) {
+                    // O must hold every earlier tile's P V. (The region's next P V needs a P that is not released yet: the
+                    // parity cannot alias.)
+                    const int k = g - 1;
+                    if (!__all_sync(0xffffffffu, mbar_wait_suspend(&r_free[k % NR], (k / NR) & 1, abort_flag))) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < DH / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(to + c * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st_32x32b_x32(to + c * 32, o);
+                    }
+                }
+                if (grow) {
+                    l *= alpha;
+                    m = mx;
+                }
+                // P = 2^(s * sl2 - m) as packed bf16, the type that the tensor cores take beside V's (off by 2^-8 of itself at
+                // most; the sum keeps fp32). A row with no visible key yet keeps m = -inf and gets P = 0.
+                const float nm = m == -INFINITY ? 0.f : -m;
+                const float2 sl2x2 = make_float2(sl2, sl2), nmx2 = make_float2(nm, nm);
+                float2 rs2 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 x = fma2(make_float2(__uint_as_float(sr[half * 64 + 2 * e]),
+                                                          __uint_as_float(sr[half * 64 + 2 * e + 1])),
+                                              sl2x2, nmx2);
+                        const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        rs2 = add2(rs2, pp);
+                        pk[e] = pack_bf16(pp.x, pp.y);
+                    }
+                    tmem_st_32x32b_x32(ts + half * 32, pk);
+                }
+                tmem_st_wait();
+                l += rs2.x + rs2.y;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[r]);
+            }
+            if (!ok) break;
+            // the sums go to the output warps, once those of item n - 2 have been read
+            if (!__all_sync(0xffffffffu, mbar_wait_suspend(&o_free[n & 1], ((n >> 1) & 1) ^ 1, abort_flag))) { ok = false; break; }
+            inv_sh[(n & 1) * PK_BM + row] = l == 0.f ? 0.f : 1.f / l;  // (a row without a key: zeros)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&l_full[n & 1]);
+        }
+    } else {
+        setmaxnreg_dec<PK_REG_OUTPUT>();
+        // ---------------- output: thread <-> query row
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        for (int n = 0; ok; ++n) {
+            const Item it = next_item();
+            if (it.n_tiles == 0) break;
+            const int ph = (n >> 1) & 1;
+            const uint32_t to = tmem_o + (n & 1) * 128 + lane_off;
+            if (!__all_sync(0xffffffffu, mbar_wait_suspend(&l_full[n & 1], ph, abort_flag) &&
+                                             mbar_wait_suspend(&o_full[n & 1], ph, abort_flag))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float inv = inv_sh[(n & 1) * PK_BM + row];
+            const int row0 = quarter * 32 + (lane & ~3);  // of the four rows that four neighbouring lanes hold and store together
+#pragma unroll 1
+            for (int c = 0; c < DH / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(to + c * 32, o);
+                tmem_ld_wait();
+                // 16-byte pieces change places within groups of four lanes, so that a group stores 64 contiguous bytes of
+                // one row at a time (lane k piece j -> lane j piece k)
+                uint4 w[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    w[v] = make_uint4(pack_bf16(__uint_as_float(o[8 * v]) * inv, __uint_as_float(o[8 * v + 1]) * inv),
+                                      pack_bf16(__uint_as_float(o[8 * v + 2]) * inv, __uint_as_float(o[8 * v + 3]) * inv),
+                                      pack_bf16(__uint_as_float(o[8 * v + 4]) * inv, __uint_as_float(o[8 * v + 5]) * inv),
+                                      pack_bf16(__uint_as_float(o[8 * v + 6]) * inv, __uint_as_float(o[8 * v + 7]) * inv));
+                auto swap = [&](uint4& lo, uint4& hi, int bit) {  // the low lane's hi with the high lane's lo
+                    const bool up = lane & bit;
+                    uint4 x = up ? lo : hi;
+                    x.x = __shfl_xor_sync(0xffffffffu, x.x, bit);
+                    x.y = __shfl_xor_sync(0xffffffffu, x.y, bit);
+                    x.z = __shfl_xor_sync(0xffffffffu, x.z, bit);
+                    x.w = __shfl_xor_sync(0xffffffffu, x.w, bit);
+                    if (up) lo = x;
+                    else hi = x;
+                };
+                swap(w[0], w[1], 1);
+                swap(w[2], w[3], 1);
+                swap(w[0], w[2], 2);
+                swap(w[1], w[3], 2);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int r = row0 + v, t = it.q0 + (r >> pg_log), h = (it.hg << pg_log) + (r & ((1 << pg_log) - 1));
+                    if (t < it.q_end)
+                        *reinterpret_cast<uint4*>(a.out + ((size_t)t * Hq + h) * DH + c * 32 + (lane & 3) * 8) = w[v];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[n & 1]);
+        }
+    }
+    if (!ok) {
+        *abort_flag = 1;
+        if (a.err) atomicOr(a.err, ERR_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int DH>
+cudaError_t packed_launch_dh(const PackedCall& c, cudaStream_t st) {
+    // heads of a tile: the largest power of two in the group, up to a tile's rows
+    int pg_log = 0;
+    while (pg_log < 7 && (c.Hq / c.Hkv) % (2 << pg_log) == 0) ++pg_log;
+    CUtensorMap tq, tk, tv;
+    // without a key row there is nothing to read: any memory serves as the masked tile
+    const bool none = c.Nk == 0;
+    const void *k = none ? c.q : c.k, *v = none ? c.q : c.v;
+    const uint64_t rows = none ? 1 : c.Nk, ldk = none ? c.ldq : c.ldk, ldv = none ? c.ldq : c.ldv;
+    const uint64_t blocks = (uint64_t)c.Hkv * (DH / 64);
+    if (!encode_tmap_bf16_head_groups(&tq, c.q, DH, 1u << pg_log, c.Hq >> pg_log, c.Nq, (uint64_t)c.ldq * 2, PK_BM >> pg_log) ||
+        !encode_tmap_bf16_rows(&tk, k, blocks, rows, ldk * 2, PK_BN, DH / 64) ||
+        !encode_tmap_bf16_rows(&tv, v, blocks, rows, ldv * 2, PK_BN, DH / 64))
+        return cudaErrorInvalidValue;
+    const PackedArgs a{reinterpret_cast<const int4*>(static_cast<const char*>(c.plan) + kPlanHeader),
+                       static_cast<const int*>(c.plan), c.capacity, c.Nk, c.Nq, c.Hq, c.Hkv, pg_log, c.out, c.err};
+    const unsigned grid = (unsigned)std::min<long long>((long long)c.capacity * c.Hq, device_sm_count());
+    return launch_pdl(attn_packed_kernel<DH>, dim3(grid), dim3(PK_THREADS), PkLayout<DH>::SMEM, st, tq, tk, tv, a);
+}
+
+// setmaxnreg.inc waits until the registers it asks for are free: the compiled kernel has to be given at least those that its
+// split hands out.
+template <int DH>
+cudaError_t packed_prepare_dh() {
+    cudaFuncAttributes fa{};
+    cudaError_t e = cudaFuncGetAttributes(&fa, attn_packed_kernel<DH>);
+    if (e != cudaSuccess) return e;
+    if (PK_THREADS * fa.numRegs < 128 * (int)(PK_REG_PRODUCER + PK_REG_SOFTMAX + PK_REG_OUTPUT)) return cudaErrorLaunchOutOfResources;
+    return cudaFuncSetAttribute(attn_packed_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, PkLayout<DH>::SMEM);
+}
+
+}  // namespace
+
+size_t attn_packed_plan_bytes(int Nq, int S) {
+    return kPlanHeader + ((size_t)(Nq + PK_BM - 1) / PK_BM + (size_t)S) * sizeof(int4);
+}
+int attn_packed_capacity(size_t bytes) {
+    return bytes < kPlanHeader ? 0 : (int)std::min<size_t>((bytes - kPlanHeader) / sizeof(int4), 0x7fffffff);
+}
+cudaError_t attn_packed_plan_launch(const int* cu_q, const int* cu_k, int S, int Nq, int Nk, void* plan, int capacity, int* err,
+                                    cudaStream_t st) {
+    return launch_pdl(attn_packed_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, cu_q, cu_k, S, Nq, Nk,
+                      static_cast<int*>(plan), reinterpret_cast<int4*>(static_cast<char*>(plan) + kPlanHeader), capacity, err);
+}
+cudaError_t attn_packed_launch(const PackedCall& c, int dh, cudaStream_t st) {
+    if (dh == 128) return packed_launch_dh<128>(c, st);
+    if (dh == 64) return packed_launch_dh<64>(c, st);
+    return cudaErrorInvalidValue;
+}
+cudaError_t attention_packed_prepare() {
+    cudaError_t e = packed_prepare_dh<128>();
+    return e == cudaSuccess ? packed_prepare_dh<64>() : e;
+}
+
+}  // namespace q3

@@ -1038,6 +1038,19 @@ bool encode_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t blocks, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_bf16_head_groups(CUtensorMap* map, const void* base, uint64_t dh, uint64_t group, uint64_t groups,
+                                  uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[5] = {64, group, rows, dh / 64, groups};
+    cuuint64_t strides[4] = {dh * 2, row_bytes, 128, dh * group * 2};
+    cuuint32_t box[5] = {64, (cuuint32_t)group, box_rows, (cuuint32_t)(dh / 64), 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_tmap_bf16_groups(CUtensorMap* map, const void* base, uint64_t dh, uint64_t group, uint64_t heads,
                              uint64_t seqs, uint32_t box_seqs) {
     auto fn = encode_fn();

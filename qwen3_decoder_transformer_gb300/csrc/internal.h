@@ -141,6 +141,10 @@ bool encode_tmap_bf16_units(CUtensorMap* map, const void* base, uint64_t dh, uin
 // (0, row, block), rows past `rows` read as zero.
 bool encode_tmap_bf16_rows(CUtensorMap* map, const void* base, uint64_t blocks, uint64_t rows, uint64_t row_bytes,
                            uint32_t box_rows, uint32_t box_blocks);
+// Query rows [rows][groups of `group` heads][dh], row_bytes apart, in boxes of one group's heads in box_rows rows, stored as
+// dh / 64 parts of 64 columns with the heads of a row next to each other; coordinates (0, 0, row, 0, group).
+bool encode_tmap_bf16_head_groups(CUtensorMap* map, const void* base, uint64_t dh, uint64_t group, uint64_t groups,
+                                  uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
 // Query rows [seqs][heads][group][dh] in boxes of 64 x group x 1 x box_seqs: one head's groups of box_seqs sequences.
 bool encode_tmap_bf16_groups(CUtensorMap* map, const void* base, uint64_t dh, uint64_t group, uint64_t heads,
                              uint64_t seqs, uint32_t box_seqs);
@@ -233,18 +237,13 @@ int attn_decode_kernel_count();
 size_t attn_decode_noalloc_max_bytes();
 cudaError_t attn_decode_noalloc_scratch(float** ptr);
 
-// Packed sequences: the work list of attn_packed_plan_launch, and a call that walks it (the persistent prefill kernel).
-struct PackedTiles {
-    const int4* items;  // (first query row, rows, first key row of the sequence, key position of the first query row)
-    const int* count;
-    int capacity, max_keys;
-};
+// ---------------------------------------------------------------- packed sequences (attention_packed.cu)
 struct PackedCall {
     const __nv_bfloat16 *q, *k, *v;
     long long ldq, ldk, ldv;  // elements from row to row
     int Nq, Nk, Hq, Hkv;
     const void* plan;
-    int capacity, longest;  // longest: keys of the longest sequence; it only picks between equivalent forms
+    int capacity;  // entries that the plan has room for
     __nv_bfloat16* out;
     int* err;
 };
@@ -316,6 +315,7 @@ cudaError_t gemm_prepare();
 cudaError_t attention_prepare();
 cudaError_t attention_tiles_prepare();
 cudaError_t attention_ranges_prepare();
+cudaError_t attention_packed_prepare();
 cudaError_t attention_paged4_prepare();
 cudaError_t token_logprobs_prepare();
 cudaError_t prepare_kernels();
