@@ -591,9 +591,12 @@ def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rol
 
 
 # ------------------------------------------------------------------ the paged 4-bit cache and packed batches
+#
+# As above, what is wrong with a call's tensors is worked out (the _why functions) only when one expression finds something.
 
 _U8 = torch.uint8
 PAGE_SIZES = (16, 32, 64, 128, 256)
+_PAGE_OF = {(p * (dh // 2 + dh // 16), dh): p for p in PAGE_SIZES for dh in (64, 128)}  # by page bytes and head_dim
 
 
 def paged4_page_bytes(page_size, dh) -> int:
@@ -601,16 +604,15 @@ def paged4_page_bytes(page_size, dh) -> int:
     return lib().qwen3_paged4_page_bytes(_int32(page_size), _int32(dh))
 
 
-def _pages(k_pages, v_pages, page_table, dh, dev):
-    """Check a paged cache (k_pages, v_pages [n_pages, Hkv, page bytes] uint8, page_table [sequences, max_pages] int32).
-    Returns n_pages, Hkv, the page size and max_pages."""
+def _why_pages(k_pages, v_pages, page_table, dh, dev):
+    """Find what is wrong with a paged cache (k_pages, v_pages [n_pages, Hkv, page bytes] uint8, page_table [sequences,
+    max_pages] int32). Returns n_pages, Hkv, the page size and max_pages."""
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
         _want(isinstance(t, torch.Tensor) and t.dim() == 3, f"{name} must be a tensor [n_pages, Hkv, page bytes]")
     _want(dh in (64, 128), "head_dim must be 64 or 128")
     n, Hkv, size = k_pages.shape
-    page = size // (dh // 2 + dh // 16)
-    _want(page in PAGE_SIZES and size == page * (dh // 2 + dh // 16),
-          "a page must hold 16, 32, 64, 128 or 256 tokens of paged4_page_bytes")
+    page = _PAGE_OF.get((size, dh))
+    _want(page is not None, "a page must hold 16, 32, 64, 128 or 256 tokens of paged4_page_bytes")
     _dense("k_pages", k_pages, _U8, (n, Hkv, size), dev)
     _dense("v_pages", v_pages, _U8, (n, Hkv, size), dev)
     _want(isinstance(page_table, torch.Tensor) and page_table.dim() == 2, "page_table must be a tensor [sequences, max_pages]")
@@ -619,11 +621,31 @@ def _pages(k_pages, v_pages, page_table, dh, dev):
     return n, Hkv, page, page_table.shape[1]
 
 
-def _bounds(cu, start, sequences, dev):
-    """Check cu [S + 1] and start [S] against the page table's sequences; returns S."""
+def _why_bounds(cu, start, sequences, dev):
     _dense("cu", cu, _I32, (sequences + 1,), dev)
     _dense("start", start, _I32, (sequences,), dev)
-    return sequences
+
+
+def _why_append(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out, q_gamma, k_gamma):
+    _want(isinstance(qkv, torch.Tensor) and qkv.dim() == 2, "qkv must be a tensor [N, (Hq + 2 Hkv) dh]")
+    _want(isinstance(q_out, torch.Tensor) and q_out.dim() == 3, "q_out must be a tensor [N, Hq, dh]")
+    N, Hq, dh = q_out.shape
+    dev = qkv.get_device()
+    _, Hkv, _, _ = _why_pages(k_pages, v_pages, page_table, dh, dev)
+    _want(Hq >= 1 and Hq % Hkv == 0, "query heads must be a multiple of kv heads")
+    width = (Hq + 2 * Hkv) * dh
+    _want(qkv.dtype is _BF16 and qkv.shape == (N, width) and qkv.stride(1) == 1,
+          f"qkv must be bf16 rows {(N, width)}, dense along a row")
+    _why_bounds(cu, start, page_table.shape[0], dev)
+    _dense("q_out", q_out, _BF16, (N, Hq, dh), dev)
+    _want(isinstance(cos_sin, torch.Tensor) and cos_sin.dim() == 2, "cos_sin must be a tensor [positions, dh]")
+    _dense("cos_sin", cos_sin, _BF16, (cos_sin.shape[0], dh), dev)
+    if k_out is not None:
+        _dense("k_out", k_out, _BF16, (N, Hkv, dh), dev)
+    for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+        if g is not None:
+            _dense(name, g, _BF16, (dh,), dev)
+    raise ValueError("the tensors do not fit the call")
 
 
 def op_append_paged4(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out=None, q_gamma=None, k_gamma=None,
@@ -632,42 +654,80 @@ def op_append_paged4(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_ou
     stride along a row): rows cu[s] .. cu[s+1]-1 take the slots start[s] .. of sequence s. Writes q_out [N, Hq, dh], k_out
     [N, Hkv, dh] (None: not wanted) and the pages; rows from cu[-1] on are left as they were. err: device int (bit 4: a
     page id or a position out of range)."""
-    _want(isinstance(qkv, torch.Tensor) and qkv.dim() == 2, "qkv must be a tensor [N, (Hq + 2 Hkv) dh]")
-    _want(isinstance(q_out, torch.Tensor) and q_out.dim() == 3, "q_out must be a tensor [N, Hq, dh]")
-    N, Hq, dh = q_out.shape
-    dev = qkv.get_device()
-    n_pages, Hkv, page, max_pages = _pages(k_pages, v_pages, page_table, dh, dev)
-    _want(Hq >= 1 and Hq % Hkv == 0, "query heads must be a multiple of kv heads")
-    width = (Hq + 2 * Hkv) * dh
-    _want(qkv.dtype is _BF16 and qkv.shape == (N, width) and qkv.stride(1) == 1,
-          f"qkv must be bf16 rows {(N, width)}, dense along a row")
-    ld = qkv.stride(0) if N > 1 else width
-    S = _bounds(cu, start, page_table.shape[0], dev)
-    _dense("q_out", q_out, _BF16, (N, Hq, dh), dev)
-    _want(isinstance(cos_sin, torch.Tensor) and cos_sin.dim() == 2, "cos_sin must be a tensor [positions, dh]")
-    _dense("cos_sin", cos_sin, _BF16, (cos_sin.shape[0], dh), dev)
-    p_k = None if k_out is None else _dense("k_out", k_out, _BF16, (N, Hkv, dh), dev)
-    p_qg = None if q_gamma is None else _dense("q_gamma", q_gamma, _BF16, (dh,), dev)
-    p_kg = None if k_gamma is None else _dense("k_gamma", k_gamma, _BF16, (dh,), dev)
+    try:
+        N, Hq, dh = q_out.shape
+        shape = k_pages.shape
+        n_pages, Hkv, size = shape
+        S, max_pages = page_table.shape
+        n_pos, _ = angles = cos_sin.shape
+        ld, unit = qkv.stride()
+        page = _PAGE_OF.get((size, dh))
+        dev = qkv.get_device()
+        ok = (page is not None and n_pages and Hkv and max_pages and Hq and Hq % Hkv == 0 and unit == 1
+              and qkv.shape == (N, (Hq + 2 * Hkv) * dh) and v_pages.shape == shape and angles == (n_pos, dh)
+              and cu.shape == (S + 1,) and start.shape == (S,)
+              and qkv.dtype is _BF16 and q_out.dtype is _BF16 and cos_sin.dtype is _BF16 and k_pages.dtype is _U8
+              and v_pages.dtype is _U8 and page_table.dtype is _I32 and cu.dtype is _I32 and start.dtype is _I32
+              and q_out.get_device() == dev and cos_sin.get_device() == dev and k_pages.get_device() == dev
+              and v_pages.get_device() == dev and page_table.get_device() == dev and cu.get_device() == dev
+              and start.get_device() == dev and q_out.is_contiguous() and cos_sin.is_contiguous() and k_pages.is_contiguous()
+              and v_pages.is_contiguous() and page_table.is_contiguous() and cu.is_contiguous() and start.is_contiguous()
+              and (k_out is None or (k_out.shape == (N, Hkv, dh) and k_out.dtype is _BF16 and k_out.get_device() == dev
+                                     and k_out.is_contiguous()))
+              and (q_gamma is None or (q_gamma.shape == (dh,) and q_gamma.dtype is _BF16 and q_gamma.get_device() == dev
+                                       and q_gamma.is_contiguous()))
+              and (k_gamma is None or (k_gamma.shape == (dh,) and k_gamma.dtype is _BF16 and k_gamma.get_device() == dev
+                                       and k_gamma.is_contiguous())))
+    except (AttributeError, ValueError):  # not tensors, or not of these numbers of dimensions
+        ok = False
+    if not ok:
+        _why_append(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out, q_gamma, k_gamma)
     p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
     if N == 0 or S == 0:
         return
+    if N == 1:  # (the stride of a single row says nothing)
+        ld = (Hq + 2 * Hkv) * dh
     _launch(lib().qwen3_op_append_paged4,
-            (qkv.data_ptr(), ld, N, cu.data_ptr(), start.data_ptr(), S, Hq, Hkv, dh, p_qg, p_kg, eps, cos_sin.data_ptr(),
-             cos_sin.shape[0], q_out.data_ptr(), p_k, k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page,
-             page_table.data_ptr(), max_pages, p_err), dev, stream)
+            (qkv.data_ptr(), ld, N, cu.data_ptr(), start.data_ptr(), S, Hq, Hkv, dh,
+             None if q_gamma is None else q_gamma.data_ptr(), None if k_gamma is None else k_gamma.data_ptr(), eps,
+             cos_sin.data_ptr(), n_pos, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), k_pages.data_ptr(),
+             v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, p_err), dev, stream)
+
+
+def _why_read(k_pages, v_pages, page_table, cu, start, k_out, v_out):
+    _want(isinstance(k_out, torch.Tensor) and k_out.dim() == 3, "k_out must be a tensor [N, Hkv, dh]")
+    N, _, dh = k_out.shape
+    dev = k_out.get_device()
+    _, Hkv, _, _ = _why_pages(k_pages, v_pages, page_table, dh, dev)
+    _why_bounds(cu, start, page_table.shape[0], dev)
+    _dense("k_out", k_out, _BF16, (N, Hkv, dh), dev)
+    _dense("v_out", v_out, _BF16, (N, Hkv, dh), dev)
+    raise ValueError("the tensors do not fit the call")
 
 
 def op_read_paged4(k_pages, v_pages, page_table, cu, start, k_out, v_out, err=None, stream=None):
     """Slots start[s] .. of sequence s of the paged 4-bit cache into the rows cu[s] .. cu[s+1]-1 of k_out and v_out
     [N, Hkv, dh] bf16."""
-    _want(isinstance(k_out, torch.Tensor) and k_out.dim() == 3, "k_out must be a tensor [N, Hkv, dh]")
-    N, Hkv, dh = k_out.shape
-    dev = k_out.get_device()
-    n_pages, heads, page, max_pages = _pages(k_pages, v_pages, page_table, dh, dev)
-    S = _bounds(cu, start, page_table.shape[0], dev)
-    _dense("k_out", k_out, _BF16, (N, heads, dh), dev)
-    _dense("v_out", v_out, _BF16, (N, heads, dh), dev)
+    try:
+        rows = k_out.shape
+        N, heads, dh = rows
+        shape = k_pages.shape
+        n_pages, Hkv, size = shape
+        S, max_pages = page_table.shape
+        page = _PAGE_OF.get((size, dh))
+        dev = k_out.get_device()
+        ok = (page is not None and n_pages and Hkv and max_pages and heads == Hkv and v_pages.shape == shape
+              and v_out.shape == rows and cu.shape == (S + 1,) and start.shape == (S,)
+              and k_out.dtype is _BF16 and v_out.dtype is _BF16 and k_pages.dtype is _U8 and v_pages.dtype is _U8
+              and page_table.dtype is _I32 and cu.dtype is _I32 and start.dtype is _I32
+              and v_out.get_device() == dev and k_pages.get_device() == dev and v_pages.get_device() == dev
+              and page_table.get_device() == dev and cu.get_device() == dev and start.get_device() == dev
+              and k_out.is_contiguous() and v_out.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
+              and page_table.is_contiguous() and cu.is_contiguous() and start.is_contiguous())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _why_read(k_pages, v_pages, page_table, cu, start, k_out, v_out)
     p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
     if N == 0 or S == 0:
         return
@@ -680,26 +740,49 @@ def attention_decode_paged4_workspace(B, Hq, Hkv, dh) -> int:
     return lib().qwen3_attention_decode_paged4_workspace(B, Hq, Hkv, dh)
 
 
-def op_attention_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out, err=None, stream=None):
-    """Decode attention of q [B, Hq, dh] over the slots 0..len0[b] of each sequence of the paged 4-bit cache, into out
-    [B, Hq*dh]. work: attention_decode_paged4_workspace bytes of scratch of any type."""
+def _why_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out):
     _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [B, Hq, dh]")
     B, Hq, dh = q.shape
     dev = q.get_device()
-    n_pages, Hkv, page, max_pages = _pages(k_pages, v_pages, page_table, dh, dev)
+    _, Hkv, _, _ = _why_pages(k_pages, v_pages, page_table, dh, dev)
     _want(Hq >= 1 and Hq % Hkv == 0 and Hq // Hkv <= 8, "query heads must be 1 to 8 times the kv heads")
     _want(page_table.shape[0] == B, "page_table must have a row for each sequence")
-    p_q = _dense("q", q, _BF16, (B, Hq, dh), dev)
-    p_len = _dense("len0", len0, _I32, (B,), dev)
-    p_out = _dense("out", out, _BF16, (B, Hq * dh), dev)
+    _dense("q", q, _BF16, (B, Hq, dh), dev)
+    _dense("len0", len0, _I32, (B,), dev)
+    _dense("out", out, _BF16, (B, Hq * dh), dev)
     _want(isinstance(work, torch.Tensor) and work.get_device() == dev and work.is_contiguous(),
           "work must be contiguous scratch on the same device, of attention_decode_paged4_workspace bytes")
+    raise ValueError("the tensors do not fit the call")
+
+
+def op_attention_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out, err=None, stream=None):
+    """Decode attention of q [B, Hq, dh] over the slots 0..len0[b] of each sequence of the paged 4-bit cache, into out
+    [B, Hq*dh]. work: attention_decode_paged4_workspace bytes of scratch of any type."""
+    try:
+        B, Hq, dh = q.shape
+        shape = k_pages.shape
+        n_pages, Hkv, size = shape
+        rows, max_pages = page_table.shape
+        page = _PAGE_OF.get((size, dh))
+        dev = q.get_device()
+        ok = (page is not None and n_pages and Hkv and max_pages and Hq and Hq % Hkv == 0 and Hq <= 8 * Hkv and rows == B
+              and v_pages.shape == shape and len0.shape == (B,) and out.shape == (B, Hq * dh)
+              and q.dtype is _BF16 and out.dtype is _BF16 and k_pages.dtype is _U8 and v_pages.dtype is _U8
+              and page_table.dtype is _I32 and len0.dtype is _I32
+              and out.get_device() == dev and k_pages.get_device() == dev and v_pages.get_device() == dev
+              and page_table.get_device() == dev and len0.get_device() == dev and work.get_device() == dev
+              and q.is_contiguous() and out.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
+              and page_table.is_contiguous() and len0.is_contiguous() and work.is_contiguous())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _why_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out)
     p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
     if B == 0:
         return
     _launch(lib().qwen3_op_attention_decode_paged4,
-            (p_q, k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, p_len, B, Hq, Hkv,
-             dh, work.data_ptr(), work.nbytes, p_out, p_err), dev, stream)
+            (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,
+             len0.data_ptr(), B, Hq, Hkv, dh, work.data_ptr(), work.nbytes, out.data_ptr(), p_err), dev, stream)
 
 
 def attention_packed_plan_bytes(Nq, S) -> int:
@@ -722,32 +805,50 @@ def op_attention_packed_plan(cu_q, cu_k, Nq, Nk, plan, err=None, stream=None):
             (cu_q.data_ptr(), cu_k.data_ptr(), n - 1, _int32(Nq), _int32(Nk), plan.data_ptr(), plan.nbytes, p_err), dev, stream)
 
 
-def _packed_rows(name, t, dh, dev):
-    """Check t [rows, heads, dh] bf16, its heads and dims dense; returns the elements from row to row."""
-    ok = (isinstance(t, torch.Tensor) and t.dim() == 3 and t.dtype is _BF16 and t.get_device() == dev and t.shape[2] == dh
-          and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == dh))
-    _want(ok, f"{name} must be a bf16 tensor [rows, heads, dh], dense along heads and dims")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dh
+def _why_packed(q, k, v, plan, out):
+    _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [Nq, Hq, dh]")
+    Nq, Hq, dh = q.shape
+    dev = q.get_device()
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _want(isinstance(t, torch.Tensor) and t.dim() == 3 and t.dtype is _BF16 and t.get_device() == dev and t.shape[2] == dh
+              and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == dh),
+              f"{name} must be a bf16 tensor [rows, heads, dh], dense along heads and dims")
+    _want(v.shape == k.shape and k.shape[1] >= 1 and Hq >= 1 and Hq % k.shape[1] == 0,
+          "k and v must have the same rows and heads, and query heads must be a multiple of them")
+    _dense("out", out, _BF16, (Nq, Hq * dh), dev)
+    _want(isinstance(plan, torch.Tensor) and plan.get_device() == dev and plan.is_contiguous(),
+          "plan must be the contiguous work list that op_attention_packed_plan wrote, on the same device")
+    raise ValueError("the tensors do not fit the call")
 
 
 def op_attention_prefill_packed(q, k, v, plan, longest, out, err=None, stream=None):
     """Causal attention over packed sequences: q [Nq, Hq, dh], k and v [Nk, Hkv, dh] (rows may be further apart, as views of
-    packed qkv rows are), plan as op_attention_packed_plan wrote it for these Nq and Nk, longest = keys of the longest sequence
-    (any value is right, it picks the kernel's form); out [Nq, Hq*dh]."""
-    _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [Nq, Hq, dh]")
-    Nq, Hq, dh = q.shape
-    dev = q.get_device()
-    ldq = _packed_rows("q", q, dh, dev)
-    ldk, ldv = _packed_rows("k", k, dh, dev), _packed_rows("v", v, dh, dev)
-    Nk, Hkv = k.shape[0], k.shape[1]
-    _want(v.shape[:2] == (Nk, Hkv) and Hkv >= 1 and Hq >= 1 and Hq % Hkv == 0,
-          "k and v must have the same rows and heads, and query heads must be a multiple of them")
-    p_out = _dense("out", out, _BF16, (Nq, Hq * dh), dev)
-    _want(isinstance(plan, torch.Tensor) and plan.get_device() == dev and plan.is_contiguous(),
-          "plan must be the contiguous work list that op_attention_packed_plan wrote, on the same device")
+    packed qkv rows are), plan as op_attention_packed_plan wrote it for these Nq and Nk; out [Nq, Hq*dh]. longest = keys of
+    the longest sequence, a hint for the launch (any value is right)."""
+    try:
+        Nq, Hq, dh = q.shape
+        keys = k.shape
+        Nk, Hkv, kd = keys
+        ldq, hq, uq = q.stride()
+        ldk, hk, uk = k.stride()
+        ldv, hv, uv = v.stride()
+        dev = q.get_device()
+        ok = (kd == dh and v.shape == keys and Hkv and Hq and Hq % Hkv == 0 and uq == uk == uv == 1
+              and (hq == dh or Hq == 1) and ((hk == dh and hv == dh) or Hkv == 1) and out.shape == (Nq, Hq * dh)
+              and q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and out.dtype is _BF16
+              and k.get_device() == dev and v.get_device() == dev and out.get_device() == dev and plan.get_device() == dev
+              and out.is_contiguous() and plan.is_contiguous())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _why_packed(q, k, v, plan, out)
     p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
     if Nq == 0:
         return
+    if Nq == 1:  # (the stride of a single row says nothing)
+        ldq = Hq * dh
+    if Nk <= 1:
+        ldk = ldv = Hkv * dh
     _launch(lib().qwen3_op_attention_prefill_packed,
             (q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, Nq, Nk, Hq, Hkv, dh, plan.data_ptr(), plan.nbytes,
-             _int32(longest), p_out, p_err), dev, stream)
+             _int32(longest), out.data_ptr(), p_err), dev, stream)

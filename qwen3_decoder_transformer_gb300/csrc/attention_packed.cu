@@ -100,20 +100,25 @@ __global__ void __launch_bounds__(kPlanThreads)
 // of 512 tokens, 32 heads, 315 us.
 // O is rescaled only when a row's maximum grew by more than 2^8. Rows of another sequence that a tile reaches into are masked
 // (keys), zeroed (values) and not stored (queries).
-constexpr int PK_THREADS = 384, PK_NR = 2;
-constexpr uint32_t PK_REG_PRODUCER = 56, PK_REG_SOFTMAX = 240, PK_REG_OUTPUT = 104;
+constexpr int PK_THREADS = 384;
+constexpr uint32_t PK_REG_PRODUCER = 56, PK_REG_SOFTMAX = 208, PK_REG_OUTPUT = 104;
 static_assert(PK_REG_PRODUCER + PK_REG_SOFTMAX + PK_REG_OUTPUT <= 3 * 168, "register split exceeds the launch");
-template <int DH>
+// Shared memory holds seven tiles at head_dim 128 and little else. Long key ranges take a third stage of keys; short ones
+// (LONG false), with many items a CTA, room for more of them looked up at its start (64 prompts of 512 tokens 260 us
+// against 266, three of 5,000 and more 548 against 535; head_dim 64 has room for both).
+template <int DH, bool LONG>
 struct PkLayout {
     static constexpr int NCH = DH / 64;
     static constexpr int TILE_BYTES = 128 * DH * 2;
-    static constexpr int QST = 2, KST = 3, VST = 2;
+    static constexpr int QST = 2, KST = LONG ? 3 : 2, VST = 2;
+    static constexpr int TABLE = LONG && DH == 128 ? 48 : 512;  // items of a CTA that are looked up at its start
     static constexpr int K_OFF = QST * TILE_BYTES, V_OFF = K_OFF + KST * TILE_BYTES;
     static constexpr int INV_OFF = V_OFF + VST * TILE_BYTES;  // [item parity][row]: 1 / sum
-    static constexpr int BAR_OFF = INV_OFF + 2 * PK_BM * 4;
+    static constexpr int TABLE_OFF = INV_OFF + 2 * PK_BM * 4;
+    static constexpr int BAR_OFF = TABLE_OFF + TABLE * 16;
     static constexpr int SMEM = BAR_OFF + 256 + 1024;
 };
-static_assert(PkLayout<128>::SMEM <= 227 * 1024, "shared memory");
+static_assert(PkLayout<128, true>::SMEM <= 227 * 1024 && PkLayout<128, false>::SMEM <= 227 * 1024, "shared memory");
 
 struct PackedArgs {
     const int4* items;
@@ -124,12 +129,12 @@ struct PackedArgs {
     int* err;
 };
 
-template <int DH>
+template <int DH, bool LONG>
 __global__ void __launch_bounds__(PK_THREADS, 1)
     attn_packed_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const PackedArgs a) {
-    using Ly = PkLayout<DH>;
-    constexpr int NCH = Ly::NCH, QST = Ly::QST, KST = Ly::KST, VST = Ly::VST, NR = PK_NR, TB = Ly::TILE_BYTES;
+    using Ly = PkLayout<DH, LONG>;
+    constexpr int NCH = Ly::NCH, QST = Ly::QST, KST = Ly::KST, VST = Ly::VST, TB = Ly::TILE_BYTES;
     constexpr uint32_t IDESC_S = idesc_bf16(PK_BM, PK_BN);
     constexpr uint32_t IDESC_O = idesc_bf16(PK_BM, DH, true);
     extern __shared__ uint8_t smem_raw[];
@@ -142,21 +147,22 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
     uint64_t* k_empty = k_full + KST;     // [KST]
     uint64_t* v_full = k_empty + KST;     // [VST]
     uint64_t* v_empty = v_full + VST;     // [VST]
-    uint64_t* s_full = v_empty + VST;     // [NR] scores of the region are complete
-    uint64_t* p_full = s_full + NR;       // [NR] P of the region is written (one arrival a warp, as for the next ones but o_full)
-    uint64_t* r_free = p_full + NR;       // [NR] P V of the region's tile is done
-    uint64_t* o_full = r_free + NR;       // [item parity] the item's last P V is done
+    uint64_t* s_full = v_empty + VST;     // the tile's scores are complete
+    uint64_t* s_empty = s_full + 1;       // they have been read (one arrival a warp, as for p_full, l_full and o_free)
+    uint64_t* p_full = s_empty + 1;       // [tile parity] P is written
+    uint64_t* pv_done = p_full + 2;       // [tile parity] P V is done
+    uint64_t* o_full = pv_done + 2;       // [item parity] the item's last P V is done
     uint64_t* l_full = o_full + 2;        // [item parity] the rows' sums are in shared memory
     uint64_t* o_free = l_full + 2;        // [item parity] accumulator and sums have been read out
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_free + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(o_free + 3);
-    static_assert((2 * (QST + KST + VST) + 3 * NR + 6 + 2) * 8 <= 256, "barriers");
+    static_assert((2 * (QST + KST + VST) + 6 + 6 + 2) * 8 <= 256, "barriers");
     volatile float* inv_sh = reinterpret_cast<volatile float*>(smem + Ly::INV_OFF);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (uint64_t* b = bars; b < o_free + 2; ++b) {
-            const bool by_warps = (b >= p_full && b < r_free) || b >= l_full;
+            const bool by_warps = (b >= s_empty && b < pv_done) || b >= l_full;
             mbar_init(b, by_warps ? 4 : 1);
         }
         *abort_flag = 0;
@@ -172,45 +178,51 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot, tmem_o = tmem + NR * PK_BN;  // accumulator of item n: tmem_o + (n & 1) * 128
+    const uint32_t tmem = *tmem_slot, tmem_p = tmem + PK_BN, tmem_o = tmem_p + PK_BN;  // P of tile g: tmem_p + (g & 1) * 64, O of item n: tmem_o + (n & 1) * 128
     bool ok = true;
     pdl_wait();  // the plan, Q, K and V come from earlier kernels
     pdl_trigger();
 
-    // A role's items, read one ahead of their use. n_tiles = 0: none left.
+    // This CTA's items, n_tiles = 0: none left. The first Ly::TABLE are looked up at the start by all threads (looked up by each role
+    // when its turn came, an item cost some 1,000 cycles of it).
     const int Hq = a.Hq, pg_log = a.pg_log, groups = Hq >> pg_log, tpt_log = 7 - pg_log;  // tokens of a tile
     const int n_items = min(max(*a.count, 0), a.capacity) * Hq;
     const int G = (int)gridDim.x, me = (int)blockIdx.x;
+    int4* table = reinterpret_cast<int4*>(smem + Ly::TABLE_OFF);
+    auto look_up = [&](int round) -> int4 {  // first query row, query rows + 256 * group of heads, first key row, key position
+        const int k = round * G + ((round & 1) ? G - 1 - me : me);
+        const int entry = (int)((unsigned)k / (unsigned)Hq), rem = k - entry * Hq;
+        const int sub = (int)((unsigned)rem / (unsigned)groups), first = sub << tpt_log;
+        const int4 v = __ldg(a.items + entry);
+        const int rows = max(0, min(v.y - first, 1 << tpt_log));  // (0: the entry has fewer tokens)
+        return make_int4(v.x + first, rows + 256 * (rem - sub * groups), v.z, v.w + first);
+    };
+    auto is_item = [&](int round) { return round * G + ((round & 1) ? G - 1 - me : me) < n_items; };
+    for (int round = threadIdx.x; round < Ly::TABLE && round <= n_items / G && is_item(round); round += PK_THREADS)
+        table[round] = look_up(round);
+    __syncthreads();
     struct Item {
         int q0, q_end, k0, pos0, hg, n_valid, n_tiles;  // hg: group of PG heads
     };
-    int round = 0;
-    auto fetch = [&]() -> Item {
+    int next_round = 0;
+    auto next_item = [&]() -> Item {
         Item it{};
         while (true) {
-            const int k = round * G + ((round & 1) ? G - 1 - me : me);
-            if (k >= n_items) return it;
-            ++round;
-            const int entry = (int)((unsigned)k / (unsigned)Hq), rem = k - entry * Hq;
-            const int sub = (int)((unsigned)rem / (unsigned)groups);
-            const int4 v = __ldg(a.items + entry);
-            const int first = sub << tpt_log, rows = min(v.y - first, 1 << tpt_log);
-            if (rows <= 0) continue;  // the entry has fewer tokens
-            it.hg = rem - sub * groups;
-            it.q0 = v.x + first;
-            it.q_end = min(it.q0 + rows, a.Nq);
+            const int round = next_round;
+            if (!is_item(round)) return it;
+            ++next_round;
+            const int4 v = round < Ly::TABLE ? table[round] : look_up(round);
+            const int rows = v.y & 255;
+            if (rows == 0) continue;
+            it.hg = v.y >> 8;
+            it.q0 = v.x;
+            it.q_end = min(v.x + rows, a.Nq);
             it.k0 = v.z;
-            it.pos0 = v.w + first;
-            it.n_valid = min(max(it.pos0 + rows, 0), a.max_keys);
+            it.pos0 = v.w;
+            it.n_valid = min(max(v.w + rows, 0), a.max_keys);
             it.n_tiles = max(1, (it.n_valid + PK_BN - 1) / PK_BN);  // without a key: one tile, all of it masked
             return it;
         }
-    };
-    Item ahead = fetch();
-    auto next_item = [&]() -> Item {
-        const Item it = ahead;
-        ahead = fetch();
-        return it;
     };
 
     // A role ends when what it has asked for is done, also after a wait of the CTA gave up: no copy or product of this CTA may
@@ -247,7 +259,7 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
                 drain_ring(n, QST, [&](int s, int parity) { last_wait(&q_full[s], parity); });
             }
         } else if (warp == 1) {
-            // ---------------- S of tile g into region g % NR, once P V of tile g - NR has finished with it
+            // ---------------- S of tile g, once the scores of the tile before have been read
             if (lane == 0) {
                 int g = 0;
                 for (int n = 0; ok; ++n) {
@@ -256,24 +268,22 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
                     if (nt == 0) break;
                     if (!mbar_wait_suspend(&q_full[qs], (n / QST) & 1, abort_flag)) { ok = false; break; }
                     for (int i = 0; i < nt; ++i, ++g) {
-                        const int s = g % KST, r = g % NR;
+                        const int s = g % KST;
                         if (!mbar_wait_suspend(&k_full[s], (g / KST) & 1, abort_flag)) { ok = false; break; }
-                        // the region's next completion would be P V of tile g itself: the parity cannot alias
-                        if (g >= NR && !mbar_wait_suspend(&r_free[r], ((g - NR) / NR) & 1, abort_flag)) { ok = false; break; }
+                        if (!mbar_wait_suspend(s_empty, (g & 1) ^ 1, abort_flag)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t sq = smem_u32(smem + qs * TB), sk = smem_u32(smem + Ly::K_OFF + s * TB);
 #pragma unroll
                         for (int kk = 0; kk < DH / 16; ++kk) {
                             const uint32_t off = (kk >> 2) * PK_BM * 128 + (kk & 3) * 32;
-                            umma_bf16_ss(tmem + r * PK_BN, sdesc_kmajor_sw128(sq + off), sdesc_kmajor_sw128(sk + off), IDESC_S,
-                                         kk > 0);
+                            umma_bf16_ss(tmem, sdesc_kmajor_sw128(sq + off), sdesc_kmajor_sw128(sk + off), IDESC_S, kk > 0);
                         }
-                        umma_commit(&s_full[r]);
+                        umma_commit(s_full);
                         umma_commit(&k_empty[s]);
                         if (i == nt - 1) umma_commit(&q_empty[qs]);  // the item's last scores release Q
                     }
                 }
-                if (g > 0) last_wait(&s_full[(g - 1) % NR], ((g - 1) / NR) & 1);  // (completes behind every earlier tile's)
+                if (g > 0) last_wait(s_full, (g - 1) & 1);  // (completes behind every earlier tile's)
             }
         } else if (warp == 2) {
             // ---------------- value tiles
@@ -293,7 +303,7 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
                 drain_ring(g, VST, [&](int s, int parity) { last_wait(&v_full[s], parity); });
             }
         } else {
-            // ---------------- O += P V of tile g: P from region g % NR (A operand in tensor memory), V from stage g % VST
+            // ---------------- O += P V of tile g: P as A operand in tensor memory, V from stage g % VST
             int g = 0, done = 0;
             for (int n = 0; ok; ++n) {
                 const Item it = next_item();
@@ -301,7 +311,8 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
                 if (nt == 0) break;
                 const uint32_t to = tmem_o + (n & 1) * 128;
                 for (int i = 0; ok && i < nt; ++i, ++g) {
-                    const int s = g % VST, r = g % NR;
+                    const int s = g % VST;
+                    const uint32_t tp = tmem_p + (g & 1) * 64;
                     if (!__all_sync(0xffffffffu, mbar_wait_suspend(&v_full[s], (g / VST) & 1, abort_flag))) { ok = false; break; }
                     uint8_t* sv_p = smem + Ly::V_OFF + s * TB;
                     const int r0 = it.n_valid - i * PK_BN;  // value rows from here on are not seen by the item, and may hold anything
@@ -316,21 +327,21 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
                     __syncwarp();
                     if (lane == 0) {
                         bool w = i > 0 || mbar_wait_suspend(&o_free[n & 1], ((n >> 1) & 1) ^ 1, abort_flag);  // item n - 2's O is read out
-                        w = w && mbar_wait_suspend(&p_full[r], (g / NR) & 1, abort_flag);
+                        w = w && mbar_wait_suspend(&p_full[g & 1], (g >> 1) & 1, abort_flag);
                         if (w) {
                             tc_fence_after();
                             const uint32_t sv = smem_u32(sv_p);
                             if (steps < PK_BN / 16) {
                                 for (int kk = 0; kk < steps; ++kk)
-                                    umma_bf16_ts(to, tmem + r * PK_BN + kk * 8, sdesc_mnmajor_sw128(sv + kk * 16 * 128, PK_BN * 128),
+                                    umma_bf16_ts(to, tp + kk * 8, sdesc_mnmajor_sw128(sv + kk * 16 * 128, PK_BN * 128),
                                                  IDESC_O, (i | kk) != 0);
                             } else {
 #pragma unroll
                                 for (int kk = 0; kk < PK_BN / 16; ++kk)
-                                    umma_bf16_ts(to, tmem + r * PK_BN + kk * 8, sdesc_mnmajor_sw128(sv + kk * 16 * 128, PK_BN * 128),
+                                    umma_bf16_ts(to, tp + kk * 8, sdesc_mnmajor_sw128(sv + kk * 16 * 128, PK_BN * 128),
                                                  IDESC_O, (i | kk) != 0);
                             }
-                            umma_commit(&r_free[r]);
+                            umma_commit(&pv_done[g & 1]);
                             umma_commit(&v_empty[s]);
                             if (i == nt - 1) umma_commit(&o_full[n & 1]);
                             ++done;
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                 }
             }
-            if (lane == 0 && done > 0) last_wait(&r_free[(done - 1) % NR], ((done - 1) / NR) & 1);
+            if (lane == 0 && done > 0) last_wait(&pv_done[(done - 1) & 1], ((done - 1) >> 1) & 1);
             __syncwarp();
         }
     } else if (warp < 8) {
@@ -358,20 +369,23 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
             const uint32_t to = tmem_o + (n & 1) * 128 + lane_off;
             float m = -INFINITY, l = 0.f;  // the row's scale (log2 units) and sum
             for (int i = 0; i < nt; ++i, ++g) {
-                const int r = g % NR;
-                const uint32_t ts = tmem + r * PK_BN + lane_off;
-                if (!__all_sync(0xffffffffu, mbar_wait_suspend(&s_full[r], (g / NR) & 1, abort_flag))) { ok = false; break; }
+                const uint32_t ts = tmem + lane_off, tp = tmem_p + (g & 1) * 64 + lane_off;
+                if (!__all_sync(0xffffffffu, mbar_wait_suspend(s_full, g & 1, abort_flag))) { ok = false; break; }
                 tc_fence_after();
                 uint32_t sr[PK_BN];
 #pragma unroll
                 for (int c = 0; c < PK_BN / 32; ++c)
                     tmem_ld_32x32b_x32(ts + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
                 tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_empty);  // the next tile's scores may come
                 if (i * PK_BN + PK_BN - 1 > it.pos0) {  // some row does not see all of the tile
                     const int lim = pos - i * PK_BN;    // last visible column
 #pragma unroll
-                    for (int c = 0; c < PK_BN / 32; ++c) {
+                    for (int c = 0; c < PK_BN / 32; ++c) {  // (a warp's rows are 32 tokens at most: one or two parts are mixed)
                         const uint32_t vis = low_bits(lim + 1 - 32 * c);
+                        if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             sr[c * 32 + e] = vis & (1u << e) ? sr[c * 32 + e] : __float_as_uint(-INFINITY);
@@ -386,10 +400,10 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
                 const bool grow = mx > m + 8.0f;
                 const float alpha = grow ? ex2_approx(m - mx) : 1.0f;
                 if (i > 0 && __any_sync(0xffffffffu, grow)) {
-                    // O must hold every earlier tile's P V. (The region's next P V needs a P that is not released yet: the
-                    // parity cannot alias.)
+                    // O must hold every earlier tile's P V. (The next P V of this parity needs a P that is not released yet: the
+                    // phase cannot alias.)
                     const int k = g - 1;
-                    if (!__all_sync(0xffffffffu, mbar_wait_suspend(&r_free[k % NR], (k / NR) & 1, abort_flag))) { ok = false; break; }
+                    if (!__all_sync(0xffffffffu, mbar_wait_suspend(&pv_done[k & 1], (k >> 1) & 1, abort_flag))) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < DH / 32; ++c) {
@@ -410,6 +424,9 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
                 const float nm = m == -INFINITY ? 0.f : -m;
                 const float2 sl2x2 = make_float2(sl2, sl2), nmx2 = make_float2(nm, nm);
                 float2 rs2 = make_float2(0.f, 0.f);
+                // P V of the tile before last has used the place
+                if (!__all_sync(0xffffffffu, mbar_wait_suspend(&pv_done[g & 1], ((g >> 1) & 1) ^ 1, abort_flag))) { ok = false; break; }
+                tc_fence_after();
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t pk[32];
@@ -422,13 +439,13 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
                         rs2 = add2(rs2, pp);
                         pk[e] = pack_bf16(pp.x, pp.y);
                     }
-                    tmem_st_32x32b_x32(ts + half * 32, pk);
+                    tmem_st_32x32b_x32(tp + half * 32, pk);
                 }
                 tmem_st_wait();
                 l += rs2.x + rs2.y;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[r]);
+                if (lane == 0) mbar_arrive(&p_full[g & 1]);
             }
             if (!ok) break;
             // the sums go to the output warps, once those of item n - 2 have been read
@@ -508,8 +525,11 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
     }
 }
 
-template <int DH>
-cudaError_t packed_launch_dh(const PackedCall& c, cudaStream_t st) {
+// Keys up to which a batch's longest sequence counts as short.
+constexpr int kPackedShort = 1024;
+
+template <int DH, bool LONG>
+cudaError_t packed_launch_form(const PackedCall& c, cudaStream_t st) {
     // heads of a tile: the largest power of two in the group, up to a tile's rows
     int pg_log = 0;
     while (pg_log < 7 && (c.Hq / c.Hkv) % (2 << pg_log) == 0) ++pg_log;
@@ -526,18 +546,24 @@ cudaError_t packed_launch_dh(const PackedCall& c, cudaStream_t st) {
     const PackedArgs a{reinterpret_cast<const int4*>(static_cast<const char*>(c.plan) + kPlanHeader),
                        static_cast<const int*>(c.plan), c.capacity, c.Nk, c.Nq, c.Hq, c.Hkv, pg_log, c.out, c.err};
     const unsigned grid = (unsigned)std::min<long long>((long long)c.capacity * c.Hq, device_sm_count());
-    return launch_pdl(attn_packed_kernel<DH>, dim3(grid), dim3(PK_THREADS), PkLayout<DH>::SMEM, st, tq, tk, tv, a);
+    return launch_pdl(attn_packed_kernel<DH, LONG>, dim3(grid), dim3(PK_THREADS), PkLayout<DH, LONG>::SMEM, st, tq, tk, tv, a);
+}
+template <int DH>
+cudaError_t packed_launch_dh(const PackedCall& c, cudaStream_t st) {
+    if constexpr (DH == 128)
+        if (c.longest <= kPackedShort) return packed_launch_form<DH, false>(c, st);
+    return packed_launch_form<DH, true>(c, st);
 }
 
 // setmaxnreg.inc waits until the registers it asks for are free: the compiled kernel has to be given at least those that its
 // split hands out.
-template <int DH>
-cudaError_t packed_prepare_dh() {
+template <int DH, bool LONG>
+cudaError_t packed_prepare_form() {
     cudaFuncAttributes fa{};
-    cudaError_t e = cudaFuncGetAttributes(&fa, attn_packed_kernel<DH>);
+    cudaError_t e = cudaFuncGetAttributes(&fa, attn_packed_kernel<DH, LONG>);
     if (e != cudaSuccess) return e;
     if (PK_THREADS * fa.numRegs < 128 * (int)(PK_REG_PRODUCER + PK_REG_SOFTMAX + PK_REG_OUTPUT)) return cudaErrorLaunchOutOfResources;
-    return cudaFuncSetAttribute(attn_packed_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, PkLayout<DH>::SMEM);
+    return cudaFuncSetAttribute(attn_packed_kernel<DH, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, PkLayout<DH, LONG>::SMEM);
 }
 
 }  // namespace
@@ -559,8 +585,9 @@ cudaError_t attn_packed_launch(const PackedCall& c, int dh, cudaStream_t st) {
     return cudaErrorInvalidValue;
 }
 cudaError_t attention_packed_prepare() {
-    cudaError_t e = packed_prepare_dh<128>();
-    return e == cudaSuccess ? packed_prepare_dh<64>() : e;
+    cudaError_t e = packed_prepare_form<128, true>();
+    if (e == cudaSuccess) e = packed_prepare_form<128, false>();
+    return e == cudaSuccess ? packed_prepare_form<64, true>() : e;
 }
 
 }  // namespace q3

@@ -243,7 +243,7 @@ struct PackedCall {
     long long ldq, ldk, ldv;  // elements from row to row
     int Nq, Nk, Hq, Hkv;
     const void* plan;
-    int capacity;  // entries that the plan has room for
+    int capacity, longest;  // entries that the plan has room for; keys of the longest sequence, which only picks the kernel's form
     __nv_bfloat16* out;
     int* err;
 };

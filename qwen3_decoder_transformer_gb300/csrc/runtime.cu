@@ -1259,7 +1259,7 @@ int qwen3_op_attention_prefill_packed(const void* q, int64_t ldq, const void* k,
     if (Nq == 0 || capacity == 0) return QWEN3_OK;
     if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
     const PackedCall c{static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v), ldq, ldk, ldv, Nq,
-                       Nk, Hq, Hkv, plan, (int)capacity, static_cast<bf16*>(out), err};
+                       Nk, Hq, Hkv, plan, (int)capacity, longest, static_cast<bf16*>(out), err};
     return attn_packed_launch(c, dh, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QWEN3_OK : QWEN3_E_CUDA;
 }
 
