@@ -470,6 +470,66 @@ QWEN3_API int qwen3_op_attention_prefill_packed(const void* d_q, int64_t ldq, co
                                                 int64_t ldv, int Nq, int Nk, int Hq, int Hkv, int dh, const void* d_plan,
                                                 size_t plan_bytes, int longest, void* d_out, int* d_err, void* stream);
 
+/* The calls above that every layer makes, with their arguments in one block of host memory (read during the call only): the
+ * same fields, checks and results, for bindings that pay for each argument of a foreign call. */
+typedef struct qwen3_append_paged4_args {
+    const void* d_qkv;
+    int64_t ld;
+    int32_t N;
+    const int* d_cu;
+    const int* d_start;
+    int32_t S, Hq, Hkv, dh;
+    const void *d_q_gamma, *d_k_gamma;
+    float eps;
+    const void* d_cos_sin;
+    int32_t n_pos;
+    void *d_q_out, *d_k_out, *d_k_pages, *d_v_pages;
+    int32_t n_pages, page_size;
+    const int* d_page_table;
+    int32_t max_pages;
+    int* d_err;
+} qwen3_append_paged4_args;
+typedef struct qwen3_read_paged4_args {
+    const void *d_k_pages, *d_v_pages;
+    int32_t n_pages, page_size;
+    const int* d_page_table;
+    int32_t max_pages;
+    const int *d_cu, *d_start;
+    int32_t S, N, Hkv, dh;
+    void *d_k_out, *d_v_out;
+    int* d_err;
+} qwen3_read_paged4_args;
+typedef struct qwen3_attention_decode_paged4_args {
+    const void *d_q, *d_k_pages, *d_v_pages;
+    int32_t n_pages, page_size;
+    const int* d_page_table;
+    int32_t max_pages;
+    const int* d_len0;
+    int32_t B, Hq, Hkv, dh;
+    void* d_work;
+    size_t work_bytes;
+    void* d_out;
+    int* d_err;
+} qwen3_attention_decode_paged4_args;
+typedef struct qwen3_attention_prefill_packed_args {
+    const void* d_q;
+    int64_t ldq;
+    const void* d_k;
+    int64_t ldk;
+    const void* d_v;
+    int64_t ldv;
+    int32_t Nq, Nk, Hq, Hkv, dh;
+    const void* d_plan;
+    size_t plan_bytes;
+    int32_t longest;
+    void* d_out;
+    int* d_err;
+} qwen3_attention_prefill_packed_args;
+QWEN3_API int qwen3_op_append_paged4_block(const qwen3_append_paged4_args* args, void* stream);
+QWEN3_API int qwen3_op_read_paged4_block(const qwen3_read_paged4_args* args, void* stream);
+QWEN3_API int qwen3_op_attention_decode_paged4_block(const qwen3_attention_decode_paged4_args* args, void* stream);
+QWEN3_API int qwen3_op_attention_prefill_packed_block(const qwen3_attention_prefill_packed_args* args, void* stream);
+
 /* Log probabilities of given tokens, with the entropy of each row's distribution and its largest
  * alternatives (scoring a prompt from the all-rows logits of a prefill, or a sampled token from a decode
  * step's). For row m of logits x = d_logits[m * ld ..] (V values, fp32 or bf16 by logits_type):

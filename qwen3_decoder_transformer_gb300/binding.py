@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -126,6 +127,8 @@ def lib() -> ctypes.CDLL:
     L.qwen3_attention_packed_plan_bytes.argtypes = [i, i]
     L.qwen3_op_attention_packed_plan.argtypes = [_vp, _vp, i, i, i, _vp, sz, _vp, _vp]
     L.qwen3_op_attention_prefill_packed.argtypes = [_vp, i64, _vp, i64, _vp, i64, i, i, i, i, i, _vp, sz, i, _vp, _vp, _vp]
+    for name in ("append_paged4", "read_paged4", "attention_decode_paged4", "attention_prefill_packed"):
+        getattr(L, f"qwen3_op_{name}_block").argtypes = [ctypes.c_char_p, _vp]
     _lib = L
     return L
 
@@ -594,7 +597,13 @@ def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rol
 #
 # As above, what is wrong with a call's tensors is worked out (the _why functions) only when one expression finds something.
 
+# Their arguments go in one block each (the args structs of the header, in native layout): a foreign call costs 0.1 us an argument.
+
 _U8 = torch.uint8
+_APPEND_ARGS = struct.Struct("PqiPPiiiiPPfPiPPPPiiPiP")
+_READ_ARGS = struct.Struct("PPiiPiPPiiiiPPP")
+_DECODE_ARGS = struct.Struct("PPPiiPiPiiiiPNPP")
+_PACKED_ARGS = struct.Struct("PqPqPqiiiiiPNiPP")
 PAGE_SIZES = (16, 32, 64, 128, 256)
 _PAGE_OF = {(p * (dh // 2 + dh // 16), dh): p for p in PAGE_SIZES for dh in (64, 128)}  # by page bytes and head_dim
 
@@ -682,16 +691,17 @@ def op_append_paged4(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_ou
         ok = False
     if not ok:
         _why_append(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out, q_gamma, k_gamma)
-    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
+    p_err = 0 if err is None else _dense("err", err, _I32, (1,), dev)
     if N == 0 or S == 0:
         return
     if N == 1:  # (the stride of a single row says nothing)
         ld = (Hq + 2 * Hkv) * dh
-    _launch(lib().qwen3_op_append_paged4,
-            (qkv.data_ptr(), ld, N, cu.data_ptr(), start.data_ptr(), S, Hq, Hkv, dh,
-             None if q_gamma is None else q_gamma.data_ptr(), None if k_gamma is None else k_gamma.data_ptr(), eps,
-             cos_sin.data_ptr(), n_pos, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), k_pages.data_ptr(),
-             v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, p_err), dev, stream)
+    _launch(lib().qwen3_op_append_paged4_block,
+            (_APPEND_ARGS.pack(qkv.data_ptr(), ld, N, cu.data_ptr(), start.data_ptr(), S, Hq, Hkv, dh,
+                               0 if q_gamma is None else q_gamma.data_ptr(), 0 if k_gamma is None else k_gamma.data_ptr(), eps,
+                               cos_sin.data_ptr(), n_pos, q_out.data_ptr(), 0 if k_out is None else k_out.data_ptr(),
+                               k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,
+                               p_err),), dev, stream)
 
 
 def _why_read(k_pages, v_pages, page_table, cu, start, k_out, v_out):
@@ -728,12 +738,13 @@ def op_read_paged4(k_pages, v_pages, page_table, cu, start, k_out, v_out, err=No
         ok = False
     if not ok:
         _why_read(k_pages, v_pages, page_table, cu, start, k_out, v_out)
-    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
+    p_err = 0 if err is None else _dense("err", err, _I32, (1,), dev)
     if N == 0 or S == 0:
         return
-    _launch(lib().qwen3_op_read_paged4,
-            (k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, cu.data_ptr(),
-             start.data_ptr(), S, N, Hkv, dh, k_out.data_ptr(), v_out.data_ptr(), p_err), dev, stream)
+    _launch(lib().qwen3_op_read_paged4_block,
+            (_READ_ARGS.pack(k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,
+                             cu.data_ptr(), start.data_ptr(), S, N, Hkv, dh, k_out.data_ptr(), v_out.data_ptr(), p_err),),
+            dev, stream)
 
 
 def attention_decode_paged4_workspace(B, Hq, Hkv, dh) -> int:
@@ -777,12 +788,13 @@ def op_attention_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out,
         ok = False
     if not ok:
         _why_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out)
-    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
+    p_err = 0 if err is None else _dense("err", err, _I32, (1,), dev)
     if B == 0:
         return
-    _launch(lib().qwen3_op_attention_decode_paged4,
-            (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,
-             len0.data_ptr(), B, Hq, Hkv, dh, work.data_ptr(), work.nbytes, out.data_ptr(), p_err), dev, stream)
+    _launch(lib().qwen3_op_attention_decode_paged4_block,
+            (_DECODE_ARGS.pack(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(),
+                               max_pages, len0.data_ptr(), B, Hq, Hkv, dh, work.data_ptr(), work.nbytes, out.data_ptr(),
+                               p_err),), dev, stream)
 
 
 def attention_packed_plan_bytes(Nq, S) -> int:
@@ -842,13 +854,13 @@ def op_attention_prefill_packed(q, k, v, plan, longest, out, err=None, stream=No
         ok = False
     if not ok:
         _why_packed(q, k, v, plan, out)
-    p_err = None if err is None else _dense("err", err, _I32, (1,), dev)
+    p_err = 0 if err is None else _dense("err", err, _I32, (1,), dev)
     if Nq == 0:
         return
     if Nq == 1:  # (the stride of a single row says nothing)
         ldq = Hq * dh
     if Nk <= 1:
         ldk = ldv = Hkv * dh
-    _launch(lib().qwen3_op_attention_prefill_packed,
-            (q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, Nq, Nk, Hq, Hkv, dh, plan.data_ptr(), plan.nbytes,
-             _int32(longest), out.data_ptr(), p_err), dev, stream)
+    _launch(lib().qwen3_op_attention_prefill_packed_block,
+            (_PACKED_ARGS.pack(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, Nq, Nk, Hq, Hkv, dh, plan.data_ptr(),
+                               plan.nbytes, _int32(longest), out.data_ptr(), p_err),), dev, stream)

@@ -1263,6 +1263,29 @@ int qwen3_op_attention_prefill_packed(const void* q, int64_t ldq, const void* k,
     return attn_packed_launch(c, dh, static_cast<cudaStream_t>(stream)) == cudaSuccess ? QWEN3_OK : QWEN3_E_CUDA;
 }
 
+int qwen3_op_append_paged4_block(const qwen3_append_paged4_args* a, void* stream) {
+    if (!a) return QWEN3_E_ARG;
+    return qwen3_op_append_paged4(a->d_qkv, a->ld, a->N, a->d_cu, a->d_start, a->S, a->Hq, a->Hkv, a->dh, a->d_q_gamma,
+                                  a->d_k_gamma, a->eps, a->d_cos_sin, a->n_pos, a->d_q_out, a->d_k_out, a->d_k_pages,
+                                  a->d_v_pages, a->n_pages, a->page_size, a->d_page_table, a->max_pages, a->d_err, stream);
+}
+int qwen3_op_read_paged4_block(const qwen3_read_paged4_args* a, void* stream) {
+    if (!a) return QWEN3_E_ARG;
+    return qwen3_op_read_paged4(a->d_k_pages, a->d_v_pages, a->n_pages, a->page_size, a->d_page_table, a->max_pages, a->d_cu,
+                                a->d_start, a->S, a->N, a->Hkv, a->dh, a->d_k_out, a->d_v_out, a->d_err, stream);
+}
+int qwen3_op_attention_decode_paged4_block(const qwen3_attention_decode_paged4_args* a, void* stream) {
+    if (!a) return QWEN3_E_ARG;
+    return qwen3_op_attention_decode_paged4(a->d_q, a->d_k_pages, a->d_v_pages, a->n_pages, a->page_size, a->d_page_table,
+                                            a->max_pages, a->d_len0, a->B, a->Hq, a->Hkv, a->dh, a->d_work, a->work_bytes,
+                                            a->d_out, a->d_err, stream);
+}
+int qwen3_op_attention_prefill_packed_block(const qwen3_attention_prefill_packed_args* a, void* stream) {
+    if (!a) return QWEN3_E_ARG;
+    return qwen3_op_attention_prefill_packed(a->d_q, a->ldq, a->d_k, a->ldk, a->d_v, a->ldv, a->Nq, a->Nk, a->Hq, a->Hkv, a->dh,
+                                             a->d_plan, a->plan_bytes, a->longest, a->d_out, a->d_err, stream);
+}
+
 int qwen3_op_attention_decode_noalloc(const void* q, const void* kc, const void* vc, int B, int Hq, int Hkv, int dh,
                                       int cap, const int* len0, void* out, int* err, void* stream) {
     if (!q || !kc || !vc || !len0 || !out || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (dh != 64 && dh != 128) ||

@@ -10,6 +10,8 @@ Tolerances. A bf16 result is off by half a step, 2^-8 of its value at most.
   sums of at most one step for 16 keys, each off by 2^-23 of a sum of up to 143 times the weights. Scores are fp32 sums of
   a few exact products, off by 2^-20 of their terms, and so is the exponential: 2^-18 (1 + the largest score term) of every weight.
 """
+import struct
+
 import numpy as np
 import pytest
 import torch
@@ -583,6 +585,40 @@ def test_library_refuses(bd):
     assert decode(B=0) == 0
     assert bd.attention_decode_paged4_workspace(0, 8, 4, 64) == 0
     assert bd.attention_decode_paged4_workspace(1, 36, 4, 64) == 0
+
+
+def test_argument_blocks(bd):
+    """The blocks that the binding packs have the header's layout: every field, wrong by itself, is refused as in the direct call,
+    and the right ones are taken (a call without rows does nothing)."""
+    L, p, size = bd.lib(), 4096, 1 << 30
+    # (the row count, field `rows`, stays 0: nothing is launched)
+    forms = ((L.qwen3_op_append_paged4_block, bd._APPEND_ARGS, L.qwen3_op_append_paged4, 2,
+              [p, 1024, 0, p, p, 1, 8, 4, 64, p, p, 1e-6, p, 10, p, p, p, p, 4, 16, p, 2, 0]),
+             (L.qwen3_op_read_paged4_block, bd._READ_ARGS, L.qwen3_op_read_paged4, 9,
+              [p, p, 4, 16, p, 2, p, p, 1, 0, 4, 64, p, p, 0]),
+             (L.qwen3_op_attention_decode_paged4_block, bd._DECODE_ARGS, L.qwen3_op_attention_decode_paged4, 8,
+              [p, p, p, 4, 16, p, 2, p, 0, 8, 4, 64, p, size, p, 0]),
+             (L.qwen3_op_attention_prefill_packed_block, bd._PACKED_ARGS, L.qwen3_op_attention_prefill_packed, 6,
+              [p, 512, p, 256, p, 256, 0, 100, 8, 4, 64, p, 1 << 20, 100, p, 0]))
+    for block, layout, direct, rows, args in forms:
+        assert args[rows] == 0
+        assert block(layout.pack(*args), None) == 0 and direct(*args, None) == 0
+        assert block(None, None) == 5
+        refused = 0
+        for i in range(len(args)):
+            for bad in (0, -1, 7, p + 2):
+                wrong = list(args)
+                wrong[i] = bad
+                if i == rows:
+                    continue
+                try:
+                    packed = layout.pack(*wrong)
+                except (OverflowError, struct.error):  # no such pointer or size
+                    continue
+                want = direct(*wrong, None)
+                assert want in (0, 5) and block(packed, None) == want, (block.__name__, i, bad)
+                refused += want == 5
+        assert refused > len(args)
 
 
 def test_binding_refuses(bd):
