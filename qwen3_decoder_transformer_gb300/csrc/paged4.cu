@@ -57,14 +57,6 @@ __device__ __forceinline__ bool place_token(const Packed& p, const Paged4& c, in
     return true;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& r, float* x) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
 __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
@@ -348,11 +340,13 @@ struct ReadArgs {
     int* err;
 };
 
-// One warp a token: LPH lanes take the 16 dims each of one row (K or V of a head). Every value is rounded once.
+// One warp a token: DH / 8 lanes take a row (K or V of a head), eight dims each, so that a store of the warp fills 512 contiguous
+// bytes; RD_ROWS rows' loads are on their way at once. Every value is rounded once.
+constexpr int RD_ROWS = 4;
 template <int DH>
 __global__ void __launch_bounds__(256)
     read_paged4_kernel(const ReadArgs a) {
-    constexpr int LPH = DH / 16;
+    constexpr int LPR = DH / 8, RPW = 32 / LPR;  // lanes a row, rows a warp at once
     const int lane = threadIdx.x & 31, t = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
     pdl_wait();
     pdl_trigger();
@@ -362,21 +356,27 @@ __global__ void __launch_bounds__(256)
         if (lane == 0 && a.err) atomicOr(a.err, ERR_INDEX);
         return;
     }
-    const int page = 1 << a.cache.page_log, l = lane % LPH;
-    for (int h = lane / LPH; h < 2 * a.Hkv; h += 32 / LPH) {
-        const bool is_v = h >= a.Hkv;
-        const int hh = is_v ? h - a.Hkv : h;
-        const uint8_t* base = (is_v ? a.cache.v : a.cache.k) + (size_t)(pl.page + hh) * p4_page_bytes(page, DH);
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(base + (size_t)pl.row * (DH / 2)) + l);
-        const uint32_t sd = __ldg(reinterpret_cast<const uint32_t*>(base + (size_t)page * (DH / 2)) +
-                                  pl.row * (DH / kP4Group) + l * 16 / kP4Group);
-        const float scale = bf16_lo(sd), low = bf16_hi(sd);
-        float x[16];
+    const int page_log = a.cache.page_log, head_bytes = (int)p4_page_bytes(1 << page_log, DH), l = lane % LPR;
+    const int code_at = pl.row * (DH / 2) + l * 4, side_at = (DH / 2 << page_log) + pl.row * (DH / kP4Group * 4) + l * 8 / kP4Group * 4;
+    for (int h0 = 0; h0 < a.Hkv; h0 += RPW * RD_ROWS / 2) {
+        uint32_t code[RD_ROWS], side[RD_ROWS];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = fmaf((float)(((i < 8 ? w.x : w.y) >> (4 * (i & 7))) & 15u), scale, low);
-        __nv_bfloat16* dst = (is_v ? a.v_out : a.k_out) + ((size_t)t * a.Hkv + hh) * DH + l * 16;
-        reinterpret_cast<uint4*>(dst)[0] = pack8(x);
-        reinterpret_cast<uint4*>(dst)[1] = pack8(x + 8);
+        for (int i = 0; i < RD_ROWS; ++i) {  // K and V of a head in turn
+            const int h = min(h0 + i / 2 * RPW + lane / LPR, a.Hkv - 1);
+            const uint8_t* base = (i & 1 ? a.cache.v : a.cache.k) + pl.page * head_bytes + (size_t)h * head_bytes;
+            code[i] = __ldg(reinterpret_cast<const uint32_t*>(base + code_at));
+            side[i] = __ldg(reinterpret_cast<const uint32_t*>(base + side_at));
+        }
+#pragma unroll
+        for (int i = 0; i < RD_ROWS; ++i) {
+            const int h = h0 + i / 2 * RPW + lane / LPR;
+            const float scale = bf16_lo(side[i]), low = bf16_hi(side[i]);
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = fmaf((float)((code[i] >> (4 * k)) & 15u), scale, low);
+            if (h < a.Hkv)
+                *reinterpret_cast<uint4*>((i & 1 ? a.v_out : a.k_out) + ((size_t)t * a.Hkv + h) * DH + l * 8) = pack8(x);
+        }
     }
 }
 
