@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
         const int entry = (int)((unsigned)k / (unsigned)Hq), rem = k - entry * Hq;
         const int sub = (int)((unsigned)rem / (unsigned)groups), first = sub << tpt_log;
         const int4 v = __ldg(a.items + entry);
-        const int rows = max(0, min(v.y - first, 1 << tpt_log));  // (0: the entry has fewer tokens)
+        // 0: the entry has fewer tokens, or is none of a plan for these queries
+        const int rows = (unsigned)v.x < (unsigned)a.Nq ? max(0, min(v.y - first, 1 << tpt_log)) : 0;
         return make_int4(v.x + first, rows + 256 * (rem - sub * groups), v.z, v.w + first);
     };
     auto is_item = [&](int round) { return round * G + ((round & 1) ? G - 1 - me : me) < n_items; };

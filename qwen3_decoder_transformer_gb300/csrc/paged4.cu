@@ -113,6 +113,10 @@ __device__ __forceinline__ uint32_t codes_of(const float2 (&x)[4], uint32_t side
     return c - 0x11111111u * 0x4b400000u;  // every code carries the bits of kWhole
 }
 
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 struct AppendArgs {
     const __nv_bfloat16* qkv;
     long long ld;
@@ -133,7 +137,8 @@ struct AppendArgs {
 //   (a, b) -> (r (g_a cos a - g_b sin b), r (g_b cos b + g_a sin a)) in fp32, rounded once;
 // the products of gains and angles are made once a token and kind of head. The next piece's values, and the next token's
 // angles, are on their way meanwhile; a sequence is looked up once, then followed from token to token.
-constexpr int AP_AHEAD = 2, AP_CTAS = 5;  // CTAs of four warps an SM
+constexpr int AP_AHEAD = 4, AP_CTAS = 4;  // pieces ahead; CTAs of four warps an SM (32,768 tokens and their read: 163 us, five CTAs 172,
+                                          // six 172; two pieces ahead 168, eight 177)
 template <int DH>
 __global__ void __launch_bounds__(128, AP_CTAS)
     append_paged4_kernel(const AppendArgs a, int per, int parts) {
@@ -155,22 +160,28 @@ __global__ void __launch_bounds__(128, AP_CTAS)
     __syncthreads();
     if (t0 >= t1) return;
     const int hl = lane / LPH;  // this lane's head of a piece
-    uint4 raw[AP_AHEAD][2];  // of the pieces ahead
+    // The pieces ahead, copied to shared memory asynchronously; every lane reads back what it copied itself. (Held in registers
+    // they were waited for as soon as they moved up a place.)
+    __shared__ uint4 ahead[4][AP_AHEAD][2][32];
+    uint4(*const mine)[2][32] = ahead[threadIdx.x >> 5];
     const __nv_bfloat16* load_row = a.qkv + (size_t)t0 * a.ld + l * 8;
-    int load_left = t1 - t0, load_piece = part;
-    auto load = [&](uint4 (&to)[2]) {  // the next piece of this warp, if there is one
-        if (load_left <= 0) return;
-        const __nv_bfloat16* x = load_row + min(load_piece * HPW + hl, heads - 1) * DH;
-        to[0] = __ldg(reinterpret_cast<const uint4*>(x));
-        to[1] = __ldg(reinterpret_cast<const uint4*>(x + DH / 2));
-        if ((load_piece += parts) >= pieces) {
-            load_piece = part;
-            load_row += a.ld;
-            --load_left;
+    int load_left = t1 - t0, load_piece = part, load_slot = 0, slot = 0;
+    auto load = [&]() {  // the next piece of this warp, if there is one (a group of copies either way)
+        if (load_left > 0) {
+            const __nv_bfloat16* x = load_row + min(load_piece * HPW + hl, heads - 1) * DH;
+            copy_async16(smem_u32(&mine[load_slot][0][lane]), x);
+            copy_async16(smem_u32(&mine[load_slot][1][lane]), x + DH / 2);
+            if ((load_piece += parts) >= pieces) {
+                load_piece = part;
+                load_row += a.ld;
+                --load_left;
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        load_slot = (load_slot + 1) % AP_AHEAD;
     };
 #pragma unroll
-    for (int i = 0; i < AP_AHEAD; ++i) load(raw[i]);
+    for (int i = 0; i + 1 < AP_AHEAD; ++i) load();
     int seq = -1, seq_end = t0;  // the sequence at hand and the row behind it
     Place pl{-1, -1, 0};
     uint4 ang[2];  // the token's cos and sin
@@ -249,14 +260,11 @@ __global__ void __launch_bounds__(128, AP_CTAS)
             const int h = piece * HPW + hl, hh = min(h, heads - 1);
             const bool on = h < heads;
             float2 x[4], y[4];
-            floats(raw[0][0], x);
-            floats(raw[0][1], y);
-#pragma unroll
-            for (int i = 0; i + 1 < AP_AHEAD; ++i) {
-                raw[i][0] = raw[i + 1][0];
-                raw[i][1] = raw[i + 1][1];
-            }
-            load(raw[AP_AHEAD - 1]);
+            load();  // (into the slot that the piece before has left)
+            asm volatile("cp.async.wait_group %0;" ::"n"(AP_AHEAD - 1) : "memory");
+            floats(mine[slot][0][lane], x);
+            floats(mine[slot][1][lane], y);
+            slot = (slot + 1) % AP_AHEAD;
             if (!rotates) continue;
             const int is = hh < a.Hq ? 0 : hh < a.Hq + a.Hkv ? 1 : 2;
             if (piece * HPW < a.Hq + a.Hkv) {  // (the same for the whole warp, as is what follows but for the heads' kinds)
@@ -347,7 +355,7 @@ template <int DH>
 __global__ void __launch_bounds__(256)
     read_paged4_kernel(const ReadArgs a) {
     constexpr int LPR = DH / 8, RPW = 32 / LPR;  // lanes a row, rows a warp at once
-    const int lane = threadIdx.x & 31, t = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+    const int lane = threadIdx.x & 31, t = (int)(blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5));
     pdl_wait();
     pdl_trigger();
     Place pl;

@@ -208,6 +208,26 @@ def test_plan_flags_bad_bounds(bd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("longest", FORMS)
+def test_plan_of_other_rows(bd, longest):
+    """A plan for more rows than the call has, and one that was never made: rows that the call has not are not written."""
+    heads, lens = (4, 2, 64), [40, 50, 30]
+    q, k, v = (t.cuda() for t in _inputs(heads, lens, lens, 5))
+    plan, _ = _plan(bd, _cu(lens), _cu(lens), 120, 120, 3)
+    whole = torch.full((120, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    bd.op_attention_prefill_packed(q, k, v, plan, longest, whole)
+    out = torch.full((120, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    bd.op_attention_prefill_packed(q[:60], k, v, plan, longest, out[:60])
+    torch.cuda.synchronize()
+    assert torch.equal(out[:60], whole[:60]) and torch.all(out[60:] == 7.0)
+    for fill in (0, 127, 255):
+        plan.fill_(fill)
+        bd.op_attention_prefill_packed(q[:60], k, v, plan, longest, out[:60])
+        torch.cuda.synchronize()
+        assert torch.all(out[60:] == 7.0)
+
+
+@pytest.mark.gpu
 def test_no_rows_and_no_keys(bd):
     q = torch.randn(3, 4, 64).to(torch.bfloat16).cuda()
     none = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")

@@ -527,6 +527,41 @@ def test_decode_repeats_streams_and_graph(bd):
     assert torch.equal(outs[0], want)
 
 
+@pytest.mark.gpu
+def test_pool_past_32_bits(bd):
+    """A pool of 4.4 GB a tensor whose last pages are in use: appended, read back and attended to."""
+    heads, page = (16, 8, 128), 256
+    n_pages, size = 30000, 256 * 72
+    k = torch.empty(n_pages, 8, size, dtype=torch.uint8, device="cuda")
+    v = torch.empty_like(k)
+    assert k.numel() > 2 ** 32
+    lens, start = [300, 1], [0, 40]
+    small = Cache(8, 128, page, [300, 41], 3)
+    _append(bd, heads, page, [300, 41], [0, 0], seed=4, cache=small)
+    far = small.table.copy()
+    used = np.unique(far[far < 2 ** 30])
+    for i, p in enumerate(used):
+        far[small.table == p] = n_pages - 1 - i
+        k[n_pages - 1 - i] = small.k[p]
+        v[n_pages - 1 - i] = small.v[p]
+    big = Cache(8, 128, page, [1, 1], 3)
+    big.k, big.v, big.table, big.dtable = k, v, far, torch.from_numpy(far).cuda()
+    qkv = torch.randn(301, 32 * 128, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    cs = _table(128, 300).cuda()
+    res = []
+    for c in (small, big):
+        q, kr = torch.zeros(301, 16, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(301, 8, 128, dtype=torch.bfloat16, device="cuda")
+        vr, err = torch.zeros_like(kr), torch.zeros(1, dtype=torch.int32, device="cuda")
+        cu, st = _cu(lens), torch.tensor(start, dtype=torch.int32, device="cuda")
+        bd.op_append_paged4(qkv, cu, st, cs, c.k, c.v, c.dtable, q, err=err)
+        bd.op_read_paged4(c.k, c.v, c.dtable, cu, st, kr, vr, err=err)
+        out, e = _decode(bd, q[-2:].contiguous(), c, torch.tensor([299, 40], dtype=torch.int32, device="cuda"))
+        assert e == 0 and int(err.item()) == 0
+        res.append((q, kr, vr, out))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+    assert torch.isfinite(res[0][3].float()).all() and torch.any(res[0][1] != 0)
+
+
 # ------------------------------------------------------------------------------------------------------------ refusals
 
 def test_page_bytes(bd):
