@@ -102,19 +102,27 @@ __device__ __forceinline__ int p4_keys(const P4Args& a, int b) {
     return n < 0 ? 0 : n >= a.cap ? a.cap : n + 1;
 }
 
-// A place in the list of units: unit u of n of (sequence b, kv head h).
+__device__ __forceinline__ int p4_units(int keys) { return (keys + P4_STEP - 1) / P4_STEP; }
+// n / d for a quotient below 2^21
+__device__ __forceinline__ int p4_div(int n, int d) {
+    int q = (int)((float)n * rcp_approx((float)d));
+    const int r = n - q * d;
+    return r < 0 ? q - 1 : r >= d ? q + 1 : q;
+}
+
+// A place in the list of units (of 64 keys): unit u of n of (sequence b, kv head h).
 struct P4Cursor {
     int b, h, u, n, keys;
 };
-// To the next (sequence, kv head); there is one. ulog: log2 of a unit's keys.
-__device__ __forceinline__ void p4_next(const P4Args& a, P4Cursor& c, int ulog) {
+// To the next (sequence, kv head); there is one.
+__device__ __forceinline__ void p4_next(const P4Args& a, P4Cursor& c) {
     c.u = 0;
     if (++c.h < a.Hkv) return;
     c.h = 0;
     do {  // (sequences without keys have no units)
         c.keys = p4_keys(a, ++c.b);
     } while (c.keys == 0);
-    c.n = (c.keys + (1 << ulog) - 1) >> ulog;
+    c.n = p4_units(c.keys);
 }
 
 // BT: 16-key tiles of a page that a step takes (1, 2: pages of 16 and 32 tokens, fetched whole; 4: a part of a larger page).
@@ -133,7 +141,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     __shared__ uint64_t bars[P4_WARPS][NS];
     __shared__ int strip_end[P4_STRIPS];   // units of one kv head up to the strip's end
     __shared__ int strip_keys[P4_STRIPS];  // keys of the strip's (last) sequence
-    __shared__ int2 warp_sum[P4_WARPS];
+    __shared__ int warp_sum[P4_WARPS];
     __shared__ int seg_sh[P4_WARPS], whole_sh[P4_WARPS];
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
@@ -148,42 +156,28 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     pdl_wait();
     pdl_trigger();
 
-    // ---------------- this warp's run of units [x0, x0 + mine): units of 64 keys, or of 32 where there are few of them
+    // ---------------- this warp's run of units [x0, x0 + mine)
     const int per = (a.B + P4_STRIPS - 1) / P4_STRIPS, places = (int)gridDim.x * P4_WARPS;
-    int ulog;
     {
-        int n32 = 0, n64 = 0, keys = 0;
+        int sum = 0, keys = 0;
         const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
         for (int b = b0; b < b1; ++b) {
             keys = p4_keys(a, b);
-            n32 += (keys + 31) >> 5;
-            n64 += (keys + 63) >> 6;
+            sum += p4_units(keys);
             if (keys == 0 && b % gridDim.x == blockIdx.x)  // a sequence without keys
                 for (int e = 0; e < a.Hq * DH / 8; ++e)
                     reinterpret_cast<uint4*>(a.out + (size_t)b * a.Hq * DH)[e] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, n32, o), w = __shfl_up_sync(0xffffffffu, n64, o);
-            if (lane >= o) {
-                n32 += v;
-                n64 += w;
-            }
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
         }
-        if (lane == 31) warp_sum[warp] = make_int2(n32, n64);
+        if (lane == 31) warp_sum[warp] = sum;
         __syncthreads();
-        int all = 0;
 #pragma unroll
-        for (int w = 0; w < P4_WARPS; ++w) {
-            const int2 v = warp_sum[w];
-            all += v.x;
-            if (w < warp) {
-                n32 += v.x;
-                n64 += v.y;
-            }
-        }
-        ulog = all <= 2 * places / a.Hkv ? 5 : 6;
-        strip_end[threadIdx.x] = ulog == 5 ? n32 : n64;
+        for (int w = 0; w < P4_WARPS; ++w) sum += w < warp ? warp_sum[w] : 0;
+        strip_end[threadIdx.x] = sum;
         strip_keys[threadIdx.x] = keys;
         __syncthreads();
     }
@@ -191,32 +185,30 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     const int gw = blockIdx.x * P4_WARPS + warp;
     // as many warps as there are places, but a unit a warp at least (no run between two others is empty); the first `more`
     // runs are a unit longer
-    const int warps = min(places, units), len = warps ? units / warps : 0, more = units - len * warps;
+    const int warps = min(places, units), len = units > places ? p4_div(units, places) : min(units, 1);
+    const int more = units - len * warps;
     const int x0 = gw * len + min(gw, more), mine = gw < warps ? len + (gw < more ? 1 : 0) : 0;
 
     P4Cursor use{0, 0, 0, 1, 1};
     bool inside = true;  // the current (sequence, kv head) begins in this run
     if (mine > 0) {
-        // the strip, then the sequence, that holds unit x0: sequence b's units are [Hkv P_b, Hkv P_(b+1))
-        const int y0 = x0 / a.Hkv;  // (P_b <= y0 < P_(b+1))
-        int lo = 0, hi = P4_STRIPS - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (strip_end[mid] > y0) hi = mid;
-            else lo = mid + 1;
-        }
-        int p = lo > 0 ? strip_end[lo - 1] : 0;
-        use.b = lo * per;
-        use.keys = strip_keys[lo];
+        // the strip that holds unit x0, by its sixth and then within it; then the sequence, whose units are [Hkv P_b, Hkv P_(b+1))
+        static_assert(P4_STRIPS == 32 * P4_WARPS, "strips");
+        const int coarse = __popc(__ballot_sync(0xffffffffu, strip_end[lane * P4_WARPS + P4_WARPS - 1] * a.Hkv <= x0));
+        const int strip = coarse * P4_WARPS +
+                          __popc(__ballot_sync(0xffffffffu, lane < P4_WARPS && strip_end[min(coarse * P4_WARPS + lane, P4_STRIPS - 1)] * a.Hkv <= x0));
+        int p = strip > 0 ? strip_end[strip - 1] : 0;
+        use.b = strip * per;
+        use.keys = strip_keys[strip];
         while (true) {
             if (per > 1) use.keys = p4_keys(a, use.b);
-            use.n = (use.keys + (1 << ulog) - 1) >> ulog;
-            if (per == 1 || p + use.n > y0) break;
+            use.n = p4_units(use.keys);
+            if (per == 1 || (p + use.n) * a.Hkv > x0) break;
             p += use.n;
             ++use.b;
         }
         const int in = x0 - p * a.Hkv;
-        use.h = in / use.n;
+        use.h = p4_div(in, use.n);
         use.u = in - use.h * use.n;
         inside = use.u == 0;
     }
@@ -238,7 +230,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     bool bad_page = false;
     auto issue = [&](int slot) {  // the next unit, if the run has one
         if (ask_left == 0) return;
-        const int k0 = ask.u << ulog, tiles = (min(1 << ulog, ask.keys - k0) + 15) >> 4;
+        const int k0 = ask.u * P4_STEP, tiles = (min(P4_STEP, ask.keys - k0) + 15) >> 4;
         const bool side = BT == 4 && (lane & 1);
         // (of several pages those that the sequence reaches)
         const bool copies = lane < 2 * COPY && (BT == 4 || (lane & (COPY - 1)) * BT < tiles);
@@ -259,10 +251,10 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             if constexpr (BT == 4) {
                 const int row = k0 & ((1 << page_log) - 1);
                 from += side ? (DH / 2 << page_log) + row * (NG * 4) : row * (DH / 2);
-                same_page = min((1 << page_log) - row, ask.keys - k0) - 1 >> ulog;
+                same_page = (min((1 << page_log) - row, ask.keys - k0) - 1) / P4_STEP;
             }
         } else {
-            from += (side ? NG * 4 : DH / 2) << ulog;
+            from += (side ? NG * 4 : DH / 2) * P4_STEP;
         }
         const int pages = BT == 4 ? 0 : (tiles + BT - 1) / BT;
         if (lane == 0) mbar_expect_tx(&full[slot], 2 * (TILE + SIDE) * (BT == 4 ? tiles : pages * BT));
@@ -271,7 +263,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             bulk_load(to + slot * Ly::SLOT, from, BT == 4 ? tiles * (side ? SIDE : TILE) : BT * (TILE + SIDE), &full[slot]);
         ++issued;
         if (--ask_left > 0 && ++ask.u == ask.n) {
-            p4_next(a, ask, ulog);
+            p4_next(a, ask);
             same_page = 0;
         }
     };
@@ -444,7 +436,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         if (part == k) part_side = side_at(k) - side_at(0);
     bool ok = true, fresh = true;
     int slot = 0, phase = 0, run_left = mine;
-    int keys_left = use.keys - (use.u << ulog);  // of the (sequence, kv head), from the unit at hand on
+    int keys_left = use.keys - use.u * P4_STEP;  // of the (sequence, kv head), from the unit at hand on
     if (mine > 0) fetch_q();
     __syncwarp();  // the barriers are set
 #pragma unroll 1
@@ -456,7 +448,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         if (!__all_sync(0xffffffffu, mbar_wait_suspend(&full[slot], phase, abort_flag))) { ok = false; break; }
         uint8_t* ka = p4_rings + warp * Ly::RING + slot * Ly::SLOT;
         uint8_t* va = ka + Ly::HALF;
-        const int valid = min(keys_left, 1 << ulog);  // keys of the unit
+        const int valid = keys_left;  // keys of the unit; 64 or more: all
         if (valid < P4_STEP) {
             // what stands behind the last key may be anything: its scales and minima become 0 (0 * NaN must not reach O)
             for (int e = lane; e < (P4_STEP - valid) * NG; e += 32) {
@@ -639,7 +631,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             slot = 0;
             phase ^= 1;
         }
-        keys_left -= 1 << ulog;
+        keys_left -= P4_STEP;
         fresh = keys_left <= 0;
         if (--run_left > 0 && !fresh) continue;
         // the (sequence, kv head) or the run ends: written out if all of it was in this run, left as a piece otherwise (that at the
@@ -649,7 +641,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         else leave(run_left == 0 ? my_smem : a.recs + (size_t)gw * 2 * a.G * PITCH);
         if (run_left == 0) break;
         inside = true;
-        p4_next(a, use, ulog);
+        p4_next(a, use);
         keys_left = use.keys;
         fetch_q();
     }
@@ -673,9 +665,10 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     // Join the pieces at the ends of this CTA's runs: those of neighbouring warps that belong to one (sequence, kv head), and, where
     // it ends as the first piece of the next warp's run, that warp's record. Quads of dims of the group that begins at warp w0:
     const int G = a.G, quads = G * (DH / 4);
+    constexpr int STEP = Ly::RING / 4;  // floats from one warp's piece to the next
     const int cta0 = blockIdx.x * P4_WARPS, here = max(0, min(P4_WARPS, warps - cta0));  // warps with a run
     for (int e0 = threadIdx.x; e0 < P4_WARPS * quads; e0 += P4_THREADS) {
-        const int w0 = e0 / quads, e = e0 - w0 * quads, s = seg_sh[w0];
+        const int w0 = p4_div(e0, quads), e = e0 - w0 * quads, s = seg_sh[w0];
         if (s < 0 || (w0 > 0 && seg_sh[w0 - 1] == s)) continue;
         int w1 = w0 + 1;
         while (w1 < P4_WARPS && seg_sh[w1] == s) ++w1;
@@ -684,25 +677,30 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
         const float* rec = reinterpret_cast<const float*>(p4_rings) + h * PITCH;
         const float* far = a.recs + (size_t)(cta0 + w1) * 2 * G * PITCH + h * PITCH;
-        constexpr int STEP = Ly::RING / 4;
-        float M = -INFINITY, L = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float m, float l, const float4& y) {
-            const float f = ex2_approx(m - M);
-            L = fmaf(l, f, L);
-            v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
-        };
-        float2 ml = make_float2(-INFINITY, 0.f);
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (tail && whole) {
-            ml = __ldcg(reinterpret_cast<const float2*>(far + DH));
-            y = __ldcg(reinterpret_cast<const float4*>(far + dd));
+        float2 ml[P4_WARPS + 1];
+        float4 y[P4_WARPS + 1];
+#pragma unroll
+        for (int w = 0; w < P4_WARPS; ++w) {
+            const bool in = w >= w0 && w < w1;
+            ml[w] = in ? *reinterpret_cast<const float2*>(rec + w * STEP + DH) : make_float2(-INFINITY, 0.f);
+            y[w] = in ? *reinterpret_cast<const float4*>(rec + w * STEP + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        for (int w = w0; w < w1; ++w) M = fmaxf(M, rec[w * STEP + DH]);
-        M = fmaxf(M, ml.x);  // (finite: a group has a piece)
-        for (int w = w0; w < w1; ++w)
-            add(rec[w * STEP + DH], rec[w * STEP + DH + 1], *reinterpret_cast<const float4*>(rec + w * STEP + dd));
-        add(ml.x, ml.y, y);
+        ml[P4_WARPS] = make_float2(-INFINITY, 0.f);
+        y[P4_WARPS] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (tail && whole) {
+            ml[P4_WARPS] = __ldcg(reinterpret_cast<const float2*>(far + DH));
+            y[P4_WARPS] = __ldcg(reinterpret_cast<const float4*>(far + dd));
+        }
+        float M = ml[0].x, L = 0.f;
+#pragma unroll
+        for (int w = 1; w <= P4_WARPS; ++w) M = fmaxf(M, ml[w].x);  // (finite: a group has a piece)
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w <= P4_WARPS; ++w) {
+            const float f = ex2_approx(ml[w].x - M);
+            L = fmaf(ml[w].y, f, L);
+            v = make_float4(fmaf(y[w].x, f, v.x), fmaf(y[w].y, f, v.y), fmaf(y[w].z, f, v.z), fmaf(y[w].w, f, v.w));
+        }
         if (whole) {
             const float inv = 1.f / L;
             const size_t row = (size_t)(s / a.Hkv) * a.Hq + (size_t)(s % a.Hkv) * G + h;
@@ -723,7 +721,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             while (w0 > 0 && seg_sh[w0 - 1] == s) --w0;
             if (whole_sh[w0] & 1) {
                 // the unit behind it, the warp whose run holds the one before, and whether that run goes on
-                const int end = x0 + mine + ((max(keys_left, 0) + (1 << ulog) - 1) >> ulog), longer = more * (len + 1);
+                const int end = x0 + mine + p4_units(max(keys_left, 0)), longer = more * (len + 1);
                 d.seg = s;
                 d.first = cta0 + w0;
                 d.last = end <= longer ? (end - 1) / (len + 1) : more + (end - 1 - longer) / len;
