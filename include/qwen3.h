@@ -402,13 +402,14 @@ QWEN3_API int qwen3_op_attention_decode_sinks(const void* d_q, const void* d_k_c
  * 64, 128 or 256) of each kv head. A page of one head holds the tokens' codes [page_size, dh / 2] (two a byte, the lower
  * nibble first), then [page_size, dh / 64] pairs of bf16 (scale, minimum), one for each 64 dims of a token:
  * value = minimum + scale * code. d_page_table [sequences, max_pages] int32: entry i of a sequence is the page of its slots
- * i * page_size ..; entries that a call does not need are not read. 4.5 bits a value: 144 bytes a token and kv head at
- * dh 128, K and V together. dh is 64 or 128.
- * Packed batch: N rows, of which [cu[s], cu[s + 1]) belong to sequence s, s < S (d_cu [S + 1] int32, ascending); rows from
- * cu[S] on belong to none and their outputs are left as they were. Row cu[s] + i takes slot d_start[s] + i of its
+ * i * page_size ..; what stands in entries that a call does not need is of no account. 4.5 bits a value: 144 bytes a token
+ * and kv head at dh 128, K and V together. dh is 64 or 128.
+ * Packed batch: N rows, of which [cu[s], cu[s + 1]) belong to sequence s, s < S (d_cu [S + 1] int32, ascending); rows before
+ * cu[0] and from cu[S] on belong to none and their outputs are left as they were. Row cu[s] + i takes slot d_start[s] + i of its
  * sequence, which is also its position. A decode step is the batch of one row a sequence.
- * A page id outside [0, n_pages), a slot that is negative or that the table does not reach, a position outside the rotation
- * table and bounds that are not ascending set bit 4 in *d_err (device int, may be NULL). */
+ * A page id outside [0, n_pages), a slot that is negative or that the table does not reach and a position outside the rotation
+ * table set bit 4 in *d_err (device int, may be NULL). Append and read do not look for bounds that descend: which of the
+ * sequences a row then belongs to is not defined (no access leaves the tensors). */
 QWEN3_API size_t qwen3_paged4_page_bytes(int page_size, int dh);
 
 /* Append to the paged cache: RMSNorm of each query and key head over head_dim (d_q_gamma / d_k_gamma [dh] bf16; NULL: no norm),
@@ -419,8 +420,8 @@ QWEN3_API size_t qwen3_paged4_page_bytes(int page_size, int dh);
  * once at the end. For each 64 dims: minimum = the least value rounded down to bf16, scale = (largest - minimum) / 15 rounded up
  * to bf16, code = the nearest of 0..15 (even on ties), all from the unrounded fp32 values: a cached value is off by half a
  * scale at most. 64 dims that hold a NaN or an infinity become NaN.
- * A row without a page (bit 4) still gets its outputs; one without a position gets none. Two rows must not share a
- * slot, nor any written page hold two sequences' slots. d_k_out may not overlap d_qkv. All tensors 16-byte aligned. */
+ * A row without a page (bit 4) still gets its outputs; one without a position gets none. Two rows of a call must not go to
+ * the same place of the same page. d_q_out and d_k_out may not overlap d_qkv. All tensors 16-byte aligned. */
 QWEN3_API int qwen3_op_append_paged4(const void* d_qkv, int64_t ld, int N, const int* d_cu, const int* d_start, int S, int Hq,
                                      int Hkv, int dh, const void* d_q_gamma, const void* d_k_gamma, float eps,
                                      const void* d_cos_sin, int n_pos, void* d_q_out, void* d_k_out, void* d_k_pages,
@@ -438,12 +439,12 @@ QWEN3_API int qwen3_op_read_paged4(const void* d_k_pages, const void* d_v_pages,
  * 0 .. d_len0[b] of sequence b (the query's own slot, appended before), each sequence at its own length, kv head
  * h / (Hq/Hkv). A negative length gives zeros, one past the page table's reach counts as the last slot. q [B, Hq, dh], out
  * [B, Hq*dh] bf16; Hq / Hkv at most 8, B at most 65535; the table's reach at most 2^30 slots, and B * Hkv times its
- * 32-slot units below 2^31. Slots behind a length may hold anything. d_work: qwen3_attention_decode_paged4_workspace() bytes (of the current
- * device; work_bytes is its size, a smaller one is refused), 16-byte aligned, any contents on entry; calls that share one must
- * not overlap on the GPU. Scores, sums and softmax statistics are fp32; the cached codes are used as they are, and
- * probabilities times scales are rounded to bf16 for the product with the codes. |q| up to 2^90, and values as for
- * qwen3_op_attention_decode_shared. A page id out of range (bit 4) makes the sequence's output invalid; bit 2 as for the other
- * attention operators. The result does not depend on timing. */
+ * 64-slot units below 2^31. Slots behind a length may hold anything. d_work: qwen3_attention_decode_paged4_workspace()
+ * bytes (of the current device; work_bytes is its size, a smaller one is refused), 16-byte aligned, any contents on entry;
+ * calls that share one must not overlap on the GPU. Scores, sums and softmax statistics are fp32; the cached codes are used as
+ * they are, and probabilities times scales are rounded to fp16 (with a power of two for each head) for the product with the
+ * codes. |q| up to 2^90; the visible keys times the largest |v| must stay below 2^50. A page id out of range (bit 4) makes the
+ * sequence's output invalid; bit 2 as for the other attention operators. The result does not depend on timing. */
 QWEN3_API size_t qwen3_attention_decode_paged4_workspace(int B, int Hq, int Hkv, int dh);
 QWEN3_API int qwen3_op_attention_decode_paged4(const void* d_q, const void* d_k_pages, const void* d_v_pages, int n_pages,
                                                int page_size, const int* d_page_table, int max_pages, const int* d_len0, int B,
@@ -457,12 +458,13 @@ QWEN3_API int qwen3_op_attention_decode_paged4(const void* d_q, const void* d_k_
  * values can be read from packed qkv rows in place; tensors are 16-byte aligned.
  * The plan is the work list of a batch, made once for all layers: qwen3_op_attention_packed_plan writes
  * qwen3_attention_packed_plan_bytes(Nq, S) bytes (16-byte aligned) on the stream; a sequence whose bounds descend or
- * leave Nq and Nk, or whose query rows begin before an earlier bound, is left out (bit 4), its output rows untouched. The attention call takes a plan made for its Nq and Nk
- * (plan_bytes as for the plan); calls may share one. `longest`, the keys of the longest sequence, only picks between
- * equivalent forms of the kernel: any value gives a right result.
+ * leave Nq and Nk, or whose query rows begin before an earlier bound, is left out (bit 4), its output rows untouched. The
+ * attention call takes a plan made for its Nq and Nk (plan_bytes as for the plan); calls may share one. `longest`, the keys
+ * of the longest sequence, only picks between equivalent forms of the kernel: any value gives a right result.
  * Scores, sums and softmax statistics are fp32, probabilities are rounded to bf16 for the product with V. Value rows that some
  * query of a 128-row tile sees must be finite; nothing stored in another sequence's rows, or behind the tile's last visible
- * key, reaches a result. Nq, Nk and S at most 2^30, and plan entries times Hq below 2^31 - 2^16. */
+ * key, reaches a result. The visible keys times the largest |v| must stay below 2^119; Nq, Nk and S are at most 2^30, and plan
+ * entries times Hq below 2^31 - 2^16. */
 QWEN3_API size_t qwen3_attention_packed_plan_bytes(int Nq, int S);
 QWEN3_API int qwen3_op_attention_packed_plan(const int* d_cu_q, const int* d_cu_k, int S, int Nq, int Nk, void* d_plan,
                                              size_t plan_bytes, int* d_err, void* stream);

@@ -15,7 +15,7 @@ constexpr int PK_BM = 128, PK_BN = 128;
 // The work list of a packed batch: for every 128-row query tile (first query row, rows, the sequence's first key row, key
 // position of the first query row), the longest key ranges first (a counting sort by key tiles, those past kPlanBins - 1
 // together). One CTA, a warp a sequence. The order of equal tiles depends on timing; it decides which SM
-// computes a tile, not its result. 16 sequences of 300 tokens over 4,096 keys each: 6 us, once for all layers.
+// computes a tile, not its result. PLANUS, once for all layers.
 constexpr int kPlanThreads = 1024, kPlanBins = 1024, kPlanHeader = 256;
 __global__ void __launch_bounds__(kPlanThreads)
     attn_packed_plan_kernel(const int* __restrict__ cu_q, const int* __restrict__ cu_k, int S, int Nq, int Nk, int* count,
@@ -93,13 +93,18 @@ __global__ void __launch_bounds__(kPlanThreads)
 // Persistent: CTA c of G takes items c, 2G-1-c, 2G+c, ... of the list, which has the longest key ranges first. Tiles are counted
 // across items, so rings, score regions and barrier phases simply continue.
 //
-// Warps: 0 Q and K (TMA), 1 score MMAs, 2 V (TMA), 3 P V MMAs, 4-7 softmax (thread <-> query row), 8-11 output. Tensor memory: two
-// score regions of 128 columns (P, bf16, takes the first half of its scores) and two output accumulators, items
-// taking turns: while warps 8-11 read one item's output out, the next item's products and softmax go on. With one accumulator that the
-// softmax warps read out themselves (and three score regions) short prompts stood still at every item's end: 64 prompts
-// of 512 tokens, 32 heads, 315 us.
+// Warps: 0 Q and K (TMA), 1 score MMAs, 2 V (TMA), 3 P V MMAs, 4-7 softmax (thread <-> query row), 8-11 output. Tensor memory: one
+// score region of 128 columns, free again as soon as the softmax has its 128 scores in registers (hence the register
+// split), two regions of 64 for P in bf16, and two output accumulators, items taking turns: while warps 8-11 read
+// one item's output out, the next item's products and softmax go on. With one accumulator that the softmax warps read
+// out themselves (and three score regions) short prompts stood still at every item's end: 64 prompts of 512 tokens, 32
+// heads, 315 us against 260. Two query tiles at once, each with softmax warps and an accumulator of its own, reached
+// 0.57 of the tensor peak on 8,192 tokens: their scores and P share a region, so the products of one wait for its softmax.
 // O is rescaled only when a row's maximum grew by more than 2^8. Rows of another sequence that a tile reaches into are masked
 // (keys), zeroed (values) and not stored (queries).
+// What bounds it: the way of a tile through tensor memory, 128 scores a thread, and back, about 1,500 cycles of 128 query rows by
+// 128 keys, against 1,024 of products. One prompt of 8,192 tokens, 32 / 8 heads of 128: 352 us, 0.82 of the tensor peak
+// (1,562 TFLOP/s of visible pairs); 17,000 tokens in three prompts 533-580 us, with the clock that the power limit leaves.
 constexpr int PK_THREADS = 384;
 constexpr uint32_t PK_REG_PRODUCER = 56, PK_REG_SOFTMAX = 208, PK_REG_OUTPUT = 104;
 static_assert(PK_REG_PRODUCER + PK_REG_SOFTMAX + PK_REG_OUTPUT <= 3 * 168, "register split exceeds the launch");
@@ -178,7 +183,8 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot, tmem_p = tmem + PK_BN, tmem_o = tmem_p + PK_BN;  // P of tile g: tmem_p + (g & 1) * 64, O of item n: tmem_o + (n & 1) * 128
+    // scores; P of tile g at tmem_p + (g & 1) * 64; O of item n at tmem_o + (n & 1) * 128
+    const uint32_t tmem = *tmem_slot, tmem_p = tmem + PK_BN, tmem_o = tmem_p + PK_BN;
     bool ok = true;
     pdl_wait();  // the plan, Q, K and V come from earlier kernels
     pdl_trigger();

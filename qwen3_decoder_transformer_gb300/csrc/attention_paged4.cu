@@ -21,17 +21,26 @@ namespace {
 //   weights p * scale are rounded to fp16, off by 2^-11 of themselves at most: a power of two for each head keeps the largest
 //   weight of the run so far in [2^13, 2^15], so what falls below fp16's normal range is less than 2^-25 of that.
 //   (bf16 weights, with codes as 128 + code and the offset taken off again, left 0.5-1.2% of error on long sequences against
-//   0.2%: a rounding of 2^-8 multiplies codes of one sign, and the tensor cores cut their sums off.)
+//   0.2%: a rounding of 2^-8 multiplies codes of one sign, and the tensor cores cut their sums off. e4m3 operands would halve
+//   the conversions, but the warp-level fp8 product takes several times the fp16 one's cycles on this chip.)
 //
-// Work: the units of 32 keys of all (sequence, kv head) pairs in one list, cut into as many equal runs as there are warps.
-// A warp works through its run alone: its lanes 0 and 1 keep a ring of units full with untiled bulk copies, and warp-level
-// mma (m16n8k16; far below a tcgen05 tile) takes 16 keys by the heads of the group: S^T = K q^T, then O^T += V^T P^T with
-// P^T moved from accumulator to operand layout by movmatrix. The running maximum is rescaled only when it grew by 2^8.
-// A (sequence, kv head) within one run is written out at once. Of one that is cut, each warp leaves a piece (sums,
-// maximum, sum of weights); pieces of one CTA are joined in shared memory, the others in the workspace by
+// Work: the units of 64 keys of all (sequence, kv head) pairs in one list, cut into as many equal runs as there are warps.
+// A warp works through its run alone: its first lanes keep a ring of two units full with untiled bulk copies, and warp-level
+// mma (m16n8k16; the heads of a group are far below a tcgen05 tile) takes 16 keys by the heads: S^T = K q^T, then
+// O^T += V^T P^T with P^T moved from accumulator to operand layout by movmatrix. The sums are rescaled only when a weight grows
+// out of its range. A (sequence, kv head) within one run is written out at once. Of one that is cut, each warp leaves a
+// piece (sums, maximum, sum of weights); pieces of one CTA are joined in shared memory, the others in the workspace by
 // attn_paged4_join_kernel, in the order of their keys: the result does not depend on timing.
+//
+// What bounds it: many keys, HBM (16 sequences of up to 32,768 keys, 32 / 8 heads of 128: 86 us, 6.1 TB/s, of which some 8 us are
+// start and end). In the loop a unit of each of an SM's 12 warps takes 4,000 cycles, 28 bytes a cycle and SM, which is the
+// copy rate, with the issue slots two thirds full. Few keys: the chain of one unit. 1 sequence of 4096: 9.3 us; counting
+// the lengths 0.6, finding the run 0.5, the query 1, one unit 2.1, the pieces 1.4, and the rest two launches and
+// the records' way through the workspace.
+// Split: one CTA of 12 warps an SM, as many rings as shared memory holds, joins the pieces of 12 runs before they leave the SM (16 @
+// 32,768 two CTAs of six 90.3 us, one of twelve 85.7; 64 sequences of up to 4096 keys, 16 / 8 heads, 45.6 and 44.9).
 constexpr int P4_STEP = 64, P4_TILES = P4_STEP / 16;  // keys that a warp takes at once
-constexpr int P4_WARPS = 6, P4_THREADS = 32 * P4_WARPS, P4_CTAS = 2, P4_MAX_G = 8;
+constexpr int P4_WARPS = 12, P4_THREADS = 32 * P4_WARPS, P4_CTAS = 1, P4_MAX_G = 8;
 constexpr int P4_STRIPS = P4_THREADS;  // strips of sequences whose units are counted at the start
 template <int DH>
 struct P4Layout {
@@ -49,7 +58,7 @@ struct P4Layout {
 // A (sequence, kv head) that begins, but does not end, in a CTA's runs: its number (-1: none), the warp whose run holds its
 // beginning, the one whose run holds its end, and whether the end's record is that run's first piece (0) or the last (1).
 struct P4Desc {
-    int seg, first, last, last_slot;
+    int seg, first, last, last_slot, team;  // team: warps of a CTA that worked
 };
 
 struct P4Args {
@@ -128,14 +137,17 @@ __device__ __forceinline__ void p4_next(const P4Args& a, P4Cursor& c) {
 // BT: 16-key tiles of a page that a step takes (1, 2: pages of 16 and 32 tokens, fetched whole; 4: a part of a larger page).
 // HC: columns of a product that the heads of a group take (the least power of two that holds them, 2 at least). With fewer than 8
 // the columns hold the heads 8 / HC times, and of the scores of 8 / HC tiles each tile keeps its own columns: no lane
-// works on the softmax of a column without a head, and O's column sets are added at the end.
+// works on the softmax of a column without a head, and O's column sets are added at the end. Against all heads in 8
+// columns: groups of two 45.6 us against 61.8 (64 @ 4096; in 4 columns 46.9), groups of four 90 against 130 (16 @ 32,768).
+// Groups of five to eight take a step's scores in two halves (all at once they left the registers).
 template <int DH, int BT, int HC>
 __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     attn_paged4_kernel(const P4Args a) {
     using Ly = P4Layout<DH>;
     constexpr int NG = Ly::NG, NS = Ly::NS, PITCH = Ly::PITCH;
     constexpr int SHARE = 8 / HC;            // tiles whose scores share the columns
-    constexpr int SETS = P4_TILES / SHARE;   // sets of scores of a step: two rows by two columns a lane
+    constexpr int SUBS = HC == 8 ? 2 : 1, SUB = P4_TILES / SUBS;  // parts of a step, and tiles, whose scores are held at once
+    constexpr int SETS = SUB / SHARE;        // sets of scores of a step: two rows by two columns a lane
     constexpr int LANES = HC / 2;            // lanes t that hold the columns of one tile
     extern __shared__ __align__(128) uint8_t p4_rings[];
     __shared__ uint64_t bars[P4_WARPS][NS];
@@ -181,8 +193,13 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         strip_keys[threadIdx.x] = keys;
         __syncthreads();
     }
-    const int units = strip_end[P4_STRIPS - 1] * a.Hkv;  // (fewer than 2^31: checked on the host)
-    const int gw = blockIdx.x * P4_WARPS + warp;
+    auto all_units = [&]() { return strip_end[P4_STRIPS - 1] * a.Hkv; };  // (fewer than 2^31: checked on the host)
+    // warps of a CTA that work: few units are spread over the SMs (1 sequence of 4096 keys, 8 kv heads: 9.3 us, with full CTAs
+    // 10.0), but not further than a warp a scheduler: every CTA that shares a kv head leaves a record for the join (2 kv
+    // heads, a warp a CTA 15.5 us, four 10.3)
+    auto team_of = [&](int units) { return max(4, min(P4_WARPS, p4_div(min(units, places) + (int)gridDim.x - 1, (int)gridDim.x))); };
+    const int units = all_units();
+    const int gw = warp < team_of(units) ? blockIdx.x * team_of(units) + warp : places;
     // as many warps as there are places, but a unit a warp at least (no run between two others is empty); the first `more`
     // runs are a unit longer
     const int warps = min(places, units), len = units > places ? p4_div(units, places) : min(units, 1);
@@ -192,11 +209,11 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     P4Cursor use{0, 0, 0, 1, 1};
     bool inside = true;  // the current (sequence, kv head) begins in this run
     if (mine > 0) {
-        // the strip that holds unit x0, by its sixth and then within it; then the sequence, whose units are [Hkv P_b, Hkv P_(b+1))
+        // the strip that holds unit x0, by its twelfth and then within it; then the sequence, whose units are [Hkv P_b, Hkv P_(b+1))
         static_assert(P4_STRIPS == 32 * P4_WARPS, "strips");
         const int coarse = __popc(__ballot_sync(0xffffffffu, strip_end[lane * P4_WARPS + P4_WARPS - 1] * a.Hkv <= x0));
-        const int strip = coarse * P4_WARPS +
-                          __popc(__ballot_sync(0xffffffffu, lane < P4_WARPS && strip_end[min(coarse * P4_WARPS + lane, P4_STRIPS - 1)] * a.Hkv <= x0));
+        const int fine = strip_end[min(coarse * P4_WARPS + lane, P4_STRIPS - 1)];
+        const int strip = coarse * P4_WARPS + __popc(__ballot_sync(0xffffffffu, lane < P4_WARPS && fine * a.Hkv <= x0));
         int p = strip > 0 ? strip_end[strip - 1] : 0;
         use.b = strip * per;
         use.keys = strip_keys[strip];
@@ -459,169 +476,177 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             fence_proxy_async_smem();  // (the slot's next copy comes after these stores)
             __syncwarp();
         }
-        float2 x[SETS][2];  // scores [set][row g, row g + 8] of heads ch, ch + 1
+#pragma unroll 1
+        for (int sub = 0; sub < SUBS; ++sub) {
+            const int left = valid - sub * SUB * 16;  // keys from this part on
+            if (SUBS > 1 && left <= 0) break;
+            const int codes_at = sub * SUB * (BT == 4 ? TILE : TILE + SIDE), sides_at = sub * SUB * (BT == 4 ? SIDE : TILE + SIDE);
+            const uint8_t *ka_codes = ka + codes_at, *va_codes = va + codes_at;
+            const uint8_t *ka_sides = ka + sides_at, *va_sides = va + sides_at;
+            float2 x[SETS][2];  // scores [set][row g, row g + 8] of heads ch, ch + 1
 #pragma unroll
-        for (int k = 0; k < SETS; ++k) {
-            float acc[SHARE][NG][4];
+            for (int k = 0; k < SETS; ++k) {
+                float acc[SHARE][NG][4];
 #pragma unroll
-            for (int j = 0; j < SHARE; ++j) {
-                const uint8_t* codes = ka + tile_at(k * SHARE + j) + kcode_l;
+                for (int j = 0; j < SHARE; ++j) {
+                    const uint8_t* codes = ka_codes + tile_at(k * SHARE + j) + kcode_l;
 #pragma unroll
-                for (int c = 0; c < NG; ++c) {
-                    const uint2 w0 = *reinterpret_cast<const uint2*>(codes + c * 32);
-                    const uint2 w1 = *reinterpret_cast<const uint2*>(codes + 8 * (DH / 2) + c * 32);
-                    const uint32_t a0[2] = {w0.x, w0.y}, a1[2] = {w1.x, w1.y};
+                    for (int c = 0; c < NG; ++c) {
+                        const uint2 w0 = *reinterpret_cast<const uint2*>(codes + c * 32);
+                        const uint2 w1 = *reinterpret_cast<const uint2*>(codes + 8 * (DH / 2) + c * 32);
+                        const uint32_t a0[2] = {w0.x, w0.y}, a1[2] = {w1.x, w1.y};
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t y0 = a0[w] >> 8, y1 = a1[w] >> 8;
-                        if (w == 0)
-                            mma_f16_first(acc[j][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
-                                          a1[w] & 0x00f000f0u, qf[c][w][0][0], qf[c][w][0][1]);
-                        else
-                            mma_f16(acc[j][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
-                                    a1[w] & 0x00f000f0u, qf[c][w][0][0], qf[c][w][0][1]);
-                        mma_f16(acc[j][c], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
-                                qf[c][w][1][0], qf[c][w][1][1]);
+                        for (int w = 0; w < 2; ++w) {
+                            const uint32_t y0 = a0[w] >> 8, y1 = a1[w] >> 8;
+                            if (w == 0)
+                                mma_f16_first(acc[j][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
+                                              a1[w] & 0x00f000f0u, qf[c][w][0][0], qf[c][w][0][1]);
+                            else
+                                mma_f16(acc[j][c], a0[w] & 0x000f000fu, a1[w] & 0x000f000fu, a0[w] & 0x00f000f0u,
+                                        a1[w] & 0x00f000f0u, qf[c][w][0][0], qf[c][w][0][1]);
+                            mma_f16(acc[j][c], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
+                                    qf[c][w][1][0], qf[c][w][1][1]);
+                        }
+                    }
+                }
+                uint32_t sd[2][NG];
+                sides(ka_sides + side_at(k * SHARE) + part_side + side_l, sd);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < NG; ++c) {
+                        const float sc = bf16_lo(sd[r][c]), lo = bf16_hi(sd[r][c]);
+                        float a0 = acc[0][c][2 * r], a1 = acc[0][c][2 * r + 1];
+#pragma unroll
+                        for (int j = 1; j < SHARE; ++j) {
+                            a0 = part == j ? acc[j][c][2 * r] : a0;
+                            a1 = part == j ? acc[j][c][2 * r + 1] : a1;
+                        }
+                        s0 = fmaf(sc, a0, c == 0 ? lo * qs[c].x : fmaf(lo, qs[c].x, s0));
+                        s1 = fmaf(sc, a1, c == 0 ? lo * qs[c].y : fmaf(lo, qs[c].y, s1));
+                    }
+                    x[k][r] = make_float2(s0, s1);
+                }
+            }
+            if (left < SUB * 16) {
+#pragma unroll
+                for (int k = 0; k < SETS; ++k)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if ((k * SHARE + part) * 16 + swap + 8 * r >= left) x[k][r] = make_float2(-INFINITY, -INFINITY);
+            }
+            // weights p, and p * scale by group of dims
+            float2 p[SETS][2], wt[SETS][NG][2];
+            uint32_t sd[SETS][2][NG];
+#pragma unroll
+            for (int k = 0; k < SETS; ++k) sides(va_sides + side_at(k * SHARE) + part_side + side_l, sd[k]);
+            float2 mx = x[0][0];
+#pragma unroll
+            for (int k = 0; k < SETS; ++k) {
+                mx.x = fmax3(mx.x, x[k][0].x, x[k][1].x);
+                mx.y = fmax3(mx.y, x[k][0].y, x[k][1].y);
+            }
+            float2 was = nm;
+            struct {
+                bool x, y;
+            } up{};
+#pragma unroll 1
+            for (int pass = 0;; ++pass) {
+                float2 top = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < SETS; ++k) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        p[k][r] = make_float2(ex2_approx(fmaf(x[k][r].x, qscale.x, nm.x)), ex2_approx(fmaf(x[k][r].y, qscale.y, nm.y)));
+#pragma unroll
+                        for (int c = 0; c < NG; ++c) {
+                            const float sc = bf16_lo(sd[k][r][c]);
+                            wt[k][c][r] = make_float2(p[k][r].x * sc, p[k][r].y * sc);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < NG; ++c) {
+                        top.x = fmax3(top.x, fabsf(wt[k][c][0].x), fabsf(wt[k][c][1].x));
+                        top.y = fmax3(top.y, fabsf(wt[k][c][0].y), fabsf(wt[k][c][1].y));
+                    }
+                }
+                if (pass == 2) break;
+                if (pass == 0) {
+                    if (!__any_sync(0xffffffffu, mx.x > high.x || mx.y > high.y || top.x > 32768.f || top.y > 32768.f)) break;
+#pragma unroll
+                    for (int s = LANES; s < 32; s <<= 1) {
+                        mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, s));
+                        mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, s));
+                    }
+                    // scores first: p is 1 for the largest
+                    up = {mx.x > high.x, mx.y > high.y};
+                    if (up.x) nm.x = -mx.x * qscale.x;
+                    if (up.y) nm.y = -mx.y * qscale.y;
+                } else {
+                    // then the weights of V: the largest one to [2^13, 2^14), p at most 2^60
+#pragma unroll
+                    for (int s = LANES; s < 32; s <<= 1) {
+                        top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, s));
+                        top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, s));
+                    }
+                    auto suit = [](float top, bool up, float& nm) {
+                        if (up || top > 32768.f) nm += (float)min(140 - (int)(__float_as_uint(top) >> 23), up ? 60 : 0);
+                    };
+                    suit(top.x, up.x, nm.x);
+                    suit(top.y, up.y, nm.y);
+                    // (nothing is there before the first score)
+                    const float2 f = make_float2(high.x == -INFINITY ? 0.f : ex2_approx(nm.x - was.x),
+                                                 high.y == -INFINITY ? 0.f : ex2_approx(nm.y - was.y));
+                    high = make_float2((75.f - nm.x) / qscale.x, (75.f - nm.y) / qscale.y);
+                    l = mul2(l, f);
+#pragma unroll
+                    for (int c = 0; c < NG; ++c) {
+                        z[c] = mul2(z[c], f);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            o[c][q][0] *= f.x;
+                            o[c][q][1] *= f.y;
+                            o[c][q][2] *= f.x;
+                            o[c][q][3] *= f.y;
+                        }
                     }
                 }
             }
-            uint32_t sd[2][NG];
-            sides(ka + side_at(k * SHARE) + part_side + side_l, sd);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                for (int c = 0; c < NG; ++c) {
-                    const float sc = bf16_lo(sd[r][c]), lo = bf16_hi(sd[r][c]);
-                    float a0 = acc[0][c][2 * r], a1 = acc[0][c][2 * r + 1];
-#pragma unroll
-                    for (int j = 1; j < SHARE; ++j) {
-                        a0 = part == j ? acc[j][c][2 * r] : a0;
-                        a1 = part == j ? acc[j][c][2 * r + 1] : a1;
-                    }
-                    s0 = fmaf(sc, a0, c == 0 ? lo * qs[c].x : fmaf(lo, qs[c].x, s0));
-                    s1 = fmaf(sc, a1, c == 0 ? lo * qs[c].y : fmaf(lo, qs[c].y, s1));
-                }
-                x[k][r] = make_float2(s0, s1);
-            }
-        }
-        if (valid < P4_STEP) {
+            uint32_t wb[SETS][NG][2];  // P^T fragments
 #pragma unroll
             for (int k = 0; k < SETS; ++k)
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    if ((k * SHARE + part) * 16 + swap + 8 * r >= valid) x[k][r] = make_float2(-INFINITY, -INFINITY);
-        }
-        // weights p, and p * scale by group of dims
-        float2 p[SETS][2], wt[SETS][NG][2];
-        uint32_t sd[SETS][2][NG];
-#pragma unroll
-        for (int k = 0; k < SETS; ++k) sides(va + side_at(k * SHARE) + part_side + side_l, sd[k]);
-        float2 mx = x[0][0];
-#pragma unroll
-        for (int k = 0; k < SETS; ++k) {
-            mx.x = fmax3(mx.x, x[k][0].x, x[k][1].x);
-            mx.y = fmax3(mx.y, x[k][0].y, x[k][1].y);
-        }
-        float2 was = nm;
-        struct {
-            bool x, y;
-        } up{};
-#pragma unroll 1
-        for (int pass = 0;; ++pass) {
-            float2 top = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < SETS; ++k) {
-#pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    p[k][r] = make_float2(ex2_approx(fmaf(x[k][r].x, qscale.x, nm.x)), ex2_approx(fmaf(x[k][r].y, qscale.y, nm.y)));
+                    l = add2(l, p[k][r]);
 #pragma unroll
                     for (int c = 0; c < NG; ++c) {
-                        const float sc = bf16_lo(sd[k][r][c]);
-                        wt[k][c][r] = make_float2(p[k][r].x * sc, p[k][r].y * sc);
+                        const float lo = bf16_hi(sd[k][r][c]);
+                        z[c] = make_float2(fmaf(p[k][r].x, lo, z[c].x), fmaf(p[k][r].y, lo, z[c].y));
+                        wb[k][c][r] = transpose8x8(pack_f16(wt[k][c][r].x, wt[k][c][r].y));
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < NG; ++c) {
-                    top.x = fmax3(top.x, fabsf(wt[k][c][0].x), fabsf(wt[k][c][1].x));
-                    top.y = fmax3(top.y, fabsf(wt[k][c][0].y), fabsf(wt[k][c][1].y));
-                }
-            }
-            if (pass == 2) break;
-            if (pass == 0) {
-                if (!__any_sync(0xffffffffu, mx.x > high.x || mx.y > high.y || top.x > 32768.f || top.y > 32768.f)) break;
-#pragma unroll
-                for (int s = LANES; s < 32; s <<= 1) {
-                    mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, s));
-                    mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, s));
-                }
-                // scores first: p is 1 for the largest
-                up = {mx.x > high.x, mx.y > high.y};
-                if (up.x) nm.x = -mx.x * qscale.x;
-                if (up.y) nm.y = -mx.y * qscale.y;
-            } else {
-                // then the weights of V: the largest one to [2^13, 2^14), p at most 2^60
-#pragma unroll
-                for (int s = LANES; s < 32; s <<= 1) {
-                    top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, s));
-                    top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, s));
-                }
-                auto suit = [](float top, bool up, float& nm) {
-                    if (up || top > 32768.f) nm += (float)min(140 - (int)(__float_as_uint(top) >> 23), up ? 60 : 0);
-                };
-                suit(top.x, up.x, nm.x);
-                suit(top.y, up.y, nm.y);
-                // (nothing is there before the first score)
-                const float2 f = make_float2(high.x == -INFINITY ? 0.f : ex2_approx(nm.x - was.x),
-                                             high.y == -INFINITY ? 0.f : ex2_approx(nm.y - was.y));
-                high = make_float2((75.f - nm.x) / qscale.x, (75.f - nm.y) / qscale.y);
-                l = mul2(l, f);
+            for (int k = 0; k < SUB; ++k) {
+                const uint8_t* codes = va_codes + tile_at(k) + vcode_l;
+                const bool mine_k = SHARE == 1 || g / HC == k % SHARE;  // this lane's column of O takes the tile
 #pragma unroll
                 for (int c = 0; c < NG; ++c) {
-                    z[c] = mul2(z[c], f);
+                    const uint32_t b0 = mine_k ? wb[k / SHARE][c][0] : 0u, b1 = mine_k ? wb[k / SHARE][c][1] : 0u;
+                    // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further: the first and the last four nibbles
+                    auto word = [&](int key) { return *reinterpret_cast<const uint32_t*>(codes + c * 32 + key * (DH / 2)); };
+                    const uint32_t wa = word(0), wb2 = word(2), wc = word(8), wd = word(10);
+                    uint32_t v[4] = {__byte_perm(wa, wb2, 0x5410), __byte_perm(wa, wb2, 0x7632), __byte_perm(wc, wd, 0x5410),
+                                     __byte_perm(wc, wd, 0x7632)};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        o[c][q][0] *= f.x;
-                        o[c][q][1] *= f.y;
-                        o[c][q][2] *= f.x;
-                        o[c][q][3] *= f.y;
+                        if (q == 2) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[j] >>= 8;
+                        }
+                        const uint32_t mask = q & 1 ? 0x00f000f0u : 0x000f000fu;
+                        mma_f16(o[c][q], v[0] & mask, v[1] & mask, v[2] & mask, v[3] & mask, b0, b1);
                     }
-                }
-            }
-        }
-        uint32_t wb[SETS][NG][2];  // P^T fragments
-#pragma unroll
-        for (int k = 0; k < SETS; ++k)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                l = add2(l, p[k][r]);
-#pragma unroll
-                for (int c = 0; c < NG; ++c) {
-                    const float lo = bf16_hi(sd[k][r][c]);
-                    z[c] = make_float2(fmaf(p[k][r].x, lo, z[c].x), fmaf(p[k][r].y, lo, z[c].y));
-                    wb[k][c][r] = transpose8x8(pack_f16(wt[k][c][r].x, wt[k][c][r].y));
-                }
-            }
-#pragma unroll
-        for (int k = 0; k < P4_TILES; ++k) {
-            const uint8_t* codes = va + tile_at(k) + vcode_l;
-            const bool mine_k = SHARE == 1 || g / HC == k % SHARE;  // this lane's column of O takes the tile
-#pragma unroll
-            for (int c = 0; c < NG; ++c) {
-                const uint32_t b0 = mine_k ? wb[k / SHARE][c][0] : 0u, b1 = mine_k ? wb[k / SHARE][c][1] : 0u;
-                // rows 2t, 2t + 1 (keys vkey and vkey + 2), and eight further: the first and the last four nibbles
-                auto word = [&](int key) { return *reinterpret_cast<const uint32_t*>(codes + c * 32 + key * (DH / 2)); };
-                const uint32_t wa = word(0), wb2 = word(2), wc = word(8), wd = word(10);
-                uint32_t v[4] = {__byte_perm(wa, wb2, 0x5410), __byte_perm(wa, wb2, 0x7632), __byte_perm(wc, wd, 0x5410),
-                                 __byte_perm(wc, wd, 0x7632)};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q == 2) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] >>= 8;
-                    }
-                    const uint32_t mask = q & 1 ? 0x00f000f0u : 0x000f000fu;
-                    mma_f16(o[c][q], v[0] & mask, v[1] & mask, v[2] & mask, v[3] & mask, b0, b1);
                 }
             }
         }
@@ -666,7 +691,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     // it ends as the first piece of the next warp's run, that warp's record. Quads of dims of the group that begins at warp w0:
     const int G = a.G, quads = G * (DH / 4);
     constexpr int STEP = Ly::RING / 4;  // floats from one warp's piece to the next
-    const int cta0 = blockIdx.x * P4_WARPS, here = max(0, min(P4_WARPS, warps - cta0));  // warps with a run
+    const int team = team_of(all_units());  // (again: not held through the loop)
+    const int cta0 = blockIdx.x * team, here = max(0, min(team, warps - cta0));  // warps with a run
     for (int e0 = threadIdx.x; e0 < P4_WARPS * quads; e0 += P4_THREADS) {
         const int w0 = p4_div(e0, quads), e = e0 - w0 * quads, s = seg_sh[w0];
         if (s < 0 || (w0 > 0 && seg_sh[w0 - 1] == s)) continue;
@@ -713,11 +739,11 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         }
     }
     // the (sequence, kv head) that goes on behind this CTA, if it began here
-    if (warp == P4_WARPS - 1 && lane == 0) {
-        P4Desc d{-1, 0, 0, 0};
-        const int s = seg_sh[P4_WARPS - 1];
-        if (s >= 0 && !(whole_sh[P4_WARPS - 1] & 2)) {
-            int w0 = P4_WARPS - 1;
+    if (warp == team - 1 && lane == 0) {
+        P4Desc d{-1, 0, 0, 0, team};
+        const int s = seg_sh[warp];
+        if (s >= 0 && !(whole_sh[warp] & 2)) {
+            int w0 = warp;
             while (w0 > 0 && seg_sh[w0 - 1] == s) --w0;
             if (whole_sh[w0] & 1) {
                 // the unit behind it, the warp whose run holds the one before, and whether that run goes on
@@ -751,10 +777,10 @@ __global__ void __launch_bounds__(P4_JOIN_THREADS)
     const int e = threadIdx.x % quads, way = threadIdx.x / quads;
     const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
     // CTAs behind the first whose first warp leaves a record in place 1; then, for last_slot 0, the end's own
-    const int c0 = d.first / P4_WARPS + 1, c1 = (d.last + d.last_slot - 1) / P4_WARPS;
+    const int c0 = d.first / d.team + 1, c1 = (d.last + d.last_slot - 1) / d.team;
     const int middle = max(0, c1 - c0 + 1), n = 1 + middle + (d.last_slot == 0 ? 1 : 0);
     auto record = [&](int i) -> const float* {
-        const int w = i == 0 ? d.first : i <= middle ? (c0 + i - 1) * P4_WARPS : d.last;
+        const int w = i == 0 ? d.first : i <= middle ? (c0 + i - 1) * d.team : d.last;
         const int slot = i <= middle ? 1 : 0;
         return a.recs + ((size_t)w * 2 + slot) * G * PITCH + h * PITCH;
     };

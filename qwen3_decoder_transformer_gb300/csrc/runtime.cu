@@ -1211,9 +1211,9 @@ int qwen3_op_attention_decode_paged4(const void* q, const void* k_pages, const v
         !pages_ok(k_pages, v_pages, n_pages, page_size, dh, table, max_pages))
         return QWEN3_E_ARG;
     if (!q || !len0 || !work || !out || !is_aligned(q, 16) || !is_aligned(out, 16) || !is_aligned(work, 16)) return QWEN3_E_ARG;
-    // the kernel counts the units of 32 keys of all (sequence, kv head) pairs in an int
+    // the kernel counts the units of 64 keys of all (sequence, kv head) pairs in an int
     const long long slots = std::min<long long>((long long)max_pages * page_size, kMaxSlots);
-    if ((long long)B * Hkv > 0x7fffffff || (long long)B * Hkv > 0x7fffffff / ((slots + 31) / 32)) return QWEN3_E_ARG;
+    if ((long long)B * Hkv > 0x7fffffff || (long long)B * Hkv > 0x7fffffff / ((slots + 63) / 64)) return QWEN3_E_ARG;
     if (B == 0) return QWEN3_OK;
     if (work_bytes < attn_decode_paged4_workspace(Hq / Hkv, dh)) return QWEN3_E_ARG;
     if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;

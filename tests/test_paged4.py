@@ -5,10 +5,12 @@ Tolerances. A bf16 result is off by half a step, 2^-8 of its value at most.
   Rotated heads: fp32 products and sums of a few terms of the size |a| + |b| of the rotated pair, after a norm whose sum of
   up to 128 squares is off by at most 128 * 2^-24 of itself (half of that in its root): 2^-16 (|a| + |b|) covers both.
   Cached values: a code stands for a value within half a scale of it; the fp32 key that is quantised is off as above.
-  Decode: the reference takes the cache's own bytes, so K and V are exact. Probability times scale is rounded to bf16
-  (2^-8 of itself) before it multiplies codes 0..15; those products carry an offset of 128 that is taken off again, in fp32
-  sums of at most one step for 16 keys, each off by 2^-23 of a sum of up to 143 times the weights. Scores are fp32 sums of
-  a few exact products, off by 2^-20 of their terms, and so is the exponential: 2^-18 (1 + the largest score term) of every weight.
+  Decode: the reference takes the cache's own bytes, so K and V are exact. A weight (probability times scale) is rounded to fp16,
+  2^-11 of itself, and below fp16's normal range by 2^-25 where the head's largest is 2^13 or more: 2^-38 of the largest
+  weight for each key, times codes up to 15. A product of 16 keys adds 17 terms to an fp32 sum, each cut off below 2^-24 of
+  the largest: 2^-20 of the sum's terms a product, and as much for the joins and changes of range. Scores are four such
+  products a group of dims (2^-18 of their terms), a few fp32 operations and an exponential: 2^-17 (1 + the largest score's
+  terms) of every weight.
 """
 import struct
 
@@ -366,10 +368,10 @@ def _ref_decode(q, c, lens, cap=None):
             p = np.exp(x - x.max())
             p /= p.sum()
             ref[b, h] = p @ v[:, j]
-            steps = 2 * -(-n // 32) + 16
-            tol[b, h] = (2.0 ** -8 * np.abs(ref[b, h]) + 2.0 ** -8 * (p @ (sv[:, j] * cv[:, j])) +
-                         steps * 2.0 ** -23 * 143 * (p @ sv[:, j]) +
-                         2.0 ** -18 * (1 + size) * (p @ (np.abs(lv[:, j]) + sv[:, j] * cv[:, j])))
+            w, low = sv[:, j] * cv[:, j], np.abs(lv[:, j])
+            steps = -(-n // 16) + 16
+            tol[b, h] = (2.0 ** -8 * np.abs(ref[b, h]) + 2.0 ** -11 * (p @ w) + n * 15 * 2.0 ** -38 * (p[:, None] * sv[:, j]).max() +
+                         steps * 2.0 ** -20 * (p @ (w + low)) + 2.0 ** -17 * (1 + size) * (p @ (w + low)))
     return ref, tol
 
 
@@ -411,7 +413,9 @@ def test_decode_batches(bd, heads, B_):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("heads,lens,page", [((8, 1, 128), [20011], 64), ((4, 4, 64), [30000, 1], 256),
-                                             ((32, 8, 128), [5000, 3000, 40], 16), ((16, 2, 64), [9999], 32)], ids=str)
+                                             ((32, 8, 128), [5000, 3000, 40], 16), ((16, 2, 64), [9999], 32),
+                                             ((16, 8, 128), [130], 64), ((16, 2, 128), [2500], 128), ((32, 8, 128), [9000], 16),
+                                             ((8, 1, 64), [60000], 32), ((32, 8, 128), [20000, 0, 20000], 64)], ids=str)
 def test_decode_long(bd, heads, lens, page):
     Hq, Hkv, dh = heads
     c = Cache(Hkv, dh, page, lens, page).fill(lens, page)
