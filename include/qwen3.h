@@ -463,8 +463,8 @@ QWEN3_API int qwen3_op_attention_decode_paged4(const void* d_q, const void* d_k_
  * of the longest sequence, only picks between equivalent forms of the kernel: any value gives a right result.
  * Scores, sums and softmax statistics are fp32, probabilities are rounded to bf16 for the product with V. Value rows that some
  * query of a 128-row tile sees must be finite; nothing stored in another sequence's rows, or behind the tile's last visible
- * key, reaches a result. The visible keys times the largest |v| must stay below 2^119; Nq, Nk and S are at most 2^30, and plan
- * entries times Hq below 2^31 - 2^16. */
+ * key, reaches a result. The visible keys times the largest |v| must stay below 2^119; Nq, Nk and S are at most 2^30, and
+ * plan_bytes / 16 times Hq below 2^31 - 2^16. */
 QWEN3_API size_t qwen3_attention_packed_plan_bytes(int Nq, int S);
 QWEN3_API int qwen3_op_attention_packed_plan(const int* d_cu_q, const int* d_cu_k, int S, int Nq, int Nk, void* d_plan,
                                              size_t plan_bytes, int* d_err, void* stream);

@@ -12,22 +12,48 @@ namespace {
 constexpr int PK_BM = 128, PK_BN = 128;
 
 // ------------------------------------------------------------------------------------- packed sequences
-// The work list of a packed batch: for every 128-row query tile (first query row, rows, the sequence's first key row, key
-// position of the first query row), the longest key ranges first (a counting sort by key tiles, those past kPlanBins - 1
-// together). One CTA, a warp a sequence. The order of equal tiles depends on timing; it decides which SM
-// computes a tile, not its result. PLANUS, once for all layers.
-constexpr int kPlanThreads = 1024, kPlanBins = 1024, kPlanHeader = 256;
+// The work lists of a packed batch, one for each size of a query tile: list L has an entry for every 128 >> L query rows of a
+// sequence (first query row, rows, the sequence's first key row, key position of the first query row), the longest key ranges first
+// (a counting sort by key tiles, those past kPlanBins - 1 together). The attention kernel takes the list of its tiles' tokens,
+// 128 / PG (the finest one for larger groups): with one list of 128 rows and up to PG places an entry, places that a
+// sequence's last rows do not fill left CTAs without work (16 turns of 300 tokens over up to 4096 keys: 230 us against 203;
+// 64 prompts of about 512 tokens 278 and 252).
+// One CTA, a warp a sequence (all of them a long one). The order of equal tiles depends on timing; it decides which SM
+// computes a tile, not its result. 16 sequences of 300 queries over 4,096 keys each: 7 us, 64 prompts
+// of 512 tokens 9, 3,000 of five 44, once for all layers.
+constexpr int kPlanThreads = 1024, kPlanBins = 1024, kPlanLevels = 4, kPlanLong = 4096;
+struct PlanHeader {
+    int count[kPlanLevels];        // entries of a list
+    long long first[kPlanLevels];  // where it begins
+};
+constexpr int kPlanHeader = 256;
+static_assert(sizeof(PlanHeader) <= kPlanHeader, "header");
+size_t plan_level(int Nq, int S, int level) {  // entries that list `level` can have
+    const int rows = PK_BM >> level;
+    return (size_t)(Nq + rows - 1) / rows + (size_t)S;
+}
 __global__ void __launch_bounds__(kPlanThreads)
-    attn_packed_plan_kernel(const int* __restrict__ cu_q, const int* __restrict__ cu_k, int S, int Nq, int Nk, int* count,
-                            int4* items, int capacity, int* err) {
-    __shared__ int bins[kPlanBins], warp_sum[kPlanThreads / 32];
+    attn_packed_plan_kernel(const int* __restrict__ cu_q, const int* __restrict__ cu_k, int S, int Nq, int Nk,
+                            const __grid_constant__ PlanHeader at, PlanHeader* header, int4* items, int* err) {
+    __shared__ int bins[kPlanLevels][kPlanBins], bin_sum[kPlanLevels][32], warp_sum[kPlanThreads / 32];
     __shared__ int4 seqs[kPlanThreads];  // first query row, queries (0: left out), first key row, keys in front of the queries
+    __shared__ unsigned longs[kPlanThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // a warp's lanes share the lists of a sequence: 16 the finest one, 8, 4 and 4 the others
+    const int level = lane < 16 ? 3 : lane < 24 ? 2 : lane < 28 ? 1 : 0, lanes = level == 3 ? 16 : level == 2 ? 8 : 4;
+    const int at_lane = lane & (lanes - 1), rows_log = 7 - level;
     pdl_wait();
     pdl_trigger();
-    for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) bins[i] = 0;
-    auto each = [&](auto take) {  // take(item, bin) for every tile
-        int end = 0;              // of the query rows of the sequences so far
+    for (int i = threadIdx.x; i < kPlanLevels * kPlanBins; i += kPlanThreads) bins[0][i] = 0;
+    auto each = [&](auto take) {  // take(item, bin) for every tile of this lane's level
+        auto tiles_of = [&](const int4& v, int group, int groups) {
+            for (int t = group * lanes + at_lane; t << rows_log < v.y; t += groups * lanes) {
+                const int row = t << rows_log, rows = min(1 << rows_log, v.y - row), pos = v.w + row;
+                const int tiles = (max(pos + rows, 0) + PK_BN - 1) / PK_BN;
+                take(make_int4(v.x + row, rows, v.z, pos), kPlanBins - 1 - min(tiles, kPlanBins - 1));
+            }
+        };
+        int end = 0;  // of the query rows of the sequences so far
         for (int base = 0; base < S; base += kPlanThreads) {
             const int s = base + threadIdx.x;
             int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
@@ -47,43 +73,54 @@ __global__ void __launch_bounds__(kPlanThreads)
             __syncthreads();  // the previous round's sequences are done
             if (lane == 31) warp_sum[warp] = top;
             __syncthreads();
-            for (int w = 0; w < warp; ++w) top = max(top, warp_sum[w]);
-            top = max(top, end);
-            for (int w = 0; w < kPlanThreads / 32; ++w) end = max(end, warp_sum[w]);
+            top = max(top, __reduce_max_sync(0xffffffffu, lane < warp ? max(warp_sum[lane], end) : end));
+            end = max(end, __reduce_max_sync(0xffffffffu, warp_sum[lane]));
             const bool ok = q0 >= top && q1 >= q0 && q1 <= Nq && k0 >= 0 && k1 >= k0 && k1 <= Nk;
             if (s < S && !ok && err) atomicOr(err, ERR_INDEX);
             seqs[threadIdx.x] = make_int4(q0, ok ? q1 - q0 : 0, k0, ok ? k1 - k0 - (q1 - q0) : 0);
+            const unsigned is_long = __ballot_sync(0xffffffffu, ok && q1 - q0 > kPlanLong);
+            if (lane == 0) longs[warp] = is_long;
             __syncthreads();
             for (int i = warp; i < min(kPlanThreads, S - base); i += kPlanThreads / 32) {
                 const int4 v = seqs[i];
-                for (int t = lane; t * PK_BM < v.y; t += 32) {
-                    const int rows = min(PK_BM, v.y - t * PK_BM), pos = v.w + t * PK_BM;
-                    const int tiles = (max(pos + rows, 0) + PK_BN - 1) / PK_BN;
-                    take(make_int4(v.x + t * PK_BM, rows, v.z, pos), kPlanBins - 1 - min(tiles, kPlanBins - 1));
-                }
+                if (v.y <= kPlanLong) tiles_of(v, 0, 1);
             }
+            for (int w = 0; w < kPlanThreads / 32; ++w)
+                for (unsigned left = longs[w]; left != 0; left &= left - 1)
+                    tiles_of(seqs[w * 32 + __ffs((int)left) - 1], warp, kPlanThreads / 32);
         }
     };
     __syncthreads();
-    each([&](const int4&, int bin) { atomicAdd(&bins[bin], 1); });
-    __syncthreads();
+    each([&](const int4&, int bin) { atomicAdd(&bins[level][bin], 1); });
     static_assert(kPlanBins == kPlanThreads, "a thread a bin");
-    const int mine = bins[threadIdx.x];
-    int sum = mine;
+    __syncthreads();
+    int mine[kPlanLevels], sum[kPlanLevels];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
+    for (int l = 0; l < kPlanLevels; ++l) {
+        sum[l] = mine[l] = bins[l][threadIdx.x];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum[l], o);
+            if (lane >= o) sum[l] += v;
+        }
+        if (lane == 31) bin_sum[l][warp] = sum[l];
     }
-    if (lane == 31) warp_sum[warp] = sum;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) sum += warp_sum[w];
-    bins[threadIdx.x] = sum - mine;
-    if (threadIdx.x == kPlanThreads - 1) *count = min(sum, capacity);  // (no more: the sequences do not overlap)
+#pragma unroll
+    for (int l = 0; l < kPlanLevels; ++l) {
+        sum[l] += __reduce_add_sync(0xffffffffu, lane < warp ? bin_sum[l][lane] : 0);
+        bins[l][threadIdx.x] = sum[l] - mine[l];
+        if (threadIdx.x == kPlanThreads - 1) {  // (no more than there is room for: the sequences do not overlap)
+            header->count[l] = min(sum[l], at.count[l]);
+            header->first[l] = at.first[l];
+        }
+    }
     __syncthreads();
+    int4* const list = items + at.first[level];
+    const int room = at.count[level];
     each([&](const int4& item, int bin) {
-        const int at = atomicAdd(&bins[bin], 1);
-        if (at < capacity) items[at] = item;
+        const int n = atomicAdd(&bins[level][bin], 1);
+        if (n < room) list[n] = item;
     });
 }
 
@@ -127,7 +164,7 @@ static_assert(PkLayout<128, true>::SMEM <= 227 * 1024 && PkLayout<128, false>::S
 
 struct PackedArgs {
     const int4* items;
-    const int* count;
+    const PlanHeader* plan;
     int capacity, max_keys;
     int Nq, Hq, Hkv, pg_log;
     __nv_bfloat16* out;
@@ -192,14 +229,16 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
     // This CTA's items, n_tiles = 0: none left. The first Ly::TABLE are looked up at the start by all threads (looked up by each role
     // when its turn came, an item cost some 1,000 cycles of it).
     const int Hq = a.Hq, pg_log = a.pg_log, groups = Hq >> pg_log, tpt_log = 7 - pg_log;  // tokens of a tile
-    const int n_items = min(max(*a.count, 0), a.capacity) * Hq;
+    const int level = min(pg_log, kPlanLevels - 1), places = groups << (pg_log - level);  // tiles of an entry
+    const int first_entry = (int)min(max(a.plan->first[level], 0ll), (long long)a.capacity);
+    const int n_items = min(max(a.plan->count[level], 0), a.capacity - first_entry) * places;
     const int G = (int)gridDim.x, me = (int)blockIdx.x;
     int4* table = reinterpret_cast<int4*>(smem + Ly::TABLE_OFF);
     auto look_up = [&](int round) -> int4 {  // first query row, query rows + 256 * group of heads, first key row, key position
         const int k = round * G + ((round & 1) ? G - 1 - me : me);
-        const int entry = (int)((unsigned)k / (unsigned)Hq), rem = k - entry * Hq;
+        const int entry = (int)((unsigned)k / (unsigned)places), rem = k - entry * places;
         const int sub = (int)((unsigned)rem / (unsigned)groups), first = sub << tpt_log;
-        const int4 v = __ldg(a.items + entry);
+        const int4 v = __ldg(a.items + first_entry + entry);
         // 0: the entry has fewer tokens, or is none of a plan for these queries
         const int rows = (unsigned)v.x < (unsigned)a.Nq ? max(0, min(v.y - first, 1 << tpt_log)) : 0;
         return make_int4(v.x + first, rows + 256 * (rem - sub * groups), v.z, v.w + first);
@@ -551,7 +590,7 @@ cudaError_t packed_launch_form(const PackedCall& c, cudaStream_t st) {
         !encode_tmap_bf16_rows(&tv, v, blocks, rows, ldv * 2, PK_BN, DH / 64))
         return cudaErrorInvalidValue;
     const PackedArgs a{reinterpret_cast<const int4*>(static_cast<const char*>(c.plan) + kPlanHeader),
-                       static_cast<const int*>(c.plan), c.capacity, c.Nk, c.Nq, c.Hq, c.Hkv, pg_log, c.out, c.err};
+                       static_cast<const PlanHeader*>(c.plan), c.capacity, c.Nk, c.Nq, c.Hq, c.Hkv, pg_log, c.out, c.err};
     const unsigned grid = (unsigned)std::min<long long>((long long)c.capacity * c.Hq, device_sm_count());
     return launch_pdl(attn_packed_kernel<DH, LONG>, dim3(grid), dim3(PK_THREADS), PkLayout<DH, LONG>::SMEM, st, tq, tk, tv, a);
 }
@@ -576,15 +615,24 @@ cudaError_t packed_prepare_form() {
 }  // namespace
 
 size_t attn_packed_plan_bytes(int Nq, int S) {
-    return kPlanHeader + ((size_t)(Nq + PK_BM - 1) / PK_BM + (size_t)S) * sizeof(int4);
+    size_t n = 0;
+    for (int level = 0; level < kPlanLevels; ++level) n += plan_level(Nq, S, level);
+    return kPlanHeader + n * sizeof(int4);
 }
 int attn_packed_capacity(size_t bytes) {
     return bytes < kPlanHeader ? 0 : (int)std::min<size_t>((bytes - kPlanHeader) / sizeof(int4), 0x7fffffff);
 }
-cudaError_t attn_packed_plan_launch(const int* cu_q, const int* cu_k, int S, int Nq, int Nk, void* plan, int capacity, int* err,
+cudaError_t attn_packed_plan_launch(const int* cu_q, const int* cu_k, int S, int Nq, int Nk, void* plan, int* err,
                                     cudaStream_t st) {
-    return launch_pdl(attn_packed_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, cu_q, cu_k, S, Nq, Nk,
-                      static_cast<int*>(plan), reinterpret_cast<int4*>(static_cast<char*>(plan) + kPlanHeader), capacity, err);
+    PlanHeader at{};
+    long long first = 0;
+    for (int level = 0; level < kPlanLevels; ++level) {
+        at.count[level] = (int)plan_level(Nq, S, level);
+        at.first[level] = first;
+        first += at.count[level];
+    }
+    return launch_pdl(attn_packed_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, cu_q, cu_k, S, Nq, Nk, at,
+                      static_cast<PlanHeader*>(plan), reinterpret_cast<int4*>(static_cast<char*>(plan) + kPlanHeader), err);
 }
 cudaError_t attn_packed_launch(const PackedCall& c, int dh, cudaStream_t st) {
     if (dh == 128) return packed_launch_dh<128>(c, st);

@@ -249,7 +249,7 @@ struct PackedCall {
 };
 size_t attn_packed_plan_bytes(int Nq, int S);
 int attn_packed_capacity(size_t bytes);  // items that a plan of this size holds
-cudaError_t attn_packed_plan_launch(const int* cu_q, const int* cu_k, int S, int Nq, int Nk, void* plan, int capacity, int* err,
+cudaError_t attn_packed_plan_launch(const int* cu_q, const int* cu_k, int S, int Nq, int Nk, void* plan, int* err,
                                     cudaStream_t st);
 cudaError_t attn_packed_launch(const PackedCall& c, int dh, cudaStream_t st);
 

@@ -135,10 +135,13 @@ struct AppendArgs {
 // A warp takes every `parts`-th piece of the heads of `per` consecutive tokens; a piece is 32 / LPH heads of LPH = DH / 16 lanes,
 // each with 8 dims of the first half and the 8 dims that they are rotated with. With r = (mean x^2 + eps)^-1/2,
 //   (a, b) -> (r (g_a cos a - g_b sin b), r (g_b cos b + g_a sin a)) in fp32, rounded once;
-// the products of gains and angles are made once a token and kind of head. The next piece's values, and the next token's
+// the products of gains and angles are made once a token and kind of head. The next pieces' values, and the next token's
 // angles, are on their way meanwhile; a sequence is looked up once, then followed from token to token.
-constexpr int AP_AHEAD = 4, AP_CTAS = 4;  // pieces ahead; CTAs of four warps an SM (32,768 tokens and their read: 163 us, five CTAs 172,
-                                          // six 172; two pieces ahead 168, eight 177)
+// What bounds it: many tokens, HBM and issue (32,768 tokens of 32 / 8 heads of 128, 709 MB: 134 us, 5.3 TB/s of a copy's 6.8, 0.59
+// instructions a cycle and scheduler; one warp a head with loads waited for in turn took 410); few, the chain of
+// look-up, page, gains, norm, codes: 3 us with its launch. Pieces ahead and CTAs of four warps an SM: for these tokens and the read of their slots 162 us; five
+// CTAs 172, six 172; two pieces ahead 168, eight 177.
+constexpr int AP_AHEAD = 4, AP_CTAS = 4;
 template <int DH>
 __global__ void __launch_bounds__(128, AP_CTAS)
     append_paged4_kernel(const AppendArgs a, int per, int parts) {
@@ -349,7 +352,9 @@ struct ReadArgs {
 };
 
 // One warp a token: DH / 8 lanes take a row (K or V of a head), eight dims each, so that a store of the warp fills 512 contiguous
-// bytes; RD_ROWS rows' loads are on their way at once. Every value is rounded once.
+// bytes; RD_ROWS rows' loads are on their way at once. Every value is rounded once. What bounds it: HBM writes, most of its
+// bytes (100,000 tokens of 8 heads of 128, 525 MB: 83 us, 6.3 TB/s; two rows at once 87, eight 89; a lane 16 dims in two
+// stores 104).
 constexpr int RD_ROWS = 4;
 template <int DH>
 __global__ void __launch_bounds__(256)
@@ -404,7 +409,8 @@ cudaError_t append_paged4_launch(const __nv_bfloat16* qkv, long long ld, int N, 
     AppendArgs a{qkv, ld, {cu, start, S}, {nullptr, nullptr, table, n_pages, max_pages, log2_of(page)}, N, Hq, Hkv, q_gamma,
                  k_gamma, eps, cos_sin, n_pos, q_out, k_out, static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages),
                  err};
-    // A warp a piece of a token while that does not fill the GPU; then fewer pieces apart, and several tokens a warp.
+    // A warp a piece of a token while that does not fill the GPU; then fewer pieces apart, and several tokens a warp. (A warp a
+    // token from the start: 1 token of 32 / 8 heads and its read 10.5 us against 5.7, 64 tokens of 16 / 8 heads 9.8 against 6.6.)
     const long long pieces = (Hq + 2 * Hkv + 512 / dh - 1) / (512 / dh), room = 4LL * AP_CTAS * device_sm_count();
     const int parts = (int)std::min<long long>(pieces, std::max<long long>(1, room / N));
     const int per = (int)((N + room - 1) / room);

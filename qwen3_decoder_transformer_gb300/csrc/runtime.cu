@@ -1234,8 +1234,7 @@ int qwen3_op_attention_packed_plan(const int* cu_q, const int* cu_k, int S, int 
         !is_aligned(plan, 16) || plan_bytes < attn_packed_plan_bytes(Nq, S))
         return QWEN3_E_ARG;
     if (prepare_kernels() != cudaSuccess) return QWEN3_E_CUDA;
-    return attn_packed_plan_launch(cu_q, cu_k, S, Nq, Nk, plan, attn_packed_capacity(attn_packed_plan_bytes(Nq, S)), err,
-                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return attn_packed_plan_launch(cu_q, cu_k, S, Nq, Nk, plan, err, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? QWEN3_OK
                : QWEN3_E_CUDA;
 }

@@ -12,7 +12,7 @@ import torch
 from qwen3_decoder_transformer_gb300 import build as B
 
 HEADS = [(8, 4, 64), (16, 8, 128), (4, 4, 128), (3, 1, 64)]
-FORMS = [1, 4096, 8192]  # what `longest` selects: plain, speculative, two softmax groups
+FORMS = [1, 4096, 8192]  # values of `longest` on both sides of what picks the kernel's form
 
 
 @pytest.fixture(scope="module")
@@ -181,6 +181,41 @@ def test_views_of_qkv_rows(bd, heads):
     out, err = _run(bd, *[x[1] for x in views], lens, lens, 256)
     assert err == 0
     _check(out, *[x[0] for x in views], lens, lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [(16, 1, 64), (64, 1, 128), (128, 1, 64), (24, 1, 64), (256, 1, 64)], ids=str)
+def test_large_groups(bd, heads):
+    """Groups whose tiles have fewer tokens than the plan's finest list."""
+    lq, lk = [1, 17, 0, 16, 40, 3], [30, 17, 9, 200, 40, 2]
+    q, k, v = _inputs(heads, lq, lk, heads[0], tail=2)
+    out, err = _run(bd, q.cuda(), k.cuda(), v.cuda(), lq, lk, 200)
+    assert err == 0
+    _check(out, q, k, v, lq, lk)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lq,more", [([300, 0, 1, 129, 4097, 64], 0), ([4096, 4098, 5], 3), ([9000], 2000),
+                                     ([3] * 1030 + [5000] + [2] * 20 + [6000], 1)])
+def test_plan_lists(bd, lq, more):
+    """Each of the four lists has every 128, 64, 32 and 16 rows of every sequence once, by falling numbers of key tiles."""
+    lk = [n + more for n in lq]
+    nq, nk = sum(lq), sum(lk)
+    plan, err = _plan(bd, _cu(lq), _cu(lk), nq, nk, len(lq))
+    raw = plan.cpu().numpy()
+    assert int(err.item()) == 0
+    counts, firsts = raw[:16].view(np.int32), raw[16:48].view(np.int64)
+    items = raw[256:].view(np.int32).reshape(-1, 4)
+    for level in range(4):
+        rows = 128 >> level
+        want, q0, k0 = [], 0, 0
+        for a, b in zip(lq, lk):
+            want += [(q0 + t, min(rows, a - t), k0, b - a + t) for t in range(0, a, rows)]
+            q0, k0 = q0 + a, k0 + b
+        got = items[firsts[level]:firsts[level] + counts[level]]
+        assert sorted(map(tuple, got.tolist())) == sorted(want)
+        tiles = np.minimum(-(-(got[:, 3] + got[:, 1]) // 128), 1023)
+        assert np.all(np.diff(tiles) <= 0)
 
 
 @pytest.mark.gpu
