@@ -34,7 +34,7 @@ namespace {
 //
 // What bounds it: many keys, HBM (16 sequences of up to 32,768 keys, 32 / 8 heads of 128: 86 us, 6.1 TB/s, of which some 8 us are
 // start and end). In the loop a unit of each of an SM's 12 warps takes 4,000 cycles, 28 bytes a cycle and SM, which is the
-// copy rate, with the issue slots two thirds full. Few keys: the chain of one unit. 1 sequence of 4096: 9.3 us; counting
+// copy rate, with the issue slots half full. Few keys: the chain of one unit. 1 sequence of 4096: 9.3 us; counting
 // the lengths 0.6, finding the run 0.5, the query 1, one unit 2.1, the pieces 1.4, and the rest two launches and
 // the records' way through the workspace.
 // Split: one CTA of 12 warps an SM, as many rings as shared memory holds, joins the pieces of 12 runs before they leave the SM (16 @

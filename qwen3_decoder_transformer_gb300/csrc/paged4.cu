@@ -137,7 +137,7 @@ struct AppendArgs {
 //   (a, b) -> (r (g_a cos a - g_b sin b), r (g_b cos b + g_a sin a)) in fp32, rounded once;
 // the products of gains and angles are made once a token and kind of head. The next pieces' values, and the next token's
 // angles, are on their way meanwhile; a sequence is looked up once, then followed from token to token.
-// What bounds it: many tokens, HBM and issue (32,768 tokens of 32 / 8 heads of 128, 709 MB: 134 us, 5.3 TB/s of a copy's 6.8, 0.59
+// What bounds it: many tokens, HBM and issue (32,768 tokens of 32 / 8 heads of 128, 776 MB: 134 us, 5.8 TB/s of a copy's 6.8, 0.59
 // instructions a cycle and scheduler; one warp a head with loads waited for in turn took 410); few, the chain of
 // look-up, page, gains, norm, codes: 3 us with its launch. Pieces ahead and CTAs of four warps an SM: for these tokens and the read of their slots 162 us; five
 // CTAs 172, six 172; two pieces ahead 168, eight 177.
