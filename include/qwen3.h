@@ -443,8 +443,9 @@ QWEN3_API int qwen3_op_read_paged4(const void* d_k_pages, const void* d_v_pages,
  * bytes (of the current device; work_bytes is its size, a smaller one is refused), 16-byte aligned, any contents on entry;
  * calls that share one must not overlap on the GPU. Scores, sums and softmax statistics are fp32; the cached codes are used as
  * they are, and probabilities times scales are rounded to fp16 (with a power of two for each head) for the product with the
- * codes. |q| up to 2^90; the visible keys times the largest |v| must stay below 2^50. A page id out of range (bit 4) makes the
- * sequence's output invalid; bit 2 as for the other attention operators. The result does not depend on timing. */
+ * codes. |q| up to 2^90, scores up to 2^30 in size; the visible keys times the largest |v| must stay below 2^50. A page id
+ * out of range (bit 4) makes the sequence's output invalid; bit 2 as for the other attention operators. The result does not
+ * depend on timing. */
 QWEN3_API size_t qwen3_attention_decode_paged4_workspace(int B, int Hq, int Hkv, int dh);
 QWEN3_API int qwen3_op_attention_decode_paged4(const void* d_q, const void* d_k_pages, const void* d_v_pages, int n_pages,
                                                int page_size, const int* d_page_table, int max_pages, const int* d_len0, int B,
@@ -463,8 +464,8 @@ QWEN3_API int qwen3_op_attention_decode_paged4(const void* d_q, const void* d_k_
  * of the longest sequence, only picks between equivalent forms of the kernel: any value gives a right result.
  * Scores, sums and softmax statistics are fp32, probabilities are rounded to bf16 for the product with V. Value rows that some
  * query of a 128-row tile sees must be finite; nothing stored in another sequence's rows, or behind the tile's last visible
- * key, reaches a result. The visible keys times the largest |v| must stay below 2^119; Nq, Nk and S are at most 2^30, and
- * plan_bytes / 16 times Hq below 2^31 - 2^16. */
+ * key, reaches a result. Scores must stay below 2^30 in size, and the visible keys times the largest |v| below 2^119; Nq, Nk
+ * and S are at most 2^30, and plan_bytes / 16 times Hq below 2^31 - 2^16. */
 QWEN3_API size_t qwen3_attention_packed_plan_bytes(int Nq, int S);
 QWEN3_API int qwen3_op_attention_packed_plan(const int* d_cu_q, const int* d_cu_k, int S, int Nq, int Nk, void* d_plan,
                                              size_t plan_bytes, int* d_err, void* stream);

@@ -396,7 +396,7 @@ def test_decode(bd, heads, page):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B_", [1, 2, 7, 255, 256, 257, 600])
+@pytest.mark.parametrize("B_", [1, 2, 7, 255, 256, 257, 383, 384, 385, 600, 1500])
 @pytest.mark.parametrize("heads", [(8, 4, 64), (16, 8, 128)], ids=str)
 def test_decode_batches(bd, heads, B_):
     """Batches past the strips in which lengths are counted, with empty sequences among them."""
@@ -493,6 +493,86 @@ def test_decode_bad_page_and_nan_stay_in_their_sequence(bd):
     assert torch.isnan(o[0, 4:6]).all()
     g = good.view(3, 8, 64)
     assert torch.equal(o[0, :4], g[0, :4]) and torch.equal(o[0, 6:], g[0, 6:]) and torch.equal(o[1:], g[1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [(8, 4, 64), (16, 4, 128), (8, 1, 128)], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_decode_bad_query_stays_in_its_head(bd, heads, bad):
+    """A query value of NaN or infinity makes that head NaN, and no other."""
+    Hq, Hkv, dh = heads
+    lens = [900, 20, 64]
+    c = Cache(Hkv, dh, 32, lens, 11).fill(lens, 11)
+    q = torch.randn(3, Hq, dh, generator=torch.Generator().manual_seed(11)).to(torch.bfloat16)
+    q[0, 1, 5] = bad
+    q[2, Hq - 1] = bad
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    o = out.view(3, Hq, dh).cpu()
+    assert torch.isnan(o[0, 1]).all() and torch.isnan(o[2, Hq - 1]).all()
+    q[0, 1, 5] = 0
+    q[2, Hq - 1] = 0
+    ref, tol = _ref_decode(q, c, lens)
+    good = np.ones((3, Hq), dtype=bool)
+    good[0, 1] = good[2, Hq - 1] = False
+    assert np.all((np.abs(o.double().numpy() - ref) <= tol)[good])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("slot", [3, 500, 899])
+def test_decode_bad_value_stays_in_its_dims(bd, slot):
+    """A NaN pair of V makes its 64 dims of its kv head NaN."""
+    lens = [900]
+    c = Cache(2, 128, 64, lens, 12).fill(lens, 12)
+    q = torch.randn(1, 8, 128, generator=torch.Generator().manual_seed(12)).to(torch.bfloat16)
+    ref, tol = _ref_decode(q, c, lens)
+    side = c.v[:, :, 64 * 64:].view(torch.bfloat16)
+    side[int(c.table[0, slot // 64]), 1, (slot % 64) * 4 + 2:(slot % 64) * 4 + 4] = float("nan")
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([899], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    o = out.view(1, 8, 128).cpu().double().numpy()
+    assert np.isnan(o[0, 4:, 64:]).all()
+    near = np.abs(o - ref) <= tol
+    assert near[0, :4].all() and near[0, 4:, :64].all()
+
+
+@pytest.mark.gpu
+def test_steps_in_a_graph(bd):
+    """A decode step (append and attention of every sequence) captured once and replayed as the lengths grow over the ends of units
+    and pages, against the same calls made one by one on a second cache; each capture has its workspace."""
+    heads, page, S, steps = (16, 8, 128), 16, 3, 9
+    Hq, Hkv, dh = heads
+    lens = [60, 127, 1]
+    first = Cache(Hkv, dh, page, [n + steps for n in lens], 13).fill(lens, 13)
+    pages = [(first.k, first.v), (first.k.clone(), first.v.clone())]
+    cs = torch.empty(300, dh, dtype=torch.bfloat16, device="cuda")
+    bd.op_rope_table(1e6, dh, 300, cs)
+    gen = torch.Generator().manual_seed(13)
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    size = bd.attention_decode_paged4_workspace(S, Hq, Hkv, dh)
+    qkv = torch.empty(S, (Hq + 2 * Hkv) * dh, dtype=torch.bfloat16, device="cuda")
+    at = torch.empty(S, dtype=torch.int32, device="cuda")
+    bufs = [(torch.empty(S, Hq, dh, dtype=torch.bfloat16, device="cuda"), torch.empty(size, dtype=torch.uint8, device="cuda"),
+             torch.empty(S, Hq * dh, dtype=torch.bfloat16, device="cuda")) for _ in range(2)]
+
+    def step(i):
+        (kp, vp), (q, work, out) = pages[i], bufs[i]
+        bd.op_append_paged4(qkv, cu, at, cs, kp, vp, first.dtable, q)
+        bd.op_attention_decode_paged4(q, kp, vp, first.dtable, at, work, out)
+
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        step(0)
+    for i in range(steps):
+        qkv.copy_(torch.randn(qkv.shape, generator=gen).to(torch.bfloat16))
+        at.copy_(torch.tensor([n + i for n in lens], dtype=torch.int32))
+        graph.replay()
+        step(1)
+        torch.cuda.synchronize()
+        assert torch.equal(bufs[0][0], bufs[1][0]) and torch.equal(bufs[0][2], bufs[1][2])
+    assert torch.equal(pages[0][0], pages[1][0]) and torch.equal(pages[0][1], pages[1][1])
+    _check_decode(bufs[0][2], bufs[0][0].cpu(), first, [n + steps for n in lens])
 
 
 @pytest.mark.gpu
