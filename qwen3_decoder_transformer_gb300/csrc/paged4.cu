@@ -354,9 +354,9 @@ struct ReadArgs {
 // One warp a token: DH / 8 lanes take a row (K or V of a head), eight dims each, so that a store of the warp fills 512 contiguous
 // bytes; RD_ROWS rows' loads are on their way at once. Every value is rounded once. What bounds it: HBM writes, most of its
 // bytes (100,000 tokens of 8 heads of 128, 525 MB: 83 us, 6.3 TB/s; two rows at once 87, eight 89; a lane 16 dims in two
-// stores 104).
-constexpr int RD_ROWS = 4;
-template <int DH>
+// stores 104). Where two rows at once are all of a token's, more would only repeat them: RD_ROWS is 2 (65,536 tokens of 2
+// heads of 128 or 4 of 64: 20 us, with four 23.5).
+template <int DH, int RD_ROWS>
 __global__ void __launch_bounds__(256)
     read_paged4_kernel(const ReadArgs a) {
     constexpr int LPR = DH / 8, RPW = 32 / LPR;  // lanes a row, rows a warp at once
@@ -428,8 +428,11 @@ cudaError_t read_paged4_launch(const void* k_pages, const void* v_pages, int n_p
                 log2_of(page)},
                N, Hkv, k_out, v_out, err};
     const unsigned grid = ((unsigned)N + 7) / 8;
-    return dh == 128 ? launch_pdl(read_paged4_kernel<128>, dim3(grid), dim3(256), 0, st, a)
-                     : launch_pdl(read_paged4_kernel<64>, dim3(grid), dim3(256), 0, st, a);
+    if (dh == 128)  // (a step is 2 RD_ROWS rows, or at head_dim 64 4 RD_ROWS)
+        return Hkv <= 2 ? launch_pdl(read_paged4_kernel<128, 2>, dim3(grid), dim3(256), 0, st, a)
+                        : launch_pdl(read_paged4_kernel<128, 4>, dim3(grid), dim3(256), 0, st, a);
+    return Hkv <= 4 ? launch_pdl(read_paged4_kernel<64, 2>, dim3(grid), dim3(256), 0, st, a)
+                    : launch_pdl(read_paged4_kernel<64, 4>, dim3(grid), dim3(256), 0, st, a);
 }
 
 }  // namespace q3
