@@ -1,5 +1,6 @@
 // Appending to and reading from the paged KV cache held in 4 bits (layout: paged4.cuh).
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "internal.h"
@@ -141,7 +142,7 @@ struct AppendArgs {
 // instructions a cycle and scheduler; one warp a head with loads waited for in turn took 410); few, the chain of
 // look-up, page, gains, norm, codes: 3 us with its launch. Pieces ahead and CTAs of four warps an SM: for these tokens and the read of their slots 162 us; five
 // CTAs 172, six 172; two pieces ahead 168, eight 177.
-constexpr int AP_AHEAD = 4, AP_CTAS = 4;
+constexpr int AP_AHEAD = 4, AP_CTAS = 4, AP_START = 2, AP_ALL = 4;
 template <int DH>
 __global__ void __launch_bounds__(128, AP_CTAS)
     append_paged4_kernel(const AppendArgs a, int per, int parts) {
@@ -409,11 +410,23 @@ cudaError_t append_paged4_launch(const __nv_bfloat16* qkv, long long ld, int N, 
     AppendArgs a{qkv, ld, {cu, start, S}, {nullptr, nullptr, table, n_pages, max_pages, log2_of(page)}, N, Hq, Hkv, q_gamma,
                  k_gamma, eps, cos_sin, n_pos, q_out, k_out, static_cast<uint8_t*>(k_pages), static_cast<uint8_t*>(v_pages),
                  err};
-    // A warp a piece of a token while that does not fill the GPU; then fewer pieces apart, and several tokens a warp. (A warp a
-    // token from the start: 1 token of 32 / 8 heads and its read 10.5 us against 5.7, 64 tokens of 16 / 8 heads 9.8 against 6.6.)
-    const long long pieces = (Hq + 2 * Hkv + 512 / dh - 1) / (512 / dh), room = 4LL * AP_CTAS * device_sm_count();
-    const int parts = (int)std::min<long long>(pieces, std::max<long long>(1, room / N));
-    const int per = (int)((N + room - 1) / room);
+    // `parts` warps share the pieces of a token, and each takes `per` tokens. The split with the shortest way of a warp, in pieces: a
+    // token costs AP_START more, and a GPU full of warps that start together AP_ALL more. With the reads of the same slots, 32 / 8
+    // heads of 128: 1 token 5.9 us (a warp a token 10.5), 200 tokens 7.2 (as many warps as there are pieces 10.0), 3,000 25.2 (a
+    // warp a token 28.5), 32,768 163.
+    const double room = 4. * AP_CTAS * device_sm_count();
+    const int pieces = (Hq + 2 * Hkv + 512 / dh - 1) / (512 / dh);
+    int parts = 1, per = 0;
+    double least = 0;
+    for (int p = 1; p <= std::min(pieces, 64); ++p) {
+        const int n = (int)std::ceil(N * (double)p / room);
+        const double way = n * (double)((pieces + p - 1) / p + AP_START) + AP_ALL * (N * (double)p / (n * room));
+        if (per == 0 || way < least) {
+            parts = p;
+            per = n;
+            least = way;
+        }
+    }
     const long long warps = ((long long)N + per - 1) / per * parts;
     const dim3 grid((unsigned)((warps + 3) / 4));
     return dh == 128 ? launch_pdl(append_paged4_kernel<128>, grid, dim3(128), 0, st, a, per, parts)

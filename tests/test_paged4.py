@@ -217,6 +217,17 @@ def test_append_decode_batches(bd, seqs):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads,n", [((32, 8, 128), 150), ((32, 8, 128), 300), ((16, 8, 128), 801), ((32, 8, 128), 2600),
+                                     ((4, 4, 64), 5003)], ids=str)
+def test_append_splits(bd, heads, n):
+    """Tokens shared by several warps, and warps with several tokens, over the ends of sequences and pages."""
+    lens, start = [n // 3, 0, n // 3 + 1, n - n // 3 * 2 - 1], [7, 0, 30, 0]
+    r = _append(bd, heads, 16, lens, start, pad=5, seed=n)
+    assert r["err"] == 0
+    _check_append(r, heads, lens, start)
+
+
+@pytest.mark.gpu
 def test_append_rows_further_apart_and_no_keys_out(bd):
     heads, lens, start = (8, 4, 64), [9, 2], [3, 30]
     r = _append(bd, heads, 16, lens, start, ld_extra=24, seed=3)
