@@ -6,13 +6,14 @@ The library must have been built (``__graft_entry__.build()``); loading fails lo
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 
 import numpy as np
 import torch
 
-from .build import LIB
+from .build import LIB, TENSORS
 
 _vp = ctypes.c_void_p
 _i32p = ctypes.POINTER(ctypes.c_int)
@@ -595,17 +596,25 @@ def op_attention_decode_sinks(q, k_cache, v_cache, len0, out, window, sinks, rol
 
 # ------------------------------------------------------------------ the paged 4-bit cache and packed batches
 #
-# As above, what is wrong with a call's tensors is worked out (the _why functions) only when one expression finds something.
-
-# Their arguments go in one block each (the args structs of the header, in native layout): a foreign call costs 0.1 us an argument.
+# The extension module _tensors (csrc/tensors.cpp) looks the tensors over and packs their arguments in one block each (the args
+# structs of the header); what is wrong with them is worked out here (the _why functions) only when it finds something.
 
 _U8 = torch.uint8
-_APPEND_ARGS = struct.Struct("PqiPPiiiiPPfPiPPPPiiPiP")
-_READ_ARGS = struct.Struct("PPiiPiPPiiiiPPP")
-_DECODE_ARGS = struct.Struct("PPPiiPiPiiiiPNPP")
-_PACKED_ARGS = struct.Struct("PqPqPqiiiiiPNiPP")
 PAGE_SIZES = (16, 32, 64, 128, 256)
+_tensors = None
 _PAGE_OF = {(p * (dh // 2 + dh // 16), dh): p for p in PAGE_SIZES for dh in (64, 128)}  # by page bytes and head_dim
+
+
+def _checks():
+    global _tensors
+    if _tensors is None:
+        if not os.path.exists(TENSORS):
+            raise RuntimeError(f"extension not built ({TENSORS}); run __graft_entry__.build() first")
+        loader = importlib.machinery.ExtensionFileLoader("_tensors", TENSORS)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensors", loader))
+        loader.exec_module(module)
+        _tensors = module
+    return _tensors
 
 
 def paged4_page_bytes(page_size, dh) -> int:
@@ -635,7 +644,7 @@ def _why_bounds(cu, start, sequences, dev):
     _dense("start", start, _I32, (sequences,), dev)
 
 
-def _why_append(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out, q_gamma, k_gamma):
+def _why_append(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out, q_gamma, k_gamma, err):
     _want(isinstance(qkv, torch.Tensor) and qkv.dim() == 2, "qkv must be a tensor [N, (Hq + 2 Hkv) dh]")
     _want(isinstance(q_out, torch.Tensor) and q_out.dim() == 3, "q_out must be a tensor [N, Hq, dh]")
     N, Hq, dh = q_out.shape
@@ -654,6 +663,8 @@ def _why_append(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_
     for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
         if g is not None:
             _dense(name, g, _BF16, (dh,), dev)
+    if err is not None:
+        _dense("err", err, _I32, (1,), dev)
     raise ValueError("the tensors do not fit the call")
 
 
@@ -663,48 +674,14 @@ def op_append_paged4(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_ou
     stride along a row): rows cu[s] .. cu[s+1]-1 take the slots start[s] .. of sequence s. Writes q_out [N, Hq, dh], k_out
     [N, Hkv, dh] (None: not wanted) and the pages; rows from cu[-1] on are left as they were. err: device int (bit 4: a
     page id or a position out of range)."""
-    try:
-        N, Hq, dh = q_out.shape
-        shape = k_pages.shape
-        n_pages, Hkv, size = shape
-        S, max_pages = page_table.shape
-        n_pos, _ = angles = cos_sin.shape
-        ld, unit = qkv.stride()
-        page = _PAGE_OF.get((size, dh))
-        dev = qkv.get_device()
-        ok = (page is not None and n_pages and Hkv and max_pages and Hq and Hq % Hkv == 0 and unit == 1
-              and qkv.shape == (N, (Hq + 2 * Hkv) * dh) and v_pages.shape == shape and angles == (n_pos, dh)
-              and cu.shape == (S + 1,) and start.shape == (S,)
-              and qkv.dtype is _BF16 and q_out.dtype is _BF16 and cos_sin.dtype is _BF16 and k_pages.dtype is _U8
-              and v_pages.dtype is _U8 and page_table.dtype is _I32 and cu.dtype is _I32 and start.dtype is _I32
-              and q_out.get_device() == dev and cos_sin.get_device() == dev and k_pages.get_device() == dev
-              and v_pages.get_device() == dev and page_table.get_device() == dev and cu.get_device() == dev
-              and start.get_device() == dev and q_out.is_contiguous() and cos_sin.is_contiguous() and k_pages.is_contiguous()
-              and v_pages.is_contiguous() and page_table.is_contiguous() and cu.is_contiguous() and start.is_contiguous()
-              and (k_out is None or (k_out.shape == (N, Hkv, dh) and k_out.dtype is _BF16 and k_out.get_device() == dev
-                                     and k_out.is_contiguous()))
-              and (q_gamma is None or (q_gamma.shape == (dh,) and q_gamma.dtype is _BF16 and q_gamma.get_device() == dev
-                                       and q_gamma.is_contiguous()))
-              and (k_gamma is None or (k_gamma.shape == (dh,) and k_gamma.dtype is _BF16 and k_gamma.get_device() == dev
-                                       and k_gamma.is_contiguous())))
-    except (AttributeError, ValueError):  # not tensors, or not of these numbers of dimensions
-        ok = False
-    if not ok:
-        _why_append(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out, q_gamma, k_gamma)
-    p_err = 0 if err is None else _dense("err", err, _I32, (1,), dev)
-    if N == 0 or S == 0:
-        return
-    if N == 1:  # (the stride of a single row says nothing)
-        ld = (Hq + 2 * Hkv) * dh
-    _launch(lib().qwen3_op_append_paged4_block,
-            (_APPEND_ARGS.pack(qkv.data_ptr(), ld, N, cu.data_ptr(), start.data_ptr(), S, Hq, Hkv, dh,
-                               0 if q_gamma is None else q_gamma.data_ptr(), 0 if k_gamma is None else k_gamma.data_ptr(), eps,
-                               cos_sin.data_ptr(), n_pos, q_out.data_ptr(), 0 if k_out is None else k_out.data_ptr(),
-                               k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,
-                               p_err),), dev, stream)
+    block = _checks().append_paged4(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out, q_gamma, k_gamma, eps, err)
+    if block is None:
+        _why_append(qkv, cu, start, cos_sin, k_pages, v_pages, page_table, q_out, k_out, q_gamma, k_gamma, err)
+    if block:
+        _launch(lib().qwen3_op_append_paged4_block, (block,), qkv.get_device(), stream)
 
 
-def _why_read(k_pages, v_pages, page_table, cu, start, k_out, v_out):
+def _why_read(k_pages, v_pages, page_table, cu, start, k_out, v_out, err):
     _want(isinstance(k_out, torch.Tensor) and k_out.dim() == 3, "k_out must be a tensor [N, Hkv, dh]")
     N, _, dh = k_out.shape
     dev = k_out.get_device()
@@ -712,46 +689,26 @@ def _why_read(k_pages, v_pages, page_table, cu, start, k_out, v_out):
     _why_bounds(cu, start, page_table.shape[0], dev)
     _dense("k_out", k_out, _BF16, (N, Hkv, dh), dev)
     _dense("v_out", v_out, _BF16, (N, Hkv, dh), dev)
+    if err is not None:
+        _dense("err", err, _I32, (1,), dev)
     raise ValueError("the tensors do not fit the call")
 
 
 def op_read_paged4(k_pages, v_pages, page_table, cu, start, k_out, v_out, err=None, stream=None):
     """Slots start[s] .. of sequence s of the paged 4-bit cache into the rows cu[s] .. cu[s+1]-1 of k_out and v_out
     [N, Hkv, dh] bf16."""
-    try:
-        rows = k_out.shape
-        N, heads, dh = rows
-        shape = k_pages.shape
-        n_pages, Hkv, size = shape
-        S, max_pages = page_table.shape
-        page = _PAGE_OF.get((size, dh))
-        dev = k_out.get_device()
-        ok = (page is not None and n_pages and Hkv and max_pages and heads == Hkv and v_pages.shape == shape
-              and v_out.shape == rows and cu.shape == (S + 1,) and start.shape == (S,)
-              and k_out.dtype is _BF16 and v_out.dtype is _BF16 and k_pages.dtype is _U8 and v_pages.dtype is _U8
-              and page_table.dtype is _I32 and cu.dtype is _I32 and start.dtype is _I32
-              and v_out.get_device() == dev and k_pages.get_device() == dev and v_pages.get_device() == dev
-              and page_table.get_device() == dev and cu.get_device() == dev and start.get_device() == dev
-              and k_out.is_contiguous() and v_out.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
-              and page_table.is_contiguous() and cu.is_contiguous() and start.is_contiguous())
-    except (AttributeError, ValueError):
-        ok = False
-    if not ok:
-        _why_read(k_pages, v_pages, page_table, cu, start, k_out, v_out)
-    p_err = 0 if err is None else _dense("err", err, _I32, (1,), dev)
-    if N == 0 or S == 0:
-        return
-    _launch(lib().qwen3_op_read_paged4_block,
-            (_READ_ARGS.pack(k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages,
-                             cu.data_ptr(), start.data_ptr(), S, N, Hkv, dh, k_out.data_ptr(), v_out.data_ptr(), p_err),),
-            dev, stream)
+    block = _checks().read_paged4(k_pages, v_pages, page_table, cu, start, k_out, v_out, err)
+    if block is None:
+        _why_read(k_pages, v_pages, page_table, cu, start, k_out, v_out, err)
+    if block:
+        _launch(lib().qwen3_op_read_paged4_block, (block,), k_out.get_device(), stream)
 
 
 def attention_decode_paged4_workspace(B, Hq, Hkv, dh) -> int:
     return lib().qwen3_attention_decode_paged4_workspace(B, Hq, Hkv, dh)
 
 
-def _why_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out):
+def _why_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out, err):
     _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [B, Hq, dh]")
     B, Hq, dh = q.shape
     dev = q.get_device()
@@ -763,38 +720,19 @@ def _why_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out):
     _dense("out", out, _BF16, (B, Hq * dh), dev)
     _want(isinstance(work, torch.Tensor) and work.get_device() == dev and work.is_contiguous(),
           "work must be contiguous scratch on the same device, of attention_decode_paged4_workspace bytes")
+    if err is not None:
+        _dense("err", err, _I32, (1,), dev)
     raise ValueError("the tensors do not fit the call")
 
 
 def op_attention_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out, err=None, stream=None):
     """Decode attention of q [B, Hq, dh] over the slots 0..len0[b] of each sequence of the paged 4-bit cache, into out
     [B, Hq*dh]. work: attention_decode_paged4_workspace bytes of scratch of any type."""
-    try:
-        B, Hq, dh = q.shape
-        shape = k_pages.shape
-        n_pages, Hkv, size = shape
-        rows, max_pages = page_table.shape
-        page = _PAGE_OF.get((size, dh))
-        dev = q.get_device()
-        ok = (page is not None and n_pages and Hkv and max_pages and Hq and Hq % Hkv == 0 and Hq <= 8 * Hkv and rows == B
-              and v_pages.shape == shape and len0.shape == (B,) and out.shape == (B, Hq * dh)
-              and q.dtype is _BF16 and out.dtype is _BF16 and k_pages.dtype is _U8 and v_pages.dtype is _U8
-              and page_table.dtype is _I32 and len0.dtype is _I32
-              and out.get_device() == dev and k_pages.get_device() == dev and v_pages.get_device() == dev
-              and page_table.get_device() == dev and len0.get_device() == dev and work.get_device() == dev
-              and q.is_contiguous() and out.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
-              and page_table.is_contiguous() and len0.is_contiguous() and work.is_contiguous())
-    except (AttributeError, ValueError):
-        ok = False
-    if not ok:
-        _why_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out)
-    p_err = 0 if err is None else _dense("err", err, _I32, (1,), dev)
-    if B == 0:
-        return
-    _launch(lib().qwen3_op_attention_decode_paged4_block,
-            (_DECODE_ARGS.pack(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, page_table.data_ptr(),
-                               max_pages, len0.data_ptr(), B, Hq, Hkv, dh, work.data_ptr(), work.nbytes, out.data_ptr(),
-                               p_err),), dev, stream)
+    block = _checks().attention_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out, err)
+    if block is None:
+        _why_decode_paged4(q, k_pages, v_pages, page_table, len0, work, out, err)
+    if block:
+        _launch(lib().qwen3_op_attention_decode_paged4_block, (block,), q.get_device(), stream)
 
 
 def attention_packed_plan_bytes(Nq, S) -> int:
@@ -817,7 +755,7 @@ def op_attention_packed_plan(cu_q, cu_k, Nq, Nk, plan, err=None, stream=None):
             (cu_q.data_ptr(), cu_k.data_ptr(), n - 1, _int32(Nq), _int32(Nk), plan.data_ptr(), plan.nbytes, p_err), dev, stream)
 
 
-def _why_packed(q, k, v, plan, out):
+def _why_packed(q, k, v, plan, out, err):
     _want(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a tensor [Nq, Hq, dh]")
     Nq, Hq, dh = q.shape
     dev = q.get_device()
@@ -830,6 +768,8 @@ def _why_packed(q, k, v, plan, out):
     _dense("out", out, _BF16, (Nq, Hq * dh), dev)
     _want(isinstance(plan, torch.Tensor) and plan.get_device() == dev and plan.is_contiguous(),
           "plan must be the contiguous work list that op_attention_packed_plan wrote, on the same device")
+    if err is not None:
+        _dense("err", err, _I32, (1,), dev)
     raise ValueError("the tensors do not fit the call")
 
 
@@ -837,30 +777,8 @@ def op_attention_prefill_packed(q, k, v, plan, longest, out, err=None, stream=No
     """Causal attention over packed sequences: q [Nq, Hq, dh], k and v [Nk, Hkv, dh] (rows may be further apart, as views of
     packed qkv rows are), plan as op_attention_packed_plan wrote it for these Nq and Nk; out [Nq, Hq*dh]. longest = keys of
     the longest sequence, a hint for the launch (any value is right)."""
-    try:
-        Nq, Hq, dh = q.shape
-        keys = k.shape
-        Nk, Hkv, kd = keys
-        ldq, hq, uq = q.stride()
-        ldk, hk, uk = k.stride()
-        ldv, hv, uv = v.stride()
-        dev = q.get_device()
-        ok = (kd == dh and v.shape == keys and Hkv and Hq and Hq % Hkv == 0 and uq == uk == uv == 1
-              and (hq == dh or Hq == 1) and ((hk == dh and hv == dh) or Hkv == 1) and out.shape == (Nq, Hq * dh)
-              and q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and out.dtype is _BF16
-              and k.get_device() == dev and v.get_device() == dev and out.get_device() == dev and plan.get_device() == dev
-              and out.is_contiguous() and plan.is_contiguous())
-    except (AttributeError, ValueError):
-        ok = False
-    if not ok:
-        _why_packed(q, k, v, plan, out)
-    p_err = 0 if err is None else _dense("err", err, _I32, (1,), dev)
-    if Nq == 0:
-        return
-    if Nq == 1:  # (the stride of a single row says nothing)
-        ldq = Hq * dh
-    if Nk <= 1:
-        ldk = ldv = Hkv * dh
-    _launch(lib().qwen3_op_attention_prefill_packed_block,
-            (_PACKED_ARGS.pack(q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, Nq, Nk, Hq, Hkv, dh, plan.data_ptr(),
-                               plan.nbytes, _int32(longest), out.data_ptr(), p_err),), dev, stream)
+    block = _checks().attention_prefill_packed(q, k, v, plan, longest, out, err)
+    if block is None:
+        _why_packed(q, k, v, plan, out, err)
+    if block:
+        _launch(lib().qwen3_op_attention_prefill_packed_block, (block,), q.get_device(), stream)

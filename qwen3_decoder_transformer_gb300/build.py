@@ -1,7 +1,8 @@
 """Build the CUDA library in-tree: qwen3_decoder_transformer_gb300/_build/libqwen3_gb300.so.
 
 Each translation unit in csrc/ is compiled by nvcc for sm_103a only (one -gencode) in parallel,
-then linked into one shared library with the CUDA runtime linked statically. No CMake.
+then linked into one shared library with the CUDA runtime linked statically. No CMake. Beside it, tensors.cpp
+(the binding's checks of tensors) becomes the extension module _build/_tensors.so.
 """
 from __future__ import annotations
 
@@ -9,12 +10,14 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libqwen3_gb300.so")
+TENSORS = os.path.join(BUILD, "_tensors.so")
 SOURCES = ["gemm.cu", "kernels.cu", "attention.cu", "attention_tiles.cu", "attention_ranges.cu", "attention_packed.cu", "attention_paged4.cu", "paged4.cu", "logprobs.cu", "runtime.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -33,9 +36,26 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _build_tensors() -> None:
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    paths = [os.path.join(ROOT, "include"), os.path.join(root, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(root, "lib")
+    tmp = TENSORS + ".tmp"
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + ["-I" + p for p in paths]
+           + [os.path.join(CSRC, "tensors.cpp"), "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu",
+              "-lc10"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for tensors.cpp:\n{r.stderr}")
+    os.replace(tmp, TENSORS)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, TENSORS)):
         return LIB
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
 
@@ -47,8 +67,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        tensors = ex.submit(_build_tensors)
         results = list(ex.map(compile_one, SOURCES))
+        tensors.result()
     if verbose_ptxas:
         for _, err in results:
             print(err)

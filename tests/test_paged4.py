@@ -717,18 +717,22 @@ def test_library_refuses(bd):
     assert bd.attention_decode_paged4_workspace(1, 36, 4, 64) == 0
 
 
+APPEND_ARGS, READ_ARGS, DECODE_ARGS, PACKED_ARGS = (struct.Struct(f) for f in (
+    "PqiPPiiiiPPfPiPPPPiiPiP", "PPiiPiPPiiiiPPP", "PPPiiPiPiiiiPNPP", "PqPqPqiiiiiPNiPP"))  # the header's argument blocks
+
+
 def test_argument_blocks(bd):
-    """The blocks that the binding packs have the header's layout: every field, wrong by itself, is refused as in the direct call,
-    and the right ones are taken (a call without rows does nothing)."""
+    """Argument blocks: every field, wrong by itself, is refused as in the direct call, and the right ones are taken (a call
+    without rows does nothing)."""
     L, p, size = bd.lib(), 4096, 1 << 30
     # (the row count, field `rows`, stays 0: nothing is launched)
-    forms = ((L.qwen3_op_append_paged4_block, bd._APPEND_ARGS, L.qwen3_op_append_paged4, 2,
+    forms = ((L.qwen3_op_append_paged4_block, APPEND_ARGS, L.qwen3_op_append_paged4, 2,
               [p, 1024, 0, p, p, 1, 8, 4, 64, p, p, 1e-6, p, 10, p, p, p, p, 4, 16, p, 2, 0]),
-             (L.qwen3_op_read_paged4_block, bd._READ_ARGS, L.qwen3_op_read_paged4, 9,
+             (L.qwen3_op_read_paged4_block, READ_ARGS, L.qwen3_op_read_paged4, 9,
               [p, p, 4, 16, p, 2, p, p, 1, 0, 4, 64, p, p, 0]),
-             (L.qwen3_op_attention_decode_paged4_block, bd._DECODE_ARGS, L.qwen3_op_attention_decode_paged4, 8,
+             (L.qwen3_op_attention_decode_paged4_block, DECODE_ARGS, L.qwen3_op_attention_decode_paged4, 8,
               [p, p, p, 4, 16, p, 2, p, 0, 8, 4, 64, p, size, p, 0]),
-             (L.qwen3_op_attention_prefill_packed_block, bd._PACKED_ARGS, L.qwen3_op_attention_prefill_packed, 6,
+             (L.qwen3_op_attention_prefill_packed_block, PACKED_ARGS, L.qwen3_op_attention_prefill_packed, 6,
               [p, 512, p, 256, p, 256, 0, 100, 8, 4, 64, p, 1 << 20, 100, p, 0]))
     for block, layout, direct, rows, args in forms:
         assert args[rows] == 0
@@ -749,6 +753,50 @@ def test_argument_blocks(bd):
                 assert want in (0, 5) and block(packed, None) == want, (block.__name__, i, bad)
                 refused += want == 5
         assert refused > len(args)
+
+
+def _fields(layout, got):
+    return layout.unpack(got.ljust(layout.size, b"\0"))
+
+
+@pytest.mark.parametrize("one", [False, True])
+def test_packed_blocks(bd, one):
+    """The binding's blocks hold the fields of the header's, from tensors of any of the allowed strides; no rows, no block."""
+    bf, i32, u8, c = torch.bfloat16, torch.int32, torch.uint8, bd._checks()
+    N = 1 if one else 6
+    z = lambda *shape, dtype=bf: torch.zeros(shape, dtype=dtype)  # noqa: E731
+    kp, vp, table = z(5, 4, 16 * 72, dtype=u8), z(5, 4, 16 * 72, dtype=u8), z(2, 3, dtype=i32)
+    cu, start, err, work = z(3, dtype=i32), z(2, dtype=i32), z(1, dtype=i32), z(333, dtype=torch.float64)
+    qkv, cs, q, k, v, g = z(N, 2100)[:, :2048], z(9, 128), z(N, 8, 128), z(N, 4, 128), z(N, 4, 128), z(128)
+    at = lambda *ts: [0 if t is None else t.data_ptr() for t in ts]  # noqa: E731
+    for k_out, gq, e in ((k, g, None), (None, None, err)):
+        got = _fields(APPEND_ARGS, c.append_paged4(qkv, cu, start, cs, kp, vp, table, q, k_out, gq, g, 0.25, e))
+        want = at(qkv) + [2048 if one else 2100, N] + at(cu, start) + [2, 8, 4, 128] + at(gq, g) + [0.25] + at(cs) + [9] + \
+            at(q, k_out, kp, vp) + [5, 16] + at(table) + [3] + at(e)
+        assert list(got) == want
+        got = _fields(READ_ARGS, c.read_paged4(kp, vp, table, cu, start, k, v, e))
+        assert list(got) == at(kp, vp) + [5, 16] + at(table) + [3] + at(cu, start) + [2, N, 4, 128] + at(k, v, e)
+        B = z(2, 8, 128)
+        got = _fields(DECODE_ARGS, c.attention_decode_paged4(B, kp, vp, table, start, work, z(2, 1024), e))
+        assert list(got)[:-2] == at(B, kp, vp) + [5, 16] + at(table) + [3] + at(start) + [2, 8, 4, 128] + at(work) + [2664]
+        heads = qkv.as_strided((N, 4, 128), (2100, 128, 1), 1024)
+        out = z(N, 1024)
+        got = _fields(PACKED_ARGS, c.attention_prefill_packed(q, heads, v, work, 77, out, e))
+        assert list(got) == at(q) + [1024] + at(heads) + [512 if one else 2100] + at(v) + [512, N, N, 8, 4, 128] + at(work) + \
+            [2664, 77] + at(out, e)
+    assert c.append_paged4(qkv[:0], cu, start, cs, kp, vp, table, q[:0], None, None, None, 0.25, None) == b""
+    assert c.read_paged4(kp, vp, table, cu, start, k[:0], v[:0], None) == b""
+    assert c.attention_decode_paged4(B[:0], kp, vp, table[:0], start[:0], work, z(0, 1024), None) == b""
+    assert c.attention_prefill_packed(q[:0], k, v, work, 77, z(0, 1024), None) == b""
+    for bad in (None, 3, "q", [q], q.to_sparse()):
+        assert c.read_paged4(kp, vp, table, cu, start, bad, v, None) is None
+        assert c.attention_prefill_packed(q, k, v, bad, 77, out, None) is None
+    with pytest.raises(TypeError):
+        c.read_paged4(kp, vp)
+    with pytest.raises(TypeError):
+        c.append_paged4(qkv, cu, start, cs, kp, vp, table, q, None, None, None, "eps", None)
+    with pytest.raises(TypeError):
+        c.attention_prefill_packed(q, k, v, work, None, out, None)
 
 
 def test_binding_refuses(bd):
