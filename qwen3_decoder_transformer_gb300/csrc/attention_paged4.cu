@@ -29,12 +29,12 @@ namespace {
 // mma (m16n8k16; the heads of a group are far below a tcgen05 tile) takes 16 keys by the heads: S^T = K q^T, then
 // O^T += V^T P^T with P^T moved from accumulator to operand layout by movmatrix. The sums are rescaled only when a weight grows
 // out of its range. A (sequence, kv head) within one run is written out at once. Of one that is cut, each warp leaves a
-// piece (sums, maximum, sum of weights); pieces of one CTA are joined in shared memory, the others in the workspace by
+// piece (sums of weighted values, reference of the weights, sum of weights); pieces of one CTA are joined in shared memory, the others in the workspace by
 // attn_paged4_join_kernel, in the order of their keys: the result does not depend on timing.
 //
 // What bounds it: many keys, HBM (16 sequences of up to 32,768 keys, 32 / 8 heads of 128: 86 us, 6.1 TB/s, of which some 8 us are
 // start and end). In the loop a unit of each of an SM's 12 warps takes 4,000 cycles, 28 bytes a cycle and SM, which is the
-// copy rate, with the issue slots half full. Few keys: the chain of one unit. 1 sequence of 4096: 9.3 us; counting
+// copy rate, with the issue slots half full. Few keys: the chain of one unit. 1 sequence of 4096: 9.5 us; counting
 // the lengths 0.6, finding the run 0.5, the query 1, one unit 2.1, the pieces 1.4, and the rest two launches and
 // the records' way through the workspace.
 // Split: one CTA of 12 warps an SM, as many rings as shared memory holds, joins the pieces of 12 runs before they leave the SM (16 @
@@ -49,7 +49,7 @@ struct P4Layout {
     static constexpr int SLOT = 2 * HALF;
     static constexpr int NS = 2 * 128 / DH;  // slots of a ring
     static constexpr int RING = NS * SLOT;
-    static constexpr int PITCH = DH + 4;  // floats of a head's piece: sums, maximum, sum of weights
+    static constexpr int PITCH = DH + 4;  // floats of a head's piece: sums; reference, adjustment, scale of scores, sum of weights
     static constexpr int SMEM = P4_WARPS * RING;
     static_assert(P4_MAX_G * PITCH * 4 <= RING, "a piece fits a ring");
     static_assert(P4_CTAS * (SMEM + 4096) <= 227 * 1024, "shared memory");
@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         __syncthreads();
     }
     auto all_units = [&]() { return strip_end[P4_STRIPS - 1] * a.Hkv; };  // (fewer than 2^31: checked on the host)
-    // warps of a CTA that work: few units are spread over the SMs (1 sequence of 4096 keys, 8 kv heads: 9.3 us, with full CTAs
-    // 10.0), but not further than a warp a scheduler: every CTA that shares a kv head leaves a record for the join (2 kv
+    // warps of a CTA that work: few units are spread over the SMs (1 sequence of 4096 keys, 8 kv heads: 9.3 us, with full
+    // CTAs 10.0), but not further than a warp a scheduler: every CTA that shares a kv head leaves a record for the join (2 kv
     // heads, a warp a CTA 15.5 us, four 10.3)
     auto team_of = [&](int units) { return max(4, min(P4_WARPS, p4_div(min(units, places) + (int)gridDim.x - 1, (int)gridDim.x))); };
     const int units = all_units();
@@ -292,9 +292,10 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     uint4 qraw[NG][2];
     uint32_t qf[NG][2][2][2];  // q^T fragments [group][word][nibbles][half]; zero past G
     float2 qs[NG], qscale;     // heads ch, ch + 1: sums of the scaled queries over a group of dims; what scores are scaled by
-    // Weights p = 2^(score * qscale + nm) and p * scale, which has to fit fp16: nm is chosen so that the largest p * scale of the
-    // run so far lies in [2^13, 2^15] (p itself below 2^75: a score past `high` is looked at first).
-    float2 nm, high, l;
+    // Weights p = 2^((score - ref) * qscale + adj) and p * scale, which has to fit fp16: ref is a score, and adj a whole number
+    // chosen so that the largest p * scale of the run so far lies in [2^13, 2^15] (p itself below 2^75: a score past `high` is
+    // looked at first). In one number the two lose adj where scores are large.
+    float2 ref, adj, high, l;
     float o[NG][4][4];  // sums of weight * code, in units of 2^-24 (tiles 1 and 3 of a group: 2^-20)
     float2 z[NG];       // sums of weight * minimum
     auto fetch_q = [&]() {
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
             for (int i = 0; i < 4; ++i) o[c][0][i] = o[c][1][i] = o[c][2][i] = o[c][3][i] = 0.f;
         }
         l = make_float2(0.f, 0.f);
-        nm = make_float2(0.f, 0.f);
+        ref = adj = make_float2(0.f, 0.f);
         high = make_float2(-INFINITY, -INFINITY);  // the first score moves it
     };
     // the sums of this warp's piece: dims c * 64 + 8 g + (0..7) of head ch + e
@@ -412,7 +413,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 dst[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
             if (g == 0 && stores(0))
-                *reinterpret_cast<float2*>(rec + h * PITCH + DH) = e ? make_float2(-nm.y, l.y) : make_float2(-nm.x, l.x);
+                *reinterpret_cast<float4*>(rec + h * PITCH + DH) =
+                    e ? make_float4(ref.y, adj.y, qscale.y, l.y) : make_float4(ref.x, adj.x, qscale.x, l.x);
         }
     };
     auto write_out = [&]() {
@@ -547,69 +549,85 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 mx.x = fmax3(mx.x, x[k][0].x, x[k][1].x);
                 mx.y = fmax3(mx.y, x[k][0].y, x[k][1].y);
             }
-            float2 was = nm;
+            float2 f = make_float2(1.f, 1.f);  // what the sums so far are multiplied by (nothing is there before the first score)
             struct {
                 bool x, y;
             } up{};
-#pragma unroll 1
-            for (int pass = 0;; ++pass) {
-                float2 top = make_float2(0.f, 0.f);
+            // a score past `high` comes first: p is 1 for the largest
+            const bool moved = __any_sync(0xffffffffu, mx.x > high.x || mx.y > high.y);
+            if (moved) {
 #pragma unroll
-                for (int k = 0; k < SETS; ++k) {
+                for (int s = LANES; s < 32; s <<= 1) {
+                    mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, s));
+                    mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, s));
+                }
+                up = {mx.x > high.x, mx.y > high.y};
+                auto raise = [](bool up, float mx, float qscale, float high, float& ref, float& adj, float& f) {
+                    if (!up) return;
+                    f = high == -INFINITY ? 0.f : ex2_approx(fmaf(ref - mx, qscale, -adj));
+                    ref = mx;
+                    adj = 0.f;
+                };
+                raise(up.x, mx.x, qscale.x, high.x, ref.x, adj.x, f.x);
+                raise(up.y, mx.y, qscale.y, high.y, ref.y, adj.y, f.y);
+            }
+            float2 top = make_float2(0.f, 0.f);
+            auto weigh = [&]() {
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        p[k][r] = make_float2(ex2_approx(fmaf(x[k][r].x, qscale.x, nm.x)), ex2_approx(fmaf(x[k][r].y, qscale.y, nm.y)));
+                for (int k = 0; k < SETS; ++k)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
 #pragma unroll
                         for (int c = 0; c < NG; ++c) {
                             const float sc = bf16_lo(sd[k][r][c]);
-                            wt[k][c][r] = make_float2(p[k][r].x * sc, p[k][r].y * sc);
+                            wt[k][c][r] = mul2(p[k][r], make_float2(sc, sc));
                         }
-                    }
+            };
 #pragma unroll
-                    for (int c = 0; c < NG; ++c) {
-                        top.x = fmax3(top.x, fabsf(wt[k][c][0].x), fabsf(wt[k][c][1].x));
-                        top.y = fmax3(top.y, fabsf(wt[k][c][0].y), fabsf(wt[k][c][1].y));
-                    }
+            for (int k = 0; k < SETS; ++k)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 a = fma2(add2(x[k][r], make_float2(-ref.x, -ref.y)), qscale, adj);
+                    p[k][r] = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                 }
-                if (pass == 2) break;
-                if (pass == 0) {
-                    if (!__any_sync(0xffffffffu, mx.x > high.x || mx.y > high.y || top.x > 32768.f || top.y > 32768.f)) break;
+            weigh();
 #pragma unroll
-                    for (int s = LANES; s < 32; s <<= 1) {
-                        mx.x = fmaxf(mx.x, __shfl_xor_sync(0xffffffffu, mx.x, s));
-                        mx.y = fmaxf(mx.y, __shfl_xor_sync(0xffffffffu, mx.y, s));
-                    }
-                    // scores first: p is 1 for the largest
-                    up = {mx.x > high.x, mx.y > high.y};
-                    if (up.x) nm.x = -mx.x * qscale.x;
-                    if (up.y) nm.y = -mx.y * qscale.y;
-                } else {
-                    // then the weights of V: the largest one to [2^13, 2^14), p at most 2^60
+            for (int k = 0; k < SETS; ++k)
 #pragma unroll
-                    for (int s = LANES; s < 32; s <<= 1) {
-                        top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, s));
-                        top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, s));
-                    }
-                    auto suit = [](float top, bool up, float& nm) {
-                        if (up || top > 32768.f) nm += (float)min(140 - (int)(__float_as_uint(top) >> 23), up ? 60 : 0);
-                    };
-                    suit(top.x, up.x, nm.x);
-                    suit(top.y, up.y, nm.y);
-                    // (nothing is there before the first score)
-                    const float2 f = make_float2(high.x == -INFINITY ? 0.f : ex2_approx(nm.x - was.x),
-                                                 high.y == -INFINITY ? 0.f : ex2_approx(nm.y - was.y));
-                    high = make_float2((75.f - nm.x) / qscale.x, (75.f - nm.y) / qscale.y);
-                    l = mul2(l, f);
+                for (int c = 0; c < NG; ++c) {
+                    top.x = fmax3(top.x, fabsf(wt[k][c][0].x), fabsf(wt[k][c][1].x));
+                    top.y = fmax3(top.y, fabsf(wt[k][c][0].y), fabsf(wt[k][c][1].y));
+                }
+            if (moved || __any_sync(0xffffffffu, top.x > 32768.f || top.y > 32768.f)) {
+                // then the weights of V: the largest one to [2^13, 2^14), p at most 2^60
 #pragma unroll
-                    for (int c = 0; c < NG; ++c) {
-                        z[c] = mul2(z[c], f);
+                for (int s = LANES; s < 32; s <<= 1) {
+                    top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, s));
+                    top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, s));
+                }
+                auto suit = [](float top, bool up) {
+                    return up || top > 32768.f ? (float)min(140 - (int)(__float_as_uint(top) >> 23), up ? 60 : 0) : 0.f;
+                };
+                const float2 more = make_float2(suit(top.x, up.x), suit(top.y, up.y));
+                const float2 by = make_float2(ex2_approx(more.x), ex2_approx(more.y));
+                adj = add2(adj, more);
+                f = mul2(f, by);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            o[c][q][0] *= f.x;
-                            o[c][q][1] *= f.y;
-                            o[c][q][2] *= f.x;
-                            o[c][q][3] *= f.y;
-                        }
+                for (int k = 0; k < SETS; ++k)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) p[k][r] = mul2(p[k][r], by);
+                weigh();
+                high = make_float2(ref.x + (75.f - adj.x) / qscale.x, ref.y + (75.f - adj.y) / qscale.y);
+                l = mul2(l, f);
+#pragma unroll
+                for (int c = 0; c < NG; ++c) {
+                    z[c] = mul2(z[c], f);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        o[c][q][0] *= f.x;
+                        o[c][q][1] *= f.y;
+                        o[c][q][2] *= f.x;
+                        o[c][q][3] *= f.y;
                     }
                 }
             }
@@ -703,28 +721,33 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
         const float* rec = reinterpret_cast<const float*>(p4_rings) + h * PITCH;
         const float* far = a.recs + (size_t)(cta0 + w1) * 2 * G * PITCH + h * PITCH;
-        float2 ml[P4_WARPS + 1];
-        float4 y[P4_WARPS + 1];
+        float4 st[P4_WARPS + 1], y[P4_WARPS + 1];  // reference, adjustment, scale of scores, sum of weights; sums
 #pragma unroll
         for (int w = 0; w < P4_WARPS; ++w) {
             const bool in = w >= w0 && w < w1;
-            ml[w] = in ? *reinterpret_cast<const float2*>(rec + w * STEP + DH) : make_float2(-INFINITY, 0.f);
+            st[w] = in ? *reinterpret_cast<const float4*>(rec + w * STEP + DH) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
             y[w] = in ? *reinterpret_cast<const float4*>(rec + w * STEP + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        ml[P4_WARPS] = make_float2(-INFINITY, 0.f);
+        st[P4_WARPS] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
         y[P4_WARPS] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (tail && whole) {
-            ml[P4_WARPS] = __ldcg(reinterpret_cast<const float2*>(far + DH));
+            st[P4_WARPS] = __ldcg(reinterpret_cast<const float4*>(far + DH));
             y[P4_WARPS] = __ldcg(reinterpret_cast<const float4*>(far + dd));
         }
-        float M = ml[0].x, L = 0.f;
+        const float scale = reinterpret_cast<const float*>(rec + w0 * STEP + DH)[2];
+        float R = st[0].x, E = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 1; w <= P4_WARPS; ++w) M = fmaxf(M, ml[w].x);  // (finite: a group has a piece)
+        for (int w = 1; w <= P4_WARPS; ++w) R = fmaxf(R, st[w].x);  // (finite: a group has a piece)
+#pragma unroll
+        for (int w = 0; w <= P4_WARPS; ++w) {  // 2^(what a piece's weights are above those with reference R and no adjustment)
+            st[w].x = st[w].x == -INFINITY ? -INFINITY : fmaf(st[w].x - R, scale, -st[w].y);
+            E = fmaxf(E, st[w].x);
+        }
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w <= P4_WARPS; ++w) {
-            const float f = ex2_approx(ml[w].x - M);
-            L = fmaf(ml[w].y, f, L);
+            const float f = ex2_approx(st[w].x - E);
+            L = fmaf(st[w].w, f, L);
             v = make_float4(fmaf(y[w].x, f, v.x), fmaf(y[w].y, f, v.y), fmaf(y[w].z, f, v.z), fmaf(y[w].w, f, v.w));
         }
         if (whole) {
@@ -735,7 +758,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         } else {
             float* dst = a.recs + ((size_t)(cta0 + w0) * 2 + 1) * G * PITCH + h * PITCH;
             *reinterpret_cast<float4*>(dst + dd) = v;
-            if (dd == 0) *reinterpret_cast<float2*>(dst + DH) = make_float2(M, L);
+            if (dd == 0) *reinterpret_cast<float4*>(dst + DH) = make_float4(R, -E, scale, L);
         }
     }
     // the (sequence, kv head) that goes on behind this CTA, if it began here
@@ -767,7 +790,7 @@ __global__ void __launch_bounds__(P4_JOIN_THREADS)
     attn_paged4_join_kernel(const P4Args a) {
     constexpr int PITCH = P4Layout<DH>::PITCH;
     __shared__ float4 part[P4_JOIN_THREADS];
-    __shared__ float2 stat[P4_JOIN_THREADS];
+    __shared__ float4 stat[P4_JOIN_THREADS];
     pdl_wait();
     pdl_trigger();
     const P4Desc d = a.desc[blockIdx.x];
@@ -784,42 +807,44 @@ __global__ void __launch_bounds__(P4_JOIN_THREADS)
         const int slot = i <= middle ? 1 : 0;
         return a.recs + ((size_t)w * 2 + slot) * G * PITCH + h * PITCH;
     };
-    float M = -INFINITY, L = 0.f;
+    float4 t = make_float4(-INFINITY, 0.f, 0.f, 0.f);  // reference (-inf: no record yet), adjustment, scale of scores, sum of weights
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float m, float l, const float4& y) {
-        if (m > M) {
-            const float f = ex2_approx(M - m);
-            L *= f;
-            v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-            M = m;
+    auto add = [&](const float4& s, const float4& y) {
+        // 2^(what the record's weights are above the sum's)
+        const float up = t.x == -INFINITY ? INFINITY : fmaf(s.x - t.x, s.z, t.y - s.y);
+        float f = 1.f;
+        if (up > 0.f) {
+            const float g = ex2_approx(-up);
+            t = make_float4(s.x, s.y, s.z, t.w * g);
+            v = make_float4(v.x * g, v.y * g, v.z * g, v.w * g);
+        } else {
+            f = ex2_approx(up);
         }
-        const float f = m == -INFINITY ? 0.f : ex2_approx(m - M);  // (-inf: a way without a record)
-        L = fmaf(l, f, L);
+        t.w = fmaf(s.w, f, t.w);
         v = make_float4(fmaf(y.x, f, v.x), fmaf(y.y, f, v.y), fmaf(y.z, f, v.z), fmaf(y.w, f, v.w));
     };
     if (way < ways) {
         constexpr int U = 4;  // records on their way at once
         for (int i0 = way; i0 < n; i0 += U * ways) {
-            float2 ml[U];
-            float4 y[U];
+            float4 s[U], y[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (i0 + u * ways < n) {
                     const float* rec = record(i0 + u * ways);
-                    ml[u] = __ldcg(reinterpret_cast<const float2*>(rec + DH));
+                    s[u] = __ldcg(reinterpret_cast<const float4*>(rec + DH));
                     y[u] = __ldcg(reinterpret_cast<const float4*>(rec + dd));
                 }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (i0 + u * ways < n) add(ml[u].x, ml[u].y, y[u]);
+                if (i0 + u * ways < n) add(s[u], y[u]);
         }
     }
     part[threadIdx.x] = v;
-    stat[threadIdx.x] = make_float2(M, L);
+    stat[threadIdx.x] = t;
     __syncthreads();
     if (way > 0) return;
-    for (int k = 1; k < min(ways, n); ++k) add(stat[k * quads + e].x, stat[k * quads + e].y, part[k * quads + e]);
-    const float inv = 1.f / L;
+    for (int k = 1; k < min(ways, n); ++k) add(stat[k * quads + e], part[k * quads + e]);
+    const float inv = 1.f / t.w;
     const size_t row = (size_t)(d.seg / a.Hkv) * a.Hq + (size_t)(d.seg % a.Hkv) * G + h;
     *reinterpret_cast<uint2*>(a.out + row * DH + dd) =
         make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));

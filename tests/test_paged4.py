@@ -437,7 +437,7 @@ def test_decode_long(bd, heads, lens, page):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("q_scale,spread", [(30.0, 1.0), (1e-6, 1.0), (1.0, 1e4), (1e10, 1e-10), (1.0, 1e-3)])
+@pytest.mark.parametrize("q_scale,spread", [(30.0, 1.0), (1e-6, 1.0), (1.0, 1e4), (1e10, 1e-10), (1.0, 1e-3), (1e8, 1.0)])
 def test_decode_sizes_of_values(bd, q_scale, spread):
     """Scores far apart, all alike, and values of other sizes."""
     heads, lens = (12, 4, 128), [300, 64]
