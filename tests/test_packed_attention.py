@@ -122,6 +122,19 @@ def test_long(bd, dh, longest):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scale", [1e-8, 300.0, 1e7])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_sizes_of_scores(bd, dh, scale):
+    lens = [200, 90]
+    q, k, v = _inputs((4, 2, dh), lens, lens, 5)
+    q = (q.float() * scale).to(torch.bfloat16)
+    q[3] = 0
+    out, err = _run(bd, q.cuda(), k.cuda(), v.cuda(), lens, lens, 200)
+    assert err == 0
+    _check(out, q, k, v, lens, lens)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("S", [1, 33, 2000])
 def test_many_sequences(bd, S):
     lens = [(i * 7919 + 5) % 23 for i in range(S)]
