@@ -95,11 +95,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-__device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -711,7 +706,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     constexpr int STEP = Ly::RING / 4;  // floats from one warp's piece to the next
     const int team = team_of(all_units());  // (again: not held through the loop)
     const int cta0 = blockIdx.x * team, here = max(0, min(team, warps - cta0));  // warps with a run
-    for (int e0 = threadIdx.x; e0 < P4_WARPS * quads; e0 += P4_THREADS) {
+    for (int e0 = threadIdx.x; e0 < here * quads; e0 += P4_THREADS) {
         const int w0 = p4_div(e0, quads), e = e0 - w0 * quads, s = seg_sh[w0];
         if (s < 0 || (w0 > 0 && seg_sh[w0 - 1] == s)) continue;
         int w1 = w0 + 1;
@@ -721,34 +716,51 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         const int h = e / (DH / 4), dd = e % (DH / 4) * 4;
         const float* rec = reinterpret_cast<const float*>(p4_rings) + h * PITCH;
         const float* far = a.recs + (size_t)(cta0 + w1) * 2 * G * PITCH + h * PITCH;
-        float4 st[P4_WARPS + 1], y[P4_WARPS + 1];  // reference, adjustment, scale of scores, sum of weights; sums
-#pragma unroll
-        for (int w = 0; w < P4_WARPS; ++w) {
-            const bool in = w >= w0 && w < w1;
-            st[w] = in ? *reinterpret_cast<const float4*>(rec + w * STEP + DH) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-            y[w] = in ? *reinterpret_cast<const float4*>(rec + w * STEP + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        st[P4_WARPS] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-        y[P4_WARPS] = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 far_st = make_float4(-INFINITY, 0.f, 0.f, 0.f), far_y = make_float4(0.f, 0.f, 0.f, 0.f);
         if (tail && whole) {
-            st[P4_WARPS] = __ldcg(reinterpret_cast<const float4*>(far + DH));
-            y[P4_WARPS] = __ldcg(reinterpret_cast<const float4*>(far + dd));
+            far_st = __ldcg(reinterpret_cast<const float4*>(far + DH));
+            far_y = __ldcg(reinterpret_cast<const float4*>(far + dd));
         }
+        // the joined piece so far: reference R (that of the largest scores), E: its weights are 2^E above those of R without adjustment
         const float scale = reinterpret_cast<const float*>(rec + w0 * STEP + DH)[2];
-        float R = st[0].x, E = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int w = 1; w <= P4_WARPS; ++w) R = fmaxf(R, st[w].x);  // (finite: a group has a piece)
-#pragma unroll
-        for (int w = 0; w <= P4_WARPS; ++w) {  // 2^(what a piece's weights are above those with reference R and no adjustment)
-            st[w].x = st[w].x == -INFINITY ? -INFINITY : fmaf(st[w].x - R, scale, -st[w].y);
-            E = fmaxf(E, st[w].x);
-        }
+        float R = -INFINITY, E = -INFINITY, L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto join = [&](auto& st, auto& y) {  // (a reference of -inf: no piece)
+            constexpr int N = sizeof(st) / sizeof(st[0]);
+            float top = R;
 #pragma unroll
-        for (int w = 0; w <= P4_WARPS; ++w) {
-            const float f = ex2_approx(st[w].x - E);
-            L = fmaf(st[w].w, f, L);
-            v = make_float4(fmaf(y[w].x, f, v.x), fmaf(y[w].y, f, v.y), fmaf(y[w].z, f, v.z), fmaf(y[w].w, f, v.w));
+            for (int k = 0; k < N; ++k) top = fmaxf(top, st[k].x);
+            const float was = R == -INFINITY ? -INFINITY : fmaf(R - top, scale, E);
+            R = top;
+            E = was;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                st[k].x = st[k].x == -INFINITY ? -INFINITY : fmaf(st[k].x - R, scale, -st[k].y);
+                E = fmaxf(E, st[k].x);
+            }
+            const float g = was == -INFINITY ? 0.f : ex2_approx(was - E);
+            L *= g;
+            v = make_float4(v.x * g, v.y * g, v.z * g, v.w * g);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const float f = ex2_approx(st[k].x - E);
+                L = fmaf(st[k].w, f, L);
+                v = make_float4(fmaf(y[k].x, f, v.x), fmaf(y[k].y, f, v.y), fmaf(y[k].z, f, v.z), fmaf(y[k].w, f, v.w));
+            }
+        };
+#pragma unroll 1
+        for (int w = w0; w < w1; w += 4) {  // four pieces' loads at once
+            float4 st[4], y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                st[k] = w + k < w1 ? *reinterpret_cast<const float4*>(rec + (w + k) * STEP + DH) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+                y[k] = w + k < w1 ? *reinterpret_cast<const float4*>(rec + (w + k) * STEP + dd) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            join(st, y);
+        }
+        if (tail && whole) {
+            float4 st[1] = {far_st}, y[1] = {far_y};
+            join(st, y);
         }
         if (whole) {
             const float inv = 1.f / L;
@@ -773,7 +785,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 const int end = x0 + mine + p4_units(max(keys_left, 0)), longer = more * (len + 1);
                 d.seg = s;
                 d.first = cta0 + w0;
-                d.last = end <= longer ? (end - 1) / (len + 1) : more + (end - 1 - longer) / len;
+                d.last = end <= longer ? p4_div(end - 1, len + 1) : more + p4_div(end - 1 - longer, len);
                 d.last_slot = (d.last + 1) * len + min(d.last + 1, more) == end ? 1 : 0;
             }
         }
