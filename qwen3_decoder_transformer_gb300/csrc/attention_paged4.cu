@@ -34,11 +34,11 @@ namespace {
 //
 // What bounds it: many keys, HBM (16 sequences of up to 32,768 keys, 32 / 8 heads of 128: 86 us, 6.1 TB/s, of which some 8 us are
 // start and end). In the loop a unit of each of an SM's 12 warps takes 4,000 cycles, 28 bytes a cycle and SM, which is the
-// copy rate, with the issue slots half full. Few keys: the chain of one unit. 1 sequence of 4096: 9.5 us; counting
-// the lengths 0.6, finding the run 0.5, the query 1, one unit 2.1, the pieces 1.4, and the rest two launches and
+// copy rate, with the issue slots half full. Few keys: the chain of one unit. 1 sequence of 4096: 9.1 us; counting
+// the lengths 0.6, finding the run 0.5, the query 1, one unit 2.1, the pieces 1.2, and the rest two launches and
 // the records' way through the workspace.
 // Split: one CTA of 12 warps an SM, as many rings as shared memory holds, joins the pieces of 12 runs before they leave the SM (16 @
-// 32,768 two CTAs of six 90.3 us, one of twelve 85.7; 64 sequences of up to 4096 keys, 16 / 8 heads, 45.6 and 44.9).
+// 32,768 two CTAs of six 90.3 us, one of twelve 85.7, when it was changed; 64 @ 4096, 16 / 8 heads, 45.6 and 44.9).
 constexpr int P4_STEP = 64, P4_TILES = P4_STEP / 16;  // keys that a warp takes at once
 constexpr int P4_WARPS = 12, P4_THREADS = 32 * P4_WARPS, P4_CTAS = 1, P4_MAX_G = 8;
 constexpr int P4_STRIPS = P4_THREADS;  // strips of sequences whose units are counted at the start
