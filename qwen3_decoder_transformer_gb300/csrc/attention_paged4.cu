@@ -5,6 +5,7 @@
 #include "internal.h"
 #include "paged4.cuh"
 #include "rings.h"
+#include "runs.h"
 
 namespace q3 {
 namespace {
@@ -780,13 +781,13 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         if (s >= 0 && !(whole_sh[warp] & 2)) {
             int w0 = warp;
             while (w0 > 0 && seg_sh[w0 - 1] == s) --w0;
-            if (whole_sh[w0] & 1) {
-                // the unit behind it, the warp whose run holds the one before, and whether that run goes on
-                const int end = x0 + mine + p4_units(max(keys_left, 0)), longer = more * (len + 1);
+            const RunEnd end = run_of_end(x0 + mine, p4_units(max(keys_left, 0)), len, more, *abort_flag != 0,
+                                          [](int n, int d) { return p4_div(n, d); });
+            if ((whole_sh[w0] & 1) && end.run >= 0) {
                 d.seg = s;
                 d.first = cta0 + w0;
-                d.last = end <= longer ? p4_div(end - 1, len + 1) : more + p4_div(end - 1 - longer, len);
-                d.last_slot = (d.last + 1) * len + min(d.last + 1, more) == end ? 1 : 0;
+                d.last = end.run;
+                d.last_slot = end.with_run ? 1 : 0;
             }
         }
         a.desc[blockIdx.x] = d;
