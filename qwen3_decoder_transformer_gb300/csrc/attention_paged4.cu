@@ -20,7 +20,10 @@ namespace {
 //   next nibble code * 2^-20, exact on the tensor cores (K: its query value is divided by 16; V: output rows of its own).
 //   q is scaled by a power of two for each head so that its fp16 form is exact (its largest value lies in [2^10, 2^11)). V's
 //   weights p * scale are rounded to fp16, off by 2^-11 of themselves at most: a power of two for each head keeps the largest
-//   weight of the run so far in [2^13, 2^15], so what falls below fp16's normal range is less than 2^-25 of that.
+//   weight of the run so far in [2^13, 2^15], so what falls below fp16's normal range is less than 2^-25 of that. p itself
+//   takes 2^60 of it at most, as its sums have to stay in fp32's range; where scales below 2^-47 need more, the weights of
+//   each step are lifted by a power of two of their own, up to 2^86, and the sums with them (without it, scales below 2^-85
+//   left nothing of the codes).
 //   (bf16 weights, with codes as 128 + code and the offset taken off again, left 0.5-1.2% of error on long sequences against
 //   0.2%: a rounding of 2^-8 multiplies codes of one sign, and the tensor cores cut their sums off. e4m3 operands would halve
 //   the conversions, but the warp-level fp8 product takes several times the fp16 one's cycles on this chip.)
@@ -53,7 +56,7 @@ struct P4Layout {
     static constexpr int PITCH = DH + 4;  // floats of a head's piece: sums; reference, adjustment, scale of scores, sum of weights
     static constexpr int SMEM = P4_WARPS * RING;
     static_assert(P4_MAX_G * PITCH * 4 <= RING, "a piece fits a ring");
-    static_assert(P4_CTAS * (SMEM + 4096) <= 227 * 1024, "shared memory");
+    static_assert(P4_CTAS * (SMEM + 4608) <= 227 * 1024, "shared memory");
 };
 
 // A (sequence, kv head) that begins, but does not end, in a CTA's runs: its number (-1: none), the warp whose run holds its
@@ -151,6 +154,7 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     __shared__ int strip_keys[P4_STRIPS];  // keys of the strip's (last) sequence
     __shared__ int warp_sum[P4_WARPS];
     __shared__ int seg_sh[P4_WARPS], whole_sh[P4_WARPS];
+    __shared__ float2 lift_sh[P4_WARPS][4];  // [warp][pair of heads]: exponents of the lifts (every lane reads what it wrote)
     __shared__ int abort_sh;
     volatile int* abort_flag = &abort_sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -290,9 +294,10 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     float2 qs[NG], qscale;     // heads ch, ch + 1: sums of the scaled queries over a group of dims; what scores are scaled by
     // Weights p = 2^((score - ref) * qscale + adj) and p * scale, which has to fit fp16: ref is a score, and adj a whole number
     // chosen so that the largest p * scale of the run so far lies in [2^13, 2^15] (p itself below 2^75: a score past `high` is
-    // looked at first). In one number the two lose adj where scores are large.
+    // looked at first). In one number the two lose adj where scores are large. adj is 60 where it should be more: then the
+    // weights are lifted; and 61 as long as all of them were 0.
     float2 ref, adj, high, l;
-    float o[NG][4][4];  // sums of weight * code, in units of 2^-24 (tiles 1 and 3 of a group: 2^-20)
+    float o[NG][4][4];  // sums of weight * code (with its lift), in units of 2^-24 (tiles 1 and 3 of a group: 2^-20)
     float2 z[NG];       // sums of weight * minimum
     auto fetch_q = [&]() {
         const __nv_bfloat16* row = a.q + ((size_t)use.b * a.Hq + (size_t)use.h * a.G + qh) * DH + 16 * t;
@@ -360,19 +365,34 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
         }
         l = make_float2(0.f, 0.f);
         ref = adj = make_float2(0.f, 0.f);
+        lift_sh[warp][t & (LANES - 1)] = make_float2(0.f, 0.f);
         high = make_float2(-INFINITY, -INFINITY);  // the first score moves it
     };
+    float2 down;  // what takes the lifts off
     // the sums of this warp's piece: dims c * 64 + 8 g + (0..7) of head ch + e
     auto piece = [&](int c, int e, float (&v)[8]) {
         const float add = e ? z[c].y : z[c].x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float u = i & 1 ? 1048576.f : 16777216.f;
+            const float u = (i & 1 ? 1048576.f : 16777216.f) * (e ? down.y : down.x);
             v[i] = fmaf(o[c][i][e], u, add);
             v[4 + i] = fmaf(o[c][i][2 + e], u, add);
         }
     };
+    auto rescale = [&](float2 f) {
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                o[c][q][0] *= f.x;
+                o[c][q][1] *= f.y;
+                o[c][q][2] *= f.x;
+                o[c][q][3] *= f.y;
+            }
+    };
     auto total = [&]() {  // sums over the keys that other lanes took
+        const float2 lift = lift_sh[warp][t & (LANES - 1)];
+        down = make_float2(ex2_approx(-lift.x), ex2_approx(-lift.y));
 #pragma unroll
         for (int s = LANES; s < 32; s <<= 1) {
             l.x += __shfl_xor_sync(0xffffffffu, l.x, s);
@@ -594,19 +614,21 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                     top.x = fmax3(top.x, fabsf(wt[k][c][0].x), fabsf(wt[k][c][1].x));
                     top.y = fmax3(top.y, fabsf(wt[k][c][0].y), fabsf(wt[k][c][1].y));
                 }
-            if (moved || __any_sync(0xffffffffu, top.x > 32768.f || top.y > 32768.f)) {
+            if (moved || __any_sync(0xffffffffu, top.x > (adj.x >= 60.f ? 0.f : 32768.f) || top.y > (adj.y >= 60.f ? 0.f : 32768.f))) {
                 // then the weights of V: the largest one to [2^13, 2^14), p at most 2^60
 #pragma unroll
                 for (int s = LANES; s < 32; s <<= 1) {
                     top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, s));
                     top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, s));
                 }
-                auto suit = [](float top, bool up) {
-                    return up || top > 32768.f ? (float)min(140 - (int)(__float_as_uint(top) >> 23), up ? 60 : 0) : 0.f;
+                auto suit = [](float top, bool up, float adj) {
+                    const int e = (int)(__float_as_uint(top) >> 23);
+                    return up || top > (adj == 61.f ? 0.f : 32768.f) ? fminf((float)(140 - e), (top > 0.f ? 60.f : 61.f) - adj) : 0.f;
                 };
-                const float2 more = make_float2(suit(top.x, up.x), suit(top.y, up.y));
+                const float2 more = make_float2(suit(top.x, up.x, adj.x), suit(top.y, up.y, adj.y));
                 const float2 by = make_float2(ex2_approx(more.x), ex2_approx(more.y));
                 adj = add2(adj, more);
+                const float2 was = lift_sh[warp][t & (LANES - 1)];
                 f = mul2(f, by);
 #pragma unroll
                 for (int k = 0; k < SETS; ++k)
@@ -616,16 +638,24 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
                 high = make_float2(ref.x + (75.f - adj.x) / qscale.x, ref.y + (75.f - adj.y) / qscale.y);
                 l = mul2(l, f);
 #pragma unroll
-                for (int c = 0; c < NG; ++c) {
-                    z[c] = mul2(z[c], f);
+                for (int c = 0; c < NG; ++c) z[c] = mul2(z[c], f);
+                if (fmaxf(adj.x, adj.y) >= 60.f || was.x + was.y > 0.f) {
+                    // the lifts of this part of the step (weights take them after the scale: p and the lift alone may overflow)
+                    auto lift_of = [](float top, float adj) {
+                        return adj == 60.f ? (float)min(max(140 - (int)(__float_as_uint(top) >> 23), 0), 86) : 0.f;
+                    };
+                    const float2 lift = make_float2(lift_of(top.x * by.x, adj.x), lift_of(top.y * by.y, adj.y));
+                    const float2 up_by = make_float2(ex2_approx(lift.x), ex2_approx(lift.y));
+                    lift_sh[warp][t & (LANES - 1)] = lift;
+                    f = mul2(f, make_float2(ex2_approx(lift.x - was.x), ex2_approx(lift.y - was.y)));
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        o[c][q][0] *= f.x;
-                        o[c][q][1] *= f.y;
-                        o[c][q][2] *= f.x;
-                        o[c][q][3] *= f.y;
-                    }
+                    for (int k = 0; k < SETS; ++k)
+#pragma unroll
+                        for (int c = 0; c < NG; ++c)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) wt[k][c][r] = mul2(wt[k][c][r], up_by);
                 }
+                rescale(f);
             }
             uint32_t wb[SETS][NG][2];  // P^T fragments
 #pragma unroll

@@ -450,6 +450,78 @@ def test_decode_sizes_of_values(bd, q_scale, spread):
     _check_decode(out, q, c, lens)
 
 
+def _smaller_values(c, powers):
+    """Multiply the scales and minima of V by 2^-powers[s] (exact), s: the slot, of every sequence."""
+    host = c.v.cpu()
+    side = host[:, :, c.page * c.dh // 2:].view(torch.bfloat16).view(*host.shape[:2], c.page, c.dh // 64, 2)
+    s = np.arange(len(powers))
+    by = torch.from_numpy(2.0 ** -np.asarray(powers, dtype=np.float64)).float()
+    for b in range(c.table.shape[0]):
+        have = c.table[b, s // c.page] < 2 ** 30
+        at, off = torch.from_numpy(c.table[b, s // c.page][have]).long(), torch.from_numpy((s % c.page)[have])
+        side[at, :, off] = (side[at, :, off].float() * by[torch.from_numpy(have)][:, None, None, None]).to(torch.bfloat16)
+    c.v.copy_(host)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [(16, 8, 128), (12, 4, 64), (8, 1, 128)], ids=str)
+@pytest.mark.parametrize("power", [45, 50, 62, 75, 84, 86, 100, 114])
+@pytest.mark.parametrize("q_scale", [1.0, 30.0])
+def test_decode_small_values(bd, heads, power, q_scale):
+    """Values down to 2^-114: their codes count as those of any other size do, also where scores far above the ones before come."""
+    Hq, Hkv, dh = heads
+    lens = [700, 64, 3]
+    c = Cache(Hkv, dh, 16, lens, 21).fill(lens, 21)
+    _smaller_values(c, [power] * 700)
+    q = (torch.randn(3, Hq, dh, generator=torch.Generator().manual_seed(21)) * q_scale).to(torch.bfloat16)
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    _check_decode(out, q, c, lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("step", [0.01, 0.1])
+def test_decode_small_values_and_rising_scores(bd, step):
+    """Small values whose scores grow along the sequence, past the running maximum in every unit or past its range."""
+    c = Cache(2, 64, 64, [2048], 23).fill([2048], 23)
+    _smaller_values(c, [90] * 2048)
+    host = c.k.cpu()
+    side = host[:, :, 64 * 32:].view(torch.bfloat16).view(*host.shape[:2], 64, 2)
+    s = np.arange(2048)
+    at, off = torch.from_numpy(c.table[0, s // 64]).long(), torch.from_numpy(s % 64)
+    side[at, :, off, 1] = (torch.from_numpy(s).float() * step).to(torch.bfloat16)[:, None].expand(-1, 2)
+    c.k.copy_(host)
+    q = torch.full((1, 8, 64), 0.5).to(torch.bfloat16)
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([2047], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    _check_decode(out, q, c, [2048])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("order", ["falling", "rising", "one large", "one large, unseen", "zeros first"])
+@pytest.mark.parametrize("heads", [(16, 8, 128), (12, 4, 64), (8, 1, 128)], ids=str)
+def test_decode_values_of_many_sizes(bd, heads, order):
+    """Values whose sizes change along a sequence by up to 2^110, and a key of large values that some heads' scores leave nothing of."""
+    Hq, Hkv, dh = heads
+    n = 900
+    c = Cache(Hkv, dh, 64, [n], 22).fill([n], 22)
+    s = np.arange(n)
+    powers = {"falling": s * 110 // n, "rising": 110 - s * 110 // n, "zeros first": np.where(s < 200, 1000, 90)}.get(
+        order, np.where(s == 450, 0, 90))
+    _smaller_values(c, powers)
+    q = torch.randn(1, Hq, dh, generator=torch.Generator().manual_seed(22)).to(torch.bfloat16)
+    if order == "one large, unseen":  # key 450 is -30 in every dim: scores of -300 and less for a positive query
+        host = c.k.cpu()
+        side = host[:, :, 64 * dh // 2:].view(torch.bfloat16).view(*host.shape[:2], 64, dh // 64, 2)
+        side[int(c.table[0, 7]), :, 2, :, 0], side[int(c.table[0, 7]), :, 2, :, 1] = 0.0, -30.0
+        c.k.copy_(host)
+        q[0, ::2] = 1.25
+        q[0, ::2, ::3] = 0.5
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([n - 1], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    _check_decode(out, q, c, [n])
+
+
 @pytest.mark.gpu
 def test_decode_rising_scores(bd):
     """Keys that grow along the sequence: the running maximum moves in every unit."""
