@@ -418,8 +418,9 @@ QWEN3_API size_t qwen3_paged4_page_bytes(int page_size, int dh);
  * elements apart (a multiple of 8); d_cos_sin [n_pos, dh] as qwen3_op_rope_table writes it.
  * Unlike qwen3_op_qknorm_rope_append, which rounds where the pages' bf16 model does, everything is fp32 and rounded
  * once at the end. For each 64 dims: minimum = the least value rounded down to bf16, scale = (largest - minimum) / 15 rounded up
- * to bf16, code = the nearest of 0..15 (even on ties), all from the unrounded fp32 values: a cached value is off by half a
- * scale at most. 64 dims that hold a NaN or an infinity become NaN.
+ * to bf16, code = the nearest of 0..15 (even on ties) to (value - minimum) / scale, all from the unrounded fp32 values and their
+ * fp32 differences: a cached value is off by half a scale at most, and the differences' rounding (2^-24 of them). 64 dims that
+ * hold a NaN or an infinity, or span more than fp32 does, become NaN.
  * A row without a page (bit 4) still gets its outputs; one without a position gets none. Two rows of a call must not go to
  * the same place of the same page. d_q_out and d_k_out may not overlap d_qkv. All tensors 16-byte aligned. */
 QWEN3_API int qwen3_op_append_paged4(const void* d_qkv, int64_t ld, int N, const int* d_cu, const int* d_start, int S, int Hq,

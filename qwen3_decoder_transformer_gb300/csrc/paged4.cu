@@ -83,10 +83,12 @@ __device__ __forceinline__ uint32_t side_of(float mn, float mx) {
     return (uint32_t)__bfloat16_as_ushort(sc) | (uint32_t)__bfloat16_as_ushort(lo) << 16;
 }
 
-// The codes of eight values, the first one in the lowest nibble: the whole number nearest to q = (x - minimum) / scale, the even
-// one of a tie, without a division a value: q is bracketed by products with floats below and above 1 / scale, each rounded
-// to a whole number by one fused multiply-add. Where they agree that is the code; where they do not, q is a tie (of
-// bf16 values there are many) and the even one of the two is meant. (A quotient within 2^-20 of a tie counts as one.)
+// The codes of eight values, the first one in the lowest nibble: the whole number nearest to (x - minimum) / scale, the even one
+// of a tie (of bf16 values there are many), with the difference d = x - minimum in fp32. Without a division a value: d times a float just
+// below 1 / scale, rounded to a whole number by one fused multiply-add, is that code or the one before it; the middle between
+// the two, (code + 1/2) scale, is exact, so the sign of what d has over it tells which. (Quotients bracketed by two
+// products, those that end at different codes taken for ties, saved 2 us of these 164, and took quotients within 2^-20 of
+// a tie for one.)
 __device__ __forceinline__ uint32_t codes_of(const float2 (&x)[4], uint32_t side) {
     const float scale = bf16_lo(side), low = bf16_hi(side);
     // scale 0 (all values alike), NaN, and scales whose reciprocal is no normal float: one by one
@@ -95,23 +97,37 @@ __device__ __forceinline__ uint32_t codes_of(const float2 (&x)[4], uint32_t side
         if (scale > 0.f)
             for (int i = 0; i < 8; ++i) {
                 const float d = __fsub_rn(i & 1 ? x[i / 2].y : x[i / 2].x, low);
-                c |= (uint32_t)min(__float2int_rn(__fdiv_rn(d, scale)), 15) << (4 * i);
+                int y = max(__float2int_rn(__fdiv_rn(d, scale)) - 1, 0);  // a rounded quotient's code may be off by one
+                for (int k = 0; k < 2; ++k) {
+                    const float over = __fsub_rn(d, ((float)y + 0.5f) * scale);
+                    y += over > 0.f || (over == 0.f && (y & 1));
+                }
+                c |= (uint32_t)min(y, 15) << (4 * i);
             }
         return c;
     }
     const uint32_t inv = __float_as_uint(rcp_approx(scale));  // off by one unit in the last place at most
-    const float below = __uint_as_float(inv - 2), above = __uint_as_float(inv + 2);
+    const float below = __uint_as_float(inv - 2);
     constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number, in the lowest bits
-    const float2 whole = make_float2(kWhole, kWhole), b2 = make_float2(below, below), a2 = make_float2(above, above);
+    const float2 whole = make_float2(kWhole, kWhole), b2 = make_float2(below, below), s2 = make_float2(-scale, -scale),
+                 h2 = make_float2(-0.5f * scale, -0.5f * scale);
     uint32_t c = 0;
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
-        const float2 d = add2(x[i], make_float2(-low, -low)), q0 = fma2(d, b2, whole), q1 = fma2(d, a2, whole);
-        const uint32_t y0 = __float_as_uint(q0.y), x0 = __float_as_uint(q0.x);
-        c = c * 16u + y0 + ((__float_as_uint(q1.y) - y0) & y0);  // (the difference is 0 or 1: the odd one of two goes up)
-        c = c * 16u + x0 + ((__float_as_uint(q1.x) - x0) & x0);
+        const float2 d = add2(x[i], make_float2(-low, -low)), q = fma2(d, b2, whole);
+        const float2 over = add2(d, fma2(add2(q, make_float2(-kWhole, -kWhole)), s2, h2));
+        // y if the next code is meant (over > 0, or 0 and y odd: its bits, less 1 where y is even, have no sign; 0 is never negative
+        // here), else y - 1. (The shift in PTX: from C++ nvcc 13.0 made code that added nibbles in the wrong places. With
+        // comparisons of floats 32,768 tokens and their read take 168 us, so 164.)
+        auto next = [](uint32_t y, float over) {
+            uint32_t stays;
+            asm("shr.u32 %0, %1, 31;" : "=r"(stays) : "r"(__float_as_uint(over) + (y & 1u) - 1u));
+            return y - stays;
+        };
+        c = c * 16u + next(__float_as_uint(q.y), over.y);
+        c = c * 16u + next(__float_as_uint(q.x), over.x);
     }
-    return c - 0x11111111u * 0x4b400000u;  // every code carries the bits of kWhole
+    return c - 0x11111111u * (0x4b400000u - 1u);  // every code carries the bits of kWhole, and is one short
 }
 
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {

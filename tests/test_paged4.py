@@ -271,6 +271,27 @@ def test_append_values_at_the_edges(bd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dh", [64, 128])
+def test_append_quotients_beside_a_tie(bd, dh):
+    """Values less than 2^-20 of a scale on either side of the middle between two codes take the nearer code, those in the middle the
+    even one. The differences to the minimum are exact in fp32, and the scale is 2."""
+    lows = [-1.0, -3.0, -5.0, -15.0]  # 0 lies in the middle of codes 0 and 1, 1 and 2, 2 and 3, 7 and 8
+    x = torch.zeros(len(lows), 3 * dh, dtype=torch.bfloat16)
+    v = x[:, 2 * dh:].view(len(lows), dh // 64, 64)
+    for i, low in enumerate(lows):
+        step = 2.0 ** (np.floor(np.log2(-low)) - 23)  # of fp32 at the difference
+        v[i, :, 0], v[i, :, 1] = low, low + 30
+        for j, d in enumerate((1, -1, 2, -2, 3, -3, 4, -4)):
+            v[i, :, 2 + j] = d * step
+    r = _append(bd, (1, 1, dh), 16, [len(lows)], [0], norm=False, qkv=x)
+    codes, scale, low = _unpack(r["cache"].v.cpu(), 16, dh)
+    at = r["cache"].table[0, 0]
+    assert np.all(scale[at, 0, :len(lows)] == 2) and np.all(low[at, 0, :len(lows)] == np.array(lows)[:, None])
+    q = (v.double().numpy() - np.array(lows)[:, None, None]) / 2  # exact
+    assert np.array_equal(codes[at, 0, :len(lows)].reshape(q.shape), np.rint(q))
+
+
+@pytest.mark.gpu
 def test_append_flags_what_it_cannot_place(bd):
     heads, lens = (8, 4, 64), [4, 4, 4, 4]
     ref = _append(bd, heads, 16, lens, [14, 3, 5, 9], seed=5, n_pos=64)
