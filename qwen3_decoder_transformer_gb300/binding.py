@@ -13,7 +13,7 @@ import os
 import numpy as np
 import torch
 
-from .build import LIB, TENSORS
+from .build import LIB, tensors_path
 
 _vp = ctypes.c_void_p
 _i32p = ctypes.POINTER(ctypes.c_int)
@@ -608,9 +608,10 @@ _PAGE_OF = {(p * (dh // 2 + dh // 16), dh): p for p in PAGE_SIZES for dh in (64,
 def _checks():
     global _tensors
     if _tensors is None:
-        if not os.path.exists(TENSORS):
-            raise RuntimeError(f"extension not built ({TENSORS}); run __graft_entry__.build() first")
-        loader = importlib.machinery.ExtensionFileLoader("_tensors", TENSORS)
+        path = tensors_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"extension not built for this PyTorch and Python ({path}); run __graft_entry__.build() first")
+        loader = importlib.machinery.ExtensionFileLoader("_tensors", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensors", loader))
         loader.exec_module(module)
         _tensors = module
