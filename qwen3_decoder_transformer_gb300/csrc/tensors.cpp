@@ -184,8 +184,10 @@ PyObject* attention_decode_paged4(PyObject* const* o) {
 PyObject* attention_prefill_packed(PyObject* const* o) {
     Call c{device_of(o[0])};
     qwen3_attention_prefill_packed_args a{};
-    const long longest = PyLong_AsLong(o[4]);
+    int past = 0;  // of a whole number past 64 bits: its sign
+    long long longest = PyLong_AsLongLongAndOverflow(o[4], &past);
     if (PyErr_Occurred()) return nullptr;
+    if (past) longest = past < 0 ? 0 : std::numeric_limits<int32_t>::max();
     const at::Tensor *q = c.tensor(o[0], 3), *k = c.tensor(o[1], 3), *v = c.tensor(o[2], 3);
     if (!c.ok) Py_RETURN_NONE;
     const int64_t Nq = q->size(0), Hq = q->size(1), dh = q->size(2), Nk = k->size(0), Hkv = k->size(1);
@@ -205,7 +207,7 @@ PyObject* attention_prefill_packed(PyObject* const* o) {
     a.Hkv = c.i32(Hkv);
     a.dh = c.i32(dh);
     a.d_plan = c.scratch(o[3], a.plan_bytes);
-    a.longest = (int32_t)std::min<long>(std::max<long>(longest, 0), std::numeric_limits<int32_t>::max());  // (any value is right)
+    a.longest = (int32_t)std::clamp<long long>(longest, 0, std::numeric_limits<int32_t>::max());  // (any value is right)
     a.d_out = c.dense(o[5], at::kBFloat16, {Nq, Hq * dh});
     a.d_err = (int*)c.dense_or_none(o[6], at::kInt, {1});
     return block(c, Nq > 0, a);

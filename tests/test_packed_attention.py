@@ -441,3 +441,12 @@ def test_binding_refuses(bd):
                    dict(out=base["out"].float()), dict(plan=None), dict(err=torch.zeros(1)), {}):
         with pytest.raises(ValueError):
             bd.op_attention_prefill_packed(**{**base, **change})
+
+
+@pytest.mark.parametrize("longest,field", [(-5, 0), (0, 0), (77, 77), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                           (2 ** 63, 2 ** 31 - 1), (-2 ** 70, 0), (2 ** 200, 2 ** 31 - 1)])
+def test_longest_is_any_whole_number(bd, longest, field):
+    """A hint: what passes the field is its limit."""
+    q, out = torch.zeros(3, 8, 64, dtype=torch.bfloat16), torch.zeros(3, 512, dtype=torch.bfloat16)
+    block = bd._checks().attention_prefill_packed(q, q, q, torch.zeros(4096, dtype=torch.uint8), longest, out, None)
+    assert int.from_bytes(block[88:92], "little") == field
