@@ -208,6 +208,56 @@ def test_large_groups(bd, heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("longest", FORMS[:2])
+@pytest.mark.parametrize("heads", [(16, 8, 128), (32, 8, 128), (8, 8, 64)], ids=str)
+def test_many_items_a_cta(bd, heads, longest):
+    """Ten and more tiles a CTA with one to three key tiles each, and histories in front of some: every accumulator, stage of Q and
+    list of sums is used again and again."""
+    lq = [300 - (i * 37) % 90 for i in range(24)] + [128, 1, 0, 257]
+    lk = [n + (i % 3) * 60 for i, n in enumerate(lq)]
+    q, k, v = _inputs(heads, lq, lk, heads[0] + longest, tail=3)
+    out, err = _run(bd, q.cuda(), k.cuda(), v.cuda(), lq, lk, longest)
+    assert err == 0
+    _check(out, q, k, v, lq, lk)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,S,n,longest", [((32, 8, 128), 1100, 20, 4096), ((8, 8, 128), 10500, 3, 1), ((8, 8, 64), 10500, 3, 1),
+                                               ((8, 8, 64), 10500, 2, 4096)], ids=str)
+def test_more_items_than_are_looked_up_at_the_start(bd, heads, S, n, longest):
+    """More tiles a CTA than its table holds (48 in the long form at head_dim 128, 512 otherwise; 152 CTAs): the others are found
+    one by one. Sequences of one length, so that the reference takes them all at once."""
+    Hq, Hkv, dh = heads
+    lens = [n] * S
+    q, k, v = _inputs(heads, lens, lens, S + n, tail=2)
+    out, err = _run(bd, q.cuda(), k.cuda(), v.cuda(), lens, lens, longest)
+    assert err == 0 and torch.all(out[S * n:] == 7.0)
+    a = q[:S * n].cuda().double().view(S, n, Hkv, Hq // Hkv, dh)
+    b, w = (t[:S * n].cuda().double().view(S, n, Hkv, dh) for t in (k, v))
+    x = torch.einsum("sihgd,sjhd->shgij", a, b) / dh ** 0.5
+    size = (torch.einsum("sihgd,sjhd->shgij", a.abs(), b.abs()).tril() / dh ** 0.5).amax(dim=(3, 4))
+    x.masked_fill_(torch.ones(n, n, device="cuda").triu(1).bool(), float("-inf"))
+    p = torch.softmax(x, dim=-1)
+    ref, weighted = (torch.einsum("shgij,sjhd->sihgd", p, t) for t in (w, w.abs()))
+    # (the bound of _ref)
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -13 * (1 + 2.0 ** -4 * size))[:, None, :, :, None] * weighted
+    assert torch.all((out[:S * n].double().view(ref.shape) - ref).abs() <= tol)
+
+
+@pytest.mark.gpu
+def test_one_long_prompt(bd):
+    """A prompt of 40,000 tokens (66 tiles a CTA, up to 313 key tiles each), on sampled rows."""
+    n, Hq, Hkv, dh = 40000, 32, 8, 128
+    gen = torch.Generator(device="cuda").manual_seed(40)
+    q, k, v = (torch.randn(n, h, dh, generator=gen, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    out, err = _run(bd, q, k, v, [n], [n], n)
+    assert err == 0
+    for i in (0, 1, 127, 128, 4095, 17000, 31999, 32000, 39935, 39936, 39999):
+        ref, tol = _ref(q[i:i + 1].cpu(), k[:i + 1].cpu(), v[:i + 1].cpu())
+        assert np.all(np.abs(out[i].cpu().double().numpy().reshape(ref.shape) - ref) <= tol), i
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("lq,more", [([300, 0, 1, 129, 4097, 64], 0), ([4096, 4098, 5], 3), ([9000], 2000),
                                      ([3] * 1030 + [5000] + [2] * 20 + [6000], 1)])
 def test_plan_lists(bd, lq, more):

@@ -750,6 +750,101 @@ def test_pool_past_32_bits(bd):
     assert torch.isfinite(res[0][3].float()).all() and torch.any(res[0][1] != 0)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", PAGES)
+@pytest.mark.parametrize("heads", [(8, 1, 128), (16, 2, 128), (8, 8, 64), (16, 2, 64), (10, 5, 64), (9, 3, 128)], ids=str)
+def test_read_forms(bd, heads, page):
+    """The rows that a warp takes at once, for kv heads on both sides of each form."""
+    _, Hkv, dh = heads
+    lens, start = [3, 0, 130, 70], [page - 1, 9, 0, 2 * page + 5]
+    ends = [a + n for a, n in zip(start, lens)]
+    c = Cache(Hkv, dh, page, ends, page).fill(ends, page)
+    n = sum(lens)
+    k = torch.full((n + 3, Hkv, dh), 7.0, dtype=torch.bfloat16, device="cuda")
+    v, err = k.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    bd.op_read_paged4(c.k, c.v, c.dtable, _cu(lens), torch.tensor(start, dtype=torch.int32, device="cuda"), k, v, err=err)
+    assert int(err.item()) == 0
+    seq, pos = np.repeat(np.arange(len(lens)), lens), _positions(lens, start)
+    for got, pages in ((k, c.k), (v, c.v)):
+        val = _values(pages.cpu(), page, dh)[c.table[seq, pos // page], :, pos % page]
+        # the sum is rounded to fp32 (2^-24 of it), then to bf16
+        assert np.all(np.abs(got[:n].cpu().double().numpy() - val) <= 2.0 ** -8 * np.abs(val) * (1 + 2.0 ** -14))
+        assert torch.all(got[n:] == 7.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("heads,lens", [((5, 1, 128), [9000, 100]), ((12, 2, 64), [3000, 0, 700]), ((7, 1, 64), [20000]),
+                                        ((7, 1, 128), [5000, 1, 2000]), ((40, 8, 128), [2100, 65, 900]),
+                                        ((24, 4, 128), [64, 65, 63, 800])], ids=str)
+def test_decode_odd_groups(bd, heads, lens, page):
+    """Groups of five to seven query heads, with sequences that are cut between warps and between CTAs."""
+    Hq, Hkv, dh = heads
+    c = Cache(Hkv, dh, page, lens, page).fill(lens, page)
+    q = torch.randn(len(lens), Hq, dh, generator=torch.Generator().manual_seed(page)).to(torch.bfloat16)
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    _check_decode(out, q, c, lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,lens,page", [((8, 1, 128), [20011], 64), ((4, 2, 64), [9000, 1, 4000], 16),
+                                             ((12, 4, 128), [2500, 2500], 32), ((7, 1, 64), [30000], 128)], ids=str)
+def test_decode_counts_every_unit_once(bd, heads, lens, page):
+    """One key in every 64 has nearly all of the weight, and a value in a dim of its own (which up to eight share): a unit
+    that is left out, or taken twice, changes that dim by an eighth of it at least, against a bound of about a hundredth."""
+    Hq, Hkv, dh = heads
+    c = Cache(Hkv, dh, page, lens, page)
+    for pages, is_k in ((c.k, True), (c.v, False)):
+        host = pages.cpu()
+        codes = host[:, :, :page * dh // 2].view(*host.shape[:2], page, dh // 2)
+        side = host[:, :, page * dh // 2:].view(torch.bfloat16).view(*host.shape[:2], page, dh // 64, 2)
+        for b, n in enumerate(lens):
+            s = np.arange(n)
+            unit = s // 64
+            # (the last unit's key is its first one)
+            marked = s == unit * 64 + np.where((unit + 1) * 64 <= n, unit * 29 % 64, 0)
+            at, off = torch.from_numpy(c.table[b, s // page]).long(), torch.from_numpy(s % page)
+            m = torch.from_numpy(marked)
+            row = torch.zeros(n, dh // 2, dtype=torch.uint8)
+            if is_k:  # scores of 2 sqrt(dh) and the negative of it, 32 and more apart
+                pair = torch.where(m, 2.0, -2.0).to(torch.bfloat16)
+                side[at, :, off] = torch.stack([torch.zeros_like(pair), pair], -1)[:, None, None].expand(n, host.shape[1], dh // 64, 2)
+            else:
+                dim = unit[marked] % dh
+                row[np.nonzero(marked)[0], dim // 2] = torch.from_numpy(np.where(dim % 2, 0xf0, 0x0f).astype(np.uint8))
+                side[at, :, off] = torch.tensor([1.0, 0.0], dtype=torch.bfloat16).expand(n, host.shape[1], dh // 64, 2)
+            codes[at, :, off] = row[:, None].expand(n, host.shape[1], dh // 2)
+        pages.copy_(host)
+    q = torch.ones(len(lens), Hq, dh, dtype=torch.bfloat16)
+    out, err = _decode(bd, q.cuda(), c, torch.tensor([n - 1 for n in lens], dtype=torch.int32, device="cuda"))
+    assert err == 0
+    _check_decode(out, q, c, lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,page", [((16, 8, 128), 16), ((8, 4, 64), 64), ((40, 8, 128), 32)], ids=str)
+def test_appended_tokens_are_attended_to(bd, heads, page):
+    """Prompts, then single tokens: after every append the attention of all sequences, the new key among those it sees, against
+    float64 on the cache's own bytes. The new key is the query itself times 8 in every other sequence, so that it has most of the weight."""
+    Hq, Hkv, dh = heads
+    lens, steps = [37, 5, 150, 64], 4
+    ends = [n + steps for n in lens]
+    c = Cache(Hkv, dh, page, ends, 17)
+    _append(bd, heads, page, lens, [0] * 4, seed=17, cache=c)
+    gen = torch.Generator().manual_seed(18)
+    for i in range(steps):
+        at = [n + i for n in lens]
+        qkv = torch.randn(4, (Hq + 2 * Hkv) * dh, generator=gen)
+        x = qkv.view(4, Hq + 2 * Hkv, dh)
+        x[::2, Hq:Hq + Hkv] = 8 * x[::2, :Hq:Hq // Hkv]
+        r = _append(bd, heads, page, [1] * 4, at, norm=False, qkv=qkv.to(torch.bfloat16), cache=c)
+        assert r["err"] == 0
+        out, err = _decode(bd, r["q"].cuda(), c, torch.tensor(at, dtype=torch.int32, device="cuda"))
+        assert err == 0
+        _check_decode(out, r["q"], c, [n + 1 for n in at])
+
+
 # ------------------------------------------------------------------------------------------------------------ refusals
 
 def test_page_bytes(bd):
