@@ -385,7 +385,8 @@ QWEN3_API int qwen3_op_attention_decode_shared(const void* d_q, const void* d_k_
  * Decode: the form for one token per sequence, q [B, Hq, dh], out [B, Hq*dh], Hq / Hkv at most 8, B at most
  * 65535; hidden rows may hold anything; a sequence with a negative length gets zeros. Neither needs a workspace.
  * window >= 1, sinks >= 0, dh 64 or 128, cap at most 2^30 and lengths too (a longer one counts as 2^30), 16-byte
- * aligned tensors; values of the size that qwen3_op_attention_decode_shared takes. d_err (may be NULL) as for
+ * aligned tensors; values of the size that qwen3_op_attention_decode_shared takes (in a prefill whose scores pass 2^23 in
+ * size, 2^55 over the visible keys, as in qwen3_op_attention_prefill_packed). d_err (may be NULL) as for
  * qwen3_op_attention_prefill. */
 QWEN3_API int qwen3_attention_sink_rows(int sinks);
 QWEN3_API int qwen3_op_attention_prefill_sinks(const void* d_q, const void* d_k_cache, const void* d_v_cache, int B,
@@ -430,7 +431,7 @@ QWEN3_API int qwen3_op_append_paged4(const void* d_qkv, int64_t ld, int N, const
                                      int* d_err, void* stream);
 
 /* Read slots of the paged cache: row cu[s] + i of d_k_out and d_v_out [N, Hkv, dh] bf16 becomes slot d_start[s] + i of sequence s,
- * each value rounded once (to go on from a cached history with qwen3_op_attention_prefill_packed, or to look at it). A row
+ * each value taken in fp32 (one rounding) and rounded to bf16 (to go on from a cached history with qwen3_op_attention_prefill_packed, or to look at it). A row
  * whose slot has no page is left as it was (bit 4). */
 QWEN3_API int qwen3_op_read_paged4(const void* d_k_pages, const void* d_v_pages, int n_pages, int page_size,
                                    const int* d_page_table, int max_pages, const int* d_cu, const int* d_start, int S, int N,
@@ -444,7 +445,7 @@ QWEN3_API int qwen3_op_read_paged4(const void* d_k_pages, const void* d_v_pages,
  * bytes (of the current device; work_bytes is its size, a smaller one is refused), 16-byte aligned, any contents on entry;
  * calls that share one must not overlap on the GPU. Scores, sums and softmax statistics are fp32; the cached codes are used as
  * they are, and probabilities times scales are rounded to fp16 (with a power of two for each head) for the product with the
- * codes. |q| up to 2^90, scores up to 2^30 in size; the visible keys times the largest |v| must stay below 2^50. A page id
+ * codes. |q| and |k| up to 2^90, scores up to 2^30 in size; the visible keys times the largest |v| must stay below 2^50. A page id
  * out of range (bit 4) makes the sequence's output invalid; bit 2 as for the other attention operators. The result does not
  * depend on timing. */
 QWEN3_API size_t qwen3_attention_decode_paged4_workspace(int B, int Hq, int Hkv, int dh);
@@ -465,8 +466,9 @@ QWEN3_API int qwen3_op_attention_decode_paged4(const void* d_q, const void* d_k_
  * of the longest sequence, only picks between equivalent forms of the kernel: any value gives a right result.
  * Scores, sums and softmax statistics are fp32, probabilities are rounded to bf16 for the product with V. Value rows that some
  * query of a 128-row tile sees must be finite; nothing stored in another sequence's rows, or behind the tile's last visible
- * key, reaches a result. Scores must stay below 2^30 in size, and the visible keys times the largest |v| below 2^119; Nq, Nk
- * and S are at most 2^30, and plan_bytes / 16 times Hq below 2^31 - 2^16. */
+ * key, reaches a result. Scores must stay below 2^30 in size, and the visible keys times the largest |v| below 2^119 where they
+ * stay below 2^23, 2^55 beyond (a row's weights then share a power of two of up to 2^64, from the rounding of its
+ * largest score); Nq, Nk and S are at most 2^30, and plan_bytes / 16 times Hq below 2^31 - 2^16. */
 QWEN3_API size_t qwen3_attention_packed_plan_bytes(int Nq, int S);
 QWEN3_API int qwen3_op_attention_packed_plan(const int* d_cu_q, const int* d_cu_k, int S, int Nq, int Nk, void* d_plan,
                                              size_t plan_bytes, int* d_err, void* stream);

@@ -135,6 +135,31 @@ def test_sizes_of_scores(bd, dh, scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_and_values_at_their_limits(bd, dh, sign):
+    """Scores just below 2^30, whose rounding in fp32 gives a row's weights a factor of up to 2^64 either way, beside values of
+    2^55 over the visible keys: the result is the value of the row's largest score, to the roundings of its weight and of itself."""
+    # the pair of bf16 values whose product, in log2 units, is furthest above (below) its fp32 rounding
+    sl2 = np.float32(np.float32(1.4426950408889634) / np.sqrt(np.float32(dh)))
+    a = np.arange(128, 256, dtype=np.float64)
+    s = a[:, None] * a * 2.0 ** np.floor(30 + np.log2(dh) / 2 - np.log2(a[:, None] * a))
+    x = s * np.float64(sl2)  # (40 bits: exact)
+    off = np.where(s / dh ** 0.5 < 2.0 ** 30, (x - np.float32(x)) * sign, -1.0)
+    i, j = np.unravel_index(off.argmax(), off.shape)
+    assert off[i, j] > 56
+    n, heads = 200, (4, 2, dh)
+    q, k, v = (torch.zeros(n, h, dh) for h in (4, 2, 2))
+    q[:, :, 0], k[0, :, 0] = a[i], s[i, j] / a[i]  # key 0 has all of the weight
+    v[:] = torch.randn(n, 2, dh, generator=torch.Generator().manual_seed(1)).clamp(-1, 1) * 2.0 ** 55 / n
+    q, k, v = (t.to(torch.bfloat16) for t in (q, k, v))
+    out, err = _run(bd, q.cuda(), k.cuda(), v.cuda(), [n], [n], n)
+    assert err == 0
+    ref = v[0].double()[None, :, None].expand(n, 2, 2, dh).reshape(n, -1)
+    assert torch.all((out.cpu().double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -15) * ref.abs())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("S", [1, 33, 2000])
 def test_many_sequences(bd, S):
     lens = [(i * 7919 + 5) % 23 for i in range(S)]
