@@ -204,6 +204,22 @@ def test_later_tiles_of_the_same_sequence_do_not_leak(bd):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("longest", FORMS[:2])
+def test_rows_before_the_first_sequence(bd, longest):
+    """Bounds that begin behind row 0: the rows in front belong to no sequence."""
+    heads, lens, front = (8, 4, 128), [70, 0, 131], 37
+    q, k, v = _inputs(heads, lens, lens, 6, tail=front)
+    for t in (q, k, v):
+        t[:front] = float("nan")
+    cu = _cu(lens) + front
+    plan, err = _plan(bd, cu, cu, q.shape[0], k.shape[0], 3)
+    out = torch.full((q.shape[0], 8 * 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    bd.op_attention_prefill_packed(q.cuda(), k.cuda(), v.cuda(), plan, longest, out, err=err)
+    assert int(err.item()) == 0 and torch.all(out[:front] == 7.0)
+    _check(out[front:], q[front:], k[front:], v[front:], lens, lens)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads", HEADS[:2], ids=str)
 def test_views_of_qkv_rows(bd, heads):
     """Queries, keys and values read in place from packed rows, with a stride of their own."""

@@ -240,6 +240,46 @@ def test_append_rows_further_apart_and_no_keys_out(bd):
 
 
 @pytest.mark.gpu
+def test_rows_before_the_first_sequence(bd):
+    """Bounds that begin behind row 0: the rows in front belong to no sequence and are left as they were."""
+    heads, lens, start, front = (8, 4, 64), [9, 0, 30], [3, 1, 20], 5
+    ref = _append(bd, heads, 16, lens, start, seed=8)
+    c = Cache(4, 64, 16, [a + n for a, n in zip(start, lens)], 8)
+    qkv = torch.cat([torch.full((front, 16 * 64), float("nan"), dtype=torch.bfloat16), ref["qkv"]]).cuda()
+    q = torch.full((front + 39, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    k = torch.full((front + 39, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = ref["cu"] + front
+    bd.op_append_paged4(qkv, cu, ref["start"], ref["cs"].cuda(), c.k, c.v, c.dtable, q, k_out=k, q_gamma=ref["g"][0].cuda(),
+                        k_gamma=ref["g"][1].cuda(), eps=EPS, err=err)
+    assert torch.equal(q[front:].cpu(), ref["q"]) and torch.equal(k[front:].cpu(), ref["k"])
+    assert torch.all(q[:front] == 7.0) and torch.all(k[:front] == 7.0)
+    assert torch.equal(c.k, ref["cache"].k) and torch.equal(c.v, ref["cache"].v)
+    kr, vr = torch.full_like(k, 7.0), torch.full_like(k, 7.0)
+    bd.op_read_paged4(c.k, c.v, c.dtable, cu, ref["start"], kr, vr, err=err)
+    assert torch.all(kr[:front] == 7.0) and torch.all(vr[:front] == 7.0) and torch.isfinite(kr[front:].float()).all()
+    assert int(err.item()) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_append_with_one_gamma(bd, which):
+    """A norm of the queries alone, or of the keys alone: each as with both or none."""
+    heads, lens, start = (8, 4, 64), [9, 30], [3, 20]
+    both = _append(bd, heads, 16, lens, start, seed=9)
+    none = _append(bd, heads, 16, lens, start, seed=9, norm=False, qkv=both["qkv"])
+    c = Cache(4, 64, 16, [12, 50], 9)
+    q = torch.empty(39, 8, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.empty(39, 4, 64, dtype=torch.bfloat16, device="cuda")
+    g = {which + "_gamma": both["g"]["qk".index(which)].cuda()}
+    bd.op_append_paged4(both["qkv"].contiguous().cuda(), both["cu"], both["start"], both["cs"].cuda(), c.k, c.v, c.dtable, q,
+                        k_out=k, eps=EPS, **g)
+    a, b = (both, none) if which == "q" else (none, both)
+    assert torch.equal(q.cpu(), a["q"]) and torch.equal(k.cpu(), b["k"])
+    assert torch.equal(c.k, b["cache"].k) and torch.equal(c.v, both["cache"].v)
+
+
+@pytest.mark.gpu
 def test_append_values_at_the_edges(bd):
     """Groups of one value, of both signs, of zeros, of very large and of subnormal values; NaN and infinities."""
     heads, dh = (2, 2, 64), 64
