@@ -141,10 +141,11 @@ __global__ void __launch_bounds__(kPlanThreads)
 // (keys), zeroed (values) and not stored (queries).
 // What bounds it: the way of a tile through tensor memory, 128 scores a thread, and back, about 1,500 cycles of 128 query rows by
 // 128 keys, against 1,024 of products. One prompt of 8,192 tokens, 32 / 8 heads of 128: 352 us, 0.82 of the tensor peak
-// (1,562 TFLOP/s of visible pairs); 17,000 tokens in three prompts 533-580 us, with the clock that the power limit leaves. Short
-// prompts: masked tiles, 2,500 cycles each, are a third of theirs (64 of about 512 tokens: 253 us). Leaving out the parts of
-// a masked tile that no row sees made 242 us of that, but 377-381 of the 352 of one long prompt, in every form tried: the
-// softmax loop, which fills its registers, was then compiled with less of it in flight.
+// (1,562 TFLOP/s of visible pairs); 17,000 tokens in three prompts 550 us; in a loop, with the clock that the power limit
+// leaves, 380 and 575. Short prompts: masked tiles, 2,500 cycles each, are 40% of the key tiles of prompts of 512 tokens at
+// groups of four (64 of them: 253 us). Leaving out the parts of a masked tile that no row sees made 242 us of that, in the
+// form for short key ranges, but 377-381 of the 352 of one long prompt, in the other: tried in both forms at once, it is
+// in neither.
 constexpr int PK_THREADS = 384;
 constexpr uint32_t PK_REG_PRODUCER = 56, PK_REG_SOFTMAX = 208, PK_REG_OUTPUT = 104;
 static_assert(PK_REG_PRODUCER + PK_REG_SOFTMAX + PK_REG_OUTPUT <= 3 * 168, "register split exceeds the launch");

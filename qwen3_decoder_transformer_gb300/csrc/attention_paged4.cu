@@ -36,11 +36,10 @@ namespace {
 // piece (sums of weighted values, reference of the weights, sum of weights); pieces of one CTA are joined in shared memory, the others in the workspace by
 // attn_paged4_join_kernel, in the order of their keys: the result does not depend on timing.
 //
-// What bounds it: many keys, HBM (16 sequences of up to 32,768 keys, 32 / 8 heads of 128: 86 us, 6.1 TB/s, of which some 8 us are
-// start and end). In the loop a unit of each of an SM's 12 warps takes 4,000 cycles, 28 bytes a cycle and SM, which is the
-// copy rate, with the issue slots half full. Few keys: the chain of one unit. 1 sequence of 4096: 9.1 us; counting
-// the lengths 0.6, finding the run 0.5, the query 1, one unit 2.1, the pieces 1.2, and the rest two launches and
-// the records' way through the workspace.
+// What bounds it: many keys, HBM (16 sequences of up to 32,768 keys, 32 / 8 heads of 128: 86.5 us, 6.0 TB/s, of which some 8 us are
+// start and end: in the loop 6.6 TB/s of a copy's 6.8), with the issue slots half full. Few keys: the chain of one
+// unit. 1 sequence of 4096: 9.4 us; counting the lengths 0.6, finding the run 0.5, the query 1, one unit 2.2, the
+// pieces 1.2, and the rest two launches and the records' way through the workspace.
 // Split: one CTA of 12 warps an SM, as many rings as shared memory holds, joins the pieces of 12 runs before they leave the SM (16 @
 // 32,768 two CTAs of six 90.3 us, one of twelve 85.7, when it was changed; 64 @ 4096, 16 / 8 heads, 45.6 and 44.9).
 constexpr int P4_STEP = 64, P4_TILES = P4_STEP / 16;  // keys that a warp takes at once
@@ -195,8 +194,8 @@ __global__ void __launch_bounds__(P4_THREADS, P4_CTAS)
     }
     auto all_units = [&]() { return strip_end[P4_STRIPS - 1] * a.Hkv; };  // (fewer than 2^31: checked on the host)
     // warps of a CTA that work: few units are spread over the SMs (1 sequence of 4096 keys, 8 kv heads: 9.3 us, with full
-    // CTAs 10.0), but not further than a warp a scheduler: every CTA that shares a kv head leaves a record for the join (2 kv
-    // heads, a warp a CTA 15.5 us, four 10.3)
+    // CTAs 10.0, when it was changed), but not further than a warp a scheduler: every CTA that shares a kv head leaves a
+    // record for the join (2 kv heads, a warp a CTA 15.5 us, four 10.3)
     auto team_of = [&](int units) { return max(4, min(P4_WARPS, p4_div(min(units, places) + (int)gridDim.x - 1, (int)gridDim.x))); };
     const int units = all_units();
     const int gw = warp < team_of(units) ? blockIdx.x * team_of(units) + warp : places;

@@ -154,10 +154,10 @@ struct AppendArgs {
 //   (a, b) -> (r (g_a cos a - g_b sin b), r (g_b cos b + g_a sin a)) in fp32, rounded once;
 // the products of gains and angles are made once a token and kind of head. The next pieces' values, and the next token's
 // angles, are on their way meanwhile; a sequence is looked up once, then followed from token to token.
-// What bounds it: many tokens, HBM and issue (32,768 tokens of 32 / 8 heads of 128, 776 MB: 134 us, 5.8 TB/s of a copy's 6.8, 0.59
+// What bounds it: many tokens, HBM and issue (32,768 tokens of 32 / 8 heads of 128, 776 MB: 136 us, 5.7 TB/s of a copy's 6.8, 0.60
 // instructions a cycle and scheduler; one warp a head with loads waited for in turn took 410); few, the chain of
-// look-up, page, gains, norm, codes: 3 us with its launch. Pieces ahead and CTAs of four warps an SM: for these tokens and the read of their slots 162 us; five
-// CTAs 172, six 172; two pieces ahead 168, eight 177.
+// look-up, page, gains, norm, codes: 3 us with its launch. Pieces ahead and CTAs of four warps an SM: for these tokens and the read of their slots 162 us when
+// it was chosen (164 now); five CTAs 172, six 172; two pieces ahead 168, eight 177.
 constexpr int AP_AHEAD = 4, AP_CTAS = 4, AP_START = 2, AP_ALL = 4;
 template <int DH>
 __global__ void __launch_bounds__(128, AP_CTAS)
@@ -428,8 +428,8 @@ cudaError_t append_paged4_launch(const __nv_bfloat16* qkv, long long ld, int N, 
                  err};
     // `parts` warps share the pieces of a token, and each takes `per` tokens. The split with the shortest way of a warp, in pieces: a
     // token costs AP_START more, and a GPU full of warps that start together AP_ALL more. With the reads of the same slots, 32 / 8
-    // heads of 128: 1 token 5.9 us (a warp a token 10.5), 200 tokens 7.2 (as many warps as there are pieces 10.0), 3,000 25.2 (a
-    // warp a token 28.5), 32,768 163.
+    // heads of 128: 1 token 5.9 us (a warp a token 10.5), 200 tokens 7.2 (as many warps as there are pieces 10.0), 3,000 23.7 (a
+    // warp a token 28.5), 32,768 164.
     const double room = 4. * AP_CTAS * device_sm_count();
     const int pieces = (Hq + 2 * Hkv + 512 / dh - 1) / (512 / dh);
     int parts = 1, per = 0;
